@@ -387,6 +387,73 @@ uw_status uw_sequence_run(const uw_step *steps, int n, int64_t B, void *workspac
 uw_status uw_sequence_tune(const uw_step *steps, int n, int64_t B, void *workspace, size_t ws_bytes, uw_stream stream,
                            uw_stream side_stream, int *decode_sms);
 
+/* ------------------------------------------------------------------------------------------------------------
+ * Operators around the compressed products of a mixture-of-experts decoder: the experts' grouped products on
+ * compressed weights.  Sizes that only the device knows (rows per expert) are read there: no call waits for the GPU,
+ * so every call can be captured into a CUDA graph.  uw_out_dtype names the type of inputs here too.
+ * ------------------------------------------------------------------------------------------------------------ */
+
+/*
+ * uw_group - the weight matrices of `experts` experts, all [N, K], compressed without loss in the form the grouped
+ *   kernels read: per weight a sign+mantissa byte and 4 bits of exponent (its distance from the lowest of 16
+ *   consecutive exponents, chosen per matrix to cover the most weights), per 64 weights of a row that hold an
+ *   exponent outside those 16 the 64 exponent bytes.  With up matrices the group is gated: an expert's product is
+ *   silu(W x) * (W_up x), both products in one pass.
+ */
+typedef struct uw_group uw_group;
+
+typedef struct {
+    int64_t N, K;            /* per matrix: N outputs, K inputs */
+    int32_t experts;
+    int32_t gated;           /* made with up matrices */
+    uint64_t n_verbatim;     /* 64-weight runs stored with their exponent bytes */
+    uint64_t device_bytes;   /* device memory held by the group */
+} uw_group_info;
+
+/*
+ * uw_group_create - a group from loaded matrices (any codec or resident form): w[0..experts), and w_up[0..experts)
+ *   for a gated group (NULL: not gated).  The group holds its own copy; the matrices may be freed afterwards.
+ *   Decodes one matrix at a time into a temporary N*K*2-byte device buffer.  Synchronous.
+ * uw_group_create_dense - the same from bf16 weights on the device: w_dev [experts, N, K] row-major, 16-byte
+ *   aligned, and w_up_dev (NULL: not gated).
+ *   Errors: UW_ERR_INVALID_ARG (NULL, alignment, experts outside 1..1024, a matrix of another device),
+ *   UW_ERR_SHAPE (K % 64, N or K < 1 or above 2^31 - 256, matrices of different shapes, 2^32 or more verbatim
+ *   runs), UW_ERR_CORRUPT, UW_ERR_NO_MEMORY, UW_ERR_CUDA.
+ */
+uw_status uw_group_create(const uw_matrix *const *w, const uw_matrix *const *w_up, int experts, uw_stream stream,
+                          uw_group **out);
+uw_status uw_group_create_dense(const uint16_t *w_dev, const uint16_t *w_up_dev, int experts, int64_t N, int64_t K,
+                                uw_stream stream, uw_group **out);
+
+/* uw_group_free - release a group and its device memory (as uw_free).  NULL is a no-op. */
+void uw_group_free(uw_group *g);
+uw_status uw_group_get_info(const uw_group *g, uw_group_info *out);
+
+/* uw_group_decode - rebuild one expert's matrix bit-exactly into w_dev [N, K] bf16 (16-byte aligned); up != 0: its
+ *   up matrix.  Asynchronous.  Errors: UW_ERR_INVALID_ARG, UW_ERR_UNSUPPORTED (up of a group that is not gated),
+ *   UW_ERR_CUDA. */
+uw_status uw_group_decode(const uw_group *g, int expert, int up, uint16_t *w_dev, uw_stream stream);
+
+/*
+ * uw_group_matmul - for every expert e and every row r in [offsets[e], offsets[e + 1]):
+ *     y[r, :] = W_e x[s]           or, gated,   y[r, :] = silu(W_e x[s]) * (W_up_e x[s])
+ *   with s = row_src[r], or s = r when row_src is NULL (fp32 accumulation, one rounding to the output type).
+ *   x_dev: [x_rows, K] bf16, rows ldx elements apart (ldx 0: K; a multiple of 8).  y_dev: [rows, N] fp32 or bf16,
+ *   rows ldy elements apart (0: N).  offsets_dev: int32 [experts + 1], ascending, on the device; rows of y outside
+ *   [offsets[0], offsets[experts]) are not written.  Offsets are clamped to [0, rows]; a row whose source lies
+ *   outside [0, x_rows) counts as zeros, so an expert's rows may be padded with a source of -1.  An expert may have
+ *   any number of rows, none included.  Results do not depend on the run or on the other experts' rows.
+ *   No workspace.  Asynchronous on `stream`.
+ *   Errors: UW_ERR_INVALID_ARG (NULL, x or y not 16-byte aligned, bad dtype), UW_ERR_SHAPE (negative sizes, rows
+ *   or x_rows above 2^31 - 1024, ldx < K or not a multiple of 8, ldy < N), UW_ERR_CUDA.
+ */
+uw_status uw_group_matmul(const uw_group *g, const uint16_t *x_dev, int64_t x_rows, int64_t ldx,
+                          const int32_t *row_src_dev, const int32_t *offsets_dev, int64_t rows, void *y_dev,
+                          int64_t ldy, uw_out_dtype out_dtype, uw_stream stream);
+
+/* uw_group_check - as uw_check, for a group: UW_ERR_TIMEOUT if a bounded wait of a kernel on it expired. */
+uw_status uw_group_check(const uw_group *g, uw_stream stream);
+
 /* uw_check - synchronise `stream` and report (then clear) the matrix's device status word. */
 uw_status uw_check(const uw_matrix *m, uw_stream stream);
 

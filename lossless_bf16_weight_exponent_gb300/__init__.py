@@ -76,6 +76,14 @@ class Info(ctypes.Structure):
         return d
 
 
+class GroupInfo(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int64), ("K", ctypes.c_int64), ("experts", ctypes.c_int32), ("gated", ctypes.c_int32),
+                ("n_verbatim", ctypes.c_uint64), ("device_bytes", ctypes.c_uint64)]
+
+    def as_dict(self):
+        return {f: getattr(self, f) for f, _ in self._fields_}
+
+
 _lib = None
 _VP, _SZ, _I64, _INT = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int64, ctypes.c_int
 
@@ -103,6 +111,13 @@ _SIGS = {
     "uw_sequence_workspace_size": [ctypes.POINTER(Step), _INT, _I64, ctypes.POINTER(_SZ)],
     "uw_sequence_run": [ctypes.POINTER(Step), _INT, _I64, _VP, _SZ, _VP, _VP, _INT],
     "uw_sequence_tune": [ctypes.POINTER(Step), _INT, _I64, _VP, _SZ, _VP, _VP, ctypes.POINTER(_INT)],
+    "uw_group_create": [ctypes.POINTER(_VP), ctypes.POINTER(_VP), _INT, _VP, ctypes.POINTER(_VP)],
+    "uw_group_create_dense": [_VP, _VP, _INT, _I64, _I64, _VP, ctypes.POINTER(_VP)],
+    "uw_group_free": [_VP],
+    "uw_group_get_info": [_VP, ctypes.POINTER(GroupInfo)],
+    "uw_group_decode": [_VP, _INT, _INT, _VP, _VP],
+    "uw_group_matmul": [_VP, _VP, _I64, _I64, _VP, _VP, _I64, _VP, _I64, _INT, _VP],
+    "uw_group_check": [_VP, _VP],
     "uw_status_string": [_INT],
     "uw_last_error": [],
     "uw_version": [],
@@ -121,6 +136,7 @@ def lib():
             f.argtypes = args
             f.restype = _INT
         L.uw_free.restype = None
+        L.uw_group_free.restype = None
         L.uw_status_string.restype = ctypes.c_char_p
         L.uw_last_error.restype = ctypes.c_char_p
         L.uw_version.restype = ctypes.c_char_p
@@ -306,3 +322,57 @@ def sequence_tune(steps, B: int, workspace, ws_bytes: int, stream=None, side_str
     _check(lib().uw_sequence_tune(_steps(steps), len(steps), B, _ptr(workspace), ws_bytes, _stream(stream),
                                   _stream(side_stream), ctypes.byref(d)), "uw_sequence_tune")
     return d.value
+
+
+class Group:
+    """The weight matrices of a layer's experts, compressed on the current CUDA device (owns a ``uw_group``).
+
+    w: bf16 tensor [experts, N, K] on the device, or a list of loaded ``Matrix``; w_up: the same for the up matrices of
+    a gated group, whose product is silu(W x) * (W_up x)."""
+
+    def __init__(self, w, w_up=None, stream=None):
+        h = ctypes.c_void_p()
+        if isinstance(w, (list, tuple)):
+            arr = [(ctypes.c_void_p * len(v))(*[m.handle for m in v]) if v is not None else None for v in (w, w_up)]
+            if w_up is not None and len(w_up) != len(w):
+                raise ValueError("w and w_up differ in length")
+            _check(lib().uw_group_create(arr[0], arr[1], len(w), _stream(stream), ctypes.byref(h)), "uw_group_create")
+        else:
+            for t in (w, w_up):
+                if t is not None and (t.dim() != 3 or t.shape != w.shape or not t.is_contiguous() or t.element_size() != 2):
+                    raise ValueError("weights must be contiguous 16-bit tensors [experts, N, K] of one shape")
+            E, N, K = w.shape
+            _check(lib().uw_group_create_dense(_ptr(w), _ptr(w_up), E, N, K, _stream(stream), ctypes.byref(h)),
+                   "uw_group_create_dense")
+        self._h = h
+        info = GroupInfo()
+        _check(lib().uw_group_get_info(self._h, ctypes.byref(info)), "uw_group_get_info")
+        self.info = info.as_dict()
+        self.N, self.K, self.experts = self.info["N"], self.info["K"], self.info["experts"]
+
+    def close(self):
+        if getattr(self, "_h", None):
+            lib().uw_group_free(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    @property
+    def handle(self):
+        return self._h
+
+    def decode(self, expert: int, out, up: bool = False, stream=None):
+        _check(lib().uw_group_decode(self._h, expert, int(up), _ptr(out), _stream(stream)), "uw_group_decode")
+
+    def matmul(self, x, offsets, rows: int, y, row_src=None, x_rows=None, out_dtype: int = OUT_BF16, ldx: int = 0,
+               ldy: int = 0, stream=None):
+        """uw_group_matmul; x_rows None: rows of x (a tensor)."""
+        _check(lib().uw_group_matmul(self._h, _ptr(x), x.shape[0] if x_rows is None else x_rows, ldx, _ptr(row_src),
+                                     _ptr(offsets), rows, _ptr(y), ldy, out_dtype, _stream(stream)), "uw_group_matmul")
+
+    def check(self, stream=None):
+        _check(lib().uw_group_check(self._h, _stream(stream)), "uw_group_check")

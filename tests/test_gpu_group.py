@@ -1,0 +1,307 @@
+"""Groups of compressed expert matrices and their grouped product: the form is lossless for every bit pattern, and
+the product matches a plain 64-bit one for ragged rows per expert, odd sizes, strides, padding rows and both output
+types, gated and not.
+
+Tolerance of a product: fp32 accumulation in a tree of at most K / 16 sequential steps of 16 products each, every step
+off by at most 2^-22 of the running sum of magnitudes (the tensor pipe may truncate), is within K 2^-26 sum |w x|,
+6e-5 of it at the largest K here; the suite's 1e-4 sum |w x| + 1e-6 covers that.  A bf16 output adds half a unit in the
+last place, at most 2^-8 |y|.  A gated output a/(1+e^-a) b moves by at most 1.1 |b| per unit of a and |a| per unit of b, and
+the exponential and division add a few 2^-23 |y| (4e-6 taken)."""
+import numpy as np
+import pytest
+
+import lossless_bf16_weight_exponent_gb300 as uw
+import synth
+
+pytestmark = pytest.mark.gpu
+
+
+def torch():
+    import torch as t
+    return t
+
+
+def dev(a, dtype=None):
+    t = torch()
+    a = np.ascontiguousarray(a)
+    if a.dtype == np.uint16:
+        return t.from_numpy(a.view(np.int16)).cuda().view(t.bfloat16)
+    r = t.from_numpy(a).cuda()
+    return r if dtype is None else r.to(dtype)
+
+
+def f64(bits):
+    return synth.bf16_to_f32(bits).astype(np.float64)
+
+
+def weights(E, N, K, seed, outliers=2e-3):
+    return synth.fill((E, N, K), seed=seed, scale=0.02, p1=outliers, f1=300.0)
+
+
+def offsets_of(counts, start=0):
+    return np.concatenate([[start], start + np.cumsum(counts)]).astype(np.int32)
+
+
+def reference(w, w_up, x, src, offsets, rows):
+    """(y, bound of its fp32 error) of every row of [0, rows); NaN rows are not written."""
+    E, N, K = w.shape
+    y = np.full((rows, N), np.nan)
+    bound = np.zeros((rows, N))
+    for e in range(E):
+        lo, hi = offsets[e], offsets[e + 1]
+        if hi <= lo:
+            continue
+        s = src[lo:hi]
+        ok = (s >= 0) & (s < x.shape[0])
+        xe = np.where(ok[:, None], x[np.clip(s, 0, x.shape[0] - 1)], 0.0)
+        a, ea = xe @ f64(w[e]).T, 1e-4 * (np.abs(xe) @ np.abs(f64(w[e])).T) + 1e-6
+        if w_up is None:
+            y[lo:hi], bound[lo:hi] = a, ea
+            continue
+        b, eb = xe @ f64(w_up[e]).T, 1e-4 * (np.abs(xe) @ np.abs(f64(w_up[e])).T) + 1e-6
+        silu = a / (1 + np.exp(-a))
+        y[lo:hi] = silu * b
+        bound[lo:hi] = 1.1 * ea * (np.abs(b) + eb) + np.abs(silu) * eb + 4e-6 * np.abs(silu * b) + 1e-6
+    return y, bound
+
+
+def check(y, ref, bound, bf16):
+    wr = ~np.isnan(ref)
+    assert np.array_equal(np.isnan(y), ~wr)
+    b = bound + (2.0 ** -8 * (np.abs(ref) + bound) if bf16 else 0)
+    err = np.abs(y - ref)[wr]
+    assert (err <= b[wr]).all(), float((err / b[wr]).max())
+
+
+def run(g, x, offsets, rows, out_bf16, src=None, x_rows=None, ldx=0, ldy=0, stream=None):
+    t = torch()
+    y = t.full((rows, ldy or g.N), float("nan"), dtype=t.bfloat16 if out_bf16 else t.float32, device="cuda")
+    g.matmul(x, offsets, rows, y, row_src=src, x_rows=x_rows, out_dtype=uw.OUT_BF16 if out_bf16 else uw.OUT_F32, ldx=ldx, ldy=ldy,
+             stream=stream)
+    g.check(stream)
+    return y.float().cpu().numpy().astype(np.float64)
+
+
+# ------------------------------------------------------------------------------------------------ the form
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("N,K", [(1, 64), (15, 128), (16, 192), (17, 64), (130, 1408), (257, 320)])
+@pytest.mark.parametrize("kind", ["normal", "bits", "zeros", "wide"])
+def test_form_is_lossless(kind, N, K, gated):
+    t = torch()
+    E = 3
+
+    def make(seed):
+        if kind == "bits":
+            return synth.random_bits((E, N, K), seed)
+        if kind == "zeros":
+            w = weights(E, N, K, seed)
+            w[:, :, ::7] = 0
+            w[1] = 0x8000
+            return w
+        w = weights(E, N, K, seed)
+        if kind == "wide":  # every fourth row spans all exponents
+            w[:, ::4] = (w[:, ::4] & 0x807F) | ((np.arange(K) % 256).astype(np.uint16) << 7)
+        return w
+
+    w, u = make(5), make(6)
+    g = uw.Group(dev(w), dev(u) if gated else None)
+    for e in range(E):
+        for up, ref in ((False, w), (True, u)) if gated else ((False, w),):
+            out = t.full((N, K), 0x5555, dtype=t.int16, device="cuda")
+            g.decode(e, out, up=up)
+            assert np.array_equal(out.cpu().numpy().view(np.uint16), ref[e]), (e, up)
+
+
+@pytest.mark.parametrize("outliers", [0.0, 2e-3])
+def test_form_size_and_verbatim_runs(outliers):
+    # 12 bits a weight, 32 bytes a step of 8192, and 64 bytes for each run that the 16 consecutive exponents that cover
+    # the most weights of its matrix do not hold: counted here from the bits
+    E, N, K = 2, 1024, 1024
+    w = weights(E, N, K, 3, outliers)
+    g = uw.Group(dev(w))
+    runs = 0
+    for e in range(E):
+        exps = (w[e] >> 7) & 255
+        cover = np.convolve(np.bincount(exps.ravel(), minlength=256), np.ones(16, np.int64), "valid")
+        base = int(np.argmax(cover))
+        runs += int(((exps < base) | (exps > base + 15)).reshape(-1, 64).any(1).sum())
+    assert g.info["n_verbatim"] == runs
+    steps = E * (N // 128) * (K // 64)
+    assert steps * (12288 + 32) + 64 * runs <= g.info["device_bytes"] <= steps * (12288 + 32) + 64 * runs + 8192
+
+
+@pytest.mark.parametrize("codec,resident", [(uw.CODEC_PALETTE, "both"), (uw.CODEC_HUFFMAN, "huffman"), (uw.CODEC_HUFFMAN, "palette")])
+def test_group_of_loaded_matrices(codec, resident):
+    t = torch()
+    E, N, K = 3, 100, 320
+    w, u = weights(E, N, K, 21), weights(E, N, K, 22)
+    ms = [[uw.Matrix(uw.encode(a[e], codec), resident=resident) for e in range(E)] for a in (w, u)]
+    g = uw.Group(ms[0], ms[1])
+    for m in ms[0] + ms[1]:
+        m.close()  # the group holds its own copy
+    for up, ref in ((False, w), (True, u)):
+        for e in range(E):
+            out = t.empty((N, K), dtype=t.int16, device="cuda")
+            g.decode(e, out, up=up)
+            assert np.array_equal(out.cpu().numpy().view(np.uint16), ref[e])
+
+
+# ------------------------------------------------------------------------------------------------ the product
+COUNTS = {"one": [1], "single_row": [0, 0, 1, 0], "few": [3, 0, 8, 9, 1], "ragged": [0, 17, 1, 130, 0, 64, 5, 300],
+          "all_in_last": [0, 0, 0, 40], "even": [16] * 6, "many_empty": [0] * 70 + [2] + [0] * 30 + [11]}
+
+
+@pytest.mark.parametrize("out_bf16", [False, True])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("counts", list(COUNTS))
+@pytest.mark.parametrize("N,K", [(48, 256), (130, 448), (1, 64)])
+def test_product(N, K, counts, gated, out_bf16):
+    c = COUNTS[counts]
+    E, rows = len(c), sum(c)
+    w = weights(E, N, K, N + rows)
+    u = weights(E, N, K, N + rows + 1) if gated else None
+    x = synth.fill((rows, K), seed=rows)
+    off = offsets_of(c)
+    ref, bound = reference(w, u, f64(x), np.arange(rows), off, rows)
+    g = uw.Group(dev(w), dev(u) if gated else None)
+    check(run(g, dev(x), dev(off), rows, out_bf16), ref, bound, out_bf16)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("rows_each", [2, 40, 600])
+def test_gathered_rows_strides_and_padding(rows_each, gated):
+    t = torch()
+    rng = np.random.default_rng(rows_each)
+    E, N, K, T, ldx, ldy = 5, 70, 192, 37, 208, 75
+    c = rng.integers(0, 2 * rows_each, E)
+    off = offsets_of(c, start=3)  # the first three rows belong to nobody
+    rows = int(off[-1]) + 2       # nor do the last two
+    src = rng.integers(0, T, rows).astype(np.int32)
+    src[::5] = -1
+    src[1::11] = T                # past the end
+    src[2::13] = 2 ** 31 - 1
+    w, u = weights(E, N, K, 31), weights(E, N, K, 32) if gated else None
+    x = synth.fill((T, ldx), seed=33)
+    ref, bound = reference(w, u, f64(x)[:, :K], src.astype(np.int64), off, rows)
+    g = uw.Group(dev(w), dev(u) if gated else None)
+    y = run(g, dev(x), dev(off), rows, False, src=dev(src), ldx=ldx, ldy=ldy)
+    check(y[:, :N], ref, bound, False)
+    assert np.isnan(y[:, N:]).all()  # nothing is written between the rows
+
+
+def test_offsets_outside_the_rows_are_clamped():
+    E, N, K, rows = 3, 32, 64, 20
+    w, x = weights(E, N, K, 41), synth.fill((rows, K), seed=42)
+    off = np.array([-5, 8, 8, 1000], np.int32)
+    ref, bound = reference(w, None, f64(x), np.arange(rows), np.clip(off, 0, rows), rows)
+    check(run(uw.Group(dev(w)), dev(x), dev(off), rows, False), ref, bound, False)
+
+
+@pytest.mark.parametrize("rows_each", [3, 48, 300])
+def test_exact_integers(rows_each):
+    # small integers: every partial sum is exact, so the result is, whatever the order
+    rng = np.random.default_rng(7)
+    E, N, K = 4, 100, 512
+    wi = (rng.integers(-3, 4, (E, N, K)) * 2.0 ** rng.integers(0, 3, (E, N, K))).astype(np.float32)
+    c = [rows_each, 0, rows_each + 1, 2]
+    rows = sum(c)
+    xi = rng.integers(-4, 5, (rows, K)).astype(np.float32)
+    off = offsets_of(c)
+    g = uw.Group(dev((wi.view(np.uint32) >> 16).astype(np.uint16)))
+    y = run(g, dev((xi.view(np.uint32) >> 16).astype(np.uint16)), dev(off), rows, False)
+    for e in range(E):
+        assert np.array_equal(y[off[e]:off[e + 1]], xi[off[e]:off[e + 1]].astype(np.float64) @ wi[e].astype(np.float64).T)
+
+
+def test_non_finite_weights_stay_in_their_outputs():
+    E, N, K, rows = 2, 40, 128, 20
+    w, x = weights(E, N, K, 51, 0.0), np.abs(f64(synth.fill((rows, K), seed=52)))
+    xb = (np.maximum(x, 0.1).astype(np.float32).view(np.uint32) >> 16).astype(np.uint16)
+    w[0, 5, 9], w[0, 7, 3], w[1, 33, 100] = 0x7F80, 0x7FC0, 0xFF80  # inf, NaN, -inf
+    off = offsets_of([12, 8])
+    y = run(uw.Group(dev(w)), dev(xb), dev(off), rows, False)
+    assert np.isposinf(y[:12, 5]).all() and np.isnan(y[:12, 7]).all() and np.isneginf(y[12:, 33]).all()
+    ok = np.isfinite(y)
+    ok[:12, [5, 7]] = ok[12:, 33] = True
+    assert ok.all()
+
+
+def test_rows_do_not_depend_on_other_rows_or_runs():
+    t = torch()
+    E, N, K = 6, 96, 256
+    w, u = weights(E, N, K, 61), weights(E, N, K, 62)
+    g = uw.Group(dev(w), dev(u))
+    x = synth.fill((200, K), seed=63)
+    a = run(g, dev(x), dev(offsets_of([40, 40, 40, 40, 20, 20])), 200, False)
+    b = run(g, dev(x), dev(offsets_of([40, 40, 40, 40, 20, 20])), 200, False)
+    assert np.array_equal(a, b)
+    x2 = x.copy()
+    x2[40:] = synth.fill((160, K), seed=64)
+    assert np.array_equal(run(g, dev(x2), dev(offsets_of([40, 40, 40, 40, 20, 20])), 200, False)[:40], a[:40])
+
+
+def test_other_stream_and_graph():
+    t = torch()
+    E, N, K, rows = 4, 64, 192, 50
+    w, x = weights(E, N, K, 71), synth.fill((rows, K), seed=72)
+    off = offsets_of([10, 0, 33, 7])
+    ref, bound = reference(w, None, f64(x), np.arange(rows), off, rows)
+    g = uw.Group(dev(w))
+    xd, od = dev(x), dev(off)
+    s = t.cuda.Stream()
+    s.wait_stream(t.cuda.current_stream())
+    check(run(g, xd, od, rows, False, stream=s), ref, bound, False)
+    y = t.zeros((rows, N), dtype=t.float32, device="cuda")
+    graph = t.cuda.CUDAGraph()
+    with t.cuda.graph(graph, stream=s):
+        g.matmul(xd, od, rows, y, out_dtype=uw.OUT_F32, stream=s)
+    # the rows per expert are read when the graph runs
+    off2 = offsets_of([0, 45, 0, 5])
+    od.copy_(dev(off2))
+    y.fill_(float("nan"))
+    graph.replay()
+    t.cuda.synchronize()
+    ref, bound = reference(w, None, f64(x), np.arange(rows), off2, rows)
+    check(y.cpu().numpy().astype(np.float64), ref, bound, False)
+
+
+def test_no_rows_is_a_no_op():
+    g = uw.Group(dev(weights(2, 16, 64, 81)))
+    t = torch()
+    y = t.full((1, 16), 7.0, device="cuda")
+    g.matmul(y, dev(np.zeros(3, np.int32)), 0, y, x_rows=0, out_dtype=uw.OUT_F32)
+    # rows exist, but no expert has them and there is nothing to read
+    g.matmul(0, dev(np.zeros(3, np.int32)), 1, y, x_rows=0, out_dtype=uw.OUT_F32)
+    t.cuda.synchronize()
+    assert (y == 7.0).all()
+
+
+def test_refusals():
+    t = torch()
+    w = dev(weights(2, 32, 128, 91))
+    g = uw.Group(w)
+    x, off = dev(synth.fill((4, 128), seed=1)), dev(offsets_of([2, 2]))
+    y = t.empty((4, 32), device="cuda")
+
+    def status(fn):
+        with pytest.raises(uw.UwError) as e:
+            fn()
+        return e.value.status
+
+    assert status(lambda: uw.Group(w.view(2, 64, 64)[:, :, :32].contiguous())) == uw.ERR_SHAPE
+    assert status(lambda: uw.Group(w[:0])) == uw.ERR_INVALID_ARG
+    ms = [uw.Matrix(uw.encode(synth.fill(s, seed=2))) for s in ((32, 64), (32, 128))]
+    assert status(lambda: uw.Group(ms)) == uw.ERR_SHAPE
+    assert status(lambda: uw.Group([])) == uw.ERR_INVALID_ARG
+    f = dict(out_dtype=uw.OUT_F32)
+    assert status(lambda: g.matmul(x, off, -1, y, **f)) == uw.ERR_SHAPE
+    assert status(lambda: g.matmul(x, off, 4, y, ldx=120, **f)) == uw.ERR_SHAPE
+    assert status(lambda: g.matmul(x, off, 4, y, ldx=132, **f)) == uw.ERR_SHAPE
+    assert status(lambda: g.matmul(x, off, 4, y, ldy=16, **f)) == uw.ERR_SHAPE
+    assert status(lambda: g.matmul(x, off, 4, y, out_dtype=7)) == uw.ERR_INVALID_ARG
+    assert status(lambda: g.matmul(x, None, 4, y, **f)) == uw.ERR_INVALID_ARG
+    assert status(lambda: g.matmul(x, off, 4, None, **f)) == uw.ERR_INVALID_ARG
+    assert status(lambda: g.matmul(x.data_ptr() + 2, off, 4, y, x_rows=3, **f)) == uw.ERR_INVALID_ARG
+    assert status(lambda: g.matmul(x, off, 4, y.data_ptr() + 4, **f)) == uw.ERR_INVALID_ARG
+    assert status(lambda: g.decode(2, w)) == uw.ERR_INVALID_ARG
+    assert status(lambda: g.decode(0, w, up=True)) == uw.ERR_UNSUPPORTED
