@@ -388,9 +388,12 @@ uw_status uw_sequence_tune(const uw_step *steps, int n, int64_t B, void *workspa
                            uw_stream side_stream, int *decode_sms);
 
 /* ------------------------------------------------------------------------------------------------------------
- * Operators around the compressed products of a mixture-of-experts decoder: the experts' grouped products on
- * compressed weights.  Sizes that only the device knows (rows per expert) are read there: no call waits for the GPU,
- * so every call can be captured into a CUDA graph.  uw_out_dtype names the type of inputs here too.
+ * Operators around the compressed products of a mixture-of-experts decoder: the router, the experts' grouped
+ * products on compressed weights, the norms and residual around a block, and the log probabilities on the head's
+ * logits.  A token's way: uw_block_norm; uw_matmul for the router's logits; uw_route; uw_group_matmul for gate and
+ * up, and for down; uw_block_norm, which joins the token's expert rows; uw_matmul for the head; uw_token_logprobs.
+ * Sizes that only the device knows (rows per expert) are read there: no call waits for the GPU, so every call can be
+ * captured into a CUDA graph.  uw_out_dtype names the type of inputs here too.
  * ------------------------------------------------------------------------------------------------------------ */
 
 /*
@@ -453,6 +456,88 @@ uw_status uw_group_matmul(const uw_group *g, const uint16_t *x_dev, int64_t x_ro
 
 /* uw_group_check - as uw_check, for a group: UW_ERR_TIMEOUT if a bounded wait of a kernel on it expired. */
 uw_status uw_group_check(const uw_group *g, uw_stream stream);
+
+/* How uw_route turns a token's logits into weights. */
+typedef enum {
+    UW_SCORE_SOFTMAX = 0,    /* softmax over all experts */
+    UW_SCORE_SIGMOID = 1     /* 1 / (1 + e^-logit), each expert by itself */
+} uw_score;
+
+typedef struct {
+    int32_t experts;         /* 1..1024 */
+    int32_t topk;            /* 1..min(16, experts) */
+    int32_t score;           /* uw_score */
+    int32_t renormalize;     /* divide a token's chosen weights by their sum (a sum of 0 leaves zeros) */
+    float scale;             /* multiplies the weights */
+    const float *bias;       /* device fp32 [experts], added to the logits for the choice alone; NULL: none */
+} uw_router;
+
+/*
+ * uw_route - choose each token's experts and the order of the grouped products' rows.
+ *   logits_dev: [tokens, experts] of `dtype`, rows ld elements apart (0: experts).  Token t takes the topk experts
+ *   with the largest logit + bias (in fp32; equal ones by the lower index; NaN counts above +inf):
+ *     ids     int32 [tokens, topk]  the experts, largest first
+ *     weights fp32  [tokens, topk]  score [/ the sum over the chosen] * scale
+ *     offsets int32 [experts + 1]   rows of expert e are [offsets[e], offsets[e + 1])
+ *     row_src int32 [tokens * topk] the token of each row; rows are ordered by (expert, token)
+ *     pos     int32 [tokens, topk]  the row of each (token, choice)
+ *   A row of logits that is all -inf has weights 0 (softmax) and takes experts 0..topk-1.
+ *   workspace: uw_route_workspace_size bytes of device scratch, 16-byte aligned (0 for a few tokens; needs no
+ *   initialisation).  Asynchronous.  The result does not depend on the run.
+ *   Errors: UW_ERR_INVALID_ARG, UW_ERR_SHAPE (tokens < 0, tokens * topk above 2^31 - 1024, ld < experts),
+ *   UW_ERR_WORKSPACE, UW_ERR_CUDA.
+ */
+uw_status uw_route_workspace_size(const uw_router *r, int64_t tokens, size_t *bytes);
+uw_status uw_route(const uw_router *r, const void *logits_dev, uw_out_dtype dtype, int64_t tokens, int64_t ld,
+                   int32_t *ids, float *weights, int32_t *offsets, int32_t *row_src, int32_t *pos, void *workspace,
+                   size_t ws_bytes, uw_stream stream);
+
+/* What uw_block_norm does with each row; the pointers are device addresses, 16-byte aligned. */
+typedef struct {
+    int64_t dim;             /* elements of a row, 1..65536 */
+    const uint16_t *post_weight; /* bf16 [dim]: the block's output is normed with it; NULL: it is not */
+    const uint16_t *gate;    /* bf16 [ceil(rows / gate_every), dim]: multiplies the block's output; NULL: none */
+    int64_t gate_every;      /* consecutive rows that share a row of the gate (rows or more: one row for all) */
+    const uint16_t *pre_weight;  /* bf16 [dim]: weight of the norm that makes u (NULL: no u) */
+    float res_scale, out_scale, eps;
+    int32_t res_dtype;       /* uw_out_dtype of h and h_out */
+    int32_t block_dtype;     /* uw_out_dtype of y */
+} uw_norm;
+
+/*
+ * uw_block_norm - what stands between one block's output and the next block's input, for each row t:
+ *     o = y[t], or sum over j < topk of weights[t, j] y[pos[t, j]]    (a pos outside [0, y_rows) adds nothing)
+ *     o = post_weight * o / sqrt(mean(o^2) + eps)                     with a post_weight
+ *     o = gate[t / gate_every] * o                                    with a gate
+ *     h_out[t] = res_scale * h[t] + out_scale * o
+ *     u[t] = pre_weight * h_out[t] / sqrt(mean(h_out[t]^2) + eps)     with a pre_weight; h_out before its rounding
+ *   All in fp32, one rounding per output.  h, h_out: [rows, dim] of res_dtype; y of block_dtype: [rows, dim], or
+ *   [y_rows, dim] with topk > 0; u: bf16 [rows, dim].  y NULL: no block output (o = 0), for a model's first norm.
+ *   h NULL: no residual.  h_out NULL: not stored.  h_out may be h; u may be y where y is bf16 and topk 0.  Rows are dim elements
+ *   apart; any dim is taken, multiples of 8 (16-byte rows) are fast.  Asynchronous.
+ *   Errors: UW_ERR_INVALID_ARG (NULL or misaligned pointers, bad dtypes, u without pre_weight or the reverse,
+ *   nothing to write, topk outside 0..16, gate_every < 1 with a gate), UW_ERR_SHAPE, UW_ERR_CUDA.
+ */
+uw_status uw_block_norm(const uw_norm *n, int64_t rows, const void *h, void *h_out, const void *y, int64_t y_rows,
+                        const int32_t *pos, const float *weights, int topk, uint16_t *u, uw_stream stream);
+
+/*
+ * uw_token_logprobs - log probabilities of given tokens under softmax(logits / temperature), with the entropy of
+ *   each row's distribution and its most probable tokens, in one call on logits as uw_matmul of a head leaves them.
+ *   logits_dev: [rows, vocab] of `dtype`, rows ld elements apart (0: vocab).
+ *     logprob [rows] fp32: of token targets[r]; 0 where targets[r] < 0 (no token given), NaN where it is >= vocab
+ *     entropy [rows] fp32 in nats
+ *     top_ids int32, top_logprobs fp32 [rows, n_top]: the n_top largest logits, largest first, equal ones by the
+ *     lower index (NaN counts above +inf)
+ *   targets/logprob, entropy and top_ids/top_logprobs are each optional (NULL).  Logits of -inf are tokens masked
+ *   out: probability 0.  A row with nothing but -inf has log probabilities -inf and entropy 0; a row with a NaN or
+ *   +inf has NaN.  0 <= n_top <= min(32, vocab).  No workspace.  Asynchronous; the result does not depend on the run.
+ *   Errors: UW_ERR_INVALID_ARG (NULL, misaligned to the element, temperature not finite and > 0, bad n_top, logprob
+ *   without targets or the reverse), UW_ERR_SHAPE (vocab outside 1..2^24, ld < vocab), UW_ERR_CUDA.
+ */
+uw_status uw_token_logprobs(const void *logits_dev, uw_out_dtype dtype, int64_t rows, int64_t vocab, int64_t ld,
+                            float temperature, const int32_t *targets, float *logprob, float *entropy, int n_top,
+                            int32_t *top_ids, float *top_logprobs, uw_stream stream);
 
 /* uw_check - synchronise `stream` and report (then clear) the matrix's device status word. */
 uw_status uw_check(const uw_matrix *m, uw_stream stream);

@@ -29,6 +29,7 @@ OUT_F32, OUT_BF16 = 0, 1
 KERNEL_AUTO, KERNEL_GEMV, KERNEL_TC = 0, 1, 2
 RESIDENT_HUFFMAN, RESIDENT_BOTH, RESIDENT_PALETTE = 0, 1, 2
 RESIDENT = {"huffman": RESIDENT_HUFFMAN, "both": RESIDENT_BOTH, "palette": RESIDENT_PALETTE}
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 SEQ_DIRECT = -1  # uw_sequence_run schedule: no side-stream transcode, every step its own AUTO plan
 STEP_CONCURRENT = 1  # uw_step flag: the step may overlap the step before it
 SEQ_GROUPS = 65536  # added to a uw_sequence_run schedule: overlap the groups of STEP_CONCURRENT steps
@@ -84,6 +85,18 @@ class GroupInfo(ctypes.Structure):
         return {f: getattr(self, f) for f, _ in self._fields_}
 
 
+class RouterDesc(ctypes.Structure):
+    _fields_ = [("experts", ctypes.c_int32), ("topk", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float), ("bias", ctypes.c_void_p)]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int64), ("post_weight", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("gate_every", ctypes.c_int64), ("pre_weight", ctypes.c_void_p), ("res_scale", ctypes.c_float),
+                ("out_scale", ctypes.c_float), ("eps", ctypes.c_float), ("res_dtype", ctypes.c_int32),
+                ("block_dtype", ctypes.c_int32)]
+
+
 _lib = None
 _VP, _SZ, _I64, _INT = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int64, ctypes.c_int
 
@@ -118,6 +131,10 @@ _SIGS = {
     "uw_group_decode": [_VP, _INT, _INT, _VP, _VP],
     "uw_group_matmul": [_VP, _VP, _I64, _I64, _VP, _VP, _I64, _VP, _I64, _INT, _VP],
     "uw_group_check": [_VP, _VP],
+    "uw_route_workspace_size": [ctypes.POINTER(RouterDesc), _I64, ctypes.POINTER(_SZ)],
+    "uw_route": [ctypes.POINTER(RouterDesc), _VP, _INT, _I64, _I64, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP],
+    "uw_block_norm": [ctypes.POINTER(NormDesc), _I64, _VP, _VP, _VP, _I64, _VP, _VP, _INT, _VP, _VP],
+    "uw_token_logprobs": [_VP, _INT, _I64, _I64, _I64, ctypes.c_float, _VP, _VP, _VP, _INT, _VP, _VP, _VP],
     "uw_status_string": [_INT],
     "uw_last_error": [],
     "uw_version": [],
@@ -376,3 +393,46 @@ class Group:
 
     def check(self, stream=None):
         _check(lib().uw_group_check(self._h, _stream(stream)), "uw_group_check")
+
+
+class Router:
+    """How a layer's router chooses its experts (a ``uw_router``); bias: fp32 [experts] on the device, for the choice
+    alone."""
+
+    def __init__(self, experts: int, topk: int, score: int = SCORE_SOFTMAX, bias=None, renormalize: bool = True, scale: float = 1.0):
+        self._bias = bias  # keeps it alive
+        self.desc = RouterDesc(experts, topk, score, int(renormalize), scale, _ptr(bias) or None)
+
+    def workspace_size(self, tokens: int) -> int:
+        n = ctypes.c_size_t(0)
+        _check(lib().uw_route_workspace_size(ctypes.byref(self.desc), tokens, ctypes.byref(n)), "uw_route_workspace_size")
+        return n.value
+
+    def route(self, logits, tokens: int, ids, weights, offsets, row_src, pos, dtype: int = OUT_F32, ld: int = 0, workspace=None,
+              ws_bytes: int = 0, stream=None):
+        """uw_route: ids, row_src, pos and offsets int32, weights fp32."""
+        _check(lib().uw_route(ctypes.byref(self.desc), _ptr(logits), dtype, tokens, ld, _ptr(ids), _ptr(weights), _ptr(offsets),
+                              _ptr(row_src), _ptr(pos), _ptr(workspace), ws_bytes, _stream(stream)), "uw_route")
+
+
+class BlockNorm:
+    """What stands between one block's output and the next block's input (a ``uw_norm``): the norm after the block, its
+    gate, the residual, the norm before the next block.  Weights and gate are bf16 tensors on the device."""
+
+    def __init__(self, dim: int, post_weight=None, gate=None, gate_every: int = 1, pre_weight=None, res_scale: float = 1.0,
+                 out_scale: float = 1.0, eps: float = 1e-5, res_dtype: int = OUT_BF16, block_dtype: int = OUT_BF16):
+        self._keep = (post_weight, gate, pre_weight)
+        self.desc = NormDesc(dim, _ptr(post_weight) or None, _ptr(gate) or None, gate_every, _ptr(pre_weight) or None, res_scale,
+                             out_scale, eps, res_dtype, block_dtype)
+
+    def run(self, rows: int, h, h_out, y=None, pos=None, weights=None, topk: int = 0, y_rows: int = 0, u=None, stream=None):
+        """uw_block_norm; topk > 0: y holds expert rows, joined by pos and weights [rows, topk]."""
+        _check(lib().uw_block_norm(ctypes.byref(self.desc), rows, _ptr(h), _ptr(h_out), _ptr(y), y_rows, _ptr(pos), _ptr(weights),
+                                   topk, _ptr(u), _stream(stream)), "uw_block_norm")
+
+
+def token_logprobs(logits, rows: int, vocab: int, logprob=None, targets=None, entropy=None, n_top: int = 0, top_ids=None,
+                   top_logprobs=None, dtype: int = OUT_F32, ld: int = 0, temperature: float = 1.0, stream=None):
+    """uw_token_logprobs: log probabilities of `targets` (int32), entropies and the n_top most probable tokens."""
+    _check(lib().uw_token_logprobs(_ptr(logits), dtype, rows, vocab, ld, temperature, _ptr(targets), _ptr(logprob), _ptr(entropy),
+                                   n_top, _ptr(top_ids), _ptr(top_logprobs), _stream(stream)), "uw_token_logprobs")
