@@ -86,6 +86,9 @@ __device__ __forceinline__ void rebuild_chunk_verbatim(const uint4 &S, const uin
     }
 }
 
+// silu(gate) * up; the quotient is within 2 ulp, and 0 where e^-gate overflows
+__device__ __forceinline__ float gated(float gate, float up) { return __fdividef(gate, 1.f + __expf(-gate)) * up; }
+
 // the rank of row r's run among a step's verbatim runs
 __device__ __forceinline__ uint32_t verbatim_rank(const uint32_t *mask, int r)
 {
@@ -108,5 +111,7 @@ struct GroupCall {
     int out_bf16;
 };
 int launch_group_gemv(const GroupCall &c, void *stream);
+bool group_tc_supported(const GroupCall &c);
+int launch_group_tc(const GroupCall &c, void *stream);
 
 }  // namespace uw

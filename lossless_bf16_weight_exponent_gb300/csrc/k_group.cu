@@ -485,6 +485,7 @@ extern "C" uw_status uw_group_matmul(const uw_group *g, const uint16_t *x, int64
     c.y = y;
     c.ldy = ldy;
     c.out_bf16 = od == UW_OUT_BF16;
-    const cudaError_t e = (cudaError_t)launch_group_gemv(c, stream);
+    const bool tc = rows > 8 * (int64_t)g->v.experts && group_tc_supported(c);
+    const cudaError_t e = (cudaError_t)(tc ? launch_group_tc(c, stream) : launch_group_gemv(c, stream));
     return e == cudaSuccess ? UW_OK : cuda_fail(e, "uw_group_matmul: launch");
 }

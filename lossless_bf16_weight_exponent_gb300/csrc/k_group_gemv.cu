@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(32 * kWarps) group_gemv_kernel(const GroupCall
                 for (int w = 0; w < kWarps; w++) s[n] += part[w][n][o][j];
             }
             float f = s[0];
-            if (GATED) f = s[0] / (1.f + __expf(-s[0])) * s[NG - 1];
+            if (GATED) f = gated(s[0], s[NG - 1]);
             const int64_t col = (int64_t)blockIdx.x * kGran + o;
             if (r0 + j < hi && col < v.N) {
                 const int64_t i = (int64_t)(r0 + j) * c.ldy + col;

@@ -1,0 +1,526 @@
+// k_group_tc.cu - the grouped product for experts with many rows (sm_103a): weights rebuilt into tensor memory, tcgen05.
+//
+// A unit is one tile (128 virtual rows of an expert's matrices) times up to 192 of the expert's rows of X, over all of
+// K; one persistent CTA per SM takes every gridDim-th unit of the list (expert, row tile of X, weight tile), the weight
+// tile innermost so that CTAs that run together share their rows of X.  The list follows from the offsets, which each
+// CTA reads on the device.  Warps:
+//   - 0-11, three groups of four: group i % 3 rebuilds step i (128 rows x 64 weights).  Thread = row: four 16-byte and
+//     four 8-byte reads of shared memory without bank conflicts, 32 bf16 pairs, four tcgen05.st of eight columns.  The
+//     A operand never passes through shared memory, which the X tiles need.
+//   - 12: bulk copies of the steps (12 KB, one run of memory each), their records and verbatim runs;
+//   - 13: one thread issues four tcgen05.mma (M = 128, N = rows of X up to a multiple of 16, K = 16) a step, A from
+//     tensor memory;
+//   - 14, 15: X tiles [<= 192 rows x 64] bf16 in the 128-byte swizzle.  Rows in order come in tensor copies of 32 rows
+//     (warp 14); rows with sources in 16-byte cp.async, eight lanes a row, three steps in flight.
+//   - 16-23: the epilogue of a finished unit, two warps per lane quarter of tensor memory.  In a gated tile lanes 0-15
+//     of a warp hold gate rows and lanes 16-31 the up rows that belong to them: eight exchanges between the halves per
+//     16 columns give each lane both factors of eight outputs.
+// Tensor memory: two accumulators of 192 columns, so that a unit's epilogue runs under the next unit's products, and
+// four slots of 32 columns for A.
+// Every wait is bounded; when one runs out the kernel latches DEV_TIMEOUT, waits for its copies and products in flight,
+// frees its tensor memory and ends.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "group.cuh"
+#include "uw_internal.h"
+
+namespace uw {
+
+namespace {
+
+using namespace dev;
+
+constexpr int kGroups = 3;                    // rebuild groups of four warps
+constexpr int kRebuildWarps = 4 * kGroups;
+constexpr int kProdWarp = kRebuildWarps, kMmaWarp = kProdWarp + 1, kXWarp0 = kProdWarp + 2, kXWarps = 2;
+constexpr int kEpiWarp0 = kXWarp0 + kXWarps;  // a multiple of four: warp % 4 is the lane quarter of tensor memory
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+constexpr int kBN = 192;                      // rows of X per unit at most
+constexpr int kVCs = 8;                       // verbatim runs of a step staged with it (beyond: global loads)
+constexpr uint32_t kRecOff = kStepBytes, kVOff = kRecOff + 128;
+constexpr uint32_t kWStage = kVOff + kVCs * 64;
+constexpr uint32_t kXStage = kBN * 128;
+constexpr int kSW = 6, kSX = 5, kSA = 4;
+constexpr int kXFlight = 3;                   // steps of X that a gathering warp has in flight
+constexpr int kACol = 2 * kBN;                // tensor memory: two accumulators, then kSA slots of 32 columns
+constexpr size_t kSmem = 1024 + (size_t)kSX * kXStage + (size_t)kSW * kWStage + 512 + 2 * 4 * (kMaxExperts + 4) + 8 * kBN;
+static_assert(kSmem <= 227 * 1024, "shared memory");
+static_assert(kEpiWarp0 % 4 == 0 && kWStage % 128 == 0 && kACol + 32 * kSA <= 512 && kXFlight < kSX, "layout");
+static_assert((2 * (kSW + kSX + kSA) + 5) * 8 + 8 <= 512, "barriers");
+
+struct TcArgs {
+    CUtensorMap tm_x;  // X [x_rows, K] bf16, box {64, 32}, 128-byte swizzle (rows in order only)
+    GroupCall c;
+};
+
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// 16 bytes to shared memory, or zeros
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool zero)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(zero ? 0u : 16u) : "memory");
+}
+
+// eight consecutive 32-bit columns of this warp's 32 lanes of tensor memory
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+struct Unit {
+    int e, r0, n, tile;  // expert, first row, rows (1..kBN), weight tile
+};
+
+// this CTA's units in order; off: clamped offsets, tcum: row tiles of X before each expert (shared memory)
+struct Units {
+    const int *off, *tcum;
+    int64_t u, total;
+    int e, tiles, experts;
+    __device__ __forceinline__ Units(const int *off_, const int *tcum_, const GroupView &v)
+        : off(off_), tcum(tcum_), u(blockIdx.x), e(0), tiles(v.tiles), experts(v.experts)
+    {
+        total = (int64_t)tcum[experts] * tiles;
+    }
+    __device__ __forceinline__ bool next(Unit &w)
+    {
+        if (u >= total) return false;
+        const int tt = (int)(u / tiles);
+        w.tile = (int)(u - (int64_t)tt * tiles);
+        while (tt >= tcum[e + 1]) e++;
+        w.e = e;
+        w.r0 = off[e] + (tt - tcum[e]) * kBN;
+        w.n = min(kBN, off[e + 1] - w.r0);
+        u += gridDim.x;
+        return true;
+    }
+};
+
+template <bool GATED, bool GATHER>
+__global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_constant__ TcArgs a)
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t pad = (1024u - (saddr(smem_raw) & 1023u)) & 1023u;
+    uint8_t *xring = smem_raw + pad;                  // [kSX][kXStage], 1024-aligned
+    uint8_t *wring = xring + kSX * kXStage;           // [kSW][kWStage]: step, record, verbatim runs
+    uint64_t *wfull = (uint64_t *)(wring + kSW * kWStage);
+    uint64_t *wempty = wfull + kSW;
+    uint64_t *xfull = wempty + kSW;
+    uint64_t *xempty = xfull + kSX;
+    uint64_t *afull = xempty + kSX;
+    uint64_t *aempty = afull + kSA;
+    uint64_t *accfull = aempty + kSA, *accempty = accfull + 2, *done = accempty + 2;
+    uint32_t *tmem_slot = (uint32_t *)(done + 1);
+    int *off = (int *)((uint8_t *)wfull + 512);       // [experts + 1]
+    int *tcum = off + kMaxExperts + 4;                // [experts + 1]
+    int64_t *xsrc = (int64_t *)(tcum + kMaxExperts + 4);  // [kBN] a unit's rows of X (gather): byte offset, -1 for zeros
+
+    const GroupView &v = a.c.v;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int ksteps = v.ksteps;
+
+    if (threadIdx.x == 32 * kProdWarp) {
+        for (int s = 0; s < kSW; s++) {
+            mbar_init(&wfull[s], 1);
+            mbar_init(&wempty[s], 4);
+        }
+        for (int s = 0; s < kSX; s++) {
+            mbar_init(&xfull[s], GATHER ? kXWarps : 1);
+            mbar_init(&xempty[s], 1);
+        }
+        for (int s = 0; s < kSA; s++) {
+            mbar_init(&afull[s], 4);
+            mbar_init(&aempty[s], 1);
+        }
+        for (int b = 0; b < 2; b++) {
+            mbar_init(&accfull[b], 1);
+            mbar_init(&accempty[b], kEpiWarps);
+        }
+        mbar_init(done, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_slot)), "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (warp == 0) {
+        // the experts' row tiles: a running sum, 32 experts at a time
+        const int R = (int)a.c.rows;
+        int carry = 0;
+        for (int e0 = 0; e0 < v.experts; e0 += 32) {
+            const int e = e0 + lane;
+            int l = 0, h = 0;
+            if (e < v.experts) {
+                l = min(max(__ldg(a.c.offsets + e), 0), R);
+                h = min(max(__ldg(a.c.offsets + e + 1), 0), R);
+            }
+            const int t = h > l ? (h - l + kBN - 1) / kBN : 0;
+            int s = t;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xFFFFFFFFu, s, d);
+                if (lane >= d) s += o;
+            }
+            if (e < v.experts) {
+                off[e] = l;
+                tcum[e] = carry + s - t;
+                if (e == v.experts - 1) {
+                    off[e + 1] = h;
+                    tcum[e + 1] = carry + s;
+                }
+            }
+            carry += __shfl_sync(0xFFFFFFFFu, s, 31);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    Units units(off, tcum, v);
+    Unit w;
+
+    if (warp == kProdWarp) {
+        // ---------------------------------------------------------------------------------------- weight copies
+        bool ok = true;
+        int i = 0, s = 0;
+        uint32_t ph = 0;
+        // lane l: {first, count} of the verbatim runs of step l of the 32 at hand; the next 32 in flight
+        auto recs_at = [&](const Unit &q, int ks) {
+            const int64_t st = ((int64_t)q.e * v.tiles + q.tile) * ksteps + ks + lane;
+            return ks + lane < ksteps ? __ldg((const uint2 *)&v.recs[st].first) : make_uint2(0, 0);
+        };
+        Unit nx;
+        bool have = units.next(w), have_nx = false;
+        uint2 cur = make_uint2(0, 0), nxt = cur;
+        if (have) nxt = recs_at(w, 0);
+        while (have && ok) {
+            have_nx = units.next(nx);
+            const int64_t st0 = ((int64_t)w.e * v.tiles + w.tile) * ksteps;
+            for (int ks = 0; ks < ksteps; ks++, i++) {
+                if ((ks & 31) == 0) {
+                    cur = nxt;
+                    if (ks + 32 < ksteps) nxt = recs_at(w, ks + 32);
+                    else if (have_nx) nxt = recs_at(nx, 0);
+                }
+                const uint32_t first = __shfl_sync(0xFFFFFFFFu, cur.x, ks & 31);
+                const uint32_t nv = min(__shfl_sync(0xFFFFFFFFu, cur.y, ks & 31), (uint32_t)kVCs);
+                int go = 1;
+                if (lane == 0) {
+                    if (i >= kSW && !mbar_wait(&wempty[s], ph ^ 1u)) go = 0;
+                    else {
+                        uint8_t *d = wring + s * kWStage;
+                        const uint32_t fb = saddr(&wfull[s]);
+                        mbar_expect_tx(&wfull[s], kStepBytes + 32u + 64u * nv);
+                        bulk_copy(saddr(d), v.steps + (st0 + ks) * kStepBytes, kStepBytes, fb);
+                        bulk_copy(saddr(d + kRecOff), v.recs + st0 + ks, 32u, fb);
+                        if (nv) bulk_copy(saddr(d + kVOff), v.verb + (uint64_t)first * 64, nv * 64u, fb);
+                    }
+                }
+                if (!__shfl_sync(0xFFFFFFFFu, go, 0)) {
+                    ok = false;
+                    break;
+                }
+                if (++s == kSW) { s = 0; ph ^= 1u; }
+            }
+            w = nx;
+            have = have_nx;
+        }
+        if (!ok && lane == 0) {
+            atomicExch(v.status, (int)DEV_TIMEOUT);
+            for (int q = max(0, i - kSW); q < i; q++) mbar_wait(&wfull[q % kSW], (q / kSW) & 1);
+        }
+    } else if (warp >= kXWarp0 && warp < kEpiWarp0) {
+        // ---------------------------------------------------------------------------------------- X copies
+        bool ok = true;
+        int i = 0, s = 0;
+        uint32_t ph = 0;
+        if constexpr (GATHER) {
+            // rows 8 j + 4 (warp) + lane / 8 of the unit; 16-byte chunk lane % 8 of their 128 bytes
+            const int xw = warp - kXWarp0, rl = 4 * xw + (lane >> 3), ch = lane & 7;
+            const uint32_t d0 = (uint32_t)(rl * 128 + ((ch ^ rl) << 4));  // row 8 j + rl, its swizzle phase rl
+            int ready = 0, rs = 0;  // steps handed over, the next one's stage
+            auto hand_over = [&] {
+                // this step's bytes have landed in every lane's view: visible to the tensor core before the arrival
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&xfull[rs]);
+                if (++rs == kSX) rs = 0;
+                ready++;
+            };
+            while (ok && units.next(w)) {
+                const int bn = (w.n + 15) & ~15;
+                // each warp lists its own rows
+                __syncwarp();
+                for (int q = lane; q < bn / 2; q += 32) {
+                    const int r = 8 * (q >> 2) + 4 * xw + (q & 3);
+                    int64_t o = -1;
+                    if (r < w.n) {
+                        const int src = __ldg(a.c.row_src + w.r0 + r);
+                        if (src >= 0 && src < a.c.x_rows) o = (int64_t)src * a.c.ldx * 2;
+                    }
+                    xsrc[r] = o;
+                }
+                __syncwarp();
+                for (int ks = 0; ks < ksteps; ks++) {
+                    int go = 1;
+                    if (lane == 0 && i >= kSX && !mbar_wait(&xempty[s], ph ^ 1u)) go = 0;
+                    if (!__shfl_sync(0xFFFFFFFFu, go, 0)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t d = saddr(xring + s * kXStage) + d0;
+                    const uint8_t *xk = (const uint8_t *)a.c.x + ks * 128 + 16 * ch;
+                    for (int j = 0; j < bn / 8; j++) {
+                        const int64_t o = xsrc[8 * j + rl];
+                        copy16(d + 1024 * j, xk + (o < 0 ? 0 : o), o < 0);
+                    }
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+                    i++;
+                    if (++s == kSX) { s = 0; ph ^= 1u; }
+                    if (i - ready > kXFlight) {
+                        asm volatile("cp.async.wait_group %0;" ::"n"(kXFlight) : "memory");
+                        hand_over();
+                    }
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            while (ready < i) hand_over();
+        } else if (warp == kXWarp0) {
+            while (ok && units.next(w)) {
+                const int boxes = (w.n + 31) / 32;
+                for (int ks = 0; ks < ksteps; ks++) {
+                    int go = 1;
+                    if (lane == 0) {
+                        if (i >= kSX && !mbar_wait(&xempty[s], ph ^ 1u)) go = 0;
+                        else mbar_expect_tx(&xfull[s], (uint32_t)boxes * 4096u);
+                    }
+                    if (!__shfl_sync(0xFFFFFFFFu, go, 0)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane < boxes) tma2d(xring + s * kXStage + 4096 * lane, &a.tm_x, ks * kStepW, w.r0 + 32 * lane, &xfull[s]);
+                    __syncwarp();
+                    i++;
+                    if (++s == kSX) { s = 0; ph ^= 1u; }
+                }
+            }
+            if (!ok && lane == 0)
+                for (int q = max(0, i - kSX); q < i; q++) mbar_wait(&xfull[q % kSX], (q / kSX) & 1);
+        }
+        if (!ok && lane == 0) atomicExch(v.status, (int)DEV_TIMEOUT);
+    } else if (warp == kMmaWarp) {
+        // ---------------------------------------------------------------------------------------- MMA issue
+        if (lane == 0) {
+            bool ok = true, any = false;
+            int sx = 0, sa = 0, nu = 0;
+            uint32_t phx = 0, pha = 0;
+            while (ok && units.next(w)) {
+                const uint32_t id = idesc_bf16(kTileRows, (w.n + 15) & ~15);
+                const int buf = nu & 1;
+                if (nu >= 2 && !mbar_wait(&accempty[buf], ((nu >> 1) - 1) & 1)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t d = tmem + buf * kBN;
+                for (int ks = 0; ks < ksteps; ks++) {
+                    if (!mbar_wait(&afull[sa], pha) || !mbar_wait(&xfull[sx], phx)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t at = tmem + kACol + 32 * sa, xb = saddr(xring + sx * kXStage);
+#pragma unroll
+                    for (int kk = 0; kk < 4; kk++)
+                        mma_ts(d, at + 8 * kk, smem_desc_sw128(xb + 32 * kk), id, (ks | kk) ? 1u : 0u);
+                    any = true;
+                    mma_commit(&aempty[sa]);
+                    mma_commit(&xempty[sx]);
+                    if (++sa == kSA) { sa = 0; pha ^= 1u; }
+                    if (++sx == kSX) { sx = 0; phx ^= 1u; }
+                }
+                if (ok) mma_commit(&accfull[buf]);
+                nu++;
+            }
+            if (!ok) atomicExch(v.status, (int)DEV_TIMEOUT);
+            if (any) {
+                // every product issued has completed before the tensor memory is freed
+                mma_commit(done);
+                if (!mbar_wait(done, 0)) atomicExch(v.status, (int)DEV_TIMEOUT);
+            }
+        }
+    } else if (warp < kRebuildWarps) {
+        // ---------------------------------------------------------------------------------------- rebuild
+        const int grp = warp >> 2, r = 32 * (warp & 3) + lane;  // row of the tile
+        const uint32_t o_s = (r >> 4) * 1024 + ((r >> 3) & 1) * 512 + (r & 7) * 16;
+        const uint32_t o_c = kStepSm + (r >> 4) * 512 + (r & 7) * 16 + ((r >> 3) & 1) * 8;
+        const uint32_t t_lane = (uint32_t)(32 * (warp & 3)) << 16;
+        bool ok = true;
+        int i = 0;  // steps before this unit
+        while (ok && units.next(w)) {
+            const uint32_t B = GATED ? __ldg(v.base + 2 * w.e + ((r >> 4) & 1)) : __ldg(v.base + w.e);
+            for (int ks = (kGroups - i % kGroups + grp) % kGroups; ks < ksteps; ks += kGroups) {
+                const int q = i + ks, s = q % kSW, sa = q % kSA;
+                if (!mbar_wait(&wfull[s], (q / kSW) & 1)) { ok = false; break; }
+                const uint8_t *st = wring + s * kWStage;
+                const uint32_t *mask = (const uint32_t *)(st + kRecOff);
+                const uint32_t mw = mask[r >> 5];
+                uint4 S[4];
+                uint2 C[4];
+#pragma unroll
+                for (int t = 0; t < 4; t++) {
+                    S[t] = *(const uint4 *)(st + o_s + 128 * t);
+                    C[t] = *(const uint2 *)(st + o_c + 128 * t);
+                }
+                // the stage's reads of steps and the A slot are apart: wait for the slot with the words in registers
+                if (q >= kSA && !mbar_wait(&aempty[sa], ((q / kSA) & 1) ^ 1)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t at = tmem + t_lane + kACol + 32 * sa;
+                const bool verb = (mw >> lane) & 1u;
+                const uint32_t rank = verb ? verbatim_rank(mask, r) : 0u;
+#pragma unroll
+                for (int t = 0; t < 4; t++) {
+                    uint32_t p[8];
+                    rebuild_chunk(S[t], C[t], B, p);
+                    if (mw) {
+                        // a verbatim run among the warp's rows (the same word for every lane)
+                        if (verb) {
+                            uint4 E;
+                            if (rank < (uint32_t)kVCs) E = *(const uint4 *)(st + kVOff + rank * 64 + 16 * t);
+                            else E = __ldg((const uint4 *)(v.verb + ((uint64_t)mask[4] + rank) * 64 + 16 * t));
+                            rebuild_chunk_verbatim(S[t], E, p);
+                        }
+                        __syncwarp();
+                    }
+                    tmem_st8(at + 8 * t, p);
+                }
+                // the stage's reads are done before the next copy into it (the async proxy) is asked for
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&wempty[s]);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&afull[sa]);
+            }
+            i += ksteps;
+        }
+        if (!ok && lane == 0) atomicExch(v.status, (int)DEV_TIMEOUT);
+    } else if (warp >= kEpiWarp0) {
+        // ---------------------------------------------------------------------------------------- epilogue
+        const int q = warp & 3, half = (warp - kEpiWarp0) >> 2;
+        bool ok = true;
+        int nu = 0;
+        while (units.next(w)) {
+            const int buf = nu & 1;
+            if (!mbar_wait(&accfull[buf], (nu >> 1) & 1)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + buf * kBN;
+            const int64_t col = GATED ? ((int64_t)w.tile * 4 + q) * 16 + (lane & 15) : (int64_t)w.tile * kTileRows + 32 * q + lane;
+            const bool in = col < v.N;
+            for (int c0 = 16 * half; c0 < w.n; c0 += 32) {
+                uint32_t x[16];
+                tmem_ld16(acc + c0, x);
+                tmem_wait_ld();
+                constexpr int NO = GATED ? 8 : 16;
+                float f[NO];
+                int first = c0;
+                if constexpr (GATED) {
+                    const bool up = lane >= 16;
+                    first += up ? 8 : 0;
+#pragma unroll
+                    for (int j = 0; j < 8; j++) {
+                        const float mine = __uint_as_float(up ? x[8 + j] : x[j]);
+                        const float other = __shfl_xor_sync(0xFFFFFFFFu, __uint_as_float(up ? x[j] : x[8 + j]), 16);
+                        f[j] = gated(up ? other : mine, up ? mine : other);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; j++) f[j] = __uint_as_float(x[j]);
+                }
+                const int m = in ? w.n - first : 0;
+                const int64_t o = (int64_t)(w.r0 + first) * a.c.ldy + col;
+                if (a.c.out_bf16) {
+                    __nv_bfloat16 *p = (__nv_bfloat16 *)a.c.y + o;
+#pragma unroll
+                    for (int j = 0; j < NO; j++, p += a.c.ldy)
+                        if (j < m) *p = __float2bfloat16_rn(f[j]);
+                } else {
+                    float *p = (float *)a.c.y + o;
+#pragma unroll
+                    for (int j = 0; j < NO; j++, p += a.c.ldy)
+                        if (j < m) *p = f[j];
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&accempty[buf]);
+            nu++;
+        }
+        if (!ok && lane == 0) atomicExch(v.status, (int)DEV_TIMEOUT);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    }
+}
+
+template <bool GATED, bool GATHER>
+cudaError_t launch_one(const TcArgs &a, int grid, cudaStream_t st)
+{
+    static bool attr = false;
+    if (!attr) {
+        const cudaError_t e = cudaFuncSetAttribute(group_tc_kernel<GATED, GATHER>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+        if (e != cudaSuccess) return e;
+        attr = true;
+    }
+    group_tc_kernel<GATED, GATHER><<<grid, kThreads, kSmem, st>>>(a);
+    return cudaGetLastError();
+}
+
+bool map_x(CUtensorMap *m, const GroupCall &c)
+{
+    auto fn = (PFN_cuTensorMapEncodeTiled_v12000)tensor_map_encoder();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)c.v.K, (cuuint64_t)c.x_rows};
+    cuuint64_t strides[1] = {(cuuint64_t)c.ldx * 2};
+    cuuint32_t box[2] = {64, 32};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t *>(c.x), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+bool group_tc_supported(const GroupCall &c)
+{
+    // the map's row stride is below 2^40 bytes
+    return c.x_rows > 0 && c.ldx < ((int64_t)1 << 39) && tensor_map_encoder() != nullptr;
+}
+
+int launch_group_tc(const GroupCall &c, void *stream)
+{
+    TcArgs a;
+    memset(&a, 0, sizeof a);
+    if (!c.row_src && !map_x(&a.tm_x, c)) return cudaErrorInvalidValue;
+    a.c = c;
+    // at least one expert's row tile for each kBN rows, at most one more for each expert
+    const int64_t most = ((c.rows + kBN - 1) / kBN + std::min<int64_t>(c.v.experts, c.rows)) * c.v.tiles;
+    const int grid = (int)std::min<int64_t>(num_sms(), most);
+    cudaStream_t st = (cudaStream_t)stream;
+    if (c.v.gated) return c.row_src ? launch_one<true, true>(a, grid, st) : launch_one<true, false>(a, grid, st);
+    return c.row_src ? launch_one<false, true>(a, grid, st) : launch_one<false, false>(a, grid, st);
+}
+
+}  // namespace uw
