@@ -10,9 +10,10 @@
 //   - 12: bulk copies of the steps (12 KB, one run of memory each), their records and verbatim runs;
 //   - 13: one thread issues four tcgen05.mma (M = 128, N = rows of X up to a multiple of 16, K = 16) a step, A from
 //     tensor memory;
-//   - 14, 15: X tiles [<= 192 rows x 64] bf16 in the 128-byte swizzle.  Rows in order come in tensor copies of 32 rows
-//     (warp 14); rows with sources in 16-byte cp.async, eight lanes a row, three steps in flight.
-//   - 16-23: the epilogue of a finished unit, two warps per lane quarter of tensor memory.  In a gated tile lanes 0-15
+//   - 14-19: X tiles [<= 192 rows x 64] bf16 in the 128-byte swizzle.  Rows in order come in tensor copies of 32 rows
+//     (warp 14); rows with sources in 16-byte cp.async, a warp for each
+//     stage of the ring.
+//   - 20-27: the epilogue of a finished unit, two warps per lane quarter of tensor memory.  In a gated tile lanes 0-15
 //     of a warp hold gate rows and lanes 16-31 the up rows that belong to them: eight exchanges between the halves per
 //     16 columns give each lane both factors of eight outputs.
 // Tensor memory: two accumulators of 192 columns, so that a unit's epilogue runs under the next unit's products, and
@@ -38,8 +39,8 @@ using namespace dev;
 
 constexpr int kGroups = 3;                    // rebuild groups of four warps
 constexpr int kRebuildWarps = 4 * kGroups;
-constexpr int kProdWarp = kRebuildWarps, kMmaWarp = kProdWarp + 1, kXWarp0 = kProdWarp + 2, kXWarps = 2;
-constexpr int kEpiWarp0 = kXWarp0 + kXWarps;  // a multiple of four: warp % 4 is the lane quarter of tensor memory
+constexpr int kProdWarp = kRebuildWarps, kMmaWarp = kProdWarp + 1, kXWarp0 = kProdWarp + 2;
+constexpr int kEpiWarp0 = kXWarp0 + 6;  // a multiple of four: warp % 4 is the lane quarter of tensor memory
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 constexpr int kBN = 192;                      // rows of X per unit at most
@@ -48,11 +49,14 @@ constexpr uint32_t kRecOff = kStepBytes, kVOff = kRecOff + 128;
 constexpr uint32_t kWStage = kVOff + kVCs * 64;
 constexpr uint32_t kXStage = kBN * 128;
 constexpr int kSW = 6, kSX = 5, kSA = 4;
-constexpr int kXFlight = 3;                   // steps of X that a gathering warp has in flight
 constexpr int kACol = 2 * kBN;                // tensor memory: two accumulators, then kSA slots of 32 columns
-constexpr size_t kSmem = 1024 + (size_t)kSX * kXStage + (size_t)kSW * kWStage + 512 + 2 * 4 * (kMaxExperts + 4) + 8 * kBN;
+constexpr size_t kSmem = 1024 + (size_t)kSX * kXStage + (size_t)kSW * kWStage + 512 + 2 * 4 * (kMaxExperts + 4) + 4 * kSX * kBN;
 static_assert(kSmem <= 227 * 1024, "shared memory");
-static_assert(kEpiWarp0 % 4 == 0 && kWStage % 128 == 0 && kACol + 32 * kSA <= 512 && kXFlight < kSX, "layout");
+// A stage of the weight ring belongs to one rebuild group for good.  Copies land out of order, so a group that waited for
+// a stage last read by another group could be a whole turn ahead of a copy that has not landed, where the barrier's
+// parity is the same as of the turn it waits for.
+static_assert(kSW % kGroups == 0, "weight ring");
+static_assert(kEpiWarp0 % 4 == 0 && kWStage % 128 == 0 && kACol + 32 * kSA <= 512 && kXWarp0 + kSX <= kEpiWarp0, "layout");
 static_assert((2 * (kSW + kSX + kSA) + 5) * 8 + 8 <= 512, "barriers");
 
 struct TcArgs {
@@ -65,6 +69,14 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                  "l"(src), "r"(bytes), "r"(bar)
                  : "memory");
+}
+
+// true in one thread of the (whole) warp
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
 }
 
 // 16 bytes to shared memory, or zeros
@@ -126,10 +138,10 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
     uint32_t *tmem_slot = (uint32_t *)(done + 1);
     int *off = (int *)((uint8_t *)wfull + 512);       // [experts + 1]
     int *tcum = off + kMaxExperts + 4;                // [experts + 1]
-    int64_t *xsrc = (int64_t *)(tcum + kMaxExperts + 4);  // [kBN] a unit's rows of X (gather): byte offset, -1 for zeros
+    int *xrows = tcum + kMaxExperts + 4;              // [kSX][kBN] (sources) a warp's unit's rows of X, -1: zeros
 
     const GroupView &v = a.c.v;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: a uniform value
     const int ksteps = v.ksteps;
 
     if (threadIdx.x == 32 * kProdWarp) {
@@ -138,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
             mbar_init(&wempty[s], 4);
         }
         for (int s = 0; s < kSX; s++) {
-            mbar_init(&xfull[s], GATHER ? kXWarps : 1);
+            mbar_init(&xfull[s], 1);
             mbar_init(&xempty[s], 1);
         }
         for (int s = 0; s < kSA; s++) {
@@ -249,56 +261,49 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
         int i = 0, s = 0;
         uint32_t ph = 0;
         if constexpr (GATHER) {
-            // rows 8 j + 4 (warp) + lane / 8 of the unit; 16-byte chunk lane % 8 of their 128 bytes
-            const int xw = warp - kXWarp0, rl = 4 * xw + (lane >> 3), ch = lane & 7;
-            const uint32_t d0 = (uint32_t)(rl * 128 + ((ch ^ rl) << 4));  // row 8 j + rl, its swizzle phase rl
-            int ready = 0, rs = 0;  // steps handed over, the next one's stage
-            auto hand_over = [&] {
-                // this step's bytes have landed in every lane's view: visible to the tensor core before the arrival
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&xfull[rs]);
-                if (++rs == kSX) rs = 0;
-                ready++;
-            };
-            while (ok && units.next(w)) {
-                const int bn = (w.n + 15) & ~15;
-                // each warp lists its own rows
-                __syncwarp();
-                for (int q = lane; q < bn / 2; q += 32) {
-                    const int r = 8 * (q >> 2) + 4 * xw + (q & 3);
-                    int64_t o = -1;
-                    if (r < w.n) {
-                        const int src = __ldg(a.c.row_src + w.r0 + r);
-                        if (src >= 0 && src < a.c.x_rows) o = (int64_t)src * a.c.ldx * 2;
+            // Warp x copies steps x, x + kSX, ... into stage x: it asks for a step's 16-byte pieces (eight lanes a row),
+            // waits for them and hands the stage over, while the other warps' steps are on their way.
+            const int x = warp - kXWarp0;
+            if (x < kSX) {
+                int *rows = xrows + x * kBN;
+                const uint32_t xs = saddr(xring + x * kXStage);
+                constexpr int kL = kBN / 32;
+                int r[kL];  // the next unit's rows, on their way before it begins
+                auto fetch = [&](const Unit &q) {
+#pragma unroll
+                    for (int j = 0; j < kL; j++) r[j] = 32 * j + lane < q.n ? __ldg(a.c.row_src + q.r0 + 32 * j + lane) : -1;
+                };
+                Unit nx;
+                bool have = units.next(w);
+                if (have) fetch(w);
+                int turn = 0;
+                while (ok && have) {
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < kL; j++) rows[32 * j + lane] = r[j] >= 0 && r[j] < a.c.x_rows ? r[j] : -1;
+                    __syncwarp();
+                    const bool more = units.next(nx);
+                    if (more) fetch(nx);
+                    const int pieces = (((w.n + 15) & ~15) * 8) / 32;  // 32 lanes copy four rows
+                    for (int ks = (kSX - i % kSX + x) % kSX; ks < ksteps; ks += kSX, turn++) {
+                        if (turn > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(&xempty[x], (turn - 1) & 1))) { ok = false; break; }
+                        const uint8_t *xk = (const uint8_t *)a.c.x + ks * 128 + 16 * (lane & 7);
+#pragma unroll 8
+                        for (int j = 0; j < pieces; j++) {
+                            const int q = 4 * j + (lane >> 3), row = rows[q];
+                            copy16(xs + q * 128 + (((lane ^ q) & 7) << 4), xk + (row < 0 ? 0 : (int64_t)row * a.c.ldx * 2), row < 0);
+                        }
+                        asm volatile("cp.async.wait_all;" ::: "memory");
+                        // every lane's pieces are visible to the tensor core before the arrival
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&xfull[x]);
                     }
-                    xsrc[r] = o;
-                }
-                __syncwarp();
-                for (int ks = 0; ks < ksteps; ks++) {
-                    int go = 1;
-                    if (lane == 0 && i >= kSX && !mbar_wait(&xempty[s], ph ^ 1u)) go = 0;
-                    if (!__shfl_sync(0xFFFFFFFFu, go, 0)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t d = saddr(xring + s * kXStage) + d0;
-                    const uint8_t *xk = (const uint8_t *)a.c.x + ks * 128 + 16 * ch;
-                    for (int j = 0; j < bn / 8; j++) {
-                        const int64_t o = xsrc[8 * j + rl];
-                        copy16(d + 1024 * j, xk + (o < 0 ? 0 : o), o < 0);
-                    }
-                    asm volatile("cp.async.commit_group;" ::: "memory");
-                    i++;
-                    if (++s == kSX) { s = 0; ph ^= 1u; }
-                    if (i - ready > kXFlight) {
-                        asm volatile("cp.async.wait_group %0;" ::"n"(kXFlight) : "memory");
-                        hand_over();
-                    }
+                    i += ksteps;
+                    w = nx;
+                    have = more;
                 }
             }
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            while (ready < i) hand_over();
         } else if (warp == kXWarp0) {
             while (ok && units.next(w)) {
                 const int boxes = (w.n + 31) / 32;
@@ -324,38 +329,44 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
         if (!ok && lane == 0) atomicExch(v.status, (int)DEV_TIMEOUT);
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------------------------------------- MMA issue
-        if (lane == 0) {
-            bool ok = true, any = false;
-            int sx = 0, sa = 0, nu = 0;
-            uint32_t phx = 0, pha = 0;
-            while (ok && units.next(w)) {
-                const uint32_t id = idesc_bf16(kTileRows, (w.n + 15) & ~15);
-                const int buf = nu & 1;
-                if (nu >= 2 && !mbar_wait(&accempty[buf], ((nu >> 1) - 1) & 1)) { ok = false; break; }
+        // The whole warp walks the steps, so that the addresses and descriptors are uniform values; one elected thread
+        // issues.  (A loop inside `if (lane == 0)` moved every operand from an ordinary register for each instruction:
+        // 870 cycles a step at any N.)
+        bool ok = true;
+        int sx = 0, sa = 0, nu = 0;
+        uint32_t phx = 0, pha = 0;
+        const bool leader = elect_one();
+        const uint64_t desc0 = smem_desc_sw128(saddr(xring));
+        while (ok && units.next(w)) {
+            const uint32_t id = idesc_bf16(kTileRows, (w.n + 15) & ~15);
+            const int buf = nu & 1;
+            if (nu >= 2 && !__all_sync(0xFFFFFFFFu, mbar_wait(&accempty[buf], ((nu >> 1) - 1) & 1))) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t d = tmem + buf * kBN;
+            for (int ks = 0; ks < ksteps; ks++) {
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(&afull[sa], pha) && mbar_wait(&xfull[sx], phx))) { ok = false; break; }
                 tc_fence_after();
-                const uint32_t d = tmem + buf * kBN;
-                for (int ks = 0; ks < ksteps; ks++) {
-                    if (!mbar_wait(&afull[sa], pha) || !mbar_wait(&xfull[sx], phx)) { ok = false; break; }
-                    tc_fence_after();
-                    const uint32_t at = tmem + kACol + 32 * sa, xb = saddr(xring + sx * kXStage);
+                if (leader) {
+                    const uint32_t at = tmem + kACol + 32 * sa;
+                    const uint64_t xd = desc0 + (uint64_t)(sx * (int)(kXStage >> 4));
 #pragma unroll
-                    for (int kk = 0; kk < 4; kk++)
-                        mma_ts(d, at + 8 * kk, smem_desc_sw128(xb + 32 * kk), id, (ks | kk) ? 1u : 0u);
-                    any = true;
+                    for (int kk = 0; kk < 4; kk++) mma_ts(d, at + 8 * kk, xd + 2 * kk, id, (ks | kk) ? 1u : 0u);
                     mma_commit(&aempty[sa]);
                     mma_commit(&xempty[sx]);
-                    if (++sa == kSA) { sa = 0; pha ^= 1u; }
-                    if (++sx == kSX) { sx = 0; phx ^= 1u; }
+                    if (ks == ksteps - 1) mma_commit(&accfull[buf]);
                 }
-                if (ok) mma_commit(&accfull[buf]);
-                nu++;
+                __syncwarp();
+                if (++sa == kSA) { sa = 0; pha ^= 1u; }
+                if (++sx == kSX) { sx = 0; phx ^= 1u; }
             }
-            if (!ok) atomicExch(v.status, (int)DEV_TIMEOUT);
-            if (any) {
-                // every product issued has completed before the tensor memory is freed
-                mma_commit(done);
-                if (!mbar_wait(done, 0)) atomicExch(v.status, (int)DEV_TIMEOUT);
-            }
+            nu++;
+        }
+        if (!ok && leader) atomicExch(v.status, (int)DEV_TIMEOUT);
+        if (nu > 0) {
+            // every product issued has completed before the tensor memory is freed
+            if (leader) mma_commit(done);
+            __syncwarp();
+            if (!mbar_wait(done, 0) && leader) atomicExch(v.status, (int)DEV_TIMEOUT);
         }
     } else if (warp < kRebuildWarps) {
         // ---------------------------------------------------------------------------------------- rebuild
