@@ -3,9 +3,10 @@
 // A group's matrices are cut into virtual rows: of one matrix its rows; of a gated expert 16 rows of the gate matrix,
 // the 16 rows of the up matrix that belong to them, the next 16 of the gate matrix, and so on, so that a kernel that
 // holds 32 virtual rows holds both factors of 16 outputs.  16 virtual rows x 64 weights of K are a granule, eight
-// granules (128 rows) a tile, and a tile's 64 weights of K a step.  A step is one run of 12288 bytes: 8 KB of
-// sign+mantissa bytes (granule after granule), then 4 KB of 4-bit exponent distances.  Steps follow each other along
-// K, tiles along N, experts last, so a tile is one stream of memory whatever N is.
+// granules (128 rows) a tile, and a tile's 64 weights of K a step.  A step is one run of 12320 bytes: 8 KB of
+// sign+mantissa bytes (granule after granule), 4 KB of 4-bit exponent distances, and a record of 32 bytes, so that one
+// bulk copy brings it.  Steps follow each other along K, tiles along N, experts last, so a tile is one stream of memory
+// whatever N is.
 //
 // Within a granule, rows are (half, g) = (row / 8, row % 8) and the 64 weights of a row four chunks t of 16:
 //   sign+mantissa: 16 bytes of (half, t, g) at 512 half + 128 t + 16 g
@@ -24,8 +25,8 @@
 // as the lowest exponent is at most 240 and a distance at most 15.  No table is needed (a palette of 16 arbitrary
 // exponents takes a shared-memory lookup per pair, as the single-matrix kernels do).
 //
-// Verbatim runs: per step a record {mask[4] (bit r: row r's run is verbatim), index of its first run, count}; the
-// runs' exponent bytes follow in (expert, tile, step, row) order, 64 each, in the order of K.
+// Verbatim runs: a step's record is {mask[4] (bit r: row r's run is verbatim), index of its first run, count}; the
+// runs' exponent bytes are kept in (expert, tile, step, row) order, 64 each, in the order of K.
 #pragma once
 
 #include <cstdint>
@@ -37,20 +38,20 @@ namespace uw {
 constexpr int kGran = 16;                 // rows of a granule
 constexpr int kTileRows = 128;            // virtual rows of a tile
 constexpr int kStepW = 64;                // weights of K per step
-constexpr uint32_t kStepBytes = 12288;    // a step: 8 KB sign+mantissa, 4 KB distances
-constexpr uint32_t kStepSm = 8192;
+constexpr uint32_t kStepSm = 8192;        // a step: sign+mantissa bytes, distances, record
+constexpr uint32_t kStepRec = 12288;
+constexpr uint32_t kStepBytes = kStepRec + 32;
 constexpr int kMaxExperts = 1024;
 
 struct StepRec {
     uint32_t mask[4];
     uint32_t first, count, pad[2];
 };
-static_assert(sizeof(StepRec) == 32, "step record");
+static_assert(sizeof(StepRec) == 32 && kStepBytes % 16 == 0, "step record");
 
 // device view of a group
 struct GroupView {
     const uint8_t *steps;     // [experts][tiles][ksteps][kStepBytes]
-    const StepRec *recs;      // [experts][tiles][ksteps]
     const uint8_t *verb;      // [n_verbatim][64]
     const uint32_t *base;     // [experts][1 or 2]: a matrix's lowest exponent, in both exponent fields of a pair
     int *status;
@@ -59,6 +60,11 @@ struct GroupView {
 };
 
 namespace dev {
+
+__device__ __forceinline__ const StepRec *step_rec(const uint8_t *steps, int64_t step)
+{
+    return (const StepRec *)(steps + step * kStepBytes + kStepRec);
+}
 
 // the eight pairs of a chunk: sign+mantissa words S, distance words C, lowest exponent B
 __device__ __forceinline__ void rebuild_chunk(const uint4 &S, const uint2 &C, uint32_t B, uint32_t (&p)[8])

@@ -18,8 +18,7 @@ using namespace uw;
 struct uw_group {
     GroupView v{};
     uint64_t n_verb = 0, bytes = 0;
-    void *dev = nullptr;   // steps, bases, status
-    void *recs = nullptr;  // records
+    void *dev = nullptr;   // steps with their records, bases, status
     void *verb = nullptr;  // verbatim runs
     int device = 0;
 };
@@ -34,7 +33,6 @@ struct MatPlace {
     int64_t N, K;
     int tiles, ksteps, stride, first;
     uint8_t *steps;     // the expert's steps
-    StepRec *recs;      // the expert's records
     uint8_t *verb;
     uint32_t *base;     // the matrix's entry
 };
@@ -103,20 +101,21 @@ __global__ void __launch_bounds__(256) mask_kernel(MatPlace m, int64_t warps)
     for (int r = 0; r < 16; r++) bits |= ((bal >> (2 * r)) & 1u) << r;
     if (lane == 0) {
         const int64_t vg = gr * m.stride + m.first;
-        ((uint16_t *)m.recs[(vg / 8) * m.ksteps + ks].mask)[vg % 8] = (uint16_t)bits;
+        ((uint16_t *)((StepRec *)step_rec(m.steps, (vg / 8) * m.ksteps + ks))->mask)[vg % 8] = (uint16_t)bits;
     }
 }
 
 // numbers the verbatim runs: one CTA, an exclusive scan over all records; total in *total
-__global__ void __launch_bounds__(1024) scan_kernel(StepRec *recs, int64_t n, unsigned long long *total)
+__global__ void __launch_bounds__(1024) scan_kernel(uint8_t *steps, int64_t n, unsigned long long *total)
 {
     __shared__ uint32_t wsum[32];
     unsigned long long carry = 0;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int64_t i0 = 0; i0 < n; i0 += 1024) {
         const int64_t i = i0 + threadIdx.x;
+        StepRec *rec = (StepRec *)step_rec(steps, i);
         uint32_t c = 0;
-        if (i < n) c = __popc(recs[i].mask[0]) + __popc(recs[i].mask[1]) + __popc(recs[i].mask[2]) + __popc(recs[i].mask[3]);
+        if (i < n) c = __popc(rec->mask[0]) + __popc(rec->mask[1]) + __popc(rec->mask[2]) + __popc(rec->mask[3]);
         uint32_t s = c;
         for (int d = 1; d < 32; d <<= 1) {
             const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, s, d);
@@ -130,8 +129,8 @@ __global__ void __launch_bounds__(1024) scan_kernel(StepRec *recs, int64_t n, un
             all += wsum[w];
         }
         if (i < n) {
-            recs[i].first = (uint32_t)(carry + before + s - c);
-            recs[i].count = c;
+            rec->first = (uint32_t)(carry + before + s - c);
+            rec->count = c;
         }
         carry += all;
         __syncthreads();
@@ -150,7 +149,7 @@ __global__ void __launch_bounds__(256) pack_kernel(MatPlace m, int64_t warps)
     const int64_t vg = gr * m.stride + m.first;
     const int64_t step = (vg / 8) * m.ksteps + ks;
     const int gi = (int)(vg % 8);
-    const StepRec &rec = m.recs[step];
+    const StepRec &rec = *step_rec(m.steps, step);
     const uint32_t b0 = (*m.base >> 7) & 255u;
     uint8_t *st = m.steps + step * kStepBytes;
     uint32_t codes[4];
@@ -200,7 +199,7 @@ __global__ void __launch_bounds__(256) unpack_kernel(MatPlace m, uint16_t *out, 
     const int64_t vg = gr * m.stride + m.first;
     const int64_t step = (vg / 8) * m.ksteps + ks;
     const int gi = (int)(vg % 8);
-    const StepRec &rec = m.recs[step];
+    const StepRec &rec = *step_rec(m.steps, step);
     const uint8_t *st = m.steps + step * kStepBytes;
     const uint4 codes = *(const uint4 *)(st + kStepSm + gi * 512 + t * 128 + g * 16);
 #pragma unroll
@@ -237,7 +236,6 @@ MatPlace place_of(const uw_group *g, int expert, int up)
     m.first = up;
     const int64_t s0 = (int64_t)expert * v.tiles * v.ksteps;
     m.steps = const_cast<uint8_t *>(v.steps) + s0 * kStepBytes;
-    m.recs = const_cast<StepRec *>(v.recs) + s0;
     m.verb = const_cast<uint8_t *>(v.verb);
     m.base = const_cast<uint32_t *>(v.base) + (int64_t)expert * m.stride + up;
     return m;
@@ -294,19 +292,14 @@ uw_status make_group(const Source &src, int experts, bool gated, int64_t N, int6
         }
         return code;
     };
-    if (!check(cudaMalloc(&g->dev, bytes), "memory of the steps") ||
-        !check(cudaMalloc(&g->recs, n_steps * sizeof(StepRec)), "memory of the records"))
-        return done(s);
+    if (!check(cudaMalloc(&g->dev, bytes), "memory of the steps")) return done(s);
     uint8_t *d = (uint8_t *)g->dev;
     unsigned long long *hist = (unsigned long long *)(d + o_hist), *total = (unsigned long long *)(d + o_total);
     v.steps = d;
-    v.recs = (const StepRec *)g->recs;
     v.base = (const uint32_t *)(d + o_base);
     v.status = (int *)(d + o_status);
     // padding granules keep zeros
-    if (!check(cudaMemsetAsync(d, 0, bytes, st), "memset") ||
-        !check(cudaMemsetAsync(g->recs, 0, n_steps * sizeof(StepRec), st), "memset"))
-        return done(s);
+    if (!check(cudaMemsetAsync(d, 0, bytes, st), "memset")) return done(s);
     for (int e = 0; e < experts; e++)
         for (int u = 0; u < mats; u++) {
             MatPlace m = place_of(g, e, u);
@@ -318,7 +311,7 @@ uw_status make_group(const Source &src, int experts, bool gated, int64_t N, int6
             mask_kernel<<<place_blocks(m), 256, 0, st>>>(m, place_warps(m));
             if (!check(cudaGetLastError(), "uw_group_create: launch")) return done(s);
         }
-    scan_kernel<<<1, 1024, 0, st>>>((StepRec *)g->recs, (int64_t)n_steps, total);
+    scan_kernel<<<1, 1024, 0, st>>>(d, (int64_t)n_steps, total);
     unsigned long long n_verb = 0;
     if (!check(cudaGetLastError(), "uw_group_create: launch") ||
         !check(cudaMemcpyAsync(&n_verb, total, 8, cudaMemcpyDeviceToHost, st), "uw_group_create: count") ||
@@ -328,7 +321,7 @@ uw_status make_group(const Source &src, int experts, bool gated, int64_t N, int6
     g->n_verb = n_verb;
     if (!check(cudaMalloc(&g->verb, n_verb * 64 + 256), "memory of the verbatim runs")) return done(s);
     v.verb = (const uint8_t *)g->verb;
-    g->bytes = bytes + n_steps * sizeof(StepRec) + n_verb * 64 + 256;
+    g->bytes = bytes + n_verb * 64 + 256;
     for (int e = 0; e < experts; e++)
         for (int u = 0; u < mats; u++) {
             MatPlace m = place_of(g, e, u);
@@ -410,7 +403,6 @@ extern "C" void uw_group_free(uw_group *g)
 {
     if (!g) return;
     cudaFree(g->verb);
-    cudaFree(g->recs);
     cudaFree(g->dev);
     delete g;
 }

@@ -54,7 +54,7 @@ __device__ __forceinline__ Part load_part(const GroupView &v, int64_t step, int 
     p.s0 = ld_stream(st + gi * 1024 + at);
     p.s1 = ld_stream(st + gi * 1024 + 512 + at);
     p.c = ld_stream(st + kStepSm + gi * 512 + at);
-    p.mask = __ldg((const uint16_t *)v.recs[step].mask + gi);
+    p.mask = __ldg((const uint16_t *)(st + kStepRec) + gi);
     return p;
 }
 
@@ -65,7 +65,7 @@ __device__ __forceinline__ void rebuild_part(const GroupView &v, const Part &p, 
     rebuild_chunk(p.s0, make_uint2(p.c.x, p.c.y), B, a);
     rebuild_chunk(p.s1, make_uint2(p.c.z, p.c.w), B, b);
     if (p.mask) {
-        const StepRec &r = v.recs[step];
+        const StepRec &r = *step_rec(v.steps, step);
         uint32_t m[4];
 #pragma unroll
         for (int i = 0; i < 4; i++) m[i] = __ldg(&r.mask[i]);

@@ -7,10 +7,11 @@
 //   - 0-11, three groups of four: group i % 3 rebuilds step i (128 rows x 64 weights).  Thread = row: four 16-byte and
 //     four 8-byte reads of shared memory without bank conflicts, 32 bf16 pairs, four tcgen05.st of eight columns.  The
 //     A operand never passes through shared memory, which the X tiles need.
-//   - 12: bulk copies of the steps (12 KB, one run of memory each), their records and verbatim runs;
+//   - 12, 19: bulk copies of the steps (12 KB and the record, one run of memory) and their verbatim runs, alternate
+//     steps each;
 //   - 13: one thread issues four tcgen05.mma (M = 128, N = rows of X up to a multiple of 16, K = 16) a step, A from
 //     tensor memory;
-//   - 14-19: X tiles [<= 192 rows x 64] bf16 in the 128-byte swizzle.  Rows in order come in tensor copies of 32 rows
+//   - 14-18: X tiles [<= 192 rows x 64] bf16 in the 128-byte swizzle.  Rows in order come in tensor copies of 32 rows
 //     (warp 14); rows with sources in 16-byte cp.async, a warp for each
 //     stage of the ring.
 //   - 20-27: the epilogue of a finished unit, two warps per lane quarter of tensor memory.  In a gated tile lanes 0-15
@@ -39,13 +40,14 @@ using namespace dev;
 
 constexpr int kGroups = 3;                    // rebuild groups of four warps
 constexpr int kRebuildWarps = 4 * kGroups;
-constexpr int kProdWarp = kRebuildWarps, kMmaWarp = kProdWarp + 1, kXWarp0 = kProdWarp + 2;
-constexpr int kEpiWarp0 = kXWarp0 + 6;  // a multiple of four: warp % 4 is the lane quarter of tensor memory
+constexpr int kProdWarp = kRebuildWarps, kMmaWarp = kProdWarp + 1, kXWarp0 = kProdWarp + 2, kXWarps = 5;
+constexpr int kProdWarp2 = kXWarp0 + kXWarps;
+constexpr int kEpiWarp0 = kProdWarp2 + 1;  // a multiple of four: warp % 4 is the lane quarter of tensor memory
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 constexpr int kBN = 192;                      // rows of X per unit at most
 constexpr int kVCs = 8;                       // verbatim runs of a step staged with it (beyond: global loads)
-constexpr uint32_t kRecOff = kStepBytes, kVOff = kRecOff + 128;
+constexpr uint32_t kVOff = kStepRec + 128;    // a stage: the step with its record, then its verbatim runs
 constexpr uint32_t kWStage = kVOff + kVCs * 64;
 constexpr uint32_t kXStage = kBN * 128;
 constexpr int kSW = 6, kSX = 5, kSA = 4;
@@ -55,8 +57,8 @@ static_assert(kSmem <= 227 * 1024, "shared memory");
 // A stage of the weight ring belongs to one rebuild group for good.  Copies land out of order, so a group that waited for
 // a stage last read by another group could be a whole turn ahead of a copy that has not landed, where the barrier's
 // parity is the same as of the turn it waits for.
-static_assert(kSW % kGroups == 0, "weight ring");
-static_assert(kEpiWarp0 % 4 == 0 && kWStage % 128 == 0 && kACol + 32 * kSA <= 512 && kXWarp0 + kSX <= kEpiWarp0, "layout");
+static_assert(kSW % kGroups == 0 && kSW % 2 == 0, "weight ring");
+static_assert(kEpiWarp0 % 4 == 0 && kWStage % 128 == 0 && kACol + 32 * kSA <= 512 && kSX == kXWarps, "layout");
 static_assert((2 * (kSW + kSX + kSA) + 5) * 8 + 8 <= 512, "barriers");
 
 struct TcArgs {
@@ -205,15 +207,18 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
     Units units(off, tcum, v);
     Unit w;
 
-    if (warp == kProdWarp) {
+    if (warp == kProdWarp || warp == kProdWarp2) {
         // ---------------------------------------------------------------------------------------- weight copies
+        // Two warps take alternate steps: one alone, with a wait, a copy or two and their addresses, took 820 cycles a
+        // step, twice what the products of a step take.
+        const int p = warp == kProdWarp ? 0 : 1;
         bool ok = true;
-        int i = 0, s = 0;
-        uint32_t ph = 0;
+        const bool leader = elect_one();
+        int i = 0, last = -1;  // steps before this unit; the last step asked for
         // lane l: {first, count} of the verbatim runs of step l of the 32 at hand; the next 32 in flight
         auto recs_at = [&](const Unit &q, int ks) {
             const int64_t st = ((int64_t)q.e * v.tiles + q.tile) * ksteps + ks + lane;
-            return ks + lane < ksteps ? __ldg((const uint2 *)&v.recs[st].first) : make_uint2(0, 0);
+            return ks + lane < ksteps ? __ldg((const uint2 *)&step_rec(v.steps, st)->first) : make_uint2(0, 0);
         };
         Unit nx;
         bool have = units.next(w), have_nx = false;
@@ -221,41 +226,38 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
         if (have) nxt = recs_at(w, 0);
         while (have && ok) {
             have_nx = units.next(nx);
-            const int64_t st0 = ((int64_t)w.e * v.tiles + w.tile) * ksteps;
-            for (int ks = 0; ks < ksteps; ks++, i++) {
-                if ((ks & 31) == 0) {
-                    cur = nxt;
-                    if (ks + 32 < ksteps) nxt = recs_at(w, ks + 32);
-                    else if (have_nx) nxt = recs_at(nx, 0);
-                }
-                const uint32_t first = __shfl_sync(0xFFFFFFFFu, cur.x, ks & 31);
-                const uint32_t nv = min(__shfl_sync(0xFFFFFFFFu, cur.y, ks & 31), (uint32_t)kVCs);
-                int go = 1;
-                if (lane == 0) {
-                    if (i >= kSW && !mbar_wait(&wempty[s], ph ^ 1u)) go = 0;
-                    else {
-                        uint8_t *d = wring + s * kWStage;
-                        const uint32_t fb = saddr(&wfull[s]);
-                        mbar_expect_tx(&wfull[s], kStepBytes + 32u + 64u * nv);
-                        bulk_copy(saddr(d), v.steps + (st0 + ks) * kStepBytes, kStepBytes, fb);
-                        bulk_copy(saddr(d + kRecOff), v.recs + st0 + ks, 32u, fb);
-                        if (nv) bulk_copy(saddr(d + kVOff), v.verb + (uint64_t)first * 64, nv * 64u, fb);
+            const uint8_t *src = v.steps + ((int64_t)w.e * v.tiles + w.tile) * ksteps * kStepBytes;
+            for (int k0 = 0; k0 < ksteps && ok; k0 += 32) {
+                cur = nxt;
+                if (k0 + 32 < ksteps) nxt = recs_at(w, k0 + 32);
+                else if (have_nx) nxt = recs_at(nx, 0);
+                const int ke = min(ksteps, k0 + 32);
+                for (int ks = k0 + ((i + k0 + p) & 1); ks < ke; ks += 2) {
+                    const int q = i + ks, s = q % kSW;
+                    const uint32_t first = __shfl_sync(0xFFFFFFFFu, cur.x, ks - k0);
+                    const uint32_t nv = min(__shfl_sync(0xFFFFFFFFu, cur.y, ks - k0), (uint32_t)kVCs);
+                    if (q >= kSW && !__all_sync(0xFFFFFFFFu, mbar_wait(&wempty[s], ((q / kSW) & 1) ^ 1))) { ok = false; break; }
+                    if (leader) {
+                        const uint32_t d = saddr(wring) + s * kWStage, fb = saddr(&wfull[s]);
+                        mbar_expect_tx(&wfull[s], kStepBytes + 64u * nv);
+                        bulk_copy(d, src + (int64_t)ks * kStepBytes, kStepBytes, fb);
+                        if (nv) bulk_copy(d + kVOff, v.verb + (uint64_t)first * 64, nv * 64u, fb);
                     }
+                    __syncwarp();
+                    last = q;
                 }
-                if (!__shfl_sync(0xFFFFFFFFu, go, 0)) {
-                    ok = false;
-                    break;
-                }
-                if (++s == kSW) { s = 0; ph ^= 1u; }
             }
+            if (!ok) break;
+            i += ksteps;
             w = nx;
             have = have_nx;
         }
-        if (!ok && lane == 0) {
+        if (!ok && leader) {
+            // the copies in flight land before the block ends
             atomicExch(v.status, (int)DEV_TIMEOUT);
-            for (int q = max(0, i - kSW); q < i; q++) mbar_wait(&wfull[q % kSW], (q / kSW) & 1);
+            for (int n = 0; n < kSW / 2 && last >= 0; n++, last -= 2) mbar_wait(&wfull[last % kSW], (last / kSW) & 1);
         }
-    } else if (warp >= kXWarp0 && warp < kEpiWarp0) {
+    } else if (warp >= kXWarp0 && warp < kXWarp0 + kXWarps) {
         // ---------------------------------------------------------------------------------------- X copies
         bool ok = true;
         int i = 0, s = 0;
@@ -264,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
             // Warp x copies steps x, x + kSX, ... into stage x: it asks for a step's 16-byte pieces (eight lanes a row),
             // waits for them and hands the stage over, while the other warps' steps are on their way.
             const int x = warp - kXWarp0;
-            if (x < kSX) {
+            {
                 int *rows = xrows + x * kBN;
                 const uint32_t xs = saddr(xring + x * kXStage);
                 constexpr int kL = kBN / 32;
@@ -382,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
                 const int q = i + ks, s = q % kSW, sa = q % kSA;
                 if (!mbar_wait(&wfull[s], (q / kSW) & 1)) { ok = false; break; }
                 const uint8_t *st = wring + s * kWStage;
-                const uint32_t *mask = (const uint32_t *)(st + kRecOff);
+                const uint32_t *mask = (const uint32_t *)(st + kStepRec);
                 const uint32_t mw = mask[r >> 5];
                 uint4 S[4];
                 uint2 C[4];
