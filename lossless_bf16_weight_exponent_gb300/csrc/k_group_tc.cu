@@ -11,9 +11,8 @@
 //     steps each;
 //   - 13: one thread issues four tcgen05.mma (M = 128, N = rows of X up to a multiple of 16, K = 16) a step, A from
 //     tensor memory;
-//   - 14-18: X tiles [<= 192 rows x 64] bf16 in the 128-byte swizzle.  Rows in order come in tensor copies of 32 rows
-//     (warp 14); rows with sources in 16-byte cp.async, a warp for each
-//     stage of the ring.
+//   - 14-18: X tiles [<= 192 rows x 64] bf16 in the 128-byte swizzle, a warp for each stage of the ring.  Rows in order
+//     come in tensor copies of 32 rows, rows with sources in 16-byte cp.async.
 //   - 20-27: the epilogue of a finished unit, two warps per lane quarter of tensor memory.  In a gated tile lanes 0-15
 //     of a warp hold gate rows and lanes 16-31 the up rows that belong to them: eight exchanges between the halves per
 //     16 columns give each lane both factors of eight outputs.
@@ -259,74 +258,70 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
         }
     } else if (warp >= kXWarp0 && warp < kXWarp0 + kXWarps) {
         // ---------------------------------------------------------------------------------------- X copies
+        // Warp x brings steps x, x + kSX, ... into stage x: a step's copies take one warp longer than its products.
+        const int x = warp - kXWarp0;
+        const uint32_t xs = saddr(xring + x * kXStage);
         bool ok = true;
-        int i = 0, s = 0;
-        uint32_t ph = 0;
+        int i = 0, turn = 0;  // steps before this unit, this stage's turns
+        auto stage_free = [&] { return turn == 0 || __all_sync(0xFFFFFFFFu, mbar_wait(&xempty[x], (turn - 1) & 1)); };
         if constexpr (GATHER) {
-            // Warp x copies steps x, x + kSX, ... into stage x: it asks for a step's 16-byte pieces (eight lanes a row),
-            // waits for them and hands the stage over, while the other warps' steps are on their way.
-            const int x = warp - kXWarp0;
-            {
-                int *rows = xrows + x * kBN;
-                const uint32_t xs = saddr(xring + x * kXStage);
-                constexpr int kL = kBN / 32;
-                int r[kL];  // the next unit's rows, on their way before it begins
-                auto fetch = [&](const Unit &q) {
+            int *rows = xrows + x * kBN;
+            constexpr int kL = kBN / 32, kBatch = 8;
+            static_assert(kBN % (4 * kBatch) == 0, "rows past the last whole batch");
+            int r[kL];  // the next unit's rows, on their way before it begins
+            auto fetch = [&](const Unit &q) {
 #pragma unroll
-                    for (int j = 0; j < kL; j++) r[j] = 32 * j + lane < q.n ? __ldg(a.c.row_src + q.r0 + 32 * j + lane) : -1;
-                };
-                Unit nx;
-                bool have = units.next(w);
-                if (have) fetch(w);
-                int turn = 0;
-                while (ok && have) {
-                    __syncwarp();
+                for (int j = 0; j < kL; j++) r[j] = 32 * j + lane < q.n ? __ldg(a.c.row_src + q.r0 + 32 * j + lane) : -1;
+            };
+            Unit nx;
+            bool have = units.next(w);
+            if (have) fetch(w);
+            while (ok && have) {
+                __syncwarp();
 #pragma unroll
-                    for (int j = 0; j < kL; j++) rows[32 * j + lane] = r[j] >= 0 && r[j] < a.c.x_rows ? r[j] : -1;
-                    __syncwarp();
-                    const bool more = units.next(nx);
-                    if (more) fetch(nx);
-                    const int pieces = (((w.n + 15) & ~15) * 8) / 32;  // 32 lanes copy four rows
-                    for (int ks = (kSX - i % kSX + x) % kSX; ks < ksteps; ks += kSX, turn++) {
-                        if (turn > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(&xempty[x], (turn - 1) & 1))) { ok = false; break; }
-                        const uint8_t *xk = (const uint8_t *)a.c.x + ks * 128 + 16 * (lane & 7);
-#pragma unroll 8
-                        for (int j = 0; j < pieces; j++) {
-                            const int q = 4 * j + (lane >> 3), row = rows[q];
-                            copy16(xs + q * 128 + (((lane ^ q) & 7) << 4), xk + (row < 0 ? 0 : (int64_t)row * a.c.ldx * 2), row < 0);
+                for (int j = 0; j < kL; j++) rows[32 * j + lane] = r[j] >= 0 && r[j] < a.c.x_rows ? r[j] : -1;
+                __syncwarp();
+                const bool more = units.next(nx);
+                if (more) fetch(nx);
+                const int pieces = ((w.n + 15) & ~15) / 4;  // 32 lanes copy four rows
+                for (int ks = (kSX - i % kSX + x) % kSX; ks < ksteps; ks += kSX, turn++) {
+                    if (!stage_free()) { ok = false; break; }
+                    const uint8_t *xk = (const uint8_t *)a.c.x + ks * 128 + 16 * (lane & 7);
+                    for (int j0 = 0; j0 < pieces; j0 += kBatch) {
+                        int row[kBatch];
+#pragma unroll
+                        for (int j = 0; j < kBatch; j++) row[j] = rows[4 * (j0 + j) + (lane >> 3)];
+#pragma unroll
+                        for (int j = 0; j < kBatch; j++) {
+                            const int q = 4 * (j0 + j) + (lane >> 3);
+                            if (j0 + j < pieces)
+                                copy16(xs + q * 128 + (((lane ^ q) & 7) << 4), xk + (row[j] < 0 ? 0 : (int64_t)row[j] * a.c.ldx * 2), row[j] < 0);
                         }
-                        asm volatile("cp.async.wait_all;" ::: "memory");
-                        // every lane's pieces are visible to the tensor core before the arrival
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&xfull[x]);
                     }
-                    i += ksteps;
-                    w = nx;
-                    have = more;
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    // every lane's pieces are visible to the tensor core before the arrival
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&xfull[x]);
                 }
+                i += ksteps;
+                w = nx;
+                have = more;
             }
-        } else if (warp == kXWarp0) {
+        } else {
             while (ok && units.next(w)) {
                 const int boxes = (w.n + 31) / 32;
-                for (int ks = 0; ks < ksteps; ks++) {
-                    int go = 1;
-                    if (lane == 0) {
-                        if (i >= kSX && !mbar_wait(&xempty[s], ph ^ 1u)) go = 0;
-                        else mbar_expect_tx(&xfull[s], (uint32_t)boxes * 4096u);
-                    }
-                    if (!__shfl_sync(0xFFFFFFFFu, go, 0)) {
-                        ok = false;
-                        break;
-                    }
-                    if (lane < boxes) tma2d(xring + s * kXStage + 4096 * lane, &a.tm_x, ks * kStepW, w.r0 + 32 * lane, &xfull[s]);
+                for (int ks = (kSX - i % kSX + x) % kSX; ks < ksteps; ks += kSX, turn++) {
+                    if (!stage_free()) { ok = false; break; }
+                    if (lane == 0) mbar_expect_tx(&xfull[x], (uint32_t)boxes * 4096u);
                     __syncwarp();
-                    i++;
-                    if (++s == kSX) { s = 0; ph ^= 1u; }
+                    if (lane < boxes) tma2d(xring + x * kXStage + 4096 * lane, &a.tm_x, ks * kStepW, w.r0 + 32 * lane, &xfull[x]);
+                    __syncwarp();
                 }
+                i += ksteps;
             }
-            if (!ok && lane == 0)
-                for (int q = max(0, i - kSX); q < i; q++) mbar_wait(&xfull[q % kSX], (q / kSX) & 1);
+            // the copy in flight lands before the block ends
+            if (!ok && lane == 0 && turn > 0) mbar_wait(&xfull[x], (turn - 1) & 1);
         }
         if (!ok && lane == 0) atomicExch(v.status, (int)DEV_TIMEOUT);
     } else if (warp == kMmaWarp) {
