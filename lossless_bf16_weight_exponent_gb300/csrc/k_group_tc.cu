@@ -12,7 +12,8 @@
 //   - 13: one thread issues four tcgen05.mma (M = 128, N = rows of X up to a multiple of 16, K = 16) a step, A from
 //     tensor memory;
 //   - 14-18: X tiles [<= 192 rows x 64] bf16 in the 128-byte swizzle, a warp for each stage of the ring.  Rows in order
-//     come in tensor copies of 32 rows, rows with sources in 16-byte cp.async.
+//     come in tensor copies of 32 rows, rows with sources in tensor copies that gather four (a source outside X
+//     reads zeros).
 //   - 20-27: the epilogue of a finished unit, two warps per lane quarter of tensor memory.  In a gated tile lanes 0-15
 //     of a warp hold gate rows and lanes 16-31 the up rows that belong to them: eight exchanges between the halves per
 //     16 columns give each lane both factors of eight outputs.
@@ -61,7 +62,7 @@ static_assert(kEpiWarp0 % 4 == 0 && kWStage % 128 == 0 && kACol + 32 * kSA <= 51
 static_assert((2 * (kSW + kSX + kSA) + 5) * 8 + 8 <= 512, "barriers");
 
 struct TcArgs {
-    CUtensorMap tm_x;  // X [x_rows, K] bf16, box {64, 32}, 128-byte swizzle (rows in order only)
+    CUtensorMap tm_x;  // X [x_rows, K] bf16, box {64, 32} or (sources) {64, 1}, 128-byte swizzle
     GroupCall c;
 };
 
@@ -80,10 +81,14 @@ __device__ __forceinline__ bool elect_one()
     return p != 0;
 }
 
-// 16 bytes to shared memory, or zeros
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool zero)
+// four rows of a map whose box is one row high (a row past the end reads zeros)
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map, int x, const int4 &y, uint32_t bar)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(zero ? 0u : 16u) : "memory");
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+        "%5, %6}], [%7];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w), "r"(bar)
+        : "memory");
 }
 
 // eight consecutive 32-bit columns of this warp's 32 lanes of tensor memory
@@ -139,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
     uint32_t *tmem_slot = (uint32_t *)(done + 1);
     int *off = (int *)((uint8_t *)wfull + 512);       // [experts + 1]
     int *tcum = off + kMaxExperts + 4;                // [experts + 1]
-    int *xrows = tcum + kMaxExperts + 4;              // [kSX][kBN] (sources) a warp's unit's rows of X, -1: zeros
+    int *xrows = tcum + kMaxExperts + 4;              // [kSX][kBN] (sources) a warp's unit's rows of X (past the end: zeros)
 
     const GroupView &v = a.c.v;
     const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: a uniform value
@@ -266,8 +271,9 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
         auto stage_free = [&] { return turn == 0 || __all_sync(0xFFFFFFFFu, mbar_wait(&xempty[x], (turn - 1) & 1)); };
         if constexpr (GATHER) {
             int *rows = xrows + x * kBN;
-            constexpr int kL = kBN / 32, kBatch = 8;
-            static_assert(kBN % (4 * kBatch) == 0, "rows past the last whole batch");
+            constexpr int kL = kBN / 32;
+            const bool leader = elect_one();
+            const int none = (int)a.c.x_rows;  // past the end
             int r[kL];  // the next unit's rows, on their way before it begins
             auto fetch = [&](const Unit &q) {
 #pragma unroll
@@ -279,30 +285,25 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
             while (ok && have) {
                 __syncwarp();
 #pragma unroll
-                for (int j = 0; j < kL; j++) rows[32 * j + lane] = r[j] >= 0 && r[j] < a.c.x_rows ? r[j] : -1;
+                for (int j = 0; j < kL; j++) rows[32 * j + lane] = r[j] >= 0 && r[j] < none ? r[j] : none;
                 __syncwarp();
                 const bool more = units.next(nx);
                 if (more) fetch(nx);
-                const int pieces = ((w.n + 15) & ~15) / 4;  // 32 lanes copy four rows
+                const int bn = (w.n + 15) & ~15;
                 for (int ks = (kSX - i % kSX + x) % kSX; ks < ksteps; ks += kSX, turn++) {
                     if (!stage_free()) { ok = false; break; }
-                    const uint8_t *xk = (const uint8_t *)a.c.x + ks * 128 + 16 * (lane & 7);
-                    for (int j0 = 0; j0 < pieces; j0 += kBatch) {
-                        int row[kBatch];
+                    if (leader) {
+                        const uint32_t fb = saddr(&xfull[x]);
+                        mbar_expect_tx(&xfull[x], (uint32_t)bn * 128u);
+                        for (int q = 0; q < bn; q += 16) {
+                            int4 y[4];
 #pragma unroll
-                        for (int j = 0; j < kBatch; j++) row[j] = rows[4 * (j0 + j) + (lane >> 3)];
+                            for (int j = 0; j < 4; j++) y[j] = *(const int4 *)(rows + q + 4 * j);
 #pragma unroll
-                        for (int j = 0; j < kBatch; j++) {
-                            const int q = 4 * (j0 + j) + (lane >> 3);
-                            if (j0 + j < pieces)
-                                copy16(xs + q * 128 + (((lane ^ q) & 7) << 4), xk + (row[j] < 0 ? 0 : (int64_t)row[j] * a.c.ldx * 2), row[j] < 0);
+                            for (int j = 0; j < 4; j++) tma_gather4(xs + 128 * q + 512 * j, &a.tm_x, ks * kStepW, y[j], fb);
                         }
                     }
-                    asm volatile("cp.async.wait_all;" ::: "memory");
-                    // every lane's pieces are visible to the tensor core before the arrival
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&xfull[x]);
                 }
                 i += ksteps;
                 w = nx;
@@ -320,9 +321,9 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
                 }
                 i += ksteps;
             }
-            // the copy in flight lands before the block ends
-            if (!ok && lane == 0 && turn > 0) mbar_wait(&xfull[x], (turn - 1) & 1);
         }
+        // the copies in flight land before the block ends
+        if (!ok && lane == 0 && turn > 0) mbar_wait(&xfull[x], (turn - 1) & 1);
         if (!ok && lane == 0) atomicExch(v.status, (int)DEV_TIMEOUT);
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------------------------------------- MMA issue
@@ -503,7 +504,7 @@ bool map_x(CUtensorMap *m, const GroupCall &c)
     if (!fn) return false;
     cuuint64_t dims[2] = {(cuuint64_t)c.v.K, (cuuint64_t)c.x_rows};
     cuuint64_t strides[1] = {(cuuint64_t)c.ldx * 2};
-    cuuint32_t box[2] = {64, 32};
+    cuuint32_t box[2] = {64, c.row_src ? 1u : 32u};
     cuuint32_t estr[2] = {1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t *>(c.x), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -521,7 +522,7 @@ int launch_group_tc(const GroupCall &c, void *stream)
 {
     TcArgs a;
     memset(&a, 0, sizeof a);
-    if (!c.row_src && !map_x(&a.tm_x, c)) return cudaErrorInvalidValue;
+    if (!map_x(&a.tm_x, c)) return cudaErrorInvalidValue;
     a.c = c;
     // at least one expert's row tile for each kBN rows, at most one more for each expert
     const int64_t most = ((c.rows + kBN - 1) / kBN + std::min<int64_t>(c.v.experts, c.rows)) * c.v.tiles;
