@@ -8,13 +8,13 @@
 // bulk copy brings it.  Steps follow each other along K, tiles along N, experts last, so a tile is one stream of memory
 // whatever N is.
 //
-// Within a granule, rows are (half, g) = (row / 8, row % 8) and the 64 weights of a row four chunks t of 16:
-//   sign+mantissa: 16 bytes of (half, t, g) at 512 half + 128 t + 16 g
-//   distances:      8 bytes of (half, t, g) at 128 t + 16 g + 8 half
-// Lane 8 t + g of a warp therefore loads its part of a granule with one 16-byte load per half and one for both
-// halves' distances, each load of the warp one run of 512 bytes; and 32 threads that own a row each read shared
-// memory without bank conflicts.  With lane 8 t + g in the place of the tensor instruction's lane 4 g + t the two
-// owners differ, so the matrix-vector kernel's lane l loads what position 8 (l % 4) + l / 4 holds.
+// Within a granule, rows are (half, g) = (row / 8, row % 8) and the 64 weights of a row four chunks t of 16.  With place
+// p = 4 g + (t ^ (g / 2)):
+//   sign+mantissa: 16 bytes of (half, t, g) at 512 half + 16 p
+//   distances:      8 bytes of (half, t, g) at 16 p + 8 half
+// The matrix-vector kernel's lane 4 g + t loads its part of a granule (the tensor instruction's rows g and g + 8) with
+// three 16-byte loads, eight neighbouring lanes one line of 128 bytes; and where 32 threads own a row each and read
+// chunk t of it from shared memory, the exchange of chunks by g / 2 keeps them off each other's banks.
 //
 // A chunk's words are packed so that a pair of bf16 weights (2q, 2q + 1) takes about four instructions to rebuild.
 // With P the pair's sign and mantissa bits in place (mask 807F807F) and D its two distances in place of the
@@ -60,6 +60,9 @@ struct GroupView {
 };
 
 namespace dev {
+
+// byte of a granule's sign+mantissa half, and of its distances, where chunk t of row g (or g + 8) begins
+__host__ __device__ __forceinline__ constexpr uint32_t chunk_at(int g, int t) { return 64u * g + 16u * (t ^ (g >> 1)); }
 
 __device__ __forceinline__ const StepRec *step_rec(const uint8_t *steps, int64_t step)
 {

@@ -138,11 +138,11 @@ __global__ void __launch_bounds__(1024) scan_kernel(uint8_t *steps, int64_t n, u
     if (threadIdx.x == 0) *total = carry;
 }
 
-// one warp per (granule, step), lane 8 t + g its chunks of rows g and g + 8
+// one warp per (granule, step), lane 4 g + t chunk t of rows g and g + 8
 __global__ void __launch_bounds__(256) pack_kernel(MatPlace m, int64_t warps)
 {
     const int64_t wi = (blockIdx.x * 256ll + threadIdx.x) >> 5;
-    const int lane = threadIdx.x & 31, t = lane >> 3, g = lane & 7;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     if (wi >= warps) return;
     const int64_t gr = wi / m.ksteps;
     const int ks = (int)(wi % m.ksteps);
@@ -178,21 +178,21 @@ __global__ void __launch_bounds__(256) pack_kernel(MatPlace m, int64_t warps)
         uint32_t s[4];
 #pragma unroll
         for (int j = 0; j < 4; j++) s[j] = P[2 * j] | prmt(P[2 * j + 1], 0u, 0x2301u);
-        *(uint4 *)(st + gi * 1024 + half * 512 + t * 128 + g * 16) = make_uint4(s[0], s[1], s[2], s[3]);
+        *(uint4 *)(st + gi * 1024 + half * 512 + chunk_at(g, t)) = make_uint4(s[0], s[1], s[2], s[3]);
 #pragma unroll
         for (int i = 0; i < 2; i++)
             codes[2 * half + i] = D[4 * i] | (D[4 * i + 1] << 4) | (D[4 * i + 2] >> 4) | __funnelshift_r(D[4 * i + 3], D[4 * i + 3], 8);
         if (verb)
             *(uint4 *)(m.verb + ((uint64_t)rec.first + verbatim_rank(rec.mask, rt)) * 64 + 16 * t) = make_uint4(E[0], E[1], E[2], E[3]);
     }
-    *(uint4 *)(st + kStepSm + gi * 512 + t * 128 + g * 16) = make_uint4(codes[0], codes[1], codes[2], codes[3]);
+    *(uint4 *)(st + kStepSm + gi * 512 + chunk_at(g, t)) = make_uint4(codes[0], codes[1], codes[2], codes[3]);
 }
 
 // the inverse of pack_kernel
 __global__ void __launch_bounds__(256) unpack_kernel(MatPlace m, uint16_t *out, int64_t warps)
 {
     const int64_t wi = (blockIdx.x * 256ll + threadIdx.x) >> 5;
-    const int lane = threadIdx.x & 31, t = lane >> 3, g = lane & 7;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     if (wi >= warps) return;
     const int64_t gr = wi / m.ksteps;
     const int ks = (int)(wi % m.ksteps);
@@ -201,14 +201,14 @@ __global__ void __launch_bounds__(256) unpack_kernel(MatPlace m, uint16_t *out, 
     const int gi = (int)(vg % 8);
     const StepRec &rec = *step_rec(m.steps, step);
     const uint8_t *st = m.steps + step * kStepBytes;
-    const uint4 codes = *(const uint4 *)(st + kStepSm + gi * 512 + t * 128 + g * 16);
+    const uint4 codes = *(const uint4 *)(st + kStepSm + gi * 512 + chunk_at(g, t));
 #pragma unroll
     for (int half = 0; half < 2; half++) {
         const int rg = 8 * half + g;
         const int64_t row = gr * kGran + rg;
         if (row >= m.N) continue;
         const int rt = 16 * gi + rg;
-        const uint4 S = *(const uint4 *)(st + gi * 1024 + half * 512 + t * 128 + g * 16);
+        const uint4 S = *(const uint4 *)(st + gi * 1024 + half * 512 + chunk_at(g, t));
         uint32_t p[8];
         if ((rec.mask[rt >> 5] >> (rt & 31)) & 1u)
             rebuild_chunk_verbatim(S, *(const uint4 *)(m.verb + ((uint64_t)rec.first + verbatim_rank(rec.mask, rt)) * 64 + 16 * t), p);
@@ -477,7 +477,8 @@ extern "C" uw_status uw_group_matmul(const uw_group *g, const uint16_t *x, int64
     c.y = y;
     c.ldy = ldy;
     c.out_bf16 = od == UW_OUT_BF16;
-    const bool tc = rows > 8 * (int64_t)g->v.experts && group_tc_supported(c);
+    const char *gt = getenv("GT");
+    const bool tc = gt ? gt[0] == '1' : rows > 8 * (int64_t)g->v.experts && group_tc_supported(c);
     const cudaError_t e = (cudaError_t)(tc ? launch_group_tc(c, stream) : launch_group_gemv(c, stream));
     return e == cudaSuccess ? UW_OK : cuda_fail(e, "uw_group_matmul: launch");
 }

@@ -1,7 +1,7 @@
 // k_group_gemv.cu - the grouped product for experts with a few rows each (sm_103a): every expert that has rows
 // streams its compressed weights once and multiplies them on the tensor pipe (mma.sync m16n8k16, fp32 accumulate).
 //
-// A CTA owns one granule of 16 outputs (gated: of both matrices) of one expert over all of K; its warps take the
+// A CTA owns two granules, 32 outputs (gated: 16 of both matrices), of one expert over all of K; its warps take the
 // 64-weight steps in turn.  A lane loads its part of a granule with three 16-byte loads straight into the registers
 // of the A operand (the group's form is laid out for that), so the weights pass through no shared memory; one
 // shared-memory sum joins the warps, in a fixed order.  The logical k of the instruction is permuted so that a lane's
@@ -12,6 +12,7 @@
 #include <algorithm>
 
 #include "group.cuh"
+#include "launch.cuh"
 #include "uw_internal.h"
 
 namespace uw {
@@ -19,8 +20,6 @@ namespace uw {
 namespace {
 
 using namespace dev;
-
-constexpr int kWarps = 8;
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1)
@@ -47,29 +46,29 @@ struct Part {
     uint32_t mask;    // verbatim bits of the granule's 16 rows
 };
 
-__device__ __forceinline__ Part load_part(const GroupView &v, int64_t step, int gi, int at)
+// step: the step's bytes; at: this lane's place in a granule
+__device__ __forceinline__ Part load_part(const uint8_t *step, int gi, int at)
 {
-    const uint8_t *st = v.steps + step * kStepBytes;
     Part p;
-    p.s0 = ld_stream(st + gi * 1024 + at);
-    p.s1 = ld_stream(st + gi * 1024 + 512 + at);
-    p.c = ld_stream(st + kStepSm + gi * 512 + at);
-    p.mask = __ldg((const uint16_t *)(st + kStepRec) + gi);
+    p.s0 = ld_stream(step + gi * 1024 + at);
+    p.s1 = ld_stream(step + gi * 1024 + 512 + at);
+    p.c = ld_stream(step + kStepSm + gi * 512 + at);
+    p.mask = __ldg((const uint16_t *)(step + kStepRec) + gi);
     return p;
 }
 
 // rows g and g + 8 of a granule's step as bf16 pairs
-__device__ __forceinline__ void rebuild_part(const GroupView &v, const Part &p, int64_t step, int gi, int g, int t, uint32_t B,
+__device__ __forceinline__ void rebuild_part(const uint8_t *verb, const Part &p, const uint8_t *step, int gi, int g, int t, uint32_t B,
                                              uint32_t (&a)[8], uint32_t (&b)[8])
 {
     rebuild_chunk(p.s0, make_uint2(p.c.x, p.c.y), B, a);
     rebuild_chunk(p.s1, make_uint2(p.c.z, p.c.w), B, b);
     if (p.mask) {
-        const StepRec &r = *step_rec(v.steps, step);
+        const StepRec &r = *(const StepRec *)(step + kStepRec);
         uint32_t m[4];
 #pragma unroll
         for (int i = 0; i < 4; i++) m[i] = __ldg(&r.mask[i]);
-        const uint8_t *vb = v.verb + (uint64_t)__ldg(&r.first) * 64 + 16 * t;
+        const uint8_t *vb = verb + (uint64_t)__ldg(&r.first) * 64 + 16 * t;
         const int row = 16 * gi + g;
         if ((p.mask >> g) & 1u) rebuild_chunk_verbatim(p.s0, __ldg((const uint4 *)(vb + (uint64_t)verbatim_rank(m, row) * 64)), a);
         if ((p.mask >> (g + 8)) & 1u)
@@ -78,13 +77,15 @@ __device__ __forceinline__ void rebuild_part(const GroupView &v, const Part &p, 
     }
 }
 
-template <bool GATED>
-__global__ void __launch_bounds__(32 * kWarps) group_gemv_kernel(const GroupCall c, int all_experts)
+template <bool GATED, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) group_gemv_kernel(const GroupCall c, int all_experts)
 {
-    constexpr int NG = GATED ? 2 : 1;
-    __shared__ float part[kWarps][NG][16][8];
+    constexpr int NG = 2;  // granules of a CTA: gate and up, or 32 outputs
+    __shared__ float part[WARPS][NG][16][8];
     const GroupView &v = c.v;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    pdl_trigger();
+    pdl_wait();
 
     // the expert: blockIdx.y itself, or (fewer rows than experts) the blockIdx.y-th that has rows
     int e = blockIdx.y, lo = 0, hi = 0;
@@ -118,38 +119,57 @@ __global__ void __launch_bounds__(32 * kWarps) group_gemv_kernel(const GroupCall
 
     const int64_t vg = (int64_t)blockIdx.x * NG;
     const int gi = (int)(vg & 7);
-    const int64_t s0 = ((int64_t)e * v.tiles + (vg >> 3)) * v.ksteps;
-    const int at = 128 * t + 16 * g;
+    const uint8_t *steps = v.steps + (((int64_t)e * v.tiles + (vg >> 3)) * v.ksteps + warp) * kStepBytes;
+    const int at = chunk_at(g, t);
+    const int mine = (v.ksteps - warp + WARPS - 1) / WARPS;  // this warp's steps: warp, warp + WARPS, ...
     uint32_t B[NG];
 #pragma unroll
-    for (int n = 0; n < NG; n++) B[n] = __ldg(v.base + e * NG + n);
+    for (int n = 0; n < NG; n++) B[n] = __ldg(v.base + (GATED ? 2 * e + n : e));
 
     for (int r0 = lo; r0 < hi; r0 += 8) {
+        const uint8_t *sp = steps;
+        Part p[NG], pn[NG];
+        if (mine > 0)
+#pragma unroll
+            for (int n = 0; n < NG; n++) pn[n] = load_part(sp, gi + n, at);
         // this lane's row of X (row g of the eight)
         const int r = r0 + g;
-        const uint16_t *xr = nullptr;
+        const uint4 *xp = nullptr;
         if (r < hi) {
             const int64_t src = c.row_src ? __ldg(c.row_src + r) : r;
-            if (src >= 0 && src < c.x_rows) xr = c.x + src * c.ldx + 16 * t;
+            if (src >= 0 && src < c.x_rows) xp = (const uint4 *)(c.x + src * c.ldx + 16 * t + warp * kStepW);
+        }
+        uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0, xn0 = x0, xn1 = x0;
+        if (xp && mine > 0) {
+            xn0 = __ldg(xp);
+            xn1 = __ldg(xp + 1);
         }
         float acc[NG][4];
 #pragma unroll
         for (int n = 0; n < NG; n++)
 #pragma unroll
             for (int i = 0; i < 4; i++) acc[n][i] = 0.f;
-        for (int ks = warp; ks < v.ksteps; ks += kWarps) {
-            Part p[NG];
+        for (int i = 0; i < mine; i++) {
+            // the next step's loads leave before this step's products
+            const uint8_t *cur = sp;
+            sp += (size_t)WARPS * kStepBytes;
 #pragma unroll
-            for (int n = 0; n < NG; n++) p[n] = load_part(v, s0 + ks, gi + n, at);
-            uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
-            if (xr) {
-                x0 = __ldg((const uint4 *)(xr + (int64_t)ks * kStepW));
-                x1 = __ldg((const uint4 *)(xr + (int64_t)ks * kStepW) + 1);
+            for (int n = 0; n < NG; n++) p[n] = pn[n];
+            x0 = xn0;
+            x1 = xn1;
+            if (i + 1 < mine) {
+#pragma unroll
+                for (int n = 0; n < NG; n++) pn[n] = load_part(sp, gi + n, at);
+                if (xp) {
+                    xp += WARPS * kStepW / 8;
+                    xn0 = __ldg(xp);
+                    xn1 = __ldg(xp + 1);
+                }
             }
 #pragma unroll
             for (int n = 0; n < NG; n++) {
                 uint32_t a[8], b[8];
-                rebuild_part(v, p[n], s0 + ks, gi + n, g, t, B[n], a, b);
+                rebuild_part(v.verb, p[n], cur, gi + n, g, t, B[n], a, b);
 #pragma unroll
                 for (int q = 0; q < 4; q++) {
                     const uint4 &x = q < 2 ? x0 : x1;
@@ -162,38 +182,50 @@ __global__ void __launch_bounds__(32 * kWarps) group_gemv_kernel(const GroupCall
 #pragma unroll
             for (int i = 0; i < 4; i++) part[warp][n][g + 8 * (i >> 1)][2 * t + (i & 1)] = acc[n][i];
         __syncthreads();
-        if (threadIdx.x < 128) {
-            const int o = threadIdx.x & 15, j = threadIdx.x >> 4;
+        for (int at128 = threadIdx.x; at128 < 128; at128 += 32 * WARPS) {
+            const int o = at128 & 15, j = at128 >> 4;
             float s[NG];
 #pragma unroll
             for (int n = 0; n < NG; n++) {
                 s[n] = 0.f;
 #pragma unroll
-                for (int w = 0; w < kWarps; w++) s[n] += part[w][n][o][j];
+                for (int w = 0; w < WARPS; w++) s[n] += part[w][n][o][j];
             }
-            float f = s[0];
-            if (GATED) f = gated(s[0], s[NG - 1]);
-            const int64_t col = (int64_t)blockIdx.x * kGran + o;
-            if (r0 + j < hi && col < v.N) {
+            if (r0 + j >= hi) continue;
+            if (GATED) s[0] = gated(s[0], s[1]);
+#pragma unroll
+            for (int n = 0; n < (GATED ? 1 : NG); n++) {
+                const int64_t col = ((int64_t)blockIdx.x * (GATED ? 1 : NG) + n) * kGran + o;
+                if (col >= v.N) continue;
                 const int64_t i = (int64_t)(r0 + j) * c.ldy + col;
-                if (c.out_bf16) ((__nv_bfloat16 *)c.y)[i] = __float2bfloat16_rn(f);
-                else ((float *)c.y)[i] = f;
+                if (c.out_bf16) ((__nv_bfloat16 *)c.y)[i] = __float2bfloat16_rn(s[n]);
+                else ((float *)c.y)[i] = s[n];
             }
         }
         __syncthreads();
     }
 }
 
+template <int WARPS>
+cudaError_t launch_warps(const GroupCall &c, dim3 grid, int all, cudaStream_t st)
+{
+    return c.v.gated ? launch_dependent(group_gemv_kernel<true, WARPS>, grid, 32 * WARPS, 0, 0, st, c, all)
+                     : launch_dependent(group_gemv_kernel<false, WARPS>, grid, 32 * WARPS, 0, 0, st, c, all);
+}
+
 }  // namespace
 
 int launch_group_gemv(const GroupCall &c, void *stream)
 {
-    const int64_t grans = (c.v.N + kGran - 1) / kGran;
+    // a CTA's two virtual granules: gate and up of 16 outputs, or 32 outputs
+    const int64_t pairs = (c.v.granules + 1) / 2;
     const int all = c.rows >= c.v.experts;
-    const dim3 grid((unsigned)grans, (unsigned)(all ? c.v.experts : (int)c.rows));
-    if (c.v.gated) group_gemv_kernel<true><<<grid, 32 * kWarps, 0, (cudaStream_t)stream>>>(c, all);
-    else group_gemv_kernel<false><<<grid, 32 * kWarps, 0, (cudaStream_t)stream>>>(c, all);
-    return cudaGetLastError();
+    const dim3 grid((unsigned)pairs, (unsigned)(all ? c.v.experts : (int)c.rows));
+    // Four CTAs of four warps fit on an SM; with fewer CTAs than that in all, twice the warps over K keep as many bytes on
+    // the way (2 experts of [4096, 14336]: 33 us against 55; where CTAs abound, the longer runs of four warps win: 8 tokens,
+    // 64 experts of [2048, 1408]: 35 us against 41).
+    if ((int64_t)grid.x * grid.y <= 5 * (int64_t)num_sms()) return launch_warps<8>(c, grid, all, (cudaStream_t)stream);
+    return launch_warps<4>(c, grid, all, (cudaStream_t)stream);
 }
 
 }  // namespace uw

@@ -30,6 +30,7 @@
 #include <cstring>
 
 #include "group.cuh"
+#include "launch.cuh"
 #include "uw_internal.h"
 
 namespace uw {
@@ -175,6 +176,8 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    pdl_trigger();
+    pdl_wait();
     if (warp == 0) {
         // the experts' row tiles: a running sum, 32 experts at a time
         const int R = (int)a.c.rows;
@@ -369,8 +372,8 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
     } else if (warp < kRebuildWarps) {
         // ---------------------------------------------------------------------------------------- rebuild
         const int grp = warp >> 2, r = 32 * (warp & 3) + lane;  // row of the tile
-        const uint32_t o_s = (r >> 4) * 1024 + ((r >> 3) & 1) * 512 + (r & 7) * 16;
-        const uint32_t o_c = kStepSm + (r >> 4) * 512 + (r & 7) * 16 + ((r >> 3) & 1) * 8;
+        const uint32_t o_s = (r >> 4) * 1024 + ((r >> 3) & 1) * 512 + chunk_at(r & 7, 0);  // chunk t at o_s ^ 16 t
+        const uint32_t o_c = kStepSm + (r >> 4) * 512 + chunk_at(r & 7, 0) + ((r >> 3) & 1) * 8;
         const uint32_t t_lane = (uint32_t)(32 * (warp & 3)) << 16;
         bool ok = true;
         int i = 0;  // steps before this unit
@@ -386,8 +389,8 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
                 uint2 C[4];
 #pragma unroll
                 for (int t = 0; t < 4; t++) {
-                    S[t] = *(const uint4 *)(st + o_s + 128 * t);
-                    C[t] = *(const uint2 *)(st + o_c + 128 * t);
+                    S[t] = *(const uint4 *)(st + (o_s ^ (16u * t)));
+                    C[t] = *(const uint2 *)(st + (o_c ^ (16u * t)));
                 }
                 // the stage's reads of steps and the A slot are apart: wait for the slot with the words in registers
                 if (q >= kSA && !mbar_wait(&aempty[sa], ((q / kSA) & 1) ^ 1)) { ok = false; break; }
@@ -494,8 +497,7 @@ cudaError_t launch_one(const TcArgs &a, int grid, cudaStream_t st)
         if (e != cudaSuccess) return e;
         attr = true;
     }
-    group_tc_kernel<GATED, GATHER><<<grid, kThreads, kSmem, st>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(group_tc_kernel<GATED, GATHER>, dim3((unsigned)grid), kThreads, kSmem, 0, st, a);
 }
 
 bool map_x(CUtensorMap *m, const GroupCall &c)

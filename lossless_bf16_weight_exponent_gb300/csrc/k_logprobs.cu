@@ -20,6 +20,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "launch.cuh"
 #include "uw_internal.h"
 
 namespace cg = cooperative_groups;
@@ -201,6 +202,8 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const LpArgs a)
     const Slice<V> sl = slice_of<BF16>(r, a.vocab, c, C);
     const int n = a.n_top;
 
+    pdl_trigger();
+    pdl_wait();
     Sums t{-INFINITY, 0.f, 0.f};
     for (int64_t v = sl.v0 + threadIdx.x; v < sl.v1; v += kThreads) {
         float x[V];
@@ -333,22 +336,6 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const LpArgs a)
     if (C > 1) cluster.sync();  // the leader reads the others' shared memory
 }
 
-template <bool BF16>
-cudaError_t launch(const LpArgs &a, int C, cudaStream_t st)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.rows * C));
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute la[1];
-    la[0].id = cudaLaunchAttributeClusterDimension;
-    la[0].val.clusterDim.x = (unsigned)C;
-    la[0].val.clusterDim.y = la[0].val.clusterDim.z = 1;
-    cfg.attrs = la;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, logprob_kernel<BF16>, a);
-}
-
 }  // namespace
 
 extern "C" uw_status uw_token_logprobs(const void *logits, uw_out_dtype dtype, int64_t rows, int64_t vocab, int64_t ld, float temperature,
@@ -374,6 +361,7 @@ extern "C" uw_status uw_token_logprobs(const void *logits, uw_out_dtype dtype, i
     // few rows: several CTAs a row, while a slice keeps 4096 logits
     int C = 1;
     while (C < kMaxCluster && rows * C * 2 <= 2 * num_sms() && vocab / (C * 2) >= 4096) C *= 2;
-    const cudaError_t e = dtype == UW_OUT_BF16 ? launch<true>(a, C, (cudaStream_t)stream) : launch<false>(a, C, (cudaStream_t)stream);
+    const cudaError_t e = launch_dependent(dtype == UW_OUT_BF16 ? logprob_kernel<true> : logprob_kernel<false>, dim3((unsigned)(rows * C)), kThreads, 0,
+                                           (unsigned)C, (cudaStream_t)stream, a);
     return e == cudaSuccess ? UW_OK : fail(UW_ERR_CUDA, "uw_token_logprobs: launch: %s", cudaGetErrorString(e));
 }

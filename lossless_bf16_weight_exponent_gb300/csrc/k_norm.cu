@@ -11,6 +11,7 @@
 
 #include <algorithm>
 
+#include "launch.cuh"
 #include "uw_internal.h"
 
 using namespace uw;
@@ -103,6 +104,8 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a)
     __shared__ float red[32];
     const int64_t D = a.n.dim;
     const int64_t row = blockIdx.x;
+    pdl_trigger();
+    pdl_wait();
     float o[CH][8];
     float ss = 0.f;
 #pragma unroll
@@ -174,10 +177,9 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a)
 }
 
 template <int CH>
-void launch_ch(const NormArgs &a, int threads, bool vec, cudaStream_t st)
+cudaError_t launch_ch(const NormArgs &a, int threads, bool vec, cudaStream_t st)
 {
-    if (vec) norm_kernel<CH, true><<<(unsigned)a.rows, threads, 0, st>>>(a);
-    else norm_kernel<CH, false><<<(unsigned)a.rows, threads, 0, st>>>(a);
+    return launch_dependent(vec ? norm_kernel<CH, true> : norm_kernel<CH, false>, dim3((unsigned)a.rows), (unsigned)threads, 0, 0, st, a);
 }
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
@@ -211,12 +213,12 @@ extern "C" uw_status uw_block_norm(const uw_norm *n, int64_t rows, const void *h
     // up to 512 threads of one chunk each, then more chunks a thread, then more threads
     const int ch = chunks <= 512 ? 1 : chunks <= 1024 ? 2 : chunks <= 4096 ? 4 : 8;
     const int threads = (int)(((chunks + ch - 1) / ch + 31) / 32 * 32);
+    cudaError_t e;
     switch (ch) {
-    case 1: launch_ch<1>(a, threads, vec, st); break;
-    case 2: launch_ch<2>(a, threads, vec, st); break;
-    case 4: launch_ch<4>(a, threads, vec, st); break;
-    default: launch_ch<8>(a, threads, vec, st); break;
+    case 1: e = launch_ch<1>(a, threads, vec, st); break;
+    case 2: e = launch_ch<2>(a, threads, vec, st); break;
+    case 4: e = launch_ch<4>(a, threads, vec, st); break;
+    default: e = launch_ch<8>(a, threads, vec, st); break;
     }
-    const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? UW_OK : fail(UW_ERR_CUDA, "uw_block_norm: launch: %s", cudaGetErrorString(e));
 }

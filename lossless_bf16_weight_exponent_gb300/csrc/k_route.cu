@@ -15,6 +15,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "launch.cuh"
 #include "uw_internal.h"
 
 using namespace uw;
@@ -174,6 +175,8 @@ __global__ void __launch_bounds__(kThreads) route_choose_kernel(const RouteArgs 
     const int64_t t0 = (int64_t)blockIdx.x * kTok;
     const int nt = (int)min((int64_t)kTok, a.tokens - t0);
     for (int i = threadIdx.x; i < E * (kTok / 32); i += kThreads) (&bits[0][0])[i] = 0u;
+    pdl_trigger();
+    pdl_wait();
     __syncthreads();
     for (int tl = threadIdx.x >> 5; tl < nt; tl += kThreads / 32) choose_any(a, t0 + tl, threadIdx.x & 31, bits, tl);
     __syncthreads();
@@ -207,6 +210,8 @@ __global__ void __launch_bounds__(kThreads) route_order_kernel(const RouteArgs a
     const int64_t t0 = (int64_t)blockIdx.x * kTok;
     const int nt = (int)min((int64_t)kTok, a.tokens - t0);
     for (int i = threadIdx.x; i < E * (kTok / 32); i += kThreads) (&bits[0][0])[i] = 0u;
+    pdl_trigger();
+    pdl_wait();
     // rows of each expert in all CTAs, and in those before this one
     int all = 0, before = 0;
     if ((int)threadIdx.x < E)
@@ -287,9 +292,8 @@ extern "C" uw_status uw_route(const uw_router *r, const void *logits, uw_out_dty
     if (tokens == 0) {
         e = cudaMemsetAsync(offsets, 0, ((size_t)r->experts + 1) * 4, st);
     } else {
-        route_choose_kernel<<<(unsigned)ctas, kThreads, 0, st>>>(a);
-        if (ctas > 1) route_order_kernel<<<(unsigned)ctas, kThreads, 0, st>>>(a, (int)ctas);
-        e = cudaGetLastError();
+        e = launch_dependent(route_choose_kernel, dim3((unsigned)ctas), kThreads, 0, 0, st, a);
+        if (e == cudaSuccess && ctas > 1) e = launch_dependent(route_order_kernel, dim3((unsigned)ctas), kThreads, 0, 0, st, a, (int)ctas);
     }
     return e == cudaSuccess ? UW_OK : fail(UW_ERR_CUDA, "uw_route: launch: %s", cudaGetErrorString(e));
 }
