@@ -33,8 +33,6 @@ using namespace uw;
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
 constexpr int kMaxTop = 32;
 constexpr int kCand = 2048;
 constexpr int kUnroll = 4;             // 16-byte loads of a thread on their way
@@ -111,9 +109,8 @@ struct PairSums {
     float m;
     Pair s, w;
     __device__ __forceinline__ PairSums() : m(kLow), s(pair(0.f, 0.f)), w(pair(0.f, 0.f)) {}
-    // x: clamped logits, v: their maximum
-    template <int N>
-    __device__ __forceinline__ void add(const float (&x)[N], float v, float scale)
+    // the maximum becomes at least v
+    __device__ __forceinline__ void raise(float v, float scale)
     {
         if (v > m) {
             const float d = m - v, e = exp2_fast(d * scale);
@@ -125,6 +122,11 @@ struct PairSums {
             }
             m = v;
         }
+    }
+    // x: raised logits, none above m
+    template <int N>
+    __device__ __forceinline__ void add(const float (&x)[N], float scale)
+    {
         const Pair nm = pair(-m, -m), sc = pair(scale, scale);
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
@@ -138,16 +140,7 @@ struct PairSums {
     }
     __device__ __forceinline__ void add1(float x, float scale)
     {
-        if (x > m) {
-            const float d = m - x, e = exp2_fast(d * scale);
-            if (e == 0.f) {
-                s = w = pair(0.f, 0.f);
-            } else {
-                w = mul2(fma2(pair(d, d), s, w), pair(e, e));
-                s = mul2(s, pair(e, e));
-            }
-            m = x;
-        }
+        raise(x, scale);
         const float d = x - m, e = exp2_fast(d * scale);
         s = add2(s, pair(e, 0.f));
         w = fma2(pair(d, 0.f), pair(e, 0.f), w);
@@ -189,72 +182,94 @@ template <bool BF16>
 struct Row {
     static constexpr int V = BF16 ? 8 : 4;  // elements of a 16-byte load
     const void *p;
-    __device__ __forceinline__ float at(int64_t i) const
+    __device__ __forceinline__ float at(int i) const
     {
         return BF16 ? __bfloat162float(((const __nv_bfloat16 *)p)[i]) : ((const float *)p)[i];
     }
-    __device__ __forceinline__ uint4 load(int64_t i) const  // i: 16-byte aligned element
+    __device__ __forceinline__ uint4 load(int i) const  // i: 16-byte aligned element
     {
-        return __ldg((const uint4 *)((const uint8_t *)p + i * (16 / V)));
+        return __ldg((const uint4 *)((const uint8_t *)p + (uint32_t)i * (16u / V)));
     }
-    // the elements of a load; CLAMP: with clamp_low
-    template <bool CLAMP>
+    // a load with its masked logits raised to kLow or the next value below it
+    static __device__ __forceinline__ uint4 raised(const uint4 &v)
+    {
+        return make_uint4(raised1(v.x), raised1(v.y), raised1(v.z), raised1(v.w));
+    }
+    static __device__ __forceinline__ uint32_t raised1(uint32_t w)
+    {
+        uint32_t u;
+        if constexpr (BF16) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(u) : "r"(w), "r"(0xFCF1FCF1u));
+        else asm("max.NaN.f32 %0, %1, %2;" : "=r"(u) : "r"(w), "r"(__float_as_uint(kLow)));
+        return u;
+    }
+    // the largest element of N loads
+    template <int N>
+    static __device__ __forceinline__ float largest(const uint4 (&v)[N])
+    {
+        auto max1 = [](uint32_t a, uint32_t b) {
+            uint32_t u;
+            if constexpr (BF16) asm("max.bf16x2 %0, %1, %2;" : "=r"(u) : "r"(a), "r"(b));
+            else asm("max.f32 %0, %1, %2;" : "=r"(u) : "r"(a), "r"(b));
+            return u;
+        };
+        uint32_t m = max1(max1(v[0].x, v[0].y), max1(v[0].z, v[0].w));
+#pragma unroll
+        for (int i = 1; i < N; i++) m = max1(m, max1(max1(v[i].x, v[i].y), max1(v[i].z, v[i].w)));
+        if constexpr (BF16) return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+        else return __uint_as_float(m);
+    }
     static __device__ __forceinline__ void split(const uint4 &v, float (&f)[V])
     {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int q = 0; q < 4; q++) {
             if constexpr (BF16) {
-                uint32_t u = w[q];
-                // -1e37 in bf16 twice
-                if (CLAMP) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(u) : "r"(u), "r"(0xFCF1FCF1u));
-                f[2 * q] = __uint_as_float(u << 16);
-                f[2 * q + 1] = __uint_as_float(u & 0xFFFF0000u);
+                f[2 * q] = __uint_as_float(w[q] << 16);
+                f[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
             } else {
-                f[q] = CLAMP ? clamp_low(__uint_as_float(w[q])) : __uint_as_float(w[q]);
+                f[q] = __uint_as_float(w[q]);
             }
         }
     }
 };
 
 // a CTA's slice of a row: whole 16-byte vectors [v0, v1) from element `head` on, and single elements (the row's
-// unaligned head for the first CTA, its tail for the last) that threads take one each
-template <int V>
+// unaligned head for the first CTA, its tail for the last) that threads take one each; a row has at most 2^24 elements
 struct Slice {
-    int64_t head, v0, v1, s0, s1;  // singles: [s0, s1)
-    int64_t t0, t1;                // and [t0, t1)
+    int head, v0, v1, s1;  // singles: [0, s1)
+    int t0, t1;            // and [t0, t1)
 };
 
+// CTA c of 1 << cs
 template <bool BF16>
-__device__ __forceinline__ Slice<Row<BF16>::V> slice_of(const Row<BF16> &r, int64_t vocab, int c, int C)
+__device__ __forceinline__ Slice slice_of(const Row<BF16> &r, int vocab, int c, int cs)
 {
     constexpr int V = Row<BF16>::V;
-    Slice<V> s;
-    const int mis = (int)(((uintptr_t)r.p & 15) / (16 / V));
-    s.head = min((int64_t)((V - mis) % V), vocab);
-    const int64_t nv = (vocab - s.head) / V;
-    s.v0 = nv * c / C;
-    s.v1 = nv * (c + 1) / C;
-    s.s0 = 0;
+    Slice s;
+    const int mis = (int)((uint32_t)(uintptr_t)r.p & 15u) / (16 / V);
+    s.head = min((V - mis) % V, vocab);
+    const int nv = (vocab - s.head) / V;
+    s.v0 = (nv * c) >> cs;  // at most 2^22 vectors by 8
+    s.v1 = (nv * (c + 1)) >> cs;
     s.s1 = c == 0 ? s.head : 0;
     s.t0 = s.head + nv * V;
-    s.t1 = c == C - 1 ? vocab : s.t0;
+    s.t1 = c == (1 << cs) - 1 ? vocab : s.t0;
     return s;
 }
 
 // f(x, index) on each of this thread's elements
-template <bool BF16, typename F>
-__device__ __forceinline__ void each(const Row<BF16> &r, const Slice<Row<BF16>::V> &s, F f)
+template <bool BF16, int THREADS, typename F>
+__device__ __forceinline__ void each(const Row<BF16> &r, const Slice &s, F f)
 {
     constexpr int V = Row<BF16>::V;
-    for (int64_t v = s.v0 + threadIdx.x; v < s.v1; v += kThreads) {
+    for (int v = s.v0 + threadIdx.x; v < s.v1; v += THREADS) {
         float x[V];
-        Row<BF16>::template split<false>(r.load(s.head + v * V), x);
+        Row<BF16>::split(r.load(s.head + v * V), x);
 #pragma unroll
         for (int i = 0; i < V; i++) f(x[i], (uint32_t)(s.head + v * V + i));
     }
-    for (int64_t i = s.s0 + threadIdx.x; i < s.s1; i += kThreads) f(r.at(i), (uint32_t)i);
-    for (int64_t i = s.t0 + threadIdx.x; i < s.t1; i += kThreads) f(r.at(i), (uint32_t)i);
+    for (int i = threadIdx.x; i < s.s1; i += THREADS) f(r.at(i), (uint32_t)i);
+    for (int i = s.t0 + threadIdx.x; i < s.t1; i += THREADS) f(r.at(i), (uint32_t)i);
 }
 
 __device__ __forceinline__ unsigned long long warp_max(unsigned long long k)
@@ -267,150 +282,188 @@ __device__ __forceinline__ unsigned long long warp_max(unsigned long long k)
     return k;
 }
 
-// a bound that at least n of the values behind the threads' maxima reach: the warps whose lanes all have one (the first
-// `full`) bring q of their lanes' maxima each, n in all, and the least of those is it; -inf without such a warp
-__device__ __forceinline__ float bound_of(float m, int full, int n, float *warp_bounds)
+// A bound that at least n of the values behind the threads' maxima reach, and few more: the warps whose lanes all have
+// one (the first `full`) bring a few of their largest each, and the n-th largest of these is it; -inf without such a warp.
+template <int kWarps>
+__device__ __forceinline__ float bound_of(float m, int full, int n, float *top)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float bound = INFINITY;
-    if (warp < full) {
-        const int q = (n + full - 1) / full;
-        for (int i = 0; i < q; i++) {
-            bound = m;
-#pragma unroll
-            for (int d = 16; d; d >>= 1) bound = fmaxf(bound, __shfl_xor_sync(0xFFFFFFFFu, bound, d));
-            const uint32_t who = __ballot_sync(0xFFFFFFFFu, m == bound);
-            if (who && lane == __ffs(who) - 1) m = -INFINITY;
-        }
-    }
-    __syncthreads();
-    if (lane == 0) warp_bounds[warp] = bound;
-    __syncthreads();
     if (full == 0) return -INFINITY;
-    float b = warp_bounds[0];
+    const int q = min(32, (n + full - 1) / full + 1);  // full q <= 63 values, at least n
+    if (warp < full)
+        for (int i = 0; i < q; i++) {
+            float best = m;
 #pragma unroll
-    for (int w = 1; w < kWarps; w++) b = fminf(b, warp_bounds[w]);
+            for (int d = 16; d; d >>= 1) best = fmaxf(best, __shfl_xor_sync(0xFFFFFFFFu, best, d));
+            const uint32_t who = __ballot_sync(0xFFFFFFFFu, m == best);
+            if (lane == __ffs(who) - 1) m = -INFINITY;
+            if (lane == 0) top[warp * q + i] = best;
+        }
+    __syncthreads();
+    const int k = full * q;
+    const float v0 = lane < k ? top[lane] : -INFINITY, v1 = lane + 32 < k ? top[lane + 32] : -INFINITY;
+    int g0 = 0, g1 = 0;  // larger values
+    for (int i = 0; i < k; i++) {
+        const float v = top[i];
+        g0 += v > v0;
+        g1 += v > v1;
+    }
+    float b = fminf(lane < k && g0 < n ? v0 : INFINITY, lane + 32 < k && g1 < n ? v1 : INFINITY);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) b = fminf(b, __shfl_xor_sync(0xFFFFFFFFu, b, d));
+    __syncthreads();
     return b;
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(kThreads, 2) logprob_kernel(const LpArgs a)
+template <bool BF16, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(const LpArgs a, int cs)
 {
+    constexpr int kWarps = kThreads / 32;
     constexpr int V = Row<BF16>::V;
-    __shared__ Sums warp_sums[kWarps], cta_sums;
-    __shared__ float bounds[kWarps];
+    __shared__ Sums warp_sums[kWarps];
+    __shared__ float bounds[64];
     __shared__ unsigned long long cand[kCand], best[kMaxTop], merged[kMaxTop];
     __shared__ uint16_t kept[kCand];
-    __shared__ int n_cand, n_kept, n_best;
+    __shared__ int n_cand, n_kept;
+    // written by the row's CTAs: their sums and counts in each, their top tokens in the leader
+    __shared__ Sums row_parts[kMaxCluster];
+    __shared__ int row_have[kMaxCluster];
+    __shared__ unsigned long long row_tops[kMaxCluster * kMaxTop];
     cg::cluster_group cluster = cg::this_cluster();
-    const int C = (int)cluster.num_blocks(), c = (int)cluster.block_rank();
-    const int64_t row = blockIdx.x / C;
+    const int C = 1 << cs, c = (int)(blockIdx.x & (C - 1));  // the cluster's CTAs are a row's
+    const int64_t row = blockIdx.x >> cs;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Row<BF16> r{BF16 ? (const void *)((const uint16_t *)a.logits + row * a.ld) : (const void *)((const float *)a.logits + row * a.ld)};
-    const Slice<V> sl = slice_of<BF16>(r, a.vocab, c, C);
+    const int vocab = (int)a.vocab;
+    const Slice sl = slice_of<BF16>(r, vocab, c, cs);
     const int n = a.n_top;
     const float scale = a.scale;
 
     if (threadIdx.x == 0) n_cand = n_kept = 0;
     pdl_trigger();
+    __syncthreads();
     pdl_wait();
 
-    // joins the threads' sums; the CTA's in cta_sums after the last barrier
-    auto cta_join = [&](Sums t, auto join_fn) {
-        auto lanes = [&](Sums u) {
+    auto lanes_join = [&](Sums u, auto join_fn) {
 #pragma unroll
-            for (int d = 16; d; d >>= 1) {
-                // both lanes join in the same order: the result is the same in each
-                const Sums o{__shfl_xor_sync(0xFFFFFFFFu, u.m, d), __shfl_xor_sync(0xFFFFFFFFu, u.s, d), __shfl_xor_sync(0xFFFFFFFFu, u.w, d)};
-                u = (lane & d) ? join_fn(o, u, scale) : join_fn(u, o, scale);
-            }
-            return u;
-        };
-        t = lanes(t);
-        __syncthreads();
+        for (int d = 16; d; d >>= 1) {
+            // both lanes join in the same order: the result is the same in each
+            const Sums o{__shfl_xor_sync(0xFFFFFFFFu, u.m, d), __shfl_xor_sync(0xFFFFFFFFu, u.s, d), __shfl_xor_sync(0xFFFFFFFFu, u.w, d)};
+            u = (lane & d) ? join_fn(o, u, scale) : join_fn(u, o, scale);
+        }
+        return u;
+    };
+    // the CTA's sums, in every thread (lowest: the maximum of none)
+    auto cta_join = [&](Sums t, float lowest, auto join_fn) {
+        t = lanes_join(t, join_fn);
         if (lane == 0) warp_sums[warp] = t;
         __syncthreads();
-        if (warp == 0) {
-            t = lanes(lane < kWarps ? warp_sums[lane] : Sums{-INFINITY, 0.f, 0.f});
-            if (lane == 0) cta_sums = t;
+        return lanes_join(lane < kWarps ? warp_sums[lane] : Sums{lowest, 0.f, 0.f}, join_fn);
+    };
+    // to every CTA of the row, and to the leader
+    auto publish = [&](const Sums &t, int have) {
+        if (threadIdx.x < C) {
+            *cluster.map_shared_rank(&row_parts[c], threadIdx.x) = t;
+            *cluster.map_shared_rank(&row_have[c], threadIdx.x) = have;
         }
-        __syncthreads();
+        if ((int)threadIdx.x < n) cluster.map_shared_rank(row_tops, 0)[c * n + threadIdx.x] = best[threadIdx.x];
+    };
+    auto row_sync = [&] {
+        if (C > 1) cluster.sync();
+        else __syncthreads();
     };
     static_assert(kWarps <= 32, "the join of the warps' sums");
 
     PairSums sums;
     float bound = INFINITY;
+    auto list = [&](float x, int i) {
+        const int at = atomicAdd(&n_cand, 1);
+        if (at < kCand) cand[at] = key_of(x, (uint32_t)i);
+    };
     // the sums over vectors [v, v1), kThreads apart, and the list of those that reach the bound
-    auto sweep = [&](int64_t v, int64_t v1, auto collect) {
-        for (; v < v1; v += kUnroll * kThreads) {
-            uint4 raw[kUnroll];
+    auto sweep = [&](int v, int v1, auto collect) {
+        constexpr uint32_t kPad = BF16 ? 0xFCF1FCF1u : 0xFCF0BDC2u;  // kLow, as raised: adds nothing and is not listed
+        uint4 next[kUnroll];
+        auto load = [&](int at) {
 #pragma unroll
             for (int u = 0; u < kUnroll; u++)
-                if (v + u * kThreads < v1) raw[u] = r.load(sl.head + (v + u * kThreads) * V);
+                next[u] = at + u * kThreads < v1 ? r.load(sl.head + (at + u * kThreads) * V) : make_uint4(kPad, kPad, kPad, kPad);
+        };
+        if (v < v1) load(v);
+        for (; v < v1; v += kUnroll * kThreads) {
+            uint4 x[kUnroll];
+#pragma unroll
+            for (int u = 0; u < kUnroll; u++) x[u] = Row<BF16>::raised(next[u]);
+            if (v + kUnroll * kThreads < v1) load(v + kUnroll * kThreads);  // on their way during the sums
+            const float mx = Row<BF16>::largest(x);
+            sums.raise(mx, scale);
 #pragma unroll
             for (int u = 0; u < kUnroll; u++) {
-                if (v + u * kThreads >= v1) break;
-                float x[V];
-                Row<BF16>::template split<true>(raw[u], x);
-                float mx = x[0];
+                float f[V];
+                Row<BF16>::split(x[u], f);
+                sums.add(f, scale);
+            }
+            if (decltype(collect)::value && mx >= bound) {
 #pragma unroll
-                for (int i = 1; i < V; i++) mx = fmaxf(mx, x[i]);
-                sums.add(x, mx, scale);
-                if (decltype(collect)::value && mx >= bound) {
+                for (int u = 0; u < kUnroll; u++) {
+                    float f[V];
+                    Row<BF16>::split(x[u], f);
 #pragma unroll
                     for (int i = 0; i < V; i++)
-                        if (x[i] >= bound) {
-                            const int k = atomicAdd(&n_cand, 1);
-                            if (k < kCand) cand[k] = key_of(x[i], (uint32_t)(sl.head + (v + u * kThreads) * V + i));
-                        }
+                        if (f[i] >= bound) list(f[i], sl.head + (v + u * kThreads) * V + i);
                 }
             }
         }
     };
-    const int64_t nv = sl.v1 - sl.v0;
-    int64_t done = sl.v0;
+    const int nv = sl.v1 - sl.v0;
+    int done = sl.v0;
     if (n) {
-        constexpr int64_t kStep = kUnroll * kThreads;
-        const int64_t first = min(nv, (nv / 8 + kStep - 1) / kStep * kStep);
+        constexpr int kStep = kUnroll * kThreads;
+        const int first = min(nv, (nv / 8 + kStep - 1) / kStep * kStep);
         done = sl.v0 + first;
         sweep(sl.v0 + threadIdx.x, done, std::false_type());
-        bound = bound_of(sums.m, (int)min((int64_t)kWarps, first / 32), n, bounds);
+        bound = bound_of<kWarps>(sums.m, min(kWarps, first / 32), n, bounds);
         // no bound above the masked logits: every logit above them is listed
         const float above = BF16 ? __uint_as_float(0xFCF00000u) : __uint_as_float(__float_as_uint(kLow) - 1);
         bound = fmaxf(bound, above);
-        for (int64_t v = sl.v0 + threadIdx.x; v < done; v += kThreads) {
-            float x[V];
-            Row<BF16>::template split<false>(r.load(sl.head + v * V), x);
+        for (int v = sl.v0 + threadIdx.x; v < done; v += kStep) {
+            uint4 x[kUnroll];
 #pragma unroll
-            for (int i = 0; i < V; i++)
-                if (x[i] >= bound) {
-                    const int k = atomicAdd(&n_cand, 1);
-                    if (k < kCand) cand[k] = key_of(x[i], (uint32_t)(sl.head + v * V + i));
-                }
+            for (int u = 0; u < kUnroll; u++)
+                if (v + u * kThreads < done) x[u] = r.load(sl.head + (v + u * kThreads) * V);
+#pragma unroll
+            for (int u = 0; u < kUnroll; u++) {
+                if (v + u * kThreads >= done) break;
+                float f[V];
+                Row<BF16>::split(x[u], f);
+#pragma unroll
+                for (int i = 0; i < V; i++)
+                    if (f[i] >= bound) list(f[i], sl.head + (v + u * kThreads) * V + i);
+            }
         }
         sweep(done + threadIdx.x, sl.v1, std::true_type());
     } else {
         sweep(done + threadIdx.x, sl.v1, std::false_type());
     }
     const float vec_max = sums.m;  // over whole vectors alone
-    auto single = [&](int64_t i) {
+    auto single = [&](int i) {
         const float x = r.at(i);
         sums.add1(clamp_low(x), scale);
-        if (n && x >= bound) {
-            const int k = atomicAdd(&n_cand, 1);
-            if (k < kCand) cand[k] = key_of(x, (uint32_t)i);
-        }
+        if (n && x >= bound) list(x, i);
     };
-    for (int64_t i = sl.s0 + threadIdx.x; i < sl.s1; i += kThreads) single(i);
-    for (int64_t i = sl.t0 + threadIdx.x; i < sl.t1; i += kThreads) single(i);
-    cta_join(sums.total(), [](const Sums &p, const Sums &q, float s) { return join(p, q, s); });
+    for (int i = threadIdx.x; i < sl.s1; i += kThreads) single(i);
+    for (int i = sl.t0 + threadIdx.x; i < sl.t1; i += kThreads) single(i);
+    auto plain_join = [](const Sums &p, const Sums &q, float s) { return join(p, q, s); };
+    auto exact_join = [](const Sums &p, const Sums &q, float s) { return join_exact(p, q, s); };
+    Sums row_sums = cta_join(sums.total(), kLow, plain_join);
+    int have = 0;
 
     // the slice's top: complete (n, or all it has), or all of its unmasked logits
     auto rounds = [&](int from) {
         unsigned long long last = from ? best[from - 1] : ~0ull;
         for (int j = from; j < n; j++) {
             unsigned long long k = 0ull;
-            each<BF16>(r, sl, [&](float x, uint32_t i) {
+            each<BF16, kThreads>(r, sl, [&](float x, uint32_t i) {
                 const unsigned long long o = key_of(x, i);
                 if (o < last && o > k) k = o;
             });
@@ -429,10 +482,9 @@ __global__ void __launch_bounds__(kThreads, 2) logprob_kernel(const LpArgs a)
     if (n) {
         if ((int)threadIdx.x < kMaxTop) best[threadIdx.x] = 0ull;
         const int nc = n_cand;
-        const bool odd = cta_sums.s != cta_sums.s;  // a NaN or +inf
-        if (!odd && nc <= kCand) {
-            // the closer bound
-            const float b2 = bound_of(vec_max, (int)min((int64_t)kWarps, nv / 32), n, bounds);
+        if (row_sums.s == row_sums.s && nc <= kCand) {
+            // the closer bound, where the list is long
+            const float b2 = nc > 256 ? bound_of<kWarps>(vec_max, min(kWarps, nv / 32), n, bounds) : -INFINITY;
             const unsigned long long kb = b2 > bound ? key_of(b2, 0xFFFFFFFFu) : 0ull;
             for (int i = threadIdx.x; i < nc; i += kThreads)
                 if (cand[i] >= kb) kept[atomicAdd(&n_kept, 1)] = (uint16_t)i;
@@ -444,47 +496,42 @@ __global__ void __launch_bounds__(kThreads, 2) logprob_kernel(const LpArgs a)
                 for (int j = 0; j < nk; j++) rank += cand[kept[j]] > k;
                 if (rank < n) best[rank] = k;
             }
-            if (threadIdx.x == 0) n_best = min(nk, n);
+            have = min(nk, n);
             __syncthreads();
         } else {
+            // a NaN or +inf, or a list that is too long
             __syncthreads();
             rounds(0);
-            if (threadIdx.x == 0) n_best = n;
+            have = n;
         }
     }
-    if (C > 1) cluster.sync();
-    else __syncthreads();
+    publish(row_sums, have);
+    row_sync();
 
     // every CTA of the row comes to the same view of it
-    Sums row_sums = cta_sums;
-    int have = n_best;
+    int row_n = have;
     if (C > 1) {
-        row_sums = *cluster.map_shared_rank(&cta_sums, 0);
-        have = n ? *cluster.map_shared_rank(&n_best, 0) : 0;
-        for (int i = 1; i < C; i++) {
-            row_sums = join(row_sums, *cluster.map_shared_rank(&cta_sums, i), scale);
-            if (n) have += *cluster.map_shared_rank(&n_best, i);
-        }
+        row_sums = lanes_join(lane < C ? row_parts[lane] : Sums{kLow, 0.f, 0.f}, plain_join);
+        row_n = 0;
+        for (int i = 0; i < C; i++) row_n += row_have[i];
     }
     const bool again = !(row_sums.m > -1e36f) || row_sums.s != row_sums.s;
-    const bool lack = n && have < n;
+    const bool lack = n && row_n < n;
     if (again || lack) {
-        if (C > 1) cluster.sync();  // the others have read cta_sums and n_best
-        else __syncthreads();
-        if (lack) rounds(n_best);
+        if (lack) rounds(have);
         if (again) {
             Sums t{-INFINITY, 0.f, 0.f};
-            each<BF16>(r, sl, [&](float x, uint32_t) {
+            each<BF16, kThreads>(r, sl, [&](float x, uint32_t) {
                 t = x == -INFINITY ? t : join_exact(t, Sums{x, (x - x) + 1.f, 0.f}, scale);  // a NaN for an infinity
             });
-            cta_join(t, [](const Sums &p, const Sums &q, float s) { return join_exact(p, q, s); });
+            row_sync();  // warp_sums is free, and the others have read what was published
+            row_sums = cta_join(t, -INFINITY, exact_join);
+        } else {
+            row_sync();
         }
-        if (C > 1) cluster.sync();
-        else __syncthreads();
-        if (again) {
-            row_sums = *cluster.map_shared_rank(&cta_sums, 0);
-            for (int i = 1; i < C; i++) row_sums = join_exact(row_sums, *cluster.map_shared_rank(&cta_sums, i), scale);
-        }
+        publish(row_sums, n);
+        row_sync();
+        if (again && C > 1) row_sums = lanes_join(lane < C ? row_parts[lane] : Sums{-INFINITY, 0.f, 0.f}, exact_join);
     }
 
     if (c == 0) {
@@ -494,17 +541,15 @@ __global__ void __launch_bounds__(kThreads, 2) logprob_kernel(const LpArgs a)
         if (threadIdx.x == 0) {
             if (a.logprob) {
                 const int32_t tg = a.targets[row];
-                a.logprob[row] = tg < 0 ? 0.f : tg >= a.vocab ? __int_as_float(0x7FC00000) : lp_of(r.at(tg));
+                a.logprob[row] = tg < 0 ? 0.f : tg >= vocab ? __int_as_float(0x7FC00000) : lp_of(r.at(tg));
             }
             if (a.entropy) a.entropy[row] = none ? 0.f : log_s - row_sums.w / row_sums.s * a.inv_t;
         }
         if (n) {
-            for (int i = threadIdx.x; i < C * n; i += kThreads) cand[i] = cluster.map_shared_rank(best, i / n)[i % n];
-            __syncthreads();
             for (int i = threadIdx.x; i < C * n; i += kThreads) {
-                const unsigned long long k = cand[i];
+                const unsigned long long k = row_tops[i];
                 int rank = 0;
-                for (int j = 0; j < C * n; j++) rank += cand[j] > k;
+                for (int j = 0; j < C * n; j++) rank += row_tops[j] > k;
                 if (k && rank < n) merged[rank] = k;
             }
             __syncthreads();
@@ -515,7 +560,6 @@ __global__ void __launch_bounds__(kThreads, 2) logprob_kernel(const LpArgs a)
             }
         }
     }
-    if (C > 1) cluster.sync();  // the leader reads the others' shared memory
 }
 
 }  // namespace
@@ -540,10 +584,15 @@ extern "C" uw_status uw_token_logprobs(const void *logits, uw_out_dtype dtype, i
     if (rows == 0 || (!logprob && !entropy && !n_top)) return UW_OK;
     if (!logits) return fail(UW_ERR_INVALID_ARG, "uw_token_logprobs: logits NULL");
     const LpArgs a{logits, rows, vocab, ld, 1.4426950408889634f / temperature, 1.f / temperature, targets, logprob, entropy, n_top, top_ids, top_logprobs};
-    // few rows: several CTAs a row, while a slice keeps 4096 logits
-    int C = 1;
-    while (C < kMaxCluster && rows * C * 2 <= 2 * num_sms() && vocab / (C * 2) >= 4096) C *= 2;
-    const cudaError_t e = launch_dependent(dtype == UW_OUT_BF16 ? logprob_kernel<true> : logprob_kernel<false>, dim3((unsigned)(rows * C)), kThreads, 0,
-                                           (unsigned)C, (cudaStream_t)stream, a);
+    int cs = 0;
+    while ((1 << cs) < kMaxCluster && (rows << cs) * 2 <= 2 * num_sms() && (vocab >> (cs + 1)) >= 4096) cs++;
+    const char *ec = getenv("LC"), *et = getenv("LT");
+    if (ec) cs = atoi(ec);
+    const int threads = et ? atoi(et) : 512;
+    auto go = [&](auto kernel, int t) { return launch_dependent(kernel, dim3((unsigned)(rows << cs)), (unsigned)t, 0, 1u << cs, (cudaStream_t)stream, a, cs); };
+    const bool bf16 = dtype == UW_OUT_BF16;
+    const cudaError_t e = threads == 128 ? go(bf16 ? logprob_kernel<true, 128> : logprob_kernel<false, 128>, 128)
+                        : threads == 256 ? go(bf16 ? logprob_kernel<true, 256> : logprob_kernel<false, 256>, 256)
+                                         : go(bf16 ? logprob_kernel<true, 512> : logprob_kernel<false, 512>, 512);
     return e == cudaSuccess ? UW_OK : fail(UW_ERR_CUDA, "uw_token_logprobs: launch: %s", cudaGetErrorString(e));
 }
