@@ -12,18 +12,18 @@
 // slices' sums and candidates through distributed shared memory in a fixed order.
 //
 // Top tokens in the same pass: from the maxima of the threads over the slice's first eighth comes a bound that at least n
-// of its logits reach; logits at or above it are listed (those of the first eighth in a second look at it), a few
-// hundred of an ordinary row.  The threads' final maxima give a closer bound, and each remaining one's rank is the number
-// of larger keys (logit order above the complement of the index, so equal logits go by the lower index).  A slice in
-// which fewer than n logits are not masked lists all of these.  Where too many reach the bound (many equal logits), in a
-// row with a NaN or an infinity, and where a row has fewer than n unmasked logits, rounds of an exact maximum find the rest.
+// of its logits reach.  Groups of four loads that hold a logit at or above it are noted, a few dozen of an ordinary row,
+// and looked through at the end; each listed logit's rank is the number of larger keys (logit order above the complement of
+// the index, so equal logits go by the lower index).  A long list is first cut by the bound of the threads' final maxima.
+// A slice in which fewer than n logits are not masked lists all of these.  Where too many reach the bound (many equal
+// logits), in a row with a NaN or an infinity, and where a row has fewer than n unmasked logits, rounds of an exact maximum
+// find the rest.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cmath>
-#include <type_traits>
 
 #include "launch.cuh"
 #include "uw_internal.h"
@@ -34,7 +34,8 @@ using namespace uw;
 namespace {
 
 constexpr int kMaxTop = 32;
-constexpr int kCand = 2048;
+constexpr int kCand = 1024;            // logits listed for the top tokens
+constexpr int kGroups = 1024;          // groups of loads that hold one
 constexpr int kUnroll = 4;             // 16-byte loads of a thread on their way
 constexpr float kLow = -1e37f;         // masked logits count as this, or in bf16 as the next value below it
 constexpr int kMaxCluster = 8;
@@ -282,6 +283,32 @@ __device__ __forceinline__ unsigned long long warp_max(unsigned long long k)
     return k;
 }
 
+// What few threads come to stays out of line: the kernel's own code has to fit the instruction cache (with these inline,
+// waits for instructions were a third of its time on short rows).
+
+// this thread's largest key below `last`
+template <bool BF16, int THREADS>
+__device__ __noinline__ unsigned long long largest_below(const Row<BF16> r, const Slice s, unsigned long long last)
+{
+    unsigned long long k = 0ull;
+    each<BF16, THREADS>(r, s, [&](float x, uint32_t i) {
+        const unsigned long long o = key_of(x, i);
+        if (o < last && o > k) k = o;
+    });
+    return k;
+}
+
+// this thread's sums, exactly: a NaN for an infinity, nothing for a masked token
+template <bool BF16, int THREADS>
+__device__ __noinline__ Sums exact_sums(const Row<BF16> r, const Slice s, float scale)
+{
+    Sums t{-INFINITY, 0.f, 0.f};
+    each<BF16, THREADS>(r, s, [&](float x, uint32_t) {
+        if (x != -INFINITY) t = join_exact(t, Sums{x, (x - x) + 1.f, 0.f}, scale);
+    });
+    return t;
+}
+
 // A bound that at least n of the values behind the threads' maxima reach, and few more: the warps whose lanes all have
 // one (the first `full`) bring a few of their largest each, and the n-th largest of these is it; -inf without such a warp.
 template <int kWarps>
@@ -324,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
     __shared__ float bounds[64];
     __shared__ unsigned long long cand[kCand], best[kMaxTop], merged[kMaxTop];
     __shared__ uint16_t kept[kCand];
-    __shared__ int n_cand, n_kept;
+    __shared__ int groups[kGroups], n_groups, n_cand, n_kept;
     // written by the row's CTAs: their sums and counts in each, their top tokens in the leader
     __shared__ Sums row_parts[kMaxCluster];
     __shared__ int row_have[kMaxCluster];
@@ -339,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
     const int n = a.n_top;
     const float scale = a.scale;
 
-    if (threadIdx.x == 0) n_cand = n_kept = 0;
+    if (threadIdx.x == 0) n_groups = n_cand = n_kept = 0;
     pdl_trigger();
     __syncthreads();
     pdl_wait();
@@ -372,17 +399,23 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
         if (C > 1) cluster.sync();
         else __syncthreads();
     };
+    static_assert(kUnroll * V <= 32, "a group's elements");
     static_assert(kWarps <= 32, "the join of the warps' sums");
 
     PairSums sums;
     float bound = INFINITY;
+    // a thread's group of loads, from vector v, holds a logit that reaches the bound
+    auto note = [&](int v) {
+        const int at = atomicAdd(&n_groups, 1);
+        if (at < kGroups) groups[at] = v;
+    };
     auto list = [&](float x, int i) {
         const int at = atomicAdd(&n_cand, 1);
         if (at < kCand) cand[at] = key_of(x, (uint32_t)i);
     };
-    // the sums over vectors [v, v1), kThreads apart, and the list of those that reach the bound
-    auto sweep = [&](int v, int v1, auto collect) {
-        constexpr uint32_t kPad = BF16 ? 0xFCF1FCF1u : 0xFCF0BDC2u;  // kLow, as raised: adds nothing and is not listed
+    constexpr uint32_t kPad = BF16 ? 0xFCF1FCF1u : 0xFCF0BDC2u;  // kLow, as raised: adds nothing and is not listed
+    // the sums over vectors [v, v1), kThreads apart, in groups
+    auto sweep = [&](int v, int v1) {
         uint4 next[kUnroll];
         auto load = [&](int at) {
 #pragma unroll
@@ -403,16 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
                 Row<BF16>::split(x[u], f);
                 sums.add(f, scale);
             }
-            if (decltype(collect)::value && mx >= bound) {
-#pragma unroll
-                for (int u = 0; u < kUnroll; u++) {
-                    float f[V];
-                    Row<BF16>::split(x[u], f);
-#pragma unroll
-                    for (int i = 0; i < V; i++)
-                        if (f[i] >= bound) list(f[i], sl.head + (v + u * kThreads) * V + i);
-                }
-            }
+            if (mx >= bound) note(v);
         }
     };
     const int nv = sl.v1 - sl.v0;
@@ -421,35 +445,19 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
         constexpr int kStep = kUnroll * kThreads;
         const int first = min(nv, (nv / 8 + kStep - 1) / kStep * kStep);
         done = sl.v0 + first;
-        sweep(sl.v0 + threadIdx.x, done, std::false_type());
+        sweep(sl.v0 + threadIdx.x, done);
         bound = bound_of<kWarps>(sums.m, min(kWarps, first / 32), n, bounds);
         // no bound above the masked logits: every logit above them is listed
-        const float above = BF16 ? __uint_as_float(0xFCF00000u) : __uint_as_float(__float_as_uint(kLow) - 1);
-        bound = fmaxf(bound, above);
-        for (int v = sl.v0 + threadIdx.x; v < done; v += kStep) {
-            uint4 x[kUnroll];
-#pragma unroll
-            for (int u = 0; u < kUnroll; u++)
-                if (v + u * kThreads < done) x[u] = r.load(sl.head + (v + u * kThreads) * V);
-#pragma unroll
-            for (int u = 0; u < kUnroll; u++) {
-                if (v + u * kThreads >= done) break;
-                float f[V];
-                Row<BF16>::split(x[u], f);
-#pragma unroll
-                for (int i = 0; i < V; i++)
-                    if (f[i] >= bound) list(f[i], sl.head + (v + u * kThreads) * V + i);
-            }
-        }
-        sweep(done + threadIdx.x, sl.v1, std::true_type());
-    } else {
-        sweep(done + threadIdx.x, sl.v1, std::false_type());
+        bound = fmaxf(bound, BF16 ? __uint_as_float(0xFCF00000u) : __uint_as_float(__float_as_uint(kLow) - 1));
+        if (sums.m >= bound)
+            for (int v = sl.v0 + threadIdx.x; v < done; v += kStep) note(v);
     }
+    sweep(done + threadIdx.x, sl.v1);
     const float vec_max = sums.m;  // over whole vectors alone
     auto single = [&](int i) {
         const float x = r.at(i);
         sums.add1(clamp_low(x), scale);
-        if (n && x >= bound) list(x, i);
+        if (x >= bound) list(x, i);
     };
     for (int i = threadIdx.x; i < sl.s1; i += kThreads) single(i);
     for (int i = sl.t0 + threadIdx.x; i < sl.t1; i += kThreads) single(i);
@@ -462,12 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
     auto rounds = [&](int from) {
         unsigned long long last = from ? best[from - 1] : ~0ull;
         for (int j = from; j < n; j++) {
-            unsigned long long k = 0ull;
-            each<BF16, kThreads>(r, sl, [&](float x, uint32_t i) {
-                const unsigned long long o = key_of(x, i);
-                if (o < last && o > k) k = o;
-            });
-            k = warp_max(k);
+            unsigned long long k = warp_max(largest_below<BF16, kThreads>(r, sl, last));
             __syncthreads();  // cand is free
             if (lane == 0) cand[warp] = k;
             __syncthreads();
@@ -481,8 +484,22 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
     };
     if (n) {
         if ((int)threadIdx.x < kMaxTop) best[threadIdx.x] = 0ull;
+        const int ng = n_groups;
+        bool listed = row_sums.s == row_sums.s && ng <= kGroups;  // no NaN, no +inf
+        if (listed) {
+            // a warp takes a group, a lane an element
+            for (int g = warp; g < ng; g += kWarps) {
+                const int v = groups[g] + lane / V * kThreads, i = sl.head + v * V + lane % V;
+                if (lane < kUnroll * V && v < sl.v1) {
+                    const float x = r.at(i);
+                    if (x >= bound) list(x, i);
+                }
+            }
+            __syncthreads();
+        }
         const int nc = n_cand;
-        if (row_sums.s == row_sums.s && nc <= kCand) {
+        listed = listed && nc <= kCand;
+        if (listed) {
             // the closer bound, where the list is long
             const float b2 = nc > 256 ? bound_of<kWarps>(vec_max, min(kWarps, nv / 32), n, bounds) : -INFINITY;
             const unsigned long long kb = b2 > bound ? key_of(b2, 0xFFFFFFFFu) : 0ull;
@@ -520,10 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
     if (again || lack) {
         if (lack) rounds(have);
         if (again) {
-            Sums t{-INFINITY, 0.f, 0.f};
-            each<BF16, kThreads>(r, sl, [&](float x, uint32_t) {
-                t = x == -INFINITY ? t : join_exact(t, Sums{x, (x - x) + 1.f, 0.f}, scale);  // a NaN for an infinity
-            });
+            const Sums t = exact_sums<BF16, kThreads>(r, sl, scale);
             row_sync();  // warp_sums is free, and the others have read what was published
             row_sums = cta_join(t, -INFINITY, exact_join);
         } else {
@@ -584,11 +598,12 @@ extern "C" uw_status uw_token_logprobs(const void *logits, uw_out_dtype dtype, i
     if (rows == 0 || (!logprob && !entropy && !n_top)) return UW_OK;
     if (!logits) return fail(UW_ERR_INVALID_ARG, "uw_token_logprobs: logits NULL");
     const LpArgs a{logits, rows, vocab, ld, 1.4426950408889634f / temperature, 1.f / temperature, targets, logprob, entropy, n_top, top_ids, top_logprobs};
+    // Few rows: a cluster of CTAs a row, while the rows fill the GPU at most and a slice keeps 4096 logits (1 row of 128256:
+    // 20 us alone, 11 with eight).  Many rows: smaller CTAs, whose fixed part costs less, as soon as their number fills the
+    // SMs' 1024 threads (2047 rows of 32064 bf16: 42 us with 512 threads, 31 with 256, 27 with 128).
     int cs = 0;
-    while ((1 << cs) < kMaxCluster && (rows << cs) * 2 <= 2 * num_sms() && (vocab >> (cs + 1)) >= 4096) cs++;
-    const char *ec = getenv("LC"), *et = getenv("LT");
-    if (ec) cs = atoi(ec);
-    const int threads = et ? atoi(et) : 512;
+    while ((1 << cs) < kMaxCluster && (rows << (cs + 1)) <= 2 * num_sms() && (vocab >> (cs + 1)) >= 4096) cs++;
+    const int threads = (rows << cs) <= 2 * num_sms() ? 512 : rows <= 4 * num_sms() ? 256 : 128;
     auto go = [&](auto kernel, int t) { return launch_dependent(kernel, dim3((unsigned)(rows << cs)), (unsigned)t, 0, 1u << cs, (cudaStream_t)stream, a, cs); };
     const bool bf16 = dtype == UW_OUT_BF16;
     const cudaError_t e = threads == 128 ? go(bf16 ? logprob_kernel<true, 128> : logprob_kernel<false, 128>, 128)

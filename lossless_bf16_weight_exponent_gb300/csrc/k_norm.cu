@@ -4,8 +4,14 @@
 // optionally o <- gate o; h' = a h + s o; optionally u = pre h' / rms(h').  Two sums of squares depend on each other
 // (the second needs the first), so a row is held on chip between them and each input is read once.
 //
-// One CTA per row.  Each thread holds kVec * chunks elements of o in registers; a row's sum of squares is joined
-// through shared memory in a fixed order.
+// One CTA per row, several rows on an SM.  A row's inputs are asked for at once, two chunks of eight elements a thread,
+// before the first of its two sums of squares; the weights, which all rows share, come when they are needed.  A join of a
+// sum takes one barrier, in a fixed order.  Rows of a multiple of 8 elements are read in 16-byte pieces, others in pairs or
+// single elements with neighbouring threads side by side.
+// Bound by memory: 4096 rows of 4096 bf16 with residual and pre-norm take 22.8 us (5.9 TB/s), with post-norm and gate too
+// 28.6; 8192 rows of 8192 fp32 136 us (6.9 TB/s); 4096 rows of 2048 joined from 8 expert rows each 36.3 us (6.0 TB/s).
+// One chunk a thread took 31.3 us in the second case, four 30.5; a persistent CTA that keeps the weights and asks for its
+// next row ahead 54, as its registers leave too few rows on an SM to hide the joins.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -29,31 +35,79 @@ struct NormArgs {
     uint16_t *u;
 };
 
-__device__ __forceinline__ float bf(uint32_t bits) { return __uint_as_float(bits << 16); }
+// eight elements as loaded: bf16 in a, fp32 in a and b
+template <bool F32>
+struct Raw {
+    uint4 a;
+};
+template <>
+struct Raw<true> {
+    uint4 a, b;
+};
 
-// eight elements at i of an fp32 or bf16 array, the first cnt of them (VEC: all, 16-byte aligned)
-template <bool VEC>
-__device__ __forceinline__ void load8(const void *p, int dtype, int64_t i, int cnt, float (&f)[8])
+// A thread's chunk c of a row of D elements is 8 / W pieces of W elements, blockDim pieces apart.
+template <int W>
+__device__ __forceinline__ int piece_at(int c, int j)
 {
-    if (VEC) {
-        if (dtype == UW_OUT_BF16) {
-            const uint4 v = *(const uint4 *)((const uint16_t *)p + i);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    return ((c * (8 / W) + j) * (int)blockDim.x + (int)threadIdx.x) * W;
+}
+
+// zeros past the row's end, or where !in
+template <int W, bool F32>
+__device__ __forceinline__ Raw<F32> load8(const void *p, int64_t row, int D, int c, bool in = true)
+{
+    Raw<F32> r;
+    const uint8_t *base = (const uint8_t *)p + row * D * (F32 ? 4 : 2);
+    if constexpr (W == 8) {
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        const int i = piece_at<W>(c, 0);
+        const uint4 *q = (const uint4 *)(base + (int64_t)i * (F32 ? 4 : 2));
+        in = in && i < D;
+        r.a = in ? q[0] : zero;
+        if constexpr (F32) r.b = in ? q[1] : zero;
+    } else {
+        uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-            for (int q = 0; q < 4; q++) {
-                f[2 * q] = __uint_as_float(w[q] << 16);
-                f[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
+        for (int j = 0; j < 8 / W; j++) {
+            const int i = piece_at<W>(c, j);
+            if (!in || i >= D) continue;
+            if constexpr (F32 && W == 2) {
+                const uint2 v = *(const uint2 *)(base + (int64_t)i * 4);
+                w[2 * j] = v.x;
+                w[2 * j + 1] = v.y;
+            } else if constexpr (F32) {
+                w[j] = *(const uint32_t *)(base + (int64_t)i * 4);
+            } else if constexpr (W == 2) {
+                w[j] = *(const uint32_t *)(base + (int64_t)i * 2);
+            } else {
+                w[j >> 1] |= (uint32_t) * (const uint16_t *)(base + (int64_t)i * 2) << (16 * (j & 1));
             }
-        } else {
-            const float4 a = *(const float4 *)((const float *)p + i), b = *(const float4 *)((const float *)p + i + 4);
-            f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-            f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
         }
-        return;
+        r.a = make_uint4(w[0], w[1], w[2], w[3]);
+        if constexpr (F32) r.b = make_uint4(w[4], w[5], w[6], w[7]);
     }
+    return r;
+}
+
+template <bool F32>
+__device__ __forceinline__ void unpack8(const Raw<F32> &r, float (&f)[8])
+{
+    const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
 #pragma unroll
-    for (int q = 0; q < 8; q++)
-        f[q] = q < cnt ? (dtype == UW_OUT_BF16 ? bf(((const uint16_t *)p)[i + q]) : ((const float *)p)[i + q]) : 0.f;
+    for (int q = 0; q < 4; q++) {
+        if constexpr (F32) {
+            f[q] = __uint_as_float(w[q]);
+        } else {
+            f[2 * q] = __uint_as_float(w[q] << 16);
+            f[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
+        }
+    }
+    if constexpr (F32) {
+        f[4] = __uint_as_float(r.b.x);
+        f[5] = __uint_as_float(r.b.y);
+        f[6] = __uint_as_float(r.b.z);
+        f[7] = __uint_as_float(r.b.w);
+    }
 }
 
 __device__ __forceinline__ uint32_t pack2(float a, float b)
@@ -62,124 +116,191 @@ __device__ __forceinline__ uint32_t pack2(float a, float b)
     return *(const uint32_t *)&v;
 }
 
-template <bool VEC>
-__device__ __forceinline__ void store8(void *p, int dtype, int64_t i, int cnt, const float (&f)[8])
+template <int W, bool F32>
+__device__ __forceinline__ void store8(void *p, int64_t row, int D, int c, const float (&f)[8])
 {
-    if (VEC) {
-        if (dtype == UW_OUT_BF16) {
-            *(uint4 *)((uint16_t *)p + i) = make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
-        } else {
-            *(float4 *)((float *)p + i) = make_float4(f[0], f[1], f[2], f[3]);
-            *(float4 *)((float *)p + i + 4) = make_float4(f[4], f[5], f[6], f[7]);
-        }
-        return;
-    }
+    uint8_t *base = (uint8_t *)p + row * D * (F32 ? 4 : 2);
 #pragma unroll
-    for (int q = 0; q < 8; q++)
-        if (q < cnt) {
-            if (dtype == UW_OUT_BF16) ((__nv_bfloat16 *)p)[i + q] = __float2bfloat16_rn(f[q]);
-            else ((float *)p)[i + q] = f[q];
+    for (int j = 0; j < 8 / W; j++) {
+        const int i = piece_at<W>(c, j);
+        if (i >= D) continue;
+        if constexpr (F32) {
+            float *q = (float *)(base + (int64_t)i * 4);
+            if constexpr (W == 8) {
+                *(float4 *)q = make_float4(f[0], f[1], f[2], f[3]);
+                *(float4 *)(q + 4) = make_float4(f[4], f[5], f[6], f[7]);
+            } else if constexpr (W == 2) {
+                *(float2 *)q = make_float2(f[2 * j], f[2 * j + 1]);
+            } else {
+                *q = f[j];
+            }
+        } else {
+            uint8_t *q = base + (int64_t)i * 2;
+            if constexpr (W == 8) *(uint4 *)q = make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+            else if constexpr (W == 2) *(uint32_t *)q = pack2(f[2 * j], f[2 * j + 1]);
+            else *(__nv_bfloat16 *)q = __float2bfloat16_rn(f[j]);
         }
+    }
 }
 
-// the sum over the CTA, in a fixed order, to every thread
+// the sum over the CTA, in a fixed order, to every thread; red: a buffer of this call's own
 __device__ __forceinline__ float block_sum(float v, float *red)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
 #pragma unroll
     for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
     if (warps == 1) return v;
-    __syncthreads();
     if (lane == 0) red[warp] = v;
     __syncthreads();
-    float s = 0.f;
-    for (int w = 0; w < warps; w++) s += red[w];
+    float s = lane < warps ? red[lane] : 0.f;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
     return s;
 }
 
-// CH: chunks of 8 elements a thread holds (dim <= 8 CH blockDim)
-template <int CH, bool VEC>
-__global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a)
+// CH: chunks of 8 elements a thread holds (dim <= 8 CH blockDim); TOPK: y holds expert rows; W: elements of an access;
+// RF, BF: h and h_out, y in fp32
+template <int CH, int MAXT, bool TOPK, int W, bool RF, bool BF>
+__global__ void __launch_bounds__(MAXT) norm_kernel(const NormArgs a)
 {
-    __shared__ float red[32];
-    const int64_t D = a.n.dim;
+    __shared__ float red[2][32];
+    const int D = (int)a.n.dim;
     const int64_t row = blockIdx.x;
     pdl_trigger();
     pdl_wait();
     float o[CH][8];
-    float ss = 0.f;
-#pragma unroll
-    for (int c = 0; c < CH; c++) {
-        const int64_t i = 8 * ((int64_t)c * blockDim.x + threadIdx.x);
-        const int cnt = (int)max((int64_t)0, min((int64_t)8, D - i));
-#pragma unroll
-        for (int q = 0; q < 8; q++) o[c][q] = 0.f;
-        if (cnt <= 0 || !a.y) continue;
-        if (a.topk) {
-            for (int j = 0; j < a.topk; j++) {
-                const int64_t p = __ldg(a.pos + row * a.topk + j);
-                if (p < 0 || p >= a.y_rows) continue;
-                const float w = __ldg(a.weights + row * a.topk + j);
-                float f[8];
-                load8<VEC>(a.y, a.n.block_dtype, p * D + i, cnt, f);
-#pragma unroll
-                for (int q = 0; q < 8; q++) o[c][q] = fmaf(w, f[q], o[c][q]);
-            }
-        } else {
-            load8<VEC>(a.y, a.n.block_dtype, row * D + i, cnt, o[c]);
+    Raw<RF> h[CH];
+    if constexpr (TOPK) {
+        // lane j: place and weight of the row's j-th expert row
+        const int lane = threadIdx.x & 31;
+        int pos = -1;
+        float weight = 0.f;
+        if (lane < a.topk) {
+            pos = __ldg(a.pos + row * a.topk + lane);
+            weight = __ldg(a.weights + row * a.topk + lane);
         }
 #pragma unroll
-        for (int q = 0; q < 8; q++)
-            if (q < cnt) ss = fmaf(o[c][q], o[c][q], ss);
+        for (int c = 0; c < CH; c++) {
+            if (a.h) h[c] = load8<W, RF>(a.h, row, D, c);
+#pragma unroll
+            for (int q = 0; q < 8; q++) o[c][q] = 0.f;
+        }
+        constexpr int kB = CH <= 2 ? 4 : 1;  // expert rows on their way
+        for (int j0 = 0; j0 < a.topk; j0 += kB) {
+            Raw<BF> e[kB][CH];
+            float w[kB];
+#pragma unroll
+            for (int j = 0; j < kB; j++) {
+                const int p = __shfl_sync(0xFFFFFFFFu, pos, (j0 + j) & 31);
+                const bool in = j0 + j < a.topk && p >= 0 && p < a.y_rows;
+                w[j] = __shfl_sync(0xFFFFFFFFu, weight, (j0 + j) & 31);
+                if (!in) w[j] = 0.f;
+#pragma unroll
+                for (int c = 0; c < CH; c++) e[j][c] = load8<W, BF>(a.y, in ? p : 0, D, c, in);
+            }
+#pragma unroll
+            for (int j = 0; j < kB; j++)
+#pragma unroll
+                for (int c = 0; c < CH; c++) {
+                    float f[8];
+                    unpack8(e[j][c], f);
+#pragma unroll
+                    for (int q = 0; q < 8; q++) o[c][q] = fmaf(w[j], f[q], o[c][q]);
+                }
+        }
+    } else {
+        Raw<BF> y[CH];
+#pragma unroll
+        for (int c = 0; c < CH; c++) {
+            if (a.y) y[c] = load8<W, BF>(a.y, row, D, c);
+            if (a.h) h[c] = load8<W, RF>(a.h, row, D, c);
+        }
+#pragma unroll
+        for (int c = 0; c < CH; c++) {
+            if (a.y) unpack8(y[c], o[c]);
+            else
+#pragma unroll
+                for (int q = 0; q < 8; q++) o[c][q] = 0.f;
+        }
     }
-    float scale = a.n.out_scale;
-    if (a.n.post_weight) scale *= rsqrtf(block_sum(ss, red) / (float)D + a.n.eps);
-    ss = 0.f;
+    float scale = a.n.out_scale, ss = 0.f;
+    if (a.n.post_weight) {
+#pragma unroll
+        for (int c = 0; c < CH; c++)
+#pragma unroll
+            for (int q = 0; q < 8; q++) ss = fmaf(o[c][q], o[c][q], ss);  // zeros past the row's end
+        scale *= rsqrtf(block_sum(ss, red[0]) / (float)D + a.n.eps);
+        ss = 0.f;
+    }
 #pragma unroll
     for (int c = 0; c < CH; c++) {
-        const int64_t i = 8 * ((int64_t)c * blockDim.x + threadIdx.x);
-        const int cnt = (int)max((int64_t)0, min((int64_t)8, D - i));
-        if (cnt <= 0) continue;
         float f[8];
         if (a.n.post_weight) {
-            load8<VEC>(a.n.post_weight, UW_OUT_BF16, i, cnt, f);
+            unpack8(load8<W, false>(a.n.post_weight, 0, D, c), f);
 #pragma unroll
             for (int q = 0; q < 8; q++) o[c][q] *= f[q];
         }
         if (a.n.gate) {
-            load8<VEC>(a.n.gate, UW_OUT_BF16, row / a.n.gate_every * D + i, cnt, f);
+            unpack8(load8<W, false>(a.n.gate, row / a.n.gate_every, D, c), f);
 #pragma unroll
             for (int q = 0; q < 8; q++) o[c][q] *= f[q];
         }
-        if (a.h) load8<VEC>(a.h, a.n.res_dtype, row * D + i, cnt, f);
+        if (a.h) unpack8(h[c], f);
 #pragma unroll
         for (int q = 0; q < 8; q++) {
             float r = a.y ? scale * o[c][q] : 0.f;
             if (a.h) r = fmaf(a.n.res_scale, f[q], r);
             o[c][q] = r;
-            if (q < cnt) ss = fmaf(r, r, ss);
         }
-        if (a.h_out) store8<VEC>(a.h_out, a.n.res_dtype, row * D + i, cnt, o[c]);
+        if (a.h_out) store8<W, RF>(a.h_out, row, D, c, o[c]);
     }
     if (!a.u) return;
-    const float inv = rsqrtf(block_sum(ss, red) / (float)D + a.n.eps);
+#pragma unroll
+    for (int c = 0; c < CH; c++)
+#pragma unroll
+        for (int j = 0; j < 8 / W; j++)
+            if (piece_at<W>(c, j) < D)
+#pragma unroll
+                for (int q = 0; q < W; q++) ss = fmaf(o[c][W * j + q], o[c][W * j + q], ss);
+    const float inv = rsqrtf(block_sum(ss, red[1]) / (float)D + a.n.eps);
 #pragma unroll
     for (int c = 0; c < CH; c++) {
-        const int64_t i = 8 * ((int64_t)c * blockDim.x + threadIdx.x);
-        const int cnt = (int)max((int64_t)0, min((int64_t)8, D - i));
-        if (cnt <= 0) continue;
         float f[8];
-        load8<VEC>(a.n.pre_weight, UW_OUT_BF16, i, cnt, f);
+        unpack8(load8<W, false>(a.n.pre_weight, 0, D, c), f);
 #pragma unroll
         for (int q = 0; q < 8; q++) f[q] *= o[c][q] * inv;
-        store8<VEC>(a.u, UW_OUT_BF16, row * D + i, cnt, f);
+        store8<W, false>(a.u, row, D, c, f);
     }
 }
 
-template <int CH>
-cudaError_t launch_ch(const NormArgs &a, int threads, bool vec, cudaStream_t st)
+template <int CH, int MAXT, bool TOPK, int W>
+cudaError_t launch_width(const NormArgs &a, int threads, cudaStream_t st)
 {
-    return launch_dependent(vec ? norm_kernel<CH, true> : norm_kernel<CH, false>, dim3((unsigned)a.rows), (unsigned)threads, 0, 0, st, a);
+    const bool rf = a.n.res_dtype == UW_OUT_F32, bf = a.n.block_dtype == UW_OUT_F32;
+    auto kernel = rf ? (bf ? norm_kernel<CH, MAXT, TOPK, W, true, true> : norm_kernel<CH, MAXT, TOPK, W, true, false>)
+                     : (bf ? norm_kernel<CH, MAXT, TOPK, W, false, true> : norm_kernel<CH, MAXT, TOPK, W, false, false>);
+    return launch_dependent(kernel, dim3((unsigned)a.rows), (unsigned)threads, 0, 0, st, a);
+}
+
+template <int CH, int MAXT>
+cudaError_t launch_chunks(const NormArgs &a, int threads, cudaStream_t st)
+{
+    const int w = a.n.dim % 8 == 0 ? 8 : a.n.dim % 2 == 0 ? 2 : 1;
+    if (a.topk)
+        return w == 8 ? launch_width<CH, MAXT, true, 8>(a, threads, st)
+               : w == 2 ? launch_width<CH, MAXT, true, 2>(a, threads, st) : launch_width<CH, MAXT, true, 1>(a, threads, st);
+    return w == 8 ? launch_width<CH, MAXT, false, 8>(a, threads, st)
+           : w == 2 ? launch_width<CH, MAXT, false, 2>(a, threads, st) : launch_width<CH, MAXT, false, 1>(a, threads, st);
+}
+
+// two chunks a thread up to 1024 threads, then eight
+cudaError_t launch_norm(const NormArgs &a, cudaStream_t st)
+{
+    const int64_t chunks = (a.n.dim + 7) / 8;
+    const int ch = chunks <= 2048 ? 2 : 8;
+    const int threads = (int)(((chunks + ch - 1) / ch + 31) / 32 * 32);
+    if (ch == 2) return threads <= 512 ? launch_chunks<2, 512>(a, threads, st) : launch_chunks<2, 1024>(a, threads, st);
+    return launch_chunks<8, 1024>(a, threads, st);
 }
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
@@ -207,18 +328,6 @@ extern "C" uw_status uw_block_norm(const uw_norm *n, int64_t rows, const void *h
         return fail(UW_ERR_INVALID_ARG, "uw_block_norm: a pointer is not 16-byte aligned");
     if (rows == 0) return UW_OK;
     const NormArgs a{*n, rows, y_rows, h, y, h_out, pos, weights, topk, u};
-    const int64_t chunks = (n->dim + 7) / 8;
-    const bool vec = n->dim % 8 == 0;
-    cudaStream_t st = (cudaStream_t)stream;
-    // up to 512 threads of one chunk each, then more chunks a thread, then more threads
-    const int ch = chunks <= 512 ? 1 : chunks <= 1024 ? 2 : chunks <= 4096 ? 4 : 8;
-    const int threads = (int)(((chunks + ch - 1) / ch + 31) / 32 * 32);
-    cudaError_t e;
-    switch (ch) {
-    case 1: e = launch_ch<1>(a, threads, vec, st); break;
-    case 2: e = launch_ch<2>(a, threads, vec, st); break;
-    case 4: e = launch_ch<4>(a, threads, vec, st); break;
-    default: e = launch_ch<8>(a, threads, vec, st); break;
-    }
+    const cudaError_t e = launch_norm(a, (cudaStream_t)stream);
     return e == cudaSuccess ? UW_OK : fail(UW_ERR_CUDA, "uw_block_norm: launch: %s", cudaGetErrorString(e));
 }
