@@ -8,8 +8,8 @@
 // before the first of its two sums of squares; the weights, which all rows share, come when they are needed.  A join of a
 // sum takes one barrier, in a fixed order.  Rows of a multiple of 8 elements are read in 16-byte pieces, others in pairs or
 // single elements with neighbouring threads side by side.
-// Bound by memory: 4096 rows of 4096 bf16 with residual and pre-norm take 22.8 us (5.9 TB/s), with post-norm and gate too
-// 28.6; 8192 rows of 8192 fp32 136 us (6.9 TB/s); 4096 rows of 2048 joined from 8 expert rows each 36.3 us (6.0 TB/s).
+// Bound by memory: 4096 rows of 4096 bf16 with residual and pre-norm take 22.4 us (6.0 TB/s), with post-norm and gate too
+// 28.1; 8192 rows of 8192 fp32 137 us (6.9 TB/s); 4096 rows of 2048 joined from 8 expert rows each 37.1 us (5.9 TB/s).
 // One chunk a thread took 31.3 us in the second case, four 30.5; a persistent CTA that keeps the weights and asks for its
 // next row ahead 54, as its registers leave too few rows on an SM to hide the joins.
 #include <cuda_bf16.h>
@@ -161,7 +161,7 @@ __device__ __forceinline__ float block_sum(float v, float *red)
 // CH: chunks of 8 elements a thread holds (dim <= 8 CH blockDim); TOPK: y holds expert rows; W: elements of an access;
 // RF, BF: h and h_out, y in fp32
 template <int CH, int MAXT, bool TOPK, int W, bool RF, bool BF>
-__global__ void __launch_bounds__(MAXT) norm_kernel(const NormArgs a)
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) norm_kernel(const NormArgs a)
 {
     __shared__ float red[2][32];
     const int D = (int)a.n.dim;
@@ -299,6 +299,7 @@ cudaError_t launch_norm(const NormArgs &a, cudaStream_t st)
     const int64_t chunks = (a.n.dim + 7) / 8;
     const int ch = chunks <= 2048 ? 2 : 8;
     const int threads = (int)(((chunks + ch - 1) / ch + 31) / 32 * 32);
+    if (ch == 2 && threads <= 256) return launch_chunks<2, 256>(a, threads, st);
     if (ch == 2) return threads <= 512 ? launch_chunks<2, 512>(a, threads, st) : launch_chunks<2, 1024>(a, threads, st);
     return launch_chunks<8, 1024>(a, threads, st);
 }
