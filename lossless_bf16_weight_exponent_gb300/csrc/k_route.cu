@@ -1,14 +1,14 @@
 // k_route.cu - the router of a mixture of experts: each token's top-k experts, their weights, and the order of the
 // grouped products' rows (sm_103a).
 //
-// A warp takes a token.  A logit's sort key is its (logit + bias) mapped to an unsigned integer of the same order, above
-// the complement of its index, so that the k largest 64-bit keys are the k experts in the wanted order with ties to the
-// lower index; k rounds of a warp-wide maximum find them.
+// A warp takes a token.  A logit's sort key is its (logit + bias) mapped to an unsigned integer of the same order; a round
+// of the choice is a warp-wide maximum of the keys left and a warp-wide minimum of the experts that hold it, one
+// instruction each, so equal logits go to the lower index.
 //
-// Rows are ordered by (expert, token) without atomics on counters: a CTA of 128 tokens sets, for each expert, one bit
-// per token in shared memory (a token takes an expert at most once), so a token's rank within the CTA is a population
-// count and the CTA's rows per expert are another.  The second kernel adds up the counts of the CTAs before its own and
-// the offsets.  Up to 128 tokens one CTA does everything in one launch.
+// Rows are ordered by (expert, token) without counters whose order could change: a CTA sets, for each expert, one bit per
+// token in shared memory (a token takes an expert at most once), so a token's rank within the CTA is a population count
+// and the CTA's rows per expert are another.  The second kernel adds up the counts of the CTAs before its own and the
+// offsets.  Up to 128 tokens one CTA does everything in one launch; beyond, a CTA takes 64.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -22,8 +22,8 @@ using namespace uw;
 
 namespace {
 
-constexpr int kTok = 128;        // tokens per CTA
-constexpr int kThreads = 1024;
+constexpr int kTokOne = 128;     // tokens that one CTA takes alone
+constexpr int kTokMany = 64;     // and when there are more
 constexpr int kMaxE = 1024, kMaxTop = 16;
 
 struct RouteArgs {
@@ -50,19 +50,18 @@ __device__ __forceinline__ float logit_at(const RouteArgs &a, int64_t t, int e)
     return a.bf16 ? __bfloat162float(((const __nv_bfloat16 *)a.logits)[t * a.ld + e]) : ((const float *)a.logits)[t * a.ld + e];
 }
 
-// the choice of token t by one warp; chosen[j] in lane j; sets the token's bits
-template <int PER>  // experts per lane
-__device__ __forceinline__ void choose(const RouteArgs &a, int64_t t, int lane, uint32_t (*bits)[kTok / 32], int tl)
+// the choice of token t by one warp; sets the token's bits (WORDS per expert)
+template <int PER, int WORDS>  // PER: experts per lane
+__device__ __forceinline__ void choose(const RouteArgs &a, int64_t t, int lane, uint32_t *bits, int tl)
 {
     const int E = a.r.experts, k = a.r.topk;
     float z[PER];
-    unsigned long long key[PER];
+    uint32_t key[PER];  // 0: none, or taken
 #pragma unroll
     for (int i = 0; i < PER; i++) {
         const int e = lane + 32 * i;
         z[i] = e < E ? logit_at(a, t, e) : -INFINITY;
-        const float s = e < E && a.r.bias ? z[i] + __ldg(a.r.bias + e) : z[i];
-        key[i] = e < E ? ((unsigned long long)order_key(s) << 32) | (uint32_t)~e : 0ull;
+        key[i] = e < E ? order_key(a.r.bias ? z[i] + __ldg(a.r.bias + e) : z[i]) : 0u;
     }
     float m = -INFINITY, total = 1.f;
     if (a.r.score == UW_SCORE_SOFTMAX) {
@@ -80,22 +79,22 @@ __device__ __forceinline__ void choose(const RouteArgs &a, int64_t t, int lane, 
     int my_e = 0;
     float my_z = 0.f;
     for (int j = 0; j < k; j++) {
-        unsigned long long best = 0ull;
+        uint32_t best = 0u;
+        int first = 0;
 #pragma unroll
-        for (int i = 0; i < PER; i++) best = key[i] > best ? key[i] : best;
-        unsigned long long all = best;
-#pragma unroll
-        for (int d = 16; d; d >>= 1) {
-            const unsigned long long o = __shfl_xor_sync(0xFFFFFFFFu, all, d);
-            all = o > all ? o : all;
-        }
-        const int e = (int)~(uint32_t)all;
+        for (int i = PER - 1; i >= 0; i--)
+            if (key[i] >= best) {
+                best = key[i];
+                first = i;
+            }
+        const uint32_t all = __reduce_max_sync(0xFFFFFFFFu, best);
+        const int e = (int)__reduce_min_sync(0xFFFFFFFFu, best == all ? (uint32_t)(lane + 32 * first) : 0xFFFFFFFFu);
         float ze = 0.f;
 #pragma unroll
         for (int i = 0; i < PER; i++)
-            if (key[i] == all) {
+            if (lane + 32 * i == e) {
                 ze = z[i];
-                key[i] = 0ull;
+                key[i] = 0u;
             }
         ze = __shfl_sync(0xFFFFFFFFu, ze, e & 31);
         if (lane == j) {
@@ -117,25 +116,16 @@ __device__ __forceinline__ void choose(const RouteArgs &a, int64_t t, int lane, 
     if (lane < k) {
         a.ids[t * k + lane] = my_e;
         a.weights[t * k + lane] = w * a.r.scale;
-        atomicOr(&bits[my_e][tl >> 5], 1u << (tl & 31));
+        atomicOr(&bits[my_e * WORDS + (tl >> 5)], 1u << (tl & 31));
     }
 }
 
-__device__ __forceinline__ void choose_any(const RouteArgs &a, int64_t t, int lane, uint32_t (*bits)[kTok / 32], int tl)
-{
-    const int E = a.r.experts;
-    if (E <= 32) choose<1>(a, t, lane, bits, tl);
-    else if (E <= 64) choose<2>(a, t, lane, bits, tl);
-    else if (E <= 128) choose<4>(a, t, lane, bits, tl);
-    else if (E <= 256) choose<8>(a, t, lane, bits, tl);
-    else choose<32>(a, t, lane, bits, tl);
-}
-
+template <int WORDS>
 __device__ __forceinline__ int bits_count(const uint32_t *b)
 {
     int n = 0;
 #pragma unroll
-    for (int i = 0; i < kTok / 32; i++) n += __popc(b[i]);
+    for (int i = 0; i < WORDS; i++) n += __popc(b[i]);
     return n;
 }
 
@@ -147,98 +137,126 @@ __device__ __forceinline__ int bits_rank(const uint32_t *b, int tl)
     return n;
 }
 
-// exclusive scan of v over the CTA's 1024 threads; returns the total
-__device__ __forceinline__ int block_scan(int &v, int *wsum)
+// v[0..E) in shared memory becomes its exclusive sum; returns the total.  Begins and ends with a barrier.
+template <int THREADS>
+__device__ __forceinline__ int exclusive_sum(int *v, int E, int *wsum)
 {
+    constexpr int Q = kMaxE / THREADS;  // consecutive values of a thread
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int s = v;
+    __syncthreads();
+    int x[Q], s = 0;
+#pragma unroll
+    for (int i = 0; i < Q; i++) {
+        x[i] = Q * (int)threadIdx.x + i < E ? v[Q * threadIdx.x + i] : 0;
+        s += x[i];
+    }
+    int sum = s;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xFFFFFFFFu, s, d);
-        if (lane >= d) s += o;
+        const int o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+        if (lane >= d) sum += o;
     }
-    if (lane == 31) wsum[warp] = s;
+    if (lane == 31) wsum[warp] = sum;
     __syncthreads();
-    int before = 0, all = 0;
-    for (int w = 0; w < kThreads / 32; w++) {
-        if (w < warp) before += wsum[w];
-        all += wsum[w];
+    int w = lane < THREADS / 32 ? wsum[lane] : 0;
+    const int mine = lane < warp ? w : 0;
+    int at = sum - s + __reduce_add_sync(0xFFFFFFFFu, mine);
+    const int total = __reduce_add_sync(0xFFFFFFFFu, w);
+#pragma unroll
+    for (int i = 0; i < Q; i++) {
+        if (Q * (int)threadIdx.x + i < E) v[Q * threadIdx.x + i] = at;
+        at += x[i];
     }
-    v = before + s - v;
-    return all;
+    __syncthreads();
+    return total;
 }
 
-__global__ void __launch_bounds__(kThreads) route_choose_kernel(const RouteArgs a)
+template <int PER, int TOK>
+__global__ void __launch_bounds__(8 * TOK) route_choose_kernel(const RouteArgs a)
 {
-    __shared__ uint32_t bits[kMaxE][kTok / 32];
+    constexpr int kThreads = 8 * TOK, WORDS = TOK / 32;  // a warp for each four tokens
+    extern __shared__ uint32_t bits[];                   // [experts][WORDS]
     const int E = a.r.experts, k = a.r.topk;
-    const int64_t t0 = (int64_t)blockIdx.x * kTok;
-    const int nt = (int)min((int64_t)kTok, a.tokens - t0);
-    for (int i = threadIdx.x; i < E * (kTok / 32); i += kThreads) (&bits[0][0])[i] = 0u;
+    const int64_t t0 = (int64_t)blockIdx.x * TOK;
+    const int nt = (int)min((int64_t)TOK, a.tokens - t0);
+    for (int i = threadIdx.x; i < E * WORDS; i += kThreads) bits[i] = 0u;
     pdl_trigger();
     pdl_wait();
     __syncthreads();
-    for (int tl = threadIdx.x >> 5; tl < nt; tl += kThreads / 32) choose_any(a, t0 + tl, threadIdx.x & 31, bits, tl);
+    for (int tl = threadIdx.x >> 5; tl < nt; tl += kThreads / 32) choose<PER, WORDS>(a, t0 + tl, threadIdx.x & 31, bits, tl);
     __syncthreads();
     if (gridDim.x > 1) {
-        if ((int)threadIdx.x < E) a.counts[(int64_t)blockIdx.x * E + threadIdx.x] = bits_count(bits[threadIdx.x]);
+        for (int e = threadIdx.x; e < E; e += kThreads) a.counts[(int64_t)blockIdx.x * E + e] = bits_count<WORDS>(bits + e * WORDS);
         return;
     }
     // all tokens are here: the order too
-    __shared__ int wsum[kThreads / 32], base[kMaxE];
-    int v = (int)threadIdx.x < E ? bits_count(bits[threadIdx.x]) : 0;
-    const int total = block_scan(v, wsum);
-    if ((int)threadIdx.x < E) {
-        base[threadIdx.x] = v;
-        a.offsets[threadIdx.x] = v;
-    }
+    __shared__ int wsum[32], base[kMaxE];
+    for (int e = threadIdx.x; e < E; e += kThreads) base[e] = bits_count<WORDS>(bits + e * WORDS);
+    const int total = exclusive_sum<kThreads>(base, E, wsum);
+    for (int e = threadIdx.x; e < E; e += kThreads) a.offsets[e] = base[e];
     if (threadIdx.x == 0) a.offsets[E] = total;
-    __syncthreads();
     for (int i = threadIdx.x; i < nt * k; i += kThreads) {
         const int tl = i / k, e = a.ids[i];
-        const int r = base[e] + bits_rank(bits[e], tl);
+        const int r = base[e] + bits_rank(bits + e * WORDS, tl);
         a.pos[i] = r;
         a.row_src[r] = tl;
     }
 }
 
-__global__ void __launch_bounds__(kThreads) route_order_kernel(const RouteArgs a, int ctas)
+__global__ void __launch_bounds__(8 * kTokMany) route_order_kernel(const RouteArgs a, int ctas)
 {
-    __shared__ uint32_t bits[kMaxE][kTok / 32];
-    __shared__ int wsum[kThreads / 32], base[kMaxE];
+    constexpr int kThreads = 8 * kTokMany, WORDS = kTokMany / 32;
+    extern __shared__ uint32_t bits[];  // [experts][WORDS]
+    __shared__ int wsum[32], base[kMaxE], before[kMaxE];
     const int E = a.r.experts, k = a.r.topk;
-    const int64_t t0 = (int64_t)blockIdx.x * kTok;
-    const int nt = (int)min((int64_t)kTok, a.tokens - t0);
-    for (int i = threadIdx.x; i < E * (kTok / 32); i += kThreads) (&bits[0][0])[i] = 0u;
+    const int64_t t0 = (int64_t)blockIdx.x * kTokMany;
+    const int nt = (int)min((int64_t)kTokMany, a.tokens - t0);
+    for (int i = threadIdx.x; i < E * WORDS; i += kThreads) bits[i] = 0u;
+    for (int e = threadIdx.x; e < E; e += kThreads) base[e] = before[e] = 0;
     pdl_trigger();
-    pdl_wait();
-    // rows of each expert in all CTAs, and in those before this one
-    int all = 0, before = 0;
-    if ((int)threadIdx.x < E)
-        for (int c = 0; c < ctas; c++) {
-            const int n = __ldg(a.counts + (int64_t)c * E + threadIdx.x);
-            all += n;
-            if (c < (int)blockIdx.x) before += n;
-        }
     __syncthreads();
+    pdl_wait();
+    // rows of each expert in all CTAs, and in those before this one: the threads beyond one for each expert share the CTAs
+    const int parts = max(1, kThreads / E);
+    for (int i = threadIdx.x; i < E * parts; i += kThreads) {
+        const int e = i % E, part = i / E;
+        int all = 0, mine = 0;
+#pragma unroll 8
+        for (int c = part; c < ctas; c += parts) {
+            const int n = __ldg(a.counts + (int64_t)c * E + e);
+            all += n;
+            mine += c < (int)blockIdx.x ? n : 0;
+        }
+        if (all) atomicAdd(&base[e], all);
+        if (mine) atomicAdd(&before[e], mine);
+    }
     for (int i = threadIdx.x; i < nt * k; i += kThreads) {
         const int tl = i / k;
-        atomicOr(&bits[a.ids[t0 * k + i]][tl >> 5], 1u << (tl & 31));
+        atomicOr(&bits[a.ids[t0 * k + i] * WORDS + (tl >> 5)], 1u << (tl & 31));
     }
-    int v = all;
-    const int total = block_scan(v, wsum);
-    if ((int)threadIdx.x < E) {
-        base[threadIdx.x] = v + before;
-        if (blockIdx.x == 0) a.offsets[threadIdx.x] = v;
+    const int total = exclusive_sum<kThreads>(base, E, wsum);
+    if (blockIdx.x == 0) {
+        for (int e = threadIdx.x; e < E; e += kThreads) a.offsets[e] = base[e];
+        if (threadIdx.x == 0) a.offsets[E] = total;
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[E] = total;
-    __syncthreads();
     for (int i = threadIdx.x; i < nt * k; i += kThreads) {
         const int tl = i / k, e = a.ids[t0 * k + i];
-        const int r = base[e] + bits_rank(bits[e], tl);
+        const int r = base[e] + before[e] + bits_rank(bits + e * WORDS, tl);
         a.pos[t0 * k + i] = r;
         a.row_src[r] = (int32_t)(t0 + tl);
     }
+}
+
+template <int TOK>
+cudaError_t launch_choose(const RouteArgs &a, int64_t ctas, cudaStream_t st)
+{
+    const int E = a.r.experts;
+    auto kernel = E <= 32    ? route_choose_kernel<1, TOK>
+                  : E <= 64  ? route_choose_kernel<2, TOK>
+                  : E <= 128 ? route_choose_kernel<4, TOK>
+                  : E <= 256 ? route_choose_kernel<8, TOK>
+                             : route_choose_kernel<32, TOK>;
+    return launch_dependent(kernel, dim3((unsigned)ctas), 8 * TOK, (size_t)E * (TOK / 8), 0, st, a);
 }
 
 uw_status check_router(const uw_router *r, const char *who)
@@ -250,7 +268,7 @@ uw_status check_router(const uw_router *r, const char *who)
     return UW_OK;
 }
 
-int64_t route_ctas(int64_t tokens) { return (tokens + kTok - 1) / kTok; }
+int64_t route_ctas(int64_t tokens) { return tokens <= kTokOne ? 1 : (tokens + kTokMany - 1) / kTokMany; }
 
 }  // namespace
 
@@ -262,7 +280,7 @@ extern "C" uw_status uw_route_workspace_size(const uw_router *r, int64_t tokens,
     if (s != UW_OK) return s;
     if (tokens < 0 || tokens > (((int64_t)1 << 31) - 1024) / r->topk)
         return fail(UW_ERR_SHAPE, "uw_route_workspace_size: tokens=%lld", (long long)tokens);
-    *bytes = tokens <= kTok ? 0 : (size_t)route_ctas(tokens) * (size_t)r->experts * 4;
+    *bytes = tokens <= kTokOne ? 0 : (size_t)route_ctas(tokens) * (size_t)r->experts * 4;
     return UW_OK;
 }
 
@@ -283,7 +301,7 @@ extern "C" uw_status uw_route(const uw_router *r, const void *logits, uw_out_dty
         ((uintptr_t)logits & (dtype == UW_OUT_F32 ? 3 : 1)))
         return fail(UW_ERR_INVALID_ARG, "uw_route: a pointer is not aligned to its elements");
     const int64_t ctas = route_ctas(tokens);
-    const size_t need = tokens <= kTok ? 0 : (size_t)ctas * (size_t)r->experts * 4;
+    const size_t need = tokens <= kTokOne ? 0 : (size_t)ctas * (size_t)r->experts * 4;
     if (ws_bytes < need || (need && !ws)) return fail(UW_ERR_WORKSPACE, "uw_route: workspace %zu bytes, need %zu", ws_bytes, need);
     if ((uintptr_t)ws & 15) return fail(UW_ERR_INVALID_ARG, "uw_route: workspace not 16-byte aligned");
     const RouteArgs a{*r, logits, dtype == UW_OUT_BF16, tokens, ld, ids, weights, offsets, row_src, pos, (int32_t *)ws};
@@ -292,8 +310,9 @@ extern "C" uw_status uw_route(const uw_router *r, const void *logits, uw_out_dty
     if (tokens == 0) {
         e = cudaMemsetAsync(offsets, 0, ((size_t)r->experts + 1) * 4, st);
     } else {
-        e = launch_dependent(route_choose_kernel, dim3((unsigned)ctas), kThreads, 0, 0, st, a);
-        if (e == cudaSuccess && ctas > 1) e = launch_dependent(route_order_kernel, dim3((unsigned)ctas), kThreads, 0, 0, st, a, (int)ctas);
+        e = ctas == 1 ? launch_choose<kTokOne>(a, 1, st) : launch_choose<kTokMany>(a, ctas, st);
+        if (e == cudaSuccess && ctas > 1)
+            e = launch_dependent(route_order_kernel, dim3((unsigned)ctas), 8 * kTokMany, (size_t)r->experts * (kTokMany / 8), 0, st, a, (int)ctas);
     }
     return e == cudaSuccess ? UW_OK : fail(UW_ERR_CUDA, "uw_route: launch: %s", cudaGetErrorString(e));
 }
