@@ -22,6 +22,7 @@ using namespace uw;
 
 namespace {
 
+constexpr int kThreads = 1024;
 constexpr int kTokOne = 128;     // tokens that one CTA takes alone
 constexpr int kTokMany = 64;     // and when there are more
 constexpr int kMaxE = 1024, kMaxTop = 16;
@@ -138,10 +139,9 @@ __device__ __forceinline__ int bits_rank(const uint32_t *b, int tl)
 }
 
 // v[0..E) in shared memory becomes its exclusive sum; returns the total.  Begins and ends with a barrier.
-template <int THREADS>
 __device__ __forceinline__ int exclusive_sum(int *v, int E, int *wsum)
 {
-    constexpr int Q = kMaxE / THREADS;  // consecutive values of a thread
+    constexpr int Q = kMaxE / kThreads;  // consecutive values of a thread
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     __syncthreads();
     int x[Q], s = 0;
@@ -158,7 +158,7 @@ __device__ __forceinline__ int exclusive_sum(int *v, int E, int *wsum)
     }
     if (lane == 31) wsum[warp] = sum;
     __syncthreads();
-    int w = lane < THREADS / 32 ? wsum[lane] : 0;
+    int w = lane < kThreads / 32 ? wsum[lane] : 0;
     const int mine = lane < warp ? w : 0;
     int at = sum - s + __reduce_add_sync(0xFFFFFFFFu, mine);
     const int total = __reduce_add_sync(0xFFFFFFFFu, w);
@@ -172,9 +172,9 @@ __device__ __forceinline__ int exclusive_sum(int *v, int E, int *wsum)
 }
 
 template <int PER, int TOK>
-__global__ void __launch_bounds__(8 * TOK) route_choose_kernel(const RouteArgs a)
+__global__ void __launch_bounds__(kThreads) route_choose_kernel(const RouteArgs a)
 {
-    constexpr int kThreads = 8 * TOK, WORDS = TOK / 32;  // a warp for each four tokens
+    constexpr int WORDS = TOK / 32;
     extern __shared__ uint32_t bits[];                   // [experts][WORDS]
     const int E = a.r.experts, k = a.r.topk;
     const int64_t t0 = (int64_t)blockIdx.x * TOK;
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(8 * TOK) route_choose_kernel(const RouteArgs a
     // all tokens are here: the order too
     __shared__ int wsum[32], base[kMaxE];
     for (int e = threadIdx.x; e < E; e += kThreads) base[e] = bits_count<WORDS>(bits + e * WORDS);
-    const int total = exclusive_sum<kThreads>(base, E, wsum);
+    const int total = exclusive_sum(base, E, wsum);
     for (int e = threadIdx.x; e < E; e += kThreads) a.offsets[e] = base[e];
     if (threadIdx.x == 0) a.offsets[E] = total;
     for (int i = threadIdx.x; i < nt * k; i += kThreads) {
@@ -203,9 +203,9 @@ __global__ void __launch_bounds__(8 * TOK) route_choose_kernel(const RouteArgs a
     }
 }
 
-__global__ void __launch_bounds__(8 * kTokMany) route_order_kernel(const RouteArgs a, int ctas)
+__global__ void __launch_bounds__(kThreads) route_order_kernel(const RouteArgs a, int ctas)
 {
-    constexpr int kThreads = 8 * kTokMany, WORDS = kTokMany / 32;
+    constexpr int WORDS = kTokMany / 32;
     extern __shared__ uint32_t bits[];  // [experts][WORDS]
     __shared__ int wsum[32], base[kMaxE], before[kMaxE];
     const int E = a.r.experts, k = a.r.topk;
@@ -216,12 +216,14 @@ __global__ void __launch_bounds__(8 * kTokMany) route_order_kernel(const RouteAr
     pdl_trigger();
     __syncthreads();
     pdl_wait();
+    // this CTA's choices; few enough that each thread keeps its first
+    const int first = (int)threadIdx.x < nt * k ? a.ids[t0 * k + threadIdx.x] : 0;
     // rows of each expert in all CTAs, and in those before this one: the threads beyond one for each expert share the CTAs
     const int parts = max(1, kThreads / E);
     for (int i = threadIdx.x; i < E * parts; i += kThreads) {
         const int e = i % E, part = i / E;
         int all = 0, mine = 0;
-#pragma unroll 8
+#pragma unroll 16
         for (int c = part; c < ctas; c += parts) {
             const int n = __ldg(a.counts + (int64_t)c * E + e);
             all += n;
@@ -231,16 +233,16 @@ __global__ void __launch_bounds__(8 * kTokMany) route_order_kernel(const RouteAr
         if (mine) atomicAdd(&before[e], mine);
     }
     for (int i = threadIdx.x; i < nt * k; i += kThreads) {
-        const int tl = i / k;
-        atomicOr(&bits[a.ids[t0 * k + i] * WORDS + (tl >> 5)], 1u << (tl & 31));
+        const int tl = i / k, e = i == (int)threadIdx.x ? first : a.ids[t0 * k + i];
+        atomicOr(&bits[e * WORDS + (tl >> 5)], 1u << (tl & 31));
     }
-    const int total = exclusive_sum<kThreads>(base, E, wsum);
+    const int total = exclusive_sum(base, E, wsum);
     if (blockIdx.x == 0) {
         for (int e = threadIdx.x; e < E; e += kThreads) a.offsets[e] = base[e];
         if (threadIdx.x == 0) a.offsets[E] = total;
     }
     for (int i = threadIdx.x; i < nt * k; i += kThreads) {
-        const int tl = i / k, e = a.ids[t0 * k + i];
+        const int tl = i / k, e = i == (int)threadIdx.x ? first : a.ids[t0 * k + i];
         const int r = base[e] + before[e] + bits_rank(bits + e * WORDS, tl);
         a.pos[t0 * k + i] = r;
         a.row_src[r] = (int32_t)(t0 + tl);
@@ -256,7 +258,7 @@ cudaError_t launch_choose(const RouteArgs &a, int64_t ctas, cudaStream_t st)
                   : E <= 128 ? route_choose_kernel<4, TOK>
                   : E <= 256 ? route_choose_kernel<8, TOK>
                              : route_choose_kernel<32, TOK>;
-    return launch_dependent(kernel, dim3((unsigned)ctas), 8 * TOK, (size_t)E * (TOK / 8), 0, st, a);
+    return launch_dependent(kernel, dim3((unsigned)ctas), kThreads, (size_t)E * (TOK / 8), 0, st, a);
 }
 
 uw_status check_router(const uw_router *r, const char *who)
@@ -312,7 +314,7 @@ extern "C" uw_status uw_route(const uw_router *r, const void *logits, uw_out_dty
     } else {
         e = ctas == 1 ? launch_choose<kTokOne>(a, 1, st) : launch_choose<kTokMany>(a, ctas, st);
         if (e == cudaSuccess && ctas > 1)
-            e = launch_dependent(route_order_kernel, dim3((unsigned)ctas), 8 * kTokMany, (size_t)r->experts * (kTokMany / 8), 0, st, a, (int)ctas);
+            e = launch_dependent(route_order_kernel, dim3((unsigned)ctas), kThreads, (size_t)r->experts * (kTokMany / 8), 0, st, a, (int)ctas);
     }
     return e == cudaSuccess ? UW_OK : fail(UW_ERR_CUDA, "uw_route: launch: %s", cudaGetErrorString(e));
 }
