@@ -18,7 +18,7 @@
 //     of a warp hold gate rows and lanes 16-31 the up rows that belong to them: eight exchanges between the halves per
 //     16 columns give each lane both factors of eight outputs.
 // Tensor memory: two accumulators of 192 columns, so that a unit's epilogue runs under the next unit's products, and
-// four slots of 32 columns for A.
+// four slots of 32 columns for A (64 and eight in the shape for few rows).
 // Every wait is bounded; when one runs out the kernel latches DEV_TIMEOUT, waits for its copies and products in flight,
 // frees its tensor memory and ends.
 #include <cuda.h>
@@ -46,6 +46,7 @@ constexpr int kProdWarp2 = kXWarp0 + kXWarps;
 constexpr int kEpiWarp0 = kProdWarp2 + 1;  // a multiple of four: warp % 4 is the lane quarter of tensor memory
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+constexpr int kSegSteps = 8;                  // steps of a segment (fp32 output)
 constexpr int kVCs = 8;                       // verbatim runs of a step staged with it (beyond: global loads)
 constexpr uint32_t kVOff = kStepRec + 128;    // a stage: the step with its record, then its verbatim runs
 constexpr uint32_t kWStage = kVOff + kVCs * 64;
@@ -136,7 +137,8 @@ struct Units {
     }
 };
 
-template <bool GATED, bool GATHER, int BN>
+// SUMS: an fp32 output of several segments, whose sums the epilogue keeps in registers
+template <bool GATED, bool GATHER, int BN, bool SUMS>
 __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_constant__ TcArgs a)
 {
     using Sh = Shape<BN>;
@@ -224,6 +226,10 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
     const uint32_t tmem = *tmem_slot;
     Units<BN> units(off, tcum, v);
     Unit w;
+    // A unit's sums are taken in segments of K, the two accumulators in turn: the tensor core cuts low bits off a running
+    // sum at every product, an error that grows with the sum's length (2e-6 of a result at K = 4096).  For a bf16 output
+    // that is far below the rounding, and a segment is all of K; an fp32 output gets segments of 512, added in fp32.
+    const int seg_steps = a.c.out_bf16 ? ksteps : kSegSteps;
 
     if (warp == kProdWarp || warp == kProdWarp2) {
         // ---------------------------------------------------------------------------------------- weight copies
@@ -345,36 +351,37 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
         // issues.  (A loop inside `if (lane == 0)` moved every operand from an ordinary register for each instruction:
         // 870 cycles a step at any N.)
         bool ok = true;
-        int sx = 0, sa = 0, nu = 0;
+        int sx = 0, sa = 0, ns = 0;  // ns: segments begun
         uint32_t phx = 0, pha = 0;
         const bool leader = elect_one();
         const uint64_t desc0 = smem_desc_sw128(saddr(xring));
         while (ok && units.next(w)) {
             const uint32_t id = idesc_bf16(kTileRows, (w.n + 15) & ~15);
-            const int buf = nu & 1;
-            if (nu >= 2 && !__all_sync(0xFFFFFFFFu, mbar_wait(&accempty[buf], ((nu >> 1) - 1) & 1))) { ok = false; break; }
-            tc_fence_after();
-            const uint32_t d = tmem + buf * kBN;
-            for (int ks = 0; ks < ksteps; ks++) {
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait(&afull[sa], pha) && mbar_wait(&xfull[sx], phx))) { ok = false; break; }
+            for (int k0 = 0; k0 < ksteps && ok; k0 += seg_steps, ns++) {
+                const int buf = ns & 1, n = min(seg_steps, ksteps - k0);
+                if (ns >= 2 && !__all_sync(0xFFFFFFFFu, mbar_wait(&accempty[buf], ((ns >> 1) - 1) & 1))) { ok = false; break; }
                 tc_fence_after();
-                if (leader) {
-                    const uint32_t at = tmem + kACol + 32 * sa;
-                    const uint64_t xd = desc0 + (uint64_t)(sx * (int)(kXStage >> 4));
+                const uint32_t d = tmem + buf * kBN;
+                for (int j = 0; j < n; j++) {
+                    if (!__all_sync(0xFFFFFFFFu, mbar_wait(&afull[sa], pha) && mbar_wait(&xfull[sx], phx))) { ok = false; break; }
+                    tc_fence_after();
+                    if (leader) {
+                        const uint32_t at = tmem + kACol + 32 * sa;
+                        const uint64_t xd = desc0 + (uint64_t)(sx * (int)(kXStage >> 4));
 #pragma unroll
-                    for (int kk = 0; kk < 4; kk++) mma_ts(d, at + 8 * kk, xd + 2 * kk, id, (ks | kk) ? 1u : 0u);
-                    mma_commit(&aempty[sa]);
-                    mma_commit(&xempty[sx]);
-                    if (ks == ksteps - 1) mma_commit(&accfull[buf]);
+                        for (int kk = 0; kk < 4; kk++) mma_ts(d, at + 8 * kk, xd + 2 * kk, id, (j | kk) ? 1u : 0u);
+                        mma_commit(&aempty[sa]);
+                        mma_commit(&xempty[sx]);
+                        if (j == n - 1) mma_commit(&accfull[buf]);
+                    }
+                    __syncwarp();
+                    if (++sa == kSA) { sa = 0; pha ^= 1u; }
+                    if (++sx == kSX) { sx = 0; phx ^= 1u; }
                 }
-                __syncwarp();
-                if (++sa == kSA) { sa = 0; pha ^= 1u; }
-                if (++sx == kSX) { sx = 0; phx ^= 1u; }
             }
-            nu++;
         }
         if (!ok && leader) atomicExch(v.status, (int)DEV_TIMEOUT);
-        if (nu > 0) {
+        if (ns > 0) {
             // every product issued has completed before the tensor memory is freed
             if (leader) mma_commit(done);
             __syncwarp();
@@ -448,53 +455,85 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
         // ---------------------------------------------------------------------------------------- epilogue
         const int q = warp & 3, half = (warp - kEpiWarp0) >> 2;
         bool ok = true;
-        int nu = 0;
-        while (units.next(w)) {
-            const int buf = nu & 1;
-            if (!mbar_wait(&accfull[buf], (nu >> 1) & 1)) { ok = false; break; }
-            tc_fence_after();
-            const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + buf * kBN;
-            const int64_t col = GATED ? ((int64_t)w.tile * 4 + q) * 16 + (lane & 15) : (int64_t)w.tile * kTileRows + 32 * q + lane;
-            const bool in = col < v.N;
-            for (int c0 = 16 * half; c0 < w.n; c0 += 32) {
-                uint32_t x[16];
-                tmem_ld16(acc + c0, x);
-                tmem_wait_ld();
-                constexpr int NO = GATED ? 8 : 16;
-                float f[NO];
-                int first = c0;
-                if constexpr (GATED) {
-                    const bool up = lane >= 16;
-                    first += up ? 8 : 0;
+        int ns = 0;
+        // 16 columns from c0 on into the output; add: to what an earlier segment left there (not gated)
+        auto emit = [&](const float (&x)[16], int c0, bool add) {
+            constexpr int NO = GATED ? 8 : 16;
+            float f[NO];
+            int first = c0;
+            int64_t col;
+            if constexpr (GATED) {
+                const bool up = lane >= 16;
+                first += up ? 8 : 0;
 #pragma unroll
-                    for (int j = 0; j < 8; j++) {
-                        const float mine = __uint_as_float(up ? x[8 + j] : x[j]);
-                        const float other = __shfl_xor_sync(0xFFFFFFFFu, __uint_as_float(up ? x[j] : x[8 + j]), 16);
-                        f[j] = gated(up ? other : mine, up ? mine : other);
+                for (int j = 0; j < 8; j++) {
+                    const float mine = up ? x[8 + j] : x[j];
+                    const float other = __shfl_xor_sync(0xFFFFFFFFu, up ? x[j] : x[8 + j], 16);
+                    f[j] = gated(up ? other : mine, up ? mine : other);
+                }
+                col = ((int64_t)w.tile * 4 + q) * 16 + (lane & 15);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; j++) f[j] = x[j];
+                col = (int64_t)w.tile * kTileRows + 32 * q + lane;
+            }
+            const int m = col < v.N ? w.n - first : 0;
+            const int64_t o = (int64_t)(w.r0 + first) * a.c.ldy + col;
+            if (a.c.out_bf16) {
+                __nv_bfloat16 *p = (__nv_bfloat16 *)a.c.y + o;
+#pragma unroll
+                for (int j = 0; j < NO; j++, p += a.c.ldy)
+                    if (j < m) *p = __float2bfloat16_rn(f[j]);
+            } else {
+                float *p = (float *)a.c.y + o;
+#pragma unroll
+                for (int j = 0; j < NO; j++, p += a.c.ldy)
+                    if (j < m) *p = add ? *p + f[j] : f[j];
+            }
+            __syncwarp();
+        };
+        auto columns = [&](uint32_t acc, float (&x)[16]) {
+            uint32_t u[16];
+            tmem_ld16(acc, u);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; j++) x[j] = __uint_as_float(u[j]);
+        };
+        while (ok && units.next(w)) {
+            constexpr int NC = BN / 32;  // a warp's groups of columns
+            float run[SUMS ? NC : 1][16];
+            for (int k0 = 0; k0 < ksteps; k0 += seg_steps, ns++) {
+                const int buf = ns & 1;
+                if (!mbar_wait(&accfull[buf], (ns >> 1) & 1)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + buf * kBN;
+                if constexpr (SUMS) {
+#pragma unroll
+                    for (int i = 0; i < NC; i++) {
+                        const int c0 = 16 * half + 32 * i;
+                        if (c0 >= w.n) continue;
+                        float x[16];
+                        columns(acc + c0, x);
+#pragma unroll
+                        for (int j = 0; j < 16; j++) run[i][j] = k0 ? run[i][j] + x[j] : x[j];
                     }
                 } else {
-#pragma unroll
-                    for (int j = 0; j < 16; j++) f[j] = __uint_as_float(x[j]);
+                    for (int c0 = 16 * half; c0 < w.n; c0 += 32) {
+                        float x[16];
+                        columns(acc + c0, x);
+                        emit(x, c0, k0 > 0);
+                    }
                 }
-                const int m = in ? w.n - first : 0;
-                const int64_t o = (int64_t)(w.r0 + first) * a.c.ldy + col;
-                if (a.c.out_bf16) {
-                    __nv_bfloat16 *p = (__nv_bfloat16 *)a.c.y + o;
-#pragma unroll
-                    for (int j = 0; j < NO; j++, p += a.c.ldy)
-                        if (j < m) *p = __float2bfloat16_rn(f[j]);
-                } else {
-                    float *p = (float *)a.c.y + o;
-#pragma unroll
-                    for (int j = 0; j < NO; j++, p += a.c.ldy)
-                        if (j < m) *p = f[j];
-                }
+                tc_fence_before();
                 __syncwarp();
+                if (lane == 0) mbar_arrive(&accempty[buf]);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&accempty[buf]);
-            nu++;
+            if constexpr (SUMS) {
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < NC; i++)
+                    if (16 * half + 32 * i < w.n) emit(run[i], 16 * half + 32 * i, false);
+            }
         }
         if (!ok && lane == 0) atomicExch(v.status, (int)DEV_TIMEOUT);
     }
@@ -506,26 +545,26 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
     }
 }
 
-template <bool GATED, bool GATHER, int BN>
+template <bool GATED, bool GATHER, int BN, bool SUMS>
 cudaError_t launch_one(const TcArgs &a, cudaStream_t st)
 {
     static bool attr = false;
     if (!attr) {
-        const cudaError_t e = cudaFuncSetAttribute(group_tc_kernel<GATED, GATHER, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<BN>::smem);
+        const cudaError_t e = cudaFuncSetAttribute(group_tc_kernel<GATED, GATHER, BN, SUMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<BN>::smem);
         if (e != cudaSuccess) return e;
         attr = true;
     }
     // at least one row tile for each BN rows, at most one more for each expert
     const GroupCall &c = a.c;
     const int64_t most = ((c.rows + BN - 1) / BN + std::min<int64_t>(c.v.experts, c.rows)) * c.v.tiles;
-    return launch_dependent(group_tc_kernel<GATED, GATHER, BN>, dim3((unsigned)std::min<int64_t>(num_sms(), most)), kThreads, Shape<BN>::smem, 0, st, a);
+    return launch_dependent(group_tc_kernel<GATED, GATHER, BN, SUMS>, dim3((unsigned)std::min<int64_t>(num_sms(), most)), kThreads, Shape<BN>::smem, 0, st, a);
 }
 
-template <int BN>
+template <int BN, bool SUMS>
 cudaError_t launch_shape(const TcArgs &a, cudaStream_t st)
 {
-    if (a.c.v.gated) return a.c.row_src ? launch_one<true, true, BN>(a, st) : launch_one<true, false, BN>(a, st);
-    return a.c.row_src ? launch_one<false, true, BN>(a, st) : launch_one<false, false, BN>(a, st);
+    if (a.c.v.gated) return a.c.row_src ? launch_one<true, true, BN, SUMS>(a, st) : launch_one<true, false, BN, SUMS>(a, st);
+    return a.c.row_src ? launch_one<false, true, BN, SUMS>(a, st) : launch_one<false, false, BN, SUMS>(a, st);
 }
 
 bool map_x(CUtensorMap *m, const GroupCall &c)
@@ -556,7 +595,12 @@ int launch_group_tc(const GroupCall &c, void *stream)
     a.c = c;
     // The smaller shape up to 32 rows an expert on average: 64 experts of [2048, 1408] take 54 us against 60 at 16 rows
     // each, 60 against 61 at 32, 79 against 63 at 64.
-    return c.rows <= 32 * (int64_t)c.v.experts ? launch_shape<64>(a, (cudaStream_t)stream) : launch_shape<192>(a, (cudaStream_t)stream);
+    // An fp32 output of several segments is summed in registers by the smaller shape, which has room for them, and in the
+    // output by the larger, which a gated output cannot be.
+    const bool sums = !c.out_bf16 && c.v.ksteps > kSegSteps;
+    if (c.rows <= 32 * (int64_t)c.v.experts || (c.v.gated && sums))
+        return sums ? launch_shape<64, true>(a, (cudaStream_t)stream) : launch_shape<64, false>(a, (cudaStream_t)stream);
+    return launch_shape<192, false>(a, (cudaStream_t)stream);
 }
 
 }  // namespace uw

@@ -305,3 +305,20 @@ def test_refusals():
     assert status(lambda: g.matmul(x, off, 4, y.data_ptr() + 4, **f)) == uw.ERR_INVALID_ARG
     assert status(lambda: g.decode(2, w)) == uw.ERR_INVALID_ARG
     assert status(lambda: g.decode(0, w, up=True)) == uw.ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("rows_each", [3, 20, 150])
+def test_long_sums_in_fp32(rows_each, gated):
+    # An fp32 output is summed in segments of 512: 32 products of 16 that each cut at most 2^-24 of a running sum no larger
+    # (in the norm) than the result, and 16 additions of segments at K = 8192, 2^-24 each: 48 2^-24 of the result's norm
+    # (a gated result has two such factors; its activation passes errors on at most 1.1-fold).  One sum of all of K would be off by
+    # several times that.
+    t = torch()
+    E, N, K = 3, 64, 8192
+    w, u = weights(E, N, K, 101, 0.0), weights(E, N, K, 102, 0.0)
+    rows = E * rows_each
+    x, off = synth.fill((rows, K), seed=103), offsets_of([rows_each] * E)
+    y = run(uw.Group(dev(w), dev(u) if gated else None), dev(x), dev(off), rows, False)
+    ref, _ = reference(w, u if gated else None, f64(x), np.arange(rows), off, rows)
+    assert np.linalg.norm(y - ref) <= (2.1 if gated else 1.0) * 48 * 2.0 ** -24 * np.linalg.norm(ref)
