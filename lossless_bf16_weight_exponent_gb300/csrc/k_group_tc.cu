@@ -5,7 +5,7 @@
 // tile innermost so that CTAs that run together share their rows of X.  The list follows from the offsets, which each
 // CTA reads on the device.  Warps:
 //   - 0-11, three groups of four: group i % 3 rebuilds step i (128 rows x 64 weights).  Thread = row: four 16-byte and
-//     four 8-byte reads of shared memory without bank conflicts, 32 bf16 pairs, four tcgen05.st of eight columns.  The
+//     four 8-byte reads of shared memory without bank conflicts, 32 bf16 pairs, one tcgen05.st of 32 columns.  The
 //     A operand never passes through shared memory, which the X tiles need.
 //   - 12, 19: bulk copies of the steps (12 KB and the record, one run of memory) and their verbatim runs, alternate
 //     steps each;
@@ -51,21 +51,24 @@ constexpr int kVCs = 8;                       // verbatim runs of a step staged 
 constexpr uint32_t kVOff = kStepRec + 128;    // a stage: the step with its record, then its verbatim runs
 constexpr uint32_t kWStage = kVOff + kVCs * 64;
 
-// The shapes, by the rows of X per unit at most.  With 192 rows the X tiles take most of shared memory; with 64 the
-// weights do, whose bytes in flight bound a product of few rows.
-template <int BN_>
+// The shapes: 192 rows of X per unit at most on a pair of CTAs, each with half of the X tile; 64 on one, where the weights
+// have most of shared memory: their bytes in flight bound a product of few rows.
+template <int BN_, bool PAIR_>
 struct Shape {
     static constexpr int BN = BN_;
-    static constexpr int SX = kXWarps, SW = BN == 192 ? 6 : 12, SA = BN == 192 ? 4 : 8;  // stages of X, of the weights; A slots
-    static constexpr uint32_t XStage = BN * 128;
+    static constexpr bool PAIR = PAIR_;
+    static constexpr int SX = kXWarps, SW = 12, SA = BN == 192 ? 4 : 8;  // stages of X, of the weights; A slots
+    static constexpr int XRows = PAIR ? BN / 2 : BN;                      // rows of the X tile in a CTA
+    static constexpr uint32_t XStage = XRows * 128;
     static constexpr int ACol = 2 * BN;       // tensor memory: two accumulators, then the A slots of 32 columns
-    static constexpr size_t smem = 1024 + (size_t)SX * XStage + (size_t)SW * kWStage + 512 + 2 * 4 * (kMaxExperts + 4) + 4 * SX * BN;
+    static constexpr size_t smem = 1024 + (size_t)SX * XStage + (size_t)SW * kWStage + 512 + 2 * 4 * (kMaxExperts + 4) + 4 * SX * XRows;
     static_assert(smem <= 227 * 1024, "shared memory");
     // A stage of the weight ring belongs to one rebuild group and one copying warp for good.  Copies land out of order,
     // so a group that waited for a stage last read by another group could be a whole turn ahead of a copy that has not
-    // landed, where the barrier's parity is the same as of the turn it waits for.
-    static_assert(SW % kGroups == 0 && SW % 2 == 0, "weight ring");
-    static_assert(ACol + 32 * SA <= 512 && BN % 32 == 0, "layout");
+    // landed, where the barrier's parity is the same as of the turn it waits for.  (The A slots need no such rule: products
+    // complete in order, and a group that is at step q has seen step q - kGroups - SA done.)
+    static_assert(SW % kGroups == 0 && SW % 2 == 0 && SA >= kGroups, "rings");
+    static_assert(ACol + 32 * SA <= 512 && XRows % 32 == 0, "layout");
     static_assert((2 * (SW + SX + SA) + 5) * 8 + 8 <= 512, "barriers");
 };
 static_assert(kEpiWarp0 % 4 == 0 && kWStage % 128 == 0, "layout");
@@ -100,50 +103,102 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
-// eight consecutive 32-bit columns of this warp's 32 lanes of tensor memory
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8])
+// The pair of CTAs on one product (cta_group::2): D of 256 rows, each CTA's tensor memory holds its 128 of A and D, each
+// CTA's shared memory half of the rows of B.  Issued by one thread of the first CTA.
+__device__ __forceinline__ void mma_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc)
 {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
-                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(
+                     d_tmem),
+                 "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
                  : "memory");
 }
 
+// arrive on this barrier in both CTAs once every product issued so far by this thread has completed
+__device__ __forceinline__ void mma_commit_pair(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(saddr(bar)),
+                 "h"((uint16_t)3)
+                 : "memory");
+}
+
+// Arrive on the first CTA's barrier at the same place.  What it tells of are tensor-memory stores and tensor copies, which
+// the tensor-core fences and the copies' own barrier order; no ordinary store of this thread is behind it, and a release
+// at cluster scope, which would wait for those, takes 1400 cycles.
+__device__ __forceinline__ void arrive_first(uint64_t *bar)
+{
+    asm volatile(
+        "{\n .reg .b32 ra;\n mapa.shared::cluster.u32 ra, %0, 0;\n mbarrier.arrive.shared::cluster.b64 _, [ra];\n}\n" ::"r"(
+            saddr(bar))
+        : "memory");
+}
+
+// mbar_wait with the other CTA's writes in view
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *b, uint32_t parity)
+{
+    auto test = [&] {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(saddr(b)), "r"(parity)
+            : "memory");
+        return ok != 0;
+    };
+    if (test()) return true;
+    const uint64_t t0 = gtime();
+    for (;;) {
+        for (int i = 0; i < 64; i++)
+            if (test()) return true;
+        if (gtime() - t0 > kWaitLimitNs) return false;
+    }
+}
+
+__device__ __forceinline__ void cluster_barrier()
+{
+    asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
+}
+
 struct Unit {
-    int e, r0, n, tile;  // expert, first row, rows (1..kBN), weight tile
+    int e, r0, n, tile;  // expert, first row, rows (1..BN), weight tile
+    bool real;           // false: the second CTA of a pair has no tile of its own and stores nothing
 };
 
-// this CTA's units in order; off: clamped offsets, tcum: row tiles of X before each expert (shared memory)
-template <int BN>
+// this CTA's (a pair's) units in order; off: clamped offsets, tcum: row tiles of X before each expert (shared memory)
+template <typename Sh>
 struct Units {
     const int *off, *tcum;
     int64_t u, total;
-    int e, tiles, experts;
+    int e, tiles, per;  // per: units for each row tile of X
     __device__ __forceinline__ Units(const int *off_, const int *tcum_, const GroupView &v)
-        : off(off_), tcum(tcum_), u(blockIdx.x), e(0), tiles(v.tiles), experts(v.experts)
+        : off(off_), tcum(tcum_), u(Sh::PAIR ? blockIdx.x >> 1 : blockIdx.x), e(0), tiles(v.tiles), per(Sh::PAIR ? (v.tiles + 1) / 2 : v.tiles)
     {
-        total = (int64_t)tcum[experts] * tiles;
+        total = (int64_t)tcum[v.experts] * per;
     }
     __device__ __forceinline__ bool next(Unit &w)
     {
         if (u >= total) return false;
-        const int tt = (int)(u / tiles);
-        w.tile = (int)(u - (int64_t)tt * tiles);
+        const int tt = (int)(u / per), t = (int)(u - (int64_t)tt * per);
+        const int tile = Sh::PAIR ? 2 * t + (int)(blockIdx.x & 1) : t;
+        w.real = tile < tiles;
+        w.tile = min(tile, tiles - 1);
         while (tt >= tcum[e + 1]) e++;
         w.e = e;
-        w.r0 = off[e] + (tt - tcum[e]) * BN;
-        w.n = min(BN, off[e + 1] - w.r0);
-        u += gridDim.x;
+        w.r0 = off[e] + (tt - tcum[e]) * Sh::BN;
+        w.n = min(Sh::BN, off[e + 1] - w.r0);
+        u += Sh::PAIR ? gridDim.x >> 1 : gridDim.x;
         return true;
     }
 };
 
 // SUMS: an fp32 output of several segments, whose sums the epilogue keeps in registers
-template <bool GATED, bool GATHER, int BN, bool SUMS>
+template <bool GATED, bool GATHER, typename Sh, bool SUMS>
 __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_constant__ TcArgs a)
 {
-    using Sh = Shape<BN>;
-    constexpr int kBN = BN, kSX = Sh::SX, kSW = Sh::SW, kSA = Sh::SA, kACol = Sh::ACol;
+    constexpr int BN = Sh::BN, kBN = BN, kSX = Sh::SX, kSW = Sh::SW, kSA = Sh::SA, kACol = Sh::ACol;
     constexpr uint32_t kXStage = Sh::XStage;
+    constexpr bool PAIR = Sh::PAIR;
+    constexpr int kXRows = Sh::XRows, kNStep = PAIR ? 32 : 16;  // N is a multiple of kNStep
+    const int rank = PAIR ? (int)(blockIdx.x & 1) : 0;            // in the pair
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t pad = (1024u - (saddr(smem_raw) & 1023u)) & 1023u;
     uint8_t *xring = smem_raw + pad;                  // [kSX][kXStage], 1024-aligned
@@ -158,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
     uint32_t *tmem_slot = (uint32_t *)(done + 1);
     int *off = (int *)((uint8_t *)wfull + 512);       // [experts + 1]
     int *tcum = off + kMaxExperts + 4;                // [experts + 1]
-    int *xrows = tcum + kMaxExperts + 4;              // [kSX][kBN] (sources) a warp's unit's rows of X (past the end: zeros)
+    int *xrows = tcum + kMaxExperts + 4;              // [kSX][kXRows] (sources) a warp's unit's rows of X (past the end: zeros)
 
     const GroupView &v = a.c.v;
     const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: a uniform value
@@ -174,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
             mbar_init(&xempty[s], 1);
         }
         for (int s = 0; s < kSA; s++) {
-            mbar_init(&afull[s], 4);
+            mbar_init(&afull[s], PAIR && rank == 0 ? 5 : 4);  // a rebuild group's warps, and word from the second CTA
             mbar_init(&aempty[s], 1);
         }
         for (int b = 0; b < 2; b++) {
@@ -185,9 +240,15 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kMmaWarp) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_slot)), "r"(512)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        if constexpr (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_slot)), "r"(512)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_slot)), "r"(512)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
     }
     pdl_trigger();
     pdl_wait();
@@ -221,10 +282,11 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
         }
     }
     tc_fence_before();
+    if constexpr (PAIR) cluster_barrier();  // the barriers of both CTAs are set up
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    Units<BN> units(off, tcum, v);
+    Units<Sh> units(off, tcum, v);
     Unit w;
     // A unit's sums are taken in segments of K, the two accumulators in turn: the tensor core cuts low bits off a running
     // sum at every product, an error that grows with the sum's length (2e-6 of a result at K = 4096).  For a bf16 output
@@ -288,16 +350,22 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
         const uint32_t xs = saddr(xring + x * kXStage);
         bool ok = true;
         int i = 0, turn = 0;  // steps before this unit, this stage's turns
+        // this CTA's rows of a unit's X tile: how many, and the first (of a pair's, each half)
+        auto x_rows = [&](const Unit &q) { return ((q.n + kNStep - 1) / kNStep * kNStep) / (PAIR ? 2 : 1); };
+        auto x_first = [&](const Unit &q) { return PAIR ? rank * x_rows(q) : 0; };
         auto stage_free = [&] { return turn == 0 || __all_sync(0xFFFFFFFFu, mbar_wait(&xempty[x], (turn - 1) & 1)); };
         if constexpr (GATHER) {
-            int *rows = xrows + x * kBN;
-            constexpr int kL = kBN / 32;
+            int *rows = xrows + x * kXRows;
+            constexpr int kL = kXRows / 32;
             const bool leader = elect_one();
             const int none = (int)a.c.x_rows;  // past the end
             int r[kL];  // the next unit's rows, on their way before it begins
             auto fetch = [&](const Unit &q) {
 #pragma unroll
-                for (int j = 0; j < kL; j++) r[j] = 32 * j + lane < q.n ? __ldg(a.c.row_src + q.r0 + 32 * j + lane) : -1;
+                for (int j = 0; j < kL; j++) {
+                    const int row = x_first(q) + 32 * j + lane;
+                    r[j] = 32 * j + lane < x_rows(q) && row < q.n ? __ldg(a.c.row_src + q.r0 + row) : -1;
+                }
             };
             Unit nx;
             bool have = units.next(w);
@@ -309,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
                 __syncwarp();
                 const bool more = units.next(nx);
                 if (more) fetch(nx);
-                const int bn = (w.n + 15) & ~15;
+                const int bn = x_rows(w);
                 for (int ks = (kSX - i % kSX + x) % kSX; ks < ksteps; ks += kSX, turn++) {
                     if (!stage_free()) { ok = false; break; }
                     if (leader) {
@@ -331,12 +399,12 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
             }
         } else {
             while (ok && units.next(w)) {
-                const int boxes = (w.n + 31) / 32;
+                const int boxes = (x_rows(w) + 31) / 32, first = w.r0 + x_first(w);
                 for (int ks = (kSX - i % kSX + x) % kSX; ks < ksteps; ks += kSX, turn++) {
                     if (!stage_free()) { ok = false; break; }
                     if (lane == 0) mbar_expect_tx(&xfull[x], (uint32_t)boxes * 4096u);
                     __syncwarp();
-                    if (lane < boxes) tma2d(xring + x * kXStage + 4096 * lane, &a.tm_x, ks * kStepW, w.r0 + 32 * lane, &xfull[x]);
+                    if (lane < boxes) tma2d(xring + x * kXStage + 4096 * lane, &a.tm_x, ks * kStepW, first + 32 * lane, &xfull[x]);
                     __syncwarp();
                 }
                 i += ksteps;
@@ -355,24 +423,36 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
         uint32_t phx = 0, pha = 0;
         const bool leader = elect_one();
         const uint64_t desc0 = smem_desc_sw128(saddr(xring));
+        auto commit = [](uint64_t *bar) {
+            if constexpr (PAIR) mma_commit_pair(bar);
+            else mma_commit(bar);
+        };
         while (ok && units.next(w)) {
-            const uint32_t id = idesc_bf16(kTileRows, (w.n + 15) & ~15);
+            const uint32_t id = idesc_bf16(PAIR ? 2 * kTileRows : kTileRows, (w.n + kNStep - 1) / kNStep * kNStep);
             for (int k0 = 0; k0 < ksteps && ok; k0 += seg_steps, ns++) {
                 const int buf = ns & 1, n = min(seg_steps, ksteps - k0);
                 if (ns >= 2 && !__all_sync(0xFFFFFFFFu, mbar_wait(&accempty[buf], ((ns >> 1) - 1) & 1))) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t d = tmem + buf * kBN;
                 for (int j = 0; j < n; j++) {
-                    if (!__all_sync(0xFFFFFFFFu, mbar_wait(&afull[sa], pha) && mbar_wait(&xfull[sx], phx))) { ok = false; break; }
+                    // the first CTA's A barrier also counts the second's word that its A slot and X tile are there
+                    const bool there = (PAIR && rank == 0 ? mbar_wait_cluster(&afull[sa], pha) : mbar_wait(&afull[sa], pha)) && mbar_wait(&xfull[sx], phx);
+                    if (!__all_sync(0xFFFFFFFFu, there)) { ok = false; break; }
                     tc_fence_after();
-                    if (leader) {
+                    if (PAIR && rank == 1) {
+                        tc_fence_before();
+                        if (leader) arrive_first(&afull[sa]);
+                    } else if (leader) {
                         const uint32_t at = tmem + kACol + 32 * sa;
                         const uint64_t xd = desc0 + (uint64_t)(sx * (int)(kXStage >> 4));
 #pragma unroll
-                        for (int kk = 0; kk < 4; kk++) mma_ts(d, at + 8 * kk, xd + 2 * kk, id, (j | kk) ? 1u : 0u);
-                        mma_commit(&aempty[sa]);
-                        mma_commit(&xempty[sx]);
-                        if (j == n - 1) mma_commit(&accfull[buf]);
+                        for (int kk = 0; kk < 4; kk++) {
+                            if constexpr (PAIR) mma_ts_pair(d, at + 8 * kk, xd + 2 * kk, id, (j | kk) ? 1u : 0u);
+                            else mma_ts(d, at + 8 * kk, xd + 2 * kk, id, (j | kk) ? 1u : 0u);
+                        }
+                        commit(&aempty[sa]);
+                        commit(&xempty[sx]);
+                        if (j == n - 1) commit(&accfull[buf]);
                     }
                     __syncwarp();
                     if (++sa == kSA) { sa = 0; pha ^= 1u; }
@@ -383,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
         if (!ok && leader) atomicExch(v.status, (int)DEV_TIMEOUT);
         if (ns > 0) {
             // every product issued has completed before the tensor memory is freed
-            if (leader) mma_commit(done);
+            if (leader && rank == 0) commit(done);
             __syncwarp();
             if (!mbar_wait(done, 0) && leader) atomicExch(v.status, (int)DEV_TIMEOUT);
         }
@@ -403,46 +483,37 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
                 const uint8_t *st = wring + s * kWStage;
                 const uint32_t *mask = (const uint32_t *)(st + kStepRec);
                 const uint32_t mw = mask[r >> 5];
-                uint4 S[4];
-                uint2 C[4];
-#pragma unroll
-                for (int t = 0; t < 4; t++) {
-                    S[t] = *(const uint4 *)(st + (o_s ^ (16u * t)));
-                    C[t] = *(const uint2 *)(st + (o_c ^ (16u * t)));
-                }
-                // hands the stage back: its reads are done before the next copy into it (the async proxy) is asked for
-                auto release = [&] {
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&wempty[s]);
-                };
-                // the words are in registers: without a verbatim run among the warp's rows (a uniform test) the stage is
-                // free before the rebuild.  Few rows are bound by the weights' bytes in flight (128 tokens, 64 experts of
-                // [2048, 1408]: 54 us); many rows lose 4% to the earlier copies.
-                const bool early = BN == 64 && !mw;
-                if (early) release();
-                if (q >= kSA && !mbar_wait(&aempty[sa], ((q / kSA) & 1) ^ 1)) { ok = false; break; }
-                tc_fence_after();
-                const uint32_t at = tmem + t_lane + kACol + 32 * sa;
                 const bool verb = (mw >> lane) & 1u;
-                const uint32_t rank = verb ? verbatim_rank(mask, r) : 0u;
+                const uint32_t run = verb ? verbatim_rank(mask, r) : 0u;
+                // The 32 words are rebuilt before the wait for a slot of tensor memory, so that a slot is held for their
+                // store alone.
+                uint32_t p[32];
 #pragma unroll
                 for (int t = 0; t < 4; t++) {
-                    uint32_t p[8];
-                    rebuild_chunk(S[t], C[t], B, p);
+                    const uint4 S = *(const uint4 *)(st + (o_s ^ (16u * t)));
+                    const uint2 C = *(const uint2 *)(st + (o_c ^ (16u * t)));
+                    uint32_t c[8];
+                    rebuild_chunk(S, C, B, c);
                     if (mw) {
                         // a verbatim run among the warp's rows (the same word for every lane)
                         if (verb) {
                             uint4 E;
-                            if (rank < (uint32_t)kVCs) E = *(const uint4 *)(st + kVOff + rank * 64 + 16 * t);
-                            else E = __ldg((const uint4 *)(v.verb + ((uint64_t)mask[4] + rank) * 64 + 16 * t));
-                            rebuild_chunk_verbatim(S[t], E, p);
+                            if (run < (uint32_t)kVCs) E = *(const uint4 *)(st + kVOff + run * 64 + 16 * t);
+                            else E = __ldg((const uint4 *)(v.verb + ((uint64_t)mask[4] + run) * 64 + 16 * t));
+                            rebuild_chunk_verbatim(S, E, c);
                         }
                         __syncwarp();
                     }
-                    tmem_st8(at + 8 * t, p);
+#pragma unroll
+                    for (int k = 0; k < 8; k++) p[8 * t + k] = c[k];
                 }
-                if (!early) release();
+                // hands the stage back: its reads are done before the next copy into it (the async proxy) is asked for
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&wempty[s]);
+                if (q >= kSA && !mbar_wait(&aempty[sa], ((q / kSA) & 1) ^ 1)) { ok = false; break; }
+                tc_fence_after();
+                tmem_st32(tmem + t_lane + kACol + 32 * sa, p);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -477,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
                 for (int j = 0; j < 16; j++) f[j] = x[j];
                 col = (int64_t)w.tile * kTileRows + 32 * q + lane;
             }
-            const int m = col < v.N ? w.n - first : 0;
+            const int m = w.real && col < v.N ? w.n - first : 0;
             const int64_t o = (int64_t)(w.r0 + first) * a.c.ldy + col;
             if (a.c.out_bf16) {
                 __nv_bfloat16 *p = (__nv_bfloat16 *)a.c.y + o;
@@ -538,33 +609,38 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
         if (!ok && lane == 0) atomicExch(v.status, (int)DEV_TIMEOUT);
     }
     tc_fence_before();
+    if constexpr (PAIR) cluster_barrier();  // neither CTA ends while the other's products read its memory
     __syncthreads();
     if (warp == kMmaWarp) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+        if constexpr (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+        else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
     }
 }
 
-template <bool GATED, bool GATHER, int BN, bool SUMS>
+template <bool GATED, bool GATHER, typename Sh, bool SUMS>
 cudaError_t launch_one(const TcArgs &a, cudaStream_t st)
 {
+    auto kernel = group_tc_kernel<GATED, GATHER, Sh, SUMS>;
     static bool attr = false;
     if (!attr) {
-        const cudaError_t e = cudaFuncSetAttribute(group_tc_kernel<GATED, GATHER, BN, SUMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<BN>::smem);
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::smem);
         if (e != cudaSuccess) return e;
         attr = true;
     }
     // at least one row tile for each BN rows, at most one more for each expert
     const GroupCall &c = a.c;
-    const int64_t most = ((c.rows + BN - 1) / BN + std::min<int64_t>(c.v.experts, c.rows)) * c.v.tiles;
-    return launch_dependent(group_tc_kernel<GATED, GATHER, BN, SUMS>, dim3((unsigned)std::min<int64_t>(num_sms(), most)), kThreads, Shape<BN>::smem, 0, st, a);
+    const int64_t row_tiles = (c.rows + Sh::BN - 1) / Sh::BN + std::min<int64_t>(c.v.experts, c.rows);
+    const int64_t units = row_tiles * (Sh::PAIR ? (c.v.tiles + 1) / 2 : c.v.tiles);
+    const int64_t grid = Sh::PAIR ? 2 * std::min<int64_t>(std::max(1, num_sms() / 2), units) : std::min<int64_t>(num_sms(), units);
+    return launch_dependent(kernel, dim3((unsigned)grid), kThreads, Sh::smem, Sh::PAIR ? 2u : 0u, st, a);
 }
 
-template <int BN, bool SUMS>
+template <typename Sh, bool SUMS>
 cudaError_t launch_shape(const TcArgs &a, cudaStream_t st)
 {
-    if (a.c.v.gated) return a.c.row_src ? launch_one<true, true, BN, SUMS>(a, st) : launch_one<true, false, BN, SUMS>(a, st);
-    return a.c.row_src ? launch_one<false, true, BN, SUMS>(a, st) : launch_one<false, false, BN, SUMS>(a, st);
+    if (a.c.v.gated) return a.c.row_src ? launch_one<true, true, Sh, SUMS>(a, st) : launch_one<true, false, Sh, SUMS>(a, st);
+    return a.c.row_src ? launch_one<false, true, Sh, SUMS>(a, st) : launch_one<false, false, Sh, SUMS>(a, st);
 }
 
 bool map_x(CUtensorMap *m, const GroupCall &c)
@@ -599,8 +675,8 @@ int launch_group_tc(const GroupCall &c, void *stream)
     // output by the larger, which a gated output cannot be.
     const bool sums = !c.out_bf16 && c.v.ksteps > kSegSteps;
     if (c.rows <= 32 * (int64_t)c.v.experts || (c.v.gated && sums))
-        return sums ? launch_shape<64, true>(a, (cudaStream_t)stream) : launch_shape<64, false>(a, (cudaStream_t)stream);
-    return launch_shape<192, false>(a, (cudaStream_t)stream);
+        return sums ? launch_shape<Shape<64, false>, true>(a, (cudaStream_t)stream) : launch_shape<Shape<64, false>, false>(a, (cudaStream_t)stream);
+    return launch_shape<Shape<192, true>, false>(a, (cudaStream_t)stream);
 }
 
 }  // namespace uw
