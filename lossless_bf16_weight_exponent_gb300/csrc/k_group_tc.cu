@@ -39,13 +39,8 @@ namespace {
 
 using namespace dev;
 
-constexpr int kGroups = 3;                    // rebuild groups of four warps
-constexpr int kRebuildWarps = 4 * kGroups;
-constexpr int kProdWarp = kRebuildWarps, kMmaWarp = kProdWarp + 1, kXWarp0 = kProdWarp + 2, kXWarps = 5;
-constexpr int kProdWarp2 = kXWarp0 + kXWarps;
-constexpr int kEpiWarp0 = kProdWarp2 + 1;  // a multiple of four: warp % 4 is the lane quarter of tensor memory
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+constexpr int kWarps = 28, kThreads = 32 * kWarps;
+constexpr int kXWarps = 5;
 constexpr int kSegSteps = 8;                  // steps of a segment (fp32 output)
 constexpr int kVCs = 8;                       // verbatim runs of a step staged with it (beyond: global loads)
 constexpr uint32_t kVOff = kStepRec + 128;    // a stage: the step with its record, then its verbatim runs
@@ -57,6 +52,12 @@ template <int BN_, bool PAIR_>
 struct Shape {
     static constexpr int BN = BN_;
     static constexpr bool PAIR = PAIR_;
+    // roles: rebuild groups of four warps, a copying warp, the issuing warp, the X warps, another copying warp, the
+    // epilogue's warps (the first a multiple of four: warp % 4 is the lane quarter of tensor memory)
+    static constexpr int Groups = PAIR ? 4 : 3, EpiWarps = PAIR ? 4 : 8;
+    static constexpr int ProdWarp = 4 * Groups, MmaWarp = ProdWarp + 1, XWarp0 = ProdWarp + 2, ProdWarp2 = XWarp0 + kXWarps;
+    static constexpr int EpiWarp0 = ProdWarp2 + 1;
+    static_assert(EpiWarp0 % 4 == 0 && EpiWarp0 + EpiWarps == kWarps, "roles");
     static constexpr int SX = kXWarps, SW = 12, SA = BN == 192 ? 4 : 8;  // stages of X, of the weights; A slots
     static constexpr int XRows = PAIR ? BN / 2 : BN;                      // rows of the X tile in a CTA
     static constexpr uint32_t XStage = XRows * 128;
@@ -66,12 +67,12 @@ struct Shape {
     // A stage of the weight ring belongs to one rebuild group and one copying warp for good.  Copies land out of order,
     // so a group that waited for a stage last read by another group could be a whole turn ahead of a copy that has not
     // landed, where the barrier's parity is the same as of the turn it waits for.  (The A slots need no such rule: products
-    // complete in order, and a group that is at step q has seen step q - kGroups - SA done.)
-    static_assert(SW % kGroups == 0 && SW % 2 == 0 && SA >= kGroups, "rings");
+    // complete in order, and a group that is at step q has seen step q - Groups - SA done.)
+    static_assert(SW % Groups == 0 && SW % 2 == 0 && SA >= Groups, "rings");
     static_assert(ACol + 32 * SA <= 512 && XRows % 32 == 0, "layout");
     static_assert((2 * (SW + SX + SA) + 5) * 8 + 8 <= 512, "barriers");
 };
-static_assert(kEpiWarp0 % 4 == 0 && kWStage % 128 == 0, "layout");
+static_assert(kWStage % 128 == 0, "layout");
 
 struct TcArgs {
     CUtensorMap tm_x;  // X [x_rows, K] bf16, box {64, 32} or (sources) {64, 1}, 128-byte swizzle
@@ -103,22 +104,43 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
-// The pair of CTAs on one product (cta_group::2): D of 256 rows, each CTA's tensor memory holds its 128 of A and D, each
-// CTA's shared memory half of the rows of B.  Issued by one thread of the first CTA.
-__device__ __forceinline__ void mma_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc)
+// Where `who` is not 0: D[tmem] (+)= A[tmem] * B[smem descriptor].  On a pair of CTAs (cta_group::2) D has 256 rows, each
+// CTA's tensor memory holds its 128 of A and D, each CTA's shared memory half of the rows of B; one thread of the first CTA
+// issues.  The guard is a predicate, not a branch: the warp stays together.
+template <bool PAIR>
+__device__ __forceinline__ void mma_if(uint32_t who, uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc)
 {
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(
-                     d_tmem),
-                 "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
-                 : "memory");
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n .reg .pred p, w;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 w, %5, 0;\n @w tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, "
+            "%3, p;\n}\n" ::"r"(d_tmem),
+            "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc), "r"(who)
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred p, w;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 w, %5, 0;\n @w tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, "
+            "%3, p;\n}\n" ::"r"(d_tmem),
+            "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc), "r"(who)
+            : "memory");
 }
 
-// arrive on this barrier in both CTAs once every product issued so far by this thread has completed
-__device__ __forceinline__ void mma_commit_pair(uint64_t *bar)
+// Where `who` is not 0: arrive on this barrier (of a pair: in both CTAs) once every product issued so far by this thread has
+// completed.
+template <bool PAIR>
+__device__ __forceinline__ void commit_if(uint32_t who, uint64_t *bar)
 {
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(saddr(bar)),
-                 "h"((uint16_t)3)
-                 : "memory");
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n .reg .pred w;\n setp.ne.b32 w, %2, 0;\n @w "
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}\n" ::"r"(saddr(bar)),
+            "h"((uint16_t)3), "r"(who)
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred w;\n setp.ne.b32 w, %1, 0;\n @w tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
+                saddr(bar)),
+            "r"(who)
+            : "memory");
 }
 
 // Arrive on the first CTA's barrier at the same place.  What it tells of are tensor-memory stores and tensor copies, which
@@ -132,15 +154,16 @@ __device__ __forceinline__ void arrive_first(uint64_t *bar)
         : "memory");
 }
 
-// mbar_wait with the other CTA's writes in view
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *b, uint32_t parity)
+// both phases complete, with the other CTA's writes in view of the first; false after kWaitLimitNs
+__device__ __forceinline__ bool mbar_wait_both(uint64_t *b1, uint32_t parity1, uint64_t *b2, uint32_t parity2)
 {
     auto test = [&] {
         uint32_t ok;
         asm volatile(
-            "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+            "{\n .reg .pred p, q;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n "
+            "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n and.pred p, p, q;\n selp.u32 %0, 1, 0, p;\n}\n"
             : "=r"(ok)
-            : "r"(saddr(b)), "r"(parity)
+            : "r"(saddr(b1)), "r"(parity1), "r"(saddr(b2)), "r"(parity2)
             : "memory");
         return ok != 0;
     };
@@ -197,6 +220,8 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
     constexpr int BN = Sh::BN, kBN = BN, kSX = Sh::SX, kSW = Sh::SW, kSA = Sh::SA, kACol = Sh::ACol;
     constexpr uint32_t kXStage = Sh::XStage;
     constexpr bool PAIR = Sh::PAIR;
+    constexpr int kGroups = Sh::Groups, kRebuildWarps = 4 * kGroups, kProdWarp = Sh::ProdWarp, kMmaWarp = Sh::MmaWarp, kXWarp0 = Sh::XWarp0;
+    constexpr int kProdWarp2 = Sh::ProdWarp2, kEpiWarp0 = Sh::EpiWarp0, kEpiWarps = Sh::EpiWarps;
     constexpr int kXRows = Sh::XRows, kNStep = PAIR ? 32 : 16;  // N is a multiple of kNStep
     const int rank = PAIR ? (int)(blockIdx.x & 1) : 0;            // in the pair
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -421,12 +446,8 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
         bool ok = true;
         int sx = 0, sa = 0, ns = 0;  // ns: segments begun
         uint32_t phx = 0, pha = 0;
-        const bool leader = elect_one();
+        const uint32_t leader = elect_one();
         const uint64_t desc0 = smem_desc_sw128(saddr(xring));
-        auto commit = [](uint64_t *bar) {
-            if constexpr (PAIR) mma_commit_pair(bar);
-            else mma_commit(bar);
-        };
         while (ok && units.next(w)) {
             const uint32_t id = idesc_bf16(PAIR ? 2 * kTileRows : kTileRows, (w.n + kNStep - 1) / kNStep * kNStep);
             for (int k0 = 0; k0 < ksteps && ok; k0 += seg_steps, ns++) {
@@ -436,25 +457,21 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
                 const uint32_t d = tmem + buf * kBN;
                 for (int j = 0; j < n; j++) {
                     // the first CTA's A barrier also counts the second's word that its A slot and X tile are there
-                    const bool there = (PAIR && rank == 0 ? mbar_wait_cluster(&afull[sa], pha) : mbar_wait(&afull[sa], pha)) && mbar_wait(&xfull[sx], phx);
-                    if (!__all_sync(0xFFFFFFFFu, there)) { ok = false; break; }
+                    if (!__all_sync(0xFFFFFFFFu, mbar_wait_both(&afull[sa], pha, &xfull[sx], phx))) { ok = false; break; }
                     tc_fence_after();
                     if (PAIR && rank == 1) {
                         tc_fence_before();
                         if (leader) arrive_first(&afull[sa]);
-                    } else if (leader) {
+                        __syncwarp();
+                    } else {
                         const uint32_t at = tmem + kACol + 32 * sa;
                         const uint64_t xd = desc0 + (uint64_t)(sx * (int)(kXStage >> 4));
 #pragma unroll
-                        for (int kk = 0; kk < 4; kk++) {
-                            if constexpr (PAIR) mma_ts_pair(d, at + 8 * kk, xd + 2 * kk, id, (j | kk) ? 1u : 0u);
-                            else mma_ts(d, at + 8 * kk, xd + 2 * kk, id, (j | kk) ? 1u : 0u);
-                        }
-                        commit(&aempty[sa]);
-                        commit(&xempty[sx]);
-                        if (j == n - 1) commit(&accfull[buf]);
+                        for (int kk = 0; kk < 4; kk++) mma_if<PAIR>(leader, d, at + 8 * kk, xd + 2 * kk, id, (j | kk) ? 1u : 0u);
+                        commit_if<PAIR>(leader, &aempty[sa]);
+                        commit_if<PAIR>(leader, &xempty[sx]);
+                        if (j == n - 1) commit_if<PAIR>(leader, &accfull[buf]);
                     }
-                    __syncwarp();
                     if (++sa == kSA) { sa = 0; pha ^= 1u; }
                     if (++sx == kSX) { sx = 0; phx ^= 1u; }
                 }
@@ -463,8 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
         if (!ok && leader) atomicExch(v.status, (int)DEV_TIMEOUT);
         if (ns > 0) {
             // every product issued has completed before the tensor memory is freed
-            if (leader && rank == 0) commit(done);
-            __syncwarp();
+            commit_if<PAIR>(rank == 0 ? leader : 0u, done);
             if (!mbar_wait(done, 0) && leader) atomicExch(v.status, (int)DEV_TIMEOUT);
         }
     } else if (warp < kRebuildWarps) {
@@ -524,7 +540,8 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
         if (!ok && lane == 0) atomicExch(v.status, (int)DEV_TIMEOUT);
     } else if (warp >= kEpiWarp0) {
         // ---------------------------------------------------------------------------------------- epilogue
-        const int q = warp & 3, half = (warp - kEpiWarp0) >> 2;
+        constexpr int kParts = kEpiWarps / 4;  // warps that share a lane quarter, 16 columns in turn
+        const int q = warp & 3, part = (warp - kEpiWarp0) >> 2;
         bool ok = true;
         int ns = 0;
         // 16 columns from c0 on into the output; add: to what an earlier segment left there (not gated)
@@ -571,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
             for (int j = 0; j < 16; j++) x[j] = __uint_as_float(u[j]);
         };
         while (ok && units.next(w)) {
-            constexpr int NC = BN / 32;  // a warp's groups of columns
+            constexpr int NC = BN / (16 * kParts);  // a warp's groups of columns
             float run[SUMS ? NC : 1][16];
             for (int k0 = 0; k0 < ksteps; k0 += seg_steps, ns++) {
                 const int buf = ns & 1;
@@ -581,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
                 if constexpr (SUMS) {
 #pragma unroll
                     for (int i = 0; i < NC; i++) {
-                        const int c0 = 16 * half + 32 * i;
+                        const int c0 = 16 * (part + kParts * i);
                         if (c0 >= w.n) continue;
                         float x[16];
                         columns(acc + c0, x);
@@ -589,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
                         for (int j = 0; j < 16; j++) run[i][j] = k0 ? run[i][j] + x[j] : x[j];
                     }
                 } else {
-                    for (int c0 = 16 * half; c0 < w.n; c0 += 32) {
+                    for (int c0 = 16 * part; c0 < w.n; c0 += 16 * kParts) {
                         float x[16];
                         columns(acc + c0, x);
                         emit(x, c0, k0 > 0);
@@ -603,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
                 if (!ok) break;
 #pragma unroll
                 for (int i = 0; i < NC; i++)
-                    if (16 * half + 32 * i < w.n) emit(run[i], 16 * half + 32 * i, false);
+                    if (16 * (part + kParts * i) < w.n) emit(run[i], 16 * (part + kParts * i), false);
             }
         }
         if (!ok && lane == 0) atomicExch(v.status, (int)DEV_TIMEOUT);
