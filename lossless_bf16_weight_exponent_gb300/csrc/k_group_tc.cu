@@ -48,13 +48,13 @@ constexpr uint32_t kWStage = kVOff + kVCs * 64;
 
 // The shapes: 192 rows of X per unit at most on a pair of CTAs, each with half of the X tile; 64 on one, where the weights
 // have most of shared memory: their bytes in flight bound a product of few rows.
-template <int BN_, bool PAIR_>
+template <int BN_, bool PAIR_, bool SUMS_>
 struct Shape {
     static constexpr int BN = BN_;
-    static constexpr bool PAIR = PAIR_;
+    static constexpr bool PAIR = PAIR_, SUMS = SUMS_;  // SUMS: an fp32 output of several segments, summed in the epilogue's registers
     // roles: rebuild groups of four warps, a copying warp, the issuing warp, the X warps, another copying warp, the
     // epilogue's warps (the first a multiple of four: warp % 4 is the lane quarter of tensor memory)
-    static constexpr int Groups = PAIR ? 4 : 3, EpiWarps = PAIR ? 4 : 8;
+    static constexpr int Groups = SUMS ? 3 : 4, EpiWarps = SUMS ? 8 : 4;
     static constexpr int ProdWarp = 4 * Groups, MmaWarp = ProdWarp + 1, XWarp0 = ProdWarp + 2, ProdWarp2 = XWarp0 + kXWarps;
     static constexpr int EpiWarp0 = ProdWarp2 + 1;
     static_assert(EpiWarp0 % 4 == 0 && EpiWarp0 + EpiWarps == kWarps, "roles");
@@ -213,13 +213,12 @@ struct Units {
     }
 };
 
-// SUMS: an fp32 output of several segments, whose sums the epilogue keeps in registers
-template <bool GATED, bool GATHER, typename Sh, bool SUMS>
+template <bool GATED, bool GATHER, typename Sh>
 __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_constant__ TcArgs a)
 {
     constexpr int BN = Sh::BN, kBN = BN, kSX = Sh::SX, kSW = Sh::SW, kSA = Sh::SA, kACol = Sh::ACol;
     constexpr uint32_t kXStage = Sh::XStage;
-    constexpr bool PAIR = Sh::PAIR;
+    constexpr bool PAIR = Sh::PAIR, SUMS = Sh::SUMS;
     constexpr int kGroups = Sh::Groups, kRebuildWarps = 4 * kGroups, kProdWarp = Sh::ProdWarp, kMmaWarp = Sh::MmaWarp, kXWarp0 = Sh::XWarp0;
     constexpr int kProdWarp2 = Sh::ProdWarp2, kEpiWarp0 = Sh::EpiWarp0, kEpiWarps = Sh::EpiWarps;
     constexpr int kXRows = Sh::XRows, kNStep = PAIR ? 32 : 16;  // N is a multiple of kNStep
@@ -635,10 +634,10 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
     }
 }
 
-template <bool GATED, bool GATHER, typename Sh, bool SUMS>
+template <bool GATED, bool GATHER, typename Sh>
 cudaError_t launch_one(const TcArgs &a, cudaStream_t st)
 {
-    auto kernel = group_tc_kernel<GATED, GATHER, Sh, SUMS>;
+    auto kernel = group_tc_kernel<GATED, GATHER, Sh>;
     static bool attr = false;
     if (!attr) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::smem);
@@ -653,11 +652,11 @@ cudaError_t launch_one(const TcArgs &a, cudaStream_t st)
     return launch_dependent(kernel, dim3((unsigned)grid), kThreads, Sh::smem, Sh::PAIR ? 2u : 0u, st, a);
 }
 
-template <typename Sh, bool SUMS>
+template <typename Sh>
 cudaError_t launch_shape(const TcArgs &a, cudaStream_t st)
 {
-    if (a.c.v.gated) return a.c.row_src ? launch_one<true, true, Sh, SUMS>(a, st) : launch_one<true, false, Sh, SUMS>(a, st);
-    return a.c.row_src ? launch_one<false, true, Sh, SUMS>(a, st) : launch_one<false, false, Sh, SUMS>(a, st);
+    if (a.c.v.gated) return a.c.row_src ? launch_one<true, true, Sh>(a, st) : launch_one<true, false, Sh>(a, st);
+    return a.c.row_src ? launch_one<false, true, Sh>(a, st) : launch_one<false, false, Sh>(a, st);
 }
 
 bool map_x(CUtensorMap *m, const GroupCall &c)
@@ -692,8 +691,8 @@ int launch_group_tc(const GroupCall &c, void *stream)
     // output by the larger, which a gated output cannot be.
     const bool sums = !c.out_bf16 && c.v.ksteps > kSegSteps;
     if (c.rows <= 32 * (int64_t)c.v.experts || (c.v.gated && sums))
-        return sums ? launch_shape<Shape<64, false>, true>(a, (cudaStream_t)stream) : launch_shape<Shape<64, false>, false>(a, (cudaStream_t)stream);
-    return launch_shape<Shape<192, true>, false>(a, (cudaStream_t)stream);
+        return sums ? launch_shape<Shape<64, false, true>>(a, (cudaStream_t)stream) : launch_shape<Shape<64, false, false>>(a, (cudaStream_t)stream);
+    return launch_shape<Shape<192, true, false>>(a, (cudaStream_t)stream);
 }
 
 }  // namespace uw
