@@ -104,43 +104,30 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
-// Where `who` is not 0: D[tmem] (+)= A[tmem] * B[smem descriptor].  On a pair of CTAs (cta_group::2) D has 256 rows, each
-// CTA's tensor memory holds its 128 of A and D, each CTA's shared memory half of the rows of B; one thread of the first CTA
-// issues.  The guard is a predicate, not a branch: the warp stays together.
+// D[tmem] (+)= A[tmem] * B[smem descriptor].  On a pair of CTAs (cta_group::2) D has 256 rows, each CTA's tensor memory holds
+// its 128 of A and D, each CTA's shared memory half of the rows of B; one thread of the first CTA issues.
 template <bool PAIR>
-__device__ __forceinline__ void mma_if(uint32_t who, uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc)
+__device__ __forceinline__ void mma_of(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc)
 {
     if constexpr (PAIR)
-        asm volatile(
-            "{\n .reg .pred p, w;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 w, %5, 0;\n @w tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, "
-            "%3, p;\n}\n" ::"r"(d_tmem),
-            "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc), "r"(who)
-            : "memory");
+        asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(
+                         d_tmem),
+                     "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
+                     : "memory");
     else
-        asm volatile(
-            "{\n .reg .pred p, w;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 w, %5, 0;\n @w tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, "
-            "%3, p;\n}\n" ::"r"(d_tmem),
-            "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc), "r"(who)
-            : "memory");
+        mma_ts(d_tmem, a_tmem, b, idesc, acc);
 }
 
-// Where `who` is not 0: arrive on this barrier (of a pair: in both CTAs) once every product issued so far by this thread has
-// completed.
+// arrive on this barrier (of a pair: in both CTAs) once every product issued so far by this thread has completed
 template <bool PAIR>
-__device__ __forceinline__ void commit_if(uint32_t who, uint64_t *bar)
+__device__ __forceinline__ void commit_to(uint64_t *bar)
 {
     if constexpr (PAIR)
-        asm volatile(
-            "{\n .reg .pred w;\n setp.ne.b32 w, %2, 0;\n @w "
-            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}\n" ::"r"(saddr(bar)),
-            "h"((uint16_t)3), "r"(who)
-            : "memory");
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(saddr(bar)),
+                     "h"((uint16_t)3)
+                     : "memory");
     else
-        asm volatile(
-            "{\n .reg .pred w;\n setp.ne.b32 w, %1, 0;\n @w tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
-                saddr(bar)),
-            "r"(who)
-            : "memory");
+        mma_commit(bar);
 }
 
 // Arrive on the first CTA's barrier at the same place.  What it tells of are tensor-memory stores and tensor copies, which
@@ -195,7 +182,7 @@ struct Units {
     __device__ __forceinline__ Units(const int *off_, const int *tcum_, const GroupView &v)
         : off(off_), tcum(tcum_), u(Sh::PAIR ? blockIdx.x >> 1 : blockIdx.x), e(0), tiles(v.tiles), per(Sh::PAIR ? (v.tiles + 1) / 2 : v.tiles)
     {
-        total = (int64_t)tcum[v.experts] * per;
+        total = (int64_t)__reduce_max_sync(0xFFFFFFFFu, tcum[v.experts]) * per;  // a uniform register
     }
     __device__ __forceinline__ bool next(Unit &w)
     {
@@ -439,48 +426,50 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
         if (!ok && lane == 0) atomicExch(v.status, (int)DEV_TIMEOUT);
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------------------------------------- MMA issue
-        // The whole warp walks the steps, so that the addresses and descriptors are uniform values; one elected thread
-        // issues.  (A loop inside `if (lane == 0)` moved every operand from an ordinary register for each instruction:
-        // 870 cycles a step at any N.)
+        // The whole warp walks the steps, so that the addresses and descriptors are uniform values, and elects the issuing
+        // thread for each step, so that the compiler sees that one thread issues.  (A loop inside `if (lane == 0)` took 870
+        // cycles a step at any N, one whose thread is elected once 600.)
         bool ok = true;
         int sx = 0, sa = 0, ns = 0;  // ns: segments begun
         uint32_t phx = 0, pha = 0;
-        const uint32_t leader = elect_one();
         const uint64_t desc0 = smem_desc_sw128(saddr(xring));
         while (ok && units.next(w)) {
-            const uint32_t id = idesc_bf16(PAIR ? 2 * kTileRows : kTileRows, (w.n + kNStep - 1) / kNStep * kNStep);
+            // reductions give uniform registers
+            const int wn = __reduce_max_sync(0xFFFFFFFFu, w.n);
+            const uint32_t id = idesc_bf16(PAIR ? 2 * kTileRows : kTileRows, (wn + kNStep - 1) / kNStep * kNStep);
             for (int k0 = 0; k0 < ksteps && ok; k0 += seg_steps, ns++) {
                 const int buf = ns & 1, n = min(seg_steps, ksteps - k0);
                 if (ns >= 2 && !__all_sync(0xFFFFFFFFu, mbar_wait(&accempty[buf], ((ns >> 1) - 1) & 1))) { ok = false; break; }
                 tc_fence_after();
-                const uint32_t d = tmem + buf * kBN;
+                const uint32_t d = buf * kBN;  // all of tensor memory is this block's: it begins at 0
                 for (int j = 0; j < n; j++) {
                     // the first CTA's A barrier also counts the second's word that its A slot and X tile are there
                     if (!__all_sync(0xFFFFFFFFu, mbar_wait_both(&afull[sa], pha, &xfull[sx], phx))) { ok = false; break; }
                     tc_fence_after();
                     if (PAIR && rank == 1) {
                         tc_fence_before();
-                        if (leader) arrive_first(&afull[sa]);
-                        __syncwarp();
-                    } else {
-                        const uint32_t at = tmem + kACol + 32 * sa;
+                        if (elect_one()) arrive_first(&afull[sa]);
+                    } else if (elect_one()) {
+                        const uint32_t at = kACol + 32 * sa;
                         const uint64_t xd = desc0 + (uint64_t)(sx * (int)(kXStage >> 4));
 #pragma unroll
-                        for (int kk = 0; kk < 4; kk++) mma_if<PAIR>(leader, d, at + 8 * kk, xd + 2 * kk, id, (j | kk) ? 1u : 0u);
-                        commit_if<PAIR>(leader, &aempty[sa]);
-                        commit_if<PAIR>(leader, &xempty[sx]);
-                        if (j == n - 1) commit_if<PAIR>(leader, &accfull[buf]);
+                        for (int kk = 0; kk < 4; kk++) mma_of<PAIR>(d, at + 8 * kk, xd + 2 * kk, id, (j | kk) ? 1u : 0u);
+                        commit_to<PAIR>(&aempty[sa]);
+                        commit_to<PAIR>(&xempty[sx]);
+                        if (j == n - 1) commit_to<PAIR>(&accfull[buf]);
                     }
+                    __syncwarp();
                     if (++sa == kSA) { sa = 0; pha ^= 1u; }
                     if (++sx == kSX) { sx = 0; phx ^= 1u; }
                 }
             }
         }
-        if (!ok && leader) atomicExch(v.status, (int)DEV_TIMEOUT);
+        if (!ok && lane == 0) atomicExch(v.status, (int)DEV_TIMEOUT);
         if (ns > 0) {
             // every product issued has completed before the tensor memory is freed
-            commit_if<PAIR>(rank == 0 ? leader : 0u, done);
-            if (!mbar_wait(done, 0) && leader) atomicExch(v.status, (int)DEV_TIMEOUT);
+            if (rank == 0 && elect_one()) commit_to<PAIR>(done);
+            __syncwarp();
+            if (!mbar_wait(done, 0) && lane == 0) atomicExch(v.status, (int)DEV_TIMEOUT);
         }
     } else if (warp < kRebuildWarps) {
         // ---------------------------------------------------------------------------------------- rebuild
