@@ -477,10 +477,10 @@ extern "C" uw_status uw_group_matmul(const uw_group *g, const uint16_t *x, int64
     c.y = y;
     c.ldy = ldy;
     c.out_bf16 = od == UW_OUT_BF16;
-    // Up to four rows an expert on average the matrix-vector kernel, which reads the weights of an expert again for every
-    // eight of its rows, else tcgen05: 64 experts of [2048, 1408] take 43 us against 49 at two rows each, 54 against 53 at
-    // four, 73 against 54 at eight.
-    const bool tc = rows > 4 * (int64_t)g->v.experts && group_tc_supported(c);
+    // Up to two rows an expert on average the matrix-vector kernel, which reads the weights of an expert again for every
+    // eight of its rows, else tcgen05: 64 experts of [2048, 1408] take 43 us against 44 at two rows each, 48 against 45 at
+    // three; 8 gated experts of [14336, 4096] 218 against 209 at four.
+    const bool tc = rows > 2 * (int64_t)g->v.experts && group_tc_supported(c);
     const cudaError_t e = (cudaError_t)(tc ? launch_group_tc(c, stream) : launch_group_gemv(c, stream));
     return e == cudaSuccess ? UW_OK : cuda_fail(e, "uw_group_matmul: launch");
 }

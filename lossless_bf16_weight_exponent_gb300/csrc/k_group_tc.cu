@@ -1,24 +1,32 @@
 // k_group_tc.cu - the grouped product for experts with many rows (sm_103a): weights rebuilt into tensor memory, tcgen05.
 //
-// A unit is one tile (128 virtual rows of an expert's matrices) times up to 192 of the expert's rows of X, over all of
-// K; one persistent CTA per SM takes every gridDim-th unit of the list (expert, row tile of X, weight tile), the weight
-// tile innermost so that CTAs that run together share their rows of X.  The list follows from the offsets, which each
-// CTA reads on the device.  Warps:
-//   - 0-11, three groups of four: group i % 3 rebuilds step i (128 rows x 64 weights).  Thread = row: four 16-byte and
+// Many rows run on pairs of CTAs (cta_group::2).  A unit is two weight tiles (2 x 128 virtual rows of an expert's matrices,
+// one for each CTA) times up to 192 of the expert's rows of X, over all of K; each CTA rebuilds its own tile, holds half of
+// the X tile and the accumulator of its 128 rows.  On a single CTA every SM took in 36.9 KB a step and the copies from L2
+// bounded it at 59 bytes a cycle; a pair takes 24.6.  Few rows run on single CTAs, up to 64 rows of X a unit, with a weight
+// ring of twelve stages: their weights' bytes in flight bound them.  Persistent CTAs take every gridDim-th unit of the list
+// (expert, row tile of X, weight tile), the weight tile innermost so that CTAs that run together share their rows of X.
+// The list follows from the offsets, which each CTA reads on the device.
+//
+// Roles of the 28 warps (first warps of the shapes without sums in the epilogue):
+//   - 0-15, four groups of four: group i % 4 rebuilds step i (128 rows x 64 weights).  Thread = row: four 16-byte and
 //     four 8-byte reads of shared memory without bank conflicts, 32 bf16 pairs, one tcgen05.st of 32 columns.  The
 //     A operand never passes through shared memory, which the X tiles need.
-//   - 12, 19: bulk copies of the steps (12 KB and the record, one run of memory) and their verbatim runs, alternate
+//   - 16, 23: bulk copies of the steps (12 KB and the record, one run of memory) and their verbatim runs, alternate
 //     steps each;
-//   - 13: one thread issues four tcgen05.mma (M = 128, N = rows of X up to a multiple of 16, K = 16) a step, A from
-//     tensor memory;
-//   - 14-18: X tiles [<= 192 rows x 64] bf16 in the 128-byte swizzle, a warp for each stage of the ring.  Rows in order
-//     come in tensor copies of 32 rows, rows with sources in tensor copies that gather four (a source outside X
-//     reads zeros).
-//   - 20-27: the epilogue of a finished unit, two warps per lane quarter of tensor memory.  In a gated tile lanes 0-15
-//     of a warp hold gate rows and lanes 16-31 the up rows that belong to them: eight exchanges between the halves per
-//     16 columns give each lane both factors of eight outputs.
-// Tensor memory: two accumulators of 192 columns, so that a unit's epilogue runs under the next unit's products, and
-// four slots of 32 columns for A (64 and eight in the shape for few rows).
+//   - 17: four tcgen05.mma a step (M = 128, or 256 on a pair; N = rows of X up to a multiple of 16, or 32; K = 16), A from
+//     tensor memory.  On a pair the first CTA issues; the second's warp passes on that its own operands are there;
+//   - 18-22: X tiles [rows x 64] bf16 in the 128-byte swizzle, a warp for each stage of the ring.  Rows in order come in
+//     tensor copies of 32 rows, rows with sources in tensor copies that gather four (a source outside X reads zeros);
+//   - 24-27: the epilogue of a finished unit, a warp per lane quarter of tensor memory.  In a gated tile lanes 0-15 of a
+//     warp hold gate rows and lanes 16-31 the up rows that belong to them: eight exchanges between the halves per 16
+//     columns give each lane both factors of eight outputs.
+// Tensor memory: two accumulators of 192 columns, so that a unit's epilogue runs under the next unit's products, and four
+// slots of 32 columns for A (64 and eight in the shape for few rows).
+//
+// Measured (K = 2048, N = 1408, gated, 4096 tokens top 8 of 64 experts): 325 us, 1.16 PFLOP/s; with the rebuild left out
+// 278, with the epilogue left out 301, with both 261.  333 tokens top 2 of 8 experts of [14336, 4096], gated: 243 us, 5.9 TB/s
+// of compressed weights.  128 tokens top 8 of 64 experts of [2048, 1408]: 52 us, 5.5 TB/s.
 // Every wait is bounded; when one runs out the kernel latches DEV_TIMEOUT, waits for its copies and products in flight,
 // frees its tensor memory and ends.
 #include <cuda.h>
@@ -511,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
 #pragma unroll
                     for (int k = 0; k < 8; k++) p[8 * t + k] = c[k];
                 }
-                // hands the stage back: its reads are done before the next copy into it (the async proxy) is asked for
+                // the stage's reads are done before the next copy into it (the async proxy) is asked for
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&wempty[s]);
@@ -674,12 +682,12 @@ int launch_group_tc(const GroupCall &c, void *stream)
     memset(&a, 0, sizeof a);
     if (!map_x(&a.tm_x, c)) return cudaErrorInvalidValue;
     a.c = c;
-    // The smaller shape up to 32 rows an expert on average: 64 experts of [2048, 1408] take 54 us against 60 at 16 rows
-    // each, 60 against 61 at 32, 79 against 63 at 64.
+    // The smaller shape up to 24 rows an expert on average: 64 experts of [2048, 1408] take 51.4 us against 54.0 at 16 rows
+    // each, 56.9 against 56.0 at 32, 74 against 59 at 64.
     // An fp32 output of several segments is summed in registers by the smaller shape, which has room for them, and in the
     // output by the larger, which a gated output cannot be.
     const bool sums = !c.out_bf16 && c.v.ksteps > kSegSteps;
-    if (c.rows <= 32 * (int64_t)c.v.experts || (c.v.gated && sums))
+    if (c.rows <= 24 * (int64_t)c.v.experts || (c.v.gated && sums))
         return sums ? launch_shape<Shape<64, false, true>>(a, (cudaStream_t)stream) : launch_shape<Shape<64, false, false>>(a, (cudaStream_t)stream);
     return launch_shape<Shape<192, true, false>>(a, (cudaStream_t)stream);
 }
