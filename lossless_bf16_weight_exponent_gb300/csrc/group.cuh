@@ -120,6 +120,8 @@ struct GroupCall {
     int out_bf16;
 };
 int launch_group_gemv(const GroupCall &c, void *stream);
+constexpr int kSegSteps = 8;  // steps of a segment: tcgen05 sums of 512 products, which fp32 additions join for an fp32 output
+inline bool group_sums(const GroupCall &c) { return !c.out_bf16 && c.v.ksteps > kSegSteps; }
 bool group_tc_supported(const GroupCall &c);
 int launch_group_tc(const GroupCall &c, void *stream);
 

@@ -49,7 +49,6 @@ using namespace dev;
 
 constexpr int kWarps = 28, kThreads = 32 * kWarps;
 constexpr int kXWarps = 5;
-constexpr int kSegSteps = 8;                  // steps of a segment (fp32 output)
 constexpr int kVCs = 8;                       // verbatim runs of a step staged with it (beyond: global loads)
 constexpr uint32_t kVOff = kStepRec + 128;    // a stage: the step with its record, then its verbatim runs
 constexpr uint32_t kWStage = kVOff + kVCs * 64;
@@ -570,9 +569,19 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
                     if (j < m) *p = __float2bfloat16_rn(f[j]);
             } else {
                 float *p = (float *)a.c.y + o;
+                if (add) {
+                    // one thread per element, so the order of the sum is fixed; added where the line is, with no load to
+                    // wait for (512 tokens top 8 of 64 [2048, 1408]: 70 us, 85 with 16 loads, adds and stores at a time).
+                    // Subnormal fp32 sums may become zero.
+#pragma unroll
+                    for (int j = 0; j < NO; j++, p += a.c.ldy)
+                        if (j < m) atomicAdd(p, f[j]);
+                    __syncwarp();
+                    return;
+                }
 #pragma unroll
                 for (int j = 0; j < NO; j++, p += a.c.ldy)
-                    if (j < m) *p = add ? *p + f[j] : f[j];
+                    if (j < m) *p = f[j];
             }
             __syncwarp();
         };
@@ -650,9 +659,15 @@ cudaError_t launch_one(const TcArgs &a, cudaStream_t st)
 }
 
 template <typename Sh>
+cudaError_t launch_gated(const TcArgs &a, cudaStream_t st)
+{
+    return a.c.row_src ? launch_one<true, true, Sh>(a, st) : launch_one<true, false, Sh>(a, st);
+}
+
+template <typename Sh>
 cudaError_t launch_shape(const TcArgs &a, cudaStream_t st)
 {
-    if (a.c.v.gated) return a.c.row_src ? launch_one<true, true, Sh>(a, st) : launch_one<true, false, Sh>(a, st);
+    if (a.c.v.gated) return launch_gated<Sh>(a, st);
     return a.c.row_src ? launch_one<false, true, Sh>(a, st) : launch_one<false, false, Sh>(a, st);
 }
 
@@ -682,13 +697,13 @@ int launch_group_tc(const GroupCall &c, void *stream)
     memset(&a, 0, sizeof a);
     if (!map_x(&a.tm_x, c)) return cudaErrorInvalidValue;
     a.c = c;
-    // The smaller shape up to 24 rows an expert on average: 64 experts of [2048, 1408] take 51.4 us against 54.0 at 16 rows
-    // each, 56.9 against 56.0 at 32, 74 against 59 at 64.
-    // An fp32 output of several segments is summed in registers by the smaller shape, which has room for them, and in the
-    // output by the larger, which a gated output cannot be.
-    const bool sums = !c.out_bf16 && c.v.ksteps > kSegSteps;
-    if (c.rows <= 24 * (int64_t)c.v.experts || (c.v.gated && sums))
-        return sums ? launch_shape<Shape<64, false, true>>(a, (cudaStream_t)stream) : launch_shape<Shape<64, false, false>>(a, (cudaStream_t)stream);
+    // A gated fp32 output of several segments is summed in registers, by the shape that has room for them.  Else pairs of CTAs,
+    // or the smaller shape up to 24 rows an expert on average: 64 experts of [2048, 1408] take 51.4 us against 54.0 at 16
+    // rows each, 56.9 against 56.0 at 32, 74 against 59 at 64.  Segments that add up in the output go to the pairs whatever
+    // the rows (62 us with sums in the smaller shape's registers, 56 on pairs at 16 rows; 69 against 59 at 32).
+    const bool sums = group_sums(c);
+    if (c.v.gated && sums) return launch_gated<Shape<64, false, true>>(a, (cudaStream_t)stream);
+    if (!sums && c.rows <= 24 * (int64_t)c.v.experts) return launch_shape<Shape<64, false, false>>(a, (cudaStream_t)stream);
     return launch_shape<Shape<192, true, false>>(a, (cudaStream_t)stream);
 }
 
