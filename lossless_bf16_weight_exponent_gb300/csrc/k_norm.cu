@@ -67,20 +67,31 @@ __device__ __forceinline__ Raw<F32> load8(const void *p, int64_t row, int D, int
         if constexpr (F32) r.b = in ? q[1] : zero;
     } else {
         uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        uint32_t piece[8 / W], high[8 / W];  // every load before the first use
 #pragma unroll
         for (int j = 0; j < 8 / W; j++) {
             const int i = piece_at<W>(c, j);
-            if (!in || i >= D) continue;
+            const bool here = in && i < D;
+            const uint8_t *q = base + (int64_t)i * (F32 ? 4 : 2);
             if constexpr (F32 && W == 2) {
-                const uint2 v = *(const uint2 *)(base + (int64_t)i * 4);
-                w[2 * j] = v.x;
-                w[2 * j + 1] = v.y;
-            } else if constexpr (F32) {
-                w[j] = *(const uint32_t *)(base + (int64_t)i * 4);
-            } else if constexpr (W == 2) {
-                w[j] = *(const uint32_t *)(base + (int64_t)i * 2);
+                const uint2 v = here ? *(const uint2 *)q : make_uint2(0, 0);
+                piece[j] = v.x;
+                high[j] = v.y;
+            } else if constexpr (F32 || W == 2) {
+                piece[j] = here ? *(const uint32_t *)q : 0u;
             } else {
-                w[j >> 1] |= (uint32_t) * (const uint16_t *)(base + (int64_t)i * 2) << (16 * (j & 1));
+                piece[j] = here ? *(const uint16_t *)q : 0u;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8 / W; j++) {
+            if constexpr (F32 && W == 2) {
+                w[2 * j] = piece[j];
+                w[2 * j + 1] = high[j];
+            } else if constexpr (F32 || W == 2) {
+                w[j] = piece[j];
+            } else if (j % 2 == 0) {
+                w[j / 2] = piece[j] | piece[j + 1] << 16;
             }
         }
         r.a = make_uint4(w[0], w[1], w[2], w[3]);
@@ -161,7 +172,7 @@ __device__ __forceinline__ float block_sum(float v, float *red)
 // CH: chunks of 8 elements a thread holds (dim <= 8 CH blockDim); TOPK: y holds expert rows; W: elements of an access;
 // RF, BF: h and h_out, y in fp32
 template <int CH, int MAXT, bool TOPK, int W, bool RF, bool BF>
-__global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) norm_kernel(const NormArgs a)
+__global__ void __launch_bounds__(MAXT, W < 8 ? 1024 / MAXT : MAXT == 256 ? 3 : 1) norm_kernel(const NormArgs a)
 {
     __shared__ float red[2][32];
     const int D = (int)a.n.dim;
@@ -185,7 +196,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) norm_kernel(const N
 #pragma unroll
             for (int q = 0; q < 8; q++) o[c][q] = 0.f;
         }
-        constexpr int kB = CH <= 2 ? 4 : 1;  // expert rows on their way
+        constexpr int kB = CH > 2 ? 1 : W == 8 ? 4 : W;  // expert rows on their way, as registers allow
         for (int j0 = 0; j0 < a.topk; j0 += kB) {
             Raw<BF> e[kB][CH];
             float w[kB];
