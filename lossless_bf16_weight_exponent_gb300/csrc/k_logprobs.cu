@@ -19,6 +19,11 @@
 // A slice in which fewer than n logits are not masked lists all of these.  Where too many reach the bound (many equal
 // logits), in a row with a NaN or an infinity, and where a row has fewer than n unmasked logits, rounds of an exact maximum
 // find the rest.
+//
+// Bound by memory for long rows: 256 rows of 128256 fp32 with the top 5 take 29 us (4.5 TB/s), 2047 rows of 32064 bf16
+// without top tokens 28.0 (4.7 TB/s; the issue slots are 68 % busy, an element is about two instructions), with the top 20
+// 56, of which the lists and ranks of 2047 rows are the half.  1 row of 128256 with the top 20 takes 10.4 us: the launch,
+// one pass over 16032 logits by each of eight CTAs and four joins.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

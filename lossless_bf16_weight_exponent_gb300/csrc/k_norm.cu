@@ -10,6 +10,9 @@
 // single elements with neighbouring threads side by side.
 // Bound by memory: 4096 rows of 4096 bf16 with residual and pre-norm take 22.4 us (6.0 TB/s), with post-norm and gate too
 // 28.1; 8192 rows of 8192 fp32 137 us (6.9 TB/s); 4096 rows of 2048 joined from 8 expert rows each 37.1 us (5.9 TB/s).
+// Rows of odd lengths, read by single elements, are bound by the loads in flight: 2258 rows of 4173 joined from 8 bf16 expert
+// rows take 140 us against 34 for their bytes, 4171 of 4098 in pairs 93 against 56.  They take 64 registers a thread and
+// fewer expert rows at once (128 registers and four: 280 and 176 us).
 // One chunk a thread took 31.3 us in the second case, four 30.5; a persistent CTA that keeps the weights and asks for its
 // next row ahead 54, as its registers leave too few rows on an SM to hide the joins.
 #include <cuda_bf16.h>

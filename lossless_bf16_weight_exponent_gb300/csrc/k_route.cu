@@ -1,14 +1,20 @@
 // k_route.cu - the router of a mixture of experts: each token's top-k experts, their weights, and the order of the
 // grouped products' rows (sm_103a).
 //
-// A warp takes a token.  A logit's sort key is its (logit + bias) mapped to an unsigned integer of the same order; a round
-// of the choice is a warp-wide maximum of the keys left and a warp-wide minimum of the experts that hold it, one
-// instruction each, so equal logits go to the lower index.
+// A warp takes a token.  A logit's sort key is its (logit + bias) mapped to an unsigned integer of the same order.  Up to 64
+// experts a round of the choice is a warp-wide maximum of the keys left and a warp-wide minimum of the experts that hold
+// it, one instruction each, so equal logits go to the lower index.  With more experts the lanes' largest keys give a bound
+// that at least k keys reach; those that do, few unless many are equal, take a lane each and are ranked.
 //
 // Rows are ordered by (expert, token) without counters whose order could change: a CTA sets, for each expert, one bit per
 // token in shared memory (a token takes an expert at most once), so a token's rank within the CTA is a population count
 // and the CTA's rows per expert are another.  The second kernel adds up the counts of the CTAs before its own and the
-// offsets.  Up to 128 tokens one CTA does everything in one launch; beyond, a CTA takes 64.
+// offsets; for many CTAs a scan between the two does.  Up to 128 tokens one CTA does everything in one launch; beyond, a CTA
+// takes 64.
+//
+// Bound by latency: 16 tokens of 64 experts (top 8) take 5.4 us, 8191 of 64 14.4, 4096 of 256 17.8 (20.4 with rounds over
+// all keys), 16384 of 256 30.6 (39.5).  Their logits alone would take 0.3, 0.6 and 2.5 us from memory; a token's loads,
+// exponentials and rounds follow on each other, the order needs every choice.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -35,7 +41,7 @@ struct RouteArgs {
     int32_t *ids;
     float *weights;
     int32_t *offsets, *row_src, *pos;
-    int32_t *counts;  // [CTAs][experts]
+    int32_t *counts;  // [CTAs][experts], with a scan [CTAs + 1][experts]
 };
 
 __device__ __forceinline__ uint32_t order_key(float f)
@@ -51,9 +57,15 @@ __device__ __forceinline__ float logit_at(const RouteArgs &a, int64_t t, int e)
     return a.bf16 ? __bfloat162float(((const __nv_bfloat16 *)a.logits)[t * a.ld + e]) : ((const float *)a.logits)[t * a.ld + e];
 }
 
-// the choice of token t by one warp; sets the token's bits (WORDS per expert)
+struct Choice {
+    uint32_t key;
+    int expert;
+    float z;
+};
+
+// the choice of token t by one warp; sets the token's bits (WORDS per expert); few: the warp's 32
 template <int PER, int WORDS>  // PER: experts per lane
-__device__ __forceinline__ void choose(const RouteArgs &a, int64_t t, int lane, uint32_t *bits, int tl)
+__device__ __forceinline__ void choose(const RouteArgs &a, int64_t t, int lane, uint32_t *bits, int tl, Choice *few)
 {
     const int E = a.r.experts, k = a.r.topk;
     float z[PER];
@@ -77,9 +89,44 @@ __device__ __forceinline__ void choose(const RouteArgs &a, int64_t t, int lane, 
 #pragma unroll
         for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, d);
     }
-    int my_e = 0;
+    int my_e = 0, place = lane < k ? lane : -1;
     float my_z = 0.f;
-    for (int j = 0; j < k; j++) {
+    bool chosen = false;
+    if constexpr (PER >= 4) {
+        // Every lane has an expert, so at least k keys reach the k-th of the lanes' largest.  They are few unless many are
+        // equal: each takes a lane, and its rank is the number of keys before it.
+        uint32_t best = key[0];
+#pragma unroll
+        for (int i = 1; i < PER; i++) best = max(best, key[i]);
+        uint32_t bound = 0u;
+        for (int j = 0; j < k; j++) {
+            bound = __reduce_max_sync(0xFFFFFFFFu, best);
+            const uint32_t who = __ballot_sync(0xFFFFFFFFu, best == bound);
+            if (lane == __ffs(who) - 1) best = 0u;
+        }
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < PER; i++) {
+            const uint32_t who = __ballot_sync(0xFFFFFFFFu, key[i] >= bound);
+            if (key[i] >= bound) {
+                const int at = n + __popc(who & ((1u << lane) - 1u));
+                if (at < 32) few[at] = Choice{key[i], lane + 32 * i, z[i]};
+            }
+            n += __popc(who);
+        }
+        __syncwarp();
+        chosen = n <= 32;
+        if (chosen) {
+            const Choice mine = lane < n ? few[lane] : Choice{0u, 0, 0.f};
+            int rank = 0;
+            for (int i = 0; i < n; i++) rank += few[i].key > mine.key || (few[i].key == mine.key && few[i].expert < mine.expert);
+            place = lane < n && rank < k ? rank : -1;
+            my_e = mine.expert;
+            my_z = mine.z;
+        }
+        __syncwarp();  // before the warp's next token
+    }
+    for (int j = 0; !chosen && j < k; j++) {
         uint32_t best = 0u;
         int first = 0;
 #pragma unroll
@@ -104,7 +151,7 @@ __device__ __forceinline__ void choose(const RouteArgs &a, int64_t t, int lane, 
         }
     }
     float w = 0.f;
-    if (lane < k) {
+    if (place >= 0) {
         if (a.r.score == UW_SCORE_SOFTMAX) w = total == 0.f ? 0.f : expf(my_z - m) / total;
         else w = 1.f / (1.f + expf(-my_z));
     }
@@ -114,9 +161,9 @@ __device__ __forceinline__ void choose(const RouteArgs &a, int64_t t, int lane, 
         for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
         w = s == 0.f ? 0.f : w / s;
     }
-    if (lane < k) {
-        a.ids[t * k + lane] = my_e;
-        a.weights[t * k + lane] = w * a.r.scale;
+    if (place >= 0) {
+        a.ids[t * k + place] = my_e;
+        a.weights[t * k + place] = w * a.r.scale;
         atomicOr(&bits[my_e * WORDS + (tl >> 5)], 1u << (tl & 31));
     }
 }
@@ -175,7 +222,8 @@ template <int PER, int TOK>
 __global__ void __launch_bounds__(kThreads) route_choose_kernel(const RouteArgs a)
 {
     constexpr int WORDS = TOK / 32;
-    extern __shared__ uint32_t bits[];                   // [experts][WORDS]
+    extern __shared__ uint32_t bits[];  // [experts][WORDS]
+    __shared__ Choice few[PER >= 4 ? kThreads / 32 : 1][32];
     const int E = a.r.experts, k = a.r.topk;
     const int64_t t0 = (int64_t)blockIdx.x * TOK;
     const int nt = (int)min((int64_t)TOK, a.tokens - t0);
@@ -183,7 +231,7 @@ __global__ void __launch_bounds__(kThreads) route_choose_kernel(const RouteArgs 
     pdl_trigger();
     pdl_wait();
     __syncthreads();
-    for (int tl = threadIdx.x >> 5; tl < nt; tl += kThreads / 32) choose<PER, WORDS>(a, t0 + tl, threadIdx.x & 31, bits, tl);
+    for (int tl = threadIdx.x >> 5; tl < nt; tl += kThreads / 32) choose<PER, WORDS>(a, t0 + tl, threadIdx.x & 31, bits, tl, few[PER >= 4 ? threadIdx.x >> 5 : 0]);
     __syncthreads();
     if (gridDim.x > 1) {
         for (int e = threadIdx.x; e < E; e += kThreads) a.counts[(int64_t)blockIdx.x * E + e] = bits_count<WORDS>(bits + e * WORDS);
@@ -203,6 +251,39 @@ __global__ void __launch_bounds__(kThreads) route_choose_kernel(const RouteArgs 
     }
 }
 
+// Many CTAs: each expert's counts become the exclusive sums over the CTAs, with the total after the last.  A CTA takes 32
+// experts, lane = expert, a warp a run of consecutive CTAs.
+__global__ void __launch_bounds__(kThreads) route_scan_kernel(const RouteArgs a, int ctas)
+{
+    __shared__ int sums[kThreads / 32][32];
+    const int E = a.r.experts, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
+    const int per = (ctas + kThreads / 32 - 1) / (kThreads / 32), c0 = min(ctas, warp * per), c1 = min(ctas, c0 + per);
+    pdl_trigger();
+    pdl_wait();
+    int32_t *const p = a.counts + e;
+    int n = 0;
+    if (e < E)
+#pragma unroll 16
+        for (int c = c0; c < c1; c++) n += p[(int64_t)c * E];
+    sums[warp][lane] = n;
+    __syncthreads();
+    if (e >= E) return;
+    int at = 0;
+    for (int w = 0; w < warp; w++) at += sums[w][lane];
+    for (int c = c0; c < c1; c += 8) {
+        int v[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] = c + i < c1 ? p[(int64_t)(c + i) * E] : 0;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            if (c + i < c1) p[(int64_t)(c + i) * E] = at;
+            at += v[i];
+        }
+    }
+    if (warp == kThreads / 32 - 1) p[(int64_t)ctas * E] = at;
+}
+
+template <bool SCANNED>
 __global__ void __launch_bounds__(kThreads) route_order_kernel(const RouteArgs a, int ctas)
 {
     constexpr int WORDS = kTokMany / 32;
@@ -212,7 +293,8 @@ __global__ void __launch_bounds__(kThreads) route_order_kernel(const RouteArgs a
     const int64_t t0 = (int64_t)blockIdx.x * kTokMany;
     const int nt = (int)min((int64_t)kTokMany, a.tokens - t0);
     for (int i = threadIdx.x; i < E * WORDS; i += kThreads) bits[i] = 0u;
-    for (int e = threadIdx.x; e < E; e += kThreads) base[e] = before[e] = 0;
+    if constexpr (!SCANNED)
+        for (int e = threadIdx.x; e < E; e += kThreads) base[e] = before[e] = 0;
     pdl_trigger();
     __syncthreads();
     pdl_wait();
@@ -220,7 +302,12 @@ __global__ void __launch_bounds__(kThreads) route_order_kernel(const RouteArgs a
     const int first = (int)threadIdx.x < nt * k ? a.ids[t0 * k + threadIdx.x] : 0;
     // rows of each expert in all CTAs, and in those before this one: the threads beyond one for each expert share the CTAs
     const int parts = max(1, kThreads / E);
-    for (int i = threadIdx.x; i < E * parts; i += kThreads) {
+    if constexpr (SCANNED) {
+        for (int e = threadIdx.x; e < E; e += kThreads) {
+            base[e] = __ldg(a.counts + (int64_t)ctas * E + e);
+            before[e] = __ldg(a.counts + (int64_t)blockIdx.x * E + e);
+        }
+    } else for (int i = threadIdx.x; i < E * parts; i += kThreads) {
         const int e = i % E, part = i / E;
         int all = 0, mine = 0;
 #pragma unroll 16
@@ -272,6 +359,16 @@ uw_status check_router(const uw_router *r, const char *who)
 
 int64_t route_ctas(int64_t tokens) { return tokens <= kTokOne ? 1 : (tokens + kTokMany - 1) / kTokMany; }
 
+// Each CTA of the order kernel reads all counts, ctas^2 experts words in all, or a scan adds them up first: 8192 tokens of
+// 64 experts take 16.2 us without the scan, 17.2 with it, of 256 22.2 and 21.3; 131072 tokens of 256 645 and 267.
+bool route_scans(const uw_router *r, int64_t ctas) { return ctas * r->experts >= 32768; }
+
+size_t workspace_bytes(const uw_router *r, int64_t tokens)
+{
+    const int64_t ctas = route_ctas(tokens);
+    return ctas == 1 ? 0 : (size_t)(ctas + route_scans(r, ctas)) * (size_t)r->experts * 4;
+}
+
 }  // namespace
 
 extern "C" uw_status uw_route_workspace_size(const uw_router *r, int64_t tokens, size_t *bytes)
@@ -282,7 +379,7 @@ extern "C" uw_status uw_route_workspace_size(const uw_router *r, int64_t tokens,
     if (s != UW_OK) return s;
     if (tokens < 0 || tokens > (((int64_t)1 << 31) - 1024) / r->topk)
         return fail(UW_ERR_SHAPE, "uw_route_workspace_size: tokens=%lld", (long long)tokens);
-    *bytes = tokens <= kTokOne ? 0 : (size_t)route_ctas(tokens) * (size_t)r->experts * 4;
+    *bytes = workspace_bytes(r, tokens);
     return UW_OK;
 }
 
@@ -303,7 +400,7 @@ extern "C" uw_status uw_route(const uw_router *r, const void *logits, uw_out_dty
         ((uintptr_t)logits & (dtype == UW_OUT_F32 ? 3 : 1)))
         return fail(UW_ERR_INVALID_ARG, "uw_route: a pointer is not aligned to its elements");
     const int64_t ctas = route_ctas(tokens);
-    const size_t need = tokens <= kTokOne ? 0 : (size_t)ctas * (size_t)r->experts * 4;
+    const size_t need = workspace_bytes(r, tokens);
     if (ws_bytes < need || (need && !ws)) return fail(UW_ERR_WORKSPACE, "uw_route: workspace %zu bytes, need %zu", ws_bytes, need);
     if ((uintptr_t)ws & 15) return fail(UW_ERR_INVALID_ARG, "uw_route: workspace not 16-byte aligned");
     const RouteArgs a{*r, logits, dtype == UW_OUT_BF16, tokens, ld, ids, weights, offsets, row_src, pos, (int32_t *)ws};
@@ -313,8 +410,13 @@ extern "C" uw_status uw_route(const uw_router *r, const void *logits, uw_out_dty
         e = cudaMemsetAsync(offsets, 0, ((size_t)r->experts + 1) * 4, st);
     } else {
         e = ctas == 1 ? launch_choose<kTokOne>(a, 1, st) : launch_choose<kTokMany>(a, ctas, st);
-        if (e == cudaSuccess && ctas > 1)
-            e = launch_dependent(route_order_kernel, dim3((unsigned)ctas), kThreads, (size_t)r->experts * (kTokMany / 8), 0, st, a, (int)ctas);
+        const size_t smem = (size_t)r->experts * (kTokMany / 8);
+        if (e == cudaSuccess && route_scans(r, ctas)) {
+            e = launch_dependent(route_scan_kernel, dim3((unsigned)(r->experts + 31) / 32), kThreads, 0, 0, st, a, (int)ctas);
+            if (e == cudaSuccess) e = launch_dependent(route_order_kernel<true>, dim3((unsigned)ctas), kThreads, smem, 0, st, a, (int)ctas);
+        } else if (e == cudaSuccess && ctas > 1) {
+            e = launch_dependent(route_order_kernel<false>, dim3((unsigned)ctas), kThreads, smem, 0, st, a, (int)ctas);
+        }
     }
     return e == cudaSuccess ? UW_OK : fail(UW_ERR_CUDA, "uw_route: launch: %s", cudaGetErrorString(e));
 }

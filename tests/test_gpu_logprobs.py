@@ -83,6 +83,19 @@ def test_logprobs(R, V, n, bf16):
 
 
 @pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("rows", ["ordinary", "rising", "few_values"])
+def test_long_lists_in_many_rows(rows, bf16):
+    R, V, n = 650, 20011, 32
+    x = logits(R, V, 9, bf16)
+    if rows == "rising":  # the first part's bound is below most of what follows
+        x = (x.float() + torch().linspace(0, 40, V)).to(x.dtype)
+    elif rows == "few_values":  # many equal logits at the bound
+        x = x.round()
+    tg = np.random.default_rng(V).integers(0, V, R)
+    check(run(x, tg, n, T=1.0), plain(x.double().numpy(), tg, n, 1.0), V)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
 @pytest.mark.parametrize("V,ld,shift", [(1, 1, 0), (5, 7, 1), (1000, 1003, 3), (4097, 4099, 0), (30001, 30017, 1)])
 def test_unaligned_rows(V, ld, shift, bf16):
     # rows begin at any element; what lies between them is not read as part of one

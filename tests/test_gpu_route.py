@@ -86,6 +86,23 @@ def test_equal_logits_go_to_the_lower_index(T):
     check(run(z, 8), plain(z, 8, uw.SCORE_SOFTMAX, None, True, 1.0))  # every token takes experts 0..7
 
 
+@pytest.mark.parametrize("T,E,k", [(60, 100, 8), (300, 256, 16), (40, 1000, 16)])
+@pytest.mark.parametrize("values", [2, 30, 1000])
+def test_equal_logits_among_many_experts(T, E, k, values):
+    rng = np.random.default_rng(E + values)
+    z = rng.integers(0, values, (T, E)).astype(np.float32)  # a few equal keys at the bound, or more than a warp can hold
+    z[0, 5:] = -np.inf
+    z[1] = -np.inf
+    check(run(z, k), plain(z, k, uw.SCORE_SOFTMAX, None, True, 1.0))
+
+
+@pytest.mark.parametrize("T,E,k", [(2049, 1024, 3), (8200, 256, 8), (65000, 33, 2)])
+def test_counts_added_up_by_the_scan(T, E, k):
+    rng = np.random.default_rng(T)
+    z = (rng.standard_normal((T, E)) + 2 * rng.standard_normal(E)).astype(np.float32)
+    check(run(z, k), plain(z, k, uw.SCORE_SOFTMAX, None, True, 1.0))
+
+
 def test_masked_experts_and_non_finite_logits():
     rng = np.random.default_rng(3)
     z = rng.standard_normal((200, 32)).astype(np.float32)
