@@ -12,9 +12,9 @@
 // offsets; for many CTAs a scan between the two does.  Up to 128 tokens one CTA does everything in one launch; beyond, a CTA
 // takes 64.
 //
-// Bound by latency: 16 tokens of 64 experts (top 8) take 5.4 us, 8191 of 64 14.4, 4096 of 256 17.8 (20.4 with rounds over
-// all keys), 16384 of 256 30.6 (39.5).  Their logits alone would take 0.3, 0.6 and 2.5 us from memory; a token's loads,
-// exponentials and rounds follow on each other, the order needs every choice.
+// Bound by latency: 16 tokens of 64 experts (top 8) take 5.4 us, 8191 of 128 13.9, 4096 of 256 17.8 (20.4 with rounds over
+// all keys), 16384 of 256 30.6 (39.5).  The bytes of the second and the last would take 0.5 and 2.8 us: a token's loads,
+// exponentials and rounds follow on each other, and the order needs every choice.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
