@@ -9,7 +9,7 @@
 // sum takes one barrier, in a fixed order.  Rows of a multiple of 8 elements are read in 16-byte pieces, others in pairs or
 // single elements with neighbouring threads side by side.
 // Bound by memory: 4096 rows of 4096 bf16 with residual and pre-norm take 22.4 us (6.0 TB/s), with post-norm and gate too
-// 28.1; 8192 rows of 8192 fp32 137 us (6.9 TB/s); 4096 rows of 2048 joined from 8 expert rows each 37.1 us (5.9 TB/s).
+// 28.8; 8192 rows of 8192 fp32 137 us (6.9 TB/s); 4096 rows of 2048 joined from 8 expert rows each 37.1 us (5.9 TB/s).
 // Rows of odd lengths, read by single elements, are bound by the loads in flight: 2258 rows of 4173 joined from 8 bf16 expert
 // rows take 140 us against 34 for their bytes, 4171 of 4098 in pairs 93 against 56.  They take 64 registers a thread and
 // fewer expert rows at once (128 registers and four: 280 and 176 us).
@@ -172,10 +172,12 @@ __device__ __forceinline__ float block_sum(float v, float *red)
     return s;
 }
 
+// Five CTAs of 256 threads an SM hide more of the joins, at 48 registers; rows of y in fp32 or joined need more (4096 rows of
+// 4096 with post-norm and gate: 28.8 us with five, 30.9 with three; all in fp32 42.3 and 41.4).
 // CH: chunks of 8 elements a thread holds (dim <= 8 CH blockDim); TOPK: y holds expert rows; W: elements of an access;
 // RF, BF: h and h_out, y in fp32
 template <int CH, int MAXT, bool TOPK, int W, bool RF, bool BF>
-__global__ void __launch_bounds__(MAXT, W < 8 ? 1024 / MAXT : MAXT == 256 ? 3 : 1) norm_kernel(const NormArgs a)
+__global__ void __launch_bounds__(MAXT, W < 8 ? 1024 / MAXT : MAXT == 256 ? (TOPK || BF ? 3 : 5) : 1) norm_kernel(const NormArgs a)
 {
     __shared__ float red[2][32];
     const int D = (int)a.n.dim;
