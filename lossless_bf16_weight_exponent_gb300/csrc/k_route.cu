@@ -63,17 +63,23 @@ struct Choice {
     float z;
 };
 
+// token t's logits, a warp's lanes side by side
+template <int PER>  // PER: experts per lane
+__device__ __forceinline__ void load_logits(const RouteArgs &a, int64_t t, int lane, float (&z)[PER])
+{
+#pragma unroll
+    for (int i = 0; i < PER; i++) z[i] = lane + 32 * i < a.r.experts ? logit_at(a, t, lane + 32 * i) : -INFINITY;
+}
+
 // the choice of token t by one warp; sets the token's bits (WORDS per expert); few: the warp's 32
-template <int PER, int WORDS>  // PER: experts per lane
-__device__ __forceinline__ void choose(const RouteArgs &a, int64_t t, int lane, uint32_t *bits, int tl, Choice *few)
+template <int PER, int WORDS>
+__device__ __forceinline__ void choose(const RouteArgs &a, int64_t t, int lane, const float (&z)[PER], uint32_t *bits, int tl, Choice *few)
 {
     const int E = a.r.experts, k = a.r.topk;
-    float z[PER];
     uint32_t key[PER];  // 0: none, or taken
 #pragma unroll
     for (int i = 0; i < PER; i++) {
         const int e = lane + 32 * i;
-        z[i] = e < E ? logit_at(a, t, e) : -INFINITY;
         key[i] = e < E ? order_key(a.r.bias ? z[i] + __ldg(a.r.bias + e) : z[i]) : 0u;
     }
     float m = -INFINITY, total = 1.f;
@@ -219,7 +225,7 @@ __device__ __forceinline__ int exclusive_sum(int *v, int E, int *wsum)
 }
 
 template <int PER, int TOK>
-__global__ void __launch_bounds__(kThreads) route_choose_kernel(const RouteArgs a)
+__global__ void __launch_bounds__(kThreads, PER <= 2 ? 2 : 1) route_choose_kernel(const RouteArgs a)
 {
     constexpr int WORDS = TOK / 32;
     extern __shared__ uint32_t bits[];  // [experts][WORDS]
@@ -228,10 +234,25 @@ __global__ void __launch_bounds__(kThreads) route_choose_kernel(const RouteArgs 
     const int64_t t0 = (int64_t)blockIdx.x * TOK;
     const int nt = (int)min((int64_t)TOK, a.tokens - t0);
     for (int i = threadIdx.x; i < E * WORDS; i += kThreads) bits[i] = 0u;
-    pdl_trigger();
     pdl_wait();
     __syncthreads();
-    for (int tl = threadIdx.x >> 5; tl < nt; tl += kThreads / 32) choose<PER, WORDS>(a, t0 + tl, threadIdx.x & 31, bits, tl, few[PER >= 4 ? threadIdx.x >> 5 : 0]);
+    const int lane = threadIdx.x & 31;
+    constexpr bool kAhead = PER <= 8;  // the next token's logits on their way during a choice, where registers allow
+    float z[PER], next[PER];
+    int tl = threadIdx.x >> 5;
+    if (tl < nt) load_logits<PER>(a, t0 + tl, lane, z);
+    for (; tl < nt; tl += kThreads / 32) {
+        const bool more = tl + kThreads / 32 < nt;
+        if (kAhead && more) load_logits<PER>(a, t0 + tl + kThreads / 32, lane, next);
+        choose<PER, WORDS>(a, t0 + tl, lane, z, bits, tl, few[PER >= 4 ? threadIdx.x >> 5 : 0]);
+        if (kAhead && more) {
+#pragma unroll
+            for (int i = 0; i < PER; i++) z[i] = next[i];
+        } else if (more) {
+            load_logits<PER>(a, t0 + tl + kThreads / 32, lane, z);
+        }
+    }
+    pdl_trigger();
     __syncthreads();
     if (gridDim.x > 1) {
         for (int e = threadIdx.x; e < E; e += kThreads) a.counts[(int64_t)blockIdx.x * E + e] = bits_count<WORDS>(bits + e * WORDS);
@@ -336,16 +357,32 @@ __global__ void __launch_bounds__(kThreads) route_order_kernel(const RouteArgs a
     }
 }
 
+// Up to a CTA for each SM no two share one: what they ask of shared memory sees to it, since behind another kernel's last
+// CTAs they would (8192 tokens of 8 experts: 11.3 us sharing, 9.0 not; 131072: 84 and 95).
+template <int PER, int TOK>
+cudaError_t launch_choose_per(const RouteArgs &a, int64_t ctas, cudaStream_t st)
+{
+    constexpr int kAlone = 120 * 1024;
+    auto kernel = route_choose_kernel<PER, TOK>;
+    static bool attr = false;
+    if (!attr) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAlone);
+        if (e != cudaSuccess) return e;
+        attr = true;
+    }
+    const size_t smem = PER <= 2 && ctas > 1 && ctas <= num_sms() ? kAlone : (size_t)a.r.experts * (TOK / 8);
+    return launch_dependent(kernel, dim3((unsigned)ctas), kThreads, smem, 0, st, a);
+}
+
 template <int TOK>
 cudaError_t launch_choose(const RouteArgs &a, int64_t ctas, cudaStream_t st)
 {
     const int E = a.r.experts;
-    auto kernel = E <= 32    ? route_choose_kernel<1, TOK>
-                  : E <= 64  ? route_choose_kernel<2, TOK>
-                  : E <= 128 ? route_choose_kernel<4, TOK>
-                  : E <= 256 ? route_choose_kernel<8, TOK>
-                             : route_choose_kernel<32, TOK>;
-    return launch_dependent(kernel, dim3((unsigned)ctas), kThreads, (size_t)E * (TOK / 8), 0, st, a);
+    return E <= 32    ? launch_choose_per<1, TOK>(a, ctas, st)
+           : E <= 64  ? launch_choose_per<2, TOK>(a, ctas, st)
+           : E <= 128 ? launch_choose_per<4, TOK>(a, ctas, st)
+           : E <= 256 ? launch_choose_per<8, TOK>(a, ctas, st)
+                      : launch_choose_per<32, TOK>(a, ctas, st);
 }
 
 uw_status check_router(const uw_router *r, const char *who)
