@@ -12,9 +12,11 @@
 // offsets; for many CTAs a scan between the two does.  Up to 128 tokens one CTA does everything in one launch; beyond, a CTA
 // takes 64.
 //
-// Bound by latency: 16 tokens of 64 experts (top 8) take 5.4 us, 8191 of 128 13.9, 4096 of 256 17.8 (20.4 with rounds over
-// all keys), 16384 of 256 30.6 (39.5).  The bytes of the second and the last would take 0.5 and 2.8 us: a token's loads,
-// exponentials and rounds follow on each other, and the order needs every choice.
+// Bound by latency: 16 tokens of 64 experts (top 8) take 5.4 us, 8192 of 64 11.4, 4096 of 256 14.0, 16384 of 256 26.8.  The
+// bytes of the second and the last would take 0.4 and 2.8 us: a token's loads, exponentials and rounds follow on each
+// other, and the order needs every choice.  Rounds over all keys took 20.4 us for 4096 of 256, ranks behind a bound 17.8,
+// the next token's logits asked for during a choice 16.0, the order kernel's CTAs kept off the SMs until the choices are
+// made 14.0.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -396,8 +398,8 @@ uw_status check_router(const uw_router *r, const char *who)
 
 int64_t route_ctas(int64_t tokens) { return tokens <= kTokOne ? 1 : (tokens + kTokMany - 1) / kTokMany; }
 
-// Each CTA of the order kernel reads all counts, ctas^2 experts words in all, or a scan adds them up first: 8192 tokens of
-// 64 experts take 16.2 us without the scan, 17.2 with it, of 256 22.2 and 21.3; 131072 tokens of 256 645 and 267.
+// Each CTA of the order kernel reads all counts, ctas^2 experts words in all, or a scan adds them up first: 16384
+// tokens of 64 experts take 16.6 us without the scan, 18.6 with it; 8192 of 256 17.9 and 16.3; 32768 of 256 73 and 47.
 bool route_scans(const uw_router *r, int64_t ctas) { return ctas * r->experts >= 32768; }
 
 size_t workspace_bytes(const uw_router *r, int64_t tokens)
