@@ -31,11 +31,13 @@
 #include <algorithm>
 #include <cmath>
 
+#include "f32x2.cuh"
 #include "launch.cuh"
 #include "uw_internal.h"
 
 namespace cg = cooperative_groups;
 using namespace uw;
+using namespace uw::dev;
 
 namespace {
 
@@ -62,36 +64,6 @@ __device__ __forceinline__ float exp2_fast(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-
-// f32x2 arithmetic
-struct Pair {
-    unsigned long long v;
-};
-__device__ __forceinline__ Pair pair(float a, float b)
-{
-    Pair p;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(a), "f"(b));
-    return p;
-}
-__device__ __forceinline__ void unpair(Pair p, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p.v)); }
-__device__ __forceinline__ Pair add2(Pair a, Pair b)
-{
-    Pair r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ Pair mul2(Pair a, Pair b)
-{
-    Pair r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c)
-{
-    Pair r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
 }
 
 // running maximum m, s = sum 2^(d scale), w = sum d 2^(d scale) with d = x - m; m is finite unless a logit is +inf

@@ -8,8 +8,8 @@
 // before the first of its two sums of squares; the weights, which all rows share, come when they are needed.  A join of a
 // sum takes one barrier, in a fixed order.  Rows of a multiple of 8 elements are read in 16-byte pieces, others in pairs or
 // single elements with neighbouring threads side by side.
-// Bound by memory: 4096 rows of 4096 bf16 with residual and pre-norm take 22.4 us (6.0 TB/s), with post-norm and gate too
-// 28.8; 8192 rows of 8192 fp32 137 us (6.9 TB/s); 4096 rows of 2048 joined from 8 expert rows each 37.1 us (5.9 TB/s).
+// Bound by memory: 4096 rows of 4096 bf16 with residual and pre-norm take 22.0 us (6.1 TB/s), with post-norm and gate too
+// 26.8 (27.5 without instructions on pairs); 8192 rows of 8192 fp32 137 us (6.9 TB/s); 4096 rows of 2048 joined from 8 expert rows each 37.1 us (5.9 TB/s).
 // Rows of odd lengths, read by single elements, are bound by the loads in flight: 2258 rows of 4173 joined from 8 bf16 expert
 // rows take 140 us against 34 for their bytes, 4171 of 4098 in pairs 93 against 56.  They take 64 registers a thread and
 // fewer expert rows at once (128 registers and four: 280 and 176 us).
@@ -20,10 +20,12 @@
 
 #include <algorithm>
 
+#include "f32x2.cuh"
 #include "launch.cuh"
 #include "uw_internal.h"
 
 using namespace uw;
+using namespace uw::dev;
 
 namespace {
 
@@ -36,6 +38,7 @@ struct NormArgs {
     const float *weights;
     int topk;
     uint16_t *u;
+    uint32_t gate_every;  // as in n, at most 2^31 (rows are fewer): a 64-bit division cost 1 us of 28
 };
 
 // eight elements as loaded: bf16 in a, fp32 in a and b
@@ -157,6 +160,36 @@ __device__ __forceinline__ void store8(void *p, int64_t row, int D, int c, const
     }
 }
 
+// a chunk's eight elements two at a time
+__device__ __forceinline__ void mul8(float (&o)[8], const float (&f)[8])
+{
+#pragma unroll
+    for (int q = 0; q < 8; q += 2) unpair(mul2(pair(o[q], o[q + 1]), pair(f[q], f[q + 1])), o[q], o[q + 1]);
+}
+__device__ __forceinline__ void scale8(float (&o)[8], float s)
+{
+#pragma unroll
+    for (int q = 0; q < 8; q += 2) unpair(mul2(pair(o[q], o[q + 1]), pair(s, s)), o[q], o[q + 1]);
+}
+// o += s f
+__device__ __forceinline__ void add8(float (&o)[8], float s, const float (&f)[8])
+{
+#pragma unroll
+    for (int q = 0; q < 8; q += 2) unpair(fma2(pair(s, s), pair(f[q], f[q + 1]), pair(o[q], o[q + 1])), o[q], o[q + 1]);
+}
+__device__ __forceinline__ Pair squares8(const float (&o)[8], Pair ss)
+{
+#pragma unroll
+    for (int q = 0; q < 8; q += 2) ss = fma2(pair(o[q], o[q + 1]), pair(o[q], o[q + 1]), ss);
+    return ss;
+}
+__device__ __forceinline__ float both(Pair p)
+{
+    float a, b;
+    unpair(p, a, b);
+    return a + b;
+}
+
 // the sum over the CTA, in a fixed order, to every thread; red: a buffer of this call's own
 __device__ __forceinline__ float block_sum(float v, float *red)
 {
@@ -173,7 +206,7 @@ __device__ __forceinline__ float block_sum(float v, float *red)
 }
 
 // Five CTAs of 256 threads an SM hide more of the joins, at 48 registers; rows of y in fp32 or joined need more (4096 rows of
-// 4096 with post-norm and gate: 28.8 us with five, 30.9 with three; all in fp32 42.3 and 41.4).
+// 4096 with post-norm and gate took 28.8 us with five, 30.9 with three; all in fp32 42.3 and 41.4).
 // CH: chunks of 8 elements a thread holds (dim <= 8 CH blockDim); TOPK: y holds expert rows; W: elements of an access;
 // RF, BF: h and h_out, y in fp32
 template <int CH, int MAXT, bool TOPK, int W, bool RF, bool BF>
@@ -183,6 +216,7 @@ __global__ void __launch_bounds__(MAXT, W < 8 ? 1024 / MAXT : MAXT == 256 ? (TOP
     const int D = (int)a.n.dim;
     const int64_t row = blockIdx.x;
     pdl_trigger();
+    const uint32_t gate_row = a.n.gate ? blockIdx.x / a.gate_every : 0u;
     pdl_wait();
     float o[CH][8];
     Raw<RF> h[CH];
@@ -220,8 +254,7 @@ __global__ void __launch_bounds__(MAXT, W < 8 ? 1024 / MAXT : MAXT == 256 ? (TOP
                 for (int c = 0; c < CH; c++) {
                     float f[8];
                     unpack8(e[j][c], f);
-#pragma unroll
-                    for (int q = 0; q < 8; q++) o[c][q] = fmaf(w[j], f[q], o[c][q]);
+                    add8(o[c], w[j], f);
                 }
         }
     } else {
@@ -239,52 +272,53 @@ __global__ void __launch_bounds__(MAXT, W < 8 ? 1024 / MAXT : MAXT == 256 ? (TOP
                 for (int q = 0; q < 8; q++) o[c][q] = 0.f;
         }
     }
-    float scale = a.n.out_scale, ss = 0.f;
+    float scale = a.n.out_scale;
+    Pair ss = pair(0.f, 0.f);
     if (a.n.post_weight) {
 #pragma unroll
-        for (int c = 0; c < CH; c++)
-#pragma unroll
-            for (int q = 0; q < 8; q++) ss = fmaf(o[c][q], o[c][q], ss);  // zeros past the row's end
-        scale *= rsqrtf(block_sum(ss, red[0]) / (float)D + a.n.eps);
-        ss = 0.f;
+        for (int c = 0; c < CH; c++) ss = squares8(o[c], ss);  // zeros past the row's end
+        scale *= rsqrtf(block_sum(both(ss), red[0]) / (float)D + a.n.eps);
+        ss = pair(0.f, 0.f);
     }
 #pragma unroll
     for (int c = 0; c < CH; c++) {
         float f[8];
-        if (a.n.post_weight) {
+        if (a.y && a.n.post_weight) {
             unpack8(load8<W, false>(a.n.post_weight, 0, D, c), f);
-#pragma unroll
-            for (int q = 0; q < 8; q++) o[c][q] *= f[q];
+            mul8(o[c], f);
         }
-        if (a.n.gate) {
-            unpack8(load8<W, false>(a.n.gate, row / a.n.gate_every, D, c), f);
-#pragma unroll
-            for (int q = 0; q < 8; q++) o[c][q] *= f[q];
+        if (a.y && a.n.gate) {
+            unpack8(load8<W, false>(a.n.gate, gate_row, D, c), f);
+            mul8(o[c], f);
         }
-        if (a.h) unpack8(h[c], f);
-#pragma unroll
-        for (int q = 0; q < 8; q++) {
-            float r = a.y ? scale * o[c][q] : 0.f;
-            if (a.h) r = fmaf(a.n.res_scale, f[q], r);
-            o[c][q] = r;
+        scale8(o[c], a.y ? scale : 0.f);
+        if (a.h) {
+            unpack8(h[c], f);
+            add8(o[c], a.n.res_scale, f);
         }
         if (a.h_out) store8<W, RF>(a.h_out, row, D, c, o[c]);
     }
     if (!a.u) return;
+    // zeros past the row's end, unless a scale is not finite
 #pragma unroll
-    for (int c = 0; c < CH; c++)
+    for (int c = 0; c < CH; c++) {
+        bool whole = true;
 #pragma unroll
-        for (int j = 0; j < 8 / W; j++)
-            if (piece_at<W>(c, j) < D)
+        for (int j = 0; j < 8 / W; j++) whole = whole && piece_at<W>(c, j) < D;
+        if (whole) ss = squares8(o[c], ss);
+        else if constexpr (W < 8) {
 #pragma unroll
-                for (int q = 0; q < W; q++) ss = fmaf(o[c][W * j + q], o[c][W * j + q], ss);
-    const float inv = rsqrtf(block_sum(ss, red[1]) / (float)D + a.n.eps);
+            for (int q = 0; q < 8; q++)
+                if (piece_at<W>(c, q / W) < D) ss = fma2(pair(o[c][q], 0.f), pair(o[c][q], 0.f), ss);
+        }
+    }
+    const float inv = rsqrtf(block_sum(both(ss), red[1]) / (float)D + a.n.eps);
 #pragma unroll
     for (int c = 0; c < CH; c++) {
         float f[8];
         unpack8(load8<W, false>(a.n.pre_weight, 0, D, c), f);
-#pragma unroll
-        for (int q = 0; q < 8; q++) f[q] *= o[c][q] * inv;
+        scale8(o[c], inv);
+        mul8(f, o[c]);
         store8<W, false>(a.u, row, D, c, f);
     }
 }
@@ -344,7 +378,7 @@ extern "C" uw_status uw_block_norm(const uw_norm *n, int64_t rows, const void *h
         !aligned16(n->pre_weight))
         return fail(UW_ERR_INVALID_ARG, "uw_block_norm: a pointer is not 16-byte aligned");
     if (rows == 0) return UW_OK;
-    const NormArgs a{*n, rows, y_rows, h, y, h_out, pos, weights, topk, u};
+    const NormArgs a{*n, rows, y_rows, h, y, h_out, pos, weights, topk, u, (uint32_t)std::min<int64_t>(n->gate_every, (int64_t)1 << 31)};
     const cudaError_t e = launch_norm(a, (cudaStream_t)stream);
     return e == cudaSuccess ? UW_OK : fail(UW_ERR_CUDA, "uw_block_norm: launch: %s", cudaGetErrorString(e));
 }
