@@ -8,7 +8,7 @@
 // (expert, row tile of X, weight tile), the weight tile innermost so that CTAs that run together share their rows of X.
 // The list follows from the offsets, which each CTA reads on the device.
 //
-// Roles of the 28 warps (first warps of the shapes without sums in the epilogue):
+// Roles of the 28 warps:
 //   - 0-15, four groups of four: group i % 4 rebuilds step i (128 rows x 64 weights).  Thread = row: four 16-byte and
 //     four 8-byte reads of shared memory without bank conflicts, 32 bf16 pairs, one tcgen05.st of 32 columns.  The
 //     A operand never passes through shared memory, which the X tiles need.
@@ -22,11 +22,13 @@
 //     warp hold gate rows and lanes 16-31 the up rows that belong to them: eight exchanges between the halves per 16
 //     columns give each lane both factors of eight outputs.
 // Tensor memory: two accumulators of 192 columns, so that a unit's epilogue runs under the next unit's products, and four
-// slots of 32 columns for A (64 and eight in the shape for few rows).
+// slots of 32 columns for A (64 and eight in the shape for few rows).  A sum of segments takes 128 columns beside two
+// accumulators of 128.
 //
 // Measured (K = 2048, N = 1408, gated, 4096 tokens top 8 of 64 experts): 325 us, 1.16 PFLOP/s; with the rebuild left out
 // 278, with the epilogue left out 301, with both 261.  333 tokens top 2 of 8 experts of [14336, 4096], gated: 243 us, 5.9 TB/s
 // of compressed weights.  128 tokens top 8 of 64 experts of [2048, 1408]: 52 us, 5.5 TB/s.
+// fp32 from segments: 453 us for the first, 218 for 4096 tokens top 8 of 64 of [2048, 1408].
 // Every wait is bounded; when one runs out the kernel latches DEV_TIMEOUT, waits for its copies and products in flight,
 // frees its tensor memory and ends.
 #include <cuda.h>
@@ -54,21 +56,23 @@ constexpr uint32_t kVOff = kStepRec + 128;    // a stage: the step with its reco
 constexpr uint32_t kWStage = kVOff + kVCs * 64;
 
 // The shapes: 192 rows of X per unit at most on a pair of CTAs, each with half of the X tile; 64 on one, where the weights
-// have most of shared memory: their bytes in flight bound a product of few rows.
+// have most of shared memory: their bytes in flight bound a product of few rows; 128 on a pair for an fp32 output of several
+// segments, whose sums take a third region of tensor memory.
 template <int BN_, bool PAIR_, bool SUMS_>
 struct Shape {
     static constexpr int BN = BN_;
-    static constexpr bool PAIR = PAIR_, SUMS = SUMS_;  // SUMS: an fp32 output of several segments, summed in the epilogue's registers
+    static constexpr bool PAIR = PAIR_, SUMS = SUMS_;  // SUMS: the segments of an fp32 output are summed in tensor memory
     // roles: rebuild groups of four warps, a copying warp, the issuing warp, the X warps, another copying warp, the
     // epilogue's warps (the first a multiple of four: warp % 4 is the lane quarter of tensor memory)
-    static constexpr int Groups = SUMS ? 3 : 4, EpiWarps = SUMS ? 8 : 4;
+    static constexpr int Groups = 4, EpiWarps = 4;
     static constexpr int ProdWarp = 4 * Groups, MmaWarp = ProdWarp + 1, XWarp0 = ProdWarp + 2, ProdWarp2 = XWarp0 + kXWarps;
     static constexpr int EpiWarp0 = ProdWarp2 + 1;
     static_assert(EpiWarp0 % 4 == 0 && EpiWarp0 + EpiWarps == kWarps, "roles");
-    static constexpr int SX = kXWarps, SW = 12, SA = BN == 192 ? 4 : 8;  // stages of X, of the weights; A slots
+    static constexpr int SX = kXWarps, SW = 12, SA = BN == 64 ? 8 : 4;   // stages of X, of the weights; A slots
     static constexpr int XRows = PAIR ? BN / 2 : BN;                      // rows of the X tile in a CTA
     static constexpr uint32_t XStage = XRows * 128;
-    static constexpr int ACol = 2 * BN;       // tensor memory: two accumulators, then the A slots of 32 columns
+    static constexpr int RunCol = 2 * BN;     // tensor memory: two accumulators, the sums of segments, the A slots of 32 columns
+    static constexpr int ACol = (SUMS ? 3 : 2) * BN;
     static constexpr size_t smem = 1024 + (size_t)SX * XStage + (size_t)SW * kWStage + 512 + 2 * 4 * (kMaxExperts + 4) + 4 * SX * XRows;
     static_assert(smem <= 227 * 1024, "shared memory");
     // A stage of the weight ring belongs to one rebuild group and one copying warp for good.  Copies land out of order,
@@ -309,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
     // A unit's sums are taken in segments of K, the two accumulators in turn: the tensor core cuts low bits off a running
     // sum at every product, an error that grows with the sum's length (2e-6 of a result at K = 4096).  For a bf16 output
     // that is far below the rounding, and a segment is all of K; an fp32 output gets segments of 512, added in fp32.
-    const int seg_steps = a.c.out_bf16 ? ksteps : kSegSteps;
+    const int seg_steps = SUMS ? kSegSteps : ksteps;
 
     if (warp == kProdWarp || warp == kProdWarp2) {
         // ---------------------------------------------------------------------------------------- weight copies
@@ -535,12 +539,11 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
         if (!ok && lane == 0) atomicExch(v.status, (int)DEV_TIMEOUT);
     } else if (warp >= kEpiWarp0) {
         // ---------------------------------------------------------------------------------------- epilogue
-        constexpr int kParts = kEpiWarps / 4;  // warps that share a lane quarter, 16 columns in turn
-        const int q = warp & 3, part = (warp - kEpiWarp0) >> 2;
+        const int q = warp & 3;
         bool ok = true;
         int ns = 0;
-        // 16 columns from c0 on into the output; add: to what an earlier segment left there (not gated)
-        auto emit = [&](const float (&x)[16], int c0, bool add) {
+        // 16 columns from c0 on into the output
+        auto emit = [&](const float (&x)[16], int c0) {
             constexpr int NO = GATED ? 8 : 16;
             float f[NO];
             int first = c0;
@@ -569,16 +572,6 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
                     if (j < m) *p = __float2bfloat16_rn(f[j]);
             } else {
                 float *p = (float *)a.c.y + o;
-                if (add) {
-                    // one thread per element, so the order of the sum is fixed; added where the line is, with no load to
-                    // wait for (512 tokens top 8 of 64 [2048, 1408]: 70 us, 85 with 16 loads, adds and stores at a time).
-                    // Subnormal fp32 sums may become zero.
-#pragma unroll
-                    for (int j = 0; j < NO; j++, p += a.c.ldy)
-                        if (j < m) atomicAdd(p, f[j]);
-                    __syncwarp();
-                    return;
-                }
 #pragma unroll
                 for (int j = 0; j < NO; j++, p += a.c.ldy)
                     if (j < m) *p = f[j];
@@ -593,39 +586,36 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
             for (int j = 0; j < 16; j++) x[j] = __uint_as_float(u[j]);
         };
         while (ok && units.next(w)) {
-            constexpr int NC = BN / (16 * kParts);  // a warp's groups of columns
-            float run[SUMS ? NC : 1][16];
             for (int k0 = 0; k0 < ksteps; k0 += seg_steps, ns++) {
                 const int buf = ns & 1;
                 if (!mbar_wait(&accfull[buf], (ns >> 1) & 1)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + buf * kBN;
-                if constexpr (SUMS) {
+                const uint32_t run = tmem + ((uint32_t)(32 * q) << 16) + Sh::RunCol;  // this warp's alone
+                for (int c0 = 0; c0 < w.n; c0 += 16) {
+                    float x[16];
+                    columns(acc + c0, x);
+                    if constexpr (SUMS) {
+                        if (k0) {
+                            float y[16];
+                            columns(run + c0, y);
 #pragma unroll
-                    for (int i = 0; i < NC; i++) {
-                        const int c0 = 16 * (part + kParts * i);
-                        if (c0 >= w.n) continue;
-                        float x[16];
-                        columns(acc + c0, x);
+                            for (int j = 0; j < 16; j++) x[j] += y[j];
+                        }
+                        if (k0 + seg_steps < ksteps) {
+                            uint32_t u[16];
 #pragma unroll
-                        for (int j = 0; j < 16; j++) run[i][j] = k0 ? run[i][j] + x[j] : x[j];
+                            for (int j = 0; j < 16; j++) u[j] = __float_as_uint(x[j]);
+                            tmem_st16(run + c0, u);
+                            continue;
+                        }
                     }
-                } else {
-                    for (int c0 = 16 * part; c0 < w.n; c0 += 16 * kParts) {
-                        float x[16];
-                        columns(acc + c0, x);
-                        emit(x, c0, k0 > 0);
-                    }
+                    emit(x, c0);
                 }
+                if constexpr (SUMS) tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&accempty[buf]);
-            }
-            if constexpr (SUMS) {
-                if (!ok) break;
-#pragma unroll
-                for (int i = 0; i < NC; i++)
-                    if (16 * (part + kParts * i) < w.n) emit(run[i], 16 * (part + kParts * i), false);
             }
         }
         if (!ok && lane == 0) atomicExch(v.status, (int)DEV_TIMEOUT);
@@ -659,15 +649,9 @@ cudaError_t launch_one(const TcArgs &a, cudaStream_t st)
 }
 
 template <typename Sh>
-cudaError_t launch_gated(const TcArgs &a, cudaStream_t st)
-{
-    return a.c.row_src ? launch_one<true, true, Sh>(a, st) : launch_one<true, false, Sh>(a, st);
-}
-
-template <typename Sh>
 cudaError_t launch_shape(const TcArgs &a, cudaStream_t st)
 {
-    if (a.c.v.gated) return launch_gated<Sh>(a, st);
+    if (a.c.v.gated) return a.c.row_src ? launch_one<true, true, Sh>(a, st) : launch_one<true, false, Sh>(a, st);
     return a.c.row_src ? launch_one<false, true, Sh>(a, st) : launch_one<false, false, Sh>(a, st);
 }
 
@@ -697,13 +681,15 @@ int launch_group_tc(const GroupCall &c, void *stream)
     memset(&a, 0, sizeof a);
     if (!map_x(&a.tm_x, c)) return cudaErrorInvalidValue;
     a.c = c;
-    // A gated fp32 output of several segments is summed in registers, by the shape that has room for them.  Else pairs of CTAs,
-    // or the smaller shape up to 24 rows an expert on average: 64 experts of [2048, 1408] take 51.4 us against 54.0 at 16
-    // rows each, 56.9 against 56.0 at 32, 74 against 59 at 64.  Segments that add up in the output go to the pairs whatever
-    // the rows (62 us with sums in the smaller shape's registers, 56 on pairs at 16 rows; 69 against 59 at 32).
-    const bool sums = group_sums(c);
-    if (c.v.gated && sums) return launch_gated<Shape<64, false, true>>(a, (cudaStream_t)stream);
-    if (!sums && c.rows <= 24 * (int64_t)c.v.experts) return launch_shape<Shape<64, false, false>>(a, (cudaStream_t)stream);
+    // An fp32 output of several segments is summed in tensor memory, by the shape that has room for it.  Adding the segments up
+    // in the output instead, by the pairs of 192 rows, took 70 us against 64 for 512 tokens top 8 of 64 experts of [2048, 1408],
+    // 278 against 218 for 4096, 212 against 134 for 333 tokens top 2 of 8 of [4096, 14336]; in the epilogue's registers, by
+    // single CTAs of 64 rows, gated, 864 against 453 for 4096 tokens top 8 of 64 of [1408, 2048], 249 against 219 for 32 top 2
+    // of 8 of [14336, 4096].
+    if (group_sums(c)) return launch_shape<Shape<128, true, true>>(a, (cudaStream_t)stream);
+    // Else pairs of CTAs, or single ones up to 24 rows an expert on average: 64 experts of [2048, 1408] take 51.4 us against
+    // 54.0 at 16 rows each, 56.9 against 56.0 at 32, 74 against 59 at 64.
+    if (c.rows <= 24 * (int64_t)c.v.experts) return launch_shape<Shape<64, false, false>>(a, (cudaStream_t)stream);
     return launch_shape<Shape<192, true, false>>(a, (cudaStream_t)stream);
 }
 
