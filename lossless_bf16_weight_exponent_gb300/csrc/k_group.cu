@@ -477,12 +477,11 @@ extern "C" uw_status uw_group_matmul(const uw_group *g, const uint16_t *x, int64
     c.y = y;
     c.ldy = ldy;
     c.out_bf16 = od == UW_OUT_BF16;
-    // With few rows an expert the matrix-vector kernel, which reads the weights of an expert again for every eight of its
-    // rows, else tcgen05.  Up to two rows on average: 64 experts of [2048, 1408] take 43 us against 44 at two rows each, 48
-    // against 45 at three; 8 gated experts of [14336, 4096] 218 against 209 at four.  Up to four where tcgen05 has to sum an
-    // fp32 output from segments: 64 experts take 47.6 us against 48.6 at three rows, 54.3 against 53.6 at four, 60.6 against
-    // 54.0 at six; 8 of [4096, 14336] 118 against 130 at four; 8 gated of [14336, 4096] 216 against 219.
-    const bool tc = rows > (group_sums(c) ? 4 : 2) * (int64_t)g->v.experts && group_tc_supported(c);
+    // Up to two rows an expert on average the matrix-vector kernel, which reads the weights of an expert again for every
+    // eight of its rows, else tcgen05.  64 experts of [2048, 1408] take 43 us against 44 at two rows each, 48 against 45 at
+    // three (fp32: 47.8, 47.6; 54.4, 53.4 at four), gated fp32 of [1408, 2048] 85.6 against 82.6 at three; 8 gated experts of
+    // [14336, 4096] 218 against 209 at four (fp32: 193.6, 200.8 at three; 217.8, 218.9 at four).
+    const bool tc = rows > 2 * (int64_t)g->v.experts && group_tc_supported(c);
     const cudaError_t e = (cudaError_t)(tc ? launch_group_tc(c, stream) : launch_group_gemv(c, stream));
     return e == cudaSuccess ? UW_OK : cuda_fail(e, "uw_group_matmul: launch");
 }

@@ -9,7 +9,7 @@
 //
 // Bound by memory, then by the latency of its loads: 1 token top 8 of 64 gated experts of [1408, 2048] takes 20.5 us (69 MB:
 // 10.3 at the copy rate, and a launch with a cold start of about 5), 8 tokens 66 us with 66 % of the DRAM rate, 43 % of
-// the integer rate (the rebuild) and 4.7 of a warp's 9 waiting cycles for memory; 32 tokens of [2048, 1408] 54 us (5.1 TB/s).
+// the integer rate (the rebuild) and 4.7 of a warp's 9 waiting cycles for memory; 16 tokens top 8 of 64 of [2048, 1408] 43 us (5.1 TB/s).
 // Eight warps a CTA rather than four where the grid is small; registers held to 96 or 80 for a third CTA an SM spilled and
 // lost.
 #include <cuda_bf16.h>
