@@ -348,6 +348,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
     const float scale = a.scale;
 
     if (threadIdx.x == 0) n_groups = n_cand = 0;
+    // The row's CTAs write into each other's shared memory: each has to be known to run first.  The arrival is here and the wait
+    // before the first of those writes, so that it costs nothing.
+    if (C > 1) cluster.barrier_arrive();
     pdl_trigger();
     __syncthreads();
     pdl_wait();
@@ -506,6 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
             have = n;
         }
     }
+    if (C > 1) cluster.barrier_wait();
     publish(row_sums, have);
     row_sync();
 

@@ -208,3 +208,23 @@ def test_refusals():
     assert status(vocab=4, n_top=5, top_ids=i, top_logprobs=o) == uw.ERR_INVALID_ARG
     assert status(entropy=o, dtype=9) == status(logits=x.data_ptr() + 2, entropy=o) == status(logits=None, entropy=o) == uw.ERR_INVALID_ARG
     assert status(vocab=0, entropy=o) == status(vocab=2 ** 24 + 1, entropy=o) == status(entropy=o, ld=99) == status(rows=-1, entropy=o) == uw.ERR_SHAPE
+
+
+def test_clusters_behind_one_another():
+    # Few rows: the CTAs of a row exchange their parts through each other's shared memory.  Calls of one, two, four and
+    # eight CTAs a row follow each other without a wait, so that CTAs begin while others end.
+    t = torch()
+    V, n = 40000, 4
+    xs = [logits(R, V, 100 + R) for R in (1, 2, 40, 70, 140, 3)]
+    dev, outs = [x.cuda() for x in xs], []
+    for _ in range(20):
+        for x in dev:
+            R = x.shape[0]
+            H, ids, top = t.empty(R, device="cuda"), t.empty(R, n, dtype=t.int32, device="cuda"), t.empty(R, n, device="cuda")
+            uw.token_logprobs(x, R, V, None, None, H, n, ids, top)
+            outs.append((H, ids, top))
+    t.cuda.synchronize()
+    for i, x in enumerate(xs):
+        want = plain(x.double().numpy(), None, n, 1.0)
+        for H, ids, top in outs[i::len(xs)]:
+            check([None, H.cpu().numpy(), ids.cpu().numpy(), top.cpu().numpy()], want, V)
