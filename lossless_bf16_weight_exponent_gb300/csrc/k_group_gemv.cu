@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) group_gemv_kernel(cons
     // the expert: blockIdx.y itself, or (fewer rows than experts) the blockIdx.y-th that has rows
     int e = blockIdx.y, lo = 0, hi = 0;
     const int R = (int)c.rows;
-    auto off = [&](int i) { return min(max(__ldg(c.offsets + i), 0), R); };
+    auto off = [&](int i) { return min(max(c.offsets[i], 0), R); };
     if (all_experts) {
         lo = off(e);
         hi = off(e + 1);
@@ -142,13 +142,13 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) group_gemv_kernel(cons
         const int r = r0 + g;
         const uint4 *xp = nullptr;
         if (r < hi) {
-            const int64_t src = c.row_src ? __ldg(c.row_src + r) : r;
+            const int64_t src = c.row_src ? c.row_src[r] : r;
             if (src >= 0 && src < c.x_rows) xp = (const uint4 *)(c.x + src * c.ldx + 16 * t + warp * kStepW);
         }
         uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0, xn0 = x0, xn1 = x0;
         if (xp && mine > 0) {
-            xn0 = __ldg(xp);
-            xn1 = __ldg(xp + 1);
+            xn0 = xp[0];
+            xn1 = xp[1];
         }
         float acc[NG][4];
 #pragma unroll
@@ -168,8 +168,8 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) group_gemv_kernel(cons
                 for (int n = 0; n < NG; n++) pn[n] = load_part(sp, gi + n, at);
                 if (xp) {
                     xp += WARPS * kStepW / 8;
-                    xn0 = __ldg(xp);
-                    xn1 = __ldg(xp + 1);
+                    xn0 = xp[0];
+                    xn1 = xp[1];
                 }
             }
 #pragma unroll

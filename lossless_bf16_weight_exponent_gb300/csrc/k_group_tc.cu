@@ -282,8 +282,8 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
             const int e = e0 + lane;
             int l = 0, h = 0;
             if (e < v.experts) {
-                l = min(max(__ldg(a.c.offsets + e), 0), R);
-                h = min(max(__ldg(a.c.offsets + e + 1), 0), R);
+                l = min(max(a.c.offsets[e], 0), R);
+                h = min(max(a.c.offsets[e + 1], 0), R);
             }
             const int t = h > l ? (h - l + kBN - 1) / kBN : 0;
             int s = t;
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
 #pragma unroll
                 for (int j = 0; j < kL; j++) {
                     const int row = x_first(q) + 32 * j + lane;
-                    r[j] = 32 * j + lane < x_rows(q) && row < q.n ? __ldg(a.c.row_src + q.r0 + row) : -1;
+                    r[j] = 32 * j + lane < x_rows(q) && row < q.n ? a.c.row_src[q.r0 + row] : -1;
                 }
             };
             Unit nx;

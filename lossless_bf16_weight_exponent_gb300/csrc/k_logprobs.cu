@@ -167,7 +167,7 @@ struct Row {
     }
     __device__ __forceinline__ uint4 load(int i) const  // i: 16-byte aligned element
     {
-        return __ldg((const uint4 *)((const uint8_t *)p + (uint32_t)i * (16u / V)));
+        return *(const uint4 *)((const uint8_t *)p + (uint32_t)i * (16u / V));
     }
     // a load with its masked logits raised to kLow or the next value below it
     static __device__ __forceinline__ uint4 raised(const uint4 &v)

@@ -226,8 +226,8 @@ __global__ void __launch_bounds__(MAXT, W < 8 ? 1024 / MAXT : MAXT == 256 ? (TOP
         int pos = -1;
         float weight = 0.f;
         if (lane < a.topk) {
-            pos = __ldg(a.pos + row * a.topk + lane);
-            weight = __ldg(a.weights + row * a.topk + lane);
+            pos = a.pos[row * a.topk + lane];
+            weight = a.weights[row * a.topk + lane];
         }
 #pragma unroll
         for (int c = 0; c < CH; c++) {

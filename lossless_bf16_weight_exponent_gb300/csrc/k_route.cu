@@ -82,7 +82,7 @@ __device__ __forceinline__ void choose(const RouteArgs &a, int64_t t, int lane, 
 #pragma unroll
     for (int i = 0; i < PER; i++) {
         const int e = lane + 32 * i;
-        key[i] = e < E ? order_key(a.r.bias ? z[i] + __ldg(a.r.bias + e) : z[i]) : 0u;
+        key[i] = e < E ? order_key(a.r.bias ? z[i] + a.r.bias[e] : z[i]) : 0u;
     }
     float m = -INFINITY, total = 1.f;
     if (a.r.score == UW_SCORE_SOFTMAX) {
@@ -327,15 +327,15 @@ __global__ void __launch_bounds__(kThreads) route_order_kernel(const RouteArgs a
     const int parts = max(1, kThreads / E);
     if constexpr (SCANNED) {
         for (int e = threadIdx.x; e < E; e += kThreads) {
-            base[e] = __ldg(a.counts + (int64_t)ctas * E + e);
-            before[e] = __ldg(a.counts + (int64_t)blockIdx.x * E + e);
+            base[e] = a.counts[(int64_t)ctas * E + e];
+            before[e] = a.counts[(int64_t)blockIdx.x * E + e];
         }
     } else for (int i = threadIdx.x; i < E * parts; i += kThreads) {
         const int e = i % E, part = i / E;
         int all = 0, mine = 0;
 #pragma unroll 16
         for (int c = part; c < ctas; c += parts) {
-            const int n = __ldg(a.counts + (int64_t)c * E + e);
+            const int n = a.counts[(int64_t)c * E + e];
             all += n;
             mine += c < (int)blockIdx.x ? n : 0;
         }

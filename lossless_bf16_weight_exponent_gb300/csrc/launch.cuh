@@ -1,6 +1,8 @@
 // launch.cuh - programmatic dependent launch: a kernel starts while the one before it on the stream drains, sets itself
 // up, and waits before it touches anything that one may write or read.  Every CTA waits, also one without work, so that
 // a grid that has ended vouches for all grids before it.
+// What an earlier kernel may write is read by plain loads alone: it changes during such a kernel's life, while __ldg (the
+// non-coherent path) is for memory that does not.  Only the frozen compressed weights go that way.
 #pragma once
 
 #include <cuda_runtime.h>
