@@ -15,7 +15,7 @@
 //   - 16, 23: bulk copies of the steps (12 KB and the record, one run of memory) and their verbatim runs, alternate
 //     steps each;
 //   - 17: four tcgen05.mma a step (M = 128, or 256 on a pair; N = rows of X up to a multiple of 16, or 32; K = 16), A from
-//     tensor memory.  On a pair the first CTA issues; the second's warp passes on that its own operands are there;
+//     tensor memory.  On a pair the first CTA issues, and its barriers count what both CTAs bring;
 //   - 18-22: X tiles [rows x 64] bf16 in the 128-byte swizzle, a warp for each stage of the ring.  Rows in order come in
 //     tensor copies of 32 rows, rows with sources in tensor copies that gather four (a source outside X reads zeros);
 //   - 24-27: the epilogue of a finished unit, a warp per lane quarter of tensor memory.  In a gated tile lanes 0-15 of a
@@ -105,14 +105,48 @@ __device__ __forceinline__ bool elect_one()
     return p != 0;
 }
 
+// the address, for both CTAs of a pair, of what lies at this address in the first one's shared memory
+__device__ __forceinline__ uint32_t in_first(uint32_t addr)
+{
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(addr));
+    return a;
+}
+
+// Tensor copies into this CTA's shared memory; on a pair the barrier is either CTA's.
 // four rows of a map whose box is one row high (a row past the end reads zeros)
+template <bool PAIR>
 __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map, int x, const int4 &y, uint32_t bar)
 {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
-        "%5, %6}], [%7];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w), "r"(bar)
-        : "memory");
+    if constexpr (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, "
+            "%4, %5, %6}], [%7];" ::"r"(dst),
+            "l"(map), "r"(x), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+            "%5, %6}], [%7];" ::"r"(dst),
+            "l"(map), "r"(x), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w), "r"(bar)
+            : "memory");
+}
+
+// a box of rows
+template <bool PAIR>
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)
+{
+    if constexpr (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                dst),
+            "l"(map), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+            "l"(map), "r"(x), "r"(y), "r"(bar)
+            : "memory");
 }
 
 // D[tmem] (+)= A[tmem] * B[smem descriptor].  On a pair of CTAs (cta_group::2) D has 256 rows, each CTA's tensor memory holds
@@ -141,30 +175,32 @@ __device__ __forceinline__ void commit_to(uint64_t *bar)
         mma_commit(bar);
 }
 
-// Arrive on the first CTA's barrier at the same place.  What it tells of are tensor-memory stores and tensor copies, which
-// the tensor-core fences and the copies' own barrier order; no ordinary store of this thread is behind it, and a release
-// at cluster scope, which would wait for those, takes 1400 cycles.
+// Arrive on the first CTA's barrier at the same place.  What it tells of is tensor memory alone, written or read by this CTA
+// and waited for, which the fences around the arrival and the wait order; no shared or global memory is handed over, so
+// the arrival is a relaxed one.
 __device__ __forceinline__ void arrive_first(uint64_t *bar)
 {
-    asm volatile(
-        "{\n .reg .b32 ra;\n mapa.shared::cluster.u32 ra, %0, 0;\n mbarrier.arrive.shared::cluster.b64 _, [ra];\n}\n" ::"r"(
-            saddr(bar))
-        : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_first(saddr(bar))) : "memory");
 }
 
-// both phases complete, with the other CTA's writes in view of the first; false after kWaitLimitNs
-__device__ __forceinline__ bool mbar_wait_both(uint64_t *b1, uint32_t parity1, uint64_t *b2, uint32_t parity2)
+// true when the phase is complete, of a barrier on which both CTAs of a pair, or copies of both, arrive
+template <bool PAIR>
+__device__ __forceinline__ bool test_of(uint64_t *b, uint32_t parity)
 {
-    auto test = [&] {
-        uint32_t ok;
-        asm volatile(
-            "{\n .reg .pred p, q;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n "
-            "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n and.pred p, p, q;\n selp.u32 %0, 1, 0, p;\n}\n"
-            : "=r"(ok)
-            : "r"(saddr(b1)), "r"(parity1), "r"(saddr(b2)), "r"(parity2)
-            : "memory");
-        return ok != 0;
-    };
+    if constexpr (!PAIR) return mbar_test(b, parity);
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(saddr(b)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// until test() holds; false after kWaitLimitNs
+template <typename T>
+__device__ __forceinline__ bool wait_until(T test)
+{
     if (test()) return true;
     const uint64_t t0 = gtime();
     for (;;) {
@@ -251,12 +287,12 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
             mbar_init(&xempty[s], 1);
         }
         for (int s = 0; s < kSA; s++) {
-            mbar_init(&afull[s], PAIR && rank == 0 ? 5 : 4);  // a rebuild group's warps, and word from the second CTA
+            mbar_init(&afull[s], PAIR && rank == 0 ? 8 : 4);  // a rebuild group's warps, in the first CTA those of both
             mbar_init(&aempty[s], 1);
         }
         for (int b = 0; b < 2; b++) {
             mbar_init(&accfull[b], 1);
-            mbar_init(&accempty[b], kEpiWarps);
+            mbar_init(&accempty[b], PAIR && rank == 0 ? 2 * kEpiWarps : kEpiWarps);
         }
         mbar_init(done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -310,6 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
     const uint32_t tmem = *tmem_slot;
     Units<Sh> units(off, tcum, v);
     Unit w;
+    const bool any = units.u < units.total;
     // A unit's sums are taken in segments of K, the two accumulators in turn: the tensor core cuts low bits off a running
     // sum at every product, an error that grows with the sum's length (2e-6 of a result at K = 4096).  For a bf16 output
     // that is far below the rounding, and a segment is all of K; an fp32 output gets segments of 512, added in fp32.
@@ -370,6 +407,11 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
         // Warp x brings steps x, x + kSX, ... into stage x: a step's copies take one warp longer than its products.
         const int x = warp - kXWarp0;
         const uint32_t xs = saddr(xring + x * kXStage);
+        // On a pair both CTAs' copies complete on the first one's barrier, which expects the bytes of both: the product that the
+        // first CTA issues reads both halves of the tile.  The second is never a turn ahead of that barrier: its stage is free
+        // once the products on the turn before, and so that turn's phase, are complete.
+        const uint32_t fb = PAIR ? in_first(saddr(&xfull[x])) : saddr(&xfull[x]);
+        const uint32_t both = PAIR ? 2 : 1;
         bool ok = true;
         int i = 0, turn = 0;  // steps before this unit, this stage's turns
         // this CTA's rows of a unit's X tile: how many, and the first (of a pair's, each half)
@@ -403,14 +445,13 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
                 for (int ks = (kSX - i % kSX + x) % kSX; ks < ksteps; ks += kSX, turn++) {
                     if (!stage_free()) { ok = false; break; }
                     if (leader) {
-                        const uint32_t fb = saddr(&xfull[x]);
-                        mbar_expect_tx(&xfull[x], (uint32_t)bn * 128u);
+                        if (rank == 0) mbar_expect_tx(&xfull[x], both * (uint32_t)bn * 128u);
                         for (int q = 0; q < bn; q += 16) {
                             int4 y[4];
 #pragma unroll
                             for (int j = 0; j < 4; j++) y[j] = *(const int4 *)(rows + q + 4 * j);
 #pragma unroll
-                            for (int j = 0; j < 4; j++) tma_gather4(xs + 128 * q + 512 * j, &a.tm_x, ks * kStepW, y[j], fb);
+                            for (int j = 0; j < 4; j++) tma_gather4<PAIR>(xs + 128 * q + 512 * j, &a.tm_x, ks * kStepW, y[j], fb);
                         }
                     }
                     __syncwarp();
@@ -424,16 +465,17 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
                 const int boxes = (x_rows(w) + 31) / 32, first = w.r0 + x_first(w);
                 for (int ks = (kSX - i % kSX + x) % kSX; ks < ksteps; ks += kSX, turn++) {
                     if (!stage_free()) { ok = false; break; }
-                    if (lane == 0) mbar_expect_tx(&xfull[x], (uint32_t)boxes * 4096u);
+                    if (rank == 0 && lane == 0) mbar_expect_tx(&xfull[x], both * (uint32_t)boxes * 4096u);
                     __syncwarp();
-                    if (lane < boxes) tma2d(xring + x * kXStage + 4096 * lane, &a.tm_x, ks * kStepW, first + 32 * lane, &xfull[x]);
+                    if (lane < boxes) tma_box<PAIR>(xs + 4096u * lane, &a.tm_x, ks * kStepW, first + 32 * lane, fb);
                     __syncwarp();
                 }
                 i += ksteps;
             }
         }
-        // the copies in flight land before the block ends
-        if (!ok && lane == 0 && turn > 0) mbar_wait(&xfull[x], (turn - 1) & 1);
+        // The copies in flight land before the block ends.  (The second CTA of a pair has no barrier of its own for them; the
+        // wait that ran out began after its last one was asked for.)
+        if (!ok && lane == 0 && turn > 0 && rank == 0) mbar_wait(&xfull[x], (turn - 1) & 1);
         if (!ok && lane == 0) atomicExch(v.status, (int)DEV_TIMEOUT);
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------------------------------------- MMA issue
@@ -444,23 +486,23 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
         int sx = 0, sa = 0, ns = 0;  // ns: segments begun
         uint32_t phx = 0, pha = 0;
         const uint64_t desc0 = smem_desc_sw128(saddr(xring));
-        while (ok && units.next(w)) {
+        while (rank == 0 && ok && units.next(w)) {
             // reductions give uniform registers
             const int wn = __reduce_max_sync(0xFFFFFFFFu, w.n);
             const uint32_t id = idesc_bf16(PAIR ? 2 * kTileRows : kTileRows, (wn + kNStep - 1) / kNStep * kNStep);
             for (int k0 = 0; k0 < ksteps && ok; k0 += seg_steps, ns++) {
                 const int buf = ns & 1, n = min(seg_steps, ksteps - k0);
-                if (ns >= 2 && !__all_sync(0xFFFFFFFFu, mbar_wait(&accempty[buf], ((ns >> 1) - 1) & 1))) { ok = false; break; }
+                if (ns >= 2 && !__all_sync(0xFFFFFFFFu, wait_until([&] { return test_of<PAIR>(&accempty[buf], ((ns >> 1) - 1) & 1); }))) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t d = buf * kBN;  // all of tensor memory is this block's: it begins at 0
                 for (int j = 0; j < n; j++) {
-                    // the first CTA's A barrier also counts the second's word that its A slot and X tile are there
-                    if (!__all_sync(0xFFFFFFFFu, mbar_wait_both(&afull[sa], pha, &xfull[sx], phx))) { ok = false; break; }
+                    auto operands = [&] {
+                        const bool p = test_of<PAIR>(&afull[sa], pha), q = test_of<PAIR>(&xfull[sx], phx);
+                        return p && q;
+                    };
+                    if (!__all_sync(0xFFFFFFFFu, wait_until(operands))) { ok = false; break; }
                     tc_fence_after();
-                    if (PAIR && rank == 1) {
-                        tc_fence_before();
-                        if (elect_one()) arrive_first(&afull[sa]);
-                    } else if (elect_one()) {
+                    if (elect_one()) {
                         const uint32_t at = kACol + 32 * sa;
                         const uint64_t xd = desc0 + (uint64_t)(sx * (int)(kXStage >> 4));
 #pragma unroll
@@ -478,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
         if (!ok && lane == 0) atomicExch(v.status, (int)DEV_TIMEOUT);
         if (ns > 0) {
             // every product issued has completed before the tensor memory is freed
-            if (rank == 0 && elect_one()) commit_to<PAIR>(done);
+            if (elect_one()) commit_to<PAIR>(done);
             __syncwarp();
             if (!mbar_wait(done, 0) && lane == 0) atomicExch(v.status, (int)DEV_TIMEOUT);
         }
@@ -532,7 +574,10 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&afull[sa]);
+                if (lane == 0) {
+                    if (PAIR && rank == 1) arrive_first(&afull[sa]);
+                    else mbar_arrive(&afull[sa]);
+                }
             }
             i += ksteps;
         }
@@ -615,13 +660,22 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
                 if constexpr (SUMS) tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&accempty[buf]);
+                if (lane == 0) {
+                    if (PAIR && rank == 1) arrive_first(&accempty[buf]);
+                    else mbar_arrive(&accempty[buf]);
+                }
             }
         }
         if (!ok && lane == 0) atomicExch(v.status, (int)DEV_TIMEOUT);
     }
     tc_fence_before();
-    if constexpr (PAIR) cluster_barrier();  // neither CTA ends while the other's products read its memory
+    if constexpr (PAIR) {
+        // Neither CTA ends while products read its memory, or while word of them is on its way: of the second's barriers `done`
+        // is the last to be told, after its accumulators, which its epilogue has seen.
+        __syncthreads();
+        if (rank == 1 && any && warp == kMmaWarp && !mbar_wait(done, 0) && lane == 0) atomicExch(v.status, (int)DEV_TIMEOUT);
+        cluster_barrier();
+    }
     __syncthreads();
     if (warp == kMmaWarp) {
         tc_fence_after();

@@ -322,3 +322,26 @@ def test_long_sums_in_fp32(rows_each, gated):
     y = run(uw.Group(dev(w), dev(u) if gated else None), dev(x), dev(off), rows, False)
     ref, _ = reference(w, u if gated else None, f64(x), np.arange(rows), off, rows)
     assert np.linalg.norm(y - ref) <= (2.1 if gated else 1.0) * 48 * 2.0 ** -24 * np.linalg.norm(ref)
+
+
+# More units than CTAs in each of the tcgen05 shapes, K no multiple of a segment of 512, an odd number of weight tiles, so that
+# every ring and both accumulators go on from one unit to the next: pairs of 192 rows, single CTAs of 64, sums of segments.
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("E,mean,N,out_bf16", [(6, 450, 2180, True), (20, 20, 1300, True), (6, 380, 1700, False)])
+def test_many_units(E, mean, N, out_bf16, gated, gather):
+    K, rng = 704, np.random.default_rng(mean)
+    N = N // 2 if gated else N
+    c = rng.integers(mean // 2, mean + mean // 2, E)
+    c[E // 2] = 0
+    off, rows = offsets_of(c), int(sum(c))
+    assert 2 * E < rows and (rows <= 24 * E) == (mean == 20)
+    T = rows // 3 if gather else rows
+    src = rng.integers(-1, T + 1, rows) if gather else np.arange(rows)
+    w, u = weights(E, N, K, 111), weights(E, N, K, 112) if gated else None
+    x = synth.fill((T, K), seed=113)
+    ref, bound = reference(w, u, f64(x), src, off, rows)
+    g = uw.Group(dev(w), dev(u) if gated else None)
+    a = run(g, dev(x), dev(off), rows, out_bf16, src=dev(src.astype(np.int32)) if gather else None)
+    check(a, ref, bound, out_bf16)
+    assert np.array_equal(a, run(g, dev(x), dev(off), rows, out_bf16, src=dev(src.astype(np.int32)) if gather else None))
