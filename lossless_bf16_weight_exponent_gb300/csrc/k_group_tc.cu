@@ -183,17 +183,25 @@ __device__ __forceinline__ void arrive_first(uint64_t *bar)
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_first(saddr(bar))) : "memory");
 }
 
-// true when the phase is complete, of a barrier on which both CTAs of a pair, or copies of both, arrive
-template <bool PAIR>
+// True when the phase is complete.  On a pair both CTAs' copies, or both CTAs' warps, arrive on the barrier: copies hand over
+// shared memory, so the wait for them acquires at cluster scope, warps tensor memory alone (RELAXED).
+template <bool PAIR, bool RELAXED>
 __device__ __forceinline__ bool test_of(uint64_t *b, uint32_t parity)
 {
     if constexpr (!PAIR) return mbar_test(b, parity);
     uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(saddr(b)), "r"(parity)
-        : "memory");
+    if constexpr (RELAXED)
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(saddr(b)), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(saddr(b)), "r"(parity)
+            : "memory");
     return ok != 0;
 }
 
@@ -492,12 +500,12 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
             const uint32_t id = idesc_bf16(PAIR ? 2 * kTileRows : kTileRows, (wn + kNStep - 1) / kNStep * kNStep);
             for (int k0 = 0; k0 < ksteps && ok; k0 += seg_steps, ns++) {
                 const int buf = ns & 1, n = min(seg_steps, ksteps - k0);
-                if (ns >= 2 && !__all_sync(0xFFFFFFFFu, wait_until([&] { return test_of<PAIR>(&accempty[buf], ((ns >> 1) - 1) & 1); }))) { ok = false; break; }
+                if (ns >= 2 && !__all_sync(0xFFFFFFFFu, wait_until([&] { return test_of<PAIR, true>(&accempty[buf], ((ns >> 1) - 1) & 1); }))) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t d = buf * kBN;  // all of tensor memory is this block's: it begins at 0
                 for (int j = 0; j < n; j++) {
                     auto operands = [&] {
-                        const bool p = test_of<PAIR>(&afull[sa], pha), q = test_of<PAIR>(&xfull[sx], phx);
+                        const bool p = test_of<PAIR, true>(&afull[sa], pha), q = test_of<PAIR, false>(&xfull[sx], phx);
                         return p && q;
                     };
                     if (!__all_sync(0xFFFFFFFFu, wait_until(operands))) { ok = false; break; }
