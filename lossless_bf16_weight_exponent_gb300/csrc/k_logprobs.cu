@@ -6,7 +6,8 @@
 // scaling); differences to the maximum are taken in the logits' own units, where they are exact or nearly so.  The sums
 // are kept in pairs (f32x2 instructions): an element costs its conversion, a comparison, a power and half of five others.
 // Logits below -1e37, masked ones above all, count as -1e37: no infinity meets a zero in the sums.  A row whose maximum is
-// not above -1e36, or that holds a NaN or +inf (which make s a NaN), is summed again by an exact path.
+// not above -1e36, that holds a NaN or +inf (which make s a NaN), or whose w is past the range (a difference to a maximum above
+// 3.3e38 is) is summed again by an exact path, with w in the scaled units.
 //
 // A row is the work of a cluster of CTAs (one for many rows, up to eight for few), each on a slice; the leader joins the
 // slices' sums and candidates through distributed shared memory in a fixed order.
@@ -141,12 +142,19 @@ __device__ __forceinline__ float clamp_low(float x)
     return y;
 }
 
-// the exact path: m may be -inf (nothing but masked tokens so far)
+// The exact path: m may be -inf (nothing but masked tokens so far), and w is the sum of z 2^z with z = d scale, which ends
+// where 2^z does.  Halves keep the difference of two finite logits within the range.
 __device__ __forceinline__ Sums join_exact(const Sums &a, const Sums &b, float scale)
 {
     if (a.m == -INFINITY && a.s == 0.f) return b;
     if (b.m == -INFINITY && b.s == 0.f) return a;
-    return join(a, b, scale);
+    Sums r;
+    r.m = fmaxf(a.m, b.m);
+    const float za = 2.f * ((0.5f * a.m - 0.5f * r.m) * scale), zb = 2.f * ((0.5f * b.m - 0.5f * r.m) * scale);
+    const float ea = exp2_fast(za), eb = exp2_fast(zb);
+    r.s = a.s * ea + b.s * eb;
+    r.w = (ea == 0.f ? 0.f : ea * fmaf(za, a.s, a.w)) + (eb == 0.f ? 0.f : eb * fmaf(zb, b.s, b.w));
+    return r;
 }
 
 __device__ __forceinline__ unsigned long long key_of(float x, uint32_t i)
@@ -520,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
         row_n = 0;
         for (int i = 0; i < C; i++) row_n += row_have[i];
     }
-    const bool again = !(row_sums.m > -1e36f) || row_sums.s != row_sums.s;
+    const bool again = !(row_sums.m > -1e36f) || row_sums.s != row_sums.s || !isfinite(row_sums.w);
     const bool lack = n && row_n < n;
     if (again || lack) {
         if (lack) rounds(have);
@@ -539,13 +547,18 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
     if (c == 0) {
         const bool none = row_sums.s == 0.f;  // nothing but masked tokens
         const float log_s = logf(row_sums.s);
-        auto lp_of = [&](float x) { return none ? -INFINITY : (x - row_sums.m) * a.inv_t - log_s; };
+        auto lp_of = [&](float x) {
+            const float d = x - row_sums.m;
+            const float z = isinf(d) ? 2.f * ((0.5f * x - 0.5f * row_sums.m) * a.inv_t) : d * a.inv_t;  // past the range as a difference alone
+            return none ? -INFINITY : z - log_s;
+        };
+        const float unit = again ? 0.69314718f : a.inv_t;  // of w
         if (threadIdx.x == 0) {
             if (a.logprob) {
                 const int32_t tg = a.targets[row];
                 a.logprob[row] = tg < 0 ? 0.f : tg >= vocab ? __int_as_float(0x7FC00000) : lp_of(r.at(tg));
             }
-            if (a.entropy) a.entropy[row] = none ? 0.f : log_s - row_sums.w / row_sums.s * a.inv_t;
+            if (a.entropy) a.entropy[row] = none ? 0.f : log_s - row_sums.w / row_sums.s * unit;
         }
         if (n) {
             for (int i = threadIdx.x; i < C * n; i += kThreads) {

@@ -228,3 +228,26 @@ def test_clusters_behind_one_another():
         want = plain(x.double().numpy(), None, n, 1.0)
         for H, ids, top in outs[i::len(xs)]:
             check([None, H.cpu().numpy(), ids.cpu().numpy(), top.cpu().numpy()], want, V)
+
+
+def as_f32(want):
+    with np.errstate(over="ignore"):
+        return [None if w is None else w if w.dtype.kind == "i" else w.astype(np.float32) for w in want]
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("T", [1.0, 4.0])
+@pytest.mark.parametrize("V", [60, 20000, 70000])
+def test_logits_of_the_types_largest_value(V, T, bf16):
+    # finite logits over the type's whole range, beside masked tokens: differences to the maximum may be past the range
+    t = torch()
+    x = logits(5, V, 21, bf16)
+    big = t.finfo(x.dtype).max
+    x[0, 7] = big                                     # one forced token
+    x[1, 7], x[1, 9:40] = big, -float("inf")
+    x[2, 3:5], x[2, 20:30] = big, -big                # two of them, and the lowest
+    x[3] = -float("inf")
+    x[3, 5], x[3, 11], x[3, V - 1] = big, -big, -1.5e37
+    x[4], x[4, 12] = -1.5e37, -1e36
+    for tg in ([7, 7, 4, 5, 12], [3, 8, 20, 11, 13], [0, 10, 0, V - 1, 0]):
+        check(run(x, tg, 6, T=T), as_f32(plain(x.double().numpy(), tg, 6, T)), V)
