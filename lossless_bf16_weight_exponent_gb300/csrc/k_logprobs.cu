@@ -7,7 +7,7 @@
 // are kept in pairs (f32x2 instructions): an element costs its conversion, a comparison, a power and half of five others.
 // Logits below -1e37, masked ones above all, count as -1e37: no infinity meets a zero in the sums.  A row whose maximum is
 // not above -1e36, that holds a NaN or +inf (which make s a NaN), or whose w is past the range (a difference to a maximum above
-// 3.3e38 is) is summed again by an exact path, with w in the scaled units.
+// 3.3e38 is) is summed again by an exact path, with w in the scaled units; so is every row at temperatures above 7e34.
 //
 // A row is the work of a cluster of CTAs (one for many rows, up to eight for few), each on a slice; the leader joins the
 // slices' sums and candidates through distributed shared memory in a fixed order.
@@ -47,6 +47,7 @@ constexpr int kCand = 1024;            // logits listed for the top tokens
 constexpr int kGroups = 1024;          // groups of loads that hold one
 constexpr int kUnroll = 4;             // 16-byte loads of a thread on their way
 constexpr float kLow = -1e37f;         // masked logits count as this, or in bf16 as the next value below it
+constexpr float kLeastScale = 2e-35f;  // below, what counts as kLow would keep a probability beside a maximum of -1e36
 constexpr int kMaxCluster = 8;
 
 struct LpArgs {
@@ -528,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
         row_n = 0;
         for (int i = 0; i < C; i++) row_n += row_have[i];
     }
-    const bool again = !(row_sums.m > -1e36f) || row_sums.s != row_sums.s || !isfinite(row_sums.w);
+    const bool again = !(row_sums.m > -1e36f) || row_sums.s != row_sums.s || !isfinite(row_sums.w) || scale < kLeastScale;
     const bool lack = n && row_n < n;
     if (again || lack) {
         if (lack) rounds(have);

@@ -251,3 +251,16 @@ def test_logits_of_the_types_largest_value(V, T, bf16):
     x[4], x[4, 12] = -1.5e37, -1e36
     for tg in ([7, 7, 4, 5, 12], [3, 8, 20, 11, 13], [0, 10, 0, V - 1, 0]):
         check(run(x, tg, 6, T=T), as_f32(plain(x.double().numpy(), tg, 6, T)), V)
+
+
+@pytest.mark.parametrize("T", [1e-30, 1e10, 1e30, 1e36, 3e38])
+@pytest.mark.parametrize("V", [60, 20000])
+def test_temperatures_far_from_one(V, T):
+    t = torch()
+    x = logits(4, V, 23) * max(1.0, min(T, 1e37)) if T > 1 else logits(4, V, 23) * T
+    x[1, 5:50] = -float("inf")
+    x[2, ::3] = t.finfo(t.float32).min
+    x[3, 1:] = -float("inf")
+    T = float(np.float32(T))
+    tg = [2, 3, 4, 0]
+    check(run(x, tg, 4, T=T), as_f32(plain(x.double().numpy(), tg, 4, T)), V)
