@@ -433,6 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
         }
     };
     const int nv = sl.v1 - sl.v0;
+    const float unmasked = BF16 ? __uint_as_float(0xFCF00000u) : __uint_as_float(__float_as_uint(kLow) - 1);  // the lowest such logit
     int done = sl.v0;
     if (n) {
         constexpr int kStep = kUnroll * kThreads;
@@ -441,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
         sweep(sl.v0 + threadIdx.x, done);
         bound = bound_of<kWarps>(sums.m, min(kWarps, first / 32), n, bounds);
         // no bound above the masked logits: every logit above them is listed
-        bound = fmaxf(bound, BF16 ? __uint_as_float(0xFCF00000u) : __uint_as_float(__float_as_uint(kLow) - 1));
+        bound = fmaxf(bound, unmasked);
         if (sums.m >= bound)
             for (int v = sl.v0 + threadIdx.x; v < done; v += kStep) note(v, sums.m);
     }
@@ -515,7 +516,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
             // a NaN or +inf, or a list that is too long
             __syncthreads();
             rounds(0);
-            have = n;
+            // Of these the unmasked count, as in a list: which masked ones are among the row's top is up to all its slices.
+            const unsigned long long least = key_of(unmasked, ~0u);
+            for (int j = 0; j < n; j++) have += best[j] >= least;
         }
     }
     if (C > 1) cluster.barrier_wait();

@@ -264,3 +264,14 @@ def test_temperatures_far_from_one(V, T):
     T = float(np.float32(T))
     tg = [2, 3, 4, 0]
     check(run(x, tg, 4, T=T), as_f32(plain(x.double().numpy(), tg, 4, T)), V)
+
+
+@pytest.mark.parametrize("rest", [-float("inf"), -2e38])
+@pytest.mark.parametrize("special", [float("nan"), float("inf")])
+def test_masked_tokens_behind_a_nan_or_infinity_go_by_index(special, rest):
+    # few rows: a row is several CTAs', and only one of them sees the NaN or infinity
+    x = torch().full((2, 40000), rest)
+    x[0, 30000] = special
+    x[1, 30000], x[1, 39999] = special, -2.0
+    got = run(x, None, 5)
+    assert got[2].tolist() == [[30000, 0, 1, 2, 3], [30000, 39999, 0, 1, 2]]
