@@ -224,6 +224,15 @@ uw_status cuda_fail(cudaError_t e, const char *what) { return fail(UW_ERR_CUDA, 
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
+// memory that cannot be had leaves no error behind for the next launch's check
+template <typename T>
+cudaError_t device_alloc(T **p, uint64_t bytes)
+{
+    const cudaError_t e = cudaMalloc(p, bytes);
+    if (e != cudaSuccess) cudaGetLastError();
+    return e;
+}
+
 MatPlace place_of(const uw_group *g, int expert, int up)
 {
     const GroupView &v = g->v;
@@ -292,7 +301,7 @@ uw_status make_group(const Source &src, int experts, bool gated, int64_t N, int6
         }
         return code;
     };
-    if (!check(cudaMalloc(&g->dev, bytes), "memory of the steps")) return done(s);
+    if (!check(device_alloc(&g->dev, bytes), "memory of the steps")) return done(s);
     uint8_t *d = (uint8_t *)g->dev;
     unsigned long long *hist = (unsigned long long *)(d + o_hist), *total = (unsigned long long *)(d + o_total);
     v.steps = d;
@@ -319,7 +328,7 @@ uw_status make_group(const Source &src, int experts, bool gated, int64_t N, int6
         return done(s);
     if (n_verb >= (1ull << 32)) return done(fail(UW_ERR_SHAPE, "uw_group_create: %llu verbatim runs", n_verb));
     g->n_verb = n_verb;
-    if (!check(cudaMalloc(&g->verb, n_verb * 64 + 256), "memory of the verbatim runs")) return done(s);
+    if (!check(device_alloc(&g->verb, n_verb * 64 + 256), "memory of the verbatim runs")) return done(s);
     v.verb = (const uint8_t *)g->verb;
     g->bytes = bytes + n_verb * 64 + 256;
     for (int e = 0; e < experts; e++)
@@ -384,7 +393,7 @@ extern "C" uw_status uw_group_create(const uw_matrix *const *w, const uw_matrix 
     uw_status s = check_shape(experts, N, K);
     if (s != UW_OK) return s;
     uint16_t *buf = nullptr;
-    const cudaError_t e = cudaMalloc(&buf, (size_t)N * (size_t)K * 2);
+    const cudaError_t e = device_alloc(&buf, (uint64_t)N * (uint64_t)K * 2);
     if (e != cudaSuccess) return fail(UW_ERR_NO_MEMORY, "uw_group_create: decode buffer: %s", cudaGetErrorString(e));
     Source src{{nullptr, nullptr}, {w, w_up}, buf};
     s = make_group(src, experts, w_up != nullptr, N, K, stream, out);

@@ -130,12 +130,13 @@ extern "C" uw_status uw_load(const void *blob, size_t size, int resident, uw_str
     m->h = h;
     cudaGetDevice(&m->device);
     cudaError_t e = cudaMalloc(&m->dev, off);
-    if (e != cudaSuccess) { delete m; return fail(UW_ERR_NO_MEMORY, "uw_load: cudaMalloc(%llu): %s", (unsigned long long)off, cudaGetErrorString(e)); }
+    if (e != cudaSuccess) { cudaGetLastError(); delete m; return fail(UW_ERR_NO_MEMORY, "uw_load: cudaMalloc(%llu): %s", (unsigned long long)off, cudaGetErrorString(e)); }
     m->dev_bytes = off;
     uint8_t *d = (uint8_t *)m->dev;
     uint8_t *hd = d;  // base of the Huffman pieces
     if (huff && !resident_stream) {
         if ((e = cudaMalloc(&hd, hoff)) != cudaSuccess) {
+            cudaGetLastError();
             cudaFree(m->dev); delete m;
             return fail(UW_ERR_NO_MEMORY, "uw_load: cudaMalloc(%llu): %s", (unsigned long long)hoff, cudaGetErrorString(e));
         }

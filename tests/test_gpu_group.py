@@ -345,3 +345,13 @@ def test_many_units(E, mean, N, out_bf16, gated, gather):
     a = run(g, dev(x), dev(off), rows, out_bf16, src=dev(src.astype(np.int32)) if gather else None)
     check(a, ref, bound, out_bf16)
     assert np.array_equal(a, run(g, dev(x), dev(off), rows, out_bf16, src=dev(src.astype(np.int32)) if gather else None))
+
+
+def test_a_group_that_does_not_fit_leaves_no_error_behind():
+    import ctypes
+    w = dev(weights(2, 32, 128, 181))
+    h = ctypes.c_void_p()
+    # 413 GB of steps: refused before a weight is read
+    s = uw.lib().uw_group_create_dense(w.data_ptr(), None, 1, 2 ** 24, 2 ** 14, 0, ctypes.byref(h))
+    assert s == uw.ERR_NO_MEMORY and not h.value
+    assert torch().cuda.is_available() and uw.Group(w).N == 32
