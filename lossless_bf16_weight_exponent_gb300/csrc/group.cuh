@@ -95,8 +95,16 @@ __device__ __forceinline__ void rebuild_chunk_verbatim(const uint4 &S, const uin
     }
 }
 
-// silu(gate) * up; the quotient is within 2 ulp, and 0 where e^-gate overflows
-__device__ __forceinline__ float gated(float gate, float up) { return __fdividef(gate, 1.f + __expf(-gate)) * up; }
+// silu(gate) * up by e^-|gate|, which does not overflow, so that a far negative gate keeps its small product, and the quotient's
+// divisor is within [1, 2].  An fp32 output takes expf (within an ulp; the quotient is within two): 4096 tokens top 8 of 64 of
+// [1408, 2048] 496 us against 488 with the fast power, and 573 with the division rounded too.  For a bf16 output, whose
+// rounding is 2^-9, the fast power's 2^-16 at most is far below it.
+template <bool F32>
+__device__ __forceinline__ float gated(float gate, float up)
+{
+    const float e = F32 ? expf(-fabsf(gate)) : __expf(-fabsf(gate));
+    return gate * __fdividef(gate < 0.f ? e : 1.f, 1.f + e) * up;
+}
 
 // the rank of row r's run among a step's verbatim runs
 __device__ __forceinline__ uint32_t verbatim_rank(const uint32_t *mask, int r)

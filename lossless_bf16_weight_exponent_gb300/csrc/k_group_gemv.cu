@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) group_gemv_kernel(cons
                 for (int w = 0; w < WARPS; w++) s[n] += part[w][n][o][j];
             }
             if (r0 + j >= hi) continue;
-            if (GATED) s[0] = gated(s[0], s[1]);
+            if (GATED) s[0] = c.out_bf16 ? gated<false>(s[0], s[1]) : gated<true>(s[0], s[1]);
 #pragma unroll
             for (int n = 0; n < (GATED ? 1 : NG); n++) {
                 const int64_t col = ((int64_t)blockIdx.x * (GATED ? 1 : NG) + n) * kGran + o;

@@ -604,11 +604,20 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
             if constexpr (GATED) {
                 const bool up = lane >= 16;
                 first += up ? 8 : 0;
+                float gate[8];
 #pragma unroll
                 for (int j = 0; j < 8; j++) {
                     const float mine = up ? x[8 + j] : x[j];
                     const float other = __shfl_xor_sync(0xFFFFFFFFu, up ? x[j] : x[8 + j], 16);
-                    f[j] = gated(up ? other : mine, up ? mine : other);
+                    gate[j] = up ? other : mine;
+                    f[j] = up ? mine : other;
+                }
+                if (!SUMS && a.c.out_bf16) {
+#pragma unroll
+                    for (int j = 0; j < 8; j++) f[j] = gated<false>(gate[j], f[j]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; j++) f[j] = gated<true>(gate[j], f[j]);
                 }
                 col = ((int64_t)w.tile * 4 + q) * 16 + (lane & 15);
             } else {

@@ -355,3 +355,45 @@ def test_a_group_that_does_not_fit_leaves_no_error_behind():
     s = uw.lib().uw_group_create_dense(w.data_ptr(), None, 1, 2 ** 24, 2 ** 14, 0, ctypes.byref(h))
     assert s == uw.ERR_NO_MEMORY and not h.value
     assert torch().cuda.is_available() and uw.Group(w).N == 32
+
+
+@pytest.mark.parametrize("each", [1, 9, 60, 300])
+def test_gate_over_its_whole_range(each):
+    # One weight of 1 in the gate matrix and one in the up matrix: both factors are exact.  Of silu(g) u, e^-|g| is off by an ulp,
+    # the quotient by two, the sum and the two products by half a one each: 4.5 2^-23, and 2^-149 of each rounding below the
+    # smallest normal number, multiplied by what follows it.
+    E, N, K = 40, 33, 64
+    w, u = np.zeros((E, N, K), np.uint16), np.zeros((E, N, K), np.uint16)
+    w[:, :, 0] = u[:, :, 1] = 0x3F80
+    rows = E * each
+    gate = np.linspace(-115, 115, rows).astype(np.float32)
+    up = np.where(np.arange(rows) % 3 == 0, 1e30, np.where(np.arange(rows) % 3 == 1, -1.5, 1.0)).astype(np.float32)
+    x = np.zeros((rows, K), np.float32)
+    x[:, 0], x[:, 1] = gate, up
+    xb = (x.view(np.uint32) >> 16).astype(np.uint16)
+    g, b = f64(xb)[:, 0], f64(xb)[:, 1]
+    want = g / (1 + np.exp(-g)) * b
+    group = uw.Group(dev(w), dev(u))
+    y = run(group, dev(xb), dev(offsets_of([each] * E)), rows, False)
+    assert (y == y[:, :1]).all()
+    bound = 5 * 2.0 ** -23 * np.abs(want) + 2.0 ** -149 * (2 + (np.abs(g) + 2) * np.abs(b))
+    assert (np.abs(y[:, 0] - want) <= bound).all(), (np.abs(y[:, 0] - want) / bound).max()
+
+
+@pytest.mark.parametrize("each", [1, 9, 60, 300])
+def test_gate_over_its_whole_range_in_bf16(each):
+    # half a unit in the last place of bf16 (of the smallest normal number's below it), and 2^-15 of the faster power and
+    # quotient (2 + 1.173 |g| and 2 units in the last place)
+    E, N, K = 40, 33, 64
+    w, u = np.zeros((E, N, K), np.uint16), np.zeros((E, N, K), np.uint16)
+    w[:, :, 0] = u[:, :, 1] = 0x3F80
+    rows = E * each
+    x = np.zeros((rows, K), np.float32)
+    x[:, 0], x[:, 1] = np.linspace(-115, 115, rows), np.where(np.arange(rows) % 3 == 0, 1e30, -1.5)
+    xb = (x.view(np.uint32) >> 16).astype(np.uint16)
+    g, b = f64(xb)[:, 0], f64(xb)[:, 1]
+    want = g / (1 + np.exp(-g)) * b
+    y = run(uw.Group(dev(w), dev(u)), dev(xb), dev(offsets_of([each] * E)), rows, True)
+    assert (y == y[:, :1]).all()
+    bound = (2.0 ** -8 + 2.0 ** -15) * np.abs(want) + 2.0 ** -134 + 2.0 ** -149 * (2 + (np.abs(g) + 2) * np.abs(b))
+    assert (np.abs(y[:, 0] - want) <= bound).all(), (np.abs(y[:, 0] - want) / bound).max()
