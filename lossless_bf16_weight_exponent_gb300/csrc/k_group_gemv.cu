@@ -83,7 +83,9 @@ __device__ __forceinline__ void rebuild_part(const uint8_t *verb, const Part &p,
     }
 }
 
-template <bool GATED, int WARPS>
+// SUMS: an fp32 output with more than a segment of steps for a warp, whose sums are taken in segments as by tcgen05 (the tensor
+// pipe cuts low bits off a running sum at every product)
+template <bool GATED, int WARPS, bool SUMS>
 __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) group_gemv_kernel(const GroupCall c, int all_experts)
 {
     constexpr int NG = 2;  // granules of a CTA: gate and up, or 32 outputs
@@ -150,12 +152,20 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) group_gemv_kernel(cons
             xn0 = xp[0];
             xn1 = xp[1];
         }
-        float acc[NG][4];
+        float acc[NG][4], sum[NG][4];
 #pragma unroll
         for (int n = 0; n < NG; n++)
 #pragma unroll
-            for (int i = 0; i < 4; i++) acc[n][i] = 0.f;
+            for (int i = 0; i < 4; i++) acc[n][i] = sum[n][i] = 0.f;
         for (int i = 0; i < mine; i++) {
+            if (SUMS && i % kSegSteps == 0)
+#pragma unroll
+                for (int n = 0; n < NG; n++)
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        sum[n][j] += acc[n][j];
+                        acc[n][j] = 0.f;
+                    }
             // the next step's loads leave before this step's products
             const uint8_t *cur = sp;
             sp += (size_t)WARPS * kStepBytes;
@@ -186,7 +196,7 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) group_gemv_kernel(cons
 #pragma unroll
         for (int n = 0; n < NG; n++)
 #pragma unroll
-            for (int i = 0; i < 4; i++) part[warp][n][g + 8 * (i >> 1)][2 * t + (i & 1)] = acc[n][i];
+            for (int i = 0; i < 4; i++) part[warp][n][g + 8 * (i >> 1)][2 * t + (i & 1)] = SUMS ? sum[n][i] + acc[n][i] : acc[n][i];
         __syncthreads();
         for (int at128 = threadIdx.x; at128 < 128; at128 += 32 * WARPS) {
             const int o = at128 & 15, j = at128 >> 4;
@@ -212,11 +222,17 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) group_gemv_kernel(cons
     }
 }
 
+template <int WARPS, bool SUMS>
+cudaError_t launch_sums(const GroupCall &c, dim3 grid, int all, cudaStream_t st)
+{
+    return c.v.gated ? launch_dependent(group_gemv_kernel<true, WARPS, SUMS>, grid, 32 * WARPS, 0, 0, st, c, all)
+                     : launch_dependent(group_gemv_kernel<false, WARPS, SUMS>, grid, 32 * WARPS, 0, 0, st, c, all);
+}
+
 template <int WARPS>
 cudaError_t launch_warps(const GroupCall &c, dim3 grid, int all, cudaStream_t st)
 {
-    return c.v.gated ? launch_dependent(group_gemv_kernel<true, WARPS>, grid, 32 * WARPS, 0, 0, st, c, all)
-                     : launch_dependent(group_gemv_kernel<false, WARPS>, grid, 32 * WARPS, 0, 0, st, c, all);
+    return !c.out_bf16 && c.v.ksteps > WARPS * kSegSteps ? launch_sums<WARPS, true>(c, grid, all, st) : launch_sums<WARPS, false>(c, grid, all, st);
 }
 
 }  // namespace

@@ -397,3 +397,20 @@ def test_gate_over_its_whole_range_in_bf16(each):
     assert (y == y[:, :1]).all()
     bound = (2.0 ** -8 + 2.0 ** -15) * np.abs(want) + 2.0 ** -134 + 2.0 ** -149 * (2 + (np.abs(g) + 2) * np.abs(b))
     assert (np.abs(y[:, 0] - want) <= bound).all(), (np.abs(y[:, 0] - want) / bound).max()
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("N", [64, 1300])
+def test_few_rows_of_long_sums_in_fp32(N, gated):
+    # The bound of the test above, on the matrix-vector kernel: sums of 512 products there too.
+    E, K, c = 10, 8192, [1, 0, 5, 2, 0, 9, 1, 0, 0, 2]
+    w, u = weights(E, N, K, 161, 0.0), weights(E, N, K, 162, 0.0)
+    rows, off = sum(c), offsets_of(c)
+    x = np.abs(synth.bf16_to_f32(synth.fill((rows, K), seed=163)))  # one sign: the sums grow
+    xb = (x.astype(np.float32).view(np.uint32) >> 16).astype(np.uint16)
+    w[:, ::2] &= 0x7FFF
+    u[:, ::2] &= 0x7FFF
+    y = run(uw.Group(dev(w), dev(u) if gated else None), dev(xb), dev(off), rows, False)
+    ref, _ = reference(w, u if gated else None, f64(xb), np.arange(rows), off, rows)
+    err = np.linalg.norm(y - ref) / np.linalg.norm(ref)
+    assert err <= (2.1 if gated else 1.0) * 48 * 2.0 ** -24
