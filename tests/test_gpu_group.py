@@ -414,3 +414,81 @@ def test_few_rows_of_long_sums_in_fp32(N, gated):
     ref, _ = reference(w, u if gated else None, f64(xb), np.arange(rows), off, rows)
     err = np.linalg.norm(y - ref) / np.linalg.norm(ref)
     assert err <= (2.1 if gated else 1.0) * 48 * 2.0 ** -24
+
+
+# ------------------------------------------------------------------------------------------------ up to two rows an expert
+# the matrix-vector kernel: CTAs of eight warps for a small grid, of four for a large one (N)
+@pytest.mark.parametrize("out_bf16", [False, True])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("N", [70, 3000])
+def test_few_rows_gathered_with_strides_and_padding(N, gated, out_bf16):
+    K, T, ldx, ldy = 192, 37, 208, N + 5
+    c = [1, 0, 3, 2, 0, 9, 1, 0, 0, 2, 0, 1]
+    off = offsets_of(c, start=3)  # the first three rows belong to nobody
+    E, rows = len(c), int(off[-1]) + 2
+    assert rows <= 2 * E
+    rng = np.random.default_rng(N)
+    src = rng.integers(0, T, rows).astype(np.int32)
+    src[4], src[9], src[10], src[14] = -1, T, 2 ** 31 - 1, -2 ** 31
+    w, u = weights(E, N, K, 121), weights(E, N, K, 122) if gated else None
+    x = synth.fill((T, ldx), seed=123)
+    ref, bound = reference(w, u, f64(x)[:, :K], src.astype(np.int64), off, rows)
+    y = run(uw.Group(dev(w), dev(u) if gated else None), dev(x), dev(off), rows, out_bf16, src=dev(src), ldx=ldx, ldy=ldy)
+    check(y[:, :N], ref, bound, out_bf16)
+    assert np.isnan(y[:, N:]).all()
+
+
+@pytest.mark.parametrize("E", [3, 12])
+def test_few_rows_with_offsets_outside_them(E):
+    N, K, rows = 32, 64, 2 * E
+    w, x = weights(E, N, K, 131), synth.fill((rows, K), seed=132)
+    off = np.array([-5] + [2] * (E - 1) + [1000], np.int32)
+    ref, bound = reference(w, None, f64(x), np.arange(rows), np.clip(off, 0, rows), rows)
+    check(run(uw.Group(dev(w)), dev(x), dev(off), rows, False), ref, bound, False)
+
+
+@pytest.mark.parametrize("N", [100, 3100])
+def test_few_rows_of_exact_integers(N):
+    rng = np.random.default_rng(8)
+    c = [3, 0, 9, 2, 0, 1, 0, 0]
+    E, K, rows, off = len(c), 1088, sum(c), offsets_of(c)
+    wi = (rng.integers(-3, 4, (E, N, K)) * 2.0 ** rng.integers(0, 3, (E, N, K))).astype(np.float32)
+    xi = rng.integers(-4, 5, (rows, K)).astype(np.float32)
+    g = uw.Group(dev((wi.view(np.uint32) >> 16).astype(np.uint16)))
+    y = run(g, dev((xi.view(np.uint32) >> 16).astype(np.uint16)), dev(off), rows, False)
+    for e in range(E):
+        assert np.array_equal(y[off[e]:off[e + 1]], xi[off[e]:off[e + 1]].astype(np.float64) @ wi[e].astype(np.float64).T)
+
+
+def test_few_rows_keep_non_finite_weights_in_their_outputs():
+    E, N, K, rows = 10, 40, 128, 20
+    w, x = weights(E, N, K, 141, 0.0), np.abs(f64(synth.fill((rows, K), seed=142)))
+    xb = (np.maximum(x, 0.1).astype(np.float32).view(np.uint32) >> 16).astype(np.uint16)
+    w[0, 5, 9], w[0, 7, 3], w[1, 33, 100] = 0x7F80, 0x7FC0, 0xFF80  # inf, NaN, -inf
+    y = run(uw.Group(dev(w)), dev(xb), dev(offsets_of([12, 8] + [0] * 8)), rows, False)
+    assert np.isposinf(y[:12, 5]).all() and np.isnan(y[:12, 7]).all() and np.isneginf(y[12:, 33]).all()
+    ok = np.isfinite(y)
+    ok[:12, [5, 7]] = ok[12:, 33] = True
+    assert ok.all()
+
+
+def test_few_rows_in_a_graph_that_finds_other_experts():
+    t = torch()
+    E, N, K, rows = 30, 64, 192, 50
+    w, x = weights(E, N, K, 151), synth.fill((rows, K), seed=152)
+    g = uw.Group(dev(w))
+    xd, od, s = dev(x), dev(offsets_of([10, 0, 33, 7] + [0] * 26)), t.cuda.Stream()
+    s.wait_stream(t.cuda.current_stream())
+    run(g, xd, od, rows, False, stream=s)
+    y = t.zeros((rows, N), dtype=t.float32, device="cuda")
+    graph = t.cuda.CUDAGraph()
+    with t.cuda.graph(graph, stream=s):
+        g.matmul(xd, od, rows, y, out_dtype=uw.OUT_F32, stream=s)
+    for c in ([0] * 29 + [50], [2] * 20 + [1] * 10):
+        off = offsets_of(c)
+        od.copy_(dev(off))
+        y.fill_(float("nan"))
+        graph.replay()
+        t.cuda.synchronize()
+        ref, bound = reference(w, None, f64(x), np.arange(rows), off, rows)
+        check(y.cpu().numpy().astype(np.float64), ref, bound, False)
