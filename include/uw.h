@@ -445,7 +445,9 @@ uw_status uw_group_decode(const uw_group *g, int expert, int up, uint16_t *w_dev
  *   rows ldy elements apart (0: N).  offsets_dev: int32 [experts + 1], ascending, on the device; rows of y outside
  *   [offsets[0], offsets[experts]) are not written.  Offsets are clamped to [0, rows]; a row whose source lies
  *   outside [0, x_rows) counts as zeros, so an expert's rows may be padded with a source of -1.  An expert may have
- *   any number of rows, none included.  Results do not depend on the run or on the other experts' rows.
+ *   any number of rows, none included.  A row's result is the same bits in every run with the same `rows`, and does not
+ *   depend on what the other experts' rows hold nor how they are shared out; another `rows` may choose another kernel,
+ *   whose sums have another order.
  *   No workspace.  Asynchronous on `stream`.
  *   Errors: UW_ERR_INVALID_ARG (NULL, x or y not 16-byte aligned, bad dtype), UW_ERR_SHAPE (negative sizes, rows
  *   or x_rows above 2^31 - 1024, ldx < K or not a multiple of 8, ldy < N), UW_ERR_CUDA.

@@ -492,3 +492,18 @@ def test_few_rows_in_a_graph_that_finds_other_experts():
         t.cuda.synchronize()
         ref, bound = reference(w, None, f64(x), np.arange(rows), off, rows)
         check(y.cpu().numpy().astype(np.float64), ref, bound, False)
+
+
+@pytest.mark.parametrize("E,mine,rows,out_bf16", [(30, 5, 60, False), (8, 40, 160, True), (8, 40, 160, False), (4, 130, 700, True)])
+def test_rows_do_not_depend_on_how_the_others_are_shared_out(E, mine, rows, out_bf16):
+    # at a fixed number of rows, in each kernel and shape, bit for bit; another number may choose another order of sums
+    N, K, rng = 96, 704, np.random.default_rng(rows)
+    w, u = weights(E, N, K, 171), weights(E, N, K, 172)
+    g, x = uw.Group(dev(w), dev(u)), synth.fill((3 * rows, K), seed=173)
+    rest = rows - mine
+    shares = [[rest] + [0] * (E - 2), [0] * (E - 2) + [rest], list(np.bincount(rng.integers(0, E - 1, rest), minlength=E - 1))]
+    ys = [run(g, dev(x[:rows]), dev(offsets_of([mine] + s)), rows, out_bf16)[:mine] for s in shares]
+    assert np.array_equal(ys[0], ys[1]) and np.array_equal(ys[0], ys[2])
+    off = offsets_of([mine, 3 * rows - mine] + [0] * (E - 2))
+    ref, bound = reference(w, u, f64(x), np.arange(3 * rows), off, 3 * rows)
+    check(run(g, dev(x), dev(off), 3 * rows, out_bf16)[:mine], ref[:mine], bound[:mine], out_bf16)
