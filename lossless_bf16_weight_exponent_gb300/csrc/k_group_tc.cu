@@ -705,12 +705,9 @@ template <bool GATED, bool GATHER, typename Sh>
 cudaError_t launch_one(const TcArgs &a, cudaStream_t st)
 {
     auto kernel = group_tc_kernel<GATED, GATHER, Sh>;
-    static bool attr = false;
-    if (!attr) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::smem);
-        if (e != cudaSuccess) return e;
-        attr = true;
-    }
+    static OncePerDevice once;
+    const cudaError_t e = allow_shared(once, kernel, Sh::smem);
+    if (e != cudaSuccess) return e;
     // at least one row tile for each BN rows, at most one more for each expert
     const GroupCall &c = a.c;
     const int64_t row_tiles = (c.rows + Sh::BN - 1) / Sh::BN + std::min<int64_t>(c.v.experts, c.rows);

@@ -366,12 +366,9 @@ cudaError_t launch_choose_per(const RouteArgs &a, int64_t ctas, cudaStream_t st)
 {
     constexpr int kAlone = 120 * 1024;
     auto kernel = route_choose_kernel<PER, TOK>;
-    static bool attr = false;
-    if (!attr) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAlone);
-        if (e != cudaSuccess) return e;
-        attr = true;
-    }
+    static OncePerDevice once;
+    const cudaError_t e = allow_shared(once, kernel, kAlone);
+    if (e != cudaSuccess) return e;
     const size_t smem = PER <= 2 && ctas > 1 && ctas <= num_sms() ? kAlone : (size_t)a.r.experts * (TOK / 8);
     return launch_dependent(kernel, dim3((unsigned)ctas), kThreads, smem, 0, st, a);
 }

@@ -7,10 +7,22 @@
 
 #include <cuda_runtime.h>
 
+#include "per_device.h"
+
 namespace uw {
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// allows a kernel this much dynamic shared memory on the current device (an attribute of each device's own)
+template <typename... P>
+cudaError_t allow_shared(OncePerDevice &once, void (*kernel)(P...), size_t bytes)
+{
+    int device = 0;
+    const cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    return (cudaError_t)once(device, [&] { return (int)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes); });
+}
 
 // cluster > 0: CTAs per cluster along x
 template <typename... P, typename... A>
