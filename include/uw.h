@@ -449,7 +449,8 @@ uw_status uw_group_decode(const uw_group *g, int expert, int up, uint16_t *w_dev
  *   depend on what the other experts' rows hold nor how they are shared out; another `rows` may choose another kernel,
  *   whose sums have another order.
  *   No workspace.  Asynchronous on `stream`.
- *   Errors: UW_ERR_INVALID_ARG (NULL, x or y not 16-byte aligned, bad dtype), UW_ERR_SHAPE (negative sizes, rows
+ *   Errors: UW_ERR_INVALID_ARG (NULL, x or y not 16-byte aligned, bad dtype, another current device than the group's),
+ *   UW_ERR_SHAPE (negative sizes, rows
  *   or x_rows above 2^31 - 1024, ldx < K or not a multiple of 8, ldy < N), UW_ERR_CUDA.
  */
 uw_status uw_group_matmul(const uw_group *g, const uint16_t *x_dev, int64_t x_rows, int64_t ldx,

@@ -250,6 +250,15 @@ MatPlace place_of(const uw_group *g, int expert, int up)
     return m;
 }
 
+// a group's memory is its device's, and so is the stream of a call on it
+uw_status check_device(const uw_group *g, const char *who)
+{
+    int device = 0;
+    const cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return cuda_fail(e, who);
+    return device == g->device ? UW_OK : fail(UW_ERR_INVALID_ARG, "%s: the group is on device %d, the current one is %d", who, g->device, device);
+}
+
 int64_t place_warps(const MatPlace &m) { return (m.N + kGran - 1) / kGran * m.ksteps; }
 unsigned place_blocks(const MatPlace &m) { return (unsigned)((place_warps(m) + 7) / 8); }
 
@@ -436,6 +445,8 @@ extern "C" uw_status uw_group_decode(const uw_group *g, int expert, int up, uint
     if (!g || !w_dev || !aligned16(w_dev)) return fail(UW_ERR_INVALID_ARG, "uw_group_decode: NULL argument or output not 16-byte aligned");
     if (expert < 0 || expert >= g->v.experts) return fail(UW_ERR_INVALID_ARG, "uw_group_decode: expert %d of %d", expert, g->v.experts);
     if (up && !g->v.gated) return fail(UW_ERR_UNSUPPORTED, "uw_group_decode: the group has no up matrices");
+    const uw_status s = check_device(g, "uw_group_decode");
+    if (s != UW_OK) return s;
     const MatPlace m = place_of(g, expert, up ? 1 : 0);
     unpack_kernel<<<place_blocks(m), 256, 0, (cudaStream_t)stream>>>(m, w_dev, place_warps(m));
     const cudaError_t e = cudaGetLastError();
@@ -475,6 +486,8 @@ extern "C" uw_status uw_group_matmul(const uw_group *g, const uint16_t *x, int64
         return fail(UW_ERR_INVALID_ARG, "uw_group_matmul: NULL argument, or x or y not 16-byte aligned");
     if (((uintptr_t)offsets | (uintptr_t)row_src) & 3)
         return fail(UW_ERR_INVALID_ARG, "uw_group_matmul: offsets or row_src not 4-byte aligned");
+    const uw_status s = check_device(g, "uw_group_matmul");
+    if (s != UW_OK) return s;
     GroupCall c{};
     c.v = g->v;
     c.x = x;

@@ -507,3 +507,16 @@ def test_rows_do_not_depend_on_how_the_others_are_shared_out(E, mine, rows, out_
     off = offsets_of([mine, 3 * rows - mine] + [0] * (E - 2))
     ref, bound = reference(w, u, f64(x), np.arange(3 * rows), off, 3 * rows)
     check(run(g, dev(x), dev(off), 3 * rows, out_bf16)[:mine], ref[:mine], bound[:mine], out_bf16)
+
+
+@pytest.mark.skipif("__import__('torch').cuda.device_count() < 2", reason="one device")
+def test_a_group_is_used_on_its_own_device():
+    t = torch()
+    w = weights(2, 32, 64, 191)
+    with t.cuda.device(1):
+        g = uw.Group(dev(w))
+    x, off, y = dev(synth.fill((4, 64), seed=1)), dev(offsets_of([2, 2])), t.empty((4, 32), device="cuda")
+    for call in (lambda: g.matmul(x, off, 4, y, out_dtype=uw.OUT_F32), lambda: g.decode(0, t.empty((32, 64), dtype=t.int16, device="cuda"))):
+        with pytest.raises(uw.UwError) as e:
+            call()
+        assert e.value.status == uw.ERR_INVALID_ARG
