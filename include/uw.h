@@ -450,8 +450,8 @@ uw_status uw_group_decode(const uw_group *g, int expert, int up, uint16_t *w_dev
  *   whose sums have another order.
  *   No workspace.  Asynchronous on `stream`.
  *   Errors: UW_ERR_INVALID_ARG (NULL, x or y not 16-byte aligned, bad dtype, another current device than the group's),
- *   UW_ERR_SHAPE (negative sizes, rows
- *   or x_rows above 2^31 - 1024, ldx < K or not a multiple of 8, ldy < N), UW_ERR_CUDA.
+ *   UW_ERR_SHAPE (negative sizes, rows or x_rows above 2^31 - 1024, ldx < K or not a multiple of 8, ldy < N),
+ *   UW_ERR_CUDA.
  */
 uw_status uw_group_matmul(const uw_group *g, const uint16_t *x_dev, int64_t x_rows, int64_t ldx,
                           const int32_t *row_src_dev, const int32_t *offsets_dev, int64_t rows, void *y_dev,

@@ -183,15 +183,19 @@ def _ptr(t) -> int:
 _ELEMENTS = {}  # element types of the tensors that a call of this type (OUT_F32, OUT_BF16) takes
 
 
-def _holds(what: str, t, dtype: int):
-    """A tensor of another type than the call reads or writes is refused; addresses, and types the library refuses, pass."""
-    if t is None or isinstance(t, int):
-        return
+def _typed(what: str, t, dtype: int) -> int:
+    """_ptr of a tensor of the type that the call reads or writes; one of another type is refused.  Addresses pass, and so
+    do types that the library refuses."""
+    if t is None:
+        return 0
+    if isinstance(t, int):
+        return t
     if not _ELEMENTS:
         import torch
         _ELEMENTS.update({OUT_F32: (torch.float32,), OUT_BF16: (torch.bfloat16, torch.int16, torch.uint16)})
-    if dtype in _ELEMENTS and t.dtype not in _ELEMENTS[dtype]:
+    if t.dtype not in _ELEMENTS.get(dtype, (t.dtype,)):
         raise ValueError(f"{what} is {t.dtype}, the call's type is {('fp32', 'bf16')[dtype]}")
+    return t.data_ptr()
 
 
 def _current_stream():
@@ -377,7 +381,7 @@ class Group:
             for t in (w, w_up):
                 if t is not None and (t.dim() != 3 or t.shape != w.shape or not t.is_contiguous() or not t.is_cuda):
                     raise ValueError("weights must be contiguous tensors [experts, N, K] of one shape on the device")
-                _holds("weights", t, OUT_BF16)
+                _typed("weights", t, OUT_BF16)
             E, N, K = w.shape
             _check(lib().uw_group_create_dense(_ptr(w), _ptr(w_up), E, N, K, _stream(stream), ctypes.byref(h)),
                    "uw_group_create_dense")
@@ -408,9 +412,8 @@ class Group:
     def matmul(self, x, offsets, rows: int, y, row_src=None, x_rows=None, out_dtype: int = OUT_BF16, ldx: int = 0,
                ldy: int = 0, stream=None):
         """uw_group_matmul; x_rows None: rows of x (a tensor).  y is bf16 unless out_dtype is OUT_F32."""
-        _holds("y", y, out_dtype)
         _check(lib().uw_group_matmul(self._h, _ptr(x), x.shape[0] if x_rows is None else x_rows, ldx, _ptr(row_src),
-                                     _ptr(offsets), rows, _ptr(y), ldy, out_dtype, _stream(stream)), "uw_group_matmul")
+                                     _ptr(offsets), rows, _typed("y", y, out_dtype), ldy, out_dtype, _stream(stream)), "uw_group_matmul")
 
     def check(self, stream=None):
         _check(lib().uw_group_check(self._h, _stream(stream)), "uw_group_check")
@@ -423,6 +426,7 @@ class Router:
     def __init__(self, experts: int, topk: int, score: int = SCORE_SOFTMAX, bias=None, renormalize: bool = True, scale: float = 1.0):
         self._bias = bias  # keeps it alive
         self.desc = RouterDesc(experts, topk, score, int(renormalize), scale, _ptr(bias) or None)
+        self._ref = ctypes.byref(self.desc)
 
     def workspace_size(self, tokens: int) -> int:
         n = ctypes.c_size_t(0)
@@ -432,8 +436,7 @@ class Router:
     def route(self, logits, tokens: int, ids, weights, offsets, row_src, pos, dtype: int = OUT_F32, ld: int = 0, workspace=None,
               ws_bytes: int = 0, stream=None):
         """uw_route: ids, row_src, pos and offsets int32, weights fp32."""
-        _holds("logits", logits, dtype)
-        _check(lib().uw_route(ctypes.byref(self.desc), _ptr(logits), dtype, tokens, ld, _ptr(ids), _ptr(weights), _ptr(offsets),
+        _check(lib().uw_route(self._ref, _typed("logits", logits, dtype), dtype, tokens, ld, _ptr(ids), _ptr(weights), _ptr(offsets),
                               _ptr(row_src), _ptr(pos), _ptr(workspace), ws_bytes, _stream(stream)), "uw_route")
 
 
@@ -446,20 +449,17 @@ class BlockNorm:
         self._keep = (post_weight, gate, pre_weight)
         self.desc = NormDesc(dim, _ptr(post_weight) or None, _ptr(gate) or None, gate_every, _ptr(pre_weight) or None, res_scale,
                              out_scale, eps, res_dtype, block_dtype)
+        self._ref, self._res, self._block = ctypes.byref(self.desc), res_dtype, block_dtype
 
     def run(self, rows: int, h, h_out, y=None, pos=None, weights=None, topk: int = 0, y_rows: int = 0, u=None, stream=None):
         """uw_block_norm; topk > 0: y holds expert rows, joined by pos and weights [rows, topk]."""
-        _holds("h", h, self.desc.res_dtype)
-        _holds("h_out", h_out, self.desc.res_dtype)
-        _holds("y", y, self.desc.block_dtype)
-        _holds("u", u, OUT_BF16)
-        _check(lib().uw_block_norm(ctypes.byref(self.desc), rows, _ptr(h), _ptr(h_out), _ptr(y), y_rows, _ptr(pos), _ptr(weights),
-                                   topk, _ptr(u), _stream(stream)), "uw_block_norm")
+        _check(lib().uw_block_norm(self._ref, rows, _typed("h", h, self._res), _typed("h_out", h_out, self._res),
+                                   _typed("y", y, self._block), y_rows, _ptr(pos), _ptr(weights), topk, _typed("u", u, OUT_BF16),
+                                   _stream(stream)), "uw_block_norm")
 
 
 def token_logprobs(logits, rows: int, vocab: int, logprob=None, targets=None, entropy=None, n_top: int = 0, top_ids=None,
                    top_logprobs=None, dtype: int = OUT_F32, ld: int = 0, temperature: float = 1.0, stream=None):
     """uw_token_logprobs: log probabilities of `targets` (int32), entropies and the n_top most probable tokens."""
-    _holds("logits", logits, dtype)
-    _check(lib().uw_token_logprobs(_ptr(logits), dtype, rows, vocab, ld, temperature, _ptr(targets), _ptr(logprob), _ptr(entropy),
+    _check(lib().uw_token_logprobs(_typed("logits", logits, dtype), dtype, rows, vocab, ld, temperature, _ptr(targets), _ptr(logprob), _ptr(entropy),
                                    n_top, _ptr(top_ids), _ptr(top_logprobs), _stream(stream)), "uw_token_logprobs")
