@@ -193,7 +193,8 @@ def _typed(what: str, t, dtype: int) -> int:
     if not _ELEMENTS:
         import torch
         _ELEMENTS.update({OUT_F32: (torch.float32,), OUT_BF16: (torch.bfloat16, torch.int16, torch.uint16)})
-    if t.dtype not in _ELEMENTS.get(dtype, (t.dtype,)):
+    takes = _ELEMENTS.get(dtype)
+    if takes and t.dtype not in takes:
         raise ValueError(f"{what} is {t.dtype}, the call's type is {('fp32', 'bf16')[dtype]}")
     return t.data_ptr()
 
