@@ -463,28 +463,30 @@ uw_status uw_group_check(const uw_group *g, uw_stream stream);
 /* How uw_route turns a token's logits into weights. */
 typedef enum {
     UW_SCORE_SOFTMAX = 0,    /* softmax over all experts */
-    UW_SCORE_SIGMOID = 1     /* 1 / (1 + e^-logit), each expert by itself */
+    UW_SCORE_SIGMOID = 1,    /* 1 / (1 + e^-logit), each expert by itself */
+    UW_SCORE_CHOOSES = 16    /* added to either: the experts are chosen by score + bias, in place of logit + bias */
 } uw_score;
 
 typedef struct {
     int32_t experts;         /* 1..1024 */
     int32_t topk;            /* 1..min(16, experts) */
-    int32_t score;           /* uw_score */
+    int32_t score;           /* uw_score, with or without UW_SCORE_CHOOSES */
     int32_t renormalize;     /* divide a token's chosen weights by their sum (a sum of 0 leaves zeros) */
     float scale;             /* multiplies the weights */
-    const float *bias;       /* device fp32 [experts], added to the logits for the choice alone; NULL: none */
+    const float *bias;       /* device fp32 [experts], for the choice alone; NULL: none.  It is added to the logits, or, with
+                              * UW_SCORE_CHOOSES, to the scores, as routers with a load-balancing correction have it */
 } uw_router;
 
 /*
  * uw_route - choose each token's experts and the order of the grouped products' rows.
  *   logits_dev: [tokens, experts] of `dtype`, rows ld elements apart (0: experts).  Token t takes the topk experts
- *   with the largest logit + bias (in fp32; equal ones by the lower index; NaN counts above +inf):
+ *   with the largest logit + bias, or score + bias (in fp32; equal ones by the lower index; NaN counts above +inf):
  *     ids     int32 [tokens, topk]  the experts, largest first
  *     weights fp32  [tokens, topk]  score [/ the sum over the chosen] * scale
  *     offsets int32 [experts + 1]   rows of expert e are [offsets[e], offsets[e + 1])
  *     row_src int32 [tokens * topk] the token of each row; rows are ordered by (expert, token)
  *     pos     int32 [tokens, topk]  the row of each (token, choice)
- *   A row of logits that is all -inf has weights 0 (softmax) and takes experts 0..topk-1.
+ *   A row of logits that is all -inf has scores 0, and without a bias takes experts 0..topk-1.
  *   workspace: uw_route_workspace_size bytes of device scratch, 16-byte aligned (0 for a few tokens; needs no
  *   initialisation).  Asynchronous.  The result does not depend on the run.
  *   Errors: UW_ERR_INVALID_ARG, UW_ERR_SHAPE (tokens < 0, tokens * topk above 2^31 - 1024, ld < experts),

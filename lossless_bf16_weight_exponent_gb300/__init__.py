@@ -30,6 +30,7 @@ KERNEL_AUTO, KERNEL_GEMV, KERNEL_TC = 0, 1, 2
 RESIDENT_HUFFMAN, RESIDENT_BOTH, RESIDENT_PALETTE = 0, 1, 2
 RESIDENT = {"huffman": RESIDENT_HUFFMAN, "both": RESIDENT_BOTH, "palette": RESIDENT_PALETTE}
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+SCORE_CHOOSES = 16  # added to either: the choice is by score + bias in place of logit + bias
 SEQ_DIRECT = -1  # uw_sequence_run schedule: no side-stream transcode, every step its own AUTO plan
 STEP_CONCURRENT = 1  # uw_step flag: the step may overlap the step before it
 SEQ_GROUPS = 65536  # added to a uw_sequence_run schedule: overlap the groups of STEP_CONCURRENT steps
@@ -422,7 +423,7 @@ class Group:
 
 class Router:
     """How a layer's router chooses its experts (a ``uw_router``); bias: fp32 [experts] on the device, for the choice
-    alone."""
+    alone, added to the logits, or to the scores with a score of SCORE_SIGMOID + SCORE_CHOOSES (or SCORE_SOFTMAX + ...)."""
 
     def __init__(self, experts: int, topk: int, score: int = SCORE_SOFTMAX, bias=None, renormalize: bool = True, scale: float = 1.0):
         self._bias = bias  # keeps it alive

@@ -1,7 +1,8 @@
 // k_route.cu - the router of a mixture of experts: each token's top-k experts, their weights, and the order of the
 // grouped products' rows (sm_103a).
 //
-// A warp takes a token.  A logit's sort key is its (logit + bias) mapped to an unsigned integer of the same order.  Up to 64
+// A warp takes a token.  An expert's sort key is its (logit + bias), or (score + bias), mapped to an unsigned integer of the same
+// order.  Up to 64
 // experts a round of the choice is a warp-wide maximum of the keys left and a warp-wide minimum of the experts that hold
 // it, one instruction each, so equal logits go to the lower index.  With more experts the lanes' largest keys give a bound
 // that at least k keys reach; those that do, few unless many are equal, take a lane each and are ranked.
@@ -36,7 +37,7 @@ constexpr int kTokMany = 64;     // and when there are more
 constexpr int kMaxE = 1024, kMaxTop = 16;
 
 struct RouteArgs {
-    uw_router r;
+    uw_router r;  // score without UW_SCORE_CHOOSES
     const void *logits;
     int bf16;
     int64_t tokens, ld;
@@ -73,17 +74,21 @@ __device__ __forceinline__ void load_logits(const RouteArgs &a, int64_t t, int l
     for (int i = 0; i < PER; i++) z[i] = lane + 32 * i < a.r.experts ? logit_at(a, t, lane + 32 * i) : -INFINITY;
 }
 
-// the choice of token t by one warp; sets the token's bits (WORDS per expert); few: the warp's 32
-template <int PER, int WORDS>
+// the choice of token t by one warp, BY_SCORE by the scores in place of the logits; sets the token's bits (WORDS per expert); few:
+// the warp's 32
+template <int PER, int WORDS, bool BY_SCORE>
 __device__ __forceinline__ void choose(const RouteArgs &a, int64_t t, int lane, const float (&z)[PER], uint32_t *bits, int tl, Choice *few)
 {
     const int E = a.r.experts, k = a.r.topk;
     uint32_t key[PER];  // 0: none, or taken
+    auto keys = [&](auto value) {
 #pragma unroll
-    for (int i = 0; i < PER; i++) {
-        const int e = lane + 32 * i;
-        key[i] = e < E ? order_key(a.r.bias ? z[i] + a.r.bias[e] : z[i]) : 0u;
-    }
+        for (int i = 0; i < PER; i++) {
+            const int e = lane + 32 * i;
+            key[i] = e < E ? order_key(a.r.bias ? value(z[i]) + a.r.bias[e] : value(z[i])) : 0u;
+        }
+    };
+    if constexpr (!BY_SCORE) keys([](float x) { return x; });
     float m = -INFINITY, total = 1.f;
     if (a.r.score == UW_SCORE_SOFTMAX) {
 #pragma unroll
@@ -97,6 +102,11 @@ __device__ __forceinline__ void choose(const RouteArgs &a, int64_t t, int lane, 
 #pragma unroll
         for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, d);
     }
+    auto score_of = [&](float x) {
+        if (a.r.score == UW_SCORE_SOFTMAX) return total == 0.f ? 0.f : expf(x - m) / total;
+        return 1.f / (1.f + expf(-x));
+    };
+    if constexpr (BY_SCORE) keys(score_of);
     int my_e = 0, place = lane < k ? lane : -1;
     float my_z = 0.f;
     bool chosen = false;
@@ -158,11 +168,7 @@ __device__ __forceinline__ void choose(const RouteArgs &a, int64_t t, int lane, 
             my_z = ze;
         }
     }
-    float w = 0.f;
-    if (place >= 0) {
-        if (a.r.score == UW_SCORE_SOFTMAX) w = total == 0.f ? 0.f : expf(my_z - m) / total;
-        else w = 1.f / (1.f + expf(-my_z));
-    }
+    float w = place >= 0 ? score_of(my_z) : 0.f;
     if (a.r.renormalize) {
         float s = w;
 #pragma unroll
@@ -226,7 +232,7 @@ __device__ __forceinline__ int exclusive_sum(int *v, int E, int *wsum)
     return total;
 }
 
-template <int PER, int TOK>
+template <int PER, int TOK, bool BY_SCORE>
 __global__ void __launch_bounds__(kThreads, PER <= 2 ? 2 : 1) route_choose_kernel(const RouteArgs a)
 {
     constexpr int WORDS = TOK / 32;
@@ -246,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, PER <= 2 ? 2 : 1) route_choose_kerne
     for (; tl < nt; tl += kThreads / 32) {
         const bool more = tl + kThreads / 32 < nt;
         if (kAhead && more) load_logits<PER>(a, t0 + tl + kThreads / 32, lane, next);
-        choose<PER, WORDS>(a, t0 + tl, lane, z, bits, tl, few[PER >= 4 ? threadIdx.x >> 5 : 0]);
+        choose<PER, WORDS, BY_SCORE>(a, t0 + tl, lane, z, bits, tl, few[PER >= 4 ? threadIdx.x >> 5 : 0]);
         if (kAhead && more) {
 #pragma unroll
             for (int i = 0; i < PER; i++) z[i] = next[i];
@@ -361,11 +367,11 @@ __global__ void __launch_bounds__(kThreads) route_order_kernel(const RouteArgs a
 
 // Up to a CTA for each SM no two share one: what they ask of shared memory sees to it, since behind another kernel's last
 // CTAs they would (8192 tokens of 8 experts: 11.3 us sharing, 9.0 not; 131072: 84 and 95).
-template <int PER, int TOK>
+template <int PER, int TOK, bool BY_SCORE>
 cudaError_t launch_choose_per(const RouteArgs &a, int64_t ctas, cudaStream_t st)
 {
     constexpr int kAlone = 120 * 1024;
-    auto kernel = route_choose_kernel<PER, TOK>;
+    auto kernel = route_choose_kernel<PER, TOK, BY_SCORE>;
     static OncePerDevice once;
     const cudaError_t e = allow_shared(once, kernel, kAlone);
     if (e != cudaSuccess) return e;
@@ -373,15 +379,21 @@ cudaError_t launch_choose_per(const RouteArgs &a, int64_t ctas, cudaStream_t st)
     return launch_dependent(kernel, dim3((unsigned)ctas), kThreads, smem, 0, st, a);
 }
 
-template <int TOK>
-cudaError_t launch_choose(const RouteArgs &a, int64_t ctas, cudaStream_t st)
+template <int TOK, bool BY_SCORE>
+cudaError_t launch_choose_by(const RouteArgs &a, int64_t ctas, cudaStream_t st)
 {
     const int E = a.r.experts;
-    return E <= 32    ? launch_choose_per<1, TOK>(a, ctas, st)
-           : E <= 64  ? launch_choose_per<2, TOK>(a, ctas, st)
-           : E <= 128 ? launch_choose_per<4, TOK>(a, ctas, st)
-           : E <= 256 ? launch_choose_per<8, TOK>(a, ctas, st)
-                      : launch_choose_per<32, TOK>(a, ctas, st);
+    return E <= 32    ? launch_choose_per<1, TOK, BY_SCORE>(a, ctas, st)
+           : E <= 64  ? launch_choose_per<2, TOK, BY_SCORE>(a, ctas, st)
+           : E <= 128 ? launch_choose_per<4, TOK, BY_SCORE>(a, ctas, st)
+           : E <= 256 ? launch_choose_per<8, TOK, BY_SCORE>(a, ctas, st)
+                      : launch_choose_per<32, TOK, BY_SCORE>(a, ctas, st);
+}
+
+template <int TOK>
+cudaError_t launch_choose(const RouteArgs &a, bool by_score, int64_t ctas, cudaStream_t st)
+{
+    return by_score ? launch_choose_by<TOK, true>(a, ctas, st) : launch_choose_by<TOK, false>(a, ctas, st);
 }
 
 uw_status check_router(const uw_router *r, const char *who)
@@ -389,7 +401,8 @@ uw_status check_router(const uw_router *r, const char *who)
     if (!r) return fail(UW_ERR_INVALID_ARG, "%s: NULL router", who);
     if (r->experts < 1 || r->experts > kMaxE || r->topk < 1 || r->topk > kMaxTop || r->topk > r->experts)
         return fail(UW_ERR_INVALID_ARG, "%s: %d of %d experts (1..%d of 1..%d)", who, r->topk, r->experts, kMaxTop, kMaxE);
-    if (r->score != UW_SCORE_SOFTMAX && r->score != UW_SCORE_SIGMOID) return fail(UW_ERR_INVALID_ARG, "%s: score %d", who, r->score);
+    const int score = r->score & ~UW_SCORE_CHOOSES;
+    if (score != UW_SCORE_SOFTMAX && score != UW_SCORE_SIGMOID) return fail(UW_ERR_INVALID_ARG, "%s: score %d", who, r->score);
     return UW_OK;
 }
 
@@ -439,13 +452,15 @@ extern "C" uw_status uw_route(const uw_router *r, const void *logits, uw_out_dty
     const size_t need = workspace_bytes(r, tokens);
     if (ws_bytes < need || (need && !ws)) return fail(UW_ERR_WORKSPACE, "uw_route: workspace %zu bytes, need %zu", ws_bytes, need);
     if ((uintptr_t)ws & 15) return fail(UW_ERR_INVALID_ARG, "uw_route: workspace not 16-byte aligned");
-    const RouteArgs a{*r, logits, dtype == UW_OUT_BF16, tokens, ld, ids, weights, offsets, row_src, pos, (int32_t *)ws};
+    RouteArgs a{*r, logits, dtype == UW_OUT_BF16, tokens, ld, ids, weights, offsets, row_src, pos, (int32_t *)ws};
+    const bool by_score = r->score & UW_SCORE_CHOOSES;
+    a.r.score &= ~UW_SCORE_CHOOSES;
     cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e;
     if (tokens == 0) {
         e = cudaMemsetAsync(offsets, 0, ((size_t)r->experts + 1) * 4, st);
     } else {
-        e = ctas == 1 ? launch_choose<kTokOne>(a, 1, st) : launch_choose<kTokMany>(a, ctas, st);
+        e = ctas == 1 ? launch_choose<kTokOne>(a, by_score, 1, st) : launch_choose<kTokMany>(a, by_score, ctas, st);
         const size_t smem = (size_t)r->experts * (kTokMany / 8);
         if (e == cudaSuccess && route_scans(r, ctas)) {
             e = launch_dependent(route_scan_kernel, dim3((unsigned)(r->experts + 31) / 32), kThreads, 0, 0, st, a, (int)ctas);

@@ -157,3 +157,56 @@ def test_refusals():
     assert status(n=16) == status(w=None) == uw.ERR_WORKSPACE
     assert status(outs=[None] + o[1:]) == status(outs=o[:4] + [None]) == status(logits=None) == uw.ERR_INVALID_ARG
     assert status(logits=z.data_ptr() + 2) == status(w=ws.data_ptr() + 4) == uw.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("score", [uw.SCORE_SOFTMAX, uw.SCORE_SIGMOID])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("T,E,k", [(1, 3, 1), (7, 33, 2), (100, 64, 8), (129, 128, 8), (700, 257, 16), (2500, 40, 6), (300, 1024, 4)])
+def test_choice_by_score(T, E, k, biased, score):
+    # A score is within 2^-21 of its value (an exponential, a sum of at most 40 steps, a division), its sum with the bias off by half
+    # a unit in the last place of it: experts whose exact keys differ by less may come in either order.
+    rng = np.random.default_rng(T + E)
+    z = (rng.standard_normal((T, E)) * 3).astype(np.float32)
+    b = (rng.standard_normal(E) * 0.5).astype(np.float32) if biased else None
+    got = run(z, k, score + uw.SCORE_CHOOSES, b, True, 1.5)
+    zd = z.astype(np.float64)
+    p = 1 / (1 + np.exp(-zd)) if score == uw.SCORE_SIGMOID else np.exp(zd - zd.max(1, keepdims=True))
+    if score == uw.SCORE_SOFTMAX:
+        p /= p.sum(1, keepdims=True)
+    key = p + b if biased else p
+    slack = 2.0 ** -21 + 2.0 ** -23 * np.abs(key).max()
+    ids = got[0]
+    chosen = np.take_along_axis(key, ids, 1)
+    assert (np.sort(ids, 1)[:, 1:] != np.sort(ids, 1)[:, :-1]).all()
+    assert (chosen[:, 1:] <= chosen[:, :-1] + slack).all()
+    left = key.copy()
+    np.put_along_axis(left, ids, -np.inf, 1)
+    assert (left.max(1) <= chosen[:, -1] + slack).all()
+    # the rest follows from the experts chosen
+    w = np.take_along_axis(p, ids, 1)
+    flat = ids.reshape(-1)
+    rows = np.argsort(flat, kind="stable")
+    pos = np.empty(T * k, np.int64)
+    pos[rows] = np.arange(T * k)
+    check(got, (ids, 1.5 * w / w.sum(1, keepdims=True), np.searchsorted(flat[rows], np.arange(E + 1)), rows // k, pos.reshape(T, k)))
+
+
+def test_choice_by_score_is_not_that_by_logit():
+    z, b = np.array([[4.0, 8.0, -1.0]], np.float32), np.array([0.125, 0.0, 0.0], np.float32)
+    # sigmoid(4) + 0.125 > sigmoid(8), while 4 + 0.125 < 8
+    assert run(z, 1, uw.SCORE_SIGMOID, b)[0].tolist() == [[1]]
+    got = run(z, 1, uw.SCORE_SIGMOID + uw.SCORE_CHOOSES, b, renorm=False)
+    assert got[0].tolist() == [[0]] and abs(got[1][0, 0] - 1 / (1 + np.exp(-4.0))) < 1e-6  # the bias is not in the weight
+
+
+@pytest.mark.parametrize("score", [uw.SCORE_SOFTMAX, uw.SCORE_SIGMOID])
+def test_choice_by_score_of_masked_and_nan_logits(score):
+    z = np.full((200, 70), -np.inf, np.float32)
+    z[1, 40] = 0.0
+    z[2, 9] = np.nan
+    b = np.linspace(0, 0.01, 70, dtype=np.float32)
+    got = run(z, 3, score + uw.SCORE_CHOOSES, b, True)
+    assert got[0][0].tolist() == [69, 68, 67] and (got[1][0] == 0).all()  # nothing but the bias is left
+    assert got[0][1].tolist() == [40, 69, 68] and got[1][1].tolist() == [1, 0, 0]
+    assert got[0][2, 0] == (9 if score == uw.SCORE_SIGMOID else 0) and np.isnan(got[1][2, 0])  # a softmax is a NaN everywhere
+    assert np.array_equal(np.sort(got[4].ravel()), np.arange(600))

@@ -35,3 +35,9 @@ def test_structures(layout, name, cls):
 def test_constants(layout):
     assert (uw.SCORE_SOFTMAX, uw.SCORE_SIGMOID) == (layout["UW_SCORE_SOFTMAX"], layout["UW_SCORE_SIGMOID"])
     assert (uw.OUT_F32, uw.OUT_BF16) == (layout["UW_OUT_F32"], layout["UW_OUT_BF16"])
+
+
+def test_added_score(tmp_path):
+    (tmp_path / "c.c").write_text('#include <stdio.h>\n#include "uw.h"\nint main(void) { printf("%d\\n", UW_SCORE_CHOOSES); return 0; }\n')
+    subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), "-o", str(tmp_path / "c"), str(tmp_path / "c.c")], check=True)
+    assert int(subprocess.run([str(tmp_path / "c")], check=True, capture_output=True, text=True).stdout) == uw.SCORE_CHOOSES
