@@ -499,11 +499,19 @@ extern "C" uw_status uw_group_matmul(const uw_group *g, const uint16_t *x, int64
     c.y = y;
     c.ldy = ldy;
     c.out_bf16 = od == UW_OUT_BF16;
-    // Up to two rows an expert on average the matrix-vector kernel, which reads the weights of an expert again for every
-    // eight of its rows, else tcgen05.  64 experts of [2048, 1408] take 43 us against 44 at two rows each, 48 against 45 at
-    // three (fp32: 47.8, 47.6; 54.4, 53.4 at four), gated fp32 of [1408, 2048] 85.6 against 82.6 at three; 8 gated experts of
-    // [14336, 4096] 218 against 209 at four (fp32: 193.6, 200.8 at three; 217.8, 218.9 at four).
-    const bool tc = rows > 2 * (int64_t)g->v.experts && group_tc_supported(c);
+    // Few rows an expert on average take the matrix-vector kernel, which reads the weights of an expert again for every eight of
+    // its rows, else tcgen05: up to two rows for a bf16 output, and four for an fp32 one, whose segments cost tcgen05 more.
+    // Matrix-vector against tcgen05 in us (tokens' own choices, weights from memory):
+    //   rows each                             2              3              4              6
+    //   64 of [2048, 1408]         bf16   49.6   51.4    57.2   52.8    63.0   58.1    74.8   58.6
+    //                              fp32   49.7   55.2    57.1   56.5    63.2   62.5    74.5   63.0
+    //   64 gated of [1408, 2048]   bf16   86.9   88.1    94.9   97.2   105.3   98.3   127.7   98.4
+    //                              fp32   87.2   94.4    94.7  103.9   105.5  105.1   127.9  105.0
+    //   8 gated of [14336, 4096]   bf16  234.3  231.3   208.3  212.5   234.6  231.5   262.0  212.6
+    //                              fp32  245.8  247.5   217.9  227.5   246.3  247.6   274.7  227.8
+    //   8 of [4096, 14336]         bf16  128.8  136.1   135.7  137.4   136.0  137.1   141.9  137.2
+    //                              fp32  130.4  145.9   137.7  146.0   138.4  146.0   144.0  146.2
+    const bool tc = rows > (c.out_bf16 ? 2 : 4) * (int64_t)g->v.experts && group_tc_supported(c);
     const cudaError_t e = (cudaError_t)(tc ? launch_group_tc(c, stream) : launch_group_gemv(c, stream));
     return e == cudaSuccess ? UW_OK : cuda_fail(e, "uw_group_matmul: launch");
 }
