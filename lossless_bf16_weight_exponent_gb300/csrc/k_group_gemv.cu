@@ -83,12 +83,16 @@ __device__ __forceinline__ void rebuild_part(const uint8_t *verb, const Part &p,
     }
 }
 
-// SUMS: an fp32 output with more than a segment of steps for a warp, whose sums are taken in segments as by tcgen05 (the tensor
-// pipe cuts low bits off a running sum at every product)
-template <bool GATED, int WARPS, bool SUMS>
+// The output: bf16; fp32; or fp32 with more than a segment of steps for a warp, whose sums are taken in segments as by tcgen05
+// (the tensor pipe cuts low bits off a running sum at every product).  One instance for both types took 21.0 us for 1 token
+// where the bf16 one takes 20.7: the fp32 gate's code is in the way.
+enum Output { BF16, F32, F32_SEGMENTS };
+
+template <bool GATED, int WARPS, Output OUT>
 __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) group_gemv_kernel(const GroupCall c, int all_experts)
 {
     constexpr int NG = 2;  // granules of a CTA: gate and up, or 32 outputs
+    constexpr bool SUMS = OUT == F32_SEGMENTS;
     __shared__ float part[WARPS][NG][16][8];
     const GroupView &v = c.v;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -208,13 +212,13 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) group_gemv_kernel(cons
                 for (int w = 0; w < WARPS; w++) s[n] += part[w][n][o][j];
             }
             if (r0 + j >= hi) continue;
-            if (GATED) s[0] = c.out_bf16 ? gated<false>(s[0], s[1]) : gated<true>(s[0], s[1]);
+            if (GATED) s[0] = gated<OUT != BF16>(s[0], s[1]);
 #pragma unroll
             for (int n = 0; n < (GATED ? 1 : NG); n++) {
                 const int64_t col = ((int64_t)blockIdx.x * (GATED ? 1 : NG) + n) * kGran + o;
                 if (col >= v.N) continue;
                 const int64_t i = (int64_t)(r0 + j) * c.ldy + col;
-                if (c.out_bf16) ((__nv_bfloat16 *)c.y)[i] = __float2bfloat16_rn(s[n]);
+                if (OUT == BF16) ((__nv_bfloat16 *)c.y)[i] = __float2bfloat16_rn(s[n]);
                 else ((float *)c.y)[i] = s[n];
             }
         }
@@ -222,17 +226,18 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) group_gemv_kernel(cons
     }
 }
 
-template <int WARPS, bool SUMS>
-cudaError_t launch_sums(const GroupCall &c, dim3 grid, int all, cudaStream_t st)
+template <int WARPS, Output OUT>
+cudaError_t launch_output(const GroupCall &c, dim3 grid, int all, cudaStream_t st)
 {
-    return c.v.gated ? launch_dependent(group_gemv_kernel<true, WARPS, SUMS>, grid, 32 * WARPS, 0, 0, st, c, all)
-                     : launch_dependent(group_gemv_kernel<false, WARPS, SUMS>, grid, 32 * WARPS, 0, 0, st, c, all);
+    return c.v.gated ? launch_dependent(group_gemv_kernel<true, WARPS, OUT>, grid, 32 * WARPS, 0, 0, st, c, all)
+                     : launch_dependent(group_gemv_kernel<false, WARPS, OUT>, grid, 32 * WARPS, 0, 0, st, c, all);
 }
 
 template <int WARPS>
 cudaError_t launch_warps(const GroupCall &c, dim3 grid, int all, cudaStream_t st)
 {
-    return !c.out_bf16 && c.v.ksteps > WARPS * kSegSteps ? launch_sums<WARPS, true>(c, grid, all, st) : launch_sums<WARPS, false>(c, grid, all, st);
+    if (c.out_bf16) return launch_output<WARPS, BF16>(c, grid, all, st);
+    return c.v.ksteps > WARPS * kSegSteps ? launch_output<WARPS, F32_SEGMENTS>(c, grid, all, st) : launch_output<WARPS, F32>(c, grid, all, st);
 }
 
 }  // namespace
