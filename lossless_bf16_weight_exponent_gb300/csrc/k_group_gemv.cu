@@ -7,9 +7,9 @@
 // shared-memory sum joins the warps, in a fixed order.  The logical k of the instruction is permuted so that a lane's
 // pairs are its 16 consecutive weights; X is read in the same order.
 //
-// Bound by memory, then by the latency of its loads: 1 token top 8 of 64 gated experts of [1408, 2048] takes 20.5 us (69 MB:
-// 10.3 at the copy rate, and a launch with a cold start of about 5), 8 tokens 66 us with 66 % of the DRAM rate, 43 % of
-// the integer rate (the rebuild) and 4.7 of a warp's 9 waiting cycles for memory; 16 tokens top 8 of 64 of [2048, 1408] 43 us (5.1 TB/s).
+// Bound by memory, then by the latency of its loads: 1 token top 8 of 64 gated experts of [1408, 2048] takes 20.7 us (69 MB: 10.3
+// at the copy rate; 704 CTAs, two an SM, are 2.3 waves with a cold start each), 8 tokens 61 us with 61 % of the DRAM rate, 42 % of
+// the integer rate (the rebuild) and 4.6 of a warp's 8 waiting cycles for memory; 16 tokens top 8 of 64 of [2048, 1408] 49.6 us.
 // Eight warps a CTA rather than four where the grid is small; registers held to 96 or 80 for a third CTA an SM spilled and
 // lost.
 #include <cuda_bf16.h>

@@ -25,10 +25,12 @@
 // slots of 32 columns for A (64 and eight in the shape for few rows).  A sum of segments takes 128 columns beside two
 // accumulators of 128.
 //
-// Measured (K = 2048, N = 1408, gated, 4096 tokens top 8 of 64 experts): 325 us, 1.16 PFLOP/s; with the rebuild left out
-// 278, with the epilogue left out 301, with both 261.  333 tokens top 2 of 8 experts of [14336, 4096], gated: 243 us, 5.9 TB/s
-// of compressed weights.  128 tokens top 8 of 64 experts of [2048, 1408]: 52 us, 5.5 TB/s.
-// fp32 from segments: 453 us for the first, 218 for 4096 tokens top 8 of 64 of [2048, 1408].
+// Measured on weights of which 1.1 % of the runs are verbatim (4096 tokens top 8 of 64 gated experts of [1408, 2048]): 355 us,
+// 1.07 PFLOP/s, and 341 on weights without such runs, which a warp with one among its 32 rows rebuilds twice.  Of a form that
+// took 325 there, the rebuild left out took 278, the epilogue left out 301, both 261.  4096 tokens of [2048, 1408]: 167 us.
+// 333 tokens top 2 of 8 gated experts of [14336, 4096]: 246 to 257 us, 5.6 to 5.8 TB/s of compressed weights.  128 tokens top 8
+// of 64 experts of [2048, 1408]: 57 us, 4.9 TB/s.  fp32 from segments: 494 us for the first, 240 for the second; on weights without
+// verbatim runs 477 and 224.
 // Every wait is bounded; when one runs out the kernel latches DEV_TIMEOUT, waits for its copies and products in flight,
 // frees its tensor memory and ends.
 #include <cuda.h>
