@@ -260,9 +260,9 @@ def _run_own(s):
         s["cache"].attend(s["batch"], s["rows"], s["q"], s["out"], causal=c["causal"], window=c["window"], lse=s["lse"], workspace=s["ws"],
                           ws_bytes=s["ws_bytes"])
         return [s["out"], s["lse"]]
-    uw.adjust_logits(s["logits"], c["rows"], c["vocab"], s["out"], tokens=s["tokens"], lengths=s["lengths"], prompt_lengths=s["prompts"],
-                     repetition=s["repetition"], frequency=s["frequency"], presence=s["presence"], bias_ids=s["bias_ids"], bias=s["bias"],
-                     allowed=s["allowed"], mask_rows=s["mask_rows"], dtype=s["dt"], out_dtype=s["dt"])
+    uw.edit_logits(s["logits"], c["rows"], c["vocab"], s["out"], tokens=s["tokens"], lengths=s["lengths"], prompt_lengths=s["prompts"],
+                   repetition=s["repetition"], frequency=s["frequency"], presence=s["presence"], bias_ids=s["bias_ids"], bias=s["bias"],
+                   allowed=s["allowed"], mask_rows=s["mask_rows"], dtype=s["dt"], out_dtype=s["dt"])
     return s["out"]
 
 
