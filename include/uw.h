@@ -544,6 +544,164 @@ uw_status uw_token_logprobs(const void *logits_dev, uw_out_dtype dtype, int64_t 
                             float temperature, const int32_t *targets, float *logprob, float *entropy, int n_top,
                             int32_t *top_ids, float *top_logprobs, uw_stream stream);
 
+/* ------------------------------------------------------------------------------------------------------------
+ * Attention between the qkv product and the output product, over keys and values kept in pages; and the edits of
+ * logits in front of uw_token_logprobs.  A token's way: uw_matmul for q, k and v; uw_kv_append, which rotates q and k
+ * and stores k and v; uw_kv_attend; uw_matmul for the output; and behind the head's uw_matmul uw_edit_logits, then
+ * uw_token_logprobs.  Lengths are read on the device: no call waits for the GPU.
+ * ------------------------------------------------------------------------------------------------------------ */
+
+/* Which elements of a head are turned together: i and i + dim / 2, or 2 i and 2 i + 1. */
+typedef enum {
+    UW_ROTARY_HALF = 0,
+    UW_ROTARY_INTERLEAVED = 1
+} uw_rotary_layout;
+
+/* How the frequencies base^(-2 i / dim) are scaled for contexts longer than those of training. */
+typedef enum {
+    UW_ROTARY_PLAIN = 0,     /* not */
+    UW_ROTARY_LINEAR = 1,    /* all divided by factor */
+    UW_ROTARY_STRETCHED = 2, /* base multiplied by factor^(dim / (dim - 2)): the lowest frequency divided by factor */
+    UW_ROTARY_BANDS = 3,     /* by the turns made over `original` positions: divided by factor up to `low`, kept from `high` on,
+                              * between the two a mixture that is linear in the turns */
+    UW_ROTARY_RAMP = 4       /* the same ends, linear in the index i between the indices (rounded outwards) that make `high` and
+                              * `low` turns; cos and sin are multiplied by 0.1 ln(factor) + 1 (factor > 1) */
+} uw_rotary_scaling;
+
+/*
+ * uw_rotary_frequencies - host: freq[0..dim/2), in radians a position, and the factor on cos and sin (*scale; may be
+ *   NULL).  factor, low, high, original: as the scaling uses them (others are ignored).
+ *   Errors: UW_ERR_INVALID_ARG (NULL, base not finite and > 1, factor not finite and >= 1, low or high not finite, low < 0,
+ *   high <= low, for a ramp low <= 0, original < 1, unknown scaling), UW_ERR_SHAPE (dim not a multiple of 16 in 16..128).
+ */
+uw_status uw_rotary_frequencies(int dim, double base, uw_rotary_scaling scaling, double factor, double low, double high,
+                                int64_t original, double *freq, float *scale);
+
+typedef struct {
+    int32_t dim;             /* elements of a head that are turned, the first ones: a multiple of 16, 16..head_dim */
+    int32_t layout;          /* uw_rotary_layout */
+    const double *freq;      /* device [dim / 2], radians a position */
+    float scale;             /* multiplies cos and sin */
+} uw_rotary;
+
+/*
+ * uw_kv_cache - keys and values of many sequences in pages of page_size slots, a page being an index into k and v.  The
+ *   element i of a head's key in a page's slot is at k[page * page_stride + slot * slot_stride + head * head_stride + i], its
+ *   value at the same place in v: [pages, page_size, kv_heads, head_dim] and [pages, kv_heads, page_size, head_dim] are
+ *   both taken, k and v may be halves of one tensor.  The caller owns the memory and which sequence holds which page.
+ */
+typedef struct uw_kv_cache uw_kv_cache;
+
+typedef struct {
+    uint16_t *k, *v;         /* device, bf16, 16-byte aligned */
+    int64_t pages;           /* 1..2^31 - 1 */
+    int64_t page_stride, slot_stride, head_stride; /* elements, multiples of 8, at least head_dim, below 2^39 (one of a dimension
+                              * of size 1 is ignored) */
+    int32_t page_size;       /* slots: a multiple of 8, 8..65536 */
+    int32_t kv_heads;        /* 1..1024 */
+    int32_t head_dim;        /* 64 or 128 */
+} uw_kv_desc;
+
+/*
+ * uw_kv_create - a handle on such memory for the current device: two words of device memory and the copies'
+ *   descriptions.  Errors: UW_ERR_INVALID_ARG (NULL, alignment, strides), UW_ERR_SHAPE, UW_ERR_UNSUPPORTED (head_dim, or a
+ *   driver without tensor maps), UW_ERR_NO_MEMORY, UW_ERR_CUDA.
+ */
+uw_status uw_kv_create(const uw_kv_desc *d, uw_kv_cache **out);
+void uw_kv_free(uw_kv_cache *c);
+
+/* The new tokens of a step: sequence s brings the rows [starts[s], starts[s + 1]) of the call's tensors and holds lengths[s]
+ * tokens with them, so its i-th new token is at position lengths[s] - (starts[s + 1] - starts[s]) + i.  Device pointers;
+ * starts ascending, clamped to [0, rows]; a sequence may bring none.  pages[s * ld_pages + p] is the page of its positions
+ * [p page_size, (p + 1) page_size), for p below max_pages; entries behind its length are not read. */
+typedef struct {
+    int32_t sequences;       /* 1..65536 */
+    const int32_t *starts;   /* [sequences + 1] */
+    const int32_t *lengths;  /* [sequences] */
+    const int32_t *pages;
+    int64_t ld_pages;        /* 0: max_pages */
+    int64_t max_pages;       /* 1..2^30 / page_size */
+} uw_kv_batch;
+
+/*
+ * uw_kv_append - rotate the new tokens' queries and keys, store their keys and values in the cache.
+ *   q: [rows, q_heads, head_dim], k and v: [rows, kv_heads, head_dim] of `dtype` (as uw_matmul leaves them: fp32 or bf16), rows
+ *   ldq, ldk, ldv elements apart (0: dense; multiples of 8), so that all three may be columns of one product's output.
+ *   q_out: bf16 [rows, q_heads, head_dim], rows ldq_out apart; it may be q itself.  Either q and q_out or k and v may be NULL.
+ *   r NULL: nothing is turned.  positions: int32 [rows], what the angles go by; NULL: the position in the cache.
+ *   The angle position * freq is reduced in 64 bits; products in fp32, one rounding to bf16.  A token whose position in the
+ *   cache is negative or past the table, or whose page is outside [0, pages), is not stored.  Rows outside
+ *   [starts[0], starts[sequences]) are left as they were.  Two rows with one slot: either is stored.  Asynchronous.
+ *   Errors: UW_ERR_INVALID_ARG (NULL, alignment: 16 bytes for q, k, v, q_out and 4 for the rest, 8 for freq; another current
+ *   device than the cache's; bad dtype or layout), UW_ERR_SHAPE, UW_ERR_CUDA.
+ */
+uw_status uw_kv_append(const uw_kv_cache *c, const uw_kv_batch *b, const uw_rotary *r, int64_t rows, uw_out_dtype dtype,
+                       const void *q, int64_t ldq, int q_heads, const void *k, int64_t ldk, const void *v, int64_t ldv,
+                       const int32_t *positions, uint16_t *q_out, int64_t ldq_out, uw_stream stream);
+
+/*
+ * uw_kv_attend - for every new token t and query head h, with the keys k_j and values v_j of h's key head
+ *   h / (q_heads / kv_heads) in t's sequence:
+ *     out[t, h] = sum_j p_j v_j,  p = softmax over j of (scale * q[t, h] . k_j),  lse[t, h] = ln sum_j exp(scale * q[t, h] . k_j)
+ *   over the positions j of its sequence's length that it may see: causal != 0: j <= position, and with window > 0
+ *   position - j < window; else all.  A row that sees nothing gets zeros and an lse of -inf.
+ *   q, out: bf16 [rows, q_heads, head_dim], rows ldq and ldo elements apart (0: dense; multiples of 8).  lse: fp32
+ *   [rows, q_heads] or NULL.  Sums in fp32; probabilities are rounded to bf16 in front of the second product, as its operand.
+ *   A page outside [0, pages) reads as zeros.  Slots behind a sequence's length may hold anything; a key or value of the
+ *   sequence itself that is not finite spoils the rows that see it, and may spoil others of its sequence that do not.
+ *   Rows outside [starts[0], starts[sequences]) are left as they were.  The same call gives the same bits in every run; how a
+ *   sequence's keys are cut, and so the last bits, depends on the whole batch's lengths.
+ *   workspace: uw_kv_attend_workspace_size bytes, 16-byte aligned; needs no initialisation.  Calls that may run at the
+ *   same time need one each.  Asynchronous.
+ *   Errors: UW_ERR_INVALID_ARG (NULL, alignment, scale not finite, window < 0, a window without causal, another current device
+ *   than the cache's), UW_ERR_SHAPE (rows, q_heads not a multiple of kv_heads or above 64 kv_heads, strides),
+ *   UW_ERR_WORKSPACE, UW_ERR_CUDA.
+ */
+uw_status uw_kv_attend_workspace_size(const uw_kv_cache *c, int sequences, int64_t rows, int q_heads, size_t *bytes);
+uw_status uw_kv_attend(const uw_kv_cache *c, const uw_kv_batch *b, int64_t rows, const uint16_t *q, int64_t ldq, int q_heads,
+                       float scale, int causal, int64_t window, uint16_t *out, int64_t ldo, float *lse, void *workspace,
+                       size_t ws_bytes, uw_stream stream);
+
+/* uw_kv_check - as uw_check, for a cache: UW_ERR_TIMEOUT if a bounded wait of a kernel on it expired. */
+uw_status uw_kv_check(const uw_kv_cache *c, uw_stream stream);
+
+/*
+ * What uw_edit_logits does to each row; every pointer is a device address or NULL (that edit is left out).  tokens holds a
+ * row's prompt and, behind it, what was generated: row r's tokens are tokens[r * ld_tokens + i], i < lengths[r], the first
+ * prompt_lengths[r] (NULL: 0) of them the prompt's.  Lengths are clamped to [0, max_tokens], ids outside the vocabulary are
+ * passed over.
+ */
+typedef struct {
+    const int32_t *tokens;
+    int64_t ld_tokens, max_tokens; /* ld_tokens 0: max_tokens */
+    const int32_t *lengths;        /* [rows]; needed with tokens */
+    const int32_t *prompt_lengths; /* [rows] */
+    const float *repetition;       /* [rows], > 0: logits of tokens in the prompt or generated, divided by it above 0, else multiplied */
+    const float *frequency;        /* [rows]: times the number of times the token was generated, subtracted */
+    const float *presence;         /* [rows]: subtracted once if it was generated */
+    const int32_t *bias_ids;       /* [rows, max_bias], with bias: added to these tokens' logits, a token's several entries in order */
+    const float *bias;
+    const int32_t *bias_lengths;   /* [rows], clamped to [0, max_bias]; NULL: max_bias */
+    int64_t max_bias;              /* 0..65536; rows of bias and bias_ids are max_bias apart */
+    const uint32_t *allowed;       /* [mask_count, ld_allowed] words: a token v whose bit v % 32 of word v / 32 is 0 becomes -inf */
+    int64_t ld_allowed, mask_count; /* ld_allowed 0: ceil(vocab / 32) */
+    const int32_t *mask_rows;      /* [rows]: which row of allowed; outside [0, mask_count): none.  NULL: row r's own (r < mask_count) */
+} uw_logit_edits;
+
+/*
+ * uw_edit_logits - penalties for repeated tokens, biases and grammar masks, in this order, on each row of logits:
+ *     x = repetition; x -= frequency * count; x -= presence; x += bias; -inf where not allowed        (fp32, one rounding)
+ *   logits: [rows, vocab] of `dtype`, rows ld elements apart (0: vocab); out: of out_dtype, rows ld_out apart.  out may be
+ *   logits itself with the same type and ld; then only logits that change are written, and without a mask only those are
+ *   read.  NaN stays NaN unless it is masked.  Elements behind vocab are left as they were.  No workspace.  Asynchronous; the
+ *   result does not depend on the run.
+ *   Errors: UW_ERR_INVALID_ARG (NULL, misaligned to the element, tokens without lengths, bias_ids without bias or the reverse,
+ *   penalties without tokens, out overlapping logits in part), UW_ERR_SHAPE (vocab outside 1..2^24, ld, ld_out < vocab,
+ *   max_tokens outside 0..2^24 - 1, max_bias), UW_ERR_CUDA.
+ */
+uw_status uw_edit_logits(const uw_logit_edits *e, const void *logits, uw_out_dtype dtype, int64_t rows, int64_t vocab,
+                         int64_t ld, void *out, uw_out_dtype out_dtype, int64_t ld_out, uw_stream stream);
+
 /* uw_check - synchronise `stream` and report (then clear) the matrix's device status word. */
 uw_status uw_check(const uw_matrix *m, uw_stream stream);
 

@@ -31,6 +31,8 @@ RESIDENT_HUFFMAN, RESIDENT_BOTH, RESIDENT_PALETTE = 0, 1, 2
 RESIDENT = {"huffman": RESIDENT_HUFFMAN, "both": RESIDENT_BOTH, "palette": RESIDENT_PALETTE}
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 SCORE_CHOOSES = 16  # added to either: the choice is by score + bias in place of logit + bias
+ROTARY_HALF, ROTARY_INTERLEAVED = 0, 1
+ROTARY_PLAIN, ROTARY_LINEAR, ROTARY_STRETCHED, ROTARY_BANDS, ROTARY_RAMP = 0, 1, 2, 3, 4
 SEQ_DIRECT = -1  # uw_sequence_run schedule: no side-stream transcode, every step its own AUTO plan
 STEP_CONCURRENT = 1  # uw_step flag: the step may overlap the step before it
 SEQ_GROUPS = 65536  # added to a uw_sequence_run schedule: overlap the groups of STEP_CONCURRENT steps
@@ -98,6 +100,28 @@ class NormDesc(ctypes.Structure):
                 ("block_dtype", ctypes.c_int32)]
 
 
+class RotaryDesc(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("freq", ctypes.c_void_p), ("scale", ctypes.c_float)]
+
+
+class KVDesc(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("pages", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("slot_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32)]
+
+
+class KVBatchDesc(ctypes.Structure):
+    _fields_ = [("sequences", ctypes.c_int32), ("starts", ctypes.c_void_p), ("lengths", ctypes.c_void_p), ("pages", ctypes.c_void_p),
+                ("ld_pages", ctypes.c_int64), ("max_pages", ctypes.c_int64)]
+
+
+class LogitEditsDesc(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_void_p), ("ld_tokens", ctypes.c_int64), ("max_tokens", ctypes.c_int64), ("lengths", ctypes.c_void_p),
+                ("prompt_lengths", ctypes.c_void_p), ("repetition", ctypes.c_void_p), ("frequency", ctypes.c_void_p), ("presence", ctypes.c_void_p),
+                ("bias_ids", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("bias_lengths", ctypes.c_void_p), ("max_bias", ctypes.c_int64),
+                ("allowed", ctypes.c_void_p), ("ld_allowed", ctypes.c_int64), ("mask_count", ctypes.c_int64), ("mask_rows", ctypes.c_void_p)]
+
+
 _lib = None
 _VP, _SZ, _I64, _INT = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int64, ctypes.c_int
 
@@ -136,6 +160,16 @@ _SIGS = {
     "uw_route": [ctypes.POINTER(RouterDesc), _VP, _INT, _I64, _I64, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP],
     "uw_block_norm": [ctypes.POINTER(NormDesc), _I64, _VP, _VP, _VP, _I64, _VP, _VP, _INT, _VP, _VP],
     "uw_token_logprobs": [_VP, _INT, _I64, _I64, _I64, ctypes.c_float, _VP, _VP, _VP, _INT, _VP, _VP, _VP],
+    "uw_rotary_frequencies": [_INT, ctypes.c_double, _INT, ctypes.c_double, ctypes.c_double, ctypes.c_double, _I64, _VP,
+                              ctypes.POINTER(ctypes.c_float)],
+    "uw_kv_create": [ctypes.POINTER(KVDesc), ctypes.POINTER(_VP)],
+    "uw_kv_free": [_VP],
+    "uw_kv_append": [_VP, ctypes.POINTER(KVBatchDesc), ctypes.POINTER(RotaryDesc), _I64, _INT, _VP, _I64, _INT, _VP, _I64, _VP, _I64, _VP, _VP, _I64,
+                     _VP],
+    "uw_kv_attend_workspace_size": [_VP, _INT, _I64, _INT, ctypes.POINTER(_SZ)],
+    "uw_kv_attend": [_VP, ctypes.POINTER(KVBatchDesc), _I64, _VP, _I64, _INT, ctypes.c_float, _INT, _I64, _VP, _I64, _VP, _VP, _SZ, _VP],
+    "uw_kv_check": [_VP, _VP],
+    "uw_edit_logits": [ctypes.POINTER(LogitEditsDesc), _VP, _INT, _I64, _I64, _I64, _VP, _INT, _I64, _VP],
     "uw_status_string": [_INT],
     "uw_last_error": [],
     "uw_version": [],
@@ -155,6 +189,7 @@ def lib():
             f.restype = _INT
         L.uw_free.restype = None
         L.uw_group_free.restype = None
+        L.uw_kv_free.restype = None
         L.uw_status_string.restype = ctypes.c_char_p
         L.uw_last_error.restype = ctypes.c_char_p
         L.uw_version.restype = ctypes.c_char_p
@@ -465,3 +500,183 @@ def token_logprobs(logits, rows: int, vocab: int, logprob=None, targets=None, en
     """uw_token_logprobs: log probabilities of `targets` (int32), entropies and the n_top most probable tokens."""
     _check(lib().uw_token_logprobs(_typed("logits", logits, dtype), dtype, rows, vocab, ld, temperature, _ptr(targets), _ptr(logprob), _ptr(entropy),
                                    n_top, _ptr(top_ids), _ptr(top_logprobs), _stream(stream)), "uw_token_logprobs")
+
+
+def _at(what: str, t, *dtypes) -> int:
+    """_ptr of a tensor of one of these types ("int32", ...), in device memory and with its last dimension dense; addresses pass."""
+    if t is None:
+        return 0
+    if isinstance(t, int):
+        return t
+    import torch
+    if not any(t.dtype == getattr(torch, d) for d in dtypes):
+        raise ValueError(f"{what} is {t.dtype}, the call takes {' or '.join(dtypes)}")
+    if not t.is_cuda:
+        raise ValueError(f"{what} is not in device memory")
+    if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{what}: the last dimension is not dense")
+    return t.data_ptr()
+
+
+_BF16 = ("bfloat16", "int16", "uint16")
+
+
+def _heads(what: str, t, rows: int, dim: int, dtypes):
+    """Address, elements from row to row and heads of a tensor [rows, heads, dim] or [rows, heads * dim]."""
+    if t is None or isinstance(t, int):
+        return t or 0, 0, None
+    p = _at(what, t, *dtypes)
+    width = t.shape[-1] * (t.shape[1] if t.dim() == 3 else 1)
+    if t.dim() not in (2, 3) or t.shape[0] < rows or width % dim or (t.dim() == 3 and (t.shape[2] != dim or (t.stride(1) != dim and t.shape[1] > 1))):
+        raise ValueError(f"{what} must be [rows, heads, {dim}] or [rows, heads * {dim}], a row's heads dense")
+    return p, t.stride(0) if t.shape[0] > 1 else 0, width // dim
+
+
+class Rotary:
+    """Rotary positions (a ``uw_rotary``): the first `dim` elements of a head, in pairs `layout` apart, by frequencies of `base`
+    scaled for long contexts (ROTARY_LINEAR, ...: uw_rotary_frequencies), held on the current CUDA device."""
+
+    def __init__(self, dim: int, base: float = 10000.0, layout: int = ROTARY_HALF, scaling: int = ROTARY_PLAIN, factor: float = 1.0,
+                 low: float = 1.0, high: float = 4.0, original: int = 8192):
+        self.freq, self.scale = rotary_frequencies(dim, base, scaling, factor, low, high, original)
+        import torch
+        self._dev = torch.from_numpy(self.freq).cuda()
+        self.desc = RotaryDesc(dim, layout, self._dev.data_ptr(), self.scale)
+        self._ref = ctypes.byref(self.desc)
+
+
+def rotary_frequencies(dim: int, base: float = 10000.0, scaling: int = ROTARY_PLAIN, factor: float = 1.0, low: float = 1.0, high: float = 4.0,
+                       original: int = 8192):
+    """uw_rotary_frequencies: (float64 array [dim / 2] in radians a position, factor on cos and sin)."""
+    f, s = np.zeros(max(1, dim // 2)), ctypes.c_float(0)
+    _check(lib().uw_rotary_frequencies(dim, base, scaling, factor, low, high, original, f.ctypes.data, ctypes.byref(s)), "uw_rotary_frequencies")
+    return f, s.value
+
+
+class KVBatch:
+    """The new tokens of a step (a ``uw_kv_batch``), int32 on the device: sequence s brings rows [starts[s], starts[s + 1]) and
+    holds lengths[s] tokens with them, in the pages pages[s] (a tensor [sequences, max_pages])."""
+
+    def __init__(self, starts, lengths, pages):
+        if pages.dim() != 2 or lengths.dim() != 1 or starts.dim() != 1 or pages.shape[0] != lengths.shape[0] or starts.shape[0] != lengths.shape[0] + 1:
+            raise ValueError("starts [sequences + 1], lengths [sequences], pages [sequences, max_pages]")
+        self._keep = (starts, lengths, pages)
+        self.sequences = lengths.shape[0]
+        self.desc = KVBatchDesc(self.sequences, _at("starts", starts, "int32"), _at("lengths", lengths, "int32"), _at("pages", pages, "int32"),
+                                pages.stride(0) if self.sequences > 1 else 0, pages.shape[1])
+        self._ref = ctypes.byref(self.desc)
+
+
+class KVCache:
+    """Keys and values in pages (a ``uw_kv_cache`` on the current CUDA device): k and v bf16 tensors [pages, page_size, kv_heads,
+    head_dim] of the same strides (head_dim dense; a transposed [pages, kv_heads, page_size, head_dim] is one)."""
+
+    def __init__(self, k, v):
+        self._h = None
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride():
+            raise ValueError("k and v must be [pages, page_size, kv_heads, head_dim] with the same strides")
+        self._keep = (k, v)
+        self.pages, self.page_size, self.kv_heads, self.head_dim = k.shape
+        d = KVDesc(_at("k", k, *_BF16), _at("v", v, *_BF16), self.pages, k.stride(0), k.stride(1), k.stride(2), self.page_size, self.kv_heads,
+                   self.head_dim)
+        h = ctypes.c_void_p()
+        _check(lib().uw_kv_create(ctypes.byref(d), ctypes.byref(h)), "uw_kv_create")
+        self._h = h
+
+    def close(self):
+        if getattr(self, "_h", None):
+            lib().uw_kv_free(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    @property
+    def handle(self):
+        return self._h
+
+    def append(self, batch, rows: int, k=None, v=None, q=None, q_out=None, q_heads: int = 0, rotary=None, positions=None, dtype: int = OUT_BF16,
+               ldq: int = 0, ldk: int = 0, ldv: int = 0, ldq_out: int = 0, stream=None):
+        """uw_kv_append: q, k, v of `dtype`, tensors [rows, heads, head_dim] (their strides and heads are taken from them) or
+        addresses; q_out bf16."""
+        D = self.head_dim
+        src = {OUT_F32: ("float32",), OUT_BF16: _BF16}.get(dtype, ("float32",) + _BF16)
+        pq, sq, hq = _heads("q", q, rows, D, src)
+        po, so, ho = _heads("q_out", q_out, rows, D, _BF16)
+        pk, sk, hk = _heads("k", k, rows, D, src)
+        pv, sv, hv = _heads("v", v, rows, D, src)
+        q_heads = q_heads or hq or ho or 0
+        if any(h not in (None, q_heads) for h in (hq, ho)) or any(h not in (None, self.kv_heads) for h in (hk, hv)):
+            raise ValueError(f"heads: q {hq}, q_out {ho} of {q_heads}, k {hk}, v {hv} of {self.kv_heads}")
+        _check(lib().uw_kv_append(self._h, batch._ref, rotary._ref if rotary is not None else None, rows, dtype, pq, ldq or sq, q_heads, pk, ldk or sk, pv,
+                                  ldv or sv, _at("positions", positions, "int32"), po, ldq_out or so, _stream(stream)), "uw_kv_append")
+
+    def workspace_size(self, batch, rows: int, q_heads: int) -> int:
+        n = ctypes.c_size_t(0)
+        _check(lib().uw_kv_attend_workspace_size(self._h, batch.sequences, rows, q_heads, ctypes.byref(n)), "uw_kv_attend_workspace_size")
+        return n.value
+
+    def attend(self, batch, rows: int, q, out, q_heads: int = 0, scale=None, causal: bool = True, window: int = 0, lse=None, workspace=None,
+               ws_bytes: int = 0, ldq: int = 0, ldo: int = 0, stream=None):
+        """uw_kv_attend: q and out bf16 [rows, q_heads, head_dim] (or addresses, with q_heads); scale None: head_dim ** -0.5."""
+        pq, sq, hq = _heads("q", q, rows, self.head_dim, _BF16)
+        po, so, ho = _heads("out", out, rows, self.head_dim, _BF16)
+        q_heads = q_heads or hq or ho or 0
+        if any(h not in (None, q_heads) for h in (hq, ho)):
+            raise ValueError(f"heads: q {hq}, out {ho} of {q_heads}")
+        if scale is None:
+            scale = self.head_dim ** -0.5
+        _check(lib().uw_kv_attend(self._h, batch._ref, rows, pq, ldq or sq, q_heads, scale, int(causal), window, po, ldo or so, _at("lse", lse, "float32"),
+                                  _ptr(workspace), ws_bytes, _stream(stream)), "uw_kv_attend")
+
+    def check(self, stream=None):
+        _check(lib().uw_kv_check(self._h, _stream(stream)), "uw_kv_check")
+
+
+def edit_logits(logits, rows: int, vocab: int, out, tokens=None, lengths=None, prompt_lengths=None, repetition=None, frequency=None, presence=None,
+                bias_ids=None, bias=None, bias_lengths=None, allowed=None, mask_rows=None, dtype: int = OUT_F32, out_dtype=None, ld: int = 0,
+                ld_out: int = 0, stream=None):
+    """uw_edit_logits on tensors: logits and out [rows, vocab or more] (or addresses, with ld), tokens int32 [rows, max_tokens], lengths and
+    prompt_lengths int32 [rows], penalties fp32 [rows], bias_ids int32 and bias fp32 [rows, max_bias], allowed int32 words
+    [masks, words].  out_dtype None: dtype."""
+    out_dtype = dtype if out_dtype is None else out_dtype
+    kind = {OUT_F32: ("float32",), OUT_BF16: _BF16}
+    p, po = (_at(w, t, *kind.get(d, ("float32",) + _BF16)) for w, t, d in (("logits", logits, dtype), ("out", out, out_dtype)))
+
+    def stride(what, t, given, width):
+        if given or isinstance(t, int) or t is None:
+            return given
+        if t.dim() != 2 or t.shape[0] < rows or t.shape[1] < width:
+            raise ValueError(f"{what} must be [rows, {width} or more]")
+        return t.stride(0) if rows > 1 else 0
+
+    def of_rows(what, t, *dtypes):
+        a = _at(what, t, *dtypes)
+        if t is not None and not isinstance(t, int) and (t.dim() != 1 or t.shape[0] < rows):
+            raise ValueError(f"{what} must be [rows]")
+        return a
+
+    d = LogitEditsDesc()
+    if tokens is not None and not isinstance(tokens, int) and tokens.dim() == 2 and tokens.shape[1] == 0:
+        tokens = repetition = frequency = presence = None  # no history: no penalties
+    d.tokens = _at("tokens", tokens, "int32")
+    if tokens is not None:
+        d.ld_tokens, d.max_tokens = stride("tokens", tokens, 0, 0), tokens.shape[1]
+    d.lengths, d.prompt_lengths = of_rows("lengths", lengths, "int32"), of_rows("prompt_lengths", prompt_lengths, "int32")
+    d.repetition, d.frequency, d.presence = (of_rows(w, t, "float32") for w, t in (("repetition", repetition), ("frequency", frequency), ("presence", presence)))
+    d.bias_ids, d.bias, d.bias_lengths = _at("bias_ids", bias_ids, "int32"), _at("bias", bias, "float32"), of_rows("bias_lengths", bias_lengths, "int32")
+    if bias_ids is not None and bias is not None:
+        if bias_ids.shape != bias.shape or bias.dim() != 2 or bias.shape[0] < rows or not bias.is_contiguous() or not bias_ids.is_contiguous():
+            raise ValueError("bias_ids and bias must be contiguous [rows, max_bias]")
+        d.max_bias = bias.shape[1]
+    d.allowed = _at("allowed", allowed, "int32", "uint32")
+    if allowed is not None:
+        if allowed.dim() != 2 or allowed.shape[1] * 32 < vocab:
+            raise ValueError("allowed must be [masks, ceil(vocab / 32)]")
+        d.ld_allowed, d.mask_count = allowed.stride(0) if allowed.shape[0] > 1 else 0, allowed.shape[0]
+    d.mask_rows = of_rows("mask_rows", mask_rows, "int32")
+    _check(lib().uw_edit_logits(ctypes.byref(d), p, dtype, rows, vocab, stride("logits", logits, ld, vocab), po, out_dtype,
+                                stride("out", out, ld_out, vocab), _stream(stream)), "uw_edit_logits")

@@ -1,0 +1,312 @@
+// k_edit.cu - penalties for repeated tokens, biases and grammar masks on rows of logits (sm_103a).
+//
+// A CTA has a slice of one row's vocabulary.  It looks through the row's whole history (from L2, which all slices of the
+// row share) and counts, for each token of its slice, in a word of shared memory: bits 0-23 how often it was generated,
+// bit 31 that it is in the prompt, bit 30 that the row's biases name it.  The additions are of whole numbers, so
+// their order does not matter.  Then one pass over the slice's logits: a word of 0 and an allowed token leave a logit as
+// it is; a named token's biases are added by looking through the list again, in its order.
+// Out of place a logit is read and written once, unless a 16-byte piece is masked out as a whole, which is not read.  In
+// place a piece in which nothing changes is neither read nor written.
+// Bound by memory.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "launch.cuh"
+#include "uw_internal.h"
+
+using namespace uw;
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr uint32_t kSeen = 1u << 31, kBias = 1u << 30, kCount = (1u << 24) - 1;
+
+struct EditArgs {
+    uw_logit_edits e;
+    const void *logits;
+    void *out;
+    int64_t vocab, ld, ld_out;
+    int slice;                // tokens of a CTA, a multiple of 32
+};
+
+template <bool F32>
+__device__ __forceinline__ float value_of(const void *p, int64_t i)
+{
+    if constexpr (F32) return ((const float *)p)[i];
+    else return __uint_as_float((uint32_t)((const uint16_t *)p)[i] << 16);
+}
+
+template <bool F32>
+__device__ __forceinline__ void put(void *p, int64_t i, float x)
+{
+    if constexpr (F32) ((float *)p)[i] = x;
+    else ((__nv_bfloat16 *)p)[i] = __float2bfloat16_rn(x);
+}
+
+struct Row {
+    float rep, freq, pres;
+    const int32_t *ids;
+    const float *bias;
+    int n_bias;
+};
+
+__device__ __forceinline__ float edited(float x, uint32_t w, int token, const Row &r)
+{
+    if (w & (kSeen | kCount)) x = x > 0.f ? x / r.rep : x * r.rep;
+    const uint32_t c = w & kCount;
+    if (c) x = x - r.freq * (float)c - r.pres;
+    if (w & kBias) {
+        for (int i = 0; i < r.n_bias; i++)
+            if (r.ids[i] == token) x += r.bias[i];
+    }
+    return x;
+}
+
+// W: logits of a piece (8 of bf16, 4 of fp32 inputs; 1: rows without 16-byte alignment)
+template <bool F32, bool OUT32, int W, bool PLACE>
+__global__ void __launch_bounds__(kThreads) edit_kernel(const EditArgs a)
+{
+    extern __shared__ uint32_t words[];
+    const int64_t row = blockIdx.y;
+    const int64_t v0 = (int64_t)blockIdx.x * a.slice;
+    const int n = (int)min((int64_t)a.slice, a.vocab - v0);
+    pdl_trigger();
+    for (int i = threadIdx.x; i < n; i += kThreads) words[i] = 0;
+    pdl_wait();
+    Row r;
+    r.rep = a.e.repetition ? a.e.repetition[row] : 1.f;
+    r.freq = a.e.frequency ? a.e.frequency[row] : 0.f;
+    r.pres = a.e.presence ? a.e.presence[row] : 0.f;
+    r.n_bias = 0;
+    int len = 0, prompt = 0;
+    if (a.e.tokens) {
+        len = (int)min((int64_t)max(a.e.lengths[row], 0), a.e.max_tokens);
+        if (a.e.prompt_lengths) prompt = a.e.prompt_lengths[row];
+    }
+    if (a.e.bias_ids) {
+        r.n_bias = (int)a.e.max_bias;
+        if (a.e.bias_lengths) r.n_bias = min(max(a.e.bias_lengths[row], 0), r.n_bias);
+        r.ids = a.e.bias_ids + row * a.e.max_bias;
+        r.bias = a.e.bias + row * a.e.max_bias;
+    }
+    const uint32_t *mask = nullptr;
+    if (a.e.allowed) {
+        const int64_t m = a.e.mask_rows ? a.e.mask_rows[row] : row;
+        if (m >= 0 && m < a.e.mask_count) mask = a.e.allowed + m * a.e.ld_allowed + v0 / 32;
+    }
+    __syncthreads();
+    const int32_t *tokens = a.e.tokens + row * a.e.ld_tokens;
+    for (int i0 = 0; i0 < len; i0 += 4 * kThreads) {
+        int64_t at[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const int i = i0 + j * kThreads + threadIdx.x;
+            at[j] = i < len ? (int64_t)tokens[i] - v0 : -1;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            if (at[j] < 0 || at[j] >= n) continue;
+            if (i0 + j * kThreads + (int)threadIdx.x >= prompt) atomicAdd(&words[at[j]], 1u);
+            else atomicOr(&words[at[j]], kSeen);
+        }
+    }
+    for (int i = threadIdx.x; i < r.n_bias; i += kThreads) {
+        const int64_t at = (int64_t)r.ids[i] - v0;
+        if (at >= 0 && at < n) atomicOr(&words[at], kBias);
+    }
+    __syncthreads();
+    const uint8_t *in = (const uint8_t *)a.logits + (row * a.ld + v0) * (F32 ? 4 : 2);
+    uint8_t *out = (uint8_t *)a.out + (row * a.ld_out + v0) * (OUT32 ? 4 : 2);
+    const int whole = W > 1 ? n / W * W : 0;
+    if constexpr (W > 1) {
+        constexpr uint32_t kAll = (1u << W) - 1;
+        constexpr int U = PLACE ? 1 : 4;  // pieces of a thread on their way
+        for (int p0 = threadIdx.x * W; p0 < whole; p0 += U * kThreads * W) {
+            uint4 raw[U];
+            uint32_t ok[U];
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                const int p = p0 + u * kThreads * W;
+                ok[u] = 0;
+                raw[u] = make_uint4(0, 0, 0, 0);
+                if (p >= whole) continue;
+                ok[u] = mask ? (mask[p >> 5] >> (p & 31)) & kAll : kAll;
+                if (!PLACE && ok[u]) raw[u] = *(const uint4 *)(in + (int64_t)p * (F32 ? 4 : 2));
+            }
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                const int p = p0 + u * kThreads * W;
+                if (p >= whole) continue;
+                uint32_t w[W];
+                uint32_t any = 0;
+#pragma unroll
+                for (int q = 0; q < W; q += 4) {
+                    const uint4 v = *(const uint4 *)(words + p + q);
+                    w[q] = v.x;
+                    w[q + 1] = v.y;
+                    w[q + 2] = v.z;
+                    w[q + 3] = v.w;
+                    any |= v.x | v.y | v.z | v.w;
+                }
+                if (PLACE) {
+                    if (!any && ok[u] == kAll) continue;
+                    if (ok[u]) raw[u] = *(const uint4 *)(in + (int64_t)p * (F32 ? 4 : 2));
+                }
+                float x[W];
+                const uint32_t b[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+#pragma unroll
+                for (int q = 0; q < 4; q++) {
+                    if constexpr (F32) {
+                        x[q] = __uint_as_float(b[q]);
+                    } else {
+                        x[2 * q] = __uint_as_float(b[q] << 16);
+                        x[2 * q + 1] = __uint_as_float(b[q] & 0xFFFF0000u);
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < W; q++) {
+                    if (any && w[q]) x[q] = edited(x[q], w[q], (int)v0 + p + q, r);
+                    if (!((ok[u] >> q) & 1u)) x[q] = -INFINITY;
+                }
+                uint8_t *o = out + (int64_t)p * (OUT32 ? 4 : 2);
+                if constexpr (OUT32) {
+#pragma unroll
+                    for (int q = 0; q < W; q += 4) *(float4 *)(o + 4 * q) = make_float4(x[q], x[q + 1], x[q + 2], x[q + 3]);
+                } else {
+                    uint32_t h[W / 2];
+#pragma unroll
+                    for (int q = 0; q < W; q += 2) {
+                        const __nv_bfloat162 v = __floats2bfloat162_rn(x[q], x[q + 1]);
+                        h[q / 2] = *(const uint32_t *)&v;
+                    }
+                    if constexpr (W == 8) *(uint4 *)o = make_uint4(h[0], h[1], h[2], h[3]);
+                    else *(uint2 *)o = make_uint2(h[0], h[1]);
+                }
+            }
+        }
+    }
+    constexpr int U = PLACE ? 1 : 8;
+    for (int p0 = whole + threadIdx.x; p0 < n; p0 += U * kThreads) {
+        float x[U];
+        bool ok[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int p = p0 + u * kThreads;
+            ok[u] = p < n && (!mask || ((mask[p >> 5] >> (p & 31)) & 1u));
+            x[u] = !PLACE && ok[u] ? value_of<F32>(in, p) : -INFINITY;
+        }
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int p = p0 + u * kThreads;
+            if (p >= n) break;
+            const uint32_t w = words[p];
+            if (PLACE) {
+                if (!w && ok[u]) continue;
+                if (ok[u]) x[u] = value_of<F32>(in, p);
+            }
+            put<OUT32>(out, p, ok[u] && w ? edited(x[u], w, (int)v0 + p, r) : x[u]);
+        }
+    }
+}
+
+template <bool F32, bool OUT32>
+cudaError_t launch_types(const EditArgs &a, int64_t rows, bool wide, bool place, cudaStream_t st)
+{
+    constexpr int W = F32 ? 4 : 8;
+    const dim3 grid((unsigned)((a.vocab + a.slice - 1) / a.slice), (unsigned)rows);
+    const size_t smem = (size_t)a.slice * 4;
+    if constexpr (F32 == OUT32) {
+        if (place) return launch_dependent(wide ? edit_kernel<F32, OUT32, W, true> : edit_kernel<F32, OUT32, 1, true>, grid, kThreads, smem, 0, st, a);
+    }
+    return launch_dependent(wide ? edit_kernel<F32, OUT32, W, false> : edit_kernel<F32, OUT32, 1, false>, grid, kThreads, smem, 0, st, a);
+}
+
+bool aligned(const void *p, unsigned n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
+}  // namespace
+
+extern "C" uw_status uw_edit_logits(const uw_logit_edits *e, const void *logits, uw_out_dtype dtype, int64_t rows, int64_t vocab, int64_t ld,
+                                    void *out, uw_out_dtype out_dtype, int64_t ld_out, uw_stream stream)
+{
+    clear_error();
+    if (!e) return fail(UW_ERR_INVALID_ARG, "uw_edit_logits: NULL edits");
+    if (ld == 0) ld = vocab;
+    if (ld_out == 0) ld_out = vocab;
+    const int64_t most = (int64_t)1 << 40;
+    if (rows < 0 || rows > ((int64_t)1 << 31) - 1024 || vocab < 1 || vocab > (1 << 24) || ld < vocab || ld_out < vocab || ld > most || ld_out > most)
+        return fail(UW_ERR_SHAPE, "uw_edit_logits: rows=%lld vocab=%lld ld=%lld ld_out=%lld", (long long)rows, (long long)vocab, (long long)ld, (long long)ld_out);
+    if ((dtype != UW_OUT_F32 && dtype != UW_OUT_BF16) || (out_dtype != UW_OUT_F32 && out_dtype != UW_OUT_BF16))
+        return fail(UW_ERR_INVALID_ARG, "uw_edit_logits: bad dtype");
+    const bool f32 = dtype == UW_OUT_F32, o32 = out_dtype == UW_OUT_F32;
+    EditArgs a{*e, logits, out, vocab, ld, ld_out, 0};
+    if (a.e.tokens) {
+        if (!a.e.lengths) return fail(UW_ERR_INVALID_ARG, "uw_edit_logits: tokens without lengths");
+        if (a.e.ld_tokens == 0) a.e.ld_tokens = a.e.max_tokens;
+        if (a.e.max_tokens < 0 || a.e.max_tokens >= (1 << 24) || (rows > 1 && a.e.ld_tokens < a.e.max_tokens) || a.e.ld_tokens > most)
+            return fail(UW_ERR_SHAPE, "uw_edit_logits: max_tokens=%lld ld_tokens=%lld", (long long)a.e.max_tokens, (long long)a.e.ld_tokens);
+    } else if (a.e.repetition || a.e.frequency || a.e.presence) {
+        return fail(UW_ERR_INVALID_ARG, "uw_edit_logits: penalties without tokens");
+    }
+    if (!a.e.repetition && !a.e.frequency && !a.e.presence) a.e.tokens = nullptr;  // nothing looks at them
+    if (!a.e.bias_ids != !a.e.bias) return fail(UW_ERR_INVALID_ARG, "uw_edit_logits: bias_ids and bias go together");
+    if (a.e.max_bias < 0 || a.e.max_bias > 65536) return fail(UW_ERR_SHAPE, "uw_edit_logits: max_bias=%lld", (long long)a.e.max_bias);
+    const int64_t words = (vocab + 31) / 32;
+    if (a.e.allowed) {
+        if (a.e.ld_allowed == 0) a.e.ld_allowed = words;
+        if (a.e.mask_count < 0 || a.e.ld_allowed < words || a.e.ld_allowed > most)
+            return fail(UW_ERR_SHAPE, "uw_edit_logits: mask_count=%lld ld_allowed=%lld", (long long)a.e.mask_count, (long long)a.e.ld_allowed);
+    }
+    for (const void *p : {(const void *)a.e.tokens, (const void *)a.e.lengths, (const void *)a.e.prompt_lengths, (const void *)a.e.repetition,
+                          (const void *)a.e.frequency, (const void *)a.e.presence, (const void *)a.e.bias_ids, (const void *)a.e.bias,
+                          (const void *)a.e.bias_lengths, (const void *)a.e.allowed, (const void *)a.e.mask_rows})
+        if (!aligned(p, 4)) return fail(UW_ERR_INVALID_ARG, "uw_edit_logits: a pointer is not 4-byte aligned");
+    if (!aligned(logits, f32 ? 4 : 2) || !aligned(out, o32 ? 4 : 2)) return fail(UW_ERR_INVALID_ARG, "uw_edit_logits: logits or out not aligned to their elements");
+    if (rows == 0) return UW_OK;
+    if (!logits || !out) return fail(UW_ERR_INVALID_ARG, "uw_edit_logits: logits or out NULL");
+    const bool place = logits == out && f32 == o32 && (ld == ld_out || rows == 1);
+    if (!place) {
+        const uintptr_t i0 = (uintptr_t)logits, i1 = i0 + (uintptr_t)(((rows - 1) * ld + vocab) * (f32 ? 4 : 2));
+        const uintptr_t o0 = (uintptr_t)out, o1 = o0 + (uintptr_t)(((rows - 1) * ld_out + vocab) * (o32 ? 4 : 2));
+        // rows side by side, a stride apart, may lie between one another
+        const uintptr_t li = (uintptr_t)ld * (f32 ? 4 : 2), lo = (uintptr_t)ld_out * (o32 ? 4 : 2), d = li == lo ? (o0 - i0 + li * ((uintptr_t)1 << 20)) % li : 0;
+        const bool between = li == lo && d >= (uintptr_t)vocab * (f32 ? 4 : 2) && li - d >= (uintptr_t)vocab * (o32 ? 4 : 2);
+        if (i0 < o1 && o0 < i1 && !between) return fail(UW_ERR_INVALID_ARG, "uw_edit_logits: out overlaps logits (it may be logits itself, with their type and ld)");
+    }
+    if (place && !a.e.tokens && !a.e.bias_ids && !a.e.allowed) return UW_OK;
+    // rows of 16-byte pieces; out's pieces are of as many logits
+    const int W = f32 ? 4 : 8;
+    const bool wide = aligned(logits, 16) && aligned(out, W * (o32 ? 4 : 2) >= 16 ? 16 : 8) && (rows == 1 || (ld % W == 0 && ld_out % W == 0));
+    // A slice of 8192 tokens (32 KB of counts); smaller ones for few rows, so that the GPU is full.
+    a.slice = 8192;
+    while (a.slice > 1024 && rows * ((vocab + a.slice - 1) / a.slice) < 2 * num_sms()) a.slice /= 2;
+    for (int64_t r0 = 0; r0 < rows; r0 += 65535) {  // the grid's second dimension
+        const int64_t n = std::min<int64_t>(rows - r0, 65535);
+        EditArgs b = a;
+        b.logits = (const uint8_t *)a.logits + r0 * ld * (f32 ? 4 : 2);
+        b.out = (uint8_t *)a.out + r0 * ld_out * (o32 ? 4 : 2);
+        if (b.e.tokens) {
+            b.e.tokens += r0 * a.e.ld_tokens;
+            b.e.lengths += r0;
+            if (b.e.prompt_lengths) b.e.prompt_lengths += r0;
+        }
+        if (b.e.repetition) b.e.repetition += r0;
+        if (b.e.frequency) b.e.frequency += r0;
+        if (b.e.presence) b.e.presence += r0;
+        if (b.e.bias_ids) {
+            b.e.bias_ids += r0 * a.e.max_bias;
+            b.e.bias += r0 * a.e.max_bias;
+            if (b.e.bias_lengths) b.e.bias_lengths += r0;
+        }
+        if (b.e.allowed && b.e.mask_rows) b.e.mask_rows += r0;
+        else if (b.e.allowed) {
+            b.e.allowed += r0 * a.e.ld_allowed;
+            b.e.mask_count = std::max<int64_t>(a.e.mask_count - r0, 0);
+        }
+        const cudaError_t x = f32 ? (o32 ? launch_types<true, true>(b, n, wide, place, (cudaStream_t)stream) : launch_types<true, false>(b, n, wide, place, (cudaStream_t)stream))
+                                  : (o32 ? launch_types<false, true>(b, n, wide, place, (cudaStream_t)stream) : launch_types<false, false>(b, n, wide, place, (cudaStream_t)stream));
+        if (x != cudaSuccess) return fail(UW_ERR_CUDA, "uw_edit_logits: launch: %s", cudaGetErrorString(x));
+    }
+    return UW_OK;
+}
