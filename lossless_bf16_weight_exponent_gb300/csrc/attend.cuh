@@ -64,4 +64,8 @@ __device__ __forceinline__ SeqWork<R, K> seq_work(const AttendCall &a, int s)
 template <int R, int D>
 __host__ __device__ constexpr size_t slot_floats() { return (size_t)R * (D + 2); }
 
+// k_attend_tc.cu: items of 256 rows on tcgen05
+size_t attend_tc_slot_floats(int D);
+int launch_attend_tc(const uw_kv_cache *c, const AttendCall &a, int ctas, void *stream);
+
 }  // namespace uw

@@ -510,16 +510,19 @@ cudaError_t launch16(const uw_kv_cache *c, const AttendCall &call, int ctas, cud
 }
 
 struct Plan {
+    bool tc;                     // items of 256 rows on tcgen05, else of 16
     int ctas;
     size_t cuts, bytes;          // bytes of the cuts, of all
 };
 
-Plan plan_of(const uw_kv_cache *c)
+Plan plan_of(const uw_kv_cache *c, int sequences, int64_t rows, int q_heads)
 {
     Plan p;
+    p.tc = rows * (q_heads / c->d.kv_heads) > 64 * (int64_t)sequences;
     p.ctas = std::max(1, device_sms());
     p.cuts = (p.ctas * sizeof(Cut) + 255) / 256 * 256;
-    p.bytes = p.cuts + 2 * (size_t)p.ctas * (c->d.head_dim == 128 ? slot_floats<kRows, 128>() : slot_floats<kRows, 64>()) * sizeof(float);
+    const size_t slot = p.tc ? attend_tc_slot_floats(c->d.head_dim) : c->d.head_dim == 128 ? slot_floats<kRows, 128>() : slot_floats<kRows, 64>();
+    p.bytes = p.cuts + 2 * (size_t)p.ctas * slot * sizeof(float);
     return p;
 }
 
@@ -545,7 +548,7 @@ extern "C" uw_status uw_kv_attend_workspace_size(const uw_kv_cache *c, int seque
     if (!c || !bytes) return fail(UW_ERR_INVALID_ARG, "uw_kv_attend_workspace_size: NULL argument");
     const uw_status s = check_heads(c, sequences, rows, q_heads, "uw_kv_attend_workspace_size");
     if (s != UW_OK) return s;
-    *bytes = plan_of(c).bytes;
+    *bytes = plan_of(c, sequences, rows, q_heads).bytes;
     return UW_OK;
 }
 
@@ -570,7 +573,7 @@ extern "C" uw_status uw_kv_attend(const uw_kv_cache *c, const uw_kv_batch *b, in
     if (!q || !out || !aligned16(q) || !aligned16(out) || ((uintptr_t)lse & 3)) return fail(UW_ERR_INVALID_ARG, "uw_kv_attend: q or out NULL, or a pointer not aligned");
     if (q == out) return fail(UW_ERR_INVALID_ARG, "uw_kv_attend: out is q");
     if ((s = check_kv_device(c, "uw_kv_attend")) != UW_OK) return s;
-    const Plan p = plan_of(c);
+    const Plan p = plan_of(c, b->sequences, rows, q_heads);
     if (ws_bytes < p.bytes || !workspace) return fail(UW_ERR_WORKSPACE, "uw_kv_attend: workspace of %zu bytes, %zu needed", ws_bytes, p.bytes);
     if (!aligned16(workspace)) return fail(UW_ERR_INVALID_ARG, "uw_kv_attend: workspace not 16-byte aligned");
     a.q = q;
@@ -586,6 +589,8 @@ extern "C" uw_status uw_kv_attend(const uw_kv_cache *c, const uw_kv_batch *b, in
     a.cuts = (Cut *)workspace;
     a.part = (float *)((uint8_t *)workspace + p.cuts);
     a.status = c->status;
-    const cudaError_t e = c->d.head_dim == 128 ? launch16<128>(c, a, std::min(p.ctas, num_sms()), (cudaStream_t)stream) : launch16<64>(c, a, std::min(p.ctas, num_sms()), (cudaStream_t)stream);
+    const int ctas = std::min(p.ctas, num_sms());
+    const cudaError_t e = p.tc ? (cudaError_t)launch_attend_tc(c, a, ctas, stream)
+                        : c->d.head_dim == 128 ? launch16<128>(c, a, ctas, (cudaStream_t)stream) : launch16<64>(c, a, ctas, (cudaStream_t)stream);
     return e == cudaSuccess ? UW_OK : fail(UW_ERR_CUDA, "uw_kv_attend: launch: %s", cudaGetErrorString(e));
 }

@@ -1,0 +1,736 @@
+// k_attend_tc.cu - attention of many new tokens over a cache of keys and values in pages, on tcgen05 (sm_103a).
+//
+// An item is 256 query rows - tokens x query heads of one key head - as two tiles A and B of 128, against tiles of 128 keys.
+//   S = Q K^T   (128 x 128, operands in shared memory), P = 2^(scale2 S - m) by a warpgroup, a thread a row,
+//   O += P V    (P in tensor memory, V from shared memory as it lies in the cache: keys x elements)
+// Roles of the twelve warps:
+//   - 0-3 and 4-7: softmax, output and queries of tile A, of tile B.  A thread holds its row's 128 scores in registers, so a
+//     row's maximum and sum take no exchange.  The output is rescaled only when a maximum has grown by more than 2^8 (then
+//     by tensor memory loads and stores of the row): probabilities are at most 256 and keep their relative precision;
+//   - 8: tensor copies of the pages' slots of one head, keys and values in turn, into a ring of 128-key tiles.  Values that
+//     no row of the item sees are set to zero in shared memory when they have landed, as 0 x NaN is NaN;
+//   - 9: the products, by one thread.  The k-th product of P and V is issued behind the (k+1)-th of Q and K, so a tile's softmax
+//     runs under the other tile's products (or, in items of up to 128 rows, under the copy of the next keys);
+//   - 10, 11: none, they make up the third warpgroup, which gives registers to the other two.
+// Tensor memory: O of A and B, one S, P of A and of B: 2 D + 128 + 2 x 64 columns.  One S is enough as a warpgroup takes its
+// scores into registers at once, under the product in between, and P does not lie in S: every reuse waits on a barrier of
+// what used it last.
+// Rows of P and V are rounded to bf16 as operands (2^-9 of each; the sum of the powers is taken before that).
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "attend.cuh"
+#include "dev_async.cuh"
+#include "f32x2.cuh"
+#include "launch.cuh"
+#include "uw_internal.h"
+
+namespace uw {
+
+namespace {
+
+using namespace dev;
+
+constexpr int kWarps = 12, kThreads = 32 * kWarps;
+constexpr int kCopyWarp = 8, kMmaWarp = 9;
+constexpr int kRows = 256, kTile = 128;
+constexpr float kNegInf = -INFINITY;
+constexpr float kGrow = 8.f;      // log2 of how far a maximum may grow before the output is rescaled
+
+struct Start {
+    int s, head, rt, off;
+};
+
+template <int D>
+struct Layout {
+    static constexpr uint32_t half = kTile * 128;               // 64 elements of 128 rows or keys
+    static constexpr uint32_t tile = half * (D / 64);           // a tile of queries, keys or values
+    static constexpr int slots = D == 128 ? 5 : 10;
+    static constexpr uint32_t bars = 8 * (2 * slots + 16);
+    static constexpr size_t smem = 1024 + 2 * tile + slots * tile + bars + 8 * kWarps + sizeof(Start) + 16;
+    static_assert(smem <= 227 * 1024, "shared memory");
+    // columns of tensor memory
+    static constexpr uint32_t o = 0, s = 2 * D, p = s + 128;    // O of tile t at o + t D, P at p + 64 t
+    static_assert(p + 128 <= 512, "tensor memory");
+};
+
+struct Args {
+    CUtensorMap km, vm;
+    AttendCall c;
+    uint32_t q_xor, q_and;    // what turns a pair of query elements for a negative or zero scale
+};
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
+
+__device__ __forceinline__ void tma4d(uint32_t dst, const CUtensorMap *map, int x, int slot, int head, int page, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(slot), "r"(head), "r"(page), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, "
+        "%19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]),
+          "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]),
+          "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]),
+          "=r"(v[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+// descriptor of values as the second operand: keys (the summed dimension) 128 bytes apart, 64 elements (columns of the result)
+// in a row of the 128-byte swizzle, groups of eight keys 1024 bytes apart, blocks of 64 elements `half` bytes apart
+__device__ __forceinline__ uint64_t values_desc(uint32_t addr, uint32_t half)
+{
+    uint64_t d = (uint64_t)((addr >> 4) & 0x3FFFu);
+    d |= (uint64_t)(half >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *(const uint32_t *)&v;
+}
+
+// ------------------------------------------------------------------------------------------------ the work
+struct Seq {
+    KvSeq q;
+    int keys, row_tiles;
+};
+
+__device__ __forceinline__ Seq seq_at(const AttendCall &a, int s)
+{
+    Seq w;
+    w.q = kv_seq(a.b, s);
+    w.keys = min(w.q.len, a.b.capacity);
+    w.row_tiles = (int)(((int64_t)w.q.n * a.group + kRows - 1) / kRows);
+    return w;
+}
+
+// the keys [lo, hi) that some row of a tile of rows sees, and the tiles of keys [t0, t0 + nt) that hold them (one at least)
+struct Span {
+    int lo, hi, t0, nt;
+};
+
+__device__ __forceinline__ Span span_of(const AttendCall &a, int n, int len, int keys, int rt)
+{
+    const int i0 = (int)((int64_t)rt * kRows / a.group), i1 = (int)(min((int64_t)n * a.group, (int64_t)(rt + 1) * kRows) - 1) / a.group;
+    const int64_t p0 = (int64_t)len - n;
+    Span r;
+    r.hi = a.causal ? (int)min(max(p0 + i1 + 1, (int64_t)0), (int64_t)keys) : keys;
+    r.lo = a.window ? (int)min(max(p0 + i0 - a.window + 1, (int64_t)0), (int64_t)r.hi) : 0;
+    r.t0 = r.lo / kTile;
+    r.nt = max(1, (r.hi + kTile - 1) / kTile - r.t0);
+    return r;
+}
+
+// units of sequence s for one key head, by the whole warp, a sequence a lane (s < 0: none)
+__device__ __forceinline__ int64_t units_of(const AttendCall &a, int s)
+{
+    const int lane = threadIdx.x & 31;
+    Seq w{};
+    if (s >= 0 && s < a.b.sequences) w = seq_at(a, s);
+    int64_t u = 0;
+    const bool many = w.row_tiles > 2;
+    if (!many)
+        for (int rt = 0; rt < w.row_tiles; rt++) u += span_of(a, w.q.n, w.q.len, w.keys, rt).nt;
+    unsigned left = __ballot_sync(0xFFFFFFFFu, many);
+    while (left) {
+        const int src = __ffs(left) - 1;
+        left &= left - 1;
+        const int n = __shfl_sync(0xFFFFFFFFu, w.q.n, src), len = __shfl_sync(0xFFFFFFFFu, w.q.len, src);
+        const int keys = __shfl_sync(0xFFFFFFFFu, w.keys, src), tiles = __shfl_sync(0xFFFFFFFFu, w.row_tiles, src);
+        int64_t x = 0;
+        for (int rt = lane; rt < tiles; rt += 32) x += span_of(a, n, len, keys, rt).nt;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
+        if (lane == src) u = x;
+    }
+    return u;
+}
+
+// an item, and how many of its tiles of keys lie in front of this CTA's
+struct Cursor {
+    Seq w;
+    Span k;
+    int s, head, rt, off;
+    __device__ __forceinline__ void enter(const AttendCall &a) { k = span_of(a, w.q.n, w.q.len, w.keys, rt); }
+    __device__ __forceinline__ Cursor(const AttendCall &a, const Start &f) : s(f.s), head(f.head), rt(f.rt), off(f.off)
+    {
+        w = seq_at(a, s);
+        enter(a);
+    }
+    // the next item; only called while one is left
+    __device__ __forceinline__ void next(const AttendCall &a)
+    {
+        off = 0;
+        if (++rt >= w.row_tiles) {
+            rt = 0;
+            if (++head >= a.kv_heads) {
+                head = 0;
+                do w = seq_at(a, ++s);
+                while (!w.row_tiles);
+            }
+        }
+        enter(a);
+    }
+    __device__ __forceinline__ int tiles(int64_t left) const { return (int)min((int64_t)(k.nt - off), left); }
+    __device__ __forceinline__ int rows(const AttendCall &a) const { return (int)min((int64_t)w.q.n * a.group - (int64_t)rt * kRows, (int64_t)kRows); }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_constant__ Args g)
+{
+    using L = Layout<D>;
+    constexpr int NS = L::slots;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const AttendCall &a = g.c;
+    uint8_t *qs = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);  // [2] tiles
+    uint8_t *ring = qs + 2 * L::tile;
+    uint64_t *full = (uint64_t *)(ring + NS * L::tile);
+    uint64_t *empty = full + NS;
+    uint64_t *raw = empty + NS;                       // a tile whose values are put right before it counts as full
+    uint64_t *qfull = raw + 1, *sfull = qfull + 2, *sfree = sfull + 2, *pfull = sfree + 1, *pvdone = pfull + 2, *ofree = pvdone + 2, *done = ofree + 2;
+    int64_t *sums = (int64_t *)((uint8_t *)full + L::bars);
+    Start *found = (Start *)(sums + kWarps);
+    uint32_t *tmem_slot = (uint32_t *)(found + 1);
+    const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; i++) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        mbar_init(raw, 1);
+        mbar_init(sfree, 4);
+        mbar_init(done, 1);
+        for (int t = 0; t < 2; t++) {
+            mbar_init(&qfull[t], 4);
+            mbar_init(&sfull[t], 1);
+            mbar_init(&pfull[t], 4);
+            mbar_init(&pvdone[t], 1);
+            mbar_init(&ofree[t], 4);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_slot)), "r"(512) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    pdl_trigger();
+    pdl_wait();
+
+    // ---------------------------------------------------------------------------------- this CTA's units
+    int64_t one = 0, mine = 0;
+    for (int s0 = 0; s0 < a.b.sequences; s0 += kThreads) {
+        one = units_of(a, s0 + (int)threadIdx.x) * a.kv_heads;
+        mine += one;
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, d);
+    if (lane == 0) sums[warp] = mine;
+    __syncthreads();
+    int64_t U = 0;
+    for (int i = 0; i < kWarps; i++) U += sums[i];
+    const int64_t G = gridDim.x;
+    const int64_t ua = U * blockIdx.x / G, ub = U * (blockIdx.x + 1) / G;
+    const bool any = ua < ub;
+    if (any) {
+        int64_t before = 0;
+        for (int s0 = 0; s0 < a.b.sequences && before <= ua; s0 += kThreads) {
+            const int s = s0 + threadIdx.x;
+            const int64_t n = a.b.sequences <= kThreads ? one : units_of(a, s) * a.kv_heads;
+            int64_t incl = n;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int64_t o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+                if (lane >= d) incl += o;
+            }
+            __syncthreads();
+            if (lane == 31) sums[warp] = incl;
+            __syncthreads();
+            int64_t excl = before + incl - n;
+            for (int i = 0; i < kWarps; i++) {
+                if (i < warp) excl += sums[i];
+                before += sums[i];
+            }
+            // the warp that has the sequence looks for the tile of rows
+            const unsigned hit = __ballot_sync(0xFFFFFFFFu, n && excl <= ua && ua < excl + n);
+            if (hit) {
+                const int src = __ffs(hit) - 1;
+                const int64_t per = __shfl_sync(0xFFFFFFFFu, n, src) / a.kv_heads, in = ua - __shfl_sync(0xFFFFFFFFu, excl, src);
+                const int sq = s0 + 32 * warp + src, head = (int)(in / per);
+                int64_t at = in - (int64_t)head * per;  // units of the head in front of ours
+                const Seq w = seq_at(a, sq);
+                for (int r0 = 0; r0 < w.row_tiles; r0 += 32) {
+                    const int nt = r0 + lane < w.row_tiles ? span_of(a, w.q.n, w.q.len, w.keys, r0 + lane).nt : 0;
+                    int64_t x = nt;
+#pragma unroll
+                    for (int d = 1; d < 32; d <<= 1) {
+                        const int64_t o = __shfl_up_sync(0xFFFFFFFFu, x, d);
+                        if (lane >= d) x += o;
+                    }
+                    if (at < x && at >= x - nt) *found = Start{sq, head, r0 + lane, (int)(at - (x - nt))};
+                    const int64_t all = __shfl_sync(0xFFFFFFFFu, x, 31);
+                    if (at < all) break;
+                    at -= all;
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    bool ok = true;
+
+    // 12 warps have 168 registers a thread at launch; a row of scores wants more: 256 x 200 + 128 x 104 is what 384 x 168 is
+    if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if (any && warp == kCopyWarp) {
+        // ------------------------------------------------------------------------------ copies
+        Cursor c(a, *found);
+        int64_t left = ub - ua;
+        int n = 0;                        // tiles asked for: keys, values, keys, ...
+        // values that are to be put right when they have landed
+        bool fix = false;
+        int fix_slot = 0, fix_lo = 0, fix_hi = 0;
+        uint32_t raw_phase = 0;
+        auto mend = [&] {
+            if (!fix) return;
+            fix = false;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(raw, raw_phase & 1))) ok = false;
+            raw_phase++;
+            uint8_t *v = ring + fix_slot * L::tile;
+            for (int i = lane; i < kTile * (D / 8); i += 32) {
+                const int row = i / (D / 8), ch = i % (D / 8);
+                if (row >= fix_lo && row < fix_hi) continue;
+                *(uint4 *)(v + (ch >> 3) * L::half + row * 128 + ((ch & 7) ^ (row & 7)) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[fix_slot]);
+            __syncwarp();
+        };
+        // a lane's copies: a box of slots, 64 elements each
+        const int boxes = kTile / a.box, half = lane % (D / 64), bx0 = lane / (D / 64);
+        constexpr int kPer = 32 / (D / 64);          // boxes of one round of lanes
+        const uint32_t box_bytes = (uint32_t)a.box * 128u;
+        while (left > 0 && ok) {
+            const int nt = c.tiles(left);
+            const int32_t *table = a.b.pages + (int64_t)c.s * a.b.ld_pages;
+            for (int j = 0; j < nt && ok; j++) {
+                const int key0 = (c.k.t0 + c.off + j) * kTile;
+                const bool odd = key0 < c.k.lo || key0 + kTile > c.k.hi;
+                for (int kv = 0; kv < 2 && ok; kv++) {
+                    const int slot = n % NS;
+                    if (n >= NS && !__all_sync(0xFFFFFFFFu, mbar_test(&empty[slot], ((n / NS) & 1) ^ 1))) {
+                        mend();
+                        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&empty[slot], ((n / NS) & 1) ^ 1))) { ok = false; break; }
+                    }
+                    const bool mended = kv && odd;
+                    if (mended) mend();              // the one before
+                    uint64_t *bar = mended ? raw : &full[slot];
+                    if (lane == 0) mbar_expect_tx(bar, L::tile);
+                    __syncwarp();
+                    for (int b0 = 0; b0 < boxes; b0 += kPer) {
+                        const int bx = b0 + bx0;
+                        if (bx < boxes) {
+                            const int key = key0 + bx * a.box, pi = key / a.page_size;
+                            const int page = key < c.w.keys ? table[pi] : -1;
+                            tma4d(saddr(ring) + slot * L::tile + half * L::half + bx * box_bytes, kv ? &g.vm : &g.km, half * 64, key - pi * a.page_size, c.head,
+                                  page, saddr(bar));
+                        }
+                    }
+                    __syncwarp();
+                    if (mended) {
+                        fix = true;
+                        fix_slot = slot;
+                        fix_lo = c.k.lo - key0;
+                        fix_hi = c.k.hi - key0;
+                    }
+                    n++;
+                }
+            }
+            left -= nt;
+            if (left > 0) c.next(a);
+        }
+        mend();
+        if (!ok) {
+            if (lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
+            // what is on its way lands before the block ends (a tile that waits to be put right: above)
+            for (int i = n > NS ? n - NS : 0; i < n; i++) mbar_wait(&full[i % NS], (i / NS) & 1);
+        }
+    } else if (any && warp == kMmaWarp) {
+        // ------------------------------------------------------------------------------ products
+        Cursor c(a, *found);
+        int64_t left = ub - ua;
+        const bool leader = elect_one();
+        constexpr uint32_t id_s = idesc_bf16(128, 128), id_o = idesc_bf16(128, D) | 1u << 16;  // the second operand's columns run along memory
+        const uint32_t q0 = saddr(qs), r0 = saddr(ring);
+        int n = 0;                          // tiles of keys before this one
+        int qk = 0;                         // products of Q and K so far
+        int segs[2] = {0, 0}, pv[2] = {0, 0};  // of each tile of rows: segments begun, products of P and V
+        // the product of P and V that is due
+        struct Due {
+            int t, vtile, first, last;      // tile of rows, tile of the ring, first of its segment, last use of the values
+            int seg;
+            bool some;
+        } due{0, 0, 0, 0, 0, false};
+        auto values = [&] {
+            if (!due.some || !ok) return;
+            const int t = due.t, slot = due.vtile % NS;
+            bool w = mbar_wait(&full[slot], (due.vtile / NS) & 1) && mbar_wait(&pfull[t], pv[t] & 1);
+            if (due.first && due.seg > 0) w = w && mbar_wait(&ofree[t], (due.seg - 1) & 1);
+            ok = __all_sync(0xFFFFFFFFu, w);
+            if (!ok) return;
+            tc_fence_after();
+            if (leader) {
+#pragma unroll
+                for (int k = 0; k < kTile / 16; k++)
+                    mma_ts(tmem + L::o + t * D, tmem + L::p + t * 64 + 8 * k, values_desc(r0 + slot * L::tile + k * 2048, L::half), id_o, !(due.first && k == 0));
+                mma_commit(&pvdone[t]);
+                if (due.last) mma_commit(&empty[slot]);
+            }
+            __syncwarp();
+            pv[t]++;
+            due.some = false;
+        };
+        while (left > 0 && ok) {
+            const int nt = c.tiles(left), both = c.rows(a) > 128;
+            for (int j = 0; j < nt && ok; j++, n++) {
+                for (int t = 0; t <= both && ok; t++) {
+                    const int slot = (2 * n) % NS;
+                    bool w = mbar_wait(&full[slot], ((2 * n) / NS) & 1);
+                    if (j == 0) w = w && mbar_wait(&qfull[t], segs[t] & 1);
+                    if (qk > 0) w = w && mbar_wait(sfree, (qk - 1) & 1);
+                    ok = __all_sync(0xFFFFFFFFu, w);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (leader) {
+#pragma unroll
+                        for (int k = 0; k < D / 16; k++) {
+                            const uint32_t at = (k >> 2) * L::half + (k & 3) * 32;
+                            mma_ss(tmem + L::s, smem_desc_sw128(q0 + t * L::tile + at), smem_desc_sw128(r0 + slot * L::tile + at), id_s, k > 0);
+                        }
+                        mma_commit(&sfull[t]);
+                        if (t == both) mma_commit(&empty[slot]);
+                    }
+                    __syncwarp();
+                    qk++;
+                    values();
+                    due = Due{t, 2 * n + 1, j == 0, t == both, segs[t], true};
+                    if (j == nt - 1) segs[t]++;
+                }
+            }
+            left -= nt;
+            if (left > 0) c.next(a);
+        }
+        values();
+        if (!ok && lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
+        // every product issued is complete before the tensor memory is freed
+        if (leader) mma_commit(done);
+        __syncwarp();
+        if (!mbar_wait(done, 0) && lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
+    }
+    } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    if (any) {
+        // ------------------------------------------------------------------------------ softmax
+        const int t = warp >> 2, row = threadIdx.x & 127;
+        const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        Cursor c(a, *found);
+        int64_t left = ub - ua;
+        int steps = 0;                  // scores seen, also products of P and V asked for
+        auto arrive = [&](uint64_t *b) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b);
+        };
+        auto wait = [&](uint64_t *b, uint32_t parity) {
+            if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(b, parity));
+        };
+        // an item's queries of this tile, 16 threads a row
+        auto queries = [&](const Cursor &q) {
+            const int64_t x0 = (int64_t)q.rt * kRows + 128 * t, xn = (int64_t)q.w.q.n * a.group;
+            constexpr int kC = D / 8;     // 16-byte pieces of a row
+#pragma unroll 4
+            for (int i = row; i < 128 * kC; i += 128) {
+                const int r = i / kC, ch = i % kC;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (x0 + r < xn) {
+                    const int x = (int)(x0 + r), tok = x / a.group;
+                    v = *(const uint4 *)(a.q + (q.w.q.first + tok) * a.ldq + (int64_t)(q.head * a.group + x - tok * a.group) * D + 8 * ch);
+                    v.x = (v.x & g.q_and) ^ g.q_xor;
+                    v.y = (v.y & g.q_and) ^ g.q_xor;
+                    v.z = (v.z & g.q_and) ^ g.q_xor;
+                    v.w = (v.w & g.q_and) ^ g.q_xor;
+                }
+                *(uint4 *)(qs + t * L::tile + (ch >> 3) * L::half + r * 128 + ((ch & 7) ^ (r & 7)) * 16) = v;
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            arrive(&qfull[t]);
+        };
+        if (c.rows(a) > 128 * t) queries(c);
+        Cut cut{0, U, 0, 0, 0, 0};
+        while (left > 0) {
+            const int nt = c.tiles(left);
+            const bool begins = c.off == 0, ends = c.off + nt == c.k.nt;
+            Cursor nx = c;
+            if (left > nt) nx.next(a);
+            if (c.rows(a) <= 128 * t) {   // the item has no such tile
+                left -= nt;
+                c = nx;
+                if (left > 0 && c.rows(a) > 128 * t) queries(c);
+                continue;
+            }
+            // this thread's row, and the keys [from, upto) that it sees
+            const int64_t x = (int64_t)c.rt * kRows + 128 * t + row;
+            const bool in = x < (int64_t)c.w.q.n * a.group;
+            const int tok = in ? (int)x / a.group : 0;
+            const int64_t pos = (int64_t)c.w.q.len - c.w.q.n + tok;
+            const int upto = !in ? 0 : a.causal ? (int)min(max(pos + 1, (int64_t)0), (int64_t)c.w.keys) : c.w.keys;
+            const int from = a.window ? (int)max(pos - a.window + 1, (int64_t)0) : 0;
+            float m = kNegInf;            // what the powers are relative to, in powers of 2
+            Pair l2 = pair(0.f, 0.f);
+            for (int j = 0; j < nt; j++) {
+                const int key0 = (c.k.t0 + c.off + j) * kTile;
+                wait(&sfull[t], steps & 1);
+                tc_fence_after();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int q = 0; q < 4; q++) tmem_ld32(t_lane + L::s + 32 * q, s[q]);
+                tmem_wait_ld();
+                tc_fence_before();
+                arrive(sfree);
+                if (__any_sync(0xFFFFFFFFu, key0 < from || key0 + kTile > upto)) {
+                    const int lo = from - key0, hi = upto - key0;
+#pragma unroll
+                    for (int i = 0; i < 128; i++)
+                        if (i < lo || i >= hi) s[i >> 5][i & 31] = __float_as_uint(kNegInf);
+                }
+                float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+                for (int i = 0; i < 128; i += 8)
+#pragma unroll
+                    for (int q = 0; q < 4; q++)
+                        mx[q] = fmaxf(mx[q], fmaxf(__uint_as_float(s[i >> 5][(i & 31) + 2 * q]), __uint_as_float(s[i >> 5][(i & 31) + 2 * q + 1])));
+                const float ms = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale2;
+                bool waited = steps == 0;
+                if (j == 0) m = ms;
+                else if (__any_sync(0xFFFFFFFFu, ms > m + kGrow)) {
+                    // the output so far, in other powers
+                    const float mn = fmaxf(m, ms), f = mn == kNegInf ? 1.f : exp2_fast(m - mn);
+                    m = mn;
+                    l2 = mul2(l2, pair(f, f));
+                    wait(&pvdone[t], (steps - 1) & 1);
+                    waited = true;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int q = 0; q < D / 32; q++) {
+                        uint32_t o[32];
+                        tmem_ld32(t_lane + L::o + t * D + 32 * q, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        tmem_st32(t_lane + L::o + t * D + 32 * q, o);
+                    }
+                    tmem_wait_st();
+                }
+                const float base = m == kNegInf ? 0.f : m;
+                const Pair sc = pair(a.scale2, a.scale2), nb = pair(-base, -base);
+                Pair acc[2] = {l2, pair(0.f, 0.f)};
+                uint32_t p[2][32];
+#pragma unroll
+                for (int i = 0; i < 128; i += 2) {
+                    float e0, e1;
+                    unpair(fma2(pair(__uint_as_float(s[i >> 5][i & 31]), __uint_as_float(s[i >> 5][(i & 31) + 1])), sc, nb), e0, e1);
+                    e0 = exp2_fast(e0);
+                    e1 = exp2_fast(e1);
+                    acc[(i >> 1) & 1] = add2(acc[(i >> 1) & 1], pair(e0, e1));
+                    p[i >> 6][(i & 63) >> 1] = pack2(e0, e1);
+                }
+                l2 = add2(acc[0], acc[1]);
+                if (!waited) {
+                    wait(&pvdone[t], (steps - 1) & 1);   // the product before has read P
+                    tc_fence_after();
+                }
+#pragma unroll
+                for (int q = 0; q < 2; q++) tmem_st32(t_lane + L::p + t * 64 + 32 * q, p[q]);
+                tmem_wait_st();
+                tc_fence_before();
+                arrive(&pfull[t]);
+                steps++;
+            }
+            // the last scores are in: the products are done with the queries
+            const int64_t end = ub - left + (c.k.nt - c.off);
+            left -= nt;
+            if (left > 0 && nx.rows(a) > 128 * t) queries(nx);
+            wait(&pvdone[t], (steps - 1) & 1);
+            tc_fence_after();
+            float la, lb;
+            unpair(l2, la, lb);
+            const float l = la + lb;
+            if (begins && ends) {
+                const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+                const int h = c.head * a.group + (in ? (int)x - tok * a.group : 0);
+                const int64_t r = c.w.q.first + tok;
+                uint16_t *o = a.out + r * a.ldo + (int64_t)h * D;
+#pragma unroll 1
+                for (int q = 0; q < D / 32; q++) {
+                    uint32_t v[32];
+                    tmem_ld32(t_lane + L::o + t * D + 32 * q, v);
+                    tmem_wait_ld();
+                    if (in) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8) {
+                            uint4 w;
+                            w.x = pack2(__uint_as_float(v[i]) * inv, __uint_as_float(v[i + 1]) * inv);
+                            w.y = pack2(__uint_as_float(v[i + 2]) * inv, __uint_as_float(v[i + 3]) * inv);
+                            w.z = pack2(__uint_as_float(v[i + 4]) * inv, __uint_as_float(v[i + 5]) * inv);
+                            w.w = pack2(__uint_as_float(v[i + 6]) * inv, __uint_as_float(v[i + 7]) * inv);
+                            *(uint4 *)(o + 32 * q + i) = w;
+                        }
+                    }
+                }
+                if (in && a.lse) a.lse[r * a.q_heads + h] = l == 0.f ? kNegInf : (m + log2f(l)) * 0.69314718f;
+            } else {
+                // pieces of four columns of all rows: a warp's stores are 512 bytes in a row
+                float *o = a.part + (2 * (size_t)blockIdx.x + (begins ? 1 : 0)) * slot_floats<kRows, D>();
+                const int r = 128 * t + row;
+#pragma unroll 1
+                for (int q = 0; q < D / 32; q++) {
+                    uint32_t v[32];
+                    tmem_ld32(t_lane + L::o + t * D + 32 * q, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) *(uint4 *)(o + ((32 * q + i) / 4 * kRows + r) * 4) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                }
+                o[kRows * D + r] = m;
+                o[kRows * D + kRows + r] = l;
+                if (begins) {
+                    cut.valid = 1;
+                    cut.seq = c.s;
+                    cut.item = c.head;
+                    cut.pad = c.rt;
+                    cut.end = end;
+                }
+            }
+            tc_fence_before();
+            arrive(&ofree[t]);
+            c = nx;
+        }
+        if (threadIdx.x == 0) a.cuts[blockIdx.x] = cut;
+        if (!ok && lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
+    }
+    }
+    if (!any && threadIdx.x == 0) a.cuts[blockIdx.x] = Cut{0, U, 0, 0, 0, 0};
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    }
+}
+
+// joins the sums of the item that begins in CTA blockIdx.x's range and goes on behind it, 16 columns a block
+template <int D>
+__global__ void __launch_bounds__(kRows) join_tc_kernel(const AttendCall a)
+{
+    pdl_trigger();
+    pdl_wait();
+    const Cut cut = a.cuts[blockIdx.x];
+    if (!cut.valid) return;
+    const int64_t G = gridDim.x;
+    const Seq w = seq_at(a, cut.seq);
+    constexpr size_t kSlot = slot_floats<kRows, D>();
+    const int r = threadIdx.x, col = blockIdx.y * 16;
+    const int64_t x = (int64_t)cut.pad * kRows + r;
+    if (x >= (int64_t)w.q.n * a.group) return;
+    auto each = [&](auto f) {
+        f(a.part + (2 * (size_t)blockIdx.x + 1) * kSlot);
+        for (int64_t c = blockIdx.x + 1; c < G; c++) {
+            const int64_t ua = cut.units * c / G, ub = cut.units * (c + 1) / G;
+            if (ua >= cut.end) break;
+            if (ua < ub) f(a.part + 2 * (size_t)c * kSlot);
+        }
+    };
+    float m = kNegInf, l = 0.f, o[16];
+#pragma unroll
+    for (int i = 0; i < 16; i++) o[i] = 0.f;
+    each([&](const float *p) { m = fmaxf(m, p[kRows * D + r]); });
+    const float b = m == kNegInf ? 0.f : m;
+    each([&](const float *p) {
+        const float f = exp2_fast(p[kRows * D + r] - b);
+        l += p[kRows * D + kRows + r] * f;
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+            const float4 v = *(const float4 *)(p + ((col + i) / 4 * kRows + r) * 4);
+            o[i] += v.x * f;
+            o[i + 1] += v.y * f;
+            o[i + 2] += v.z * f;
+            o[i + 3] += v.w * f;
+        }
+    });
+    const int tok = (int)x / a.group, h = cut.item * a.group + (int)x - tok * a.group;
+    const int64_t row = w.q.first + tok;
+    const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+    uint16_t *p = a.out + row * a.ldo + (int64_t)h * D + col;
+#pragma unroll
+    for (int i = 0; i < 16; i += 8)
+        *(uint4 *)(p + i) = make_uint4(pack2(o[i] * inv, o[i + 1] * inv), pack2(o[i + 2] * inv, o[i + 3] * inv), pack2(o[i + 4] * inv, o[i + 5] * inv),
+                                       pack2(o[i + 6] * inv, o[i + 7] * inv));
+    if (a.lse && blockIdx.y == 0) a.lse[row * a.q_heads + h] = l == 0.f ? kNegInf : (m + log2f(l)) * 0.69314718f;
+}
+
+template <int D>
+cudaError_t launch_tc(const uw_kv_cache *c, const AttendCall &call, int ctas, cudaStream_t st)
+{
+    static OncePerDevice once;
+    cudaError_t e = allow_shared(once, attend_tc_kernel<D>, Layout<D>::smem);
+    if (e != cudaSuccess) return e;
+    Args g;
+    g.km = c->k128;
+    g.vm = c->v128;
+    g.c = call;
+    g.c.box = c->box128;
+    g.q_xor = call.scale2 < 0.f ? 0x80008000u : 0u;
+    g.q_and = call.scale2 == 0.f ? 0u : 0xFFFFFFFFu;
+    g.c.scale2 = call.scale2 == 0.f ? 1.f : std::fabs(call.scale2);
+    if ((e = launch_dependent(attend_tc_kernel<D>, dim3((unsigned)ctas), kThreads, Layout<D>::smem, 0, st, g)) != cudaSuccess) return e;
+    return launch_dependent(join_tc_kernel<D>, dim3((unsigned)ctas, D / 16), kRows, 0, 0, st, g.c);
+}
+
+}  // namespace
+
+size_t attend_tc_slot_floats(int D) { return D == 128 ? slot_floats<kRows, 128>() : slot_floats<kRows, 64>(); }
+
+int launch_attend_tc(const uw_kv_cache *c, const AttendCall &a, int ctas, void *stream)
+{
+    return c->d.head_dim == 128 ? launch_tc<128>(c, a, ctas, (cudaStream_t)stream) : launch_tc<64>(c, a, ctas, (cudaStream_t)stream);
+}
+
+}  // namespace uw
