@@ -11,6 +11,7 @@
 
 #include <cstdint>
 
+#include "dev_async.cuh"
 #include "kv.cuh"
 
 namespace uw {
@@ -63,6 +64,39 @@ __device__ __forceinline__ SeqWork<R, K> seq_work(const AttendCall &a, int s)
 // Partial sums of an item in the workspace: R rows of D, then R maxima (of 2^), then R sums.
 template <int R, int D>
 __host__ __device__ constexpr size_t slot_floats() { return (size_t)R * (D + 2); }
+
+namespace dev {
+
+// The phase is complete, without waiting for it.
+__device__ __forceinline__ bool mbar_poll(uint64_t *b, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok) : "r"(saddr(b)), "r"(parity) : "memory");
+    return ok != 0;
+}
+
+// Until the phase is complete; false after 2^32 cycles (2 s).  The thread may be suspended for up to a millisecond at a time:
+// polls take turns of shared memory that the tensor cores' operands need.
+__device__ __forceinline__ bool mbar_sleep(uint64_t *b, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(ok)
+                 : "r"(saddr(b)), "r"(parity), "r"(1000000u)
+                 : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ bool mbar_wait_short(uint64_t *b, uint32_t parity)
+{
+    if (mbar_sleep(b, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_sleep(b, parity))
+        if (clock64() - t0 > (1ll << 32)) return false;
+    return true;
+}
+
+}  // namespace dev
 
 // k_attend_tc.cu: items of 256 rows on tcgen05
 size_t attend_tc_slot_floats(int D);

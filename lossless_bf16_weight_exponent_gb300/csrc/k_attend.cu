@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend16_kernel(const __grid_cons
             if (use.active(warp)) {
                 ask();
                 const uint32_t st = used % kStages;
-                if (ok && !mbar_wait(&bars[st], (used / kStages) & 1)) ok = false;
+                if (ok && !mbar_wait_short(&bars[st], (used / kStages) & 1)) ok = false;
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 used++;
                 const uint32_t ks = my_ring + st * L::stage, vs = ks + L::mat;
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend16_kernel(const __grid_cons
     if (!ok) {
         // what was asked for lands before the block ends
         if (lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
-        for (uint32_t i = asked > kStages ? asked - kStages : 0; i < asked; i++) mbar_wait(&bars[i % kStages], (i / kStages) & 1);
+        for (uint32_t i = asked > kStages ? asked - kStages : 0; i < asked; i++) mbar_wait_short(&bars[i % kStages], (i / kStages) & 1);
     }
 }
 

@@ -9,9 +9,9 @@
 //     by tensor memory loads and stores of the row): probabilities are at most 256 and keep their relative precision;
 //   - 8: tensor copies of the pages' slots of one head, keys and values in turn, into a ring of 128-key tiles.  Values that
 //     no row of the item sees are set to zero in shared memory when they have landed, as 0 x NaN is NaN;
-//   - 9: the products, by one thread.  The k-th product of P and V is issued behind the (k+1)-th of Q and K, so a tile's softmax
-//     runs under the other tile's products (or, in items of up to 128 rows, under the copy of the next keys);
-//   - 10, 11: none, they make up the third warpgroup, which gives registers to the other two.
+//   - 9: the products of Q and K, A's and B's in turn; 10: those of P and V, by one thread each.  Two warps, as a warp's poll
+//     of a barrier waits in line behind the products that it has issued: with one, the tensor cores ran dry at each wait;
+//   - 11: none, it makes up the third warpgroup, which gives registers to the other two.
 // Tensor memory: O of A and B, one S, P of A and of B: 2 D + 128 + 2 x 64 columns.  One S is enough as a warpgroup takes its
 // scores into registers at once, under the product in between, and P does not lie in S: every reuse waits on a barrier of
 // what used it last.
@@ -35,13 +35,16 @@ namespace {
 using namespace dev;
 
 constexpr int kWarps = 12, kThreads = 32 * kWarps;
-constexpr int kCopyWarp = 8, kMmaWarp = 9;
+constexpr int kCopyWarp = 8, kScoreWarp = 9, kValueWarp = 10;
 constexpr int kRows = 256, kTile = 128;
 constexpr float kNegInf = -INFINITY;
 constexpr float kGrow = 8.f;      // log2 of how far a maximum may grow before the output is rescaled
 
+constexpr int kItem = 3;          // what an item costs beside its tiles of keys, in tiles: queries, output, a pipeline that runs dry
+
 struct Start {
-    int s, head, rt, off;
+    int64_t at;                   // of the item in the line of work
+    int s, head, i;               // i: place of the tile of rows
 };
 
 template <int D>
@@ -49,7 +52,7 @@ struct Layout {
     static constexpr uint32_t half = kTile * 128;               // 64 elements of 128 rows or keys
     static constexpr uint32_t tile = half * (D / 64);           // a tile of queries, keys or values
     static constexpr int slots = D == 128 ? 5 : 10;
-    static constexpr uint32_t bars = 8 * (2 * slots + 16);
+    static constexpr uint32_t bars = 8 * (2 * slots + 18);
     static constexpr size_t smem = 1024 + 2 * tile + slots * tile + bars + 8 * kWarps + sizeof(Start) + 16;
     static_assert(smem <= 227 * 1024, "shared memory");
     // columns of tensor memory
@@ -110,6 +113,21 @@ __device__ __forceinline__ uint64_t values_desc(uint32_t addr, uint32_t half)
     return d;
 }
 
+// both barriers' phases; false after the limit of a wait
+__device__ __forceinline__ bool wait_both(uint64_t *a, uint32_t pa, uint64_t *b, uint32_t pb)
+{
+    const bool x = mbar_poll(a, pa), y = mbar_poll(b, pb);
+    if (x && y) return true;
+    return mbar_wait_short(a, pa) && mbar_wait_short(b, pb);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 __device__ __forceinline__ uint32_t pack2(float a, float b)
 {
     const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
@@ -138,15 +156,21 @@ struct Span {
 
 __device__ __forceinline__ Span span_of(const AttendCall &a, int n, int len, int keys, int rt)
 {
-    const int i0 = (int)((int64_t)rt * kRows / a.group), i1 = (int)(min((int64_t)n * a.group, (int64_t)(rt + 1) * kRows) - 1) / a.group;
-    const int64_t p0 = (int64_t)len - n;
+    // n x group and the tile's end are below 2^31 (the call's rows are limited)
+    const uint32_t x0 = (uint32_t)rt * kRows, x1 = min((uint32_t)n * (uint32_t)a.group, x0 + kRows);
+    const int i0 = (int)(x0 / (uint32_t)a.group), i1 = (int)((x1 - 1) / (uint32_t)a.group);
+    const int p0 = len - n;
     Span r;
-    r.hi = a.causal ? (int)min(max(p0 + i1 + 1, (int64_t)0), (int64_t)keys) : keys;
-    r.lo = a.window ? (int)min(max(p0 + i0 - a.window + 1, (int64_t)0), (int64_t)r.hi) : 0;
+    r.hi = a.causal ? min(max(p0 + i1 + 1, 0), keys) : keys;
+    r.lo = a.window ? (int)min(max((int64_t)p0 + i0 - a.window + 1, (int64_t)0), (int64_t)r.hi) : 0;
     r.t0 = r.lo / kTile;
     r.nt = max(1, (r.hi + kTile - 1) / kTile - r.t0);
     return r;
 }
+
+// The i-th tile of rows of `tiles` in the line: from both ends in turn, as a causal sequence's first tiles see few keys and its
+// last many, and a CTA's share should not be all short items.
+__device__ __forceinline__ int tile_of(int i, int tiles) { return (i & 1) ? tiles - 1 - (i >> 1) : i >> 1; }
 
 // units of sequence s for one key head, by the whole warp, a sequence a lane (s < 0: none)
 __device__ __forceinline__ int64_t units_of(const AttendCall &a, int s)
@@ -157,7 +181,7 @@ __device__ __forceinline__ int64_t units_of(const AttendCall &a, int s)
     int64_t u = 0;
     const bool many = w.row_tiles > 2;
     if (!many)
-        for (int rt = 0; rt < w.row_tiles; rt++) u += span_of(a, w.q.n, w.q.len, w.keys, rt).nt;
+        for (int rt = 0; rt < w.row_tiles; rt++) u += span_of(a, w.q.n, w.q.len, w.keys, rt).nt + kItem;
     unsigned left = __ballot_sync(0xFFFFFFFFu, many);
     while (left) {
         const int src = __ffs(left) - 1;
@@ -165,7 +189,7 @@ __device__ __forceinline__ int64_t units_of(const AttendCall &a, int s)
         const int n = __shfl_sync(0xFFFFFFFFu, w.q.n, src), len = __shfl_sync(0xFFFFFFFFu, w.q.len, src);
         const int keys = __shfl_sync(0xFFFFFFFFu, w.keys, src), tiles = __shfl_sync(0xFFFFFFFFu, w.row_tiles, src);
         int64_t x = 0;
-        for (int rt = lane; rt < tiles; rt += 32) x += span_of(a, n, len, keys, rt).nt;
+        for (int rt = lane; rt < tiles; rt += 32) x += span_of(a, n, len, keys, rt).nt + kItem;
 #pragma unroll
         for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
         if (lane == src) u = x;
@@ -173,33 +197,44 @@ __device__ __forceinline__ int64_t units_of(const AttendCall &a, int s)
     return u;
 }
 
-// an item, and how many of its tiles of keys lie in front of this CTA's
+// An item of the line of work, where each has its tiles of keys and kItem in front of them, and which of its tiles lie in the
+// CTA's range [ua, ub): those [off, off + cnt).  Made, and moved on, to an item that has some; more(): there was one.
 struct Cursor {
     Seq w;
     Span k;
-    int s, head, rt, off;
-    __device__ __forceinline__ void enter(const AttendCall &a) { k = span_of(a, w.q.n, w.q.len, w.keys, rt); }
-    __device__ __forceinline__ Cursor(const AttendCall &a, const Start &f) : s(f.s), head(f.head), rt(f.rt), off(f.off)
+    int64_t at, ua, ub;
+    int s, head, i, rt, off, cnt;      // i: place of the tile of rows rt
+    __device__ __forceinline__ void enter(const AttendCall &a)
+    {
+        rt = tile_of(i, w.row_tiles);
+        k = span_of(a, w.q.n, w.q.len, w.keys, rt);
+        off = (int)max(ua - at - kItem, (int64_t)0);
+        cnt = (int)(min(ub - at - kItem, (int64_t)k.nt)) - off;
+    }
+    __device__ __forceinline__ Cursor(const AttendCall &a, const Start &f, int64_t ua_, int64_t ub_) : at(f.at), ua(ua_), ub(ub_), s(f.s), head(f.head), i(f.i)
     {
         w = seq_at(a, s);
         enter(a);
+        if (cnt <= 0) next(a);
     }
-    // the next item; only called while one is left
+    __device__ __forceinline__ bool more() const { return at < ub; }
     __device__ __forceinline__ void next(const AttendCall &a)
     {
-        off = 0;
-        if (++rt >= w.row_tiles) {
-            rt = 0;
-            if (++head >= a.kv_heads) {
-                head = 0;
-                do w = seq_at(a, ++s);
-                while (!w.row_tiles);
+        do {
+            at += k.nt + kItem;
+            if (at >= ub) return;
+            if (++i >= w.row_tiles) {
+                i = 0;
+                if (++head >= a.kv_heads) {
+                    head = 0;
+                    do w = seq_at(a, ++s);
+                    while (!w.row_tiles);
+                }
             }
-        }
-        enter(a);
+            enter(a);
+        } while (cnt <= 0);
     }
-    __device__ __forceinline__ int tiles(int64_t left) const { return (int)min((int64_t)(k.nt - off), left); }
-    __device__ __forceinline__ int rows(const AttendCall &a) const { return (int)min((int64_t)w.q.n * a.group - (int64_t)rt * kRows, (int64_t)kRows); }
+    __device__ __forceinline__ int rows(const AttendCall &a) const { return min(w.q.n * a.group - rt * kRows, kRows); }
 };
 
 template <int D>
@@ -214,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
     uint64_t *full = (uint64_t *)(ring + NS * L::tile);
     uint64_t *empty = full + NS;
     uint64_t *raw = empty + NS;                       // a tile whose values are put right before it counts as full
-    uint64_t *qfull = raw + 1, *sfull = qfull + 2, *sfree = sfull + 2, *pfull = sfree + 1, *pvdone = pfull + 2, *ofree = pvdone + 2, *done = ofree + 2;
+    uint64_t *qfull = raw + 1, *sfull = qfull + 2, *sfree = sfull + 2, *pfull = sfree + 1, *pvdone = pfull + 4, *ofree = pvdone + 2, *done = ofree + 2;
     int64_t *sums = (int64_t *)((uint8_t *)full + L::bars);
     Start *found = (Start *)(sums + kWarps);
     uint32_t *tmem_slot = (uint32_t *)(found + 1);
@@ -227,17 +262,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         }
         mbar_init(raw, 1);
         mbar_init(sfree, 4);
-        mbar_init(done, 1);
+        mbar_init(&done[0], 1);
+        mbar_init(&done[1], 1);
         for (int t = 0; t < 2; t++) {
             mbar_init(&qfull[t], 4);
             mbar_init(&sfull[t], 1);
-            mbar_init(&pfull[t], 4);
+            mbar_init(&pfull[2 * t], 4);
+            mbar_init(&pfull[2 * t + 1], 4);
             mbar_init(&pvdone[t], 1);
             mbar_init(&ofree[t], 4);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == kMmaWarp) {
+    if (warp == kScoreWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_slot)), "r"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -287,14 +324,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                 int64_t at = in - (int64_t)head * per;  // units of the head in front of ours
                 const Seq w = seq_at(a, sq);
                 for (int r0 = 0; r0 < w.row_tiles; r0 += 32) {
-                    const int nt = r0 + lane < w.row_tiles ? span_of(a, w.q.n, w.q.len, w.keys, r0 + lane).nt : 0;
+                    const int nt = r0 + lane < w.row_tiles ? span_of(a, w.q.n, w.q.len, w.keys, tile_of(r0 + lane, w.row_tiles)).nt + kItem : 0;
                     int64_t x = nt;
 #pragma unroll
                     for (int d = 1; d < 32; d <<= 1) {
                         const int64_t o = __shfl_up_sync(0xFFFFFFFFu, x, d);
                         if (lane >= d) x += o;
                     }
-                    if (at < x && at >= x - nt) *found = Start{sq, head, r0 + lane, (int)(at - (x - nt))};
+                    if (at < x && at >= x - nt) *found = Start{ua - (at - (x - nt)), sq, head, r0 + lane};
                     const int64_t all = __shfl_sync(0xFFFFFFFFu, x, 31);
                     if (at < all) break;
                     at -= all;
@@ -308,13 +345,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
     const uint32_t tmem = *tmem_slot;
     bool ok = true;
 
-    // 12 warps have 168 registers a thread at launch; a row of scores wants more: 256 x 200 + 128 x 104 is what 384 x 168 is
+    // 12 warps have 168 registers a thread at launch; a row of scores wants more: 256 x 208 + 128 x 88 is what 384 x 168 is
     if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (any && warp == kCopyWarp) {
         // ------------------------------------------------------------------------------ copies
-        Cursor c(a, *found);
-        int64_t left = ub - ua;
+        Cursor c(a, *found, ua, ub);
         int n = 0;                        // tiles asked for: keys, values, keys, ...
         // values that are to be put right when they have landed
         bool fix = false;
@@ -323,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         auto mend = [&] {
             if (!fix) return;
             fix = false;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(raw, raw_phase & 1))) ok = false;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait_short(raw, raw_phase & 1))) ok = false;
             raw_phase++;
             uint8_t *v = ring + fix_slot * L::tile;
             for (int i = lane; i < kTile * (D / 8); i += 32) {
@@ -340,17 +376,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         const int boxes = kTile / a.box, half = lane % (D / 64), bx0 = lane / (D / 64);
         constexpr int kPer = 32 / (D / 64);          // boxes of one round of lanes
         const uint32_t box_bytes = (uint32_t)a.box * 128u;
-        while (left > 0 && ok) {
-            const int nt = c.tiles(left);
+        for (; c.more() && ok; c.next(a)) {
             const int32_t *table = a.b.pages + (int64_t)c.s * a.b.ld_pages;
-            for (int j = 0; j < nt && ok; j++) {
+            for (int j = 0; j < c.cnt && ok; j++) {
                 const int key0 = (c.k.t0 + c.off + j) * kTile;
                 const bool odd = key0 < c.k.lo || key0 + kTile > c.k.hi;
                 for (int kv = 0; kv < 2 && ok; kv++) {
                     const int slot = n % NS;
-                    if (n >= NS && !__all_sync(0xFFFFFFFFu, mbar_test(&empty[slot], ((n / NS) & 1) ^ 1))) {
+                    if (n >= NS && !__all_sync(0xFFFFFFFFu, mbar_poll(&empty[slot], ((n / NS) & 1) ^ 1))) {
                         mend();
-                        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&empty[slot], ((n / NS) & 1) ^ 1))) { ok = false; break; }
+                        if (!__all_sync(0xFFFFFFFFu, mbar_wait_short(&empty[slot], ((n / NS) & 1) ^ 1))) { ok = false; break; }
                     }
                     const bool mended = kv && odd;
                     if (mended) mend();              // the one before
@@ -376,135 +411,157 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                     n++;
                 }
             }
-            left -= nt;
-            if (left > 0) c.next(a);
         }
         mend();
         if (!ok) {
             if (lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
             // what is on its way lands before the block ends (a tile that waits to be put right: above)
-            for (int i = n > NS ? n - NS : 0; i < n; i++) mbar_wait(&full[i % NS], (i / NS) & 1);
+            for (int i = n > NS ? n - NS : 0; i < n; i++) mbar_wait_short(&full[i % NS], (i / NS) & 1);
         }
-    } else if (any && warp == kMmaWarp) {
-        // ------------------------------------------------------------------------------ products
-        Cursor c(a, *found);
-        int64_t left = ub - ua;
+    } else if (any && warp == kScoreWarp) {
+        // ------------------------------------------------------------------------------ products of queries and keys
+        Cursor c(a, *found, ua, ub);
         const bool leader = elect_one();
-        constexpr uint32_t id_s = idesc_bf16(128, 128), id_o = idesc_bf16(128, D) | 1u << 16;  // the second operand's columns run along memory
+        constexpr uint32_t id = idesc_bf16(128, 128);
         const uint32_t q0 = saddr(qs), r0 = saddr(ring);
-        int n = 0;                          // tiles of keys before this one
-        int qk = 0;                         // products of Q and K so far
-        int segs[2] = {0, 0}, pv[2] = {0, 0};  // of each tile of rows: segments begun, products of P and V
-        // the product of P and V that is due
-        struct Due {
-            int t, vtile, first, last;      // tile of rows, tile of the ring, first of its segment, last use of the values
-            int seg;
-            bool some;
-        } due{0, 0, 0, 0, 0, false};
-        auto values = [&] {
-            if (!due.some || !ok) return;
-            const int t = due.t, slot = due.vtile % NS;
-            bool w = mbar_wait(&full[slot], (due.vtile / NS) & 1) && mbar_wait(&pfull[t], pv[t] & 1);
-            if (due.first && due.seg > 0) w = w && mbar_wait(&ofree[t], (due.seg - 1) & 1);
-            ok = __all_sync(0xFFFFFFFFu, w);
-            if (!ok) return;
-            tc_fence_after();
-            if (leader) {
-#pragma unroll
-                for (int k = 0; k < kTile / 16; k++)
-                    mma_ts(tmem + L::o + t * D, tmem + L::p + t * 64 + 8 * k, values_desc(r0 + slot * L::tile + k * 2048, L::half), id_o, !(due.first && k == 0));
-                mma_commit(&pvdone[t]);
-                if (due.last) mma_commit(&empty[slot]);
-            }
-            __syncwarp();
-            pv[t]++;
-            due.some = false;
-        };
-        while (left > 0 && ok) {
-            const int nt = c.tiles(left), both = c.rows(a) > 128;
+        int n = 0, qk = 0;                  // tiles of keys, products before this one
+        int segs[2] = {0, 0};               // of each tile of rows: items begun
+        for (; c.more() && ok; c.next(a)) {
+            const int nt = c.cnt, both = c.rows(a) > 128;
             for (int j = 0; j < nt && ok; j++, n++) {
+                const int slot = (2 * n) % NS;
                 for (int t = 0; t <= both && ok; t++) {
-                    const int slot = (2 * n) % NS;
-                    bool w = mbar_wait(&full[slot], ((2 * n) / NS) & 1);
-                    if (j == 0) w = w && mbar_wait(&qfull[t], segs[t] & 1);
-                    if (qk > 0) w = w && mbar_wait(sfree, (qk - 1) & 1);
+                    bool w = qk > 0 ? wait_both(&full[slot], ((2 * n) / NS) & 1, sfree, (qk - 1) & 1) : mbar_wait_short(&full[slot], ((2 * n) / NS) & 1);
+                    if (j == 0) w = w && mbar_wait_short(&qfull[t], segs[t]++ & 1);
                     ok = __all_sync(0xFFFFFFFFu, w);
                     if (!ok) break;
                     tc_fence_after();
+                    const uint64_t qd = smem_desc_sw128(q0 + t * L::tile), kd = smem_desc_sw128(r0 + slot * L::tile);
                     if (leader) {
 #pragma unroll
                         for (int k = 0; k < D / 16; k++) {
-                            const uint32_t at = (k >> 2) * L::half + (k & 3) * 32;
-                            mma_ss(tmem + L::s, smem_desc_sw128(q0 + t * L::tile + at), smem_desc_sw128(r0 + slot * L::tile + at), id_s, k > 0);
+                            const uint32_t at = ((k >> 2) * L::half + (k & 3) * 32) >> 4;
+                            mma_ss(tmem + L::s, qd + at, kd + at, id, k > 0);
                         }
                         mma_commit(&sfull[t]);
                         if (t == both) mma_commit(&empty[slot]);
                     }
                     __syncwarp();
                     qk++;
-                    values();
-                    due = Due{t, 2 * n + 1, j == 0, t == both, segs[t], true};
-                    if (j == nt - 1) segs[t]++;
                 }
             }
-            left -= nt;
-            if (left > 0) c.next(a);
         }
-        values();
         if (!ok && lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
         // every product issued is complete before the tensor memory is freed
-        if (leader) mma_commit(done);
+        if (leader) mma_commit(&done[0]);
         __syncwarp();
-        if (!mbar_wait(done, 0) && lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
+        if (!mbar_wait_short(&done[0], 0) && lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
+    } else if (any && warp == kValueWarp) {
+        // ------------------------------------------------------------------------------ products of probabilities and values
+        Cursor c(a, *found, ua, ub);
+        const bool leader = elect_one();
+        constexpr uint32_t id = idesc_bf16(128, D) | 1u << 16;  // the second operand's columns run along memory
+        const uint32_t r0 = saddr(ring);
+        int n = 0;
+        int segs[2] = {0, 0}, pv[2] = {0, 0};
+        for (; c.more() && ok; c.next(a)) {
+            const int nt = c.cnt, both = c.rows(a) > 128;
+            for (int j = 0; j < nt && ok; j++, n++) {
+                const int v = 2 * n + 1, slot = v % NS;
+                for (int t = 0; t <= both && ok; t++) {
+                    bool w = wait_both(&full[slot], (v / NS) & 1, &pfull[2 * t], pv[t] & 1);
+                    if (j == 0) {
+                        if (segs[t] > 0) w = w && mbar_wait_short(&ofree[t], (segs[t] - 1) & 1);
+                        segs[t]++;
+                    }
+                    ok = __all_sync(0xFFFFFFFFu, w);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t vd = values_desc(r0 + slot * L::tile, L::half);
+                    const uint32_t od = tmem + L::o + t * D, pd = tmem + L::p + t * 64;
+                    if (leader) {
+#pragma unroll
+                        for (int k = 0; k < kTile / 32; k++) mma_ts(od, pd + 8 * k, vd + k * (2048 >> 4), id, j > 0 || k > 0);
+                    }
+                    __syncwarp();
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait_short(&pfull[2 * t + 1], pv[t] & 1));
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (leader) {
+#pragma unroll
+                        for (int k = kTile / 32; k < kTile / 16; k++) mma_ts(od, pd + 8 * k, vd + k * (2048 >> 4), id, 1);
+                        mma_commit(&pvdone[t]);
+                        if (t == both) mma_commit(&empty[slot]);
+                    }
+                    __syncwarp();
+                    pv[t]++;
+                }
+            }
+        }
+        if (!ok && lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
+        if (leader) mma_commit(&done[1]);
+        __syncwarp();
+        if (!mbar_wait_short(&done[1], 0) && lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
     }
     } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     if (any) {
         // ------------------------------------------------------------------------------ softmax
         const int t = warp >> 2, row = threadIdx.x & 127;
         const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        Cursor c(a, *found);
-        int64_t left = ub - ua;
+        Cursor c(a, *found, ua, ub);
         int steps = 0;                  // scores seen, also products of P and V asked for
         auto arrive = [&](uint64_t *b) {
             __syncwarp();
             if (lane == 0) mbar_arrive(b);
         };
         auto wait = [&](uint64_t *b, uint32_t parity) {
-            if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(b, parity));
+            if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait_short(b, parity));
         };
         // an item's queries of this tile, 16 threads a row
         auto queries = [&](const Cursor &q) {
-            const int64_t x0 = (int64_t)q.rt * kRows + 128 * t, xn = (int64_t)q.w.q.n * a.group;
-            constexpr int kC = D / 8;     // 16-byte pieces of a row
-#pragma unroll 4
-            for (int i = row; i < 128 * kC; i += 128) {
-                const int r = i / kC, ch = i % kC;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (x0 + r < xn) {
-                    const int x = (int)(x0 + r), tok = x / a.group;
-                    v = *(const uint4 *)(a.q + (q.w.q.first + tok) * a.ldq + (int64_t)(q.head * a.group + x - tok * a.group) * D + 8 * ch);
-                    v.x = (v.x & g.q_and) ^ g.q_xor;
-                    v.y = (v.y & g.q_and) ^ g.q_xor;
-                    v.z = (v.z & g.q_and) ^ g.q_xor;
-                    v.w = (v.w & g.q_and) ^ g.q_xor;
+            const int x0 = q.rt * kRows + 128 * t, xn = q.w.q.n * a.group;
+            constexpr int kC = D / 8, kStep = 128 / kC;     // 16-byte pieces of a row, rows of a round
+            const int ch = row % kC;
+            int r = row / kC, tok = (int)(((uint32_t)x0 + r) / (uint32_t)a.group), h = (int)((uint32_t)x0 + r - (uint32_t)tok * a.group);
+            const int dt = kStep / a.group, dh = kStep % a.group;
+            const uint16_t *src = a.q + q.w.q.first * a.ldq + (int64_t)(q.head * a.group) * D + 8 * ch;
+#pragma unroll 1
+            for (int b = 0; b < 128 / kStep; b += 8) {
+                uint4 v[8];
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    v[i] = make_uint4(0, 0, 0, 0);
+                    if (x0 + r + i * kStep < xn) v[i] = *(const uint4 *)(src + tok * a.ldq + h * D);
+                    tok += dt;
+                    h += dh;
+                    if (h >= a.group) {
+                        h -= a.group;
+                        tok++;
+                    }
                 }
-                *(uint4 *)(qs + t * L::tile + (ch >> 3) * L::half + r * 128 + ((ch & 7) ^ (r & 7)) * 16) = v;
+#pragma unroll
+                for (int i = 0; i < 8; i++, r += kStep) {
+                    v[i].x = (v[i].x & g.q_and) ^ g.q_xor;
+                    v[i].y = (v[i].y & g.q_and) ^ g.q_xor;
+                    v[i].z = (v[i].z & g.q_and) ^ g.q_xor;
+                    v[i].w = (v[i].w & g.q_and) ^ g.q_xor;
+                    *(uint4 *)(qs + t * L::tile + (ch >> 3) * L::half + r * 128 + ((ch & 7) ^ (r & 7)) * 16) = v[i];
+                }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             arrive(&qfull[t]);
         };
-        if (c.rows(a) > 128 * t) queries(c);
+        if (c.more() && c.rows(a) > 128 * t) queries(c);
         Cut cut{0, U, 0, 0, 0, 0};
-        while (left > 0) {
-            const int nt = c.tiles(left);
+        while (c.more()) {
+            const int nt = c.cnt;
             const bool begins = c.off == 0, ends = c.off + nt == c.k.nt;
             Cursor nx = c;
-            if (left > nt) nx.next(a);
+            nx.next(a);
             if (c.rows(a) <= 128 * t) {   // the item has no such tile
-                left -= nt;
                 c = nx;
-                if (left > 0 && c.rows(a) > 128 * t) queries(c);
+                if (c.more() && c.rows(a) > 128 * t) queries(c);
                 continue;
             }
             // this thread's row, and the keys [from, upto) that it sees
@@ -537,16 +594,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                 for (int i = 0; i < 128; i += 8)
 #pragma unroll
                     for (int q = 0; q < 4; q++)
-                        mx[q] = fmaxf(mx[q], fmaxf(__uint_as_float(s[i >> 5][(i & 31) + 2 * q]), __uint_as_float(s[i >> 5][(i & 31) + 2 * q + 1])));
+                        mx[q] = max3(mx[q], __uint_as_float(s[i >> 5][(i & 31) + 2 * q]), __uint_as_float(s[i >> 5][(i & 31) + 2 * q + 1]));
                 const float ms = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale2;
-                bool waited = steps == 0;
+                bool waited = steps == 0 || __all_sync(0xFFFFFFFFu, mbar_poll(&pvdone[t], (steps - 1) & 1));  // the product before
                 if (j == 0) m = ms;
                 else if (__any_sync(0xFFFFFFFFu, ms > m + kGrow)) {
                     // the output so far, in other powers
                     const float mn = fmaxf(m, ms), f = mn == kNegInf ? 1.f : exp2_fast(m - mn);
                     m = mn;
                     l2 = mul2(l2, pair(f, f));
-                    wait(&pvdone[t], (steps - 1) & 1);
+                    if (!waited) wait(&pvdone[t], (steps - 1) & 1);
                     waited = true;
                     tc_fence_after();
 #pragma unroll 1
@@ -563,32 +620,32 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                 const float base = m == kNegInf ? 0.f : m;
                 const Pair sc = pair(a.scale2, a.scale2), nb = pair(-base, -base);
                 Pair acc[2] = {l2, pair(0.f, 0.f)};
-                uint32_t p[2][32];
 #pragma unroll
-                for (int i = 0; i < 128; i += 2) {
-                    float e0, e1;
-                    unpair(fma2(pair(__uint_as_float(s[i >> 5][i & 31]), __uint_as_float(s[i >> 5][(i & 31) + 1])), sc, nb), e0, e1);
-                    e0 = exp2_fast(e0);
-                    e1 = exp2_fast(e1);
-                    acc[(i >> 1) & 1] = add2(acc[(i >> 1) & 1], pair(e0, e1));
-                    p[i >> 6][(i & 63) >> 1] = pack2(e0, e1);
+                for (int h = 0; h < 2; h++) {        // each half's product starts when it is there
+                    uint32_t p[32];
+#pragma unroll
+                    for (int i = 64 * h; i < 64 * h + 64; i += 2) {
+                        float e0, e1;
+                        unpair(fma2(pair(__uint_as_float(s[i >> 5][i & 31]), __uint_as_float(s[i >> 5][(i & 31) + 1])), sc, nb), e0, e1);
+                        e0 = exp2_fast(e0);
+                        e1 = exp2_fast(e1);
+                        acc[(i >> 1) & 1] = add2(acc[(i >> 1) & 1], pair(e0, e1));
+                        p[(i & 63) >> 1] = pack2(e0, e1);
+                    }
+                    if (h == 0) {
+                        if (!waited) wait(&pvdone[t], (steps - 1) & 1);   // the product before has read P
+                        tc_fence_after();
+                    }
+                    tmem_st32(t_lane + L::p + t * 64 + 32 * h, p);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    arrive(&pfull[2 * t + h]);
                 }
                 l2 = add2(acc[0], acc[1]);
-                if (!waited) {
-                    wait(&pvdone[t], (steps - 1) & 1);   // the product before has read P
-                    tc_fence_after();
-                }
-#pragma unroll
-                for (int q = 0; q < 2; q++) tmem_st32(t_lane + L::p + t * 64 + 32 * q, p[q]);
-                tmem_wait_st();
-                tc_fence_before();
-                arrive(&pfull[t]);
                 steps++;
             }
             // the last scores are in: the products are done with the queries
-            const int64_t end = ub - left + (c.k.nt - c.off);
-            left -= nt;
-            if (left > 0 && nx.rows(a) > 128 * t) queries(nx);
+            if (nx.more() && nx.rows(a) > 128 * t) queries(nx);
             wait(&pvdone[t], (steps - 1) & 1);
             tc_fence_after();
             float la, lb;
@@ -636,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                     cut.seq = c.s;
                     cut.item = c.head;
                     cut.pad = c.rt;
-                    cut.end = end;
+                    cut.end = c.at + kItem + c.k.nt;
                 }
             }
             tc_fence_before();
@@ -650,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
     if (!any && threadIdx.x == 0) a.cuts[blockIdx.x] = Cut{0, U, 0, 0, 0, 0};
     tc_fence_before();
     __syncthreads();
-    if (warp == kMmaWarp) {
+    if (warp == kScoreWarp) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
     }
