@@ -1,9 +1,13 @@
 // attend.cuh - the call of uw_kv_attend as its kernels take it, and how its work is cut.
 //
-// The work is a line of units: tiles of keys for each item (a sequence's tile of query rows and a key head), item after item.
-// CTA c of G has the units [U c / G, U (c + 1) / G), so all of them have as much to do whatever the lengths are.  An item that
-// lies in one CTA's range is stored by it; of an item cut by a range's end each CTA leaves its sums (the running maximum,
-// the sum of powers, the unnormalised output) in the workspace, and a second kernel joins them in the order of the CTAs.
+// An item is a tile of R query rows of a sequence (its new tokens' query heads that share a key head) against one key head;
+// a unit is one of its tiles of 128 keys.  The work is a line: item after item - sequence, key head, tile of rows - each with
+// kItem units of its own, for what it costs beside its keys, and then its tiles.  The line is cut into ranges of C units
+// wherever these end, so that all have as much to do whatever the lengths are.  A first, small kernel measures the line,
+// chooses C and writes down where each range begins.
+// An item that lies in one range is stored by the CTA that has the range; of an item that is cut each CTA leaves its sums (the running
+// maximum, the sum of powers, the unnormalised output) in the workspace, and the one that comes last joins them, in the line's
+// order, so that the result does not depend on which that is.
 #pragma once
 
 #include <cuda.h>
@@ -26,44 +30,133 @@ struct AttendCall {
     int page_size, pages, box;        // box: slots of a copy
     int causal, window;               // window 0: none
     float scale2;                     // scale * log2(e)
-    float *part;                      // [G][2] slots: sums, then maxima, then powers' sums
-    struct Cut *cuts;                 // [G]
+    // workspace
+    struct PlanHead *plan;
+    struct Start *begin;              // [ranges]
+    int *arrived;                     // [2 ranges]: parts of an item that are there, by the range that it begins in (and the tile of rows)
+    int64_t *line;                    // [sequences + 1], for more sequences than fit in shared memory
+    float *part;                      // [ranges][2] places
     int *status;
 };
 
-// what a CTA leaves about the item that begins in its range and goes on behind it
-struct Cut {
-    int64_t end, units;               // the item's last unit + 1; all units
-    int valid, seq, item;
+// What the first kernel finds out.
+struct PlanHead {
+    int64_t units, per;               // of the line, of a range
+    int ranges, ticket;               // ticket: ranges taken beyond the first of each CTA
+};
+
+// where a range begins: the item that holds its first unit, and where that begins in the line
+struct Start {
+    int64_t at;
+    int s, head, i;                   // i: place of the tile of rows
     int pad;
 };
 
-// a sequence's items for tiles of R query rows and K keys
-template <int R, int K>
-struct SeqWork {
+constexpr int kKeys = 128;            // keys of a tile
+
+struct Seq {
     KvSeq q;
-    int keys;                         // slots that the table reaches, at most its length
-    int row_tiles, tile0, tiles;      // tiles of keys: [tile0, tile0 + tiles) for every item
-    __device__ __forceinline__ int64_t units(const AttendCall &a) const { return (int64_t)row_tiles * a.kv_heads * tiles; }
+    int keys, row_tiles;              // keys: slots that the table reaches, at most its length
 };
 
-template <int R, int K>
-__device__ __forceinline__ SeqWork<R, K> seq_work(const AttendCall &a, int s)
+template <int R>
+__device__ __forceinline__ Seq seq_at(const AttendCall &a, int s)
 {
-    SeqWork<R, K> w;
+    Seq w;
     w.q = kv_seq(a.b, s);
     w.keys = min(w.q.len, a.b.capacity);
-    w.row_tiles = (int)(((int64_t)w.q.n * a.group + R - 1) / R);
-    const int64_t first = (int64_t)w.q.len - w.q.n - a.window + 1;  // the first key that the first token sees
-    const int lo = a.window && first > 0 ? (int)min(first, (int64_t)w.keys) : 0;
-    w.tile0 = lo / K;
-    w.tiles = w.row_tiles ? max(1, (w.keys + K - 1) / K - w.tile0) : 0;
+    w.row_tiles = (int)(((uint32_t)w.q.n * (uint32_t)a.group + (R - 1)) / R);
     return w;
 }
 
-// Partial sums of an item in the workspace: R rows of D, then R maxima (of 2^), then R sums.
+// the keys [lo, hi) that some row of a tile of rows sees, and the tiles of keys [t0, t0 + nt) that hold them (one at least)
+struct Span {
+    int lo, hi, t0, nt;
+};
+
+template <int R>
+__device__ __forceinline__ Span span_of(const AttendCall &a, int n, int len, int keys, int rt)
+{
+    // n x group and the tile's end are below 2^31 (the call's rows are limited)
+    const uint32_t x0 = (uint32_t)rt * R, x1 = min((uint32_t)n * (uint32_t)a.group, x0 + R);
+    const int i0 = (int)(x0 / (uint32_t)a.group), i1 = (int)((x1 - 1) / (uint32_t)a.group);
+    const int p0 = len - n;
+    Span r;
+    r.hi = a.causal ? min(max(p0 + i1 + 1, 0), keys) : keys;
+    r.lo = a.window ? (int)min(max((int64_t)p0 + i0 - a.window + 1, (int64_t)0), (int64_t)r.hi) : 0;
+    r.t0 = r.lo / kKeys;
+    r.nt = max(1, (r.hi + kKeys - 1) / kKeys - r.t0);
+    return r;
+}
+
+// The i-th tile of rows of `tiles` in the line: from both ends in turn, as a causal sequence's first tiles see few keys and its
+// last many, and a range should not be all short items.
+__device__ __forceinline__ int tile_of(int i, int tiles) { return (i & 1) ? tiles - 1 - (i >> 1) : i >> 1; }
+
+// An item of the line and which of its tiles of keys lie in the range [ua, ub): those [off, off + cnt).  Set, and moved on, to an
+// item that has some there; more(): there was one.
+template <int R, int kItem>
+struct Cursor {
+    Seq w;
+    Span k;
+    int64_t at, ua, ub;
+    int s, head, i, rt, off, cnt;
+    __device__ __forceinline__ void enter(const AttendCall &a)
+    {
+        rt = tile_of(i, w.row_tiles);
+        k = span_of<R>(a, w.q.n, w.q.len, w.keys, rt);
+        off = (int)max(ua - at - kItem, (int64_t)0);
+        cnt = (int)(min(ub - at - kItem, (int64_t)k.nt)) - off;
+    }
+    __device__ __forceinline__ void set(const AttendCall &a, const Start &f, int64_t ua_, int64_t ub_)
+    {
+        at = f.at;
+        ua = ua_;
+        ub = ub_;
+        s = f.s;
+        head = f.head;
+        i = f.i;
+        w = seq_at<R>(a, s);
+        enter(a);
+        if (cnt <= 0) next(a);
+    }
+    __device__ __forceinline__ bool more() const { return at < ub; }
+    __device__ __forceinline__ void next(const AttendCall &a)
+    {
+        do {
+            at += k.nt + kItem;
+            if (at >= ub) return;
+            if (++i >= w.row_tiles) {
+                i = 0;
+                if (++head >= a.kv_heads) {
+                    head = 0;
+                    do {
+                        if (++s >= a.b.sequences) {   // only where `starts` is not ascending
+                            at = ub;
+                            return;
+                        }
+                        w = seq_at<R>(a, s);
+                    } while (!w.row_tiles);
+                }
+            }
+            enter(a);
+        } while (cnt <= 0);
+    }
+    __device__ __forceinline__ int rows(const AttendCall &a) const { return min(w.q.n * a.group - rt * R, R); }
+    __device__ __forceinline__ bool begins() const { return off == 0; }
+    __device__ __forceinline__ bool ends() const { return off + cnt == k.nt; }
+    // the ranges that hold the item's first and last tile
+    __device__ __forceinline__ int first_range(int64_t per) const { return (int)((at + kItem) / per); }
+    __device__ __forceinline__ int last_range(int64_t per) const { return (int)((at + kItem + k.nt - 1) / per); }
+};
+
+// Partial sums of an item in the workspace: R rows of D, then R maxima (of 2^), then R sums.  Range r has two places: 2 r for
+// the item that goes on from the range before, 2 r + 1 for the one that goes on in the next.
 template <int R, int D>
 __host__ __device__ constexpr size_t slot_floats() { return (size_t)R * (D + 2); }
+
+// The bounds of a call's work that the host knows: ranges at most, and the bytes of what the first kernel writes
+constexpr int kMaxRangesPerCta = 6;
 
 namespace dev {
 
@@ -98,8 +191,10 @@ __device__ __forceinline__ bool mbar_wait_short(uint64_t *b, uint32_t parity)
 
 }  // namespace dev
 
-// k_attend_tc.cu: items of 256 rows on tcgen05
+// k_attend_tc.cu: items of 256 rows on tcgen05.  launch_attend_plan (k_attend.cu): the first kernel, for items of 256 rows.
 size_t attend_tc_slot_floats(int D);
 int launch_attend_tc(const uw_kv_cache *c, const AttendCall &a, int ctas, void *stream);
+int launch_attend_plan256(const AttendCall &a, int ctas, void *stream);
+constexpr int kItem256 = 3;           // what an item of 256 rows costs beside its tiles of keys: queries, output, a pipeline that runs dry
 
 }  // namespace uw

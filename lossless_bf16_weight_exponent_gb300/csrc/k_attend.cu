@@ -29,7 +29,10 @@ namespace {
 using namespace dev;
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kRows = 16, kStep = 16, kTile = kStep * kWarps;
+constexpr int kRows = 16, kStep = 16;
+constexpr int kItem16 = 1;        // what an item costs beside its tiles of keys: the warps' sums joined, its queries
+constexpr int kLeast16 = 8;       // units of a range, where there is work for more than one range a CTA
+static_assert(kStep * kWarps == kKeys, "a tile is a step of every warp");
 constexpr int kStages = 3;
 constexpr float kNegInf = -INFINITY;
 
@@ -85,44 +88,104 @@ __device__ __forceinline__ uint32_t pack2(float a, float b)
     return *(const uint32_t *)&v;
 }
 
-// a place in the line of units: sequence, item (key head x row tiles + row tile), tile of keys
-struct Cursor {
-    SeqWork<kRows, kTile> w;
-    int s, item, off;          // off: tiles of the item before this one
-    int head, rt;              // of the item
-    int lo, hi;                // keys that a row of the item may see: [lo, hi)
-    __device__ __forceinline__ void enter_item(const AttendCall &a)
-    {
-        head = item / w.row_tiles;
-        rt = item - head * w.row_tiles;
-        const int i0 = rt * kRows / a.group, i1 = (int)(min((int64_t)w.q.n * a.group, (int64_t)(rt + 1) * kRows) - 1) / a.group;
-        const int64_t p0 = (int64_t)w.q.len - w.q.n;
-        hi = a.causal ? (int)min(max(p0 + i1 + 1, (int64_t)0), (int64_t)w.keys) : w.keys;
-        lo = a.window ? (int)min(max(p0 + i0 - a.window + 1, (int64_t)0), (int64_t)w.keys) : 0;
-    }
-    __device__ __forceinline__ void enter_seq(const AttendCall &a)
-    {
-        for (;; s++) {
-            w = seq_work<kRows, kTile>(a, s);
-            if (w.row_tiles) break;
-        }
-        item = 0;
-        enter_item(a);
-    }
-    // the next unit; only called while one is left
-    __device__ __forceinline__ void next(const AttendCall &a)
-    {
-        if (++off < w.tiles) return;
-        off = 0;
-        if (++item < w.row_tiles * a.kv_heads) enter_item(a);
-        else {
-            s++;
-            enter_seq(a);
-        }
-    }
-    __device__ __forceinline__ int key0(int warp) const { return (w.tile0 + off) * kTile + warp * kStep; }
-    __device__ __forceinline__ bool active(int warp) const { return key0(warp) < hi && key0(warp) + kStep > lo; }
+using Cur = Cursor<kRows, kItem16>;
+
+__device__ __forceinline__ int key0_of(const Cur &c, int j, int warp) { return (c.k.t0 + c.off + j) * kKeys + warp * kStep; }
+// some row of the item sees one of the warp's 16 keys
+__device__ __forceinline__ bool active(const Cur &c, int key0) { return key0 < c.k.hi && key0 + kStep > c.k.lo; }
+
+// the next range that the CTA has taken
+struct Ticket {
+    int tag, range;      // tag: which of the CTA's ranges it is
+    Start at;
 };
+
+// Joins the parts of an item of xn rows that was cut: those of ranges r0 .. r0 + parts - 1, by the whole CTA.  Four columns of
+// a row a thread, and where threads are left, a lot of the parts each; eight parts on their way at a time.
+template <int D>
+__device__ __forceinline__ void join16(const AttendCall &a, const Cur &c, int r0, int parts, int xn, float4 *buf, float2 *red)
+{
+    constexpr size_t kSlot = slot_floats<kRows, D>();
+    constexpr int kAt = 8;
+    const int tid = threadIdx.x, E = xn * (D / 4), lots = max(1, kThreads / E);
+    const float *base = a.part + 2 * (size_t)r0 * kSlot;
+    for (int e0 = 0; e0 < E; e0 += kThreads) {
+        const int e = lots > 1 ? tid % E : e0 + tid, lot = lots > 1 ? tid / E : 0, r = e / (D / 4);
+        const bool in = e < E && lot < lots;
+        float m = kNegInf, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i0 = lot; in && i0 < parts; i0 += kAt * lots) {
+            float pm[kAt], pl[kAt];
+            float4 v[kAt];
+#pragma unroll
+            for (int k = 0; k < kAt; k++) {
+                const int i = i0 + k * lots;
+                const float *p = base + (2 * (size_t)i + (i == 0)) * kSlot;
+                pm[k] = kNegInf;
+                pl[k] = 0.f;
+                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i < parts) {
+                    v[k] = __ldcg((const float4 *)p + e);
+                    pm[k] = __ldcg(p + kRows * D + r);
+                    pl[k] = __ldcg(p + kRows * D + kRows + r);
+                }
+            }
+            float mm = m;
+#pragma unroll
+            for (int k = 0; k < kAt; k++) mm = fmaxf(mm, pm[k]);
+            const float b = mm == kNegInf ? 0.f : mm, f0 = exp2_fast(m - b);
+            m = mm;
+            l *= f0;
+            o.x *= f0;
+            o.y *= f0;
+            o.z *= f0;
+            o.w *= f0;
+#pragma unroll
+            for (int k = 0; k < kAt; k++) {
+                const float f = exp2_fast(pm[k] - b);
+                l += pl[k] * f;
+                o.x += v[k].x * f;
+                o.y += v[k].y * f;
+                o.z += v[k].z * f;
+                o.w += v[k].w * f;
+            }
+        }
+        if (lots > 1) {
+            buf[tid] = o;
+            red[tid] = make_float2(m, l);
+            __syncthreads();
+            if (in && lot == 0) {
+                float mm = m;
+                for (int i = 1; i < lots; i++) mm = fmaxf(mm, red[i * E + e].x);
+                const float b = mm == kNegInf ? 0.f : mm, f0 = exp2_fast(m - b);
+                m = mm;
+                l *= f0;
+                o.x *= f0;
+                o.y *= f0;
+                o.z *= f0;
+                o.w *= f0;
+                for (int i = 1; i < lots; i++) {
+                    const float2 t = red[i * E + e];
+                    const float4 v = buf[i * E + e];
+                    const float f = exp2_fast(t.x - b);
+                    l += t.y * f;
+                    o.x += v.x * f;
+                    o.y += v.y * f;
+                    o.z += v.z * f;
+                    o.w += v.w * f;
+                }
+            }
+        }
+        if (in && lot == 0) {
+            const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+            const int x = c.rt * kRows + r, tok = x / a.group, h = c.head * a.group + x - tok * a.group, col = 4 * (e % (D / 4));
+            const int64_t row = c.w.q.first + tok;
+            *(uint2 *)(a.out + row * a.ldo + (int64_t)h * D + col) = make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
+            if (a.lse && col == 0) a.lse[row * a.q_heads + h] = l == 0.f ? kNegInf : (m + log2f(l)) * 0.69314718f;
+        }
+    }
+    __syncthreads();
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attend16_kernel(const __grid_constant__ Args g)
@@ -130,9 +193,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend16_kernel(const __grid_cons
     using L = Layout<D>;
     constexpr int KS = D / 16;        // steps of the first product, and pairs of column tiles of the second
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    __shared__ int64_t sums[kWarps];
-    __shared__ int64_t found_at;
-    __shared__ int found_s;
+    __shared__ Ticket tickets[2];
+    __shared__ float2 red[kThreads];
+    __shared__ int last;
     const AttendCall &a = g.c;
     uint8_t *ring = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);
     float4 *merge = (float4 *)(ring + L::ring);
@@ -143,87 +206,83 @@ __global__ void __launch_bounds__(kThreads, 1) attend16_kernel(const __grid_cons
         for (int i = 0; i < kStages; i++) mbar_init(&full[warp * kStages + i], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    if (threadIdx.x < 2) tickets[threadIdx.x].tag = 0;
     pdl_trigger();
     pdl_wait();
-
-    // ---------------------------------------------------------------------------------- this CTA's units
-    int64_t mine = 0, one = 0;
-    for (int s = threadIdx.x; s < a.b.sequences; s += kThreads) {
-        one = seq_work<kRows, kTile>(a, s).units(a);
-        mine += one;
-    }
-    int64_t v = mine;
-#pragma unroll
-    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-    if (lane == 0) sums[warp] = v;
-    __syncthreads();
-    int64_t U = 0;
-    for (int i = 0; i < kWarps; i++) U += sums[i];
-    const int64_t G = gridDim.x;
-    const int64_t ua = U * blockIdx.x / G, ub = U * (blockIdx.x + 1) / G;
-    Cut cut{0, U, 0, 0, 0, 0};
-    if (ua >= ub) {
-        if (threadIdx.x == 0) a.cuts[blockIdx.x] = cut;
-        return;
-    }
-    // the sequence with unit ua: 256 at a time in order
-    int64_t before = 0;
-    for (int s0 = 0; s0 < a.b.sequences; s0 += kThreads) {
-        const int s = s0 + threadIdx.x;
-        int64_t n = 0;
-        if (s < a.b.sequences) n = a.b.sequences <= kThreads ? one : seq_work<kRows, kTile>(a, s).units(a);
-        int64_t incl = n;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int64_t o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-            if (lane >= d) incl += o;
-        }
-        __syncthreads();
-        if (lane == 31) sums[warp] = incl;
-        __syncthreads();
-        int64_t excl = before + incl - n;
-        for (int i = 0; i < kWarps; i++) {
-            if (i < warp) excl += sums[i];
-            before += sums[i];
-        }
-        if (n && excl <= ua && ua < excl + n) {
-            found_s = s;
-            found_at = excl;
-        }
-        if (before > ua) break;
-    }
+    const int N = a.plan->ranges;
+    const int64_t C = a.plan->per, U = a.plan->units;
+    if ((int)blockIdx.x >= N) return;
     __syncthreads();
 
-    // ---------------------------------------------------------------------------------- cursors
-    Cursor use;
-    use.s = found_s;
-    use.enter_seq(a);
-    {
-        const int64_t in = ua - found_at;
-        use.item = (int)(in / use.w.tiles);
-        use.off = (int)(in - (int64_t)use.item * use.w.tiles);
-        use.enter_item(a);
-    }
-    Cursor ld = use;
-    int64_t ul = ua;                 // unit of ld
+    // ---------------------------------------------------------------------------------- ranges and cursors
+    // The CTA's first range is its own number; further ones are taken from a counter, a range ahead: thread 0 asks at a range's
+    // first tile, looks where the range begins at the second and tells the others at the third, so that it never waits.
+    int got = 0, pump = 0, next_range = N;      // thread 0's
+    Start next_at{};
+    auto pump_ticket = [&](int mine) {          // mine: which of the CTA's ranges is at work (1, 2, ...)
+        if (threadIdx.x) return;
+        if (pump == 0) {
+            got = (int)gridDim.x < N ? atomicAdd(&a.plan->ticket, 1) : N;
+            pump = 1;
+        } else if (pump == 1) {
+            next_range = min((int64_t)gridDim.x + got, (int64_t)N);
+            if (next_range < N) next_at = a.begin[next_range];
+            pump = 2;
+        } else if (pump == 2) {
+            Ticket &t = tickets[(mine + 1) & 1];
+            t.range = next_range;
+            t.at = next_at;
+            __threadfence_block();
+            *(volatile int *)&t.tag = mine + 1;
+            pump = 3;
+        }
+    };
+    int range = blockIdx.x, mine = 1;
+    Cur use, ld;
+    use.set(a, a.begin[range], range * C, min((range + 1) * C, U));
+    ld = use;
+    int ld_j = 0, ld_mine = 1;
     uint32_t asked = 0, used = 0;    // steps copied, steps consumed
     bool ok = true;
     const uint32_t my_ring = saddr(ring) + warp * kStages * L::stage;
     uint64_t *bars = full + warp * kStages;
 
-    // asks for the warp's next step, if there is one
-    auto ask = [&] {
-        while (ul < ub && !ld.active(warp)) {
-            if (++ul < ub) ld.next(a);
+    // moves ld to the warp's next step; false: there is none
+    auto seek = [&]() -> bool {
+        for (;;) {
+            if (ld.more()) {
+                for (; ld_j < ld.cnt; ld_j++)
+                    if (active(ld, key0_of(ld, ld_j, warp))) return true;
+                ld_j = 0;
+                ld.next(a);
+                continue;
+            }
+            // the CTA's next range, once thread 0 has told of it; never more than a range ahead of the one at work
+            if (ld_mine != mine) return false;
+            const volatile Ticket &t = tickets[(ld_mine + 1) & 1];
+            if (__shfl_sync(0xFFFFFFFFu, t.tag, 0) != ld_mine + 1) return false;
+            __threadfence_block();
+            const int r = t.range;
+            if (r >= N) return false;
+            Start f;
+            f.at = t.at.at;
+            f.s = t.at.s;
+            f.head = t.at.head;
+            f.i = t.at.i;
+            ld_mine++;
+            ld.set(a, f, r * C, min((r + 1) * C, U));
         }
-        if (ul >= ub || !ok) return;
+    };
+    // asks for the warp's next step, if there is one that it can know of
+    auto ask = [&]() -> bool {
+        if (!ok || !seek()) return false;
         const uint32_t st = asked % kStages;
         if (lane == 0) mbar_expect_tx(&bars[st], L::stage);
         __syncwarp();
         const int boxes = kStep / a.box;
         if (lane < 2 * (D / 64) * boxes) {
             const int is_v = lane & 1, half = (lane >> 1) % (D / 64), bx = lane / (2 * (D / 64));
-            const int key = ld.key0(warp) + bx * a.box;
+            const int key = key0_of(ld, ld_j, warp) + bx * a.box;
             const int pi = key / a.page_size;
             const int page = key < ld.w.keys ? a.b.pages[(int64_t)ld.s * a.b.ld_pages + pi] : -1;
             tma4d(my_ring + st * L::stage + is_v * L::mat + half * L::half + bx * a.box * 128, is_v ? &g.vm : &g.km, half * 64, key - pi * a.page_size, ld.head,
@@ -231,20 +290,21 @@ __global__ void __launch_bounds__(kThreads, 1) attend16_kernel(const __grid_cons
         }
         __syncwarp();
         asked++;
-        if (++ul < ub) ld.next(a);
+        ld_j++;
+        return true;
     };
-    for (int i = 0; i < kStages - 1; i++) ask();
+    while (asked < kStages && ask()) {}
 
     // ---------------------------------------------------------------------------------- items
     const int gq = lane >> 2, tq = lane & 3;
-    int64_t u = ua;
-    while (u < ub) {
-        const int seg = (int)min((int64_t)use.w.tiles - use.off, ub - u);
-        const bool begins = use.off == 0, ends = use.off + seg == use.w.tiles;
+    for (;;) {
+    for (; use.more(); use.next(a)) {
+        const int seg = use.cnt;
+        const bool begins = use.begins(), ends = use.ends();
         // the two rows of this thread: their queries, and the keys [from, upto) that they see
         uint32_t aq[KS][4];
         int from[2], upto[2];
-        const int x0 = use.rt * kRows, xn = (int)min((int64_t)use.w.q.n * a.group - x0, (int64_t)kRows);
+        const int x0 = use.rt * kRows, xn = use.rows(a);
 #pragma unroll
         for (int j = 0; j < 2; j++) {
             const int r = gq + 8 * j;
@@ -266,17 +326,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend16_kernel(const __grid_cons
         for (int n = 0; n < 2 * KS; n++) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
 
         for (int k = 0; k < seg; k++) {
-            if (use.active(warp)) {
-                ask();
+            pump_ticket(mine);
+            const int key0 = key0_of(use, k, warp);
+            if (active(use, key0)) {
+                while (asked < used + kStages && ask()) {}
                 const uint32_t st = used % kStages;
                 if (ok && !mbar_wait_short(&bars[st], (used / kStages) & 1)) ok = false;
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 used++;
                 const uint32_t ks = my_ring + st * L::stage, vs = ks + L::mat;
-                const int key0 = use.key0(warp);
-                if (key0 < use.lo || key0 + kStep > use.hi) {
+                if (key0 < use.k.lo || key0 + kStep > use.k.hi) {
                     // values that no row of the item sees: behind the sequence, or in pages that a window has left
-                    const int r0 = max(use.lo - key0, 0), r1 = min(use.hi - key0, kStep);
+                    const int r0 = max(use.k.lo - key0, 0), r1 = min(use.k.hi - key0, kStep);
                     for (int i = lane; i < kStep * (D / 8); i += 32) {
                         const int row = i / (D / 8), c = i % (D / 8);
                         if (row >= r0 && row < r1) continue;
@@ -344,8 +405,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend16_kernel(const __grid_cons
                 }
                 __syncwarp();
             }
-            u++;
-            if (k + 1 < seg) use.off++;
         }
 
         // ------------------------------------------------------------------------------ the warps' sums
@@ -412,10 +471,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend16_kernel(const __grid_cons
                     if (a.lse && tq == 0) a.lse[row * a.q_heads + h] = l[j] == 0.f ? kNegInf : (m[j] + log2f(l[j])) * 0.69314718f;
                 }
             } else {
-                float *p = a.part + (2 * (size_t)blockIdx.x + (begins ? 1 : 0)) * slot_floats<kRows, D>();
+                float *p = a.part + (2 * (size_t)range + (begins ? 1 : 0)) * slot_floats<kRows, D>();
 #pragma unroll
                 for (int j = 0; j < 2; j++) {
                     const int r = gq + 8 * j;
+                    if (r >= xn) continue;
 #pragma unroll
                     for (int n = 0; n < 2 * KS; n++) *(float2 *)(p + r * D + 8 * n + 2 * tq) = make_float2(o[n][2 * j], o[n][2 * j + 1]);
                     if (tq == 0) {
@@ -423,17 +483,38 @@ __global__ void __launch_bounds__(kThreads, 1) attend16_kernel(const __grid_cons
                         p[kRows * D + kRows + r] = l[j];
                     }
                 }
-                if (begins) {
-                    cut.valid = 1;
-                    cut.seq = use.s;
-                    cut.item = use.item;
-                    cut.end = u + (use.w.tiles - seg);
-                }
             }
         }
-        if (u < ub) use.next(a);
+        if (!begins || !ends) {
+            // the part that comes last joins them all
+            const int r0 = use.first_range(C), parts = use.last_range(C) - r0 + 1;
+            if (warp == 0) {
+                __threadfence();
+                __syncwarp();
+                if (lane == 0) last = atomicAdd(&a.arrived[2 * r0], 1) == parts - 1;
+            }
+            __syncthreads();
+            if (last) {
+                __threadfence();
+                join16<D>(a, use, r0, parts, xn, merge, red);
+            }
+        }
     }
-    if (threadIdx.x == 0) a.cuts[blockIdx.x] = cut;
+    // the CTA's next range
+    while (threadIdx.x == 0 && pump < 3) pump_ticket(mine);
+    __syncthreads();
+    const Ticket &nt = tickets[(mine + 1) & 1];
+    if (nt.range >= N) break;
+    range = nt.range;
+    mine++;
+    pump = 0;
+    use.set(a, nt.at, range * C, min((range + 1) * C, U));
+    if (ld_mine < mine) {   // it had not heard of this range: every step before it has been asked for and used
+        ld = use;
+        ld_j = 0;
+        ld_mine = mine;
+    }
+    }
     if (!ok) {
         // what was asked for lands before the block ends
         if (lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
@@ -441,57 +522,224 @@ __global__ void __launch_bounds__(kThreads, 1) attend16_kernel(const __grid_cons
     }
 }
 
-// joins the sums of items that were cut: block c those of the item that begins in CTA c's range
-template <int R, int D, int K>
-__global__ void __launch_bounds__(256) join_kernel(const AttendCall a)
+// ------------------------------------------------------------------------------------------------ the first kernel
+constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
+constexpr int kLineShared = 2048;      // sequences whose places in the line fit in shared memory
+
+// Sums over the threads in front of this one; all: over all threads.  sums: [kPlanWarps], free for the next call after a barrier.
+template <typename T>
+__device__ __forceinline__ T scan_before(T v, T *sums, T &all)
 {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    T x = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const T o = __shfl_up_sync(0xFFFFFFFFu, x, d);
+        if (lane >= d) x += o;
+    }
+    if (lane == 31) sums[warp] = x;
+    __syncthreads();
+    T y = sums[lane];                  // every warp adds them up
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const T o = __shfl_up_sync(0xFFFFFFFFu, y, d);
+        if (lane >= d) y += o;
+    }
+    const T front = __shfl_sync(0xFFFFFFFFu, y, warp ? warp - 1 : 0);
+    all = __shfl_sync(0xFFFFFFFFu, y, 31);
+    return (warp ? front : (T)0) + x - v;
+}
+
+// the last i in [lo, hi) for which at(i) <= x; at(lo) <= x
+template <typename F, typename T>
+__device__ __forceinline__ int last_at(int lo, int hi, T x, F at)
+{
+    int n = hi - lo;
+    while (n > 1) {
+        const int h = n >> 1;
+        if (at(lo + h) <= x) {
+            lo += h;
+            n -= h;
+        } else {
+            n = h;
+        }
+    }
+    return lo;
+}
+
+__device__ __forceinline__ int64_t range_units(int64_t U, int ctas, int most, int least)
+{
+    const int64_t share = (U + ctas - 1) / ctas;
+    return max(max((share + most - 1) / most, min(share, (int64_t)least)), (int64_t)1);
+}
+
+// The line's length, the ranges and where they begin; one CTA.  ctas: of the next kernel, each of which gets up to `most` ranges of
+// at least `least` units, one where there is no more work.  This form holds every tile of rows in shared memory, up to
+// kSmallSeqs sequences and kSmallTiles tiles: one tile a thread, a sum over the threads, two searches for each range (3 us
+// where the form below takes 12, for the 128 tiles of 8191 tokens).
+constexpr int kSmallSeqs = 1024, kSmallTiles = 4096;
+
+template <int R, int kItem>
+__global__ void __launch_bounds__(kPlanThreads) plan_small_kernel(const AttendCall a, int ctas, int most, int least)
+{
+    __shared__ int64_t pre[kSmallTiles + 1];       // of a key head's line, in front of each tile of rows
+    __shared__ int n_s[kSmallSeqs], len_s[kSmallSeqs], tile0[kSmallSeqs + 1];
+    __shared__ int64_t sums[kPlanWarps];
+    __shared__ int isums[kPlanWarps];
+    const int tid = threadIdx.x, S = a.b.sequences;
     pdl_trigger();
     pdl_wait();
-    const Cut cut = a.cuts[blockIdx.x];
-    if (!cut.valid) return;
-    const int64_t G = gridDim.x;
-    const SeqWork<R, K> w = seq_work<R, K>(a, cut.seq);
-    const int head = cut.item / w.row_tiles, rt = cut.item - head * w.row_tiles;
-    constexpr int kCols = D / 16;        // of a thread
-    constexpr size_t kSlot = slot_floats<R, D>();
-    const int col = (threadIdx.x % 16) * kCols;
-    for (int r = threadIdx.x / 16; r < R; r += 16) {
-        const int64_t x = (int64_t)rt * R + r;
-        if (x >= (int64_t)w.q.n * a.group) break;
-        // slot 1 of this CTA, then slot 0 of those behind it that have units of the item
-        auto each = [&](auto f) {
-            f(a.part + (2 * (size_t)blockIdx.x + 1) * kSlot);
-            for (int64_t c = blockIdx.x + 1; c < G; c++) {
-                const int64_t ua = cut.units * c / G, ub = cut.units * (c + 1) / G;
-                if (ua >= cut.end) break;
-                if (ua < ub) f(a.part + 2 * (size_t)c * kSlot);
-            }
-        };
-        float m = kNegInf, l = 0.f, o[kCols];
-#pragma unroll
-        for (int i = 0; i < kCols; i++) o[i] = 0.f;
-        each([&](const float *p) { m = fmaxf(m, p[R * D + r]); });
-        const float b = m == kNegInf ? 0.f : m;
-        each([&](const float *p) {
-            const float f = exp2_fast(p[R * D + r] - b);
-            l += p[R * D + R + r] * f;
-#pragma unroll
-            for (int i = 0; i < kCols; i += 4) {
-                const float4 t = *(const float4 *)(p + (size_t)r * D + col + i);
-                o[i] += t.x * f;
-                o[i + 1] += t.y * f;
-                o[i + 2] += t.z * f;
-                o[i + 3] += t.w * f;
-            }
-        });
-        const int i = (int)(x / a.group), h = head * a.group + (int)(x - (int64_t)i * a.group);
-        const int64_t row = w.q.first + i;
-        const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
-        uint16_t *p = a.out + row * a.ldo + (int64_t)h * D + col;
-#pragma unroll
-        for (int c = 0; c < kCols; c += 2) *(uint32_t *)(p + c) = pack2(o[c] * inv, o[c + 1] * inv);
-        if (a.lse && col == 0) a.lse[row * a.q_heads + h] = l == 0.f ? kNegInf : (m + log2f(l)) * 0.69314718f;
+    Seq w{};
+    if (tid < S) {
+        w = seq_at<R>(a, tid);
+        n_s[tid] = w.q.n;
+        len_s[tid] = w.q.len;
     }
+    int T;
+    const int mine = scan_before(w.row_tiles, isums, T);
+    T = min(T, kSmallTiles);           // as the host has counted them, unless `starts` is not ascending
+    if (tid < S) tile0[tid] = min(mine, T);
+    if (tid == 0) {
+        tile0[S] = T;
+        pre[0] = 0;
+    }
+    __syncthreads();
+    const int per = (T + kPlanThreads - 1) / kPlanThreads, f0 = tid * per, f1 = min(f0 + per, T);
+    int64_t cost = 0;
+    if (f0 < f1) {
+        int s = last_at(0, S, f0, [&](int i) { return tile0[i]; });
+        for (int f = f0; f < f1; f++) {
+            while (f >= tile0[s + 1]) s++;
+            const int tiles = tile0[s + 1] - tile0[s];
+            cost += span_of<R>(a, n_s[s], len_s[s], min(len_s[s], a.b.capacity), tile_of(f - tile0[s], tiles)).nt + kItem;
+            pre[f + 1] = cost;
+        }
+    }
+    int64_t P;
+    const int64_t front = scan_before(cost, sums, P);
+    for (int f = f0; f < f1; f++) pre[f + 1] += front;
+    __syncthreads();
+    const int64_t U = P * a.kv_heads, C = range_units(U, ctas, most, least);
+    const int N = (int)((U + C - 1) / C);
+    if (tid == 0) *a.plan = PlanHead{U, C, N, 0};
+    for (int i = tid; i < 2 * N; i += kPlanThreads) a.arrived[i] = 0;
+    for (int r = tid; r < N; r += kPlanThreads) {
+        const int64_t ua = r * C;
+        const int s = last_at(0, S, ua, [&](int i) { return pre[tile0[i]] * a.kv_heads; });
+        const int64_t p0 = pre[tile0[s]], w1 = pre[tile0[s + 1]] - p0, in = ua - p0 * a.kv_heads;
+        const int head = (int)(in / w1);
+        const int64_t at = in - head * w1;
+        const int f = last_at(tile0[s], tile0[s + 1], at, [&](int i) { return pre[i] - p0; });
+        a.begin[r] = Start{ua - (at - (pre[f] - p0)), s, head, f - tile0[s], 0};
+    }
+}
+
+// units of sequence s for one key head, by the whole warp, a sequence a lane (s past the end: none)
+template <int R, int kItem>
+__device__ __forceinline__ int64_t units_of(const AttendCall &a, int s)
+{
+    const int lane = threadIdx.x & 31;
+    Seq w{};
+    if (s < a.b.sequences) w = seq_at<R>(a, s);
+    int64_t u = 0;
+    const bool many = w.row_tiles > 2;
+    if (!many)
+        for (int rt = 0; rt < w.row_tiles; rt++) u += span_of<R>(a, w.q.n, w.q.len, w.keys, rt).nt + kItem;
+    unsigned left = __ballot_sync(0xFFFFFFFFu, many);
+    while (left) {
+        const int src = __ffs(left) - 1;
+        left &= left - 1;
+        const int n = __shfl_sync(0xFFFFFFFFu, w.q.n, src), len = __shfl_sync(0xFFFFFFFFu, w.q.len, src);
+        const int keys = __shfl_sync(0xFFFFFFFFu, w.keys, src), tiles = __shfl_sync(0xFFFFFFFFu, w.row_tiles, src);
+        int64_t x = 0;
+        for (int rt = lane; rt < tiles; rt += 32) x += span_of<R>(a, n, len, keys, rt).nt + kItem;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
+        if (lane == src) u = x;
+    }
+    return u;
+}
+
+// The same for any number of sequences and tiles, which are measured a warp at a time and again for each range.
+template <int R, int kItem>
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttendCall a, int ctas, int most, int least)
+{
+    __shared__ int64_t line_s[kLineShared + 1];
+    __shared__ int64_t sums[kPlanWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, S = a.b.sequences;
+    int64_t *line = S <= kLineShared ? line_s : a.line;   // before each sequence
+    pdl_trigger();
+    pdl_wait();
+    int64_t before = 0;
+    for (int s0 = 0; s0 < S; s0 += kPlanThreads) {
+        const int s = s0 + threadIdx.x;
+        const int64_t n = units_of<R, kItem>(a, s) * a.kv_heads;
+        __syncthreads();
+        int64_t all;
+        const int64_t front = scan_before(n, sums, all);
+        if (s < S) line[s + 1] = before + front + n;
+        before += all;
+    }
+    if (threadIdx.x == 0) line[0] = 0;
+    __syncthreads();
+    const int64_t U = before, C = range_units(U, ctas, most, least);
+    const int N = (int)((U + C - 1) / C);
+    if (threadIdx.x == 0) *a.plan = PlanHead{U, C, N, 0};
+    for (int i = threadIdx.x; i < 2 * N; i += kPlanThreads) a.arrived[i] = 0;
+    for (int r0 = 0; r0 < N; r0 += kPlanThreads) {
+        const int r = r0 + lane * kPlanWarps + warp;   // neighbours on different warps, which work through theirs one by one
+        // the sequence: the last whose place is at or before the range's
+        const int64_t ua = r * C;
+        const int lo = last_at(0, r < N ? S : 1, ua, [&](int i) { return line[i]; });
+        Seq w{};
+        Start f{0, lo, 0, 0, 0};
+        int64_t at = 0;                // of the range in the head's part of the line
+        if (r < N) {
+            w = seq_at<R>(a, lo);
+            const int64_t per = (line[lo + 1] - line[lo]) / a.kv_heads, in = ua - line[lo];
+            f.head = (int)(in / per);
+            at = in - f.head * per;
+            f.at = ua - at;
+        }
+        const bool many = w.row_tiles > 1;
+        unsigned left = __ballot_sync(0xFFFFFFFFu, many);
+        while (left) {
+            const int src = __ffs(left) - 1;
+            left &= left - 1;
+            const int qn = __shfl_sync(0xFFFFFFFFu, w.q.n, src), len = __shfl_sync(0xFFFFFFFFu, w.q.len, src);
+            const int keys = __shfl_sync(0xFFFFFFFFu, w.keys, src), tiles = __shfl_sync(0xFFFFFFFFu, w.row_tiles, src);
+            int64_t rest = __shfl_sync(0xFFFFFFFFu, at, src);
+            for (int i0 = 0; i0 < tiles; i0 += 32) {
+                const int nt = i0 + lane < tiles ? span_of<R>(a, qn, len, keys, tile_of(i0 + lane, tiles)).nt + kItem : 0;
+                int64_t x = nt;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int64_t o = __shfl_up_sync(0xFFFFFFFFu, x, d);
+                    if (lane >= d) x += o;
+                }
+                const int64_t all = __shfl_sync(0xFFFFFFFFu, x, 31);
+                if (rest < all) {
+                    const unsigned hit = __ballot_sync(0xFFFFFFFFu, rest < x);   // the first of them has it
+                    const int l = __ffs(hit) - 1;
+                    const int64_t in_item = rest - (__shfl_sync(0xFFFFFFFFu, x, l) - __shfl_sync(0xFFFFFFFFu, nt, l));
+                    if (lane == src) {
+                        f.i = i0 + l;
+                        f.at = ua - in_item;
+                    }
+                    break;
+                }
+                rest -= all;
+            }
+        }
+        if (r < N) a.begin[r] = f;
+    }
+}
+
+template <int R, int kItem>
+cudaError_t launch_plan(const AttendCall &a, int ctas, int most, int least, cudaStream_t st)
+{
+    const bool small = a.b.sequences <= kSmallSeqs && (int64_t)a.b.rows * a.group / R + a.b.sequences <= kSmallTiles;
+    return launch_dependent(small ? plan_small_kernel<R, kItem> : plan_kernel<R, kItem>, dim3(1), kPlanThreads, 0, 0, st, a, ctas, most, least);
 }
 
 template <int D>
@@ -505,24 +753,30 @@ cudaError_t launch16(const uw_kv_cache *c, const AttendCall &call, int ctas, cud
     g.vm = c->v16;
     g.c = call;
     g.c.box = c->box16;
-    if ((e = launch_dependent(attend16_kernel<D>, dim3((unsigned)ctas), kThreads, Layout<D>::smem, 0, st, g)) != cudaSuccess) return e;
-    return launch_dependent(join_kernel<kRows, D, kTile>, dim3((unsigned)ctas), 256, 0, 0, st, g.c);
+    if ((e = launch_plan<kRows, kItem16>(call, ctas, kMaxRangesPerCta, kLeast16, st)) != cudaSuccess) return e;
+    return launch_dependent(attend16_kernel<D>, dim3((unsigned)ctas), kThreads, Layout<D>::smem, 0, st, g);
 }
 
+// How a call's workspace is laid out, and which kernel it takes.
 struct Plan {
     bool tc;                     // items of 256 rows on tcgen05, else of 16
     int ctas;
-    size_t cuts, bytes;          // bytes of the cuts, of all
+    size_t begin, arrived, line, part, bytes;
 };
 
 Plan plan_of(const uw_kv_cache *c, int sequences, int64_t rows, int q_heads)
 {
     Plan p;
-    p.tc = rows * (q_heads / c->d.kv_heads) > 64 * (int64_t)sequences;
+    p.tc = rows * (q_heads / c->d.kv_heads) > 16 * (int64_t)sequences;
     p.ctas = std::max(1, device_sms());
-    p.cuts = (p.ctas * sizeof(Cut) + 255) / 256 * 256;
+    const size_t ranges = (size_t)p.ctas * (p.tc ? 1 : kMaxRangesPerCta);
+    const auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+    p.begin = up(sizeof(PlanHead));
+    p.arrived = p.begin + up(ranges * sizeof(Start));
+    p.line = p.arrived + up(2 * ranges * sizeof(int));
+    p.part = p.line + (sequences > kLineShared ? up(((size_t)sequences + 1) * sizeof(int64_t)) : 0);
     const size_t slot = p.tc ? attend_tc_slot_floats(c->d.head_dim) : c->d.head_dim == 128 ? slot_floats<kRows, 128>() : slot_floats<kRows, 64>();
-    p.bytes = p.cuts + 2 * (size_t)p.ctas * slot * sizeof(float);
+    p.bytes = p.part + 2 * ranges * slot * sizeof(float);
     return p;
 }
 
@@ -537,6 +791,11 @@ uw_status check_heads(const uw_kv_cache *c, int sequences, int64_t rows, int q_h
 }
 
 }  // namespace
+
+int launch_attend_plan256(const AttendCall &a, int ctas, void *stream)
+{
+    return launch_plan<256, kItem256>(a, ctas, 1, 1, (cudaStream_t)stream);
+}
 
 }  // namespace uw
 
@@ -586,8 +845,12 @@ extern "C" uw_status uw_kv_attend(const uw_kv_cache *c, const uw_kv_batch *b, in
     a.causal = causal != 0;
     a.window = (int)std::min<int64_t>(window, ((int64_t)1 << 31) - 1);
     a.scale2 = scale * 1.4426950408889634f;
-    a.cuts = (Cut *)workspace;
-    a.part = (float *)((uint8_t *)workspace + p.cuts);
+    uint8_t *ws = (uint8_t *)workspace;
+    a.plan = (PlanHead *)ws;
+    a.begin = (Start *)(ws + p.begin);
+    a.arrived = (int *)(ws + p.arrived);
+    a.line = (int64_t *)(ws + p.line);
+    a.part = (float *)(ws + p.part);
     a.status = c->status;
     const int ctas = std::min(p.ctas, num_sms());
     const cudaError_t e = p.tc ? (cudaError_t)launch_attend_tc(c, a, ctas, stream)

@@ -36,16 +36,9 @@ using namespace dev;
 
 constexpr int kWarps = 12, kThreads = 32 * kWarps;
 constexpr int kCopyWarp = 8, kScoreWarp = 9, kValueWarp = 10;
-constexpr int kRows = 256, kTile = 128;
+constexpr int kRows = 256, kTile = kKeys;
 constexpr float kNegInf = -INFINITY;
 constexpr float kGrow = 8.f;      // log2 of how far a maximum may grow before the output is rescaled
-
-constexpr int kItem = 3;          // what an item costs beside its tiles of keys, in tiles: queries, output, a pipeline that runs dry
-
-struct Start {
-    int64_t at;                   // of the item in the line of work
-    int s, head, i;               // i: place of the tile of rows
-};
 
 template <int D>
 struct Layout {
@@ -53,7 +46,7 @@ struct Layout {
     static constexpr uint32_t tile = half * (D / 64);           // a tile of queries, keys or values
     static constexpr int slots = D == 128 ? 5 : 10;
     static constexpr uint32_t bars = 8 * (2 * slots + 18);
-    static constexpr size_t smem = 1024 + 2 * tile + slots * tile + bars + 8 * kWarps + sizeof(Start) + 16;
+    static constexpr size_t smem = 1024 + 2 * tile + slots * tile + bars + 16;
     static_assert(smem <= 227 * 1024, "shared memory");
     // columns of tensor memory
     static constexpr uint32_t o = 0, s = 2 * D, p = s + 128;    // O of tile t at o + t D, P at p + 64 t
@@ -134,108 +127,54 @@ __device__ __forceinline__ uint32_t pack2(float a, float b)
     return *(const uint32_t *)&v;
 }
 
-// ------------------------------------------------------------------------------------------------ the work
-struct Seq {
-    KvSeq q;
-    int keys, row_tiles;
-};
+using Cur = Cursor<kRows, kItem256>;
 
-__device__ __forceinline__ Seq seq_at(const AttendCall &a, int s)
+// the 128 threads of a tile of rows
+__device__ __forceinline__ void tile_sync(int t) { asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory"); }
+
+// Joins a row's parts of an item that was cut, a thread a row: those of ranges r0 .. r0 + parts - 1.
+template <int D>
+__device__ __forceinline__ void join_row(const AttendCall &a, const Cur &c, int r0, int parts, int r, int tok, int x)
 {
-    Seq w;
-    w.q = kv_seq(a.b, s);
-    w.keys = min(w.q.len, a.b.capacity);
-    w.row_tiles = (int)(((int64_t)w.q.n * a.group + kRows - 1) / kRows);
-    return w;
-}
-
-// the keys [lo, hi) that some row of a tile of rows sees, and the tiles of keys [t0, t0 + nt) that hold them (one at least)
-struct Span {
-    int lo, hi, t0, nt;
-};
-
-__device__ __forceinline__ Span span_of(const AttendCall &a, int n, int len, int keys, int rt)
-{
-    // n x group and the tile's end are below 2^31 (the call's rows are limited)
-    const uint32_t x0 = (uint32_t)rt * kRows, x1 = min((uint32_t)n * (uint32_t)a.group, x0 + kRows);
-    const int i0 = (int)(x0 / (uint32_t)a.group), i1 = (int)((x1 - 1) / (uint32_t)a.group);
-    const int p0 = len - n;
-    Span r;
-    r.hi = a.causal ? min(max(p0 + i1 + 1, 0), keys) : keys;
-    r.lo = a.window ? (int)min(max((int64_t)p0 + i0 - a.window + 1, (int64_t)0), (int64_t)r.hi) : 0;
-    r.t0 = r.lo / kTile;
-    r.nt = max(1, (r.hi + kTile - 1) / kTile - r.t0);
-    return r;
-}
-
-// The i-th tile of rows of `tiles` in the line: from both ends in turn, as a causal sequence's first tiles see few keys and its
-// last many, and a CTA's share should not be all short items.
-__device__ __forceinline__ int tile_of(int i, int tiles) { return (i & 1) ? tiles - 1 - (i >> 1) : i >> 1; }
-
-// units of sequence s for one key head, by the whole warp, a sequence a lane (s < 0: none)
-__device__ __forceinline__ int64_t units_of(const AttendCall &a, int s)
-{
-    const int lane = threadIdx.x & 31;
-    Seq w{};
-    if (s >= 0 && s < a.b.sequences) w = seq_at(a, s);
-    int64_t u = 0;
-    const bool many = w.row_tiles > 2;
-    if (!many)
-        for (int rt = 0; rt < w.row_tiles; rt++) u += span_of(a, w.q.n, w.q.len, w.keys, rt).nt + kItem;
-    unsigned left = __ballot_sync(0xFFFFFFFFu, many);
-    while (left) {
-        const int src = __ffs(left) - 1;
-        left &= left - 1;
-        const int n = __shfl_sync(0xFFFFFFFFu, w.q.n, src), len = __shfl_sync(0xFFFFFFFFu, w.q.len, src);
-        const int keys = __shfl_sync(0xFFFFFFFFu, w.keys, src), tiles = __shfl_sync(0xFFFFFFFFu, w.row_tiles, src);
-        int64_t x = 0;
-        for (int rt = lane; rt < tiles; rt += 32) x += span_of(a, n, len, keys, rt).nt + kItem;
+    constexpr size_t kSlot = slot_floats<kRows, D>();
+    auto part = [&](int i) { return a.part + (2 * (size_t)(r0 + i) + (i == 0 ? 1 : 0)) * kSlot; };
+    float m = kNegInf, l = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < parts; i++) m = fmaxf(m, __ldcg(part(i) + kRows * D + r));
+    const float b = m == kNegInf ? 0.f : m;
+#pragma unroll 4
+    for (int i = 0; i < parts; i++) l += __ldcg(part(i) + kRows * D + kRows + r) * exp2_fast(__ldcg(part(i) + kRows * D + r) - b);
+    const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+    const int h = c.head * a.group + x - tok * a.group;
+    const int64_t row = c.w.q.first + tok;
+    uint16_t *p = a.out + row * a.ldo + (int64_t)h * D;
+#pragma unroll 1
+    for (int q = 0; q < D; q += 64) {
+        float o[64];
 #pragma unroll
-        for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
-        if (lane == src) u = x;
-    }
-    return u;
-}
-
-// An item of the line of work, where each has its tiles of keys and kItem in front of them, and which of its tiles lie in the
-// CTA's range [ua, ub): those [off, off + cnt).  Made, and moved on, to an item that has some; more(): there was one.
-struct Cursor {
-    Seq w;
-    Span k;
-    int64_t at, ua, ub;
-    int s, head, i, rt, off, cnt;      // i: place of the tile of rows rt
-    __device__ __forceinline__ void enter(const AttendCall &a)
-    {
-        rt = tile_of(i, w.row_tiles);
-        k = span_of(a, w.q.n, w.q.len, w.keys, rt);
-        off = (int)max(ua - at - kItem, (int64_t)0);
-        cnt = (int)(min(ub - at - kItem, (int64_t)k.nt)) - off;
-    }
-    __device__ __forceinline__ Cursor(const AttendCall &a, const Start &f, int64_t ua_, int64_t ub_) : at(f.at), ua(ua_), ub(ub_), s(f.s), head(f.head), i(f.i)
-    {
-        w = seq_at(a, s);
-        enter(a);
-        if (cnt <= 0) next(a);
-    }
-    __device__ __forceinline__ bool more() const { return at < ub; }
-    __device__ __forceinline__ void next(const AttendCall &a)
-    {
-        do {
-            at += k.nt + kItem;
-            if (at >= ub) return;
-            if (++i >= w.row_tiles) {
-                i = 0;
-                if (++head >= a.kv_heads) {
-                    head = 0;
-                    do w = seq_at(a, ++s);
-                    while (!w.row_tiles);
-                }
+        for (int k = 0; k < 64; k++) o[k] = 0.f;
+#pragma unroll 1
+        for (int i = 0; i < parts; i++) {
+            const float *s = part(i);
+            float4 v[16];
+#pragma unroll
+            for (int k = 0; k < 16; k++) v[k] = __ldcg((const float4 *)s + ((q / 4 + k) * kRows + r));
+            const float f = exp2_fast(__ldcg(s + kRows * D + r) - b);
+#pragma unroll
+            for (int k = 0; k < 16; k++) {
+                o[4 * k] += v[k].x * f;
+                o[4 * k + 1] += v[k].y * f;
+                o[4 * k + 2] += v[k].z * f;
+                o[4 * k + 3] += v[k].w * f;
             }
-            enter(a);
-        } while (cnt <= 0);
+        }
+#pragma unroll
+        for (int k = 0; k < 64; k += 8)
+            *(uint4 *)(p + q + k) = make_uint4(pack2(o[k] * inv, o[k + 1] * inv), pack2(o[k + 2] * inv, o[k + 3] * inv),
+                                               pack2(o[k + 4] * inv, o[k + 5] * inv), pack2(o[k + 6] * inv, o[k + 7] * inv));
     }
-    __device__ __forceinline__ int rows(const AttendCall &a) const { return min(w.q.n * a.group - rt * kRows, kRows); }
-};
+    if (a.lse) a.lse[row * a.q_heads + h] = l == 0.f ? kNegInf : (m + log2f(l)) * 0.69314718f;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_constant__ Args g)
@@ -250,9 +189,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
     uint64_t *empty = full + NS;
     uint64_t *raw = empty + NS;                       // a tile whose values are put right before it counts as full
     uint64_t *qfull = raw + 1, *sfull = qfull + 2, *sfree = sfull + 2, *pfull = sfree + 1, *pvdone = pfull + 4, *ofree = pvdone + 2, *done = ofree + 2;
-    int64_t *sums = (int64_t *)((uint8_t *)full + L::bars);
-    Start *found = (Start *)(sums + kWarps);
-    uint32_t *tmem_slot = (uint32_t *)(found + 1);
+    uint32_t *tmem_slot = (uint32_t *)((uint8_t *)full + L::bars);
+    volatile int *last = (volatile int *)(tmem_slot + 1);   // [2]: of each tile of rows
     const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -281,64 +219,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
     pdl_trigger();
     pdl_wait();
 
-    // ---------------------------------------------------------------------------------- this CTA's units
-    int64_t one = 0, mine = 0;
-    for (int s0 = 0; s0 < a.b.sequences; s0 += kThreads) {
-        one = units_of(a, s0 + (int)threadIdx.x) * a.kv_heads;
-        mine += one;
-    }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, d);
-    if (lane == 0) sums[warp] = mine;
-    __syncthreads();
-    int64_t U = 0;
-    for (int i = 0; i < kWarps; i++) U += sums[i];
-    const int64_t G = gridDim.x;
-    const int64_t ua = U * blockIdx.x / G, ub = U * (blockIdx.x + 1) / G;
-    const bool any = ua < ub;
-    if (any) {
-        int64_t before = 0;
-        for (int s0 = 0; s0 < a.b.sequences && before <= ua; s0 += kThreads) {
-            const int s = s0 + threadIdx.x;
-            const int64_t n = a.b.sequences <= kThreads ? one : units_of(a, s) * a.kv_heads;
-            int64_t incl = n;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int64_t o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-                if (lane >= d) incl += o;
-            }
-            __syncthreads();
-            if (lane == 31) sums[warp] = incl;
-            __syncthreads();
-            int64_t excl = before + incl - n;
-            for (int i = 0; i < kWarps; i++) {
-                if (i < warp) excl += sums[i];
-                before += sums[i];
-            }
-            // the warp that has the sequence looks for the tile of rows
-            const unsigned hit = __ballot_sync(0xFFFFFFFFu, n && excl <= ua && ua < excl + n);
-            if (hit) {
-                const int src = __ffs(hit) - 1;
-                const int64_t per = __shfl_sync(0xFFFFFFFFu, n, src) / a.kv_heads, in = ua - __shfl_sync(0xFFFFFFFFu, excl, src);
-                const int sq = s0 + 32 * warp + src, head = (int)(in / per);
-                int64_t at = in - (int64_t)head * per;  // units of the head in front of ours
-                const Seq w = seq_at(a, sq);
-                for (int r0 = 0; r0 < w.row_tiles; r0 += 32) {
-                    const int nt = r0 + lane < w.row_tiles ? span_of(a, w.q.n, w.q.len, w.keys, tile_of(r0 + lane, w.row_tiles)).nt + kItem : 0;
-                    int64_t x = nt;
-#pragma unroll
-                    for (int d = 1; d < 32; d <<= 1) {
-                        const int64_t o = __shfl_up_sync(0xFFFFFFFFu, x, d);
-                        if (lane >= d) x += o;
-                    }
-                    if (at < x && at >= x - nt) *found = Start{ua - (at - (x - nt)), sq, head, r0 + lane};
-                    const int64_t all = __shfl_sync(0xFFFFFFFFu, x, 31);
-                    if (at < all) break;
-                    at -= all;
-                }
-            }
-        }
-    }
+    // this CTA's range
+    const int range = blockIdx.x;
+    const bool any = range < a.plan->ranges;
+    const int64_t C = a.plan->per, ua = range * C, ub = min(ua + C, a.plan->units);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -350,7 +234,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (any && warp == kCopyWarp) {
         // ------------------------------------------------------------------------------ copies
-        Cursor c(a, *found, ua, ub);
+        Cur c;
+        c.set(a, a.begin[range], ua, ub);
         int n = 0;                        // tiles asked for: keys, values, keys, ...
         // values that are to be put right when they have landed
         bool fix = false;
@@ -420,7 +305,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         }
     } else if (any && warp == kScoreWarp) {
         // ------------------------------------------------------------------------------ products of queries and keys
-        Cursor c(a, *found, ua, ub);
+        Cur c;
+        c.set(a, a.begin[range], ua, ub);
         const bool leader = elect_one();
         constexpr uint32_t id = idesc_bf16(128, 128);
         const uint32_t q0 = saddr(qs), r0 = saddr(ring);
@@ -458,7 +344,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         if (!mbar_wait_short(&done[0], 0) && lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
     } else if (any && warp == kValueWarp) {
         // ------------------------------------------------------------------------------ products of probabilities and values
-        Cursor c(a, *found, ua, ub);
+        Cur c;
+        c.set(a, a.begin[range], ua, ub);
         const bool leader = elect_one();
         constexpr uint32_t id = idesc_bf16(128, D) | 1u << 16;  // the second operand's columns run along memory
         const uint32_t r0 = saddr(ring);
@@ -509,7 +396,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         // ------------------------------------------------------------------------------ softmax
         const int t = warp >> 2, row = threadIdx.x & 127;
         const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        Cursor c(a, *found, ua, ub);
+        Cur c;
+        c.set(a, a.begin[range], ua, ub);
         int steps = 0;                  // scores seen, also products of P and V asked for
         auto arrive = [&](uint64_t *b) {
             __syncwarp();
@@ -519,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
             if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait_short(b, parity));
         };
         // an item's queries of this tile, 16 threads a row
-        auto queries = [&](const Cursor &q) {
+        auto queries = [&](const Cur &q) {
             const int x0 = q.rt * kRows + 128 * t, xn = q.w.q.n * a.group;
             constexpr int kC = D / 8, kStep = 128 / kC;     // 16-byte pieces of a row, rows of a round
             const int ch = row % kC;
@@ -553,11 +441,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
             arrive(&qfull[t]);
         };
         if (c.more() && c.rows(a) > 128 * t) queries(c);
-        Cut cut{0, U, 0, 0, 0, 0};
         while (c.more()) {
             const int nt = c.cnt;
-            const bool begins = c.off == 0, ends = c.off + nt == c.k.nt;
-            Cursor nx = c;
+            const bool begins = c.begins(), ends = c.ends();
+            Cur nx = c;
             nx.next(a);
             if (c.rows(a) <= 128 * t) {   // the item has no such tile
                 c = nx;
@@ -676,91 +563,50 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                 if (in && a.lse) a.lse[r * a.q_heads + h] = l == 0.f ? kNegInf : (m + log2f(l)) * 0.69314718f;
             } else {
                 // pieces of four columns of all rows: a warp's stores are 512 bytes in a row
-                float *o = a.part + (2 * (size_t)blockIdx.x + (begins ? 1 : 0)) * slot_floats<kRows, D>();
+                float *o = a.part + (2 * (size_t)range + (begins ? 1 : 0)) * slot_floats<kRows, D>();
                 const int r = 128 * t + row;
 #pragma unroll 1
                 for (int q = 0; q < D / 32; q++) {
                     uint32_t v[32];
                     tmem_ld32(t_lane + L::o + t * D + 32 * q, v);
                     tmem_wait_ld();
+                    if (in) {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) *(uint4 *)(o + ((32 * q + i) / 4 * kRows + r) * 4) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                        for (int i = 0; i < 32; i += 4) __stcg((uint4 *)(o + ((32 * q + i) / 4 * kRows + r) * 4), make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+                    }
                 }
-                o[kRows * D + r] = m;
-                o[kRows * D + kRows + r] = l;
-                if (begins) {
-                    cut.valid = 1;
-                    cut.seq = c.s;
-                    cut.item = c.head;
-                    cut.pad = c.rt;
-                    cut.end = c.at + kItem + c.k.nt;
+                if (in) {
+                    __stcg(o + kRows * D + r, m);
+                    __stcg(o + kRows * D + kRows + r, l);
                 }
+                tc_fence_before();
+                arrive(&ofree[t]);
+                // the part that comes last joins them all
+                const int r0 = c.first_range(C), parts = c.last_range(C) - r0 + 1;
+                __threadfence();
+                tile_sync(t);
+                if (row == 0) last[t] = atomicAdd(&a.arrived[2 * r0 + t], 1) == parts - 1;
+                tile_sync(t);
+                if (last[t] && in) {
+                    __threadfence();
+                    join_row<D>(a, c, r0, parts, r, tok, (int)x);
+                }
+                c = nx;
+                continue;
             }
             tc_fence_before();
             arrive(&ofree[t]);
             c = nx;
         }
-        if (threadIdx.x == 0) a.cuts[blockIdx.x] = cut;
         if (!ok && lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
     }
     }
-    if (!any && threadIdx.x == 0) a.cuts[blockIdx.x] = Cut{0, U, 0, 0, 0, 0};
     tc_fence_before();
     __syncthreads();
     if (warp == kScoreWarp) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
     }
-}
-
-// joins the sums of the item that begins in CTA blockIdx.x's range and goes on behind it, 16 columns a block
-template <int D>
-__global__ void __launch_bounds__(kRows) join_tc_kernel(const AttendCall a)
-{
-    pdl_trigger();
-    pdl_wait();
-    const Cut cut = a.cuts[blockIdx.x];
-    if (!cut.valid) return;
-    const int64_t G = gridDim.x;
-    const Seq w = seq_at(a, cut.seq);
-    constexpr size_t kSlot = slot_floats<kRows, D>();
-    const int r = threadIdx.x, col = blockIdx.y * 16;
-    const int64_t x = (int64_t)cut.pad * kRows + r;
-    if (x >= (int64_t)w.q.n * a.group) return;
-    auto each = [&](auto f) {
-        f(a.part + (2 * (size_t)blockIdx.x + 1) * kSlot);
-        for (int64_t c = blockIdx.x + 1; c < G; c++) {
-            const int64_t ua = cut.units * c / G, ub = cut.units * (c + 1) / G;
-            if (ua >= cut.end) break;
-            if (ua < ub) f(a.part + 2 * (size_t)c * kSlot);
-        }
-    };
-    float m = kNegInf, l = 0.f, o[16];
-#pragma unroll
-    for (int i = 0; i < 16; i++) o[i] = 0.f;
-    each([&](const float *p) { m = fmaxf(m, p[kRows * D + r]); });
-    const float b = m == kNegInf ? 0.f : m;
-    each([&](const float *p) {
-        const float f = exp2_fast(p[kRows * D + r] - b);
-        l += p[kRows * D + kRows + r] * f;
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-            const float4 v = *(const float4 *)(p + ((col + i) / 4 * kRows + r) * 4);
-            o[i] += v.x * f;
-            o[i + 1] += v.y * f;
-            o[i + 2] += v.z * f;
-            o[i + 3] += v.w * f;
-        }
-    });
-    const int tok = (int)x / a.group, h = cut.item * a.group + (int)x - tok * a.group;
-    const int64_t row = w.q.first + tok;
-    const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
-    uint16_t *p = a.out + row * a.ldo + (int64_t)h * D + col;
-#pragma unroll
-    for (int i = 0; i < 16; i += 8)
-        *(uint4 *)(p + i) = make_uint4(pack2(o[i] * inv, o[i + 1] * inv), pack2(o[i + 2] * inv, o[i + 3] * inv), pack2(o[i + 4] * inv, o[i + 5] * inv),
-                                       pack2(o[i + 6] * inv, o[i + 7] * inv));
-    if (a.lse && blockIdx.y == 0) a.lse[row * a.q_heads + h] = l == 0.f ? kNegInf : (m + log2f(l)) * 0.69314718f;
 }
 
 template <int D>
@@ -777,8 +623,8 @@ cudaError_t launch_tc(const uw_kv_cache *c, const AttendCall &call, int ctas, cu
     g.q_xor = call.scale2 < 0.f ? 0x80008000u : 0u;
     g.q_and = call.scale2 == 0.f ? 0u : 0xFFFFFFFFu;
     g.c.scale2 = call.scale2 == 0.f ? 1.f : std::fabs(call.scale2);
-    if ((e = launch_dependent(attend_tc_kernel<D>, dim3((unsigned)ctas), kThreads, Layout<D>::smem, 0, st, g)) != cudaSuccess) return e;
-    return launch_dependent(join_tc_kernel<D>, dim3((unsigned)ctas, D / 16), kRows, 0, 0, st, g.c);
+    if ((e = (cudaError_t)launch_attend_plan256(g.c, ctas, st)) != cudaSuccess) return e;
+    return launch_dependent(attend_tc_kernel<D>, dim3((unsigned)ctas), kThreads, Layout<D>::smem, 0, st, g);
 }
 
 }  // namespace

@@ -150,6 +150,16 @@ def test_attend_long_split():
         check_attend(c, q, out, lse, new)
 
 
+@pytest.mark.parametrize("S,most,H", [(64, 500, 8), (200, 900, 4), (500, 40, 8), (150, 3000, 2)])
+def test_attend_many_sequences(S, most, H):
+    """More ranges of work than CTAs, some of them shorter than a CTA's copies reach ahead."""
+    new, past = [1 + i % 2 for i in range(S)], [(i * 7919) % most for i in range(S)]
+    c = batch_of(new, past, 16, H=H, D=64)
+    q = torch.randn(sum(new), 4 * H, 64, generator=c["g"]).to(BF16).cuda()
+    out, lse = attend(c, q, 4 * H)
+    check_attend(c, q, out, lse, new)
+
+
 def test_attend_peaked_scores():
     """Scores up to hundreds: the running maximum moves, probabilities underflow."""
     new, past = [5, 260], [900, 300]
