@@ -502,34 +502,70 @@ def token_logprobs(logits, rows: int, vocab: int, logprob=None, targets=None, en
                                    n_top, _ptr(top_ids), _ptr(top_logprobs), _stream(stream)), "uw_token_logprobs")
 
 
-def _at(what: str, t, *dtypes) -> int:
-    """_ptr of a tensor of one of these types ("int32", ...), in device memory and with its last dimension dense; addresses pass."""
-    if t is None:
-        return 0
-    if isinstance(t, int):
-        return t
+_KINDS = {}  # names of element types -> torch's types
+
+
+def _kinds():
     import torch
-    if not any(t.dtype == getattr(torch, d) for d in dtypes):
-        raise ValueError(f"{what} is {t.dtype}, the call takes {' or '.join(dtypes)}")
+    _KINDS.update(f32={torch.float32}, i32={torch.int32}, bf16={torch.bfloat16, torch.int16, torch.uint16}, bits={torch.int32, torch.uint32},
+                  any={torch.float32, torch.bfloat16, torch.int16, torch.uint16})
+    return _KINDS
+
+
+_KIND_OF = {OUT_F32: "f32", OUT_BF16: "bf16"}  # of a call's dtype; another one is the library's to refuse
+
+
+def _wrong(what, t, kind):
+    if t.dtype not in _KINDS[kind]:
+        raise ValueError(f"{what} is {t.dtype}, the call takes {' or '.join(sorted(str(d) for d in _KINDS[kind]))}")
     if not t.is_cuda:
         raise ValueError(f"{what} is not in device memory")
-    if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{what}: the last dimension is not dense")
+    raise ValueError(f"{what}: its last dimension is not dense, or its shape is another than the call's")
+
+
+def _at(what: str, t, kind: str) -> int:
+    """_ptr of a tensor of this kind in device memory; addresses pass."""
+    if t is None:
+        return 0
+    if t.__class__ is int:
+        return t
+    if t.dtype not in (_KINDS or _kinds())[kind] or not t.is_cuda:
+        _wrong(what, t, kind)
     return t.data_ptr()
 
 
-_BF16 = ("bfloat16", "int16", "uint16")
+def _of_rows(what: str, t, rows: int, kind: str) -> int:
+    """_at of a dense tensor of a number for each row."""
+    if t is None:
+        return 0
+    if t.__class__ is int:
+        return t
+    if t.dtype not in (_KINDS or _kinds())[kind] or not t.is_cuda or t.dim() != 1 or len(t) < rows or not t.is_contiguous():
+        _wrong(what, t, kind)
+    return t.data_ptr()
 
 
-def _heads(what: str, t, rows: int, dim: int, dtypes):
-    """Address, elements from row to row and heads of a tensor [rows, heads, dim] or [rows, heads * dim]."""
-    if t is None or isinstance(t, int):
-        return t or 0, 0, None
-    p = _at(what, t, *dtypes)
-    width = t.shape[-1] * (t.shape[1] if t.dim() == 3 else 1)
-    if t.dim() not in (2, 3) or t.shape[0] < rows or width % dim or (t.dim() == 3 and (t.shape[2] != dim or (t.stride(1) != dim and t.shape[1] > 1))):
+def _heads(what: str, t, rows: int, dim: int, kind: str):
+    """Address, elements from row to row (0: dense) and heads of a tensor [rows, heads, dim] or [rows, heads * dim]."""
+    if t is None:
+        return 0, 0, 0
+    if t.__class__ is int:
+        return t, 0, 0
+    if t.dtype not in (_KINDS or _kinds())[kind] or not t.is_cuda:
+        _wrong(what, t, kind)
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 3:
+        n, heads, d = shape
+        ok = d == dim and stride[2] == 1 and (stride[1] == dim or heads == 1)
+    elif len(shape) == 2:
+        n, width = shape
+        heads = width // dim
+        ok = heads * dim == width and stride[1] == 1
+    else:
+        n, heads, ok = 0, 0, False
+    if not ok or n < rows:
         raise ValueError(f"{what} must be [rows, heads, {dim}] or [rows, heads * {dim}], a row's heads dense")
-    return p, t.stride(0) if t.shape[0] > 1 else 0, width // dim
+    return t.data_ptr(), stride[0] if n > 1 else 0, heads
 
 
 class Rotary:
@@ -558,11 +594,13 @@ class KVBatch:
     holds lengths[s] tokens with them, in the pages pages[s] (a tensor [sequences, max_pages])."""
 
     def __init__(self, starts, lengths, pages):
+        if any(t.shape[-1] > 1 and t.stride(-1) != 1 for t in (starts, lengths, pages)):
+            raise ValueError("starts, lengths and rows of pages must be dense")
         if pages.dim() != 2 or lengths.dim() != 1 or starts.dim() != 1 or pages.shape[0] != lengths.shape[0] or starts.shape[0] != lengths.shape[0] + 1:
             raise ValueError("starts [sequences + 1], lengths [sequences], pages [sequences, max_pages]")
         self._keep = (starts, lengths, pages)
         self.sequences = lengths.shape[0]
-        self.desc = KVBatchDesc(self.sequences, _at("starts", starts, "int32"), _at("lengths", lengths, "int32"), _at("pages", pages, "int32"),
+        self.desc = KVBatchDesc(self.sequences, _at("starts", starts, "i32"), _at("lengths", lengths, "i32"), _at("pages", pages, "i32"),
                                 pages.stride(0) if self.sequences > 1 else 0, pages.shape[1])
         self._ref = ctypes.byref(self.desc)
 
@@ -573,11 +611,12 @@ class KVCache:
 
     def __init__(self, k, v):
         self._h = None
-        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride():
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.stride(3) != 1:
             raise ValueError("k and v must be [pages, page_size, kv_heads, head_dim] with the same strides")
         self._keep = (k, v)
         self.pages, self.page_size, self.kv_heads, self.head_dim = k.shape
-        d = KVDesc(_at("k", k, *_BF16), _at("v", v, *_BF16), self.pages, k.stride(0), k.stride(1), k.stride(2), self.page_size, self.kv_heads,
+        self._scale = self.head_dim ** -0.5 if self.head_dim else 0.0
+        d = KVDesc(_at("k", k, "bf16"), _at("v", v, "bf16"), self.pages, k.stride(0), k.stride(1), k.stride(2), self.page_size, self.kv_heads,
                    self.head_dim)
         h = ctypes.c_void_p()
         _check(lib().uw_kv_create(ctypes.byref(d), ctypes.byref(h)), "uw_kv_create")
@@ -603,16 +642,18 @@ class KVCache:
         """uw_kv_append: q, k, v of `dtype`, tensors [rows, heads, head_dim] (their strides and heads are taken from them) or
         addresses; q_out bf16."""
         D = self.head_dim
-        src = {OUT_F32: ("float32",), OUT_BF16: _BF16}.get(dtype, ("float32",) + _BF16)
-        pq, sq, hq = _heads("q", q, rows, D, src)
-        po, so, ho = _heads("q_out", q_out, rows, D, _BF16)
-        pk, sk, hk = _heads("k", k, rows, D, src)
-        pv, sv, hv = _heads("v", v, rows, D, src)
-        q_heads = q_heads or hq or ho or 0
-        if any(h not in (None, q_heads) for h in (hq, ho)) or any(h not in (None, self.kv_heads) for h in (hk, hv)):
+        kind = _KIND_OF.get(dtype, "any")
+        pq, sq, hq = _heads("q", q, rows, D, kind)
+        po, so, ho = _heads("q_out", q_out, rows, D, "bf16")
+        pk, sk, hk = _heads("k", k, rows, D, kind)
+        pv, sv, hv = _heads("v", v, rows, D, kind)
+        q_heads = q_heads or hq or ho
+        if (hq and hq != q_heads) or (ho and ho != q_heads) or (hk and hk != self.kv_heads) or (hv and hv != self.kv_heads):
             raise ValueError(f"heads: q {hq}, q_out {ho} of {q_heads}, k {hk}, v {hv} of {self.kv_heads}")
-        _check(lib().uw_kv_append(self._h, batch._ref, rotary._ref if rotary is not None else None, rows, dtype, pq, ldq or sq, q_heads, pk, ldk or sk, pv,
-                                  ldv or sv, _at("positions", positions, "int32"), po, ldq_out or so, _stream(stream)), "uw_kv_append")
+        s = lib().uw_kv_append(self._h, batch._ref, rotary._ref if rotary is not None else None, rows, dtype, pq, ldq or sq, q_heads, pk, ldk or sk, pv,
+                               ldv or sv, _of_rows("positions", positions, rows, "i32"), po, ldq_out or so, _stream(stream))
+        if s:
+            _check(s, "uw_kv_append")
 
     def workspace_size(self, batch, rows: int, q_heads: int) -> int:
         n = ctypes.c_size_t(0)
@@ -622,15 +663,17 @@ class KVCache:
     def attend(self, batch, rows: int, q, out, q_heads: int = 0, scale=None, causal: bool = True, window: int = 0, lse=None, workspace=None,
                ws_bytes: int = 0, ldq: int = 0, ldo: int = 0, stream=None):
         """uw_kv_attend: q and out bf16 [rows, q_heads, head_dim] (or addresses, with q_heads); scale None: head_dim ** -0.5."""
-        pq, sq, hq = _heads("q", q, rows, self.head_dim, _BF16)
-        po, so, ho = _heads("out", out, rows, self.head_dim, _BF16)
-        q_heads = q_heads or hq or ho or 0
-        if any(h not in (None, q_heads) for h in (hq, ho)):
+        pq, sq, hq = _heads("q", q, rows, self.head_dim, "bf16")
+        po, so, ho = _heads("out", out, rows, self.head_dim, "bf16")
+        q_heads = q_heads or hq or ho
+        if (hq and hq != q_heads) or (ho and ho != q_heads):
             raise ValueError(f"heads: q {hq}, out {ho} of {q_heads}")
-        if scale is None:
-            scale = self.head_dim ** -0.5
-        _check(lib().uw_kv_attend(self._h, batch._ref, rows, pq, ldq or sq, q_heads, scale, int(causal), window, po, ldo or so, _at("lse", lse, "float32"),
-                                  _ptr(workspace), ws_bytes, _stream(stream)), "uw_kv_attend")
+        if lse is not None and lse.__class__ is not int and (not lse.is_contiguous() or lse.numel() < rows * q_heads):
+            raise ValueError("lse must be dense [rows, q_heads]")
+        s = lib().uw_kv_attend(self._h, batch._ref, rows, pq, ldq or sq, q_heads, self._scale if scale is None else scale, causal, window, po, ldo or so,
+                               _at("lse", lse, "f32"), _ptr(workspace), ws_bytes, _stream(stream))
+        if s:
+            _check(s, "uw_kv_attend")
 
     def check(self, stream=None):
         _check(lib().uw_kv_check(self._h, _stream(stream)), "uw_kv_check")
@@ -643,40 +686,39 @@ def edit_logits(logits, rows: int, vocab: int, out, tokens=None, lengths=None, p
     prompt_lengths int32 [rows], penalties fp32 [rows], bias_ids int32 and bias fp32 [rows, max_bias], allowed int32 words
     [masks, words].  out_dtype None: dtype."""
     out_dtype = dtype if out_dtype is None else out_dtype
-    kind = {OUT_F32: ("float32",), OUT_BF16: _BF16}
-    p, po = (_at(w, t, *kind.get(d, ("float32",) + _BF16)) for w, t, d in (("logits", logits, dtype), ("out", out, out_dtype)))
-
-    def stride(what, t, given, width):
-        if given or isinstance(t, int) or t is None:
-            return given
-        if t.dim() != 2 or t.shape[0] < rows or t.shape[1] < width:
-            raise ValueError(f"{what} must be [rows, {width} or more]")
-        return t.stride(0) if rows > 1 else 0
-
-    def of_rows(what, t, *dtypes):
-        a = _at(what, t, *dtypes)
-        if t is not None and not isinstance(t, int) and (t.dim() != 1 or t.shape[0] < rows):
-            raise ValueError(f"{what} must be [rows]")
-        return a
-
-    d = LogitEditsDesc()
-    if tokens is not None and not isinstance(tokens, int) and tokens.dim() == 2 and tokens.shape[1] == 0:
-        tokens = repetition = frequency = presence = None  # no history: no penalties
-    d.tokens = _at("tokens", tokens, "int32")
+    p, po = _at("logits", logits, _KIND_OF.get(dtype, "any")), _at("out", out, _KIND_OF.get(out_dtype, "any"))
+    ld, ld_out = ld or _pitch("logits", logits, rows, vocab), ld_out or _pitch("out", out, rows, vocab)
+    max_tokens = max_bias = ld_tokens = ld_allowed = masks = 0
+    pt = _at("tokens", tokens, "i32")
     if tokens is not None:
-        d.ld_tokens, d.max_tokens = stride("tokens", tokens, 0, 0), tokens.shape[1]
-    d.lengths, d.prompt_lengths = of_rows("lengths", lengths, "int32"), of_rows("prompt_lengths", prompt_lengths, "int32")
-    d.repetition, d.frequency, d.presence = (of_rows(w, t, "float32") for w, t in (("repetition", repetition), ("frequency", frequency), ("presence", presence)))
-    d.bias_ids, d.bias, d.bias_lengths = _at("bias_ids", bias_ids, "int32"), _at("bias", bias, "float32"), of_rows("bias_lengths", bias_lengths, "int32")
-    if bias_ids is not None and bias is not None:
-        if bias_ids.shape != bias.shape or bias.dim() != 2 or bias.shape[0] < rows or not bias.is_contiguous() or not bias_ids.is_contiguous():
+        ld_tokens, max_tokens = _pitch("tokens", tokens, rows, 0), tokens.shape[1]
+        if max_tokens == 0:  # no history: no penalties
+            pt, repetition, frequency, presence = 0, None, None, None
+    pi, pb = _at("bias_ids", bias_ids, "i32"), _at("bias", bias, "f32")
+    if bias is not None and bias_ids is not None:
+        if bias_ids.shape != bias.shape or bias.dim() != 2 or len(bias) < rows or not bias.is_contiguous() or not bias_ids.is_contiguous():
             raise ValueError("bias_ids and bias must be contiguous [rows, max_bias]")
-        d.max_bias = bias.shape[1]
-    d.allowed = _at("allowed", allowed, "int32", "uint32")
+        max_bias = bias.shape[1]
+    pa = _at("allowed", allowed, "bits")
     if allowed is not None:
-        if allowed.dim() != 2 or allowed.shape[1] * 32 < vocab:
+        if allowed.dim() != 2 or allowed.shape[1] * 32 < vocab or allowed.stride(1) != 1:
             raise ValueError("allowed must be [masks, ceil(vocab / 32)]")
-        d.ld_allowed, d.mask_count = allowed.stride(0) if allowed.shape[0] > 1 else 0, allowed.shape[0]
-    d.mask_rows = of_rows("mask_rows", mask_rows, "int32")
-    _check(lib().uw_edit_logits(ctypes.byref(d), p, dtype, rows, vocab, stride("logits", logits, ld, vocab), po, out_dtype,
-                                stride("out", out, ld_out, vocab), _stream(stream)), "uw_edit_logits")
+        masks = len(allowed)
+        ld_allowed = allowed.stride(0) if masks > 1 else 0
+    d = LogitEditsDesc(pt, ld_tokens, max_tokens, _of_rows("lengths", lengths, rows, "i32"), _of_rows("prompt_lengths", prompt_lengths, rows, "i32"),
+                       _of_rows("repetition", repetition, rows, "f32"), _of_rows("frequency", frequency, rows, "f32"),
+                       _of_rows("presence", presence, rows, "f32"), pi, pb, _of_rows("bias_lengths", bias_lengths, rows, "i32"), max_bias, pa, ld_allowed,
+                       masks, _of_rows("mask_rows", mask_rows, rows, "i32"))
+    s = lib().uw_edit_logits(ctypes.byref(d), p, dtype, rows, vocab, ld, po, out_dtype, ld_out, _stream(stream))
+    if s:
+        _check(s, "uw_edit_logits")
+
+
+def _pitch(what: str, t, rows: int, width: int) -> int:
+    """Elements from row to row (0: dense) of a tensor [rows, width or more]; 0 for an address."""
+    if t is None or t.__class__ is int:
+        return 0
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] < rows or shape[1] < width or (stride[1] != 1 and shape[1] > 1):
+        raise ValueError(f"{what} must be [rows, {width} or more], its rows dense")
+    return stride[0] if rows > 1 else 0

@@ -2,9 +2,9 @@
 //
 // An item is a tile of R query rows of a sequence (its new tokens' query heads that share a key head) against one key head;
 // a unit is one of its tiles of 128 keys.  The work is a line: item after item - sequence, key head, tile of rows - each with
-// kItem units of its own, for what it costs beside its keys, and then its tiles.  The line is cut into ranges of C units
-// wherever these end, so that all have as much to do whatever the lengths are.  A first, small kernel measures the line,
-// chooses C and writes down where each range begins.
+// kItem units of its own, for what it costs beside its keys, and then its tiles.  The line is cut into a range of as many units
+// for each CTA wherever these end, so that all have as much to do whatever the lengths are.  A first, small kernel measures
+// the line and writes down where each range begins.
 // An item that lies in one range is stored by the CTA that has the range; of an item that is cut each CTA leaves its sums (the running
 // maximum, the sum of powers, the unnormalised output) in the workspace, and the one that comes last joins them, in the line's
 // order, so that the result does not depend on which that is.
@@ -42,14 +42,13 @@ struct AttendCall {
 // What the first kernel finds out.
 struct PlanHead {
     int64_t units, per;               // of the line, of a range
-    int ranges, ticket;               // ticket: ranges taken beyond the first of each CTA
+    int ranges;
 };
 
 // where a range begins: the item that holds its first unit, and where that begins in the line
 struct Start {
     int64_t at;
     int s, head, i;                   // i: place of the tile of rows
-    int pad;
 };
 
 constexpr int kKeys = 128;            // keys of a tile
@@ -154,9 +153,6 @@ struct Cursor {
 // the item that goes on from the range before, 2 r + 1 for the one that goes on in the next.
 template <int R, int D>
 __host__ __device__ constexpr size_t slot_floats() { return (size_t)R * (D + 2); }
-
-// The bounds of a call's work that the host knows: ranges at most, and the bytes of what the first kernel writes
-constexpr int kMaxRangesPerCta = 6;
 
 namespace dev {
 

@@ -31,7 +31,6 @@ using namespace dev;
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kRows = 16, kStep = 16;
 constexpr int kItem16 = 1;        // what an item costs beside its tiles of keys: the warps' sums joined, its queries
-constexpr int kLeast16 = 8;       // units of a range, where there is work for more than one range a CTA
 static_assert(kStep * kWarps == kKeys, "a tile is a step of every warp");
 constexpr int kStages = 3;
 constexpr float kNegInf = -INFINITY;
@@ -93,12 +92,6 @@ using Cur = Cursor<kRows, kItem16>;
 __device__ __forceinline__ int key0_of(const Cur &c, int j, int warp) { return (c.k.t0 + c.off + j) * kKeys + warp * kStep; }
 // some row of the item sees one of the warp's 16 keys
 __device__ __forceinline__ bool active(const Cur &c, int key0) { return key0 < c.k.hi && key0 + kStep > c.k.lo; }
-
-// the next range that the CTA has taken
-struct Ticket {
-    int tag, range;      // tag: which of the CTA's ranges it is
-    Start at;
-};
 
 // Joins the parts of an item of xn rows that was cut: those of ranges r0 .. r0 + parts - 1, by the whole CTA.  Four columns of
 // a row a thread, and where threads are left, a lot of the parts each; eight parts on their way at a time.
@@ -193,7 +186,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend16_kernel(const __grid_cons
     using L = Layout<D>;
     constexpr int KS = D / 16;        // steps of the first product, and pairs of column tiles of the second
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    __shared__ Ticket tickets[2];
     __shared__ float2 red[kThreads];
     __shared__ int last;
     const AttendCall &a = g.c;
@@ -206,76 +198,31 @@ __global__ void __launch_bounds__(kThreads, 1) attend16_kernel(const __grid_cons
         for (int i = 0; i < kStages; i++) mbar_init(&full[warp * kStages + i], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (threadIdx.x < 2) tickets[threadIdx.x].tag = 0;
     pdl_trigger();
     pdl_wait();
-    const int N = a.plan->ranges;
+    const int range = blockIdx.x;
+    if (range >= a.plan->ranges) return;
     const int64_t C = a.plan->per, U = a.plan->units;
-    if ((int)blockIdx.x >= N) return;
     __syncthreads();
 
-    // ---------------------------------------------------------------------------------- ranges and cursors
-    // The CTA's first range is its own number; further ones are taken from a counter, a range ahead: thread 0 asks at a range's
-    // first tile, looks where the range begins at the second and tells the others at the third, so that it never waits.
-    int got = 0, pump = 0, next_range = N;      // thread 0's
-    Start next_at{};
-    auto pump_ticket = [&](int mine) {          // mine: which of the CTA's ranges is at work (1, 2, ...)
-        if (threadIdx.x) return;
-        if (pump == 0) {
-            got = (int)gridDim.x < N ? atomicAdd(&a.plan->ticket, 1) : N;
-            pump = 1;
-        } else if (pump == 1) {
-            next_range = min((int64_t)gridDim.x + got, (int64_t)N);
-            if (next_range < N) next_at = a.begin[next_range];
-            pump = 2;
-        } else if (pump == 2) {
-            Ticket &t = tickets[(mine + 1) & 1];
-            t.range = next_range;
-            t.at = next_at;
-            __threadfence_block();
-            *(volatile int *)&t.tag = mine + 1;
-            pump = 3;
-        }
-    };
-    int range = blockIdx.x, mine = 1;
-    Cur use, ld;
+    // ---------------------------------------------------------------------------------- cursors
+    Cur use, ld;                     // of the step at work, of the copies
     use.set(a, a.begin[range], range * C, min((range + 1) * C, U));
     ld = use;
-    int ld_j = 0, ld_mine = 1;
+    int ld_j = 0;
     uint32_t asked = 0, used = 0;    // steps copied, steps consumed
     bool ok = true;
     const uint32_t my_ring = saddr(ring) + warp * kStages * L::stage;
     uint64_t *bars = full + warp * kStages;
 
-    // moves ld to the warp's next step; false: there is none
-    auto seek = [&]() -> bool {
-        for (;;) {
-            if (ld.more()) {
-                for (; ld_j < ld.cnt; ld_j++)
-                    if (active(ld, key0_of(ld, ld_j, warp))) return true;
-                ld_j = 0;
-                ld.next(a);
-                continue;
-            }
-            // the CTA's next range, once thread 0 has told of it; never more than a range ahead of the one at work
-            if (ld_mine != mine) return false;
-            const volatile Ticket &t = tickets[(ld_mine + 1) & 1];
-            if (__shfl_sync(0xFFFFFFFFu, t.tag, 0) != ld_mine + 1) return false;
-            __threadfence_block();
-            const int r = t.range;
-            if (r >= N) return false;
-            Start f;
-            f.at = t.at.at;
-            f.s = t.at.s;
-            f.head = t.at.head;
-            f.i = t.at.i;
-            ld_mine++;
-            ld.set(a, f, r * C, min((r + 1) * C, U));
-        }
-    };
-    // asks for the warp's next step, if there is one that it can know of
+    // asks for the warp's next step, if there is one
     auto ask = [&]() -> bool {
-        if (!ok || !seek()) return false;
+        if (!ok) return false;
+        for (;; ld.next(a), ld_j = 0) {
+            if (!ld.more()) return false;
+            while (ld_j < ld.cnt && !active(ld, key0_of(ld, ld_j, warp))) ld_j++;
+            if (ld_j < ld.cnt) break;
+        }
         const uint32_t st = asked % kStages;
         if (lane == 0) mbar_expect_tx(&bars[st], L::stage);
         __syncwarp();
@@ -297,7 +244,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend16_kernel(const __grid_cons
 
     // ---------------------------------------------------------------------------------- items
     const int gq = lane >> 2, tq = lane & 3;
-    for (;;) {
     for (; use.more(); use.next(a)) {
         const int seg = use.cnt;
         const bool begins = use.begins(), ends = use.ends();
@@ -326,7 +272,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend16_kernel(const __grid_cons
         for (int n = 0; n < 2 * KS; n++) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
 
         for (int k = 0; k < seg; k++) {
-            pump_ticket(mine);
             const int key0 = key0_of(use, k, warp);
             if (active(use, key0)) {
                 while (asked < used + kStages && ask()) {}
@@ -500,21 +445,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend16_kernel(const __grid_cons
             }
         }
     }
-    // the CTA's next range
-    while (threadIdx.x == 0 && pump < 3) pump_ticket(mine);
-    __syncthreads();
-    const Ticket &nt = tickets[(mine + 1) & 1];
-    if (nt.range >= N) break;
-    range = nt.range;
-    mine++;
-    pump = 0;
-    use.set(a, nt.at, range * C, min((range + 1) * C, U));
-    if (ld_mine < mine) {   // it had not heard of this range: every step before it has been asked for and used
-        ld = use;
-        ld_j = 0;
-        ld_mine = mine;
-    }
-    }
     if (!ok) {
         // what was asked for lands before the block ends
         if (lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
@@ -567,20 +497,15 @@ __device__ __forceinline__ int last_at(int lo, int hi, T x, F at)
     return lo;
 }
 
-__device__ __forceinline__ int64_t range_units(int64_t U, int ctas, int most, int least)
-{
-    const int64_t share = (U + ctas - 1) / ctas;
-    return max(max((share + most - 1) / most, min(share, (int64_t)least)), (int64_t)1);
-}
-
-// The line's length, the ranges and where they begin; one CTA.  ctas: of the next kernel, each of which gets up to `most` ranges of
-// at least `least` units, one where there is no more work.  This form holds every tile of rows in shared memory, up to
-// kSmallSeqs sequences and kSmallTiles tiles: one tile a thread, a sum over the threads, two searches for each range (3 us
-// where the form below takes 12, for the 128 tiles of 8191 tokens).
+// The line's length, the ranges - one for each of the next kernel's CTAs - and where they begin; one CTA.  This form holds every
+// tile of rows in shared memory, up to kSmallSeqs sequences and kSmallTiles tiles: a tile or a few a thread, a sum over the
+// threads, two searches for each range (3 us where the form below takes 12, for the 128 tiles of 8191 tokens).
+// Ranges taken in turn by CTAs that are done, up to six for each, were no faster: 64 sequences of up to 8191 tokens took 213 us
+// against 200, one token over 131000 122 against 95, as each range ends with sums to be joined.
 constexpr int kSmallSeqs = 1024, kSmallTiles = 4096;
 
 template <int R, int kItem>
-__global__ void __launch_bounds__(kPlanThreads) plan_small_kernel(const AttendCall a, int ctas, int most, int least)
+__global__ void __launch_bounds__(kPlanThreads) plan_small_kernel(const AttendCall a, int ctas)
 {
     __shared__ int64_t pre[kSmallTiles + 1];       // of a key head's line, in front of each tile of rows
     __shared__ int n_s[kSmallSeqs], len_s[kSmallSeqs], tile0[kSmallSeqs + 1];
@@ -619,9 +544,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_small_kernel(const AttendCa
     const int64_t front = scan_before(cost, sums, P);
     for (int f = f0; f < f1; f++) pre[f + 1] += front;
     __syncthreads();
-    const int64_t U = P * a.kv_heads, C = range_units(U, ctas, most, least);
+    const int64_t U = P * a.kv_heads, C = max((U + ctas - 1) / ctas, (int64_t)1);
     const int N = (int)((U + C - 1) / C);
-    if (tid == 0) *a.plan = PlanHead{U, C, N, 0};
+    if (tid == 0) *a.plan = PlanHead{U, C, N};
     for (int i = tid; i < 2 * N; i += kPlanThreads) a.arrived[i] = 0;
     for (int r = tid; r < N; r += kPlanThreads) {
         const int64_t ua = r * C;
@@ -630,7 +555,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_small_kernel(const AttendCa
         const int head = (int)(in / w1);
         const int64_t at = in - head * w1;
         const int f = last_at(tile0[s], tile0[s + 1], at, [&](int i) { return pre[i] - p0; });
-        a.begin[r] = Start{ua - (at - (pre[f] - p0)), s, head, f - tile0[s], 0};
+        a.begin[r] = Start{ua - (at - (pre[f] - p0)), s, head, f - tile0[s]};
     }
 }
 
@@ -662,7 +587,7 @@ __device__ __forceinline__ int64_t units_of(const AttendCall &a, int s)
 
 // The same for any number of sequences and tiles, which are measured a warp at a time and again for each range.
 template <int R, int kItem>
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttendCall a, int ctas, int most, int least)
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttendCall a, int ctas)
 {
     __shared__ int64_t line_s[kLineShared + 1];
     __shared__ int64_t sums[kPlanWarps];
@@ -682,9 +607,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttendCall a, 
     }
     if (threadIdx.x == 0) line[0] = 0;
     __syncthreads();
-    const int64_t U = before, C = range_units(U, ctas, most, least);
+    const int64_t U = before, C = max((U + ctas - 1) / ctas, (int64_t)1);
     const int N = (int)((U + C - 1) / C);
-    if (threadIdx.x == 0) *a.plan = PlanHead{U, C, N, 0};
+    if (threadIdx.x == 0) *a.plan = PlanHead{U, C, N};
     for (int i = threadIdx.x; i < 2 * N; i += kPlanThreads) a.arrived[i] = 0;
     for (int r0 = 0; r0 < N; r0 += kPlanThreads) {
         const int r = r0 + lane * kPlanWarps + warp;   // neighbours on different warps, which work through theirs one by one
@@ -692,7 +617,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttendCall a, 
         const int64_t ua = r * C;
         const int lo = last_at(0, r < N ? S : 1, ua, [&](int i) { return line[i]; });
         Seq w{};
-        Start f{0, lo, 0, 0, 0};
+        Start f{0, lo, 0, 0};
         int64_t at = 0;                // of the range in the head's part of the line
         if (r < N) {
             w = seq_at<R>(a, lo);
@@ -736,10 +661,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttendCall a, 
 }
 
 template <int R, int kItem>
-cudaError_t launch_plan(const AttendCall &a, int ctas, int most, int least, cudaStream_t st)
+cudaError_t launch_plan(const AttendCall &a, int ctas, cudaStream_t st)
 {
     const bool small = a.b.sequences <= kSmallSeqs && (int64_t)a.b.rows * a.group / R + a.b.sequences <= kSmallTiles;
-    return launch_dependent(small ? plan_small_kernel<R, kItem> : plan_kernel<R, kItem>, dim3(1), kPlanThreads, 0, 0, st, a, ctas, most, least);
+    return launch_dependent(small ? plan_small_kernel<R, kItem> : plan_kernel<R, kItem>, dim3(1), kPlanThreads, 0, 0, st, a, ctas);
 }
 
 template <int D>
@@ -753,7 +678,7 @@ cudaError_t launch16(const uw_kv_cache *c, const AttendCall &call, int ctas, cud
     g.vm = c->v16;
     g.c = call;
     g.c.box = c->box16;
-    if ((e = launch_plan<kRows, kItem16>(call, ctas, kMaxRangesPerCta, kLeast16, st)) != cudaSuccess) return e;
+    if ((e = launch_plan<kRows, kItem16>(call, ctas, st)) != cudaSuccess) return e;
     return launch_dependent(attend16_kernel<D>, dim3((unsigned)ctas), kThreads, Layout<D>::smem, 0, st, g);
 }
 
@@ -769,7 +694,7 @@ Plan plan_of(const uw_kv_cache *c, int sequences, int64_t rows, int q_heads)
     Plan p;
     p.tc = rows * (q_heads / c->d.kv_heads) > 16 * (int64_t)sequences;
     p.ctas = std::max(1, device_sms());
-    const size_t ranges = (size_t)p.ctas * (p.tc ? 1 : kMaxRangesPerCta);
+    const size_t ranges = (size_t)p.ctas;
     const auto up = [](size_t n) { return (n + 255) / 256 * 256; };
     p.begin = up(sizeof(PlanHead));
     p.arrived = p.begin + up(ranges * sizeof(Start));
@@ -794,7 +719,7 @@ uw_status check_heads(const uw_kv_cache *c, int sequences, int64_t rows, int q_h
 
 int launch_attend_plan256(const AttendCall &a, int ctas, void *stream)
 {
-    return launch_plan<256, kItem256>(a, ctas, 1, 1, (cudaStream_t)stream);
+    return launch_plan<256, kItem256>(a, ctas, (cudaStream_t)stream);
 }
 
 }  // namespace uw
