@@ -682,7 +682,7 @@ typedef struct {
     const int32_t *bias_ids;       /* [rows, max_bias], with bias: added to these tokens' logits, a token's several entries in order */
     const float *bias;
     const int32_t *bias_lengths;   /* [rows], clamped to [0, max_bias]; NULL: max_bias */
-    int64_t max_bias;              /* 0..65536; rows of bias and bias_ids are max_bias apart */
+    int64_t max_bias;              /* 0..4096; rows of bias and bias_ids are max_bias apart */
     const uint32_t *allowed;       /* [mask_count, ld_allowed] words: a token v whose bit v % 32 of word v / 32 is 0 becomes -inf */
     int64_t ld_allowed, mask_count; /* ld_allowed 0: ceil(vocab / 32) */
     const int32_t *mask_rows;      /* [rows]: which row of allowed; outside [0, mask_count): none.  NULL: row r's own (r < mask_count) */

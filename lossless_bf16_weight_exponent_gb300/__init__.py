@@ -540,7 +540,7 @@ def _of_rows(what: str, t, rows: int, kind: str) -> int:
         return 0
     if t.__class__ is int:
         return t
-    if t.dtype not in (_KINDS or _kinds())[kind] or not t.is_cuda or t.dim() != 1 or len(t) < rows or not t.is_contiguous():
+    if t.dtype not in (_KINDS or _kinds())[kind] or not t.is_cuda or t.numel() < rows or not t.is_contiguous():
         _wrong(what, t, kind)
     return t.data_ptr()
 
@@ -696,14 +696,14 @@ def edit_logits(logits, rows: int, vocab: int, out, tokens=None, lengths=None, p
             pt, repetition, frequency, presence = 0, None, None, None
     pi, pb = _at("bias_ids", bias_ids, "i32"), _at("bias", bias, "f32")
     if bias is not None and bias_ids is not None:
-        if bias_ids.shape != bias.shape or bias.dim() != 2 or len(bias) < rows or not bias.is_contiguous() or not bias_ids.is_contiguous():
+        if bias_ids.shape != bias.shape or bias.dim() != 2 or bias.shape[0] < rows or not bias.is_contiguous() or not bias_ids.is_contiguous():
             raise ValueError("bias_ids and bias must be contiguous [rows, max_bias]")
         max_bias = bias.shape[1]
     pa = _at("allowed", allowed, "bits")
     if allowed is not None:
         if allowed.dim() != 2 or allowed.shape[1] * 32 < vocab or allowed.stride(1) != 1:
             raise ValueError("allowed must be [masks, ceil(vocab / 32)]")
-        masks = len(allowed)
+        masks = allowed.shape[0]
         ld_allowed = allowed.stride(0) if masks > 1 else 0
     d = LogitEditsDesc(pt, ld_tokens, max_tokens, _of_rows("lengths", lengths, rows, "i32"), _of_rows("prompt_lengths", prompt_lengths, rows, "i32"),
                        _of_rows("repetition", repetition, rows, "f32"), _of_rows("frequency", frequency, rows, "f32"),

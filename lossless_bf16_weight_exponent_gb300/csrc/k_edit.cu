@@ -1,10 +1,10 @@
 // k_edit.cu - penalties for repeated tokens, biases and grammar masks on rows of logits (sm_103a).
 //
-// A CTA has a slice of one row's vocabulary.  It looks through the row's whole history (from L2, which all slices of the
-// row share) and counts, for each token of its slice, in a word of shared memory: bits 0-23 how often it was generated,
-// bit 31 that it is in the prompt, bit 30 that the row's biases name it.  The additions are of whole numbers, so
-// their order does not matter.  Then one pass over the slice's logits: a word of 0 and an allowed token leave a logit as
-// it is; a named token's biases are added by looking through the list again, in its order.
+// A CTA has a slice of one row's vocabulary, whose logits it asks for first.  It looks through the row's whole history (from L2,
+// which all slices of the row share) and counts, for each token of its slice, in a word of shared memory: bits 0-23 how often
+// it was generated, bit 31 that it is in the prompt.  The additions are of whole numbers, so their order does not matter.  A token
+// that the row's biases name is edited by the thread of its first entry, which adds the others in the list's order (bit 30
+// tells the rest to pass it over).  Then one pass over the slice: a word of 0 and an allowed token leave a logit as it is.
 // Out of place a logit is read and written once, unless a 16-byte piece is masked out as a whole, which is not read.  In
 // place a piece in which nothing changes is neither read nor written.
 // Bound by memory.
@@ -21,6 +21,10 @@ using namespace uw;
 namespace {
 
 constexpr int kThreads = 512;
+constexpr int kSlice = 8192;   // tokens of a CTA at most: 32 KB of counts
+constexpr int kMaxBias = 4096;
+constexpr int kPlaceBits = 13;
+static_assert(kSlice == 1 << kPlaceBits, "a token's place in the slice, and above it that of an entry in 4096");
 constexpr uint32_t kSeen = 1u << 31, kBias = 1u << 30, kCount = (1u << 24) - 1;
 
 struct EditArgs {
@@ -46,169 +50,222 @@ __device__ __forceinline__ void put(void *p, int64_t i, float x)
 }
 
 struct Row {
-    float rep, freq, pres;
-    const int32_t *ids;
-    const float *bias;
-    int n_bias;
+    float rep, inv, freq, pres;
 };
 
-__device__ __forceinline__ float edited(float x, uint32_t w, int token, const Row &r)
+// the penalties; without a branch, as a few tokens of most warps have some
+__device__ __forceinline__ float edited(float x, uint32_t w, const Row &r)
 {
-    if (w & (kSeen | kCount)) x = x > 0.f ? x / r.rep : x * r.rep;
     const uint32_t c = w & kCount;
-    if (c) x = x - r.freq * (float)c - r.pres;
-    if (w & kBias) {
-        for (int i = 0; i < r.n_bias; i++)
-            if (r.ids[i] == token) x += r.bias[i];
-    }
-    return x;
+    const float f = x > 0.f ? r.inv : r.rep;       // x / rep as a product: a rounding more
+    x = (w & (kSeen | kCount)) ? x * f : x;
+    const float d = r.freq * (float)c + r.pres;
+    return c ? x - d : x;
 }
 
 // W: logits of a piece (8 of bf16, 4 of fp32 inputs; 1: rows without 16-byte alignment)
 template <bool F32, bool OUT32, int W, bool PLACE>
 __global__ void __launch_bounds__(kThreads) edit_kernel(const EditArgs a)
 {
+    constexpr uint32_t kAll = (1u << W) - 1;
+    constexpr int U = kSlice / (kThreads * W);            // pieces of a thread
+    constexpr int kWords = W == 1 ? 1 : 4;                // of a piece as loaded
     extern __shared__ uint32_t words[];
+    __shared__ int counts[kThreads / 32];
     const int64_t row = blockIdx.y;
     const int64_t v0 = (int64_t)blockIdx.x * a.slice;
     const int n = (int)min((int64_t)a.slice, a.vocab - v0);
+    const int whole = n / W * W;
     pdl_trigger();
     for (int i = threadIdx.x; i < n; i += kThreads) words[i] = 0;
     pdl_wait();
-    Row r;
-    r.rep = a.e.repetition ? a.e.repetition[row] : 1.f;
-    r.freq = a.e.frequency ? a.e.frequency[row] : 0.f;
-    r.pres = a.e.presence ? a.e.presence[row] : 0.f;
-    r.n_bias = 0;
-    int len = 0, prompt = 0;
+    // what the row's edits are, then its mask, history and logits, each as soon as it can be asked for
+    const int64_t which = a.e.allowed ? (a.e.mask_rows ? a.e.mask_rows[row] : row) : -1;
+    int len = 0, prompt = 0, n_bias = 0;
     if (a.e.tokens) {
         len = (int)min((int64_t)max(a.e.lengths[row], 0), a.e.max_tokens);
         if (a.e.prompt_lengths) prompt = a.e.prompt_lengths[row];
     }
     if (a.e.bias_ids) {
-        r.n_bias = (int)a.e.max_bias;
-        if (a.e.bias_lengths) r.n_bias = min(max(a.e.bias_lengths[row], 0), r.n_bias);
-        r.ids = a.e.bias_ids + row * a.e.max_bias;
-        r.bias = a.e.bias + row * a.e.max_bias;
+        n_bias = (int)a.e.max_bias;
+        if (a.e.bias_lengths) n_bias = min(max(a.e.bias_lengths[row], 0), n_bias);
     }
-    const uint32_t *mask = nullptr;
-    if (a.e.allowed) {
-        const int64_t m = a.e.mask_rows ? a.e.mask_rows[row] : row;
-        if (m >= 0 && m < a.e.mask_count) mask = a.e.allowed + m * a.e.ld_allowed + v0 / 32;
-    }
-    __syncthreads();
+    Row r;
+    r.rep = a.e.repetition ? a.e.repetition[row] : 1.f;
+    r.inv = 1.f / r.rep;
+    r.freq = a.e.frequency ? a.e.frequency[row] : 0.f;
+    r.pres = a.e.presence ? a.e.presence[row] : 0.f;
+    const uint32_t *mask = which >= 0 && which < a.e.mask_count ? a.e.allowed + which * a.e.ld_allowed + v0 / 32 : nullptr;
     const int32_t *tokens = a.e.tokens + row * a.e.ld_tokens;
-    for (int i0 = 0; i0 < len; i0 += 4 * kThreads) {
-        int64_t at[4];
+    int32_t id[8];                    // of the history, eight of a thread on their way
+    auto history = [&](int i0) {
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
+        for (int j = 0; j < 8; j++) {
             const int i = i0 + j * kThreads + threadIdx.x;
-            at[j] = i < len ? (int64_t)tokens[i] - v0 : -1;
+            id[j] = i < len ? tokens[i] : -1;
         }
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            if (at[j] < 0 || at[j] >= n) continue;
-            if (i0 + j * kThreads + (int)threadIdx.x >= prompt) atomicAdd(&words[at[j]], 1u);
-            else atomicOr(&words[at[j]], kSeen);
-        }
-    }
-    for (int i = threadIdx.x; i < r.n_bias; i += kThreads) {
-        const int64_t at = (int64_t)r.ids[i] - v0;
-        if (at >= 0 && at < n) atomicOr(&words[at], kBias);
-    }
-    __syncthreads();
+    };
+    history(0);
     const uint8_t *in = (const uint8_t *)a.logits + (row * a.ld + v0) * (F32 ? 4 : 2);
     uint8_t *out = (uint8_t *)a.out + (row * a.ld_out + v0) * (OUT32 ? 4 : 2);
-    const int whole = W > 1 ? n / W * W : 0;
-    if constexpr (W > 1) {
-        constexpr uint32_t kAll = (1u << W) - 1;
-        constexpr int U = PLACE ? 1 : 4;  // pieces of a thread on their way
-        for (int p0 = threadIdx.x * W; p0 < whole; p0 += U * kThreads * W) {
-            uint4 raw[U];
-            uint32_t ok[U];
+    auto at = [&](int u) { return (u * kThreads + (int)threadIdx.x) * W; };
+    // the slice's logits are on their way while the history is looked through
+    uint32_t ok[U] = {}, raw[U][kWords];
+    auto fetch = [&](int u) {
 #pragma unroll
-            for (int u = 0; u < U; u++) {
-                const int p = p0 + u * kThreads * W;
-                ok[u] = 0;
-                raw[u] = make_uint4(0, 0, 0, 0);
-                if (p >= whole) continue;
-                ok[u] = mask ? (mask[p >> 5] >> (p & 31)) & kAll : kAll;
-                if (!PLACE && ok[u]) raw[u] = *(const uint4 *)(in + (int64_t)p * (F32 ? 4 : 2));
+        for (int q = 0; q < kWords; q++) raw[u][q] = 0;
+        if (at(u) >= whole || !ok[u]) return;
+        if constexpr (W == 1) {
+            if constexpr (F32) raw[u][0] = ((const uint32_t *)in)[at(u)];
+            else raw[u][0] = (uint32_t)((const uint16_t *)in)[at(u)] << 16;
+        } else {
+            const uint4 v = *(const uint4 *)(in + (int64_t)at(u) * (F32 ? 4 : 2));
+            raw[u][0] = v.x;
+            raw[u][1] = v.y;
+            raw[u][2] = v.z;
+            raw[u][3] = v.w;
+        }
+    };
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+        const int p = at(u);
+        ok[u] = p >= whole ? 0u : mask ? (mask[p >> 5] >> (p & 31)) & kAll : kAll;
+    }
+    if (!PLACE) {
+#pragma unroll
+        for (int u = 0; u < U; u++) fetch(u);
+    }
+    const float *bias = a.e.bias + row * a.e.max_bias;
+    __syncthreads();
+    for (int i0 = 0; i0 < len; i0 += 8 * kThreads) {
+        if (i0) history(i0);
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const int64_t v = (int64_t)id[j] - v0;
+            if (v < 0 || v >= n) continue;
+            if (i0 + j * kThreads + (int)threadIdx.x >= prompt) atomicAdd(&words[v], 1u);
+            else atomicOr(&words[v], kSeen);
+        }
+    }
+    __syncthreads();
+    if (n_bias) {
+        // The entries of the slice's tokens, in the list's order: the token's place in the slice below its place in the list
+        uint32_t *list = words + a.slice;
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        int m = 0;
+        for (int i0 = 0; i0 < n_bias; i0 += kThreads) {
+            const int i = i0 + threadIdx.x;
+            const int64_t p = i < n_bias ? (int64_t)a.e.bias_ids[row * a.e.max_bias + i] - v0 : -1;
+            const bool here = p >= 0 && p < n;
+            const unsigned among = __ballot_sync(0xFFFFFFFFu, here);
+            if (lane == 0) counts[warp] = __popc(among);
+            __syncthreads();
+            int front = 0, all = 0;
+            for (int k = 0; k < kThreads / 32; k++) {
+                front += k < warp ? counts[k] : 0;
+                all += counts[k];
             }
+            if (here) list[m + front + __popc(among & ((1u << lane) - 1u))] = (uint32_t)p | (uint32_t)i << kPlaceBits;
+            m += all;
+            __syncthreads();
+        }
+        // A token with biases is one thread's, that of its first entry, from its logit to its output; the pass below leaves it out.
+        for (int k = threadIdx.x; k < m; k += kThreads) {
+            const uint32_t e = list[k];
+            const int p = (int)(e & (kSlice - 1));
+            const bool allowed = !mask || ((mask[p >> 5] >> (p & 31)) & 1u);
+            float x = value_of<F32>(in, p);
+            const float own = bias[e >> kPlaceBits];
+            int before = 0, after = 0;                     // other entries of the token
+#pragma unroll 4
+            for (int j = 0; j < m; j++) {
+                const bool same = ((list[j] ^ e) & (kSlice - 1)) == 0;
+                before += same && j < k;
+                after += same && j > k;
+            }
+            if (before) continue;
+            x = edited(x, words[p], r) + own;
+            for (int j = k + 1; after; j++) {
+                if ((list[j] ^ e) & (kSlice - 1)) continue;
+                x += bias[list[j] >> kPlaceBits];
+                after--;
+            }
+            if (!allowed) x = -INFINITY;
+            put<OUT32>(out, p, x);
+            words[p] |= kBias;          // the others' threads do not look at this token's word
+        }
+        __syncthreads();
+    }
 #pragma unroll
-            for (int u = 0; u < U; u++) {
-                const int p = p0 + u * kThreads * W;
-                if (p >= whole) continue;
-                uint32_t w[W];
-                uint32_t any = 0;
+    for (int u = 0; u < U; u++) {
+        const int p = at(u);
+        if (p >= whole) break;
+        uint32_t w[W], any = 0;
+        if constexpr (W == 1) {
+            any = w[0] = words[p];
+        } else {
 #pragma unroll
-                for (int q = 0; q < W; q += 4) {
-                    const uint4 v = *(const uint4 *)(words + p + q);
-                    w[q] = v.x;
-                    w[q + 1] = v.y;
-                    w[q + 2] = v.z;
-                    w[q + 3] = v.w;
-                    any |= v.x | v.y | v.z | v.w;
+            for (int q = 0; q < W; q += 4) {
+                const uint4 v = *(const uint4 *)(words + p + q);
+                w[q] = v.x;
+                w[q + 1] = v.y;
+                w[q + 2] = v.z;
+                w[q + 3] = v.w;
+                any |= v.x | v.y | v.z | v.w;
+            }
+        }
+        if (PLACE) {
+            if (!any && ok[u] == kAll) continue;
+            fetch(u);
+        }
+        float x[W];
+#pragma unroll
+        for (int q = 0; q < W; q++) {
+            if constexpr (F32 || W == 1) x[q] = __uint_as_float(raw[u][q]);
+            else x[q] = __uint_as_float((q & 1) ? raw[u][q / 2] & 0xFFFF0000u : raw[u][q / 2] << 16);
+            if (any) x[q] = edited(x[q], w[q], r);
+            if (!((ok[u] >> q) & 1u)) x[q] = -INFINITY;
+        }
+        if (W == 1 || (any & kBias)) {
+#pragma unroll
+            for (int q = 0; q < W; q++)
+                if (!(w[q] & kBias)) put<OUT32>(out, p + q, x[q]);
+            continue;
+        }
+        if constexpr (W > 1) {
+            uint8_t *o = out + (int64_t)p * (OUT32 ? 4 : 2);
+            if constexpr (OUT32) {
+#pragma unroll
+                for (int q = 0; q < W; q += 4) *(float4 *)(o + 4 * q) = make_float4(x[q], x[q + 1], x[q + 2], x[q + 3]);
+            } else {
+                uint32_t h[W / 2];
+#pragma unroll
+                for (int q = 0; q < W; q += 2) {
+                    const __nv_bfloat162 v = __floats2bfloat162_rn(x[q], x[q + 1]);
+                    h[q / 2] = *(const uint32_t *)&v;
                 }
-                if (PLACE) {
-                    if (!any && ok[u] == kAll) continue;
-                    if (ok[u]) raw[u] = *(const uint4 *)(in + (int64_t)p * (F32 ? 4 : 2));
-                }
-                float x[W];
-                const uint32_t b[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
-#pragma unroll
-                for (int q = 0; q < 4; q++) {
-                    if constexpr (F32) {
-                        x[q] = __uint_as_float(b[q]);
-                    } else {
-                        x[2 * q] = __uint_as_float(b[q] << 16);
-                        x[2 * q + 1] = __uint_as_float(b[q] & 0xFFFF0000u);
-                    }
-                }
-#pragma unroll
-                for (int q = 0; q < W; q++) {
-                    if (any && w[q]) x[q] = edited(x[q], w[q], (int)v0 + p + q, r);
-                    if (!((ok[u] >> q) & 1u)) x[q] = -INFINITY;
-                }
-                uint8_t *o = out + (int64_t)p * (OUT32 ? 4 : 2);
-                if constexpr (OUT32) {
-#pragma unroll
-                    for (int q = 0; q < W; q += 4) *(float4 *)(o + 4 * q) = make_float4(x[q], x[q + 1], x[q + 2], x[q + 3]);
-                } else {
-                    uint32_t h[W / 2];
-#pragma unroll
-                    for (int q = 0; q < W; q += 2) {
-                        const __nv_bfloat162 v = __floats2bfloat162_rn(x[q], x[q + 1]);
-                        h[q / 2] = *(const uint32_t *)&v;
-                    }
-                    if constexpr (W == 8) *(uint4 *)o = make_uint4(h[0], h[1], h[2], h[3]);
-                    else *(uint2 *)o = make_uint2(h[0], h[1]);
-                }
+                if constexpr (W == 8) *(uint4 *)o = make_uint4(h[0], h[1], h[2], h[3]);
+                else *(uint2 *)o = make_uint2(h[0], h[1]);
             }
         }
     }
-    constexpr int U = PLACE ? 1 : 8;
-    for (int p0 = whole + threadIdx.x; p0 < n; p0 += U * kThreads) {
-        float x[U];
-        bool ok[U];
-#pragma unroll
-        for (int u = 0; u < U; u++) {
-            const int p = p0 + u * kThreads;
-            ok[u] = p < n && (!mask || ((mask[p >> 5] >> (p & 31)) & 1u));
-            x[u] = !PLACE && ok[u] ? value_of<F32>(in, p) : -INFINITY;
-        }
-#pragma unroll
-        for (int u = 0; u < U; u++) {
-            const int p = p0 + u * kThreads;
-            if (p >= n) break;
-            const uint32_t w = words[p];
-            if (PLACE) {
-                if (!w && ok[u]) continue;
-                if (ok[u]) x[u] = value_of<F32>(in, p);
-            }
-            put<OUT32>(out, p, ok[u] && w ? edited(x[u], w, (int)v0 + p, r) : x[u]);
-        }
+    // the rest of a row that is not a number of pieces
+    const int p = whole + threadIdx.x;
+    if (p < n) {
+        const uint32_t w = words[p];
+        const bool allowed = !mask || ((mask[p >> 5] >> (p & 31)) & 1u);
+        if (!(w & kBias) && (!PLACE || w || !allowed)) put<OUT32>(out, p, allowed ? edited(value_of<F32>(in, p), w, r) : -INFINITY);
     }
+}
+
+template <bool F32, bool OUT32, int W, bool PLACE>
+cudaError_t launch_one(const EditArgs &a, dim3 grid, cudaStream_t st)
+{
+    auto kernel = edit_kernel<F32, OUT32, W, PLACE>;
+    static OncePerDevice once;
+    const cudaError_t e = allow_shared(once, kernel, (kSlice + kMaxBias) * 4);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kernel, grid, kThreads, (size_t)a.slice * 4 + (a.e.bias_ids ? (size_t)a.e.max_bias * 4 : 0), 0, st, a);
 }
 
 template <bool F32, bool OUT32>
@@ -216,11 +273,10 @@ cudaError_t launch_types(const EditArgs &a, int64_t rows, bool wide, bool place,
 {
     constexpr int W = F32 ? 4 : 8;
     const dim3 grid((unsigned)((a.vocab + a.slice - 1) / a.slice), (unsigned)rows);
-    const size_t smem = (size_t)a.slice * 4;
     if constexpr (F32 == OUT32) {
-        if (place) return launch_dependent(wide ? edit_kernel<F32, OUT32, W, true> : edit_kernel<F32, OUT32, 1, true>, grid, kThreads, smem, 0, st, a);
+        if (place) return wide ? launch_one<F32, OUT32, W, true>(a, grid, st) : launch_one<F32, OUT32, 1, true>(a, grid, st);
     }
-    return launch_dependent(wide ? edit_kernel<F32, OUT32, W, false> : edit_kernel<F32, OUT32, 1, false>, grid, kThreads, smem, 0, st, a);
+    return wide ? launch_one<F32, OUT32, W, false>(a, grid, st) : launch_one<F32, OUT32, 1, false>(a, grid, st);
 }
 
 bool aligned(const void *p, unsigned n) { return ((uintptr_t)p & (n - 1)) == 0; }
@@ -251,7 +307,7 @@ extern "C" uw_status uw_edit_logits(const uw_logit_edits *e, const void *logits,
     }
     if (!a.e.repetition && !a.e.frequency && !a.e.presence) a.e.tokens = nullptr;  // nothing looks at them
     if (!a.e.bias_ids != !a.e.bias) return fail(UW_ERR_INVALID_ARG, "uw_edit_logits: bias_ids and bias go together");
-    if (a.e.max_bias < 0 || a.e.max_bias > 65536) return fail(UW_ERR_SHAPE, "uw_edit_logits: max_bias=%lld", (long long)a.e.max_bias);
+    if (a.e.max_bias < 0 || a.e.max_bias > kMaxBias) return fail(UW_ERR_SHAPE, "uw_edit_logits: max_bias=%lld", (long long)a.e.max_bias);
     const int64_t words = (vocab + 31) / 32;
     if (a.e.allowed) {
         if (a.e.ld_allowed == 0) a.e.ld_allowed = words;
@@ -279,7 +335,7 @@ extern "C" uw_status uw_edit_logits(const uw_logit_edits *e, const void *logits,
     const int W = f32 ? 4 : 8;
     const bool wide = aligned(logits, 16) && aligned(out, W * (o32 ? 4 : 2) >= 16 ? 16 : 8) && (rows == 1 || (ld % W == 0 && ld_out % W == 0));
     // A slice of 8192 tokens (32 KB of counts); smaller ones for few rows, so that the GPU is full.
-    a.slice = 8192;
+    a.slice = kSlice;
     while (a.slice > 1024 && rows * ((vocab + a.slice - 1) / a.slice) < 2 * num_sms()) a.slice /= 2;
     for (int64_t r0 = 0; r0 < rows; r0 += 65535) {  // the grid's second dimension
         const int64_t n = std::min<int64_t>(rows - r0, 65535);
