@@ -546,6 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
 #pragma unroll 1
                 for (int q = 0; q < D / 32; q++) {
                     uint32_t v[32];
+                    __syncwarp();     // rows may be left out below, the load is the whole warp's
                     tmem_ld32(t_lane + L::o + t * D + 32 * q, v);
                     tmem_wait_ld();
                     if (in) {
@@ -568,6 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
 #pragma unroll 1
                 for (int q = 0; q < D / 32; q++) {
                     uint32_t v[32];
+                    __syncwarp();     // rows may be left out below, the load is the whole warp's
                     tmem_ld32(t_lane + L::o + t * D + 32 * q, v);
                     tmem_wait_ld();
                     if (in) {
@@ -591,6 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                     __threadfence();
                     join_row<D>(a, c, r0, parts, r, tok, (int)x);
                 }
+                __syncwarp();
                 c = nx;
                 continue;
             }
