@@ -187,10 +187,9 @@ __device__ __forceinline__ bool mbar_wait_short(uint64_t *b, uint32_t parity)
 
 }  // namespace dev
 
-// k_attend_tc.cu: items of 256 rows on tcgen05.  launch_attend_plan (k_attend.cu): the first kernel, for items of 256 rows.
-size_t attend_tc_slot_floats(int D);
-int launch_attend_tc(const uw_kv_cache *c, const AttendCall &a, int ctas, void *stream);
-int launch_attend_plan256(const AttendCall &a, int ctas, void *stream);
-constexpr int kItem256 = 3;           // what an item of 256 rows costs beside its tiles of keys: queries, output, a pipeline that runs dry
+// k_attend_tc.cu: items of 128 or 256 rows on tcgen05.  launch_attend_plan (k_attend.cu): the first kernel for them.
+int launch_attend_tc(const uw_kv_cache *c, const AttendCall &a, int rows, int ctas, void *stream);
+int launch_attend_plan(const AttendCall &a, int rows, int ctas, void *stream);
+constexpr int kItemTc = 3;           // what an item of 128 or 256 rows costs beside its tiles of keys: queries, output, a pipeline that runs dry
 
 }  // namespace uw

@@ -684,7 +684,7 @@ cudaError_t launch16(const uw_kv_cache *c, const AttendCall &call, int ctas, cud
 
 // How a call's workspace is laid out, and which kernel it takes.
 struct Plan {
-    bool tc;                     // items of 256 rows on tcgen05, else of 16
+    int rows;                    // of an item: 16, or 128 or 256 on tcgen05
     int ctas;
     size_t begin, arrived, line, part, bytes;
 };
@@ -692,7 +692,8 @@ struct Plan {
 Plan plan_of(const uw_kv_cache *c, int sequences, int64_t rows, int q_heads)
 {
     Plan p;
-    p.tc = rows * (q_heads / c->d.kv_heads) > 16 * (int64_t)sequences;
+    const int64_t each = rows * (q_heads / c->d.kv_heads);
+    p.rows = each <= 16 * (int64_t)sequences ? 16 : each <= 128 * (int64_t)sequences ? 128 : 256;
     p.ctas = std::max(1, device_sms());
     const size_t ranges = (size_t)p.ctas;
     const auto up = [](size_t n) { return (n + 255) / 256 * 256; };
@@ -700,7 +701,7 @@ Plan plan_of(const uw_kv_cache *c, int sequences, int64_t rows, int q_heads)
     p.arrived = p.begin + up(ranges * sizeof(Start));
     p.line = p.arrived + up(2 * ranges * sizeof(int));
     p.part = p.line + (sequences > kLineShared ? up(((size_t)sequences + 1) * sizeof(int64_t)) : 0);
-    const size_t slot = p.tc ? attend_tc_slot_floats(c->d.head_dim) : c->d.head_dim == 128 ? slot_floats<kRows, 128>() : slot_floats<kRows, 64>();
+    const size_t slot = (size_t)p.rows * (c->d.head_dim + 2);   // slot_floats
     p.bytes = p.part + 2 * ranges * slot * sizeof(float);
     return p;
 }
@@ -717,9 +718,9 @@ uw_status check_heads(const uw_kv_cache *c, int sequences, int64_t rows, int q_h
 
 }  // namespace
 
-int launch_attend_plan256(const AttendCall &a, int ctas, void *stream)
+int launch_attend_plan(const AttendCall &a, int rows, int ctas, void *stream)
 {
-    return launch_plan<256, kItem256>(a, ctas, (cudaStream_t)stream);
+    return rows == 128 ? launch_plan<128, kItemTc>(a, ctas, (cudaStream_t)stream) : launch_plan<256, kItemTc>(a, ctas, (cudaStream_t)stream);
 }
 
 }  // namespace uw
@@ -778,7 +779,7 @@ extern "C" uw_status uw_kv_attend(const uw_kv_cache *c, const uw_kv_batch *b, in
     a.part = (float *)(ws + p.part);
     a.status = c->status;
     const int ctas = std::min(p.ctas, num_sms());
-    const cudaError_t e = p.tc ? (cudaError_t)launch_attend_tc(c, a, ctas, stream)
+    const cudaError_t e = p.rows > kRows ? (cudaError_t)launch_attend_tc(c, a, p.rows, ctas, stream)
                         : c->d.head_dim == 128 ? launch16<128>(c, a, ctas, (cudaStream_t)stream) : launch16<64>(c, a, ctas, (cudaStream_t)stream);
     return e == cudaSuccess ? UW_OK : fail(UW_ERR_CUDA, "uw_kv_attend: launch: %s", cudaGetErrorString(e));
 }

@@ -34,19 +34,17 @@ namespace {
 
 using namespace dev;
 
-constexpr int kWarps = 12, kThreads = 32 * kWarps;
-constexpr int kCopyWarp = 8, kScoreWarp = 9, kValueWarp = 10;
-constexpr int kRows = 256, kTile = kKeys;
+constexpr int kTile = kKeys;
 constexpr float kNegInf = -INFINITY;
 constexpr float kGrow = 8.f;      // log2 of how far a maximum may grow before the output is rescaled
 
-template <int D>
+template <int D, int T>
 struct Layout {
     static constexpr uint32_t half = kTile * 128;               // 64 elements of 128 rows or keys
     static constexpr uint32_t tile = half * (D / 64);           // a tile of queries, keys or values
-    static constexpr int slots = D == 128 ? 5 : 10;
+    static constexpr int slots = (D == 128 ? 7 : 12) - T;
     static constexpr uint32_t bars = 8 * (2 * slots + 18);
-    static constexpr size_t smem = 1024 + 2 * tile + slots * tile + bars + 16;
+    static constexpr size_t smem = 1024 + (T + slots) * tile + bars + 16;
     static_assert(smem <= 227 * 1024, "shared memory");
     // columns of tensor memory
     static constexpr uint32_t o = 0, s = 2 * D, p = s + 128;    // O of tile t at o + t D, P at p + 64 t
@@ -127,13 +125,11 @@ __device__ __forceinline__ uint32_t pack2(float a, float b)
     return *(const uint32_t *)&v;
 }
 
-using Cur = Cursor<kRows, kItem256>;
-
 // the 128 threads of a tile of rows
 __device__ __forceinline__ void tile_sync(int t) { asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory"); }
 
 // Joins a row's parts of an item that was cut, a thread a row: those of ranges r0 .. r0 + parts - 1.
-template <int D>
+template <int D, int kRows, typename Cur>
 __device__ __forceinline__ void join_row(const AttendCall &a, const Cur &c, int r0, int parts, int r, int tok, int x)
 {
     constexpr size_t kSlot = slot_floats<kRows, D>();
@@ -176,15 +172,19 @@ __device__ __forceinline__ void join_row(const AttendCall &a, const Cur &c, int 
     if (a.lse) a.lse[row * a.q_heads + h] = l == 0.f ? kNegInf : (m + log2f(l)) * 0.69314718f;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_constant__ Args g)
+// T: tiles of 128 rows of an item, and warpgroups that have one.
+template <int D, int T>
+__global__ void __launch_bounds__(128 * (T + 1), 1) attend_tc_kernel(const __grid_constant__ Args g)
 {
-    using L = Layout<D>;
+    using L = Layout<D, T>;
+    constexpr int kRows = 128 * T;
+    constexpr int kCopyWarp = 4 * T, kScoreWarp = kCopyWarp + 1, kValueWarp = kCopyWarp + 2;
+    using Cur = Cursor<kRows, kItemTc>;
     constexpr int NS = L::slots;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const AttendCall &a = g.c;
     uint8_t *qs = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);  // [2] tiles
-    uint8_t *ring = qs + 2 * L::tile;
+    uint8_t *ring = qs + T * L::tile;
     uint64_t *full = (uint64_t *)(ring + NS * L::tile);
     uint64_t *empty = full + NS;
     uint64_t *raw = empty + NS;                       // a tile whose values are put right before it counts as full
@@ -230,8 +230,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
     bool ok = true;
 
     // 12 warps have 168 registers a thread at launch; a row of scores wants more: 256 x 208 + 128 x 88 is what 384 x 168 is
-    if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp >= 4 * T) {
+    if constexpr (T == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (any && warp == kCopyWarp) {
         // ------------------------------------------------------------------------------ copies
         Cur c;
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         int n = 0, qk = 0;                  // tiles of keys, products before this one
         int segs[2] = {0, 0};               // of each tile of rows: items begun
         for (; c.more() && ok; c.next(a)) {
-            const int nt = c.cnt, both = c.rows(a) > 128;
+            const int nt = c.cnt, both = T == 2 && c.rows(a) > 128;
             for (int j = 0; j < nt && ok; j++, n++) {
                 const int slot = (2 * n) % NS;
                 for (int t = 0; t <= both && ok; t++) {
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         int n = 0;
         int segs[2] = {0, 0}, pv[2] = {0, 0};
         for (; c.more() && ok; c.next(a)) {
-            const int nt = c.cnt, both = c.rows(a) > 128;
+            const int nt = c.cnt, both = T == 2 && c.rows(a) > 128;
             for (int j = 0; j < nt && ok; j++, n++) {
                 const int v = 2 * n + 1, slot = v % NS;
                 for (int t = 0; t <= both && ok; t++) {
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         if (!mbar_wait_short(&done[1], 0) && lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
     }
     } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    if constexpr (T == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     if (any) {
         // ------------------------------------------------------------------------------ softmax
         const int t = warp >> 2, row = threadIdx.x & 127;
@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                 tile_sync(t);
                 if (last[t] && in) {
                     __threadfence();
-                    join_row<D>(a, c, r0, parts, r, tok, (int)x);
+                    join_row<D, kRows>(a, c, r0, parts, r, tok, (int)x);
                 }
                 __syncwarp();
                 c = nx;
@@ -612,11 +612,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
     }
 }
 
-template <int D>
+template <int D, int T>
 cudaError_t launch_tc(const uw_kv_cache *c, const AttendCall &call, int ctas, cudaStream_t st)
 {
     static OncePerDevice once;
-    cudaError_t e = allow_shared(once, attend_tc_kernel<D>, Layout<D>::smem);
+    cudaError_t e = allow_shared(once, attend_tc_kernel<D, T>, Layout<D, T>::smem);
     if (e != cudaSuccess) return e;
     Args g;
     g.km = c->k128;
@@ -626,17 +626,17 @@ cudaError_t launch_tc(const uw_kv_cache *c, const AttendCall &call, int ctas, cu
     g.q_xor = call.scale2 < 0.f ? 0x80008000u : 0u;
     g.q_and = call.scale2 == 0.f ? 0u : 0xFFFFFFFFu;
     g.c.scale2 = call.scale2 == 0.f ? 1.f : std::fabs(call.scale2);
-    if ((e = (cudaError_t)launch_attend_plan256(g.c, ctas, st)) != cudaSuccess) return e;
-    return launch_dependent(attend_tc_kernel<D>, dim3((unsigned)ctas), kThreads, Layout<D>::smem, 0, st, g);
+    if ((e = (cudaError_t)launch_attend_plan(g.c, 128 * T, ctas, st)) != cudaSuccess) return e;
+    return launch_dependent(attend_tc_kernel<D, T>, dim3((unsigned)ctas), 128 * (T + 1), Layout<D, T>::smem, 0, st, g);
 }
 
 }  // namespace
 
-size_t attend_tc_slot_floats(int D) { return D == 128 ? slot_floats<kRows, 128>() : slot_floats<kRows, 64>(); }
-
-int launch_attend_tc(const uw_kv_cache *c, const AttendCall &a, int ctas, void *stream)
+int launch_attend_tc(const uw_kv_cache *c, const AttendCall &a, int rows, int ctas, void *stream)
 {
-    return c->d.head_dim == 128 ? launch_tc<128>(c, a, ctas, (cudaStream_t)stream) : launch_tc<64>(c, a, ctas, (cudaStream_t)stream);
+    const cudaStream_t st = (cudaStream_t)stream;
+    if (c->d.head_dim == 128) return rows == 128 ? launch_tc<128, 1>(c, a, ctas, st) : launch_tc<128, 2>(c, a, ctas, st);
+    return rows == 128 ? launch_tc<64, 1>(c, a, ctas, st) : launch_tc<64, 2>(c, a, ctas, st);
 }
 
 }  // namespace uw

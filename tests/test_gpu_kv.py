@@ -141,6 +141,20 @@ def test_attend(case):
     check_attend(c, q, out, lse, new, causal, window)
 
 
+@pytest.mark.parametrize("case", [
+    ([9, 2, 5], [700, 64, 0], 12, 3, 64, 16, False, True, 0),
+    ([4, 4, 4], [30000, 200, 3], 32, 4, 128, 64, True, True, 0),
+    ([5, 3, 0, 5], [1000, 90, 4, 2000], 20, 4, 128, 16, False, True, 70),
+    ([6, 1], [300, 1], 8, 1, 64, 8, False, False, 0),
+    ([2] * 80, [(37 * i) % 700 for i in range(80)], 16, 1, 128, 32, False, True, 0)], ids=str)
+def test_attend_up_to_32_rows(case):
+    new, past, Hq, H, D, page, hf, causal, window = case
+    c = batch_of(new, past, page, H=H, D=D, heads_first=hf)
+    q = (torch.randn(sum(new), Hq, D, generator=c["g"]) * 1.5).to(BF16).cuda()
+    out, lse = attend(c, q, Hq, causal, window)
+    check_attend(c, q, out, lse, new, causal, window)
+
+
 def test_attend_long_split():
     """One sequence over all CTAs, and a batch whose items are cut in many places."""
     for new, past, Hq, H in (([1], [40000], 8, 1), ([2, 1, 1], [9000, 20000, 3], 8, 2)):
