@@ -235,10 +235,17 @@ def _typed(what: str, t, dtype: int) -> int:
     return t.data_ptr()
 
 
+_raw_stream = None  # the current stream's address by torch's own binding, a tenth of current_stream()'s cost, and that of the device
+
+
 def _current_stream():
-    import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # a tenth of current_stream()'s cost
-    return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        torch.cuda.current_device()  # sets CUDA up
+        raw, device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+        _raw_stream = (lambda: raw(device())) if raw and device else (lambda: torch.cuda.current_stream().cuda_stream)
+    return _raw_stream()
 
 
 def _stream(stream) -> int:

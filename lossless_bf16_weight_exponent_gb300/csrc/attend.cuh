@@ -45,10 +45,11 @@ struct PlanHead {
     int ranges;
 };
 
-// where a range begins: the item that holds its first unit, and where that begins in the line
+// where a range begins: the item that holds its first unit, where that begins in the line, and its sequence
 struct Start {
     int64_t at;
     int s, head, i;                   // i: place of the tile of rows
+    KvSeq q;
 };
 
 constexpr int kKeys = 128;            // keys of a tile
@@ -59,14 +60,17 @@ struct Seq {
 };
 
 template <int R>
-__device__ __forceinline__ Seq seq_at(const AttendCall &a, int s)
+__device__ __forceinline__ Seq seq_of(const AttendCall &a, const KvSeq &q)
 {
     Seq w;
-    w.q = kv_seq(a.b, s);
+    w.q = q;
     w.keys = min(w.q.len, a.b.capacity);
     w.row_tiles = (int)(((uint32_t)w.q.n * (uint32_t)a.group + (R - 1)) / R);
     return w;
 }
+
+template <int R>
+__device__ __forceinline__ Seq seq_at(const AttendCall &a, int s) { return seq_of<R>(a, kv_seq(a.b, s)); }
 
 // the keys [lo, hi) that some row of a tile of rows sees, and the tiles of keys [t0, t0 + nt) that hold them (one at least)
 struct Span {
@@ -115,7 +119,7 @@ struct Cursor {
         s = f.s;
         head = f.head;
         i = f.i;
-        w = seq_at<R>(a, s);
+        w = seq_of<R>(a, f.q);
         enter(a);
         if (cnt <= 0) next(a);
     }

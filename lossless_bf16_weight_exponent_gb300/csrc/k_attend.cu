@@ -502,13 +502,13 @@ __device__ __forceinline__ int last_at(int lo, int hi, T x, F at)
 // threads, two searches for each range (3 us where the form below takes 12, for the 128 tiles of 8191 tokens).
 // Ranges taken in turn by CTAs that are done, up to six for each, were no faster: 64 sequences of up to 8191 tokens took 213 us
 // against 200, one token over 131000 122 against 95, as each range ends with sums to be joined.
-constexpr int kSmallSeqs = 1024, kSmallTiles = 4096;
+constexpr int kSmallSeqs = 512, kSmallTiles = 4096;
 
 template <int R, int kItem>
 __global__ void __launch_bounds__(kPlanThreads) plan_small_kernel(const AttendCall a, int ctas)
 {
     __shared__ int64_t pre[kSmallTiles + 1];       // of a key head's line, in front of each tile of rows
-    __shared__ int n_s[kSmallSeqs], len_s[kSmallSeqs], tile0[kSmallSeqs + 1];
+    __shared__ int n_s[kSmallSeqs], len_s[kSmallSeqs], first_s[kSmallSeqs], tile0[kSmallSeqs + 1];
     __shared__ int64_t sums[kPlanWarps];
     __shared__ int isums[kPlanWarps];
     const int tid = threadIdx.x, S = a.b.sequences;
@@ -519,6 +519,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_small_kernel(const AttendCa
         w = seq_at<R>(a, tid);
         n_s[tid] = w.q.n;
         len_s[tid] = w.q.len;
+        first_s[tid] = w.q.first;
     }
     int T;
     const int mine = scan_before(w.row_tiles, isums, T);
@@ -555,7 +556,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_small_kernel(const AttendCa
         const int head = (int)(in / w1);
         const int64_t at = in - head * w1;
         const int f = last_at(tile0[s], tile0[s + 1], at, [&](int i) { return pre[i] - p0; });
-        a.begin[r] = Start{ua - (at - (pre[f] - p0)), s, head, f - tile0[s]};
+        a.begin[r] = Start{ua - (at - (pre[f] - p0)), s, head, f - tile0[s], KvSeq{first_s[s], n_s[s], len_s[s]}};
     }
 }
 
@@ -617,10 +618,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttendCall a, 
         const int64_t ua = r * C;
         const int lo = last_at(0, r < N ? S : 1, ua, [&](int i) { return line[i]; });
         Seq w{};
-        Start f{0, lo, 0, 0};
+        Start f{};
+        f.s = lo;
         int64_t at = 0;                // of the range in the head's part of the line
         if (r < N) {
             w = seq_at<R>(a, lo);
+            f.q = w.q;
             const int64_t per = (line[lo + 1] - line[lo]) / a.kv_heads, in = ua - line[lo];
             f.head = (int)(in / per);
             at = in - f.head * per;
