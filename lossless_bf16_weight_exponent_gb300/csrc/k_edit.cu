@@ -7,7 +7,9 @@
 // tells the rest to pass it over).  Then one pass over the slice: a word of 0 and an allowed token leave a logit as it is.
 // Out of place a logit is read and written once, unless a 16-byte piece is masked out as a whole, which is not read.  In
 // place a piece in which nothing changes is neither read nor written.
-// Bound by memory.
+// Bound by memory: 256 rows of 128256 fp32, each with 1500 to 3000 tokens of history and every second one masked, take 56 us
+// (4.8 TB/s; 49 without histories, which every slice of a row looks through); 1 row 3.9 us; 96 rows of 32003 bf16 with 300
+// biases each, their rows not aligned, 18 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -63,9 +65,11 @@ __device__ __forceinline__ float edited(float x, uint32_t w, const Row &r)
     return c ? x - d : x;
 }
 
-// W: logits of a piece (8 of bf16, 4 of fp32 inputs; 1: rows without 16-byte alignment)
+// W: logits of a piece (8 of bf16, 4 of fp32 inputs; 1: rows without 16-byte alignment).  Four CTAs an SM, for which a few
+// registers go to memory, hide more of a CTA's phases from one another: 256 rows of 128256 fp32, half of them masked, take 55.9 us
+// against 64.7 with two.
 template <bool F32, bool OUT32, int W, bool PLACE>
-__global__ void __launch_bounds__(kThreads) edit_kernel(const EditArgs a)
+__global__ void __launch_bounds__(kThreads, 4) edit_kernel(const EditArgs a)
 {
     constexpr uint32_t kAll = (1u << W) - 1;
     constexpr int U = kSlice / (kThreads * W);            // pieces of a thread
