@@ -657,6 +657,7 @@ uw_status uw_kv_append(const uw_kv_cache *c, const uw_kv_batch *b, const uw_rota
  *   than the cache's), UW_ERR_SHAPE (rows, q_heads not a multiple of kv_heads or above 64 kv_heads, strides),
  *   UW_ERR_WORKSPACE, UW_ERR_CUDA.
  */
+/* For a call of these sequences, rows and query heads; it does not shrink as rows grow. */
 uw_status uw_kv_attend_workspace_size(const uw_kv_cache *c, int sequences, int64_t rows, int q_heads, size_t *bytes);
 uw_status uw_kv_attend(const uw_kv_cache *c, const uw_kv_batch *b, int64_t rows, const uint16_t *q, int64_t ldq, int q_heads,
                        float scale, int causal, int64_t window, uint16_t *out, int64_t ldo, float *lse, void *workspace,

@@ -1,21 +1,30 @@
 // k_attend_tc.cu - attention of many new tokens over a cache of keys and values in pages, on tcgen05 (sm_103a).
 //
 // An item is 256 query rows - tokens x query heads of one key head - as two tiles A and B of 128, against tiles of 128 keys.
+// (Or 128 rows, where the sequences bring no more on average: tile A alone, with room for one more tile of keys or values.)
 //   S = Q K^T   (128 x 128, operands in shared memory), P = 2^(scale2 S - m) by a warpgroup, a thread a row,
 //   O += P V    (P in tensor memory, V from shared memory as it lies in the cache: keys x elements)
-// Roles of the twelve warps:
+// Roles of the twelve warps (of eight, with one tile: A's four, then the same):
 //   - 0-3 and 4-7: softmax, output and queries of tile A, of tile B.  A thread holds its row's 128 scores in registers, so a
 //     row's maximum and sum take no exchange.  The output is rescaled only when a maximum has grown by more than 2^8 (then
 //     by tensor memory loads and stores of the row): probabilities are at most 256 and keep their relative precision;
 //   - 8: tensor copies of the pages' slots of one head, keys and values in turn, into a ring of 128-key tiles.  Values that
 //     no row of the item sees are set to zero in shared memory when they have landed, as 0 x NaN is NaN;
-//   - 9: the products of Q and K, A's and B's in turn; 10: those of P and V, by one thread each.  Two warps, as a warp's poll
-//     of a barrier waits in line behind the products that it has issued: with one, the tensor cores ran dry at each wait;
+//   - 9: the products of Q and K, A's and B's in turn; 10: those of P and V, by one thread each (one warp for both: 680 us
+//     against 638 for 8191 tokens, at that step);
 //   - 11: none, it makes up the third warpgroup, which gives registers to the other two.
 // Tensor memory: O of A and B, one S, P of A and of B: 2 D + 128 + 2 x 64 columns.  One S is enough as a warpgroup takes its
 // scores into registers at once, under the product in between, and P does not lie in S: every reuse waits on a barrier of
-// what used it last.
-// Rows of P and V are rounded to bf16 as operands (2^-9 of each; the sum of the powers is taken before that).
+// what used it last.  The product of P and V starts when the first half of a tile's probabilities is there.
+// P is rounded to bf16 as an operand (by 2^-8 of each at most; the sum of the powers is taken before that).
+// Waits suspend the thread: polls of shared memory take turns that the operands of the products need (a spinning form took 874 us
+// where this one took 638).
+//
+// Measured: 8191 tokens of 32 query heads over 8 key heads of 128, causal: 397 us, 1.39 PFLOP/s; 16384 tokens at an earlier step 1.6
+// PFLOP/s; 509 tokens of 64 heads over 7171: 115 us, 1.08 PFLOP/s.  What an item costs beside its tiles (queries, the pipeline's ends,
+// the output, a part's way through the workspace: 3 to 10 us) is what keeps the smaller ones from that.  The chain of a tile bounds a
+// long one: scores 0.27 us, 0.15 until they are seen, 0.9 for softmax, 0.15, the second product 0.27; the tensor cores are busy half of
+// the time (4095 tokens), the units for powers a quarter.  4 tokens x 8 heads over 131067: 110 us, 4.9 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -5,6 +5,8 @@
 // it was generated, bit 31 that it is in the prompt.  The additions are of whole numbers, so their order does not matter.  A token
 // that the row's biases name is edited by the thread of its first entry, which adds the others in the list's order (bit 30
 // tells the rest to pass it over).  Then one pass over the slice: a word of 0 and an allowed token leave a logit as it is.
+// (A list of the tokens with edits, made as the words are counted and gone through behind a pass that looks at no word, was slower
+// in fp32: 70 us against 56, for its atomics with answers and its scattered stores.)
 // Out of place a logit is read and written once, unless a 16-byte piece is masked out as a whole, which is not read.  In
 // place a piece in which nothing changes is neither read nor written.
 // Bound by memory: 256 rows of 128256 fp32, each with 1500 to 3000 tokens of history and every second one masked, take 56 us
