@@ -522,44 +522,57 @@ def _kinds():
 _KIND_OF = {OUT_F32: "f32", OUT_BF16: "bf16"}  # of a call's dtype; another one is the library's to refuse
 
 
-def _wrong(what, t, kind):
+def _wrong(what, t, kind, device):
     if t.dtype not in _KINDS[kind]:
         raise ValueError(f"{what} is {t.dtype}, the call takes {' or '.join(sorted(str(d) for d in _KINDS[kind]))}")
-    if not t.is_cuda:
-        raise ValueError(f"{what} is not in device memory")
+    if t.get_device() != device:
+        raise ValueError(f"{what} is on {t.device}, the call is on CUDA device {device}")
     raise ValueError(f"{what}: its last dimension is not dense, or its shape is another than the call's")
 
 
-def _at(what: str, t, kind: str) -> int:
-    """_ptr of a tensor of this kind in device memory; addresses pass."""
+def _at(what: str, t, kind: str, device: int) -> int:
+    """_ptr of a tensor of this kind on this CUDA device; addresses pass."""
     if t is None:
         return 0
     if t.__class__ is int:
         return t
-    if t.dtype not in (_KINDS or _kinds())[kind] or not t.is_cuda:
-        _wrong(what, t, kind)
+    if t.dtype not in (_KINDS or _kinds())[kind] or t.get_device() != device:
+        _wrong(what, t, kind, device)
     return t.data_ptr()
 
 
-def _of_rows(what: str, t, rows: int, kind: str) -> int:
+def _of_rows(what: str, t, rows: int, kind: str, device: int) -> int:
     """_at of a dense tensor of a number for each row."""
     if t is None:
         return 0
     if t.__class__ is int:
         return t
-    if t.dtype not in (_KINDS or _kinds())[kind] or not t.is_cuda or t.numel() < rows or not t.is_contiguous():
-        _wrong(what, t, kind)
+    if t.dtype not in (_KINDS or _kinds())[kind] or t.get_device() != device or t.numel() < rows or not t.is_contiguous():
+        _wrong(what, t, kind, device)
     return t.data_ptr()
 
 
-def _heads(what: str, t, rows: int, dim: int, kind: str):
+_get_device = None
+
+
+def _device() -> int:
+    """The current CUDA device."""
+    global _get_device
+    if _get_device is None:
+        import torch
+        torch.cuda.current_device()  # sets CUDA up
+        _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return _get_device()
+
+
+def _heads(what: str, t, rows: int, dim: int, kind: str, device: int):
     """Address, elements from row to row (0: dense) and heads of a tensor [rows, heads, dim] or [rows, heads * dim]."""
     if t is None:
         return 0, 0, 0
     if t.__class__ is int:
         return t, 0, 0
-    if t.dtype not in (_KINDS or _kinds())[kind] or not t.is_cuda:
-        _wrong(what, t, kind)
+    if t.dtype not in (_KINDS or _kinds())[kind] or t.get_device() != device:
+        _wrong(what, t, kind, device)
     shape, stride = t.shape, t.stride()
     if len(shape) == 3:
         n, heads, d = shape
@@ -584,6 +597,7 @@ class Rotary:
         self.freq, self.scale = rotary_frequencies(dim, base, scaling, factor, low, high, original)
         import torch
         self._dev = torch.from_numpy(self.freq).cuda()
+        self.device = self._dev.get_device()
         self.desc = RotaryDesc(dim, layout, self._dev.data_ptr(), self.scale)
         self._ref = ctypes.byref(self.desc)
 
@@ -601,13 +615,14 @@ class KVBatch:
     holds lengths[s] tokens with them, in the pages pages[s] (a tensor [sequences, max_pages])."""
 
     def __init__(self, starts, lengths, pages):
-        if any(t.shape[-1] > 1 and t.stride(-1) != 1 for t in (starts, lengths, pages)):
-            raise ValueError("starts, lengths and rows of pages must be dense")
+        if any(not t.is_cuda or (t.shape[-1] > 1 and t.stride(-1) != 1) for t in (starts, lengths, pages)):
+            raise ValueError("starts, lengths and rows of pages must be dense and in device memory")
         if pages.dim() != 2 or lengths.dim() != 1 or starts.dim() != 1 or pages.shape[0] != lengths.shape[0] or starts.shape[0] != lengths.shape[0] + 1:
             raise ValueError("starts [sequences + 1], lengths [sequences], pages [sequences, max_pages]")
         self._keep = (starts, lengths, pages)
         self.sequences = lengths.shape[0]
-        self.desc = KVBatchDesc(self.sequences, _at("starts", starts, "i32"), _at("lengths", lengths, "i32"), _at("pages", pages, "i32"),
+        self.device = starts.get_device()
+        self.desc = KVBatchDesc(self.sequences, *(_at(w, x, "i32", self.device) for w, x in (("starts", starts), ("lengths", lengths), ("pages", pages))),
                                 pages.stride(0) if self.sequences > 1 else 0, pages.shape[1])
         self._ref = ctypes.byref(self.desc)
 
@@ -623,7 +638,8 @@ class KVCache:
         self._keep = (k, v)
         self.pages, self.page_size, self.kv_heads, self.head_dim = k.shape
         self._scale = self.head_dim ** -0.5 if self.head_dim else 0.0
-        d = KVDesc(_at("k", k, "bf16"), _at("v", v, "bf16"), self.pages, k.stride(0), k.stride(1), k.stride(2), self.page_size, self.kv_heads,
+        self._device = _device() if k.is_cuda else -2
+        d = KVDesc(_at("k", k, "bf16", self._device), _at("v", v, "bf16", self._device), self.pages, k.stride(0), k.stride(1), k.stride(2), self.page_size, self.kv_heads,
                    self.head_dim)
         h = ctypes.c_void_p()
         _check(lib().uw_kv_create(ctypes.byref(d), ctypes.byref(h)), "uw_kv_create")
@@ -650,15 +666,18 @@ class KVCache:
         addresses; q_out bf16."""
         D = self.head_dim
         kind = _KIND_OF.get(dtype, "any")
-        pq, sq, hq = _heads("q", q, rows, D, kind)
-        po, so, ho = _heads("q_out", q_out, rows, D, "bf16")
-        pk, sk, hk = _heads("k", k, rows, D, kind)
-        pv, sv, hv = _heads("v", v, rows, D, kind)
+        dev = self._device
+        pq, sq, hq = _heads("q", q, rows, D, kind, dev)
+        po, so, ho = _heads("q_out", q_out, rows, D, "bf16", dev)
+        pk, sk, hk = _heads("k", k, rows, D, kind, dev)
+        pv, sv, hv = _heads("v", v, rows, D, kind, dev)
+        if batch.device != dev or (rotary is not None and rotary.device != dev):
+            raise ValueError(f"the batch or the rotary is on another device than the cache's {dev}")
         q_heads = q_heads or hq or ho
         if (hq and hq != q_heads) or (ho and ho != q_heads) or (hk and hk != self.kv_heads) or (hv and hv != self.kv_heads):
             raise ValueError(f"heads: q {hq}, q_out {ho} of {q_heads}, k {hk}, v {hv} of {self.kv_heads}")
         s = lib().uw_kv_append(self._h, batch._ref, rotary._ref if rotary is not None else None, rows, dtype, pq, ldq or sq, q_heads, pk, ldk or sk, pv,
-                               ldv or sv, _of_rows("positions", positions, rows, "i32"), po, ldq_out or so, _stream(stream))
+                               ldv or sv, _of_rows("positions", positions, rows, "i32", dev), po, ldq_out or so, _stream(stream))
         if s:
             _check(s, "uw_kv_append")
 
@@ -670,15 +689,18 @@ class KVCache:
     def attend(self, batch, rows: int, q, out, q_heads: int = 0, scale=None, causal: bool = True, window: int = 0, lse=None, workspace=None,
                ws_bytes: int = 0, ldq: int = 0, ldo: int = 0, stream=None):
         """uw_kv_attend: q and out bf16 [rows, q_heads, head_dim] (or addresses, with q_heads); scale None: head_dim ** -0.5."""
-        pq, sq, hq = _heads("q", q, rows, self.head_dim, "bf16")
-        po, so, ho = _heads("out", out, rows, self.head_dim, "bf16")
+        dev = self._device
+        pq, sq, hq = _heads("q", q, rows, self.head_dim, "bf16", dev)
+        po, so, ho = _heads("out", out, rows, self.head_dim, "bf16", dev)
+        if batch.device != dev:
+            raise ValueError(f"the batch is on device {batch.device}, the cache on {dev}")
         q_heads = q_heads or hq or ho
         if (hq and hq != q_heads) or (ho and ho != q_heads):
             raise ValueError(f"heads: q {hq}, out {ho} of {q_heads}")
         if lse is not None and lse.__class__ is not int and (not lse.is_contiguous() or lse.numel() < rows * q_heads):
             raise ValueError("lse must be dense [rows, q_heads]")
         s = lib().uw_kv_attend(self._h, batch._ref, rows, pq, ldq or sq, q_heads, self._scale if scale is None else scale, causal, window, po, ldo or so,
-                               _at("lse", lse, "f32"), _ptr(workspace), ws_bytes, _stream(stream))
+                               _at("lse", lse, "f32", dev), _ptr(workspace), ws_bytes, _stream(stream))
         if s:
             _check(s, "uw_kv_attend")
 
@@ -693,29 +715,30 @@ def edit_logits(logits, rows: int, vocab: int, out, tokens=None, lengths=None, p
     prompt_lengths int32 [rows], penalties fp32 [rows], bias_ids int32 and bias fp32 [rows, max_bias], allowed int32 words
     [masks, words].  out_dtype None: dtype."""
     out_dtype = dtype if out_dtype is None else out_dtype
-    p, po = _at("logits", logits, _KIND_OF.get(dtype, "any")), _at("out", out, _KIND_OF.get(out_dtype, "any"))
+    dev = _device()
+    p, po = _at("logits", logits, _KIND_OF.get(dtype, "any"), dev), _at("out", out, _KIND_OF.get(out_dtype, "any"), dev)
     ld, ld_out = ld or _pitch("logits", logits, rows, vocab), ld_out or _pitch("out", out, rows, vocab)
     max_tokens = max_bias = ld_tokens = ld_allowed = masks = 0
-    pt = _at("tokens", tokens, "i32")
+    pt = _at("tokens", tokens, "i32", dev)
     if tokens is not None:
         ld_tokens, max_tokens = _pitch("tokens", tokens, rows, 0), tokens.shape[1]
         if max_tokens == 0:  # no history: no penalties
             pt, repetition, frequency, presence = 0, None, None, None
-    pi, pb = _at("bias_ids", bias_ids, "i32"), _at("bias", bias, "f32")
+    pi, pb = _at("bias_ids", bias_ids, "i32", dev), _at("bias", bias, "f32", dev)
     if bias is not None and bias_ids is not None:
         if bias_ids.shape != bias.shape or bias.dim() != 2 or bias.shape[0] < rows or not bias.is_contiguous() or not bias_ids.is_contiguous():
             raise ValueError("bias_ids and bias must be contiguous [rows, max_bias]")
         max_bias = bias.shape[1]
-    pa = _at("allowed", allowed, "bits")
+    pa = _at("allowed", allowed, "bits", dev)
     if allowed is not None:
         if allowed.dim() != 2 or allowed.shape[1] * 32 < vocab or allowed.stride(1) != 1:
             raise ValueError("allowed must be [masks, ceil(vocab / 32)]")
         masks = allowed.shape[0]
         ld_allowed = allowed.stride(0) if masks > 1 else 0
-    d = LogitEditsDesc(pt, ld_tokens, max_tokens, _of_rows("lengths", lengths, rows, "i32"), _of_rows("prompt_lengths", prompt_lengths, rows, "i32"),
-                       _of_rows("repetition", repetition, rows, "f32"), _of_rows("frequency", frequency, rows, "f32"),
-                       _of_rows("presence", presence, rows, "f32"), pi, pb, _of_rows("bias_lengths", bias_lengths, rows, "i32"), max_bias, pa, ld_allowed,
-                       masks, _of_rows("mask_rows", mask_rows, rows, "i32"))
+    d = LogitEditsDesc(pt, ld_tokens, max_tokens, _of_rows("lengths", lengths, rows, "i32", dev), _of_rows("prompt_lengths", prompt_lengths, rows, "i32", dev),
+                       _of_rows("repetition", repetition, rows, "f32", dev), _of_rows("frequency", frequency, rows, "f32", dev),
+                       _of_rows("presence", presence, rows, "f32", dev), pi, pb, _of_rows("bias_lengths", bias_lengths, rows, "i32", dev), max_bias, pa, ld_allowed,
+                       masks, _of_rows("mask_rows", mask_rows, rows, "i32", dev))
     s = lib().uw_edit_logits(ctypes.byref(d), p, dtype, rows, vocab, ld, po, out_dtype, ld_out, _stream(stream))
     if s:
         _check(s, "uw_edit_logits")

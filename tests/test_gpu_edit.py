@@ -206,6 +206,24 @@ def test_masks_shared_and_missing():
     check(c, run(c))
 
 
+@pytest.mark.parametrize("place", [False, True])
+def test_more_rows_than_a_grid_is_high(place):
+    R, V = 70001, 40
+    g = torch.Generator().manual_seed(2)
+    x = torch.randn(R, V, generator=g).cuda()
+    allowed = torch.randint(-2 ** 31, 2 ** 31, (R - 3, 2), generator=g, dtype=I32).cuda()   # the last rows have no mask
+    tokens = torch.randint(0, V, (R, 3), generator=g, dtype=I32).cuda()
+    presence = torch.rand(R, generator=g).cuda()
+    lengths = torch.full((R,), 3, dtype=I32, device="cuda")
+    want = x - presence[:, None] * torch.zeros(R, V, device="cuda").scatter_(1, tokens.long(), 1.0)
+    v = torch.arange(V, device="cuda")
+    want[:R - 3][((allowed[:, v // 32] >> (v % 32)) & 1) == 0] = -math.inf
+    out = x if place else torch.empty_like(x)
+    uw.edit_logits(x, R, V, out, tokens=tokens, lengths=lengths, presence=presence, allowed=allowed)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
 def test_strides_and_streams():
     """Columns of a wider tensor, in and out side by side in one tensor; a captured graph and its replay on new tokens."""
     c = make(5, 1000, 60, 4, 5)

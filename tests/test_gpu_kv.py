@@ -174,6 +174,51 @@ def test_attend_many_sequences(S, most, H):
     check_attend(c, q, out, lse, new)
 
 
+@pytest.mark.parametrize("S,few,page", [(600, 1, 8), (600, 20, 16), (2500, 1, 16)])
+def test_attend_more_sequences_than_the_small_plan_takes(S, few, page):
+    """The first kernel's general form, one sequence with many tiles of rows among them, some that bring nothing."""
+    new = [0 if i % 7 == 3 else few for i in range(S)]
+    new[5] = 400
+    past = [(i * 37) % 50 for i in range(S)]
+    past[11] = 3000
+    c = batch_of(new, past, page, H=1, D=64)
+    q = torch.randn(sum(new), 2, 64, generator=c["g"]).to(BF16).cuda()
+    out, lse = attend(c, q, 2)
+    check_attend(c, q, out, lse, new)
+
+
+def test_attend_many_tiles_of_one_sequence():
+    """More tiles of rows than the small form of the first kernel holds."""
+    new, past = [600] * 7, [0, 5, 100, 0, 0, 9, 40]
+    c = batch_of(new, past, 32, H=2, D=64)
+    q = torch.randn(sum(new), 128, 64, generator=c["g"]).to(BF16).cuda()
+    need = c["cache"].workspace_size(c["batch"], 4200, 128)
+    assert need > 0
+    out, lse = attend(c, q, 128)
+    check_attend(c, q, out, lse, new)
+
+
+def test_keys_and_values_in_one_tensor():
+    kv = torch.randn(6, 2, 16, 2, 64, generator=torch.Generator().manual_seed(3)).to(BF16).cuda()
+    k, v = kv[:, 0], kv[:, 1]
+    cache = uw.KVCache(k, v)
+    i32 = lambda x: torch.tensor(x, dtype=I32, device="cuda")  # noqa: E731
+    batch = uw.KVBatch(i32([0, 3]), i32([40]), i32([[4, 1, 2]]))
+    g = torch.Generator().manual_seed(4)
+    q, kn, vn = (torch.randn(3, n, 64, generator=g).to(BF16).cuda() for n in (4, 2, 2))
+    was = kv.clone()
+    cache.append(batch, 3, kn, vn)
+    was[2, 0, 5:8], was[2, 1, 5:8] = kn, vn
+    assert torch.equal(kv, was)
+    out = torch.zeros_like(q)
+    need = cache.workspace_size(batch, 3, 4)
+    cache.attend(batch, 3, q, out, workspace=torch.empty(need, dtype=torch.uint8, device="cuda"), ws_bytes=need)
+    cache.check()
+    kk, vv = (t[[4, 1, 2]].reshape(48, 2, 64)[:40].cpu() for t in (k, v))
+    ref, _, b, _ = plain_attend(q.cpu(), kk, vv, 3, 0.125, True, 0)
+    assert ((out.cpu().to(F64) - ref).abs() <= b).all()
+
+
 def test_attend_peaked_scores():
     """Scores up to hundreds: the running maximum moves, probabilities underflow."""
     new, past = [5, 260], [900, 300]
