@@ -354,6 +354,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend16_kernel(const __grid_cons
                     mma16816(o[2 * q], p, b[0], b[1]);
                     mma16816(o[2 * q + 1], p, b[2], b[3]);
                 }
+                // the stage's reads are done before the next copy into it (the async proxy) is asked for
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
             }
         }

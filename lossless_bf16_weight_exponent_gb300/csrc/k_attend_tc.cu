@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(128 * (T + 1), 1) attend_tc_kernel(const __gri
     constexpr int NS = L::slots;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const AttendCall &a = g.c;
-    uint8_t *qs = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);  // [2] tiles
+    uint8_t *qs = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);  // [T] tiles
     uint8_t *ring = qs + T * L::tile;
     uint64_t *full = (uint64_t *)(ring + NS * L::tile);
     uint64_t *empty = full + NS;
@@ -307,6 +307,8 @@ __global__ void __launch_bounds__(128 * (T + 1), 1) attend_tc_kernel(const __gri
             }
         }
         mend();
+        // the products' word that the last tiles are free arrives before the block ends
+        for (int i = n > NS ? n - NS : 0; i < n && ok; i++) ok = __all_sync(0xFFFFFFFFu, mbar_wait_short(&empty[i % NS], (i / NS) & 1));
         if (!ok) {
             if (lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
             // what is on its way lands before the block ends (a tile that waits to be put right: above)
