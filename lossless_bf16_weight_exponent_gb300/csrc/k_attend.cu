@@ -13,9 +13,9 @@
 // Slots that no row of the item sees (behind the sequence's length, in front of a window) may hold anything: their scores are
 // replaced, their values set to zero in shared memory.
 //
-// Bound by memory: 64 sequences of up to 8191 tokens (8 key heads of 128, 1.15 GB) take 197 us, 5.8 TB/s, all of 8191 tokens 355
-// (6.0 TB/s), one of 131000 95 us.  One token over 8190 takes 17.5 us, of which the first kernel and the hand-over are 5, looking up pages
-// and queries 3, the copies 3 and the three joins (of warps, of CTAs, by the last CTA) 5.  Items of 32 rows, two tiles of 16 in
+// Bound by memory: 64 sequences of up to 8191 tokens (8 key heads of 128, 1.15 GB) take 194 us, 5.9 TB/s, all of 8191 tokens 355
+// (6.0 TB/s), one of 131000 93 us.  One token over 8190 takes 15.1 us, of which the first kernel and the hand-over are 5, looking up pages
+// and queries 2, the copies 3 and the joins (of warps, of CTAs, by the last CTA) 4.  Items of 32 rows, two tiles of 16 in
 // a CTA with their queries in shared memory, took 305 us for 64 sequences of 24 rows, where tcgen05 takes 266.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -36,7 +36,8 @@ using namespace dev;
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kRows = 16, kStep = 16;
-constexpr int kItem16 = 1;        // what an item costs beside its tiles of keys: the warps' sums joined, its queries
+constexpr int kItem16 = 2;        // what an item costs beside its tiles of keys: the warps' sums joined, its queries (0 to 6 measured: 1 token
+                                  // over 8190 takes 14.7, 17.5, 15.1, 15.2, 14.5 us by 0 to 4, 64 sequences 219, 197, 194, 196, 202)
 static_assert(kStep * kWarps == kKeys, "a tile is a step of every warp");
 constexpr int kStages = 3;
 constexpr float kNegInf = -INFINITY;
