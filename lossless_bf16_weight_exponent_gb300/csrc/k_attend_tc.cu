@@ -240,380 +240,380 @@ __global__ void __launch_bounds__(128 * (T + 1), 1) attend_tc_kernel(const __gri
 
     // 12 warps have 168 registers a thread at launch; a row of scores wants more: 256 x 208 + 128 x 88 is what 384 x 168 is
     if (warp >= 4 * T) {
-    if constexpr (T == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (any && warp == kCopyWarp) {
-        // ------------------------------------------------------------------------------ copies
-        Cur c;
-        c.set(a, a.begin[range], ua, ub);
-        int n = 0;                        // tiles asked for: keys, values, keys, ...
-        // values that are to be put right when they have landed
-        bool fix = false;
-        int fix_slot = 0, fix_lo = 0, fix_hi = 0;
-        uint32_t raw_phase = 0;
-        auto mend = [&] {
-            if (!fix) return;
-            fix = false;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait_short(raw, raw_phase & 1))) ok = false;
-            raw_phase++;
-            uint8_t *v = ring + fix_slot * L::tile;
-            for (int i = lane; i < kTile * (D / 8); i += 32) {
-                const int row = i / (D / 8), ch = i % (D / 8);
-                if (row >= fix_lo && row < fix_hi) continue;
-                *(uint4 *)(v + (ch >> 3) * L::half + row * 128 + ((ch & 7) ^ (row & 7)) * 16) = make_uint4(0, 0, 0, 0);
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&full[fix_slot]);
-            __syncwarp();
-        };
-        // a lane's copies: a box of slots, 64 elements each
-        const int boxes = kTile / a.box, half = lane % (D / 64), bx0 = lane / (D / 64);
-        constexpr int kPer = 32 / (D / 64);          // boxes of one round of lanes
-        const uint32_t box_bytes = (uint32_t)a.box * 128u;
-        for (; c.more() && ok; c.next(a)) {
-            const int32_t *table = a.b.pages + (int64_t)c.s * a.b.ld_pages;
-            for (int j = 0; j < c.cnt && ok; j++) {
-                const int key0 = (c.k.t0 + c.off + j) * kTile;
-                const bool odd = key0 < c.k.lo || key0 + kTile > c.k.hi;
-                for (int kv = 0; kv < 2 && ok; kv++) {
-                    const int slot = n % NS;
-                    if (n >= NS && !__all_sync(0xFFFFFFFFu, mbar_poll(&empty[slot], ((n / NS) & 1) ^ 1))) {
-                        mend();
-                        if (!__all_sync(0xFFFFFFFFu, mbar_wait_short(&empty[slot], ((n / NS) & 1) ^ 1))) { ok = false; break; }
-                    }
-                    const bool mended = kv && odd;
-                    if (mended) mend();              // the one before
-                    uint64_t *bar = mended ? raw : &full[slot];
-                    if (lane == 0) mbar_expect_tx(bar, L::tile);
-                    __syncwarp();
-                    for (int b0 = 0; b0 < boxes; b0 += kPer) {
-                        const int bx = b0 + bx0;
-                        if (bx < boxes) {
-                            const int key = key0 + bx * a.box, pi = key / a.page_size;
-                            const int page = key < c.w.keys ? table[pi] : -1;
-                            tma4d(saddr(ring) + slot * L::tile + half * L::half + bx * box_bytes, kv ? &g.vm : &g.km, half * 64, key - pi * a.page_size, c.head,
-                                  page, saddr(bar));
+        if constexpr (T == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (any && warp == kCopyWarp) {
+            // ------------------------------------------------------------------------------ copies
+            Cur c;
+            c.set(a, a.begin[range], ua, ub);
+            int n = 0;                        // tiles asked for: keys, values, keys, ...
+            // values that are to be put right when they have landed
+            bool fix = false;
+            int fix_slot = 0, fix_lo = 0, fix_hi = 0;
+            uint32_t raw_phase = 0;
+            auto mend = [&] {
+                if (!fix) return;
+                fix = false;
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait_short(raw, raw_phase & 1))) ok = false;
+                raw_phase++;
+                uint8_t *v = ring + fix_slot * L::tile;
+                for (int i = lane; i < kTile * (D / 8); i += 32) {
+                    const int row = i / (D / 8), ch = i % (D / 8);
+                    if (row >= fix_lo && row < fix_hi) continue;
+                    *(uint4 *)(v + (ch >> 3) * L::half + row * 128 + ((ch & 7) ^ (row & 7)) * 16) = make_uint4(0, 0, 0, 0);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[fix_slot]);
+                __syncwarp();
+            };
+            // a lane's copies: a box of slots, 64 elements each
+            const int boxes = kTile / a.box, half = lane % (D / 64), bx0 = lane / (D / 64);
+            constexpr int kPer = 32 / (D / 64);          // boxes of one round of lanes
+            const uint32_t box_bytes = (uint32_t)a.box * 128u;
+            for (; c.more() && ok; c.next(a)) {
+                const int32_t *table = a.b.pages + (int64_t)c.s * a.b.ld_pages;
+                for (int j = 0; j < c.cnt && ok; j++) {
+                    const int key0 = (c.k.t0 + c.off + j) * kTile;
+                    const bool odd = key0 < c.k.lo || key0 + kTile > c.k.hi;
+                    for (int kv = 0; kv < 2 && ok; kv++) {
+                        const int slot = n % NS;
+                        if (n >= NS && !__all_sync(0xFFFFFFFFu, mbar_poll(&empty[slot], ((n / NS) & 1) ^ 1))) {
+                            mend();
+                            if (!__all_sync(0xFFFFFFFFu, mbar_wait_short(&empty[slot], ((n / NS) & 1) ^ 1))) { ok = false; break; }
                         }
-                    }
-                    __syncwarp();
-                    if (mended) {
-                        fix = true;
-                        fix_slot = slot;
-                        fix_lo = c.k.lo - key0;
-                        fix_hi = c.k.hi - key0;
-                    }
-                    n++;
-                }
-            }
-        }
-        mend();
-        // the products' word that the last tiles are free arrives before the block ends
-        for (int i = n > NS ? n - NS : 0; i < n && ok; i++) ok = __all_sync(0xFFFFFFFFu, mbar_wait_short(&empty[i % NS], (i / NS) & 1));
-        if (!ok) {
-            if (lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
-            // what is on its way lands before the block ends (a tile that waits to be put right: above)
-            for (int i = n > NS ? n - NS : 0; i < n; i++) mbar_wait_short(&full[i % NS], (i / NS) & 1);
-        }
-    } else if (any && warp == kScoreWarp) {
-        // ------------------------------------------------------------------------------ products of queries and keys
-        Cur c;
-        c.set(a, a.begin[range], ua, ub);
-        const bool leader = elect_one();
-        constexpr uint32_t id = idesc_bf16(128, 128);
-        const uint32_t q0 = saddr(qs), r0 = saddr(ring);
-        int n = 0, qk = 0;                  // tiles of keys, products before this one
-        int segs[2] = {0, 0};               // of each tile of rows: items begun
-        for (; c.more() && ok; c.next(a)) {
-            const int nt = c.cnt, both = T == 2 && c.rows(a) > 128;
-            for (int j = 0; j < nt && ok; j++, n++) {
-                const int slot = (2 * n) % NS;
-                for (int t = 0; t <= both && ok; t++) {
-                    bool w = qk > 0 ? wait_both(&full[slot], ((2 * n) / NS) & 1, sfree, (qk - 1) & 1) : mbar_wait_short(&full[slot], ((2 * n) / NS) & 1);
-                    if (j == 0) w = w && mbar_wait_short(&qfull[t], segs[t]++ & 1);
-                    ok = __all_sync(0xFFFFFFFFu, w);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t qd = smem_desc_sw128(q0 + t * L::tile), kd = smem_desc_sw128(r0 + slot * L::tile);
-                    if (leader) {
-#pragma unroll
-                        for (int k = 0; k < D / 16; k++) {
-                            const uint32_t at = ((k >> 2) * L::half + (k & 3) * 32) >> 4;
-                            mma_ss(tmem + L::s, qd + at, kd + at, id, k > 0);
+                        const bool mended = kv && odd;
+                        if (mended) mend();              // the one before
+                        uint64_t *bar = mended ? raw : &full[slot];
+                        if (lane == 0) mbar_expect_tx(bar, L::tile);
+                        __syncwarp();
+                        for (int b0 = 0; b0 < boxes; b0 += kPer) {
+                            const int bx = b0 + bx0;
+                            if (bx < boxes) {
+                                const int key = key0 + bx * a.box, pi = key / a.page_size;
+                                const int page = key < c.w.keys ? table[pi] : -1;
+                                tma4d(saddr(ring) + slot * L::tile + half * L::half + bx * box_bytes, kv ? &g.vm : &g.km, half * 64, key - pi * a.page_size, c.head,
+                                      page, saddr(bar));
+                            }
                         }
-                        mma_commit(&sfull[t]);
-                        if (t == both) mma_commit(&empty[slot]);
+                        __syncwarp();
+                        if (mended) {
+                            fix = true;
+                            fix_slot = slot;
+                            fix_lo = c.k.lo - key0;
+                            fix_hi = c.k.hi - key0;
+                        }
+                        n++;
                     }
-                    __syncwarp();
-                    qk++;
                 }
             }
-        }
-        if (!ok && lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
-        // every product issued is complete before the tensor memory is freed
-        if (leader) mma_commit(&done[0]);
-        __syncwarp();
-        if (!mbar_wait_short(&done[0], 0) && lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
-    } else if (any && warp == kValueWarp) {
-        // ------------------------------------------------------------------------------ products of probabilities and values
-        Cur c;
-        c.set(a, a.begin[range], ua, ub);
-        const bool leader = elect_one();
-        constexpr uint32_t id = idesc_bf16(128, D) | 1u << 16;  // the second operand's columns run along memory
-        const uint32_t r0 = saddr(ring);
-        int n = 0;
-        int segs[2] = {0, 0}, pv[2] = {0, 0};
-        for (; c.more() && ok; c.next(a)) {
-            const int nt = c.cnt, both = T == 2 && c.rows(a) > 128;
-            for (int j = 0; j < nt && ok; j++, n++) {
-                const int v = 2 * n + 1, slot = v % NS;
-                for (int t = 0; t <= both && ok; t++) {
-                    bool w = wait_both(&full[slot], (v / NS) & 1, &pfull[2 * t], pv[t] & 1);
-                    if (j == 0) {
-                        if (segs[t] > 0) w = w && mbar_wait_short(&ofree[t], (segs[t] - 1) & 1);
-                        segs[t]++;
-                    }
-                    ok = __all_sync(0xFFFFFFFFu, w);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t vd = values_desc(r0 + slot * L::tile, L::half);
-                    const uint32_t od = tmem + L::o + t * D, pd = tmem + L::p + t * 64;
-                    if (leader) {
+            mend();
+            // the products' word that the last tiles are free arrives before the block ends
+            for (int i = n > NS ? n - NS : 0; i < n && ok; i++) ok = __all_sync(0xFFFFFFFFu, mbar_wait_short(&empty[i % NS], (i / NS) & 1));
+            if (!ok) {
+                if (lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
+                // what is on its way lands before the block ends (a tile that waits to be put right: above)
+                for (int i = n > NS ? n - NS : 0; i < n; i++) mbar_wait_short(&full[i % NS], (i / NS) & 1);
+            }
+        } else if (any && warp == kScoreWarp) {
+            // ------------------------------------------------------------------------------ products of queries and keys
+            Cur c;
+            c.set(a, a.begin[range], ua, ub);
+            const bool leader = elect_one();
+            constexpr uint32_t id = idesc_bf16(128, 128);
+            const uint32_t q0 = saddr(qs), r0 = saddr(ring);
+            int n = 0, qk = 0;                  // tiles of keys, products before this one
+            int segs[2] = {0, 0};               // of each tile of rows: items begun
+            for (; c.more() && ok; c.next(a)) {
+                const int nt = c.cnt, both = T == 2 && c.rows(a) > 128;
+                for (int j = 0; j < nt && ok; j++, n++) {
+                    const int slot = (2 * n) % NS;
+                    for (int t = 0; t <= both && ok; t++) {
+                        bool w = qk > 0 ? wait_both(&full[slot], ((2 * n) / NS) & 1, sfree, (qk - 1) & 1) : mbar_wait_short(&full[slot], ((2 * n) / NS) & 1);
+                        if (j == 0) w = w && mbar_wait_short(&qfull[t], segs[t]++ & 1);
+                        ok = __all_sync(0xFFFFFFFFu, w);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t qd = smem_desc_sw128(q0 + t * L::tile), kd = smem_desc_sw128(r0 + slot * L::tile);
+                        if (leader) {
 #pragma unroll
-                        for (int k = 0; k < kTile / 32; k++) mma_ts(od, pd + 8 * k, vd + k * (2048 >> 4), id, j > 0 || k > 0);
+                            for (int k = 0; k < D / 16; k++) {
+                                const uint32_t at = ((k >> 2) * L::half + (k & 3) * 32) >> 4;
+                                mma_ss(tmem + L::s, qd + at, kd + at, id, k > 0);
+                            }
+                            mma_commit(&sfull[t]);
+                            if (t == both) mma_commit(&empty[slot]);
+                        }
+                        __syncwarp();
+                        qk++;
                     }
-                    __syncwarp();
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait_short(&pfull[2 * t + 1], pv[t] & 1));
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (leader) {
-#pragma unroll
-                        for (int k = kTile / 32; k < kTile / 16; k++) mma_ts(od, pd + 8 * k, vd + k * (2048 >> 4), id, 1);
-                        mma_commit(&pvdone[t]);
-                        if (t == both) mma_commit(&empty[slot]);
-                    }
-                    __syncwarp();
-                    pv[t]++;
                 }
             }
+            if (!ok && lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
+            // every product issued is complete before the tensor memory is freed
+            if (leader) mma_commit(&done[0]);
+            __syncwarp();
+            if (!mbar_wait_short(&done[0], 0) && lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
+        } else if (any && warp == kValueWarp) {
+            // ------------------------------------------------------------------------------ products of probabilities and values
+            Cur c;
+            c.set(a, a.begin[range], ua, ub);
+            const bool leader = elect_one();
+            constexpr uint32_t id = idesc_bf16(128, D) | 1u << 16;  // the second operand's columns run along memory
+            const uint32_t r0 = saddr(ring);
+            int n = 0;
+            int segs[2] = {0, 0}, pv[2] = {0, 0};
+            for (; c.more() && ok; c.next(a)) {
+                const int nt = c.cnt, both = T == 2 && c.rows(a) > 128;
+                for (int j = 0; j < nt && ok; j++, n++) {
+                    const int v = 2 * n + 1, slot = v % NS;
+                    for (int t = 0; t <= both && ok; t++) {
+                        bool w = wait_both(&full[slot], (v / NS) & 1, &pfull[2 * t], pv[t] & 1);
+                        if (j == 0) {
+                            if (segs[t] > 0) w = w && mbar_wait_short(&ofree[t], (segs[t] - 1) & 1);
+                            segs[t]++;
+                        }
+                        ok = __all_sync(0xFFFFFFFFu, w);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t vd = values_desc(r0 + slot * L::tile, L::half);
+                        const uint32_t od = tmem + L::o + t * D, pd = tmem + L::p + t * 64;
+                        if (leader) {
+#pragma unroll
+                            for (int k = 0; k < kTile / 32; k++) mma_ts(od, pd + 8 * k, vd + k * (2048 >> 4), id, j > 0 || k > 0);
+                        }
+                        __syncwarp();
+                        ok = __all_sync(0xFFFFFFFFu, mbar_wait_short(&pfull[2 * t + 1], pv[t] & 1));
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (leader) {
+#pragma unroll
+                            for (int k = kTile / 32; k < kTile / 16; k++) mma_ts(od, pd + 8 * k, vd + k * (2048 >> 4), id, 1);
+                            mma_commit(&pvdone[t]);
+                            if (t == both) mma_commit(&empty[slot]);
+                        }
+                        __syncwarp();
+                        pv[t]++;
+                    }
+                }
+            }
+            if (!ok && lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
+            if (leader) mma_commit(&done[1]);
+            __syncwarp();
+            if (!mbar_wait_short(&done[1], 0) && lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
         }
-        if (!ok && lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
-        if (leader) mma_commit(&done[1]);
-        __syncwarp();
-        if (!mbar_wait_short(&done[1], 0) && lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
-    }
     } else {
-    if constexpr (T == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    if (any) {
-        // ------------------------------------------------------------------------------ softmax
-        const int t = warp >> 2, row = threadIdx.x & 127;
-        const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        Cur c;
-        c.set(a, a.begin[range], ua, ub);
-        int steps = 0;                  // scores seen, also products of P and V asked for
-        auto arrive = [&](uint64_t *b) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(b);
-        };
-        auto wait = [&](uint64_t *b, uint32_t parity) {
-            if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait_short(b, parity));
-        };
-        // an item's queries of this tile, 16 threads a row
-        auto queries = [&](const Cur &q) {
-            const int x0 = q.rt * kRows + 128 * t, xn = q.w.q.n * a.group;
-            constexpr int kC = D / 8, kStep = 128 / kC;     // 16-byte pieces of a row, rows of a round
-            const int ch = row % kC;
-            int r = row / kC, tok = (int)(((uint32_t)x0 + r) / (uint32_t)a.group), h = (int)((uint32_t)x0 + r - (uint32_t)tok * a.group);
-            const int dt = kStep / a.group, dh = kStep % a.group;
-            const uint16_t *src = a.q + q.w.q.first * a.ldq + (int64_t)(q.head * a.group) * D + 8 * ch;
+        if constexpr (T == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        if (any) {
+            // ------------------------------------------------------------------------------ softmax
+            const int t = warp >> 2, row = threadIdx.x & 127;
+            const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+            Cur c;
+            c.set(a, a.begin[range], ua, ub);
+            int steps = 0;                  // scores seen, also products of P and V asked for
+            auto arrive = [&](uint64_t *b) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b);
+            };
+            auto wait = [&](uint64_t *b, uint32_t parity) {
+                if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait_short(b, parity));
+            };
+            // an item's queries of this tile, 16 threads a row
+            auto queries = [&](const Cur &q) {
+                const int x0 = q.rt * kRows + 128 * t, xn = q.w.q.n * a.group;
+                constexpr int kC = D / 8, kStep = 128 / kC;     // 16-byte pieces of a row, rows of a round
+                const int ch = row % kC;
+                int r = row / kC, tok = (int)(((uint32_t)x0 + r) / (uint32_t)a.group), h = (int)((uint32_t)x0 + r - (uint32_t)tok * a.group);
+                const int dt = kStep / a.group, dh = kStep % a.group;
+                const uint16_t *src = a.q + q.w.q.first * a.ldq + (int64_t)(q.head * a.group) * D + 8 * ch;
 #pragma unroll 1
-            for (int b = 0; b < 128 / kStep; b += 8) {
-                uint4 v[8];
+                for (int b = 0; b < 128 / kStep; b += 8) {
+                    uint4 v[8];
 #pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    v[i] = make_uint4(0, 0, 0, 0);
-                    if (x0 + r + i * kStep < xn) v[i] = *(const uint4 *)(src + tok * a.ldq + h * D);
-                    tok += dt;
-                    h += dh;
-                    if (h >= a.group) {
-                        h -= a.group;
-                        tok++;
+                    for (int i = 0; i < 8; i++) {
+                        v[i] = make_uint4(0, 0, 0, 0);
+                        if (x0 + r + i * kStep < xn) v[i] = *(const uint4 *)(src + tok * a.ldq + h * D);
+                        tok += dt;
+                        h += dh;
+                        if (h >= a.group) {
+                            h -= a.group;
+                            tok++;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; i++, r += kStep) {
+                        v[i].x = (v[i].x & g.q_and) ^ g.q_xor;
+                        v[i].y = (v[i].y & g.q_and) ^ g.q_xor;
+                        v[i].z = (v[i].z & g.q_and) ^ g.q_xor;
+                        v[i].w = (v[i].w & g.q_and) ^ g.q_xor;
+                        *(uint4 *)(qs + t * L::tile + (ch >> 3) * L::half + r * 128 + ((ch & 7) ^ (r & 7)) * 16) = v[i];
                     }
                 }
-#pragma unroll
-                for (int i = 0; i < 8; i++, r += kStep) {
-                    v[i].x = (v[i].x & g.q_and) ^ g.q_xor;
-                    v[i].y = (v[i].y & g.q_and) ^ g.q_xor;
-                    v[i].z = (v[i].z & g.q_and) ^ g.q_xor;
-                    v[i].w = (v[i].w & g.q_and) ^ g.q_xor;
-                    *(uint4 *)(qs + t * L::tile + (ch >> 3) * L::half + r * 128 + ((ch & 7) ^ (r & 7)) * 16) = v[i];
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                arrive(&qfull[t]);
+            };
+            if (c.more() && c.rows(a) > 128 * t) queries(c);
+            while (c.more()) {
+                const int nt = c.cnt;
+                const bool begins = c.begins(), ends = c.ends();
+                Cur nx = c;
+                nx.next(a);
+                if (c.rows(a) <= 128 * t) {   // the item has no such tile
+                    c = nx;
+                    if (c.more() && c.rows(a) > 128 * t) queries(c);
+                    continue;
                 }
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            arrive(&qfull[t]);
-        };
-        if (c.more() && c.rows(a) > 128 * t) queries(c);
-        while (c.more()) {
-            const int nt = c.cnt;
-            const bool begins = c.begins(), ends = c.ends();
-            Cur nx = c;
-            nx.next(a);
-            if (c.rows(a) <= 128 * t) {   // the item has no such tile
-                c = nx;
-                if (c.more() && c.rows(a) > 128 * t) queries(c);
-                continue;
-            }
-            // this thread's row, and the keys [from, upto) that it sees
-            const int64_t x = (int64_t)c.rt * kRows + 128 * t + row;
-            const bool in = x < (int64_t)c.w.q.n * a.group;
-            const int tok = in ? (int)x / a.group : 0;
-            const int64_t pos = (int64_t)c.w.q.len - c.w.q.n + tok;
-            const int upto = !in ? 0 : a.causal ? (int)min(max(pos + 1, (int64_t)0), (int64_t)c.w.keys) : c.w.keys;
-            const int from = a.window ? (int)max(pos - a.window + 1, (int64_t)0) : 0;
-            float m = kNegInf;            // what the powers are relative to, in powers of 2
-            Pair l2 = pair(0.f, 0.f);
-            for (int j = 0; j < nt; j++) {
-                const int key0 = (c.k.t0 + c.off + j) * kTile;
-                wait(&sfull[t], steps & 1);
-                tc_fence_after();
-                uint32_t s[4][32];
-#pragma unroll
-                for (int q = 0; q < 4; q++) tmem_ld32(t_lane + L::s + 32 * q, s[q]);
-                tmem_wait_ld();
-                tc_fence_before();
-                arrive(sfree);
-                if (__any_sync(0xFFFFFFFFu, key0 < from || key0 + kTile > upto)) {
-                    const int lo = from - key0, hi = upto - key0;
-#pragma unroll
-                    for (int i = 0; i < 128; i++)
-                        if (i < lo || i >= hi) s[i >> 5][i & 31] = __float_as_uint(kNegInf);
-                }
-                float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
-#pragma unroll
-                for (int i = 0; i < 128; i += 8)
-#pragma unroll
-                    for (int q = 0; q < 4; q++)
-                        mx[q] = max3(mx[q], __uint_as_float(s[i >> 5][(i & 31) + 2 * q]), __uint_as_float(s[i >> 5][(i & 31) + 2 * q + 1]));
-                const float ms = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale2;
-                bool waited = steps == 0 || __all_sync(0xFFFFFFFFu, mbar_poll(&pvdone[t], (steps - 1) & 1));  // the product before
-                if (j == 0) m = ms;
-                else if (__any_sync(0xFFFFFFFFu, ms > m + kGrow)) {
-                    // the output so far, in other powers
-                    const float mn = fmaxf(m, ms), f = mn == kNegInf ? 1.f : exp2_fast(m - mn);
-                    m = mn;
-                    l2 = mul2(l2, pair(f, f));
-                    if (!waited) wait(&pvdone[t], (steps - 1) & 1);
-                    waited = true;
+                // this thread's row, and the keys [from, upto) that it sees
+                const int64_t x = (int64_t)c.rt * kRows + 128 * t + row;
+                const bool in = x < (int64_t)c.w.q.n * a.group;
+                const int tok = in ? (int)x / a.group : 0;
+                const int64_t pos = (int64_t)c.w.q.len - c.w.q.n + tok;
+                const int upto = !in ? 0 : a.causal ? (int)min(max(pos + 1, (int64_t)0), (int64_t)c.w.keys) : c.w.keys;
+                const int from = a.window ? (int)max(pos - a.window + 1, (int64_t)0) : 0;
+                float m = kNegInf;            // what the powers are relative to, in powers of 2
+                Pair l2 = pair(0.f, 0.f);
+                for (int j = 0; j < nt; j++) {
+                    const int key0 = (c.k.t0 + c.off + j) * kTile;
+                    wait(&sfull[t], steps & 1);
                     tc_fence_after();
+                    uint32_t s[4][32];
+#pragma unroll
+                    for (int q = 0; q < 4; q++) tmem_ld32(t_lane + L::s + 32 * q, s[q]);
+                    tmem_wait_ld();
+                    tc_fence_before();
+                    arrive(sfree);
+                    if (__any_sync(0xFFFFFFFFu, key0 < from || key0 + kTile > upto)) {
+                        const int lo = from - key0, hi = upto - key0;
+#pragma unroll
+                        for (int i = 0; i < 128; i++)
+                            if (i < lo || i >= hi) s[i >> 5][i & 31] = __float_as_uint(kNegInf);
+                    }
+                    float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+                    for (int i = 0; i < 128; i += 8)
+#pragma unroll
+                        for (int q = 0; q < 4; q++)
+                            mx[q] = max3(mx[q], __uint_as_float(s[i >> 5][(i & 31) + 2 * q]), __uint_as_float(s[i >> 5][(i & 31) + 2 * q + 1]));
+                    const float ms = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale2;
+                    bool waited = steps == 0 || __all_sync(0xFFFFFFFFu, mbar_poll(&pvdone[t], (steps - 1) & 1));  // the product before
+                    if (j == 0) m = ms;
+                    else if (__any_sync(0xFFFFFFFFu, ms > m + kGrow)) {
+                        // the output so far, in other powers
+                        const float mn = fmaxf(m, ms), f = mn == kNegInf ? 1.f : exp2_fast(m - mn);
+                        m = mn;
+                        l2 = mul2(l2, pair(f, f));
+                        if (!waited) wait(&pvdone[t], (steps - 1) & 1);
+                        waited = true;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int q = 0; q < D / 32; q++) {
+                            uint32_t o[32];
+                            tmem_ld32(t_lane + L::o + t * D + 32 * q, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tmem_st32(t_lane + L::o + t * D + 32 * q, o);
+                        }
+                        tmem_wait_st();
+                    }
+                    const float base = m == kNegInf ? 0.f : m;
+                    const Pair sc = pair(a.scale2, a.scale2), nb = pair(-base, -base);
+                    Pair acc[2] = {l2, pair(0.f, 0.f)};
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {        // each half's product starts when it is there
+                        uint32_t p[32];
+#pragma unroll
+                        for (int i = 64 * h; i < 64 * h + 64; i += 2) {
+                            float e0, e1;
+                            unpair(fma2(pair(__uint_as_float(s[i >> 5][i & 31]), __uint_as_float(s[i >> 5][(i & 31) + 1])), sc, nb), e0, e1);
+                            e0 = exp2_fast(e0);
+                            e1 = exp2_fast(e1);
+                            acc[(i >> 1) & 1] = add2(acc[(i >> 1) & 1], pair(e0, e1));
+                            p[(i & 63) >> 1] = pack2(e0, e1);
+                        }
+                        if (h == 0) {
+                            if (!waited) wait(&pvdone[t], (steps - 1) & 1);   // the product before has read P
+                            tc_fence_after();
+                        }
+                        tmem_st32(t_lane + L::p + t * 64 + 32 * h, p);
+                        tmem_wait_st();
+                        tc_fence_before();
+                        arrive(&pfull[2 * t + h]);
+                    }
+                    l2 = add2(acc[0], acc[1]);
+                    steps++;
+                }
+                // the last scores are in: the products are done with the queries
+                if (nx.more() && nx.rows(a) > 128 * t) queries(nx);
+                wait(&pvdone[t], (steps - 1) & 1);
+                tc_fence_after();
+                float la, lb;
+                unpair(l2, la, lb);
+                const float l = la + lb;
+                if (begins && ends) {
+                    const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+                    const int h = c.head * a.group + (in ? (int)x - tok * a.group : 0);
+                    const int64_t r = c.w.q.first + tok;
+                    uint16_t *o = a.out + r * a.ldo + (int64_t)h * D;
 #pragma unroll 1
                     for (int q = 0; q < D / 32; q++) {
-                        uint32_t o[32];
-                        tmem_ld32(t_lane + L::o + t * D + 32 * q, o);
+                        uint32_t v[32];
+                        __syncwarp();     // rows may be left out below, the load is the whole warp's
+                        tmem_ld32(t_lane + L::o + t * D + 32 * q, v);
                         tmem_wait_ld();
+                        if (in) {
 #pragma unroll
-                        for (int i = 0; i < 32; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                        tmem_st32(t_lane + L::o + t * D + 32 * q, o);
-                    }
-                    tmem_wait_st();
-                }
-                const float base = m == kNegInf ? 0.f : m;
-                const Pair sc = pair(a.scale2, a.scale2), nb = pair(-base, -base);
-                Pair acc[2] = {l2, pair(0.f, 0.f)};
-#pragma unroll
-                for (int h = 0; h < 2; h++) {        // each half's product starts when it is there
-                    uint32_t p[32];
-#pragma unroll
-                    for (int i = 64 * h; i < 64 * h + 64; i += 2) {
-                        float e0, e1;
-                        unpair(fma2(pair(__uint_as_float(s[i >> 5][i & 31]), __uint_as_float(s[i >> 5][(i & 31) + 1])), sc, nb), e0, e1);
-                        e0 = exp2_fast(e0);
-                        e1 = exp2_fast(e1);
-                        acc[(i >> 1) & 1] = add2(acc[(i >> 1) & 1], pair(e0, e1));
-                        p[(i & 63) >> 1] = pack2(e0, e1);
-                    }
-                    if (h == 0) {
-                        if (!waited) wait(&pvdone[t], (steps - 1) & 1);   // the product before has read P
-                        tc_fence_after();
-                    }
-                    tmem_st32(t_lane + L::p + t * 64 + 32 * h, p);
-                    tmem_wait_st();
-                    tc_fence_before();
-                    arrive(&pfull[2 * t + h]);
-                }
-                l2 = add2(acc[0], acc[1]);
-                steps++;
-            }
-            // the last scores are in: the products are done with the queries
-            if (nx.more() && nx.rows(a) > 128 * t) queries(nx);
-            wait(&pvdone[t], (steps - 1) & 1);
-            tc_fence_after();
-            float la, lb;
-            unpair(l2, la, lb);
-            const float l = la + lb;
-            if (begins && ends) {
-                const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
-                const int h = c.head * a.group + (in ? (int)x - tok * a.group : 0);
-                const int64_t r = c.w.q.first + tok;
-                uint16_t *o = a.out + r * a.ldo + (int64_t)h * D;
-#pragma unroll 1
-                for (int q = 0; q < D / 32; q++) {
-                    uint32_t v[32];
-                    __syncwarp();     // rows may be left out below, the load is the whole warp's
-                    tmem_ld32(t_lane + L::o + t * D + 32 * q, v);
-                    tmem_wait_ld();
-                    if (in) {
-#pragma unroll
-                        for (int i = 0; i < 32; i += 8) {
-                            uint4 w;
-                            w.x = pack2(__uint_as_float(v[i]) * inv, __uint_as_float(v[i + 1]) * inv);
-                            w.y = pack2(__uint_as_float(v[i + 2]) * inv, __uint_as_float(v[i + 3]) * inv);
-                            w.z = pack2(__uint_as_float(v[i + 4]) * inv, __uint_as_float(v[i + 5]) * inv);
-                            w.w = pack2(__uint_as_float(v[i + 6]) * inv, __uint_as_float(v[i + 7]) * inv);
-                            *(uint4 *)(o + 32 * q + i) = w;
+                            for (int i = 0; i < 32; i += 8) {
+                                uint4 w;
+                                w.x = pack2(__uint_as_float(v[i]) * inv, __uint_as_float(v[i + 1]) * inv);
+                                w.y = pack2(__uint_as_float(v[i + 2]) * inv, __uint_as_float(v[i + 3]) * inv);
+                                w.z = pack2(__uint_as_float(v[i + 4]) * inv, __uint_as_float(v[i + 5]) * inv);
+                                w.w = pack2(__uint_as_float(v[i + 6]) * inv, __uint_as_float(v[i + 7]) * inv);
+                                *(uint4 *)(o + 32 * q + i) = w;
+                            }
                         }
                     }
-                }
-                if (in && a.lse) a.lse[r * a.q_heads + h] = l == 0.f ? kNegInf : (m + log2f(l)) * 0.69314718f;
-            } else {
-                // pieces of four columns of all rows: a warp's stores are 512 bytes in a row
-                float *o = a.part + (2 * (size_t)range + (begins ? 1 : 0)) * slot_floats<kRows, D>();
-                const int r = 128 * t + row;
+                    if (in && a.lse) a.lse[r * a.q_heads + h] = l == 0.f ? kNegInf : (m + log2f(l)) * 0.69314718f;
+                } else {
+                    // pieces of four columns of all rows: a warp's stores are 512 bytes in a row
+                    float *o = a.part + (2 * (size_t)range + (begins ? 1 : 0)) * slot_floats<kRows, D>();
+                    const int r = 128 * t + row;
 #pragma unroll 1
-                for (int q = 0; q < D / 32; q++) {
-                    uint32_t v[32];
-                    __syncwarp();     // rows may be left out below, the load is the whole warp's
-                    tmem_ld32(t_lane + L::o + t * D + 32 * q, v);
-                    tmem_wait_ld();
-                    if (in) {
+                    for (int q = 0; q < D / 32; q++) {
+                        uint32_t v[32];
+                        __syncwarp();     // rows may be left out below, the load is the whole warp's
+                        tmem_ld32(t_lane + L::o + t * D + 32 * q, v);
+                        tmem_wait_ld();
+                        if (in) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4) __stcg((uint4 *)(o + ((32 * q + i) / 4 * kRows + r) * 4), make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+                            for (int i = 0; i < 32; i += 4) __stcg((uint4 *)(o + ((32 * q + i) / 4 * kRows + r) * 4), make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+                        }
                     }
-                }
-                if (in) {
-                    __stcg(o + kRows * D + r, m);
-                    __stcg(o + kRows * D + kRows + r, l);
+                    if (in) {
+                        __stcg(o + kRows * D + r, m);
+                        __stcg(o + kRows * D + kRows + r, l);
+                    }
+                    tc_fence_before();
+                    arrive(&ofree[t]);
+                    // the part that comes last joins them all
+                    const int r0 = c.first_range(C), parts = c.last_range(C) - r0 + 1;
+                    __threadfence();
+                    tile_sync(t);
+                    if (row == 0) last[t] = atomicAdd(&a.arrived[2 * r0 + t], 1) == parts - 1;
+                    tile_sync(t);
+                    if (last[t] && in) {
+                        __threadfence();
+                        join_row<D, kRows>(a, c, r0, parts, r, tok, (int)x);
+                    }
+                    __syncwarp();
+                    c = nx;
+                    continue;
                 }
                 tc_fence_before();
                 arrive(&ofree[t]);
-                // the part that comes last joins them all
-                const int r0 = c.first_range(C), parts = c.last_range(C) - r0 + 1;
-                __threadfence();
-                tile_sync(t);
-                if (row == 0) last[t] = atomicAdd(&a.arrived[2 * r0 + t], 1) == parts - 1;
-                tile_sync(t);
-                if (last[t] && in) {
-                    __threadfence();
-                    join_row<D, kRows>(a, c, r0, parts, r, tok, (int)x);
-                }
-                __syncwarp();
                 c = nx;
-                continue;
             }
-            tc_fence_before();
-            arrive(&ofree[t]);
-            c = nx;
+            if (!ok && lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
         }
-        if (!ok && lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
-    }
     }
     tc_fence_before();
     __syncthreads();
