@@ -291,6 +291,22 @@ def test_attend_pages_a_window_left(n, window):
     assert torch.equal(out, want) and torch.equal(lse, wl)
 
 
+@pytest.mark.parametrize("n,H", [(3, 2), (20, 1), (300, 2)])
+def test_attend_a_key_that_is_not_finite(n, H):
+    """The rows that see it have no answer; those that do not have theirs."""
+    c = batch_of([n], [70], 16, H=H, D=64)
+    q = torch.randn(n, 4, 64, generator=c["g"]).to(BF16).cuda()
+    at = 70 + n - 1                                  # the last token's key
+    for bad in (float("nan"), float("inf")):
+        c["k"][c["table"][0, at // 16].item(), at % 16] = bad
+        out, lse = attend(c, q, 4)
+        k, v = c["seqs"][0]
+        ref, rl, b, bl = plain_attend(q[:n - 1].cpu(), k[:-1], v[:-1], n - 1, 0.125, True, 0)
+        assert ((out[:n - 1].cpu().to(F64) - ref).abs() <= b).all() and ((lse[:n - 1].cpu().to(F64) - rl).abs() <= bl).all()
+        if math.isnan(bad):
+            assert torch.isnan(out[n - 1].float()).all() and torch.isnan(lse[n - 1]).all()
+
+
 @pytest.mark.parametrize("n", [1, 300])
 def test_attend_pages_outside_read_as_zeros(n):
     page, past = 32, 500
