@@ -7,8 +7,9 @@
 // for 1024 sequences) and its slot, and the first dim / 2 threads turn the position into cos and sin for all heads.
 // The angle is position * freq in turns: in 64 bits the product is exact to 1e-10 of a turn at position 2^20, its fraction goes
 // into sincospi in fp32, so a far position costs no accuracy (the product in fp32 is off by 0.06 radians there).
-// Bound by memory for many tokens: 4096 of 32 query and 8 key heads of 128, bf16, take 20 us (5.0 TB/s); 253 of 64 and 8 heads 5.8 us;
-// one token 2.7 us, the launch and three loads that depend on each other.
+// Bound by memory for many tokens: 4096 of 32 query and 8 key heads of 128, bf16, take 17 us (5.9 TB/s; 20 with the angles in
+// their order in shared memory, where lanes of neighbouring items met in the same banks); 253 of 64 and 8 heads 6 us; one token
+// 2.7 us, the launch and three loads that depend on each other.
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -105,7 +106,7 @@ __device__ __forceinline__ int seq_of_row(const KvBatch &b, int t)
 template <bool F32, int ITEMS>
 __global__ void __launch_bounds__(128) append_kernel(const AppendArgs a)
 {
-    __shared__ float2 turn[64];
+    __shared__ float2 turn[64];     // pair 8 m + e at 8 e + m: lanes with neighbouring items read neighbouring places
     __shared__ int64_t slot_at;     // element of the slot in k and v; -1: the token is not stored
     __shared__ int live;
     const int t = blockIdx.x, D = a.c.head_dim, per = D / 16;
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(128) append_kernel(const AppendArgs a)
             x -= rint(x);
             float sn, cs;
             sincospif((float)(2.0 * x), &sn, &cs);
-            turn[threadIdx.x] = make_float2(cs * a.scale, sn * a.scale);
+            turn[8 * (threadIdx.x & 7) + (threadIdx.x >> 3)] = make_float2(cs * a.scale, sn * a.scale);
         }
     }
     __syncthreads();
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(128) append_kernel(const AppendArgs a)
         if (halves) {
 #pragma unroll
             for (int e = 0; e < 8; e++) {
-                const float2 w = turn[8 * m + e];
+                const float2 w = turn[8 * e + m];
                 const float u = x[e] * w.x - y[e] * w.y, v = x[e] * w.y + y[e] * w.x;
                 x[e] = u;
                 y[e] = v;
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(128) append_kernel(const AppendArgs a)
         } else if (turned) {
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
-                const float2 w = turn[8 * m + e / 2], z = turn[8 * m + 4 + e / 2];
+                const float2 w = turn[4 * e + m], z = turn[32 + 4 * e + m];
                 const float u = x[e] * w.x - x[e + 1] * w.y, v = x[e] * w.y + x[e + 1] * w.x;
                 x[e] = u;
                 x[e + 1] = v;
