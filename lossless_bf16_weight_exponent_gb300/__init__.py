@@ -565,6 +565,11 @@ def _device() -> int:
     return _get_device()
 
 
+def _shared(what: str):
+    """Of rows that share memory: their stride of 0 would be the library's word for dense rows, which end far behind the tensor."""
+    raise ValueError(f"{what}: its rows share memory (a broadcast tensor); pass a contiguous copy")
+
+
 def _heads(what: str, t, rows: int, dim: int, kind: str, device: int):
     """Address, elements from row to row (0: dense) and heads of a tensor [rows, heads, dim] or [rows, heads * dim]."""
     if t is None:
@@ -585,6 +590,8 @@ def _heads(what: str, t, rows: int, dim: int, kind: str, device: int):
         n, heads, ok = 0, 0, False
     if not ok or n < rows:
         raise ValueError(f"{what} must be [rows, heads, {dim}] or [rows, heads * {dim}], a row's heads dense")
+    if rows > 1 and stride[0] < heads * dim:
+        _shared(what)
     return t.data_ptr(), stride[0] if n > 1 else 0, heads
 
 
@@ -619,6 +626,8 @@ class KVBatch:
             raise ValueError("starts, lengths and rows of pages must be dense and in device memory")
         if pages.dim() != 2 or lengths.dim() != 1 or starts.dim() != 1 or pages.shape[0] != lengths.shape[0] or starts.shape[0] != lengths.shape[0] + 1:
             raise ValueError("starts [sequences + 1], lengths [sequences], pages [sequences, max_pages]")
+        if pages.shape[0] > 1 and pages.stride(0) < pages.shape[1]:
+            _shared("pages")
         self._keep = (starts, lengths, pages)
         self.sequences = lengths.shape[0]
         self.device = starts.get_device()
@@ -734,6 +743,8 @@ def edit_logits(logits, rows: int, vocab: int, out, tokens=None, lengths=None, p
         if allowed.dim() != 2 or allowed.shape[1] * 32 < vocab or allowed.stride(1) != 1:
             raise ValueError("allowed must be [masks, ceil(vocab / 32)]")
         masks = allowed.shape[0]
+        if masks > 1 and allowed.stride(0) * 32 < vocab:
+            _shared("allowed")
         ld_allowed = allowed.stride(0) if masks > 1 else 0
     d = LogitEditsDesc(pt, ld_tokens, max_tokens, _of_rows("lengths", lengths, rows, "i32", dev), _of_rows("prompt_lengths", prompt_lengths, rows, "i32", dev),
                        _of_rows("repetition", repetition, rows, "f32", dev), _of_rows("frequency", frequency, rows, "f32", dev),
@@ -751,4 +762,6 @@ def _pitch(what: str, t, rows: int, width: int) -> int:
     shape, stride = t.shape, t.stride()
     if len(shape) != 2 or shape[0] < rows or shape[1] < width or (stride[1] != 1 and shape[1] > 1):
         raise ValueError(f"{what} must be [rows, {width} or more], its rows dense")
+    if rows > 1 and stride[0] < (width or shape[1]):
+        _shared(what)
     return stride[0] if rows > 1 else 0
