@@ -134,8 +134,12 @@ __device__ __forceinline__ uint32_t pack2(float a, float b)
     return *(const uint32_t *)&v;
 }
 
-// the 128 threads of a tile of rows
-__device__ __forceinline__ void tile_sync(int t) { asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory"); }
+// the 128 threads of a tile of rows; the barrier is of whole warps
+__device__ __forceinline__ void tile_sync(int t)
+{
+    __syncwarp();
+    asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
+}
 
 // Joins a row's parts of an item that was cut, a thread a row: those of ranges r0 .. r0 + parts - 1.
 template <int D, int kRows, typename Cur>
@@ -221,6 +225,7 @@ __global__ void __launch_bounds__(128 * (T + 1), 1) attend_tc_kernel(const __gri
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    __syncwarp();
     if (warp == kScoreWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_slot)), "r"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -311,6 +316,7 @@ __global__ void __launch_bounds__(128 * (T + 1), 1) attend_tc_kernel(const __gri
             for (int i = n > NS ? n - NS : 0; i < n && ok; i++) ok = __all_sync(0xFFFFFFFFu, mbar_wait_short(&empty[i % NS], (i / NS) & 1));
             if (!ok) {
                 if (lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
+                __syncwarp();
                 // what is on its way lands before the block ends (a tile that waits to be put right: above)
                 for (int i = n > NS ? n - NS : 0; i < n; i++) mbar_wait_short(&full[i % NS], (i / NS) & 1);
             }
@@ -349,10 +355,12 @@ __global__ void __launch_bounds__(128 * (T + 1), 1) attend_tc_kernel(const __gri
                 }
             }
             if (!ok && lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
+            __syncwarp();
             // every product issued is complete before the tensor memory is freed
             if (leader) mma_commit(&done[0]);
             __syncwarp();
             if (!mbar_wait_short(&done[0], 0) && lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
+            __syncwarp();
         } else if (any && warp == kValueWarp) {
             // ------------------------------------------------------------------------------ products of probabilities and values
             Cur c;
@@ -397,9 +405,11 @@ __global__ void __launch_bounds__(128 * (T + 1), 1) attend_tc_kernel(const __gri
                 }
             }
             if (!ok && lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
+            __syncwarp();
             if (leader) mma_commit(&done[1]);
             __syncwarp();
             if (!mbar_wait_short(&done[1], 0) && lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
+            __syncwarp();
         }
     } else {
         if constexpr (T == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
@@ -410,9 +420,11 @@ __global__ void __launch_bounds__(128 * (T + 1), 1) attend_tc_kernel(const __gri
             Cur c;
             c.set(a, a.begin[range], ua, ub);
             int steps = 0;                  // scores seen, also products of P and V asked for
+            // Stores and loads of tensor memory follow it, which are the whole warp's: it ends as it began
             auto arrive = [&](uint64_t *b) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b);
+                __syncwarp();
             };
             auto wait = [&](uint64_t *b, uint32_t parity) {
                 if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait_short(b, parity));
@@ -557,7 +569,6 @@ __global__ void __launch_bounds__(128 * (T + 1), 1) attend_tc_kernel(const __gri
 #pragma unroll 1
                     for (int q = 0; q < D / 32; q++) {
                         uint32_t v[32];
-                        __syncwarp();     // rows may be left out below, the load is the whole warp's
                         tmem_ld32(t_lane + L::o + t * D + 32 * q, v);
                         tmem_wait_ld();
                         if (in) {
@@ -571,8 +582,10 @@ __global__ void __launch_bounds__(128 * (T + 1), 1) attend_tc_kernel(const __gri
                                 *(uint4 *)(o + 32 * q + i) = w;
                             }
                         }
+                        __syncwarp();     // rows are left out above, the next load is the whole warp's
                     }
                     if (in && a.lse) a.lse[r * a.q_heads + h] = l == 0.f ? kNegInf : (m + log2f(l)) * 0.69314718f;
+                    __syncwarp();
                 } else {
                     // pieces of four columns of all rows: a warp's stores are 512 bytes in a row
                     float *o = a.part + (2 * (size_t)range + (begins ? 1 : 0)) * slot_floats<kRows, D>();
@@ -580,18 +593,19 @@ __global__ void __launch_bounds__(128 * (T + 1), 1) attend_tc_kernel(const __gri
 #pragma unroll 1
                     for (int q = 0; q < D / 32; q++) {
                         uint32_t v[32];
-                        __syncwarp();     // rows may be left out below, the load is the whole warp's
                         tmem_ld32(t_lane + L::o + t * D + 32 * q, v);
                         tmem_wait_ld();
                         if (in) {
 #pragma unroll
                             for (int i = 0; i < 32; i += 4) __stcg((uint4 *)(o + ((32 * q + i) / 4 * kRows + r) * 4), make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]));
                         }
+                        __syncwarp();     // as above
                     }
                     if (in) {
                         __stcg(o + kRows * D + r, m);
                         __stcg(o + kRows * D + kRows + r, l);
                     }
+                    __syncwarp();
                     tc_fence_before();
                     arrive(&ofree[t]);
                     // the part that comes last joins them all
@@ -599,6 +613,7 @@ __global__ void __launch_bounds__(128 * (T + 1), 1) attend_tc_kernel(const __gri
                     __threadfence();
                     tile_sync(t);
                     if (row == 0) last[t] = atomicAdd(&a.arrived[2 * r0 + t], 1) == parts - 1;
+                    __syncwarp();
                     tile_sync(t);
                     if (last[t] && in) {
                         __threadfence();
@@ -613,11 +628,13 @@ __global__ void __launch_bounds__(128 * (T + 1), 1) attend_tc_kernel(const __gri
                 c = nx;
             }
             if (!ok && lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
+            __syncwarp();
         }
     }
     tc_fence_before();
     __syncthreads();
     if (warp == kScoreWarp) {
+        __syncwarp();
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
     }
