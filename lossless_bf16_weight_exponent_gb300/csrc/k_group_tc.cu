@@ -580,6 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
                 if (lane == 0) mbar_arrive(&wempty[s]);
                 if (q >= kSA && !mbar_wait(&aempty[sa], ((q / kSA) & 1) ^ 1)) { ok = false; break; }
                 tc_fence_after();
+                __syncwarp();  // lanes leave the waits one by one, the store is the whole warp's
                 tmem_st32(tmem + t_lane + kACol + 32 * sa, p);
                 tmem_wait_st();
                 tc_fence_before();
@@ -654,6 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
                 const int buf = ns & 1;
                 if (!mbar_wait(&accfull[buf], (ns >> 1) & 1)) { ok = false; break; }
                 tc_fence_after();
+                __syncwarp();  // lanes leave the wait one by one, the loads are the whole warp's
                 const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + buf * kBN;
                 const uint32_t run = tmem + ((uint32_t)(32 * q) << 16) + Sh::RunCol;  // this warp's alone
                 for (int c0 = 0; c0 < w.n; c0 += 16) {
@@ -698,6 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_tc_kernel(const __grid_cons
     __syncthreads();
     if (warp == kMmaWarp) {
         tc_fence_after();
+        __syncwarp();
         if constexpr (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
         else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
     }

@@ -307,6 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                     }
                     vrow[tid] = cnt;
                 }
+                __syncwarp();  // the barrier is of whole warps
                 asm volatile("bar.sync 1, %0;" ::"n"(32 * kRebuildWarps) : "memory");
                 // exclusive scan of the per-row counts (one warp)
                 if (warp == 0) {
@@ -323,6 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
 #pragma unroll
                     for (int q = 0; q < 4; q++) { vrow[4 * lane + q] = run; run += c4[q]; }
                 }
+                __syncwarp();  // the barrier is of whole warps
                 asm volatile("bar.sync 1, %0;" ::"n"(32 * kRebuildWarps) : "memory");
                 // copy each row's run of verbatim exponents (contiguous in the stream) into shared memory
                 for (int r = warp; r < BM; r += kRebuildWarps) {
@@ -333,6 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                     for (uint32_t q = lane; q < n * 4; q += 32)
                         if (base + q / 4 < (uint32_t)a.vcap) ((uint4 *)(vdata + (uint64_t)base * 64))[q] = __ldg(src + q);
                 }
+                __syncwarp();  // the barrier is of whole warps
                 asm volatile("bar.sync 1, %0;" ::"n"(32 * kRebuildWarps) : "memory");
             }
             for (int i = group; i < nks; i += kRebuildGroups) {
@@ -395,6 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
         for (int c0 = 0; c0 < a.BN && c0 < a.B; c0 += 16) {
             uint32_t v[16];
             const uint32_t taddr = tmem + ((uint32_t)(32 * warp) << 16) + (uint32_t)c0;
+            __syncwarp();  // rows are left out below, the load is the whole warp's
             asm volatile(
                 "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
@@ -420,6 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     __syncthreads();
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        __syncwarp();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(a.tmem_cols) : "memory");
     }
 }

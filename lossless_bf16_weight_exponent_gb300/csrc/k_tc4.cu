@@ -322,6 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc4_kernel(const __grid_constant_
     } else if (warp < kRebuildWarps) {
         // ---------------------------------------------------------------------------------------- rebuild
         fill_pair_table16(tab, a.palette, threadIdx.x, 32 * kRebuildWarps);
+        __syncwarp();
         asm volatile("bar.sync 1, %0;" ::"r"(32 * kRebuildWarps) : "memory");
         const uint8_t *tab_l = tab + 4 * (lane & 15);
         const int c = lane & 7;  // 16-byte chunk (8 weights) of the row
@@ -380,7 +381,10 @@ __global__ void __launch_bounds__(kThreads, 1) tc4_kernel(const __grid_constant_
         const bool lead = et == 0;
         const uint32_t t_lane = (uint32_t)(32 * q) << 16;
         volatile uint32_t *bcast = tmem_slot + 1;  // the lead thread's word to the other epilogue threads
-        auto epi_sync = [] { asm volatile("bar.sync 2, %0;" ::"r"(32 * kEpiWarps) : "memory"); };
+        auto epi_sync = [] {
+            __syncwarp();  // the barrier is of whole warps
+            asm volatile("bar.sync 2, %0;" ::"r"(32 * kEpiWarps) : "memory");
+        };
         int64_t tile = u0 / upk;
         int kq = (int)(u0 % upk), seg = 0;
         for (int cu = 0; cu < nu; cu++) {
@@ -415,6 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc4_kernel(const __grid_constant_
             float *tf = a.out_bf16 ? a.acc : (float *)a.y;  // where a shared block's sums meet
             for (int c0 = 16 * half; c0 < a.B; c0 += 32) {
                 uint32_t v[16];
+                __syncwarp();  // rows are left out below, the load is the whole warp's
                 tmem_ld16(tmem + t_lane + (uint32_t)(buf * a.buf_stride + c0), v);
                 tmem_wait_ld();
                 if (row < a.N) {
@@ -478,6 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc4_kernel(const __grid_constant_
     __syncthreads();
     if (warp == kMmaWarp) {
         tc_fence_after();
+        __syncwarp();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(a.tmem_cols) : "memory");
     }
 }

@@ -75,3 +75,20 @@ def test_tensor_memory_is_freed_by_a_whole_warp(what):
     text = code(open(os.path.join(CSRC, "k_attend_tc.cu")).read())
     at = text.index(what)
     assert "__syncwarp();" in text[text.rindex("__syncthreads();", 0, at):at]
+
+
+WHOLE = re.compile(r"\btmem_(?:ld|st)\d+\((?!uint32_t)|tcgen05\.(?:ld|dealloc)\.|\bbar\.sync|\bcolumns\((?!uint32_t)")
+
+
+@pytest.mark.parametrize("name", ["k_group_tc.cu", "k_tc4.cu", "k_tc.cu"])
+def test_whole_warps_in_the_other_tensor_memory_kernels(name):
+    """Their waits and rows left out let lanes go one by one: a meeting stands in the lines in front of each instruction of a warp."""
+    lines = code(open(os.path.join(CSRC, name)).read()).split("\n")
+    text = "\n".join(lines)
+    sites = [text[:m.start()].count("\n") for m in WHOLE.finditer(text)]
+    sites = [i for i in sites if "[=]" not in lines[i] and "[&](uint32_t" not in lines[i]]
+    assert len(sites) >= 4
+    for i in sites:
+        if "columns(run" in lines[i] or "tmem_st16(run" in lines[i] or "tmem_ld16(acc, u)" in lines[i]:
+            continue  # behind the loads or the output of the same columns, which the whole warp has just done
+        assert any("__syncwarp();" in lines[j] for j in range(max(0, i - 6), i)), (i, lines[i])
