@@ -595,6 +595,17 @@ def _heads(what: str, t, rows: int, dim: int, kind: str, device: int):
     return t.data_ptr(), stride[0] if n > 1 else 0, heads
 
 
+def _room(what: str, t, size: int, device: int) -> int:
+    """_ptr of a dense tensor of any type with that many bytes on this CUDA device; addresses pass."""
+    if t is None:
+        return 0
+    if t.__class__ is int:
+        return t
+    if t.get_device() != device or not t.is_contiguous() or t.numel() * t.element_size() < size:
+        raise ValueError(f"{what} must be dense, on CUDA device {device} (it is on {t.device}) and have {size} bytes (it has {t.numel() * t.element_size()})")
+    return t.data_ptr()
+
+
 class Rotary:
     """Rotary positions (a ``uw_rotary``): the first `dim` elements of a head, in pairs `layout` apart, by frequencies of `base`
     scaled for long contexts (ROTARY_LINEAR, ...: uw_rotary_frequencies), held on the current CUDA device."""
@@ -697,7 +708,8 @@ class KVCache:
 
     def attend(self, batch, rows: int, q, out, q_heads: int = 0, scale=None, causal: bool = True, window: int = 0, lse=None, workspace=None,
                ws_bytes: int = 0, ldq: int = 0, ldo: int = 0, stream=None):
-        """uw_kv_attend: q and out bf16 [rows, q_heads, head_dim] (or addresses, with q_heads); scale None: head_dim ** -0.5."""
+        """uw_kv_attend: q and out bf16 [rows, q_heads, head_dim] (or addresses, with q_heads); scale None: head_dim ** -0.5;
+        workspace: a tensor of at least ws_bytes bytes (or an address)."""
         dev = self._device
         pq, sq, hq = _heads("q", q, rows, self.head_dim, "bf16", dev)
         po, so, ho = _heads("out", out, rows, self.head_dim, "bf16", dev)
@@ -709,7 +721,7 @@ class KVCache:
         if lse is not None and lse.__class__ is not int and (not lse.is_contiguous() or lse.numel() < rows * q_heads):
             raise ValueError("lse must be dense [rows, q_heads]")
         s = lib().uw_kv_attend(self._h, batch._ref, rows, pq, ldq or sq, q_heads, self._scale if scale is None else scale, causal, window, po, ldo or so,
-                               _at("lse", lse, "f32", dev), _ptr(workspace), ws_bytes, _stream(stream))
+                               _at("lse", lse, "f32", dev), _room("workspace", workspace, ws_bytes, dev), ws_bytes, _stream(stream))
         if s:
             _check(s, "uw_kv_attend")
 

@@ -128,3 +128,30 @@ def test_edits_without_a_history(stopped):
     for tokens in (dev(4, 0, dtype=I32), dev(1, 0, dtype=I32).expand(4, 0)):
         reaches_the_library(edit, tokens=tokens, lengths=dev(4, dtype=I32), repetition=dev(4, dtype=torch.float32))
         assert not stopped[-1][0].tokens
+
+
+# ------------------------------------------------------------------------------------------------ the workspace
+def attend(cache, ws, n, **kw):
+    return cache.attend(batch(), 4, rows(8), rows(8), workspace=ws, ws_bytes=n, stream=1, **kw)
+
+
+def test_workspace(cache):
+    """Its type does not matter, its device and its bytes do: the kernels write as many as the call says."""
+    for ws in (dev(4096, dtype=torch.uint8), dev(1024, dtype=torch.float32), dev(2, 2048, dtype=torch.uint8), dev(5000, dtype=torch.uint8), 16, None):
+        reaches_the_library(attend, cache, ws, 4096)
+    refused(attend, cache, dev(4095, dtype=torch.uint8), 4096)
+    refused(attend, cache, dev(1023, dtype=torch.float32), 4096)
+    refused(attend, cache, dev(1, dtype=torch.uint8).expand(4096), 4096)
+    refused(attend, cache, dev(8192, dtype=torch.uint8)[::2], 4096)
+    reaches_the_library(attend, cache, dev(0, dtype=torch.uint8), 0)
+
+
+def test_workspace_on_another_device(cache):
+    t = dict(q=rows(8), out=rows(8))
+    cache._device = 1
+    for x in t.values():
+        x.get_device = lambda: 1
+    b = batch()
+    b.device = 1
+    refused(cache.attend, b, 4, workspace=dev(4096, dtype=torch.uint8), ws_bytes=4096, stream=1, **t)
+    reaches_the_library(cache.attend, b, 4, workspace=16, ws_bytes=4096, stream=1, **t)
