@@ -328,14 +328,8 @@ extern "C" uw_status uw_edit_logits(const uw_logit_edits *e, const void *logits,
     if (rows == 0) return UW_OK;
     if (!logits || !out) return fail(UW_ERR_INVALID_ARG, "uw_edit_logits: logits or out NULL");
     const bool place = logits == out && f32 == o32 && (ld == ld_out || rows == 1);
-    if (!place) {
-        const uintptr_t i0 = (uintptr_t)logits, i1 = i0 + (uintptr_t)(((rows - 1) * ld + vocab) * (f32 ? 4 : 2));
-        const uintptr_t o0 = (uintptr_t)out, o1 = o0 + (uintptr_t)(((rows - 1) * ld_out + vocab) * (o32 ? 4 : 2));
-        // rows side by side, a stride apart, may lie between one another
-        const uintptr_t li = (uintptr_t)ld * (f32 ? 4 : 2), lo = (uintptr_t)ld_out * (o32 ? 4 : 2), d = li == lo ? (o0 - i0 + li * ((uintptr_t)1 << 20)) % li : 0;
-        const bool between = li == lo && d >= (uintptr_t)vocab * (f32 ? 4 : 2) && li - d >= (uintptr_t)vocab * (o32 ? 4 : 2);
-        if (i0 < o1 && o0 < i1 && !between) return fail(UW_ERR_INVALID_ARG, "uw_edit_logits: out overlaps logits (it may be logits itself, with their type and ld)");
-    }
+    if (!place && rows_overlap({logits, ld * (f32 ? 4 : 2), vocab * (f32 ? 4 : 2)}, {out, ld_out * (o32 ? 4 : 2), vocab * (o32 ? 4 : 2)}, rows))
+        return fail(UW_ERR_INVALID_ARG, "uw_edit_logits: out overlaps logits (it may be logits itself, with their type and ld)");
     if (place && !a.e.tokens && !a.e.bias_ids && !a.e.allowed) return UW_OK;
     // rows of 16-byte pieces; out's pieces are of as many logits
     const int W = f32 ? 4 : 8;

@@ -31,6 +31,23 @@ struct BlobHeader {
 uw_status fail(uw_status s, const char *fmt, ...);
 void clear_error();
 
+// Rows of a call's tensor, in bytes: `rows` of `width`, `pitch` apart.
+struct RowBytes {
+    const void *p;
+    int64_t pitch, width;
+};
+
+// Two tensors of as many rows share bytes.  With one pitch rows may lie between one another (columns of one tensor); with
+// two, tensors whose extents meet count as sharing.
+inline bool rows_overlap(const RowBytes &a, const RowBytes &b, int64_t rows)
+{
+    const __int128 a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p, n = rows - 1;  // pitches may be anything, the products too
+    if (a0 >= b0 + n * b.pitch + b.width || b0 >= a0 + n * a.pitch + a.width) return false;
+    if (rows == 1 || a.pitch != b.pitch) return true;
+    const __int128 r = (b0 - a0) % a.pitch, d = r < 0 ? r + a.pitch : r;    // from a row of a to the next of b
+    return d < a.width || a.pitch - d < b.width;
+}
+
 // host codec (uw_host.cpp)
 uw_status parse_and_validate(const uint8_t *blob, size_t size, BlobHeader *h, bool deep);
 void canonical_codes(const uint8_t *lens, uint32_t *codes);
