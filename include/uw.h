@@ -627,13 +627,14 @@ typedef struct {
  * uw_kv_append - rotate the new tokens' queries and keys, store their keys and values in the cache.
  *   q: [rows, q_heads, head_dim], k and v: [rows, kv_heads, head_dim] of `dtype` (as uw_matmul leaves them: fp32 or bf16), rows
  *   ldq, ldk, ldv elements apart (0: dense; multiples of 8), so that all three may be columns of one product's output.
- *   q_out: bf16 [rows, q_heads, head_dim], rows ldq_out apart; it may be q itself.  Either q and q_out or k and v may be NULL.
+ *   q_out: bf16 [rows, q_heads, head_dim], rows ldq_out apart; it may be q itself (bf16, with the same stride) and else shares
+ *   nothing with q, k or v, though rows may lie between theirs.  Either q and q_out or k and v may be NULL.
  *   r NULL: nothing is turned.  positions: int32 [rows], what the angles go by; NULL: the position in the cache.
  *   The angle position * freq is reduced in 64 bits; products in fp32, one rounding to bf16.  A token whose position in the
  *   cache is negative or past the table, or whose page is outside [0, pages), is not stored.  Rows outside
  *   [starts[0], starts[sequences]) are left as they were.  Two rows with one slot: either is stored.  Asynchronous.
  *   Errors: UW_ERR_INVALID_ARG (NULL, alignment: 16 bytes for q, k, v, q_out and 4 for the rest, 8 for freq; another current
- *   device than the cache's; bad dtype or layout), UW_ERR_SHAPE, UW_ERR_CUDA.
+ *   device than the cache's; bad dtype or layout; q_out overlapping q, k or v), UW_ERR_SHAPE, UW_ERR_CUDA.
  */
 uw_status uw_kv_append(const uw_kv_cache *c, const uw_kv_batch *b, const uw_rotary *r, int64_t rows, uw_out_dtype dtype,
                        const void *q, int64_t ldq, int q_heads, const void *k, int64_t ldk, const void *v, int64_t ldv,

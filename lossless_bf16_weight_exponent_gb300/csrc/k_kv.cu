@@ -395,9 +395,16 @@ extern "C" uw_status uw_kv_append(const uw_kv_cache *c, const uw_kv_batch *b, co
     }
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(positions, 4))
         return fail(UW_ERR_INVALID_ARG, "uw_kv_append: a pointer is not aligned");
-    if (q && q == q_out && (dtype == UW_OUT_F32 || (rows > 1 && a.ldq != a.ldq_out)))
-        return fail(UW_ERR_INVALID_ARG, "uw_kv_append: q_out is q of another type or stride");
     if (rows == 0) return UW_OK;
+    if (q) {
+        // a CTA's queries are another's keys and values, or another part of the same row: only its own may be written over
+        const int es = dtype == UW_OUT_F32 ? 4 : 2;
+        const bool place = q == q_out && dtype == UW_OUT_BF16 && (rows == 1 || a.ldq == a.ldq_out);
+        const RowBytes o{q_out, a.ldq_out * 2, dense_q * 2};
+        if ((!place && rows_overlap({q, a.ldq * es, dense_q * es}, o, rows)) ||
+            (k && (rows_overlap({k, a.ldk * es, dense_k * es}, o, rows) || rows_overlap({v, a.ldv * es, dense_k * es}, o, rows))))
+            return fail(UW_ERR_INVALID_ARG, "uw_kv_append: q_out overlaps q, k or v (it may be q itself, of bf16 and with its stride)");
+    }
     if ((s = check_kv_device(c, "uw_kv_append")) != UW_OK) return s;
     a.c = c->d;
     a.q = q;
