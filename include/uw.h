@@ -646,16 +646,16 @@ uw_status uw_kv_append(const uw_kv_cache *c, const uw_kv_batch *b, const uw_rota
  *     out[t, h] = sum_j p_j v_j,  p = softmax over j of (scale * q[t, h] . k_j),  lse[t, h] = ln sum_j exp(scale * q[t, h] . k_j)
  *   over the positions j of its sequence's length that it may see: causal != 0: j <= position, and with window > 0
  *   position - j < window; else all.  A row that sees nothing gets zeros and an lse of -inf.
- *   q, out: bf16 [rows, q_heads, head_dim], rows ldq and ldo elements apart (0: dense; multiples of 8).  lse: fp32
- *   [rows, q_heads] or NULL.  Sums in fp32; probabilities are rounded to bf16 in front of the second product, as its operand.
+ *   q, out: bf16 [rows, q_heads, head_dim], rows ldq and ldo elements apart (0: dense; multiples of 8), which share nothing, though
+ *   rows may lie between one another.  lse: fp32 [rows, q_heads] or NULL.  Sums in fp32; probabilities are rounded to bf16 in front of the second product, as its operand.
  *   A page outside [0, pages) reads as zeros.  Slots behind a sequence's length may hold anything; a key or value of the
  *   sequence itself that is not finite spoils the rows that see it, and may spoil others of its sequence that do not.
  *   Rows outside [starts[0], starts[sequences]) are left as they were.  The same call gives the same bits in every run; how a
  *   sequence's keys are cut, and so the last bits, depends on the whole batch's lengths.
  *   workspace: uw_kv_attend_workspace_size bytes, 16-byte aligned; needs no initialisation.  Calls that may run at the
  *   same time need one each.  Asynchronous.
- *   Errors: UW_ERR_INVALID_ARG (NULL, alignment, scale not finite, window < 0, a window without causal, another current device
- *   than the cache's), UW_ERR_SHAPE (rows, q_heads not a multiple of kv_heads or above 64 kv_heads, strides),
+ *   Errors: UW_ERR_INVALID_ARG (NULL, alignment, scale not finite, window < 0, a window without causal, out
+ *   overlapping q, another current device than the cache's), UW_ERR_SHAPE (rows, q_heads not a multiple of kv_heads or above 64 kv_heads, strides),
  *   UW_ERR_WORKSPACE, UW_ERR_CUDA.
  */
 /* For a call of these sequences, rows and query heads; it does not shrink as rows grow. */

@@ -774,7 +774,8 @@ extern "C" uw_status uw_kv_attend(const uw_kv_cache *c, const uw_kv_batch *b, in
         return fail(UW_ERR_SHAPE, "uw_kv_attend: ldq=%lld ldo=%lld", (long long)ldq, (long long)ldo);
     if (rows == 0) return UW_OK;
     if (!q || !out || !aligned16(q) || !aligned16(out) || ((uintptr_t)lse & 3)) return fail(UW_ERR_INVALID_ARG, "uw_kv_attend: q or out NULL, or a pointer not aligned");
-    if (q == out) return fail(UW_ERR_INVALID_ARG, "uw_kv_attend: out is q");
+    // a row's queries are read by every CTA that has a part of its keys, at its own time
+    if (rows_overlap({q, a.ldq * 2, dense * 2}, {out, a.ldo * 2, dense * 2}, rows)) return fail(UW_ERR_INVALID_ARG, "uw_kv_attend: out overlaps q");
     if ((s = check_kv_device(c, "uw_kv_attend")) != UW_OK) return s;
     const Plan p = plan_of(c, b->sequences, rows, q_heads);
     if (ws_bytes < p.bytes || !workspace) return fail(UW_ERR_WORKSPACE, "uw_kv_attend: workspace of %zu bytes, %zu needed", ws_bytes, p.bytes);

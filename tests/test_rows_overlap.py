@@ -109,3 +109,26 @@ def test_append_queries_into_keys_and_values(handle, rows, dtype):
     far = append(handle, rows, o + 4 * ld * rows, ld, k, ld * es // 2, k, ld, v, ld, dtype=dtype)
     overlaps(far, "q_out")
     overlaps(append(handle, rows, o + 4 * ld * rows, ld, v + es * (WK - 8), ld * es // 2, k, ld, v, ld, dtype=dtype), "q_out")
+
+
+def attend(handle, rows, q, ldq, out, ldo):
+    s = uw.lib().uw_kv_attend(ctypes.byref(handle), ctypes.byref(batch_of(rows)), rows, q, ldq, 4, 1.0, 1, 0, out, ldo, None, 4096, 1 << 40, None)
+    return s, uw.lib().uw_last_error().decode()
+
+
+@pytest.mark.parametrize("rows", [1, 2, 300])
+def test_attend_out_over_q(handle, rows):
+    ld = 3 * WQ
+    overlaps(attend(handle, rows, A, ld, A, ld), "out")
+    overlaps(attend(handle, rows, A, ld, A + 16, ld), "out")
+    overlaps(attend(handle, rows, A, ld, A - 16, ld), "out")
+    overlaps(attend(handle, rows, A, ld, A + 2 * (WQ - 8), ld), "out")
+    passes(attend(handle, rows, A, ld, A + 2 * WQ, ld))
+    passes(attend(handle, rows, A, ld, A + 4 * WQ, ld))
+    passes(attend(handle, rows, A + 4 * WQ, ld, A, ld))
+    passes(attend(handle, rows, A, 0, A + 2 * WQ * rows, 0))
+    if rows > 1:
+        overlaps(attend(handle, rows, A, ld, A + 2 * (ld - 8), ld), "out")
+        overlaps(attend(handle, rows, A, ld, A, 2 * ld), "out")
+        overlaps(attend(handle, rows, A, 0, A + 2 * WQ * (rows - 1), 0), "out")
+        overlaps(attend(handle, rows, A + 2 * WQ * (rows - 1), 0, A, 0), "out")
