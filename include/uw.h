@@ -692,7 +692,9 @@ typedef struct {
 
 /*
  * uw_edit_logits - penalties for repeated tokens, biases and grammar masks, in this order, on each row of logits:
- *     x = repetition; x -= frequency * count; x -= presence; x += bias; -inf where not allowed        (fp32, one rounding)
+ *     x = repetition; x -= frequency * count; x -= presence; x += bias; -inf where not allowed
+ *   in fp32 (the quotient by `repetition` is a product with its reciprocal, within 2^-23; both penalties are taken off as one
+ *   sum), then rounded to out_dtype.
  *   logits: [rows, vocab] of `dtype`, rows ld elements apart (0: vocab); out: of out_dtype, rows ld_out apart.  out may be
  *   logits itself with the same type and ld; then only logits that change are written, and without a mask only those are
  *   read.  NaN stays NaN unless it is masked.  Elements behind vocab are left as they were.  No workspace.  Asynchronous; the
