@@ -608,10 +608,11 @@ def _room(what: str, t, size: int, device: int) -> int:
 
 class Rotary:
     """Rotary positions (a ``uw_rotary``): the first `dim` elements of a head, in pairs `layout` apart, by frequencies of `base`
-    scaled for long contexts (ROTARY_LINEAR, ...: uw_rotary_frequencies), held on the current CUDA device."""
+    scaled for long contexts (ROTARY_LINEAR, ...: uw_rotary_frequencies), held on the current CUDA device.  low and high None: as
+    rotary_frequencies has them."""
 
     def __init__(self, dim: int, base: float = 10000.0, layout: int = ROTARY_HALF, scaling: int = ROTARY_PLAIN, factor: float = 1.0,
-                 low: float = 1.0, high: float = 4.0, original: int = 8192):
+                 low=None, high=None, original: int = 8192):
         self.freq, self.scale = rotary_frequencies(dim, base, scaling, factor, low, high, original)
         import torch
         self._dev = torch.from_numpy(self.freq).cuda()
@@ -620,9 +621,11 @@ class Rotary:
         self._ref = ctypes.byref(self.desc)
 
 
-def rotary_frequencies(dim: int, base: float = 10000.0, scaling: int = ROTARY_PLAIN, factor: float = 1.0, low: float = 1.0, high: float = 4.0,
-                       original: int = 8192):
-    """uw_rotary_frequencies: (float64 array [dim / 2] in radians a position, factor on cos and sin)."""
+def rotary_frequencies(dim: int, base: float = 10000.0, scaling: int = ROTARY_PLAIN, factor: float = 1.0, low=None, high=None, original: int = 8192):
+    """uw_rotary_frequencies: (float64 array [dim / 2] in radians a position, factor on cos and sin).  low and high, in turns over the
+    original length, are by default those of the scaling's method: 1 and 4 by bands, 1 and 32 on a ramp."""
+    low = 1.0 if low is None else low
+    high = (32.0 if scaling == ROTARY_RAMP else 4.0) if high is None else high
     f, s = np.zeros(max(1, dim // 2)), ctypes.c_float(0)
     _check(lib().uw_rotary_frequencies(dim, base, scaling, factor, low, high, original, f.ctypes.data, ctypes.byref(s)), "uw_rotary_frequencies")
     return f, s.value
