@@ -609,12 +609,21 @@ def _room(what: str, t, size: int, device: int) -> int:
 class Rotary:
     """Rotary positions (a ``uw_rotary``): the first `dim` elements of a head, in pairs `layout` apart, by frequencies of `base`
     scaled for long contexts (ROTARY_LINEAR, ...: uw_rotary_frequencies), held on the current CUDA device.  low and high None: as
-    rotary_frequencies has them."""
+    rotary_frequencies has them.  freq: the caller's own frequencies in place of these, dim / 2 of them in radians a position; scale: the
+    caller's own factor on cos and sin."""
 
     def __init__(self, dim: int, base: float = 10000.0, layout: int = ROTARY_HALF, scaling: int = ROTARY_PLAIN, factor: float = 1.0,
-                 low=None, high=None, original: int = 8192):
-        self.freq, self.scale = rotary_frequencies(dim, base, scaling, factor, low, high, original)
+                 low=None, high=None, original: int = 8192, freq=None, scale=None):
         import torch
+        if freq is None:
+            self.freq, own = rotary_frequencies(dim, base, scaling, factor, low, high, original)
+        else:
+            self.freq, own = np.array(freq.detach().cpu().numpy() if isinstance(freq, torch.Tensor) else freq, np.float64), 1.0
+            if self.freq.shape != (dim // 2,) or not np.isfinite(self.freq).all():
+                raise ValueError(f"freq must be {dim // 2} finite numbers")
+        self.scale = own if scale is None else float(scale)
+        if not np.isfinite(self.scale):
+            raise ValueError(f"scale {scale}")
         self._dev = torch.from_numpy(self.freq).cuda()
         self.device = self._dev.get_device()
         self.desc = RotaryDesc(dim, layout, self._dev.data_ptr(), self.scale)
