@@ -632,7 +632,8 @@ typedef struct {
  *   r NULL: nothing is turned.  positions: int32 [rows], what the angles go by; NULL: the position in the cache.
  *   The angle position * freq is reduced in 64 bits; products in fp32, one rounding to bf16.  A token whose position in the
  *   cache is negative or past the table, or whose page is outside [0, pages), is not stored.  Rows outside
- *   [starts[0], starts[sequences]) are left as they were.  Two rows with one slot: either is stored.  Asynchronous.
+ *   [starts[0], starts[sequences]) are left as they were.  Two rows with one slot (a page that two
+ *   sequences write to): each eight elements there are one of the two's, not all of the same one.  Asynchronous.
  *   Errors: UW_ERR_INVALID_ARG (NULL, alignment: 16 bytes for q, k, v, q_out and 4 for the rest, 8 for freq; another current
  *   device than the cache's; bad dtype or layout; q_out overlapping q, k or v), UW_ERR_SHAPE, UW_ERR_CUDA.
  */
