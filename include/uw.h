@@ -557,15 +557,19 @@ typedef enum {
     UW_ROTARY_INTERLEAVED = 1
 } uw_rotary_layout;
 
-/* How the frequencies base^(-2 i / dim) are scaled for contexts longer than those of training. */
+/* How the frequencies base^(-2 i / dim) are scaled for contexts longer than those of training.  In brackets the published method, and
+ * what a model's configuration usually calls it. */
 typedef enum {
-    UW_ROTARY_PLAIN = 0,     /* not */
-    UW_ROTARY_LINEAR = 1,    /* all divided by factor */
-    UW_ROTARY_STRETCHED = 2, /* base multiplied by factor^(dim / (dim - 2)): the lowest frequency divided by factor */
+    UW_ROTARY_PLAIN = 0,     /* not (rotary position embedding; "default") */
+    UW_ROTARY_LINEAR = 1,    /* all divided by factor (position interpolation; "linear") */
+    UW_ROTARY_STRETCHED = 2, /* base multiplied by factor^(dim / (dim - 2)): the lowest frequency divided by factor (NTK-aware scaling of
+                              * the base, with a fixed factor; what "dynamic" does for one length) */
     UW_ROTARY_BANDS = 3,     /* by the turns made over `original` positions: divided by factor up to `low`, kept from `high` on,
-                              * between the two a mixture that is linear in the turns */
+                              * between the two a mixture that is linear in the turns (frequency bands; "llama3", with its
+                              * low_freq_factor and high_freq_factor, usually 1 and 4) */
     UW_ROTARY_RAMP = 4       /* the same ends, linear in the index i between the indices (rounded outwards) that make `high` and
-                              * `low` turns; cos and sin are multiplied by 0.1 ln(factor) + 1 (factor > 1) */
+                              * `low` turns; cos and sin are multiplied by 0.1 ln(factor) + 1 (factor > 1) (YaRN; "yarn", with its
+                              * beta_slow as `low` and beta_fast as `high`, usually 1 and 32) */
 } uw_rotary_scaling;
 
 /*

@@ -13,9 +13,9 @@
 // Slots that no row of the item sees (behind the sequence's length, in front of a window) may hold anything: their scores are
 // replaced, their values set to zero in shared memory.
 //
-// Bound by memory: 64 sequences of up to 8191 tokens (8 key heads of 128, 1.15 GB) take 194 us, 5.9 TB/s, all of 8191 tokens 355
-// (6.0 TB/s), one of 131000 93 us.  One token over 8190 takes 15.1 us, of which the first kernel and the hand-over are 5, looking up pages
-// and queries 2, the copies 3 and the joins (of warps, of CTAs, by the last CTA) 4.  Items of 32 rows, two tiles of 16 in
+// Bound by memory: 64 sequences of up to 8191 tokens (8 key heads of 128, 1.15 GB) take 194 us, 5.9 TB/s (197 as ordinary calls), all of 8191
+// tokens 348 (6.2 TB/s), one of 131000 93 us.  One token over 8190 takes 15.1 us in a captured chain, 16.6 as ordinary calls, of which the first
+// kernel and the hand-over are 5, looking up pages and queries 2, the copies 3 and the joins (of warps, of CTAs, by the last CTA) 4.  Items of 32 rows, two tiles of 16 in
 // a CTA with their queries in shared memory, took 305 us for 64 sequences of 24 rows, where tcgen05 takes 266.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -711,6 +711,11 @@ Plan plan_of(const uw_kv_cache *c, int sequences, int64_t rows, int q_heads)
     //   16             201   206   398   414  1579  2346                        23.2                      838             322
     //   128            262   263   264   253   256   494                        33.6                      140            62.4
     //   256            270   270   271   259   259   311                        34.1                      115            55.8
+    // One kernel for a whole call, by its average; sequences that bring nothing count too.  The table is of batches of equal sequences; what the
+    // rule makes of mixed ones, key heads of 4 query heads, in us in a captured chain: 256 single tokens over up to 8191 and a chunk of 512 take
+    // 703 (items of 16 rows; alone 658 and, over 4000, 52), 100 of them and a chunk of 300 344 (alone 308 and 43); but a step of 256 places of which
+    // one brings 512 tokens and the others nothing takes 51 where those 512 alone, by items of 256, take 25; and 46 single tokens beside two chunks of
+    // 755 go by items of 256 rows, 8 of which hold queries.
     p.rows = each <= 16 * (int64_t)sequences ? 16 : each <= 128 * (int64_t)sequences ? 128 : 256;
     p.ctas = std::max(1, device_sms());
     const size_t ranges = (size_t)p.ctas;

@@ -9,9 +9,9 @@
 // in fp32: 70 us against 56, for its atomics with answers and its scattered stores.)
 // Out of place a logit is read and written once, unless a 16-byte piece is masked out as a whole, which is not read.  In
 // place a piece in which nothing changes is neither read nor written.
-// Bound by memory: 256 rows of 128256 fp32, each with 1500 to 3000 tokens of history and every second one masked, take 56 us
-// (4.8 TB/s; 49 without histories, which every slice of a row looks through); 1 row 3.9 us; 96 rows of 32003 bf16 with 300
-// biases each, their rows not aligned, 18 us.
+// Bound by issue slots (79 % busy) beside memory: 256 rows of 128256 fp32, each with 1500 to 3000 tokens of history and every second one masked, take 57.2 us
+// (4.7 TB/s; 48.8 without histories, which every slice of a row looks through; in place 50); 1 row 5.0 us with 8 biases, 3.9 without; 96
+// rows of 32003 bf16 with 300 biases each, their rows not aligned, 18.3 us (11.7 without biases; 8.5 of 32000 without, aligned; in place 14.7).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -78,8 +78,8 @@ __device__ __forceinline__ float edited(float x, uint32_t w, const Row &r)
 }
 
 // W: logits of a piece (8 of bf16, 4 of fp32 inputs; 1: rows without 16-byte alignment).  Four CTAs an SM, for which a few
-// registers go to memory, hide more of a CTA's phases from one another: 256 rows of 128256 fp32, half of them masked, take 55.9 us
-// against 64.7 with two.
+// registers go to memory, hide more of a CTA's phases from one another: 256 rows of 128256 fp32, half of them masked, took 55.9 us
+// against 64.7 with two (57.2 now, with the penalties' power of 2).
 template <bool F32, bool OUT32, int W, bool PLACE>
 __global__ void __launch_bounds__(kThreads, 4) edit_kernel(const EditArgs a)
 {

@@ -7,9 +7,11 @@
 // for 1024 sequences) and its slot, and the first dim / 2 threads turn the position into cos and sin for all heads.
 // The angle is position * freq in turns: in 64 bits the product is exact to 1e-10 of a turn at position 2^20, its fraction goes
 // into sincospi in fp32, so a far position costs no accuracy (the product in fp32 is off by 0.06 radians there).
-// Bound by memory for many tokens: 4096 of 32 query and 8 key heads of 128, bf16, take 17 us (5.9 TB/s; 20 with the angles in
-// their order in shared memory, where lanes of neighbouring items met in the same banks); 253 of 64 and 8 heads 6 us; one token
-// 2.7 us, the launch and three loads that depend on each other.
+// 4096 tokens of 32 query and 8 key heads of 128, bf16, take 20.4 us as ordinary calls (4.9 TB/s) and 17.0 in a captured chain on the same
+// tensors, a part of which stays in L2 (20.1 there with the angles in their order in shared memory, where lanes of neighbouring items met in
+// the same banks).  Memory does not bound it: a CTA's threads wait at the barrier for the look-ups and for 64 angles in 64 bits, which this
+// GPU computes slowly (ncu: barrier first among the stalls, DRAM at 35 %).  253 tokens of 64 and 8 heads take 6.0 us in a chain, one token 2.6,
+// the launch and three loads that depend on each other.
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
