@@ -563,7 +563,7 @@ typedef enum {
     UW_ROTARY_PLAIN = 0,     /* not (rotary position embedding; "default") */
     UW_ROTARY_LINEAR = 1,    /* all divided by factor (position interpolation; "linear") */
     UW_ROTARY_STRETCHED = 2, /* base multiplied by factor^(dim / (dim - 2)): the lowest frequency divided by factor (NTK-aware scaling of
-                              * the base, with a fixed factor; what "dynamic" does for one length) */
+                              * the base, with a fixed factor; "dynamic" at one length, with that length's factor) */
     UW_ROTARY_BANDS = 3,     /* by the turns made over `original` positions: divided by factor up to `low`, kept from `high` on,
                               * between the two a mixture that is linear in the turns (frequency bands; "llama3", with its
                               * low_freq_factor and high_freq_factor, usually 1 and 4) */

@@ -60,7 +60,7 @@ struct Row {
     __device__ __forceinline__ void repetition(float x)
     {
         rep = x;
-        up = x < 0x1p-126f ? 0x1p64f : x > 0x1p126f ? 0x1p-64f : 1.f;
+        up = fabsf(x) < 0x1p-126f ? 0x1p64f : fabsf(x) > 0x1p126f ? 0x1p-64f : 1.f;
         inv = 1.f / (x * up);
     }
 };
