@@ -53,7 +53,7 @@ struct Layout {
     static constexpr uint32_t half = kTile * 128;               // 64 elements of 128 rows or keys
     static constexpr uint32_t tile = half * (D / 64);           // a tile of queries, keys or values
     static constexpr int slots = (D == 128 ? 7 : 12) - T;
-    static constexpr uint32_t bars = 8 * (2 * slots + 18);
+    static constexpr uint32_t bars = 8 * (3 * slots + 18);
     static constexpr size_t smem = 1024 + (T + slots) * tile + bars + 16;
     static_assert(smem <= 227 * 1024, "shared memory");
     // columns of tensor memory
@@ -199,8 +199,11 @@ __global__ void __launch_bounds__(128 * (T + 1), 1) attend_tc_kernel(const __gri
     const AttendCall &a = g.c;
     uint8_t *qs = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);  // [T] tiles
     uint8_t *ring = qs + T * L::tile;
+    // Tile i of the ring (keys, values, keys, ...) is in slot i % NS, and has landed when full[i % 2 NS] has completed phase i / 2 NS.  A slot
+    // of an odd ring holds keys and values in turn, which two warps wait for: with one barrier for both the one could ask for its tile's phase
+    // while the other's before it is still open, and the parity would answer a turn early.  So each has its own, 2 NS being even.
     uint64_t *full = (uint64_t *)(ring + NS * L::tile);
-    uint64_t *empty = full + NS;
+    uint64_t *empty = full + 2 * NS;
     uint64_t *raw = empty + NS;                       // a tile whose values are put right before it counts as full
     uint64_t *qfull = raw + 1, *sfull = qfull + 2, *sfree = sfull + 2, *pfull = sfree + 1, *pvdone = pfull + 4, *ofree = pvdone + 2, *done = ofree + 2;
     uint32_t *tmem_slot = (uint32_t *)((uint8_t *)full + L::bars);
@@ -210,6 +213,7 @@ __global__ void __launch_bounds__(128 * (T + 1), 1) attend_tc_kernel(const __gri
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; i++) {
             mbar_init(&full[i], 1);
+            mbar_init(&full[NS + i], 1);
             mbar_init(&empty[i], 1);
         }
         mbar_init(raw, 1);
@@ -254,14 +258,14 @@ __global__ void __launch_bounds__(128 * (T + 1), 1) attend_tc_kernel(const __gri
             int n = 0;                        // tiles asked for: keys, values, keys, ...
             // values that are to be put right when they have landed
             bool fix = false;
-            int fix_slot = 0, fix_lo = 0, fix_hi = 0;
+            int fix_tile = 0, fix_lo = 0, fix_hi = 0;
             uint32_t raw_phase = 0;
             auto mend = [&] {
                 if (!fix) return;
                 fix = false;
                 if (!__all_sync(0xFFFFFFFFu, mbar_wait_short(raw, raw_phase & 1))) ok = false;
                 raw_phase++;
-                uint8_t *v = ring + fix_slot * L::tile;
+                uint8_t *v = ring + fix_tile % NS * L::tile;
                 for (int i = lane; i < kTile * (D / 8); i += 32) {
                     const int row = i / (D / 8), ch = i % (D / 8);
                     if (row >= fix_lo && row < fix_hi) continue;
@@ -269,7 +273,7 @@ __global__ void __launch_bounds__(128 * (T + 1), 1) attend_tc_kernel(const __gri
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&full[fix_slot]);
+                if (lane == 0) mbar_arrive(&full[fix_tile % (2 * NS)]);
                 __syncwarp();
             };
             // a lane's copies: a box of slots, 64 elements each
@@ -289,7 +293,7 @@ __global__ void __launch_bounds__(128 * (T + 1), 1) attend_tc_kernel(const __gri
                         }
                         const bool mended = kv && odd;
                         if (mended) mend();              // the one before
-                        uint64_t *bar = mended ? raw : &full[slot];
+                        uint64_t *bar = mended ? raw : &full[n % (2 * NS)];
                         if (lane == 0) mbar_expect_tx(bar, L::tile);
                         __syncwarp();
                         for (int b0 = 0; b0 < boxes; b0 += kPer) {
@@ -304,7 +308,7 @@ __global__ void __launch_bounds__(128 * (T + 1), 1) attend_tc_kernel(const __gri
                         __syncwarp();
                         if (mended) {
                             fix = true;
-                            fix_slot = slot;
+                            fix_tile = n;
                             fix_lo = c.k.lo - key0;
                             fix_hi = c.k.hi - key0;
                         }
@@ -319,7 +323,7 @@ __global__ void __launch_bounds__(128 * (T + 1), 1) attend_tc_kernel(const __gri
                 if (lane == 0) atomicExch(a.status, (int)DEV_TIMEOUT);
                 __syncwarp();
                 // what is on its way lands before the block ends (a tile that waits to be put right: above)
-                for (int i = n > NS ? n - NS : 0; i < n; i++) mbar_wait_short(&full[i % NS], (i / NS) & 1);
+                for (int i = n > NS ? n - NS : 0; i < n; i++) mbar_wait_short(&full[i % (2 * NS)], (i / (2 * NS)) & 1);
             }
         } else if (any && warp == kScoreWarp) {
             // ------------------------------------------------------------------------------ products of queries and keys
@@ -334,8 +338,10 @@ __global__ void __launch_bounds__(128 * (T + 1), 1) attend_tc_kernel(const __gri
                 const int nt = c.cnt, both = T == 2 && c.rows(a) > 128;
                 for (int j = 0; j < nt && ok; j++, n++) {
                     const int slot = (2 * n) % NS;
+                    uint64_t *here = &full[(2 * n) % (2 * NS)];
+                    const uint32_t turn = ((2 * n) / (2 * NS)) & 1;
                     for (int t = 0; t <= both && ok; t++) {
-                        bool w = qk > 0 ? wait_both(&full[slot], ((2 * n) / NS) & 1, sfree, (qk - 1) & 1) : mbar_wait_short(&full[slot], ((2 * n) / NS) & 1);
+                        bool w = qk > 0 ? wait_both(here, turn, sfree, (qk - 1) & 1) : mbar_wait_short(here, turn);
                         if (j == 0) w = w && mbar_wait_short(&qfull[t], segs[t]++ & 1);
                         ok = __all_sync(0xFFFFFFFFu, w);
                         if (!ok) break;
@@ -376,7 +382,7 @@ __global__ void __launch_bounds__(128 * (T + 1), 1) attend_tc_kernel(const __gri
                 for (int j = 0; j < nt && ok; j++, n++) {
                     const int v = 2 * n + 1, slot = v % NS;
                     for (int t = 0; t <= both && ok; t++) {
-                        bool w = wait_both(&full[slot], (v / NS) & 1, &pfull[2 * t], pv[t] & 1);
+                        bool w = wait_both(&full[v % (2 * NS)], (v / (2 * NS)) & 1, &pfull[2 * t], pv[t] & 1);
                         if (j == 0) {
                             if (segs[t] > 0) w = w && mbar_wait_short(&ofree[t], (segs[t] - 1) & 1);
                             segs[t]++;
