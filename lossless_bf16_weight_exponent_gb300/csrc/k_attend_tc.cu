@@ -20,11 +20,11 @@
 // Waits suspend the thread: polls of shared memory take turns that the operands of the products need (a spinning form took 874 us
 // where this one took 638).
 //
-// Measured in a captured chain (as ordinary calls): 8191 tokens of 32 query heads over 8 key heads of 128, causal: 394 us (418), 1.39 PFLOP/s,
-// not causal 706, 1.56; 509 tokens of 64 heads over 7171: 114 us (117), 1.09 PFLOP/s.  What an item costs beside its tiles (queries, the pipeline's ends,
+// Measured in a captured chain (as ordinary calls): 8191 tokens of 32 query heads over 8 key heads of 128, causal: 396 us (417), 1.39 PFLOP/s,
+// not causal 704, 1.56; 509 tokens of 64 heads over 7171: 116 us (119), 1.07 PFLOP/s.  What an item costs beside its tiles (queries, the pipeline's ends,
 // the output, a part's way through the workspace: 3 to 10 us) is what keeps the smaller ones from that.  The chain of a tile bounds a
 // long one: scores 0.27 us, 0.15 until they are seen, 0.9 for softmax, 0.15, the second product 0.27; the tensor cores are busy half of
-// the time (4095 tokens), the units for powers a quarter.  4 tokens x 8 heads over 131067: 110 us (110), 4.9 TB/s: 54 tiles of keys a CTA, 1.85 us each, the chain of one
+// the time (4095 tokens), the units for powers a quarter.  4 tokens x 8 heads over 131067: 109 us (110), 4.9 TB/s: 54 tiles of keys a CTA, 1.85 us each, the chain of one
 // tile again, as an item of 128 rows has no other one to run beside it.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
